@@ -48,7 +48,9 @@ typedef enum {
   MLA_ERR_WORKSPACE = 3,     /* workspace smaller than mla_plan_workspace_size(), or (from
                                 mla_decode_check) holding another plan's table */
   MLA_ERR_CUDA = 4,          /* a CUDA runtime / driver call failed */
-  MLA_ERR_DEVICE_TIMEOUT = 5 /* a device-side pipeline wait gave up (see mla_decode_check) */
+  MLA_ERR_DEVICE_TIMEOUT = 5, /* a device-side pipeline wait gave up (see mla_decode_check) */
+  MLA_ERR_CAPACITY = 6        /* pages, table columns or output entries ran out on the device
+                                 (see mla_cache_step, mla_error_check) */
 } mla_status;
 
 typedef enum {
@@ -384,6 +386,219 @@ mla_status mla_decode_run_noalloc(mla_plan* plan, const void* q, const float* q_
  * Errors: MLA_ERR_INVALID_ARG on a NULL plan.
  */
 mla_status mla_plan_set_stage1_events(mla_plan* plan, void* before, void* after);
+
+/* ------------------------------------------------------------------------
+ * The rest of an attention layer around the decode call: the cache step, the
+ * cache write, the absorbed form's two products and the expanded form.
+ *
+ * Per layer, a projection gives every new token a 512-dim latent and 64 dims
+ * to rotate; both go into the cache as one 576-dim row.  Head h has 128
+ * unrotated and 64 rotated query dims, and weights w[h] of 256 rows x 512:
+ *     key dims   k_t = w[h][0:128] c_t      (c_t: the cached latent of token t)
+ *     value dims v_t = w[h][128:256] c_t
+ *     scores     s = sm_scale (q_nope . k_t + q_rope . k_rope_t)
+ * Expanded form (mla_prefill_*): k and v are formed, for many query tokens.
+ * Absorbed form: q_lat = w[h][0:128]^T q_nope meets the cached rows directly
+ * (mla_absorb_q, mla_decode_run), and w[h][128:256] is applied to the decode
+ * output (mla_absorb_out).  The two forms give the same attention.
+ *
+ * Calls that take `err`, a device int32 word of the caller (NULL: problems on
+ * the device are not reported), OR bits into it when a device-side input is
+ * out of range; such an input is never followed out of its array.  The caller
+ * zeroes the word once; mla_error_check reads and clears it.
+ *
+ * The rotation turns dims (2i, 2i+1) (MLA_ROPE_INTERLEAVED) or (i, i+32)
+ * (MLA_ROPE_HALF) by the angle whose cosine and sine stand in cos_sin
+ * [max_positions][64] fp32, row = the token's entry of `positions`, cosines
+ * of the 32 pairs first.  cos_sin and positions both NULL: no rotation (the
+ * caller has rotated already).
+ */
+#define MLA_NOPE_DIM 128
+#define MLA_V_HEAD_DIM 128
+
+typedef enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 } mla_rope;
+
+/*
+ * mla_cache_step -- from request lengths on the device, everything a step
+ * needs to know about the paged cache.  One launch, no host read: request b
+ * has old_lens[b] cached tokens and gets new_lens[b] more.  Pages that it does
+ * not have yet are taken from free_pages in request order, from entry 0 on.
+ *
+ *   old_lens, new_lens  device int32 [batch_size]; new_lens NULL = 1 each.
+ *   block_table   device int32 [batch_size][table_stride], table_pages columns
+ *                 used: column j of row b is the page of the request's tokens
+ *                 j*page_size .. .  Columns of cached tokens are read, new
+ *                 ones written.
+ *   free_pages    device int32 [num_free].
+ *   kv_indptr     [batch_size+1] out: pages before each request, after the step.
+ *   kv_last_page_len  [batch_size] out: tokens in the last page (0: no pages).
+ *   kv_indices    [max_indices] out: the pages of all requests, in order, as
+ *                 mla_decode_run and mla_prefill_run take them.  Entries past
+ *                 kv_indptr[batch_size] are left alone.
+ *   qo_indptr     [batch_size+1] out: new tokens before each request.
+ *   slots         int64 [max_tokens] out: pool row of every new token, for
+ *                 mla_cache_write; -1 past the last token.
+ *   positions     int32 [max_tokens] out: position of every new token; 0 past
+ *                 the last one.
+ *   pages_used    [1] out, or NULL: pages taken from free_pages.
+ * The inputs other than block_table are left alone, and a call repeated on the
+ * same inputs writes the same outputs.  No output may overlap another array.
+ * On the device: a negative length counts as 0 and a negative page of a cached
+ * token gives slot -1 (mla_error_check: MLA_ERR_INVALID_ARG).  Tokens beyond
+ * the table's columns get no page, a page that free_pages has not is -1, the
+ * slots of such tokens are -1, and entries beyond max_indices or max_tokens
+ * are not written (MLA_ERR_CAPACITY).
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
+ */
+mla_status mla_cache_step(const int32_t* old_lens, const int32_t* new_lens, int32_t batch_size,
+                          int32_t page_size, int32_t* block_table, int64_t table_stride,
+                          int32_t table_pages, const int32_t* free_pages, int32_t num_free,
+                          int32_t* kv_indptr, int32_t* kv_last_page_len, int32_t* kv_indices,
+                          int64_t max_indices, int32_t* qo_indptr, int64_t* slots,
+                          int32_t* positions, int64_t max_tokens, int32_t* pages_used,
+                          int32_t* err, mla_stream_t stream);
+
+/*
+ * mla_cache_write -- the rows of new tokens into the cache: the latent's norm
+ * y = x / sqrt(mean(x^2) + eps) * norm_weight, the rotation of the 64 position
+ * dims and the pool's encoding in one pass.
+ *
+ *   latent        bf16 [num_tokens][512], row stride latent_stride elements (a
+ *                 multiple of 8); 16-byte aligned.
+ *   k_rope        bf16 [num_tokens][64], row stride k_rope_stride elements.
+ *   norm_weight   bf16 [512], 16-byte aligned, or NULL: no norm.
+ *   slots         int64 [num_tokens]: pool row of each token; -1: not stored.
+ *                 Two tokens of a call must not share a slot.
+ *   kv_dtype, kv, kv_scale, kv_e8m0, kv_e8m0_row_stride, kv_pool_rows
+ *                 the pool, as mla_decode_run reads it.  fp8: e4m3 of the value
+ *                 divided by kv_scale, saturating; MXFP4: per block of 32 the
+ *                 exponent floor(log2 amax) - 2 and e2m1 codes, saturating (a
+ *                 block with a value that is not finite gets scale byte 255).
+ *                 Roundings are to nearest even.
+ *   rows          bf16 [num_tokens][576], 16-byte aligned, or NULL: every row
+ *                 as the values that the pool's encoding stands for.
+ * On the device: a slot outside the pool (other than -1) is not stored, a
+ * position outside the table is read as 0; both are reported.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
+ */
+mla_status mla_cache_write(const void* latent, int64_t latent_stride, const void* k_rope,
+                           int64_t k_rope_stride, const void* norm_weight, float eps,
+                           const float* cos_sin, int64_t max_positions, const int32_t* positions,
+                           mla_rope rope, const int64_t* slots, int64_t num_tokens,
+                           mla_dtype kv_dtype, void* kv, const float* kv_scale, uint8_t* kv_e8m0,
+                           int64_t kv_e8m0_row_stride, int64_t kv_pool_rows, void* rows,
+                           int32_t* err, mla_stream_t stream);
+
+/*
+ * mla_absorb_q -- the query that mla_decode_run takes, from a layer's query:
+ *     q_out[t,h,0:512]   = 24 sm_scale  w[h][0:128]^T q[t,h,0:128]
+ *     q_out[t,h,512:576] = 24 sm_scale  rotate(q[t,h,128:192])
+ * The factor 24 = sqrt(576) undoes the decode call's own scale, so that its
+ * scores carry sm_scale.
+ *
+ *   q        bf16 [num_tokens][heads][192] with strides in elements, both
+ *            multiples of 8; 16-byte aligned.
+ *   w        bf16 [heads][256][512] contiguous, 16-byte aligned.
+ *   q_dtype  MLA_DTYPE_BF16 or MLA_DTYPE_FP8_E4M3 (the value divided by the
+ *            device fp32 q_scale, saturating).
+ *   q_out    [num_tokens][heads][576] contiguous, 16-byte aligned.
+ * mla_decode_run takes heads = 16.  Sums are held in fp32.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (q_dtype), MLA_ERR_CUDA.
+ */
+mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* w, int64_t num_tokens, int32_t heads, float sm_scale,
+                        const float* cos_sin, int64_t max_positions, const int32_t* positions,
+                        mla_rope rope, mla_dtype q_dtype, const float* q_scale, void* q_out,
+                        int32_t* err, mla_stream_t stream);
+
+/*
+ * mla_absorb_out -- the layer's attention output from the decode output:
+ *     out[t,h,:] = w[h][128:256] o[t,h,:].
+ *   o    bf16 [num_tokens][heads][512] contiguous, 16-byte aligned.
+ *   out  bf16 [num_tokens][heads][128] contiguous, 16-byte aligned.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
+ */
+mla_status mla_absorb_out(const void* o, const void* w, int64_t num_tokens, int32_t heads,
+                          void* out, mla_stream_t stream);
+
+/*
+ * mla_prefill_plan -- plan of an expanded-form call over a ragged batch.
+ * Request b's query tokens are rows qo_indptr[b] .. qo_indptr[b+1]-1 and the
+ * last positions of its sequence, already in the cache: with m query and n
+ * cached tokens, query token t attends to the first n - m + 1 + t tokens
+ * (none: out = 0, lse = -inf).
+ *
+ *   qo_indptr_host  host int32 [batch_size+1], non-decreasing from 0.
+ *   kv_indptr_host, kv_last_page_len_host, page_size  as for mla_decode_plan.
+ *   heads           1 .. 1024.
+ *   kv_dtype        MLA_DTYPE_BF16, MLA_DTYPE_FP8_E4M3 or MLA_DTYPE_MXFP4.
+ *   num_sms         CTAs to plan for; 0 = the SM count of the current device.
+ * The plan follows mla_plan's rules: library-owned, one host thread at a time,
+ * one workspace per plan.
+ * Errors: MLA_ERR_INVALID_ARG (also out of host memory), MLA_ERR_CUDA.
+ */
+typedef struct mla_prefill mla_prefill;
+
+typedef struct {
+  int32_t batch_size;
+  int32_t heads;
+  int32_t num_ctas;          /* CTAs of the attention kernel */
+  int32_t num_items;         /* (up to 256 query rows, head, key range) */
+  int32_t num_partials;      /* items whose result is joined with others */
+  int64_t query_tokens;
+  int64_t key_tokens;
+  size_t workspace_bytes;
+} mla_prefill_info;
+
+mla_status mla_prefill_plan(const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
+                            const int32_t* kv_last_page_len_host, int32_t batch_size,
+                            int32_t page_size, int32_t heads, mla_dtype kv_dtype, int32_t num_sms,
+                            mla_prefill** plan_out);
+mla_status mla_prefill_get_info(const mla_prefill* plan, mla_prefill_info* info);
+void mla_prefill_destroy(mla_prefill* plan);
+
+/*
+ * mla_prefill_run -- one expanded-form attention call, enqueued on `stream`:
+ * keys and values are expanded from the cached rows into the workspace
+ * (rounded to bf16), then attended to in one pass over the keys; key ranges
+ * that the plan split are joined by their log-sum-exp.
+ *
+ *   q          bf16 [query tokens][heads][192] with strides in elements, both
+ *              multiples of 8 (and below 2^39); 16-byte aligned.
+ *   kv .. kv_pool_rows, kv_indices  the cache, as for mla_decode_run.
+ *   w          bf16 [heads][256][512] contiguous, 16-byte aligned.
+ *   sm_scale   softmax scale, finite and > 0.
+ *   cos_sin, max_positions, positions, rope
+ *              rotation of the queries' last 64 dims (cached rows hold rotated
+ *              keys); positions [query tokens].
+ *   workspace  mla_prefill_info.workspace_bytes device bytes, 256-byte
+ *              aligned; its rules are those of mla_decode_run.
+ *   out        bf16 [query tokens][heads][128] contiguous, 16-byte aligned.
+ *   lse        fp32 [query tokens][heads], natural log, or NULL.
+ * A cached token whose row holds a value that is not finite affects only the
+ * query tokens that attend to it.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_WORKSPACE, MLA_ERR_UNSUPPORTED (odd
+ * MXFP4 scale rows), MLA_ERR_CUDA.
+ */
+mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_stride,
+                           int64_t q_head_stride, const void* kv, const float* kv_scale,
+                           const uint8_t* kv_e8m0, int64_t kv_e8m0_row_stride,
+                           int64_t kv_pool_rows, const int32_t* kv_indices, const void* w,
+                           float sm_scale, const float* cos_sin, int64_t max_positions,
+                           const int32_t* positions, mla_rope rope, void* workspace,
+                           size_t workspace_bytes, void* out, float* lse, mla_stream_t stream);
+
+/* mla_decode_check for a prefill plan's workspace; a position outside the
+ * rotation table also gives MLA_ERR_INVALID_ARG. */
+mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_stream_t stream);
+
+/*
+ * mla_error_check -- synchronises `stream`, reads the device error word `err`
+ * and clears it.  MLA_OK; MLA_ERR_CAPACITY (nothing but pages, table columns
+ * or output entries ran out); MLA_ERR_INVALID_ARG (a length, page, slot or
+ * position out of range; also err NULL); MLA_ERR_CUDA.
+ */
+mla_status mla_error_check(int32_t* err, mla_stream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char* mla_status_string(mla_status status);

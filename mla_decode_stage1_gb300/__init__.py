@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the decode runs in the library's
 CUDA kernels.  The names mirror the C ABI in include/mla_decode.h:
 ``mla_decode_plan``, ``mla_decode_run``, ``mla_decode_check``,
-``mla_status_string``.  PyTorch tensors are accepted for device memory and
+``mla_status_string``.  The operators that make an attention layer of the
+decode call (``mla_cache_step``, ``mla_cache_write``, ``mla_absorb_q``,
+``mla_absorb_out``, ``mla_prefill_plan``, ``mla_prefill_run``) are in layer.py.  PyTorch tensors are accepted for device memory and
 ``torch.cuda`` streams; there is no CPU fallback -- importing this package
 fails loudly when the shared library has not been built.
 """
@@ -18,12 +20,14 @@ LIB_PATH = os.path.join(HERE, "libmla_decode.so")
 HEADS, QK_DIM, V_DIM, TILE = 16, 576, 512, 128
 DTYPES = {"bf16": 0, "fp8": 1, "mxfp4": 2}
 STATUS = {0: "MLA_OK", 1: "MLA_ERR_INVALID_ARG", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_WORKSPACE",
-          4: "MLA_ERR_CUDA", 5: "MLA_ERR_DEVICE_TIMEOUT"}
+          4: "MLA_ERR_CUDA", 5: "MLA_ERR_DEVICE_TIMEOUT", 6: "MLA_ERR_CAPACITY"}
 EXPORTS = ("mla_decode_plan", "mla_decode_plan_q", "mla_decode_plan_ex", "mla_plan_workspace_size",
            "mla_plan_get_info", "mla_plan_get_work", "mla_plan_destroy", "mla_decode_run",
            "mla_decode_check", "mla_status_string", "mla_plan_set_stage1_events",
            "mla_decode_run_noalloc", "mla_selftest_bounded_wait", "mla_decode_autotune",
-           "mla_autotune_select")
+           "mla_autotune_select", "mla_cache_step", "mla_cache_write", "mla_absorb_q",
+           "mla_absorb_out", "mla_prefill_plan", "mla_prefill_get_info", "mla_prefill_destroy",
+           "mla_prefill_run", "mla_prefill_check", "mla_error_check")
 
 
 class MlaError(RuntimeError):
@@ -329,3 +333,18 @@ class MlaDecoder:
     def __call__(self, q, kv, out, **kw):
         mla_decode_run(self.plan, q, kv, out, workspace=self.workspace, **kw)
         return out
+
+
+# The operators around the decode call (layer.py) need torch at import; they
+# are loaded when first asked for.
+LAYER = ("MlaPrefill", "PrefillInfo", "PrefillPlan", "mla_absorb_out", "mla_absorb_q",
+         "mla_cache_step", "mla_cache_write", "mla_error_check", "mla_prefill_check",
+         "mla_prefill_plan", "mla_prefill_run")
+
+
+def __getattr__(name):
+    if name in LAYER:
+        from . import layer
+        value = globals()[name] = getattr(layer, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

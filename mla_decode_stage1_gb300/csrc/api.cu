@@ -259,6 +259,11 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
+namespace mla {
+uint64_t new_plan_stamp() { return next_stamp(); }
+TiledEncoder tiled_encoder() { return encode_fn(); }
+}  // namespace mla
+
 extern "C" {
 
 // Split requests can be merged inside stage 1 when the CTAs of every
@@ -623,6 +628,7 @@ const char* mla_status_string(mla_status status) {
     case MLA_ERR_WORKSPACE: return "MLA_ERR_WORKSPACE";
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
     case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT";
+    case MLA_ERR_CAPACITY: return "MLA_ERR_CAPACITY";
   }
   return "MLA_ERR_UNKNOWN";
 }

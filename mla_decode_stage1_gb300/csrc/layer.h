@@ -1,0 +1,109 @@
+// layer.h -- internal declarations shared by the operators around the decode
+// call (cache.cu, absorb.cu, prefill.cu): their geometry, the bits of their
+// device error word and the rotation of the 64 position dims.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "mla_decode.h"
+
+namespace mla {
+
+constexpr int kRope = 64;                 // rotated dims of a query head and of the cached row
+constexpr int kNope = MLA_NOPE_DIM;       // unrotated query / key dims per head (expanded form)
+constexpr int kVHead = MLA_V_HEAD_DIM;    // value dims per head (expanded form)
+constexpr int kQHead = kNope + kRope;     // query dims per head (expanded form)
+constexpr int kWRows = kNope + kVHead;    // weight rows per head: keys, then values
+
+// Bits of the operators' device error word beside kErrBadPage (kernels.h).
+enum : int32_t {
+  kErrBadLength = 1 << 8,      // a negative length
+  kErrCapacity = 1 << 9,       // pages, table columns or output entries ran out
+  kErrBadSlot = 1 << 10,       // a slot outside the pool (other than -1)
+  kErrBadPosition = 1 << 11    // a position outside the rotation table
+};
+
+inline bool ptr_aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// The rotation's arguments: a table row holds 32 cosines, then 32 sines.
+struct Rotation {
+  const float* cos_sin;        // [max_positions, 64], or null: no rotation
+  const int32_t* positions;    // [tokens]
+  int64_t max_positions;
+  int32_t half;                // 0: pairs (2i, 2i+1); 1: pairs (i, i + 32)
+};
+
+// Checks shared by the calls that rotate: both pointers or neither.
+inline bool rotation_ok(const Rotation& r, int rope) {
+  if ((r.cos_sin == nullptr) != (r.positions == nullptr)) return false;
+  if (rope != MLA_ROPE_INTERLEAVED && rope != MLA_ROPE_HALF) return false;
+  return r.cos_sin == nullptr || (r.max_positions >= 1 && ptr_aligned(r.cos_sin, 4));
+}
+
+#ifdef __CUDACC__
+// Token t's table row.  A position outside the table is reported and read as 0.
+__device__ __forceinline__ const float* rotation_row(const Rotation& r, int64_t t, int32_t* err) {
+  int64_t pos = r.positions[t];
+  if (pos < 0 || pos >= r.max_positions) {
+    if (err != nullptr) atomicOr(err, kErrBadPosition);
+    pos = 0;
+  }
+  return r.cos_sin + pos * kRope;
+}
+
+// The two dims of rotation pair i.
+__device__ __forceinline__ int rope_dim0(int i, int half) { return half ? i : 2 * i; }
+__device__ __forceinline__ int rope_dim1(int i, int half) { return half ? i + kRope / 2 : 2 * i + 1; }
+
+// (a, b) turned by the angle with cosine c and sine s.  Products and sum are
+// rounded one by one (no fused multiply-add), so that the stored codes are
+// those of the formula in plain 32-bit arithmetic.
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+  b = y;
+}
+
+// Two values to e4m3 (round to nearest even, saturating at 448; NaN stays
+// NaN), `lo` in the low byte.
+__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 codes as half precision (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+// Two values to e2m1 (round to nearest even, saturating at 6), `lo` in the low nibble.
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+      "cvt.u32.u8 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e2m1 codes (one byte) as half precision (exact).
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.u8.u32 t, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(v));
+  return r;
+}
+#endif
+
+}  // namespace mla

@@ -50,4 +50,13 @@ namespace mla {
 // (noalloc.cu), looked up once per device.
 mla_status static_workspace(void** out);
 constexpr size_t kStaticWorkspaceBytes = size_t(16) << 20;
+
+// What the other host files take from api.cu: a process-wide unique stamp for
+// a new plan, and the driver's cuTensorMapEncodeTiled (null if not found).
+uint64_t new_plan_stamp();
+typedef CUresult (*TiledEncoder)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TiledEncoder tiled_encoder();
 }  // namespace mla

@@ -1,0 +1,88 @@
+// prefill.h -- internal interface between the host side of the expanded form
+// (prefill_api.cu) and its kernels (prefill.cu).
+#pragma once
+
+#include "layer.h"
+
+namespace mla {
+
+constexpr int kPfRows = 256;     // query rows of an item (two 128-row matrix tiles)
+constexpr int kPfTile = 128;     // keys of a tile
+
+// 128 consecutive cached tokens of one request, expanded into workspace rows
+// out_row .. out_row + 127 (rows past the request's end are written as zeros).
+struct ExpandTile {
+  int32_t page_base, tok0, len, out_row;   // first page-table entry, first token, request length
+};
+static_assert(sizeof(ExpandTile) == 16, "an expansion tile is one int4");
+
+// Query rows q_row .. q_row + rows - 1 of one head against keys
+// [kv_begin, kv_end) of their request (kv_begin a multiple of 128).  Row i
+// sees the request's first vis0 + i keys.  slot < 0: out and lse are written;
+// else a partial result.
+struct AttnItem {
+  int32_t q_row, rows, head, kv_row;       // kv_row: workspace row of the request's key 0
+  int32_t vis0, kv_begin, kv_end, slot;
+};
+static_assert(sizeof(AttnItem) == 32, "an attention item is two int4");
+
+// Join of `count` consecutive partials of the same query rows and head.
+struct JoinJob {
+  int32_t q_row, rows, head, first, count, vis0, pad[2];
+};
+
+struct ExpandParams {
+  const ExpandTile* tiles;
+  int32_t num_tiles, heads;
+  const uint8_t* kv;
+  const float* kv_scale;
+  const uint8_t* e8m0;
+  int64_t e8m0_stride;
+  int64_t pool_rows;
+  const int32_t* kv_indices;   // null: identity
+  int32_t page_size;
+  int32_t kv_dtype;
+  const uint16_t* w;           // [heads][256][512]
+  uint16_t* kx;                // [heads][kx_rows][256]: keys' 128 dims, then values'
+  uint16_t* kr;                // [kx_rows][64]: the keys' rotated dims
+  int64_t kx_rows;
+  int32_t* err;                // workspace header
+  uint64_t stamp;
+};
+
+struct AttnParams {
+  const AttnItem* items;
+  const int32_t* cta_indptr;
+  const uint16_t* q;
+  int64_t q_token_stride, q_head_stride;
+  int64_t q_tokens;
+  int32_t heads;
+  const uint16_t* kx;
+  const uint16_t* kr;
+  int64_t kx_rows;
+  float scale_log2;            // sm_scale * log2(e)
+  Rotation rot;
+  uint16_t* out;
+  float* lse;
+  float* part_o;               // [partials][256][128]
+  float* part_lse;             // [partials][256], log2 domain
+  int32_t* err;
+  uint64_t stamp;
+};
+
+struct JoinParams {
+  const JoinJob* jobs;
+  int32_t num_jobs, heads;
+  const float* part_o;
+  const float* part_lse;
+  uint16_t* out;
+  float* lse;
+  int32_t* err;
+  uint64_t stamp;
+};
+
+cudaError_t launch_expand(const ExpandParams& p, int num_ctas, cudaStream_t stream);
+cudaError_t launch_attn(const AttnParams& p, int num_ctas, cudaStream_t stream);
+cudaError_t launch_join(const JoinParams& p, cudaStream_t stream);
+
+}  // namespace mla
