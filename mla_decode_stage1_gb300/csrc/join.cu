@@ -1,0 +1,61 @@
+// join.cu -- joins the partial results of key ranges of the expanded form by
+// their log-sum-exp.
+
+#include <cuda_bf16.h>
+
+#include "prefill.h"
+
+namespace mla {
+namespace {
+
+// out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max lse): one warp per
+// row of a job, four dims a lane.
+__global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
+  if (reinterpret_cast<const WsHeader*>(p.err)->stamp != p.stamp) return;   // reported by attn_kernel
+  const int lane = threadIdx.x & 31;
+  const JoinJob j = p.jobs[blockIdx.x];
+  const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (i >= j.rows) return;
+  float M = -INFINITY;
+  bool nan = false;
+  for (int s = 0; s < j.count; ++s) {
+    const float v = p.part_lse[static_cast<int64_t>(j.first + s) * kPfRows + i];
+    nan |= v != v;
+    M = fmaxf(M, v);
+  }
+  if (nan) M = __uint_as_float(0x7fc00000u);
+  float wsum = 0.0f;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int s = 0; s < j.count; ++s) {
+    const int64_t at = static_cast<int64_t>(j.first + s) * kPfRows + i;
+    const float v = p.part_lse[at];
+    if (v == -INFINITY) continue;          // no key of this range is seen
+    const float w = exp2f(v - M);
+    const float4 o = reinterpret_cast<const float4*>(p.part_o + at * kVHead)[lane];
+    wsum += w;
+    a.x += w * o.x;
+    a.y += w * o.y;
+    a.z += w * o.z;
+    a.w += w * o.w;
+  }
+  // a row that sees no key at all is zero; one whose keys all score -inf is 0 / 0
+  const float inv = j.vis0 + i <= 0 ? 0.0f : 1.0f / wsum;
+  const int64_t at = (static_cast<int64_t>(j.q_row) + i) * p.heads + j.head;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+  uint2 v;
+  v.x = *reinterpret_cast<const uint32_t*>(&x);
+  v.y = *reinterpret_cast<const uint32_t*>(&y);
+  reinterpret_cast<uint2*>(p.out + at * kVHead)[lane] = v;
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[at] = wsum == 0.0f ? -INFINITY : (M + log2f(wsum)) * kLn2;
+}
+
+}  // namespace
+
+cudaError_t launch_join(const JoinParams& p, cudaStream_t stream) {
+  join_kernel<<<dim3(p.num_jobs, kPfRows / 8), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,5 +1,5 @@
 // prefill.h -- internal interface between the host side of the expanded form
-// (prefill_api.cu) and its kernels (prefill.cu).
+// (prefill_api.cu) and its kernels (expand.cu, attn.cu).
 #pragma once
 
 #include "layer.h"
@@ -32,6 +32,7 @@ struct JoinJob {
 };
 
 struct ExpandParams {
+  CUtensorMap map_w;           // {512, 256, heads}, boxes {64, 256, 1}
   const ExpandTile* tiles;
   int32_t num_tiles, heads;
   const uint8_t* kv;
@@ -42,7 +43,6 @@ struct ExpandParams {
   const int32_t* kv_indices;   // null: identity
   int32_t page_size;
   int32_t kv_dtype;
-  const uint16_t* w;           // [heads][256][512]
   uint16_t* kx;                // [heads][kx_rows][256]: keys' 128 dims, then values'
   uint16_t* kr;                // [kx_rows][64]: the keys' rotated dims
   int64_t kx_rows;
@@ -51,15 +51,12 @@ struct ExpandParams {
 };
 
 struct AttnParams {
+  CUtensorMap map_q;           // {192, heads, tokens}, boxes {64, 1, 128}
+  CUtensorMap map_kx;          // {256, kx_rows, heads}, boxes {64, 64, 1}
+  CUtensorMap map_kr;          // {64, kx_rows, 1}, boxes {64, 64, 1}
   const AttnItem* items;
   const int32_t* cta_indptr;
-  const uint16_t* q;
-  int64_t q_token_stride, q_head_stride;
-  int64_t q_tokens;
   int32_t heads;
-  const uint16_t* kx;
-  const uint16_t* kr;
-  int64_t kx_rows;
   float scale_log2;            // sm_scale * log2(e)
   Rotation rot;
   uint16_t* out;

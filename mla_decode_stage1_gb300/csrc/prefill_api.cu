@@ -28,7 +28,13 @@ struct mla_prefill {
          off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
   std::vector<uint8_t> table;
   uint64_t stamp = 0;
+  // per-run caches: the workspace holding the table, the tensor maps and what they describe
   mutable void* uploaded_ws = nullptr;
+  CUtensorMap map_q, map_kx, map_kr, map_w;
+  const void* map_w_ptr = nullptr;
+  const void* map_q_ptr = nullptr;
+  int64_t map_q_ts = 0, map_q_hs = 0;
+  void* map_ws = nullptr;
 };
 
 namespace {
@@ -141,7 +147,9 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
       }
     }
   }
-  if (whole.size() > static_cast<size_t>(INT32_MAX / 64)) return MLA_ERR_INVALID_ARG;
+  if (whole.size() > static_cast<size_t>(INT32_MAX / 64) ||
+      static_cast<int64_t>(P->tiles.size()) * P->heads > INT32_MAX)
+    return MLA_ERR_INVALID_ARG;
   P->q_tokens = qo[P->bs];
 
   // Cut limit: the one whose longest-first assignment ends first.  With many
@@ -224,6 +232,19 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   put(P->off_items, P->items.data(), sizeof(AttnItem) * P->items.size());
   put(P->off_jobs, P->jobs.data(), sizeof(JoinJob) * P->jobs.size());
   return MLA_OK;
+}
+
+// A 3-D tensor of bf16 whose 64-element boxes land in shared memory as rows of
+// 128 bytes with the 128-byte swizzle; rows out of bounds are zeros.
+bool make_map(CUtensorMap* map, const void* ptr, const cuuint64_t (&dims)[3],
+              const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3]) {
+  const mla::TiledEncoder enc = mla::tiled_encoder();
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -329,7 +350,16 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
   float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
   float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
   if (!plan->tiles.empty()) {
+    if (plan->map_w_ptr != w) {
+      plan->map_w_ptr = nullptr;
+      if (!make_map(&plan->map_w, w,
+                    {mla::kVDim, mla::kWRows, static_cast<cuuint64_t>(plan->heads)},
+                    {mla::kVDim * 2, mla::kVDim * mla::kWRows * 2}, {64, mla::kWRows, 1}))
+        return MLA_ERR_CUDA;
+      plan->map_w_ptr = w;
+    }
     mla::ExpandParams p{};
+    p.map_w = plan->map_w;
     p.tiles = reinterpret_cast<const ExpandTile*>(ws + plan->off_tiles);
     p.num_tiles = static_cast<int32_t>(plan->tiles.size());
     p.heads = plan->heads;
@@ -341,7 +371,6 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.kv_indices = kv_indices;
     p.page_size = plan->page_size;
     p.kv_dtype = plan->kv_dtype;
-    p.w = static_cast<const uint16_t*>(w);
     p.kx = kx;
     p.kr = kr;
     p.kx_rows = plan->kx_rows;
@@ -350,17 +379,39 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     if (mla::launch_expand(p, plan->num_sms, stream) != cudaSuccess) return MLA_ERR_CUDA;
   }
   if (plan->num_ctas > 0) {
+    if (plan->map_q_ptr != q || plan->map_q_ts != q_token_stride ||
+        plan->map_q_hs != q_head_stride) {
+      plan->map_q_ptr = nullptr;
+      if (!make_map(&plan->map_q, q,
+                    {mla::kQHead, static_cast<cuuint64_t>(plan->heads),
+                     static_cast<cuuint64_t>(plan->q_tokens)},
+                    {static_cast<cuuint64_t>(q_head_stride) * 2,
+                     static_cast<cuuint64_t>(q_token_stride) * 2},
+                    {64, 1, mla::kPfTile}))
+        return MLA_ERR_CUDA;
+      plan->map_q_ptr = q;
+      plan->map_q_ts = q_token_stride;
+      plan->map_q_hs = q_head_stride;
+    }
+    if (plan->map_ws != workspace) {
+      // (a plan without key rows has no tile to load)
+      const cuuint64_t rows = static_cast<cuuint64_t>(std::max<int64_t>(plan->kx_rows, 1));
+      plan->map_ws = nullptr;
+      if (plan->kx_rows > 0 &&
+          (!make_map(&plan->map_kx, kx, {mla::kWRows, rows, static_cast<cuuint64_t>(plan->heads)},
+                     {mla::kWRows * 2, rows * mla::kWRows * 2}, {64, 64, 1}) ||
+           !make_map(&plan->map_kr, kr, {mla::kRope, rows, 1}, {mla::kRope * 2, rows * mla::kRope * 2},
+                     {64, 64, 1})))
+        return MLA_ERR_CUDA;
+      plan->map_ws = workspace;
+    }
     mla::AttnParams p{};
+    p.map_q = plan->map_q;
+    p.map_kx = plan->map_kx;
+    p.map_kr = plan->map_kr;
     p.items = reinterpret_cast<const AttnItem*>(ws + plan->off_items);
     p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_indptr);
-    p.q = static_cast<const uint16_t*>(q);
-    p.q_token_stride = q_token_stride;
-    p.q_head_stride = q_head_stride;
-    p.q_tokens = plan->q_tokens;
     p.heads = plan->heads;
-    p.kx = kx;
-    p.kr = kr;
-    p.kx_rows = plan->kx_rows;
     p.scale_log2 = sm_scale * mla::kLog2e;
     p.rot = rot;
     p.out = static_cast<uint16_t*>(out);
