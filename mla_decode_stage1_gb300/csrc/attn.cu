@@ -59,6 +59,9 @@ __device__ __forceinline__ AttnItem load_item(const AttnItem* p) {
   return AttnItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+// A wait of the whole warp, which goes on (or gives up) together.
+__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 struct RingCursor {
   uint32_t n = 0;
   __device__ uint32_t slot() const { return n % kSlots; }
@@ -143,91 +146,101 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
 }
 
 // ------------------------------------------------------------- products
+// The whole warp walks the steps; one lane issues.
 __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32_t ring,
                              uint32_t tmem, int it0, int it1) {
   constexpr uint32_t idesc_qk = make_idesc(1, 1, false, false, 128, 128);
   constexpr uint32_t idesc_pv = make_idesc(1, 1, false, true, 128, 128);
-  RingCursor c;
-  int item = 0;
-  uint32_t np = 0;                  // bit t: parity of the P tiles consumed of query tile t
+  uint32_t n = 0;                   // ring chunks consumed
+  uint32_t item = 0;
+  uint32_t np0 = 0, np1 = 0;        // P tiles consumed of query tile 0, 1
   const uint64_t qd = smem_desc(q_smem, 16, 1024, kSwizzle128B);
   const uint64_t kd = smem_desc(ring, 16, 1024, kSwizzle128B);
   const uint64_t vd = smem_desc(ring, 8192, 1024, kSwizzle128B);
-  auto arrived = [&](uint32_t k, int count) {
-#pragma unroll 1
-    for (int i = 0; i < count; ++i)
-      if (!mbar_wait(smem_u32(&ms->full[(k + i) % kSlots]), ((k + i) / kSlots) & 1, p.err, kErrMma))
-        return false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return all_waited(mbar_wait(smem_u32(bar), parity, p.err, kErrMma));
+  };
+  // S_t = Q_t K^T, K in ring chunks k, k + 1, k + 2 (waited for by the first tile that meets them)
+  auto qk = [&](int t, uint32_t k, bool fresh) {
+#pragma unroll
+    for (int ch = 0; ch < 3; ++ch) {
+      const uint32_t s = (k + ch) % kSlots;
+      if (fresh && !wait(&ms->full[s], ((k + ch) / kSlots) & 1)) return false;
+      if (fresh) tc_fence_after();
+      const uint64_t a = qd + ((t * kQTileBytes + ch * kChunkBytes) >> 4);
+      const uint64_t b = kd + ((s * kChunkBytes) >> 4);
+      const uint32_t d = tmem + kColS + 128 * t;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16(d, a + 2 * kk, b + 2 * kk, idesc_qk, (ch | kk) != 0);
+      }
+    }
+    if (elect_one()) tc_commit(smem_u32(&ms->s_full[t]));
+    return true;
+  };
+  // O_t (+)= P_t V, V in ring chunks k, k + 1 (64 keys each)
+  auto pv = [&](int t, uint32_t k, bool fresh, bool first) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t s = (k + half) % kSlots;
+      if (fresh && !wait(&ms->full[s], ((k + half) / kSlots) & 1)) return false;
+      if (fresh) tc_fence_after();
+      const uint64_t b = vd + ((s * kChunkBytes) >> 4);
+      const uint32_t d = tmem + kColO + 128 * t, a = tmem + kColS + 128 * t + 32 * half;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ta(d, a + 8 * kk, b + 128 * kk, idesc_pv, !(first && half == 0 && kk == 0));
+      }
+    }
     return true;
   };
   auto release = [&](uint32_t k, int count) {
-#pragma unroll 1
-    for (int i = 0; i < count; ++i) tc_commit(smem_u32(&ms->empty[(k + i) % kSlots]));
-  };
-  // S_t = Q_t K^T, K in ring chunks k, k + 1, k + 2
-  auto qk = [&](int t, uint32_t k) {
-#pragma unroll 1
-    for (int ch = 0; ch < 3; ++ch) {
-      const uint64_t a = qd + ((t * kQTileBytes + ch * kChunkBytes) >> 4);
-      const uint64_t b = kd + ((((k + ch) % kSlots) * kChunkBytes) >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_f16(tmem + kColS + 128 * t, a + 2 * kk, b + 2 * kk, idesc_qk, (ch | kk) != 0);
-    }
-    tc_commit(smem_u32(&ms->s_full[t]));
-  };
-  // O_t (+)= P_t V, V in ring chunks k, k + 1 (64 keys each)
-  auto pv = [&](int t, uint32_t k, bool first) {
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const uint64_t b = vd + ((((k + half) % kSlots) * kChunkBytes) >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_f16_ta(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 32 * half + 8 * kk,
-                    b + 128 * kk, idesc_pv, !(first && half == 0 && kk == 0));
+    if (elect_one()) {
+      for (int i = 0; i < count; ++i) tc_commit(smem_u32(&ms->empty[(k + i) % kSlots]));
     }
   };
   for (int it = it0; it < it1; ++it) {
     const AttnItem w = load_item(p.items + it);
-    const int n0 = tile_steps(w, 0), n1 = tile_steps(w, 1);
+    const int n0 = uniform(tile_steps(w, 0)), n1 = uniform(tile_steps(w, 1));
     const int steps = max(n0, n1);
     if (steps == 0) continue;
-    if (!mbar_wait(smem_u32(&ms->q_ready), item & 1, p.err, kErrMma)) return;
+    if (!wait(&ms->q_ready, item & 1)) return;
     ++item;
-    if (!arrived(c.n, 3)) return;
     tc_fence_after();
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t)
-      if ((t ? n1 : n0) > 0) qk(t, c.n);
-    release(c.n, 3);
-    c.n += 3;
-    if (steps == 1) tc_commit(smem_u32(&ms->q_empty));
+    if (n0 > 0 && !qk(0, n, true)) return;
+    if (n1 > 0 && !qk(1, n, n0 == 0)) return;
+    release(n, 3);
+    n += 3;
+    if (steps == 1 && elect_one()) tc_commit(smem_u32(&ms->q_empty));
     for (int j = 0; j < steps; ++j) {
-      const uint32_t v = c.n, k = c.n + 2;
-      bool have_v = false, have_k = false;
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        const int nt = t ? n1 : n0;
-        if (j >= nt) continue;
-        if (!have_v && !arrived(v, 2)) return;
-        have_v = true;
-        if (!mbar_wait(smem_u32(&ms->p_full[t]), (np >> t) & 1, p.err, kErrMma)) return;
-        np ^= 1u << t;
+      const uint32_t v = n, k = n + 2;
+      bool fresh_v = true, fresh_k = true;
+      if (j < n0) {
+        if (!wait(&ms->p_full[0], np0++ & 1)) return;
         tc_fence_after();
-        pv(t, v, j == 0);
-        if (j + 1 == nt) tc_commit(smem_u32(&ms->o_full[t]));
-        if (j + 1 < nt) {
-          if (!have_k && !arrived(k, 3)) return;
-          have_k = true;
-          qk(t, k);
+        if (!pv(0, v, true, j == 0)) return;
+        fresh_v = false;
+        if (j + 1 == n0 && elect_one()) tc_commit(smem_u32(&ms->o_full[0]));
+        if (j + 1 < n0) {
+          if (!qk(0, k, true)) return;
+          fresh_k = false;
         }
       }
+      if (j < n1) {
+        if (!wait(&ms->p_full[1], np1++ & 1)) return;
+        tc_fence_after();
+        if (!pv(1, v, fresh_v, j == 0)) return;
+        if (j + 1 == n1 && elect_one()) tc_commit(smem_u32(&ms->o_full[1]));
+        if (j + 1 < n1 && !qk(1, k, fresh_k)) return;
+      }
       release(v, 2);
-      c.n += 2;
+      n += 2;
       if (j + 1 < steps) {
         release(k, 3);
-        c.n += 3;
-        if (j + 2 == steps) tc_commit(smem_u32(&ms->q_empty));
+        n += 3;
+        if (j + 2 == steps && elect_one()) tc_commit(smem_u32(&ms->q_empty));
       }
     }
   }
@@ -296,9 +309,6 @@ __device__ void run_rotation(const AttnParams& p, Misc* ms, uint8_t* q_smem, int
 }
 
 // -------------------------------------------------------------- softmax
-// The warp goes on together (its tensor memory accesses need every lane).
-__device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
-
 __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it0, int it1, int t,
                             int warp, int lane) {
   const int row = t * kPfTile + warp * 32 + lane;     // of the item
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t q_smem = smem_u32(smem), ring = q_smem + kQBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&ms->full[i]), 1);
@@ -467,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ms->tmem;
+  const uint32_t tmem = uniform(ms->tmem);
   if (ms->ours) {
     const int it0 = p.cta_indptr[blockIdx.x], it1 = p.cta_indptr[blockIdx.x + 1];
     if (warp < 8) {
@@ -480,9 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       } else if (warp == 12) {
         if (lane == 0) run_loads(p, ms, q_smem, ring, it0, it1);
       } else if (warp == 13) {
-        if (lane == 0) {
-          run_products(p, ms, q_smem, ring, tmem, it0, it1);
-          // no product may run on after the CTA has gone
+        run_products(p, ms, q_smem, ring, tmem, uniform(it0), uniform(it1));
+        // no product may run on after the CTA has gone
+        if (elect_one()) {
           tc_commit(smem_u32(&ms->drain));
           mbar_wait(smem_u32(&ms->drain), 0, p.err, kErrDrain);
         }

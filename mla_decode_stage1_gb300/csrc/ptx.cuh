@@ -101,6 +101,21 @@ __device__ __forceinline__ uint32_t ld_nc_u8_early(const uint8_t* ptr) {
   return v;
 }
 
+// One lane of the (converged) warp: the instructions that a single thread
+// issues sit in `if (elect_one())` inside code that the whole warp runs, so
+// that their descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// The value of lane 0, known to be the same in every lane.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ------------------------------------------------------------ cp.async rows
 // 16-byte asynchronous copy global -> shared (cached in L1, so that the other
 // 16-byte pieces of the same line hit there).
