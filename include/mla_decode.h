@@ -409,7 +409,7 @@ mla_status mla_plan_set_stage1_events(mla_plan* plan, void* before, void* after)
  *
  * The rotation turns dims (2i, 2i+1) (MLA_ROPE_INTERLEAVED) or (i, i+32)
  * (MLA_ROPE_HALF) by the angle whose cosine and sine stand in cos_sin
- * [max_positions][64] fp32, row = the token's entry of `positions`, cosines
+ * [max_positions][64] fp32 (16-byte aligned), row = the token's entry of `positions`, cosines
  * of the 32 pairs first.  cos_sin and positions both NULL: no rotation (the
  * caller has rotated already).
  */
@@ -573,7 +573,7 @@ void mla_prefill_destroy(mla_prefill* plan);
  *              keys); positions [query tokens].
  *   workspace  mla_prefill_info.workspace_bytes device bytes, 256-byte
  *              aligned; its rules are those of mla_decode_run.
- *   out        bf16 [query tokens][heads][128] contiguous, 16-byte aligned.
+ *   out        bf16 [query tokens][heads][128] contiguous, 32-byte aligned.
  *   lse        fp32 [query tokens][heads], natural log, or NULL.
  * A cached token whose row holds a value that is not finite affects only the
  * query tokens that attend to it.

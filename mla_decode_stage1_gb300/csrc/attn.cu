@@ -39,7 +39,7 @@ constexpr float kLag = 8.0f;
 
 struct Misc {
   uint64_t full[kSlots], empty[kSlots];
-  uint64_t q_full, q_ready, q_empty;
+  uint64_t q_full[2], q_ready[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;
   uint32_t tmem;
@@ -72,7 +72,7 @@ struct RingCursor {
 __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32_t ring, int it0,
                           int it1) {
   RingCursor c;
-  int item = 0;             // items with keys so far
+  uint32_t nq0 = 0, nq1 = 0;        // query tiles loaded of either kind
   bool ok = true;
   auto open = [&](uint32_t bytes) -> uint32_t {
     const uint32_t s = c.slot();
@@ -119,18 +119,21 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
     if (n == 0) continue;
     load_k(w, 0);
     if (!ok) break;
-    if (item > 0 && !mbar_wait(smem_u32(&ms->q_empty), (item - 1) & 1, p.err, kErrProducer)) {
-      ok = false;
-      break;
-    }
-    const int tiles = w.rows > kPfTile ? 2 : 1;
-    const uint32_t bar = smem_u32(&ms->q_full);
-    mbar_arrive_expect_tx(bar, tiles * kQTileBytes);
-    for (int t = 0; t < tiles; ++t)
+    for (int t = 0; t < 2 && ok; ++t) {
+      if ((t ? n1 : n0) == 0) continue;
+      const uint32_t k = t ? nq1++ : nq0++;
+      if (k > 0 && !mbar_wait(smem_u32(&ms->q_empty[t]), (k - 1) & 1, p.err, kErrProducer)) {
+        --(t ? nq1 : nq0);
+        ok = false;
+        break;
+      }
+      const uint32_t bar = smem_u32(&ms->q_full[t]);
+      mbar_arrive_expect_tx(bar, kQTileBytes);
       for (int ch = 0; ch < 3; ++ch)
         tma_load_3d(q_smem + t * kQTileBytes + ch * kChunkBytes, &p.map_q, bar, ch * 64, w.head,
                     w.q_row + t * kPfTile, keep);
-    ++item;
+    }
+    if (!ok) break;
     load_v(w, 0);
     for (int j = 1; j < n && ok; ++j) {
       load_k(w, j);
@@ -141,7 +144,8 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
     // a wait gave up: no copy may land after the CTA has gone
     for (uint32_t k = c.n > kSlots ? c.n - kSlots : 0; k < c.n; ++k)
       mbar_wait(smem_u32(&ms->full[k % kSlots]), (k / kSlots) & 1, p.err, kErrProducer);
-    if (item > 0) mbar_wait(smem_u32(&ms->q_full), (item - 1) & 1, p.err, kErrProducer);
+    if (nq0 > 0) mbar_wait(smem_u32(&ms->q_full[0]), (nq0 - 1) & 1, p.err, kErrProducer);
+    if (nq1 > 0) mbar_wait(smem_u32(&ms->q_full[1]), (nq1 - 1) & 1, p.err, kErrProducer);
   }
 }
 
@@ -152,7 +156,7 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
   constexpr uint32_t idesc_qk = make_idesc(1, 1, false, false, 128, 128);
   constexpr uint32_t idesc_pv = make_idesc(1, 1, false, true, 128, 128);
   uint32_t n = 0;                   // ring chunks consumed
-  uint32_t item = 0;
+  uint32_t nq0 = 0, nq1 = 0;        // query tiles used of either kind
   uint32_t np0 = 0, np1 = 0;        // P tiles consumed of query tile 0, 1
   const uint64_t qd = smem_desc(q_smem, 16, 1024, kSwizzle128B);
   const uint64_t kd = smem_desc(ring, 16, 1024, kSwizzle128B);
@@ -161,7 +165,8 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
     return all_waited(mbar_wait(smem_u32(bar), parity, p.err, kErrMma));
   };
   // S_t = Q_t K^T, K in ring chunks k, k + 1, k + 2 (waited for by the first tile that meets them)
-  auto qk = [&](int t, uint32_t k, bool fresh) {
+  // ; `last`: this query tile's last step of the item
+  auto qk = [&](int t, uint32_t k, bool fresh, bool last) {
 #pragma unroll
     for (int ch = 0; ch < 3; ++ch) {
       const uint32_t s = (k + ch) % kSlots;
@@ -176,7 +181,10 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
           umma_f16(d, a + 2 * kk, b + 2 * kk, idesc_qk, (ch | kk) != 0);
       }
     }
-    if (elect_one()) tc_commit(smem_u32(&ms->s_full[t]));
+    if (elect_one()) {
+      tc_commit(smem_u32(&ms->s_full[t]));
+      if (last) tc_commit(smem_u32(&ms->q_empty[t]));
+    }
     return true;
   };
   // O_t (+)= P_t V, V in ring chunks k, k + 1 (64 keys each)
@@ -206,14 +214,18 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
     const int n0 = uniform(tile_steps(w, 0)), n1 = uniform(tile_steps(w, 1));
     const int steps = max(n0, n1);
     if (steps == 0) continue;
-    if (!wait(&ms->q_ready, item & 1)) return;
-    ++item;
-    tc_fence_after();
-    if (n0 > 0 && !qk(0, n, true)) return;
-    if (n1 > 0 && !qk(1, n, n0 == 0)) return;
+    if (n0 > 0) {
+      if (!wait(&ms->q_ready[0], nq0++ & 1)) return;
+      tc_fence_after();
+      if (!qk(0, n, true, n0 == 1)) return;
+    }
+    if (n1 > 0) {
+      if (!wait(&ms->q_ready[1], nq1++ & 1)) return;
+      tc_fence_after();
+      if (!qk(1, n, n0 == 0, n1 == 1)) return;
+    }
     release(n, 3);
     n += 3;
-    if (steps == 1 && elect_one()) tc_commit(smem_u32(&ms->q_empty));
     for (int j = 0; j < steps; ++j) {
       const uint32_t v = n, k = n + 2;
       bool fresh_v = true, fresh_k = true;
@@ -224,7 +236,7 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
         fresh_v = false;
         if (j + 1 == n0 && elect_one()) tc_commit(smem_u32(&ms->o_full[0]));
         if (j + 1 < n0) {
-          if (!qk(0, k, true)) return;
+          if (!qk(0, k, true, j + 2 == n0)) return;
           fresh_k = false;
         }
       }
@@ -233,14 +245,14 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
         tc_fence_after();
         if (!pv(1, v, fresh_v, j == 0)) return;
         if (j + 1 == n1 && elect_one()) tc_commit(smem_u32(&ms->o_full[1]));
-        if (j + 1 < n1 && !qk(1, k, fresh_k)) return;
       }
+      // the values' chunks are free before the next scores are through
       release(v, 2);
       n += 2;
       if (j + 1 < steps) {
+        if (j + 1 < n1 && !qk(1, k, fresh_k, j + 2 == n1)) return;
         release(k, 3);
         n += 3;
-        if (j + 2 == steps && elect_one()) tc_commit(smem_u32(&ms->q_empty));
       }
     }
   }
@@ -249,62 +261,90 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
 // ------------------------------------------------------------- rotation
 // Rotates dims 128..191 of the item's query rows in place (chunk 2 of each
 // tile; 16-byte granule g of row r sits at g ^ (r & 7)).  Four lanes a row,
-// eight pairs a lane.  The rotated values are rounded to bf16 once more: they
-// are operands of a bf16 product.
+// eight pairs a lane, four rows a thread and tile.  The rotated values are
+// rounded to bf16 once more: they are operands of a bf16 product.
+__device__ __forceinline__ void rotate_row(const Rotation& rot, uint8_t* row, int r, int lane4,
+                                           const float4 (&c)[2], const float4 (&s)[2]) {
+  const int g0 = rot.half ? lane4 : 2 * lane4, g1 = rot.half ? lane4 + 4 : 2 * lane4 + 1;
+  uint4* p0 = reinterpret_cast<uint4*>(row + ((g0 ^ (r & 7)) << 4));
+  uint4* p1 = reinterpret_cast<uint4*>(row + ((g1 ^ (r & 7)) << 4));
+  const uint4 x = *p0, y = *p1;
+  uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const float cs[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+  const float sn[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+  auto lo = [](uint32_t v) { return __uint_as_float(v << 16); };
+  auto hi = [](uint32_t v) { return __uint_as_float(v & 0xffff0000u); };
+  auto pack = [](float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  };
+  if (rot.half) {
+    // element i of the first granule turns with element i of the second
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a0 = lo(u[i]), b0 = lo(u[4 + i]), a1 = hi(u[i]), b1 = hi(u[4 + i]);
+      rotate(a0, b0, cs[2 * i], sn[2 * i]);
+      rotate(a1, b1, cs[2 * i + 1], sn[2 * i + 1]);
+      u[i] = pack(a0, a1);
+      u[4 + i] = pack(b0, b1);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a = lo(u[i]), b = hi(u[i]);
+      rotate(a, b, cs[i], sn[i]);
+      u[i] = pack(a, b);
+    }
+  }
+  *p0 = make_uint4(u[0], u[1], u[2], u[3]);
+  *p1 = make_uint4(u[4], u[5], u[6], u[7]);
+}
+
 __device__ void run_rotation(const AttnParams& p, Misc* ms, uint8_t* q_smem, int it0, int it1,
                              int tid) {
   const int lane4 = tid & 3;
-  int item = 0;
+  uint32_t nq0 = 0, nq1 = 0;
   for (int it = it0; it < it1; ++it) {
     const AttnItem w = load_item(p.items + it);
-    if (max(tile_steps(w, 0), tile_steps(w, 1)) == 0) continue;
-    if (!mbar_wait(smem_u32(&ms->q_full), item & 1, p.err, kErrQPrep)) return;
-    ++item;
-    if (p.rot.cos_sin != nullptr) {
-      const int g0 = p.rot.half ? lane4 : 2 * lane4, g1 = p.rot.half ? lane4 + 4 : 2 * lane4 + 1;
-      for (int r = tid >> 2; r < w.rows; r += 32) {
-        const float* cs = rotation_row(p.rot, static_cast<int64_t>(w.q_row) + r,
-                                       lane4 == 0 ? p.err : nullptr) + 8 * lane4;
-        uint8_t* row = q_smem + (r >> 7) * kQTileBytes + 2 * kChunkBytes + (r & 127) * 128;
-        uint4* s0 = reinterpret_cast<uint4*>(row + ((g0 ^ (r & 7)) << 4));
-        uint4* s1 = reinterpret_cast<uint4*>(row + ((g1 ^ (r & 7)) << 4));
-        uint32_t u[8];
-        *reinterpret_cast<uint4*>(u) = *s0;
-        *reinterpret_cast<uint4*>(u + 4) = *s1;
-        // pair i of this lane: (u[i].lo, u[i].hi), or in halves element i of
-        // the first granule with element i of the second
+    for (int t = 0; t < 2; ++t) {
+      if (tile_steps(w, t) == 0) continue;
+      const uint32_t k = t ? nq1++ : nq0++;
+      const int rows = min(kPfTile, w.rows - t * kPfTile), r0 = tid >> 2;
+      const float* at[4];           // this lane's cosines of its four rows
+      if (p.rot.cos_sin != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          float a0, b0, a1, b1;
-          auto lo = [](uint32_t v) { return __uint_as_float(v << 16); };
-          auto hi = [](uint32_t v) { return __uint_as_float(v & 0xffff0000u); };
-          if (p.rot.half) {
-            a0 = lo(u[i / 2]); b0 = lo(u[4 + i / 2]);
-            a1 = hi(u[i / 2]); b1 = hi(u[4 + i / 2]);
-          } else {
-            a0 = lo(u[i]); b0 = hi(u[i]);
-            a1 = lo(u[i + 1]); b1 = hi(u[i + 1]);
-          }
-          rotate(a0, b0, cs[i], cs[kRope / 2 + i]);
-          rotate(a1, b1, cs[i + 1], cs[kRope / 2 + i + 1]);
-          auto pack = [](float x, float y) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-            return *reinterpret_cast<const uint32_t*>(&v);
-          };
-          if (p.rot.half) {
-            u[i / 2] = pack(a0, a1);
-            u[4 + i / 2] = pack(b0, b1);
-          } else {
-            u[i] = pack(a0, b0);
-            u[i + 1] = pack(a1, b1);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 32 * i;
+          at[i] = r < rows ? rotation_row(p.rot, static_cast<int64_t>(w.q_row) + t * kPfTile + r,
+                                          lane4 == 0 ? p.err : nullptr) + 8 * lane4
+                           : p.rot.cos_sin;
         }
-        *s0 = *reinterpret_cast<uint4*>(u);
-        *s1 = *reinterpret_cast<uint4*>(u + 4);
       }
-      fence_proxy_async_smem();
+      float4 c[2][2], s[2][2];
+      auto fetch = [&](int i, int b) {
+        const float4* f = reinterpret_cast<const float4*>(at[i]);
+        c[b][0] = f[0];
+        c[b][1] = f[1];
+        s[b][0] = f[kRope / 8];
+        s[b][1] = f[kRope / 8 + 1];
+      };
+      if (p.rot.cos_sin != nullptr) {
+        fetch(0, 0);
+        fetch(1, 1);
+      }
+      if (!mbar_wait(smem_u32(&ms->q_full[t]), k & 1, p.err, kErrQPrep)) return;
+      if (p.rot.cos_sin != nullptr) {
+        uint8_t* base = q_smem + t * kQTileBytes + 2 * kChunkBytes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 32 * i;
+          if (r < rows) rotate_row(p.rot, base + r * 128, r, lane4, c[i & 1], s[i & 1]);
+          if (i < 2) fetch(i + 2, i);
+        }
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(smem_u32(&ms->q_ready[t]));
     }
-    mbar_arrive(smem_u32(&ms->q_ready));
   }
 }
 
@@ -416,10 +456,12 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
       if (!live) {
         // past the item's rows: nothing to write
       } else if (w.slot >= 0) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + part * kVHead + 16 * q);
+        uint32_t u[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i]);
+        float* dst = p.part_o + part * kVHead + 16 * q;
+        st_global_32(dst, u);
+        st_global_32(dst + 8, u + 8);
       } else {
         uint32_t u[8];
 #pragma unroll
@@ -427,9 +469,7 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
           const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
           u[i] = *reinterpret_cast<const uint32_t*>(&v);
         }
-        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kVHead + 16 * q);
-        dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        st_global_32(p.out + at * kVHead + 16 * q, u);
       }
     }
     if (live) {
@@ -457,10 +497,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       mbar_init(smem_u32(&ms->full[i]), 1);
       mbar_init(smem_u32(&ms->empty[i]), 1);
     }
-    mbar_init(smem_u32(&ms->q_full), 1);
-    mbar_init(smem_u32(&ms->q_ready), 128);
-    mbar_init(smem_u32(&ms->q_empty), 1);
     for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&ms->q_full[t]), 1);
+      mbar_init(smem_u32(&ms->q_ready[t]), 128);
+      mbar_init(smem_u32(&ms->q_empty[t]), 1);
       mbar_init(smem_u32(&ms->s_full[t]), 1);
       mbar_init(smem_u32(&ms->p_full[t]), 128);
       mbar_init(smem_u32(&ms->o_full[t]), 1);
@@ -481,10 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   if (ms->ours) {
     const int it0 = p.cta_indptr[blockIdx.x], it1 = p.cta_indptr[blockIdx.x + 1];
     if (warp < 8) {
-      regs_raise<200>();
+      regs_raise<192>();
       run_softmax(p, ms, tmem, it0, it1, warp >> 2, warp & 3, lane);
     } else {
-      regs_lower<56>();
+      regs_lower<64>();
       if (warp < 12) {
         run_rotation(p, ms, smem, it0, it1, threadIdx.x - 256);
       } else if (warp == 12) {

@@ -35,6 +35,7 @@ constexpr uint32_t kAChunk = 128 * 128;    // 128 rows x 64 bf16
 constexpr uint32_t kWChunk = 256 * 128;    // 256 weight rows x 64 bf16
 constexpr int kChunks = kVDim / 64;
 constexpr int kWSlots = 3;
+constexpr int kAhead = 4;                  // row chunks loaded ahead of their use
 constexpr uint32_t kExpandSmem = kChunks * kAChunk + kWSlots * kWChunk;
 
 struct ExpandMisc {
@@ -133,20 +134,21 @@ __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem,
       live[i] = tok < t.len;
       row[i] = live[i] ? pool_row(p, t.page_base, tok) : 0;
     }
-    Raw<KV> raw[4];
+    Raw<KV> raw[kAhead][4];                  // chunks in flight from memory
     auto fetch = [&](int c) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (live[i]) raw[i] = load_raw<KV>(p, row[i], 8 * c + g);
+        if (live[i]) raw[c % kAhead][i] = load_raw<KV>(p, row[i], 8 * c + g);
     };
-    fetch(0);
-#pragma unroll 1
+#pragma unroll
+    for (int c = 0; c < kAhead; ++c) fetch(c);
+#pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[i] = live[i] ? decode<KV>(raw[i], 1.0f) : make_uint4(0, 0, 0, 0);
-      fetch(c + 1);                          // chunk 8: the rotated dims
+        v[i] = live[i] ? decode<KV>(raw[c % kAhead][i], 1.0f) : make_uint4(0, 0, 0, 0);
+      if (c + kAhead <= kChunks) fetch(c + kAhead);     // chunk 8: the rotated dims
       if (lap > 0 && !mbar_wait(smem_u32(&ms->a_empty[c]), (lap - 1) & 1, p.err, kErrProducer))
         return;
 #pragma unroll
@@ -162,7 +164,7 @@ __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem,
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4*>(p.kr + (static_cast<int64_t>(t.out_row) + r0 + 32 * i) * kRope +
                                   8 * g) =
-            live[i] ? decode<KV>(raw[i], sc) : make_uint4(0, 0, 0, 0);
+            live[i] ? decode<KV>(raw[kChunks % kAhead][i], sc) : make_uint4(0, 0, 0, 0);
     }
     u = min(u1, (tile + 1) * p.heads);
   }
@@ -191,32 +193,41 @@ __device__ void run_weights(const ExpandParams& p, ExpandMisc* ms, uint32_t w_sm
       mbar_wait(smem_u32(&ms->w_full[k % kWSlots]), (k / kWSlots) & 1, p.err, kErrProducer);
 }
 
+// The whole warp walks the units; one lane issues.
 __device__ void run_products(const ExpandParams& p, ExpandMisc* ms, uint32_t a_smem,
                              uint32_t w_smem, uint32_t tmem, int u0, int u1) {
   constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, kWRows);
   const uint64_t ad = smem_desc(a_smem, 16, 1024, kSwizzle128B);
   const uint64_t wd = smem_desc(w_smem, 16, 1024, kSwizzle128B);
-  uint32_t n = 0, lap = 0, k = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.err, kErrMma));
+  };
+  uint32_t slot = 0, phase = 0, lap = 0, k = 0;
   for (int u = u0; u < u1; ++u, ++k) {
     const bool first = u == u0 || u % p.heads == 0;          // first unit of its tile here
     const bool last = u + 1 == u1 || (u + 1) % p.heads == 0;
     const uint32_t buf = k & 1;
-    if (k >= 2 && !mbar_wait(smem_u32(&ms->acc_empty[buf]), ((k >> 1) - 1) & 1, p.err, kErrMma))
-      return;
+    if (k >= 2 && !wait(&ms->acc_empty[buf], ((k >> 1) - 1) & 1)) return;
     tc_fence_after();
-    for (int c = 0; c < kChunks; ++c, ++n) {
-      if (first && !mbar_wait(smem_u32(&ms->a_full[c]), lap & 1, p.err, kErrMma)) return;
-      const uint32_t s = n % kWSlots;
-      if (!mbar_wait(smem_u32(&ms->w_full[s]), (n / kWSlots) & 1, p.err, kErrMma)) return;
-      tc_fence_after();
-      const uint64_t a = ad + ((c * kAChunk) >> 4), w = wd + ((s * kWChunk) >> 4);
+    const uint32_t d = tmem + buf * kWRows;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_f16(tmem + buf * kWRows, a + 2 * kk, w + 2 * kk, idesc, (c | kk) != 0);
-      tc_commit(smem_u32(&ms->w_empty[s]));
-      if (last) tc_commit(smem_u32(&ms->a_empty[c]));
+    for (int c = 0; c < kChunks; ++c) {
+      if (first && !wait(&ms->a_full[c], lap & 1)) return;
+      if (!wait(&ms->w_full[slot], phase)) return;
+      tc_fence_after();
+      const uint64_t a = ad + ((c * kAChunk) >> 4), w = wd + ((slot * kWChunk) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_f16(d, a + 2 * kk, w + 2 * kk, idesc, (c | kk) != 0);
+        tc_commit(smem_u32(&ms->w_empty[slot]));
+        if (last) tc_commit(smem_u32(&ms->a_empty[c]));
+      }
+      if (++slot == kWSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-    tc_commit(smem_u32(&ms->acc_full[buf]));
+    if (elect_one()) tc_commit(smem_u32(&ms->acc_full[buf]));
     if (last) ++lap;
   }
 }
@@ -252,11 +263,11 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint32_t tme
     }
     const bool finite = fmaxf(__low2float(top), __high2float(top)) < INFINITY &&
                         !__isnanf(__low2float(top)) && !__isnanf(__high2float(top));
+    // (a sector per store: with 16-byte stores the write path was the limit)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      *reinterpret_cast<uint4*>(dst + kNope + 8 * i) =
-          finite ? make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3])
-                 : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 64; ++i) v[i] = finite ? v[i] : 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st_global_32(dst + kNope + 16 * i, v + 8 * i);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t x[64];
@@ -268,14 +279,14 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint32_t tme
         mbar_arrive(smem_u32(&ms->acc_empty[buf]));
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t o[4];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o[q] = finite ? bf16x2(__uint_as_float(x[8 * i + 2 * q]) * sc,
-                                 __uint_as_float(x[8 * i + 2 * q + 1]) * sc)
+        for (int q = 0; q < 8; ++q)
+          o[q] = finite ? bf16x2(__uint_as_float(x[16 * i + 2 * q]) * sc,
+                                 __uint_as_float(x[16 * i + 2 * q + 1]) * sc)
                         : 0x7fc07fc0u;
-        *reinterpret_cast<uint4*>(dst + 64 * half + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+        st_global_32(dst + 64 * half + 16 * i, o);
       }
     }
   }
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t a_smem = smem_u32(smem), w_smem = a_smem + kChunks * kAChunk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kChunks; ++i) {
       mbar_init(smem_u32(&ms->a_full[i]), 256);
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ms->tmem;
+  const uint32_t tmem = uniform(ms->tmem);
   if (ms->ours) {
     const int64_t units = static_cast<int64_t>(p.num_tiles) * p.heads;
     const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
@@ -325,12 +336,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       run_epilogue(p, ms, tmem, u0, u1, warp, lane);
     } else if (warp < 12) {
       run_rows<KV>(p, ms, smem, u0, u1, threadIdx.x - 128);
-    } else if (lane == 0) {
-      if (warp == 12) {
-        run_weights(p, ms, w_smem, u0, u1);
-      } else {
-        run_products(p, ms, a_smem, w_smem, tmem, u0, u1);
-        // no product may run on after the CTA has gone
+    } else if (warp == 12) {
+      if (lane == 0) run_weights(p, ms, w_smem, u0, u1);
+    } else {
+      run_products(p, ms, a_smem, w_smem, tmem, uniform(u0), uniform(u1));
+      // no product may run on after the CTA has gone
+      if (elect_one()) {
         tc_commit(smem_u32(&ms->drain));
         mbar_wait(smem_u32(&ms->drain), 0, p.err, kErrDrain);
       }

@@ -43,7 +43,7 @@ struct Rotation {
 inline bool rotation_ok(const Rotation& r, int rope) {
   if ((r.cos_sin == nullptr) != (r.positions == nullptr)) return false;
   if (rope != MLA_ROPE_INTERLEAVED && rope != MLA_ROPE_HALF) return false;
-  return r.cos_sin == nullptr || (r.max_positions >= 1 && ptr_aligned(r.cos_sin, 4));
+  return r.cos_sin == nullptr || (r.max_positions >= 1 && ptr_aligned(r.cos_sin, 16));
 }
 
 #ifdef __CUDACC__

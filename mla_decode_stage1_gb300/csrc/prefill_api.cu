@@ -316,7 +316,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     return MLA_ERR_INVALID_ARG;
   if (plan->q_tokens > 0 && (q == nullptr || out == nullptr)) return MLA_ERR_INVALID_ARG;
   if (!ptr_aligned(q, 16) || !ptr_aligned(kv, 16) || !ptr_aligned(w, 16) ||
-      !ptr_aligned(out, 16) || !ptr_aligned(workspace, 256) || !ptr_aligned(lse, 4) ||
+      !ptr_aligned(out, 32) || !ptr_aligned(workspace, 256) || !ptr_aligned(lse, 4) ||
       !ptr_aligned(kv_scale, 4) || !ptr_aligned(kv_indices, 4) || !ptr_aligned(positions, 4))
     return MLA_ERR_INVALID_ARG;
   if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;

@@ -116,6 +116,13 @@ __device__ __forceinline__ bool elect_one() {
 // The value of lane 0, known to be the same in every lane.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// 32 bytes to global memory, a whole sector per thread (32-byte aligned).
+__device__ __forceinline__ void st_global_32(void* ptr, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // ------------------------------------------------------------ cp.async rows
 // 16-byte asynchronous copy global -> shared (cached in L1, so that the other
 // 16-byte pieces of the same line hit there).

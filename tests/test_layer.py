@@ -178,6 +178,12 @@ def test_prefill_run_refuses_misaligned(mla, mem, name):
     assert mla._lib.mla_prefill_run(*run_args(p, mem, **{name: mem + 8})) == 1
 
 
+def test_prefill_run_refuses_out_and_tables_off_their_alignment(mla, mem):
+    p = plan(mla, [0, 16], [0, 16], ps=4, kd="fp8")
+    assert mla._lib.mla_prefill_run(*run_args(p, mem, out=mem + 16)) == 1
+    assert mla._lib.mla_prefill_run(*run_args(p, mem, cs=mem + 8, npos=4, pos=mem)) == 1
+
+
 def test_prefill_run_refuses_pools(mla, mem):
     p = plan(mla, [0, 16], [0, 16], ps=4, kd="fp8")
     assert mla._lib.mla_prefill_run(*run_args(p, mem, idx=mem, rows=66)) == 1     # not whole pages
