@@ -497,11 +497,11 @@ mla_status mla_cache_write(const void* latent, int64_t latent_stride, const void
  * scores carry sm_scale.
  *
  *   q        bf16 [num_tokens][heads][192] with strides in elements, both
- *            multiples of 8; 16-byte aligned.
+ *            multiples of 8 (and below 2^39); 16-byte aligned.
  *   w        bf16 [heads][256][512] contiguous, 16-byte aligned.
  *   q_dtype  MLA_DTYPE_BF16 or MLA_DTYPE_FP8_E4M3 (the value divided by the
  *            device fp32 q_scale, saturating).
- *   q_out    [num_tokens][heads][576] contiguous, 16-byte aligned.
+ *   q_out    [num_tokens][heads][576] contiguous, 32-byte aligned.
  * mla_decode_run takes heads = 16.  Sums are held in fp32.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (q_dtype), MLA_ERR_CUDA.
  */
@@ -515,7 +515,7 @@ mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_st
  * mla_absorb_out -- the layer's attention output from the decode output:
  *     out[t,h,:] = w[h][128:256] o[t,h,:].
  *   o    bf16 [num_tokens][heads][512] contiguous, 16-byte aligned.
- *   out  bf16 [num_tokens][heads][128] contiguous, 16-byte aligned.
+ *   out  bf16 [num_tokens][heads][128] contiguous, 32-byte aligned.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
  */
 mla_status mla_absorb_out(const void* o, const void* w, int64_t num_tokens, int32_t heads,
@@ -596,7 +596,8 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  * mla_error_check -- synchronises `stream`, reads the device error word `err`
  * and clears it.  MLA_OK; MLA_ERR_CAPACITY (nothing but pages, table columns
  * or output entries ran out); MLA_ERR_INVALID_ARG (a length, page, slot or
- * position out of range; also err NULL); MLA_ERR_CUDA.
+ * position out of range; also err NULL); MLA_ERR_DEVICE_TIMEOUT (a bounded
+ * wait gave up); MLA_ERR_CUDA.
  */
 mla_status mla_error_check(int32_t* err, mla_stream_t stream);
 

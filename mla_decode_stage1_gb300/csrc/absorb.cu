@@ -1,19 +1,42 @@
-// absorb.cu -- the absorbed form's two products, in their simplest form: one
-// thread per output dim of one (token, head).
+// absorb.cu -- the absorbed form's two products.
+//
+//     mla_absorb_q    q_out[t,h,c] = f sum_d q[t,h,d] w[h][d][c]        (K = 128, N = 512)
+//                     q_out[t,h,512:] = f rotate(q[t,h,128:192])
+//     mla_absorb_out  out[t,h,v] = sum_c o[t,h,c] w[h][128+v][c]        (K = 512, N = 128)
+//
+// Bound: one pass over the weights (128 KB a head, each) for few tokens,
+// where the call is latency; memory for many.  Heads do not share weights, so
+// a CTA is (head, 128 tokens, slice of the output dims): slices are narrow
+// while there are few token tiles, so that the weights stream through all
+// SMs.  Operands come by TMA, the product runs on the tensor cores (rows past
+// the last token are computed from whatever the shared memory holds and never
+// written), the epilogue scales, rounds once and writes whole sectors.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "layer.h"
+#include "plan.h"
+#include "ptx.cuh"
 
 namespace mla {
 namespace {
 
+constexpr int kTokens = 128;                       // tokens of a CTA
+constexpr uint32_t kPanel = kTokens * 128;         // a row panel: 128 tokens x 64 bf16
+constexpr int kAbsorbThreads = 128;
+
+// Where a wait that gave up is noted when the caller has no error word.
+__device__ int32_t g_unreported;
+
 struct AbsorbQParams {
+  CUtensorMap map_q;           // {192, heads, tokens}, boxes {64, 1, box_rows}
+  CUtensorMap map_w;           // {512, 256, heads}, boxes {64, 128, 1}
   const uint16_t* q;
   int64_t token_stride, head_stride;
-  const uint16_t* w;
   int64_t tokens;
   int32_t heads;
+  int32_t box_rows;            // tokens a box brings (128, or fewer when there are fewer)
   float factor;                // 24 sm_scale
   Rotation rot;
   const float* q_scale;        // null: bf16 out
@@ -21,57 +44,289 @@ struct AbsorbQParams {
   int32_t* err;
 };
 
+struct AbsorbOutParams {
+  CUtensorMap map_o;           // {512, heads, tokens}, boxes {64, 1, box_rows}
+  CUtensorMap map_w;           // {512, 256, heads}, boxes {64, N, 1}
+  int64_t tokens;
+  int32_t heads;
+  int32_t box_rows;
+  uint16_t* out;
+};
+
 __device__ __forceinline__ float bf16f(uint16_t v) {
   return __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
-__device__ __forceinline__ uint16_t bf16r(float v) {
-  const __nv_bfloat16 b = __float2bfloat16_rn(v);
-  return *reinterpret_cast<const uint16_t*>(&b);
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void store_q(const AbsorbQParams& p, int64_t at, float v) {
-  if (p.q_scale == nullptr)
-    static_cast<uint16_t*>(p.out)[at] = bf16r(v);
-  else
-    static_cast<uint8_t*>(p.out)[at] =
-        static_cast<uint8_t>(to_e4m3x2(__fdiv_rn(v, *p.q_scale), 0.0f) & 0xff);
-}
-
-__global__ void __launch_bounds__(kVDim) absorb_q_kernel(const AbsorbQParams p) {
-  __shared__ float x[kQHead];
-  const int c = threadIdx.x, h = blockIdx.y;
-  const int64_t t = blockIdx.x;
-  const uint16_t* q = p.q + t * p.token_stride + h * p.head_stride;
-  if (c < kQHead) x[c] = bf16f(q[c]);
-  __syncthreads();
-  const uint16_t* w = p.w + static_cast<int64_t>(h) * kWRows * kVDim + c;
-  float s = 0.0f;
-  for (int d = 0; d < kNope; ++d) s += x[d] * bf16f(w[d * kVDim]);
-  const int64_t at = (t * p.heads + h) * kQkDim;
-  store_q(p, at + c, s * p.factor);
-  if (c < kRope / 2) {
-    const int d0 = rope_dim0(c, p.rot.half), d1 = rope_dim1(c, p.rot.half);
-    float a = x[kNope + d0], b = x[kNope + d1];
-    if (p.rot.cos_sin != nullptr) {
-      const float* cs = rotation_row(p.rot, t, c == 0 ? p.err : nullptr);
-      rotate(a, b, cs[c], cs[kRope / 2 + c]);
-    }
-    store_q(p, at + kVDim + d0, a * p.factor);
-    store_q(p, at + kVDim + d1, b * p.factor);
+// One rotated pair of a row, scaled and stored at dims d0 and d1 behind the
+// 512 latent ones.
+__device__ __forceinline__ void store_pair(const AbsorbQParams& p, int64_t row, int d0, int d1,
+                                           float a, float b) {
+  const int64_t at = row * kQkDim + kVDim;
+  if (p.q_scale == nullptr) {
+    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+    const uint32_t v = bf16x2(a, b);
+    out[d0] = static_cast<uint16_t>(v & 0xffffu);
+    out[d1] = static_cast<uint16_t>(v >> 16);
+  } else {
+    uint8_t* out = static_cast<uint8_t*>(p.out) + at;
+    const uint16_t v = to_e4m3x2(__fdiv_rn(a, *p.q_scale), __fdiv_rn(b, *p.q_scale));
+    out[d0] = static_cast<uint8_t>(v & 0xff);
+    out[d1] = static_cast<uint8_t>(v >> 8);
   }
 }
 
-__global__ void __launch_bounds__(kVHead) absorb_out_kernel(const uint16_t* o, const uint16_t* w,
-                                                            uint16_t* out, int32_t heads) {
-  __shared__ float x[kVDim];
-  const int v = threadIdx.x, h = blockIdx.y;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * heads + h;
-  for (int c = v; c < kVDim; c += kVHead) x[c] = bf16f(o[at * kVDim + c]);
+// N output dims a CTA; kSlices = 512 / N CTAs share a (head, token tile) and
+// the rotation of its rows.
+template <int N>
+__global__ void __launch_bounds__(kAbsorbThreads)
+    absorb_q_kernel(const __grid_constant__ AbsorbQParams p) {
+  constexpr int kSlices = kVDim / N;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full, done;
+  __shared__ uint32_t tmem_base;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t a_smem = smem_u32(smem), b_smem = a_smem + 2 * kPanel;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int slice = blockIdx.x % kSlices, h = blockIdx.y;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / kSlices) * kTokens;
+  int32_t* err = p.err != nullptr ? p.err : &g_unreported;
+  if (warp == 0) {
+    if (elect_one()) {
+      mbar_init(smem_u32(&full), 1);
+      mbar_init(smem_u32(&done), 1);
+      fence_mbar_init();
+      mbar_arrive_expect_tx(smem_u32(&full), 2 * p.box_rows * 128 + N / 64 * kPanel);
+      const uint64_t keep = l2_policy_evict_normal();
+      for (int ch = 0; ch < N / 64; ++ch)
+        tma_load_3d(b_smem + ch * kPanel, &p.map_w, smem_u32(&full), slice * N + 64 * ch, 0, h,
+                    keep);
+      for (int ch = 0; ch < 2; ++ch)
+        tma_load_3d(a_smem + ch * kPanel, &p.map_q, smem_u32(&full), 64 * ch, h,
+                    static_cast<int32_t>(t0), keep);
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(&tmem_base), N);
+    tmem_relinquish();
+  }
+  // rows slice, slice + kSlices, ... of the tile are rotated here, a warp per
+  // row and a pair per lane, while the operands are on their way
+  const int d0 = rope_dim0(lane, p.rot.half), d1 = rope_dim1(lane, p.rot.half);
+  for (int r = slice + kSlices * warp; r < kTokens && t0 + r < p.tokens; r += 4 * kSlices) {
+    const uint16_t* q = p.q + (t0 + r) * p.token_stride + h * p.head_stride + kNope;
+    float a = bf16f(q[d0]), b = bf16f(q[d1]);
+    if (p.rot.cos_sin != nullptr) {
+      const float* cs = rotation_row(p.rot, t0 + r, lane == 0 && h == 0 ? p.err : nullptr);
+      rotate(a, b, cs[lane], cs[kRope / 2 + lane]);
+    }
+    store_pair(p, (t0 + r) * p.heads + h, d0, d1, a * p.factor, b * p.factor);
+  }
+  tc_fence_before();
   __syncthreads();
-  const uint16_t* wr = w + (static_cast<int64_t>(h) * kWRows + kNope + v) * kVDim;
-  float s = 0.0f;
-  for (int c = 0; c < kVDim; ++c) s += x[c] * bf16f(wr[c]);
-  out[at * kVHead + v] = bf16r(s);
+  tc_fence_after();
+  const uint32_t tmem = uniform(tmem_base);
+  bool ok = true;
+  if (warp == 0) {
+    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full), 0, err, kErrProducer));
+    tc_fence_after();
+    if (elect_one()) {
+      if (ok) {
+        constexpr uint32_t idesc = make_idesc(1, 1, false, true, 128, N);
+        const uint64_t a = smem_desc(a_smem, 16, 1024, kSwizzle128B);
+        const uint64_t b = smem_desc(b_smem, kPanel, 1024, kSwizzle128B);
+#pragma unroll
+        for (int kk = 0; kk < kNope / 16; ++kk)      // 16 dims: 32 bytes of A, 2 row groups of B
+          umma_f16(tmem, a + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), b + ((kk * 2048) >> 4),
+                   idesc, kk != 0);
+      }
+      tc_commit(smem_u32(&done));
+    }
+    __syncwarp();
+  }
+  ok = mbar_wait(smem_u32(&done), 0, err, kErrDrain) && ok;
+  ok = __all_sync(0xffffffffu, ok);
+  tc_fence_after();
+  const int64_t t = t0 + warp * 32 + lane;
+  if (ok) {
+    const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
+    const float sc = p.q_scale != nullptr ? *p.q_scale : 1.0f;
+    const int64_t at = (t * p.heads + h) * kQkDim + slice * N;
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) {
+      uint32_t x[32], u[16];
+      __syncwarp();
+      tmem_ld32(acc + 32 * c, x);
+      tmem_wait_ld();
+      if (t >= p.tokens) {
+        // past the last token
+      } else if (p.q_scale == nullptr) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          u[i] = bf16x2(__uint_as_float(x[2 * i]) * p.factor,
+                        __uint_as_float(x[2 * i + 1]) * p.factor);
+        uint16_t* out = static_cast<uint16_t*>(p.out) + at + 32 * c;
+        st_global_32(out, u);
+        st_global_32(out + 16, u + 8);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            f[k] = __fdiv_rn(__uint_as_float(x[4 * i + k]) * p.factor, sc);
+          u[i] = to_e4m3x2(f[0], f[1]) | (static_cast<uint32_t>(to_e4m3x2(f[2], f[3])) << 16);
+        }
+        st_global_32(static_cast<uint8_t*>(p.out) + at + 32 * c, u);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, N);
+}
+
+// N output dims a CTA, S stages of 64 latent dims.
+template <int N, int S>
+__global__ void __launch_bounds__(kAbsorbThreads)
+    absorb_out_kernel(const __grid_constant__ AbsorbOutParams p) {
+  constexpr int kSlices = kVHead / N, kSteps = kVDim / 64;
+  constexpr uint32_t kStage = kPanel + N * 128;
+  constexpr uint32_t kCols = N < 32 ? 32 : N;        // tensor memory comes in 32 columns
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[S], empty[S], done;
+  __shared__ uint32_t tmem_base;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_u32(smem);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int slice = blockIdx.x % kSlices, h = blockIdx.y;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / kSlices) * kTokens;
+  const uint64_t keep = l2_policy_evict_normal();
+  auto load = [&](int step) {
+    const int s = step % S;
+    const uint32_t bar = smem_u32(&full[s]);
+    mbar_arrive_expect_tx(bar, p.box_rows * 128 + N * 128);
+    tma_load_3d(base + s * kStage + kPanel, &p.map_w, bar, 64 * step, kNope + slice * N, h, keep);
+    tma_load_3d(base + s * kStage, &p.map_o, bar, 64 * step, h, static_cast<int32_t>(t0), keep);
+  };
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < S; ++s) {
+        mbar_init(smem_u32(&full[s]), 1);
+        mbar_init(smem_u32(&empty[s]), 1);
+      }
+      mbar_init(smem_u32(&done), 1);
+      fence_mbar_init();
+      for (int s = 0; s < S; ++s) load(s);
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(&tmem_base), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(tmem_base);
+  bool ok = true;
+  if (warp == 0) {
+    constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, N);
+    const uint64_t a0 = smem_desc(base, 16, 1024, kSwizzle128B);
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step) {
+      const int s = step % S;
+      // (every copy is waited for, also when an earlier wait gave up)
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), (step / S) & 1, &g_unreported,
+                                             kErrProducer)) && ok;
+      tc_fence_after();
+      const uint64_t a = a0 + ((s * kStage) >> 4), b = a + (kPanel >> 4);
+      if (elect_one()) {
+        if (ok) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16(tmem, a + 2 * kk, b + 2 * kk, idesc, (step | kk) != 0);
+        }
+        tc_commit(smem_u32(&empty[s]));
+      }
+      // refill the stage of the step before: its products are behind this one's
+      if (step >= 1 && step - 1 + S < kSteps) {
+        const int back = step - 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[back % S]), (back / S) & 1,
+                                               &g_unreported, kErrMma)) && ok;
+        if (elect_one()) load(back + S);
+      }
+    }
+    if (elect_one()) tc_commit(smem_u32(&done));
+    __syncwarp();
+  }
+  ok = mbar_wait(smem_u32(&done), 0, &g_unreported, kErrDrain) && ok;
+  ok = __all_sync(0xffffffffu, ok);
+  tc_fence_after();
+  const int64_t t = t0 + warp * 32 + lane;
+  if (ok) {
+    const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
+    uint16_t* out = p.out + (t * p.heads + h) * kVHead + slice * N;
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+      float x[16];
+      uint32_t u[8];
+      __syncwarp();
+      tmem_ld16(acc + 16 * c, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = bf16x2(x[2 * i], x[2 * i + 1]);
+      if (t < p.tokens) st_global_32(out + 16 * c, u);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kCols);
+}
+
+// A 3-D tensor of bf16 in 64-element boxes with the 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* ptr, cuuint64_t d0, cuuint64_t d1, cuuint64_t d2,
+              cuuint64_t s1, cuuint64_t s2, cuuint32_t b1, cuuint32_t b2) {
+  const TiledEncoder enc = tiled_encoder();
+  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1 * 2, s2 * 2};
+  const cuuint32_t box[3] = {64, b1, b2}, one[3] = {1, 1, 1};
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens that a box brings: all 128 of a tile, or, when there are fewer in
+// all, a multiple of 8 that holds them.
+int32_t box_rows_for(int64_t tokens) {
+  return tokens >= kTokens ? kTokens : static_cast<int32_t>((tokens + 7) / 8 * 8);
+}
+
+template <int N>
+cudaError_t launch_q(const AbsorbQParams& p, int64_t tiles, cudaStream_t stream) {
+  constexpr int bytes = (2 + N / 64) * kPanel + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(absorb_q_kernel<N>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  absorb_q_kernel<N><<<dim3(static_cast<unsigned>(tiles * (kVDim / N)), p.heads), kAbsorbThreads,
+                       bytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int N, int S>
+cudaError_t launch_out(AbsorbOutParams& p, const void* w, int64_t tiles, cudaStream_t stream) {
+  constexpr int bytes = S * (kPanel + N * 128) + 1024;
+  if (!make_map(&p.map_w, w, kVDim, kWRows, p.heads, kVDim, kVDim * kWRows, N, 1))
+    return cudaErrorUnknown;
+  const cudaError_t e = cudaFuncSetAttribute(absorb_out_kernel<N, S>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  absorb_out_kernel<N, S><<<dim3(static_cast<unsigned>(tiles * (kVHead / N)), p.heads),
+                            kAbsorbThreads, bytes, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -95,17 +350,34 @@ extern "C" mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_
     return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (q == nullptr || w == nullptr || q_out == nullptr) return MLA_ERR_INVALID_ARG;
-  if (!ptr_aligned(q, 16) || !ptr_aligned(w, 16) || !ptr_aligned(q_out, 16) ||
+  if (!ptr_aligned(q, 16) || !ptr_aligned(w, 16) || !ptr_aligned(q_out, 32) ||
+      q_token_stride >= (1LL << 39) || q_head_stride >= (1LL << 39) ||
       q_token_stride < mla::kQHead || q_head_stride < mla::kQHead || q_token_stride % 8 != 0 ||
       q_head_stride % 8 != 0)
     return MLA_ERR_INVALID_ARG;
-  const mla::AbsorbQParams p{static_cast<const uint16_t*>(q), q_token_stride, q_head_stride,
-                             static_cast<const uint16_t*>(w), num_tokens, heads,
-                             24.0f * sm_scale, rot,
-                             q_dtype == MLA_DTYPE_FP8_E4M3 ? q_scale : nullptr, q_out, err};
-  mla::absorb_q_kernel<<<dim3(static_cast<unsigned>(num_tokens), heads), mla::kVDim, 0,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  mla::AbsorbQParams p{};
+  p.box_rows = mla::box_rows_for(num_tokens);
+  if (!mla::make_map(&p.map_q, q, mla::kQHead, heads, num_tokens, q_head_stride, q_token_stride, 1,
+                     p.box_rows) ||
+      !mla::make_map(&p.map_w, w, mla::kVDim, mla::kWRows, heads, mla::kVDim,
+                     mla::kVDim * mla::kWRows, mla::kNope, 1))
+    return MLA_ERR_CUDA;
+  p.q = static_cast<const uint16_t*>(q);
+  p.token_stride = q_token_stride;
+  p.head_stride = q_head_stride;
+  p.tokens = num_tokens;
+  p.heads = heads;
+  p.factor = 24.0f * sm_scale;
+  p.rot = rot;
+  p.q_scale = q_dtype == MLA_DTYPE_FP8_E4M3 ? q_scale : nullptr;
+  p.out = q_out;
+  p.err = err;
+  const int64_t tiles = (num_tokens + mla::kTokens - 1) / mla::kTokens;
+  // eight slices of 64 dims until the (head, token tile)s alone fill the SMs
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e =
+      tiles * heads < 76 ? mla::launch_q<64>(p, tiles, s) : mla::launch_q<128>(p, tiles, s);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 extern "C" mla_status mla_absorb_out(const void* o, const void* w, int64_t num_tokens,
@@ -115,11 +387,22 @@ extern "C" mla_status mla_absorb_out(const void* o, const void* w, int64_t num_t
     return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (o == nullptr || w == nullptr || out == nullptr || !ptr_aligned(o, 16) ||
-      !ptr_aligned(w, 16) || !ptr_aligned(out, 16))
+      !ptr_aligned(w, 16) || !ptr_aligned(out, 32))
     return MLA_ERR_INVALID_ARG;
-  mla::absorb_out_kernel<<<dim3(static_cast<unsigned>(num_tokens), heads), mla::kVHead, 0,
-                           reinterpret_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(w),
-      static_cast<uint16_t*>(out), heads);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  mla::AbsorbOutParams p{};
+  p.box_rows = mla::box_rows_for(num_tokens);
+  if (!mla::make_map(&p.map_o, o, mla::kVDim, heads, num_tokens, mla::kVDim,
+                     static_cast<int64_t>(heads) * mla::kVDim, 1, p.box_rows))
+    return MLA_ERR_CUDA;
+  p.tokens = num_tokens;
+  p.heads = heads;
+  p.out = static_cast<uint16_t*>(out);
+  const int64_t tiles = (num_tokens + mla::kTokens - 1) / mla::kTokens, units = tiles * heads;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // narrower slices of the 128 output dims while there are few (head, token tile)s
+  const cudaError_t e = units < 24    ? mla::launch_out<16, 8>(p, w, tiles, s)
+                        : units < 48  ? mla::launch_out<32, 8>(p, w, tiles, s)
+                        : units < 96  ? mla::launch_out<64, 4>(p, w, tiles, s)
+                                      : mla::launch_out<128, 3>(p, w, tiles, s);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

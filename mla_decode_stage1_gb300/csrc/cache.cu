@@ -501,5 +501,6 @@ extern "C" mla_status mla_error_check(int32_t* err, mla_stream_t stream_) {
     return MLA_ERR_CUDA;
   if (word == 0) return MLA_OK;
   if (cudaMemsetAsync(err, 0, sizeof(word), stream) != cudaSuccess) return MLA_ERR_CUDA;
+  if (word & mla::kErrTimeout) return MLA_ERR_DEVICE_TIMEOUT;
   return word == mla::kErrCapacity ? MLA_ERR_CAPACITY : MLA_ERR_INVALID_ARG;
 }
