@@ -63,8 +63,8 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 // One rotated pair of a row, scaled and stored at dims d0 and d1 behind the
 // 512 latent ones.
-__device__ __forceinline__ void store_pair(const AbsorbQParams& p, int64_t row, int d0, int d1,
-                                           float a, float b) {
+__device__ __forceinline__ void store_pair(const AbsorbQParams& p, const Fp8Scale& fs, int64_t row,
+                                           int d0, int d1, float a, float b) {
   const int64_t at = row * kQkDim + kVDim;
   if (p.q_scale == nullptr) {
     uint16_t* out = static_cast<uint16_t*>(p.out) + at;
@@ -73,7 +73,9 @@ __device__ __forceinline__ void store_pair(const AbsorbQParams& p, int64_t row, 
     out[d1] = static_cast<uint16_t>(v >> 16);
   } else {
     uint8_t* out = static_cast<uint8_t*>(p.out) + at;
-    const uint16_t v = to_e4m3x2(__fdiv_rn(a, *p.q_scale), __fdiv_rn(b, *p.q_scale));
+    const float pair[2] = {a, b};
+    uint32_t v;
+    to_e4m3<2>(pair, fs, &v);
     out[d0] = static_cast<uint8_t>(v & 0xff);
     out[d1] = static_cast<uint8_t>(v >> 8);
   }
@@ -115,15 +117,30 @@ __global__ void __launch_bounds__(kAbsorbThreads)
   }
   // rows slice, slice + kSlices, ... of the tile are rotated here, a warp per
   // row and a pair per lane, while the operands are on their way
+  // (all of a warp's rows are loaded before the first is turned)
+  constexpr int kRows = kTokens / (4 * kSlices);
+  const Fp8Scale fs = p.q_scale != nullptr ? load_fp8_scale(p.q_scale) : Fp8Scale{1.0f, 1.0f, true};
   const int d0 = rope_dim0(lane, p.rot.half), d1 = rope_dim1(lane, p.rot.half);
-  for (int r = slice + kSlices * warp; r < kTokens && t0 + r < p.tokens; r += 4 * kSlices) {
-    const uint16_t* q = p.q + (t0 + r) * p.token_stride + h * p.head_stride + kNope;
-    float a = bf16f(q[d0]), b = bf16f(q[d1]);
+  float a[kRows], b[kRows], c[kRows], s[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t t = t0 + slice + kSlices * (warp + 4 * i);
+    if (t >= p.tokens) continue;
+    const uint16_t* q = p.q + t * p.token_stride + h * p.head_stride + kNope;
+    a[i] = bf16f(q[d0]);
+    b[i] = bf16f(q[d1]);
     if (p.rot.cos_sin != nullptr) {
-      const float* cs = rotation_row(p.rot, t0 + r, lane == 0 && h == 0 ? p.err : nullptr);
-      rotate(a, b, cs[lane], cs[kRope / 2 + lane]);
+      const float* cs = rotation_row(p.rot, t, lane == 0 && h == 0 ? p.err : nullptr);
+      c[i] = cs[lane];
+      s[i] = cs[kRope / 2 + lane];
     }
-    store_pair(p, (t0 + r) * p.heads + h, d0, d1, a * p.factor, b * p.factor);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t t = t0 + slice + kSlices * (warp + 4 * i);
+    if (t >= p.tokens) continue;
+    if (p.rot.cos_sin != nullptr) rotate(a[i], b[i], c[i], s[i]);
+    store_pair(p, fs, t * p.heads + h, d0, d1, a[i] * p.factor, b[i] * p.factor);
   }
   tc_fence_before();
   __syncthreads();
@@ -153,7 +170,6 @@ __global__ void __launch_bounds__(kAbsorbThreads)
   const int64_t t = t0 + warp * 32 + lane;
   if (ok) {
     const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
-    const float sc = p.q_scale != nullptr ? *p.q_scale : 1.0f;
     const int64_t at = (t * p.heads + h) * kQkDim + slice * N;
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) {
@@ -172,14 +188,10 @@ __global__ void __launch_bounds__(kAbsorbThreads)
         st_global_32(out, u);
         st_global_32(out + 16, u + 8);
       } else {
+        float f[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float f[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            f[k] = __fdiv_rn(__uint_as_float(x[4 * i + k]) * p.factor, sc);
-          u[i] = to_e4m3x2(f[0], f[1]) | (static_cast<uint32_t>(to_e4m3x2(f[2], f[3])) << 16);
-        }
+        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(x[i]) * p.factor;
+        to_e4m3<32>(f, fs, u);
         st_global_32(static_cast<uint8_t*>(p.out) + at + 32 * c, u);
       }
     }

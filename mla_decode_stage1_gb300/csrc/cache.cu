@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "layer.h"
+#include "ptx.cuh"
 
 namespace mla {
 namespace {
@@ -210,7 +211,16 @@ __device__ __forceinline__ float f16_hi(uint32_t v) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
 }
 
-// (hi, lo) += v with the rounding error of the sum added to lo.
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {      // (a - b, rounded once)
+  return fma_f32x2(b, pack_f32x2(-1.0f, -1.0f), a);
+}
+// (hi, lo) += v with the rounding error of the sum added to lo (Knuth's
+// error-free sum), two sums side by side or one.
+__device__ __forceinline__ void sum_exactly2(uint64_t& hi, uint64_t& lo, uint64_t v) {
+  const uint64_t s = add_f32x2(hi, v), t = sub2(s, hi);
+  lo = add_f32x2(lo, add_f32x2(sub2(hi, sub2(s, t)), sub2(v, t)));
+  hi = s;
+}
 __device__ __forceinline__ void sum_exactly(float& hi, float& lo, float v) {
   const float s = __fadd_rn(hi, v);
   const float t = __fsub_rn(s, hi);
@@ -234,33 +244,47 @@ __device__ __forceinline__ float mag_max(float a, float b) {
   return __uint_as_float(max(x, y));
 }
 
+// What one warp loads of a token before it computes.
+struct TokenIn {
+  int64_t slot;
+  uint4 raw[2];                 // dims 8 lane .. and 256 + 8 lane ..
+  float ra, rb, c, s;           // rotation pair `lane` and its angle
+};
+
+__device__ __forceinline__ TokenIn load_token(const WriteParams& p, int64_t t, int lane, int d0,
+                                              int d1) {
+  TokenIn in;
+  in.slot = p.slots[t];
+  const uint16_t* src = p.latent + t * p.latent_stride;
+  in.raw[0] = *reinterpret_cast<const uint4*>(src + 8 * lane);
+  in.raw[1] = *reinterpret_cast<const uint4*>(src + 256 + 8 * lane);
+  const uint16_t* rsrc = p.k_rope + t * p.rope_stride;
+  in.ra = __uint_as_float(static_cast<uint32_t>(rsrc[d0]) << 16);
+  in.rb = __uint_as_float(static_cast<uint32_t>(rsrc[d1]) << 16);
+  if (p.rot.cos_sin != nullptr) {
+    const float* cs = rotation_row(p.rot, t, lane == 0 ? p.err : nullptr);
+    in.c = cs[lane];
+    in.s = cs[kRope / 2 + lane];
+  }
+  return in;
+}
+
+// Norm, rotation, encoding and store of one token.
 template <int KV>
-__global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (t >= p.tokens) return;
-  int64_t slot = p.slots[t];
+__device__ __forceinline__ void write_token(const WriteParams& p, int64_t t, const TokenIn& in,
+                                            int lane, int d0, int d1, const uint4& w0,
+                                            const uint4& w1) {
+  int64_t slot = in.slot;
   if (slot < -1 || slot >= p.pool_rows) {
     if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrBadSlot);
     slot = -1;
   }
-  // lane's latent dims: 8 from dim 8 lane, 8 from dim 256 + 8 lane
-  const uint16_t* src = p.latent + t * p.latent_stride;
-  uint4 raw[2];
-  raw[0] = *reinterpret_cast<const uint4*>(src + 8 * lane);
-  raw[1] = *reinterpret_cast<const uint4*>(src + 256 + 8 * lane);
-  const int half = p.rot.half, d0 = rope_dim0(lane, half), d1 = rope_dim1(lane, half);
-  const uint16_t* rsrc = p.k_rope + t * p.rope_stride;
-  float ra = __uint_as_float(static_cast<uint32_t>(rsrc[d0]) << 16);
-  float rb = __uint_as_float(static_cast<uint32_t>(rsrc[d1]) << 16);
-  if (p.rot.cos_sin != nullptr) {
-    const float* cs = rotation_row(p.rot, t, lane == 0 ? p.err : nullptr);
-    rotate(ra, rb, cs[lane], cs[kRope / 2 + lane]);
-  }
+  float ra = in.ra, rb = in.rb;
+  if (p.rot.cos_sin != nullptr) rotate(ra, rb, in.c, in.s);
   float y[16];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const uint32_t u[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+    const uint32_t u[4] = {in.raw[g].x, in.raw[g].y, in.raw[g].z, in.raw[g].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       y[8 * g + 2 * i] = bf16_lo(u[i]);
@@ -268,16 +292,24 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
     }
   }
   if (p.weight != nullptr) {
-    float hi = 0.0f, lo = 0.0f;
+    uint64_t hi2 = 0, lo2 = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum_exactly(hi, lo, __fmul_rn(y[i], y[i]));
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t v = pack_f32x2(y[2 * i], y[2 * i + 1]);
+      sum_exactly2(hi2, lo2, mul_f32x2(v, v));
+    }
+    float hi, lo, h1, l1;
+    unpack_f32x2(hi2, hi, h1);
+    unpack_f32x2(lo2, lo, l1);
+    lo = __fadd_rn(lo, l1);
+    sum_exactly(hi, lo, h1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float oh = __shfl_xor_sync(0xffffffffu, hi, o);
       const float ol = __shfl_xor_sync(0xffffffffu, lo, o);
       // the same operands in the same order in both lanes of a pair
       float a = (lane & o) ? oh : hi, b = (lane & o) ? hi : oh;
-      float c = (lane & o) ? __fadd_rn(ol, lo) : __fadd_rn(lo, ol);
+      float c = __fadd_rn(lo, ol);
       sum_exactly(a, c, b);
       hi = a;
       lo = c;
@@ -286,14 +318,13 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
     // a sum that is not finite has no error term
     if (!(fabsf(hi) < INFINITY)) sum = hi;
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(sum * (1.0f / kVDim), p.eps)));
-    const uint4 w0 = *reinterpret_cast<const uint4*>(p.weight + 8 * lane);
-    const uint4 w1 = *reinterpret_cast<const uint4*>(p.weight + 256 + 8 * lane);
     const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    const uint64_t r2 = pack_f32x2(r, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[2 * i] = __fmul_rn(__fmul_rn(y[2 * i], r), bf16_lo(w[i]));
-      y[2 * i + 1] = __fmul_rn(__fmul_rn(y[2 * i + 1], r), bf16_hi(w[i]));
-    }
+    for (int i = 0; i < 8; ++i)
+      unpack_f32x2(mul_f32x2(mul_f32x2(pack_f32x2(y[2 * i], y[2 * i + 1]), r2),
+                        pack_f32x2(bf16_lo(w[i]), bf16_hi(w[i]))),
+                   y[2 * i], y[2 * i + 1]);
   }
   uint16_t* out = p.rows != nullptr ? p.rows + t * kQkDim : nullptr;
   if constexpr (KV == MLA_DTYPE_BF16) {
@@ -312,17 +343,16 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
     if (dst) { dst[kVDim + d0] = a; dst[kVDim + d1] = b; }
     if (out) { out[kVDim + d0] = a; out[kVDim + d1] = b; }
   } else if constexpr (KV == MLA_DTYPE_FP8_E4M3) {
-    const float sc = *p.kv_scale;
+    const Fp8Scale fs = load_fp8_scale(p.kv_scale);
+    const float sc = fs.sc;
     uint8_t* dst = slot >= 0 ? p.kv + slot * kQkDim : nullptr;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      uint32_t c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c[i] = to_e4m3x2(__fdiv_rn(y[8 * g + 2 * i], sc), __fdiv_rn(y[8 * g + 2 * i + 1], sc));
+      uint32_t v8[2];
+      to_e4m3<8>(y + 8 * g, fs, v8);
+      const uint32_t c[4] = {v8[0] & 0xffffu, v8[0] >> 16, v8[1] & 0xffffu, v8[1] >> 16};
       if (dst)
-        *reinterpret_cast<uint2*>(dst + 256 * g + 8 * lane) =
-            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        *reinterpret_cast<uint2*>(dst + 256 * g + 8 * lane) = make_uint2(v8[0], v8[1]);
       if (out) {
         uint32_t v[4];
 #pragma unroll
@@ -333,8 +363,13 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
         *reinterpret_cast<uint4*>(out + 256 * g + 8 * lane) = make_uint4(v[0], v[1], v[2], v[3]);
       }
     }
-    const uint16_t c = to_e4m3x2(__fdiv_rn(ra, sc), __fdiv_rn(rb, sc));
-    if (dst) {
+    const float pair[2] = {ra, rb};
+    uint32_t c2;
+    to_e4m3<2>(pair, fs, &c2);
+    const uint16_t c = static_cast<uint16_t>(c2);
+    if (dst && !p.rot.half) {
+      *reinterpret_cast<uint16_t*>(dst + kVDim + d0) = c;
+    } else if (dst) {
       dst[kVDim + d0] = static_cast<uint8_t>(c & 0xff);
       dst[kVDim + d1] = static_cast<uint8_t>(c >> 8);
     }
@@ -380,7 +415,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
     // the first; in halves, every lane holds one dim of each.  Lane i then
     // stores byte i, the dims (2i, 2i+1), and lanes 0 and 16 the exponents.
     float va = ra, vb = rb;
-    if (half) {
+    if (p.rot.half) {
       // dims (2i, 2i+1) are the a (i < 16) or b (i >= 16) of lanes 2i, 2i+1 (mod 32)
       const int s0 = (2 * lane) & 31, s1 = (2 * lane + 1) & 31;
       const float a0 = __shfl_sync(0xffffffffu, ra, s0), a1 = __shfl_sync(0xffffffffu, ra, s1);
@@ -405,6 +440,21 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const WriteParams p) {
           pack_bf16(f16_lo(h) * down, f16_hi(h) * down);
     }
   }
+}
+
+template <int KV>
+__global__ void __launch_bounds__(256, 5) cache_write_kernel(const WriteParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (t >= p.tokens) return;
+  const int d0 = rope_dim0(lane, p.rot.half), d1 = rope_dim1(lane, p.rot.half);
+  const TokenIn in = load_token(p, t, lane, d0, d1);
+  uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+  if (p.weight != nullptr) {
+    w0 = *reinterpret_cast<const uint4*>(p.weight + 8 * lane);
+    w1 = *reinterpret_cast<const uint4*>(p.weight + 256 + 8 * lane);
+  }
+  write_token<KV>(p, t, in, lane, d0, d1, w0, w1);
 }
 
 }  // namespace
