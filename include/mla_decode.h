@@ -542,9 +542,9 @@ typedef struct mla_prefill mla_prefill;
 typedef struct {
   int32_t batch_size;
   int32_t heads;
-  int32_t num_ctas;          /* CTAs of the attention kernel */
-  int32_t num_items;         /* (up to 256 query rows, head, key range) */
-  int32_t num_partials;      /* items whose result is joined with others */
+  int32_t num_ctas;          /* CTAs of the attention kernels */
+  int32_t num_items;         /* (up to 512 query rows, head, key range) */
+  int32_t num_partials;      /* 256-row partial results that are joined */
   int64_t query_tokens;
   int64_t key_tokens;
   size_t workspace_bytes;

@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   float M = -INFINITY;
   bool nan = false;
   for (int s = 0; s < j.count; ++s) {
-    const float v = p.part_lse[static_cast<int64_t>(j.first + s) * kPfRows + i];
+    const float v = p.part_lse[static_cast<int64_t>(j.first + s * j.span) * kPfRows + i];
     nan |= v != v;
     M = fmaxf(M, v);
   }
@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   float wsum = 0.0f;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int s = 0; s < j.count; ++s) {
-    const int64_t at = static_cast<int64_t>(j.first + s) * kPfRows + i;
+    const int64_t at = static_cast<int64_t>(j.first + s * j.span) * kPfRows + i;
     const float v = p.part_lse[at];
     if (v == -INFINITY) continue;          // no key of this range is seen
     const float w = exp2f(v - M);
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 }  // namespace
 
 cudaError_t launch_join(const JoinParams& p, cudaStream_t stream) {
-  join_kernel<<<dim3(p.num_jobs, kPfRows / 8), 256, 0, stream>>>(p);
+  join_kernel<<<dim3(p.num_jobs, 2 * kPfRows / 8), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

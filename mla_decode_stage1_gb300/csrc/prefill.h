@@ -1,12 +1,13 @@
 // prefill.h -- internal interface between the host side of the expanded form
-// (prefill_api.cu) and its kernels (expand.cu, attn.cu).
+// (prefill_api.cu) and its kernels (expand.cu, rotate.cu, attn.cu, join.cu).
 #pragma once
 
 #include "layer.h"
 
 namespace mla {
 
-constexpr int kPfRows = 256;     // query rows of an item (two 128-row matrix tiles)
+constexpr int kPfRows = 256;     // query rows of a CTA's item (two 128-row matrix tiles); a pair's
+                                 // item has up to twice as many
 constexpr int kPfTile = 128;     // keys of a tile
 
 // 128 consecutive cached tokens of one request, expanded into workspace rows
@@ -26,9 +27,10 @@ struct AttnItem {
 };
 static_assert(sizeof(AttnItem) == 32, "an attention item is two int4");
 
-// Join of `count` consecutive partials of the same query rows and head.
+// Join of `count` consecutive partials, of `span` slots of 256 rows each, of
+// the same query rows and head.
 struct JoinJob {
-  int32_t q_row, rows, head, first, count, vis0, pad[2];
+  int32_t q_row, rows, head, first, count, vis0, span, pad;
 };
 
 struct ExpandParams {
@@ -50,15 +52,27 @@ struct ExpandParams {
   uint64_t stamp;
 };
 
+struct RotateParams {
+  const uint16_t* q;
+  int64_t q_token_stride, q_head_stride, q_tokens;
+  int32_t heads;
+  Rotation rot;
+  uint16_t* qr;                // [q_tokens][heads][64]
+  int32_t* err;
+  uint64_t stamp;
+};
+
 struct AttnParams {
   CUtensorMap map_q;           // {192, heads, tokens}, boxes {64, 1, 128}
+  CUtensorMap map_qr;          // the rotated query dims, from x = qr_x on: {64, heads, tokens}
+                               // (workspace), or map_q itself without a rotation
   CUtensorMap map_kx;          // {256, kx_rows, heads}, boxes {64, 64, 1}
   CUtensorMap map_kr;          // {64, kx_rows, 1}, boxes {64, 64, 1}
   const AttnItem* items;
   const int32_t* cta_indptr;
   int32_t heads;
+  int32_t qr_x;
   float scale_log2;            // sm_scale * log2(e)
-  Rotation rot;
   uint16_t* out;
   float* lse;
   float* part_o;               // [partials][256][128]
@@ -79,7 +93,9 @@ struct JoinParams {
 };
 
 cudaError_t launch_expand(const ExpandParams& p, int num_ctas, cudaStream_t stream);
+cudaError_t launch_rotate(const RotateParams& p, cudaStream_t stream);
 cudaError_t launch_attn(const AttnParams& p, int num_ctas, cudaStream_t stream);
+cudaError_t launch_attn_pairs(const AttnParams& p, int num_pairs, cudaStream_t stream);
 cudaError_t launch_join(const JoinParams& p, cudaStream_t stream);
 
 }  // namespace mla

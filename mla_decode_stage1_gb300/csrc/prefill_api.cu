@@ -18,19 +18,20 @@
 
 struct mla_prefill {
   int32_t bs = 0, heads = 0, page_size = 0, kv_dtype = 0, num_sms = 0;
-  int32_t num_ctas = 0, num_partials = 0;
+  int32_t num_ctas = 0, num_pairs = 0, num_partials = 0;
   int64_t q_tokens = 0, k_tokens = 0, kx_rows = 0, identity_rows = 0;
   std::vector<mla::ExpandTile> tiles;
-  std::vector<int32_t> cta_indptr;
+  // items of CTAs on their own, then of CTA pairs, each list by CTA or pair
+  std::vector<int32_t> cta_indptr, pair_indptr;
   std::vector<mla::AttnItem> items;
   std::vector<mla::JoinJob> jobs;
-  size_t off_tiles = 0, off_indptr = 0, off_items = 0, off_jobs = 0, off_kx = 0, off_kr = 0,
+  size_t off_tiles = 0, off_indptr = 0, off_pairs = 0, off_items = 0, off_jobs = 0, off_kx = 0, off_kr = 0, off_qr = 0,
          off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
   std::vector<uint8_t> table;
   uint64_t stamp = 0;
   // per-run caches: the workspace holding the table, the tensor maps and what they describe
   mutable void* uploaded_ws = nullptr;
-  CUtensorMap map_q, map_kx, map_kr, map_w;
+  CUtensorMap map_q, map_qr, map_kx, map_kr, map_w;
   const void* map_w_ptr = nullptr;
   const void* map_q_ptr = nullptr;
   int64_t map_q_ts = 0, map_q_hs = 0;
@@ -45,17 +46,19 @@ using mla::JoinJob;
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Costs of the assignment, in tenths of one 128-key step of a 256-row item.
-constexpr int64_t kPairCost = 10;     // both 128-row tiles of an item at work
+// Costs of the assignment, in tenths of one 128-key step of an item at full
+// width (256 rows on a CTA, 512 on a pair).
+constexpr int64_t kFullCost = 10;     // both query tiles of an item at work
 constexpr int64_t kSingleCost = 6;    // one of them
 constexpr int64_t kItemCost = 15;     // prologue and epilogue of an item
 constexpr int64_t kJoinCost = 40;     // a join launch, once
+constexpr int64_t kPairRows = 384;    // more query rows than this left: a pair's item
 
 int64_t item_tiles(const AttnItem& w) {
   return (static_cast<int64_t>(w.kv_end) - w.kv_begin + mla::kPfTile - 1) / mla::kPfTile;
 }
 int64_t item_cost(const AttnItem& w) {
-  return kItemCost + item_tiles(w) * (w.rows > mla::kPfTile ? kPairCost : kSingleCost);
+  return kItemCost + item_tiles(w) * (w.rows > mla::kPfTile ? kFullCost : kSingleCost);
 }
 
 // Number of ranges of at most `limit` tiles that an item is cut into.
@@ -109,8 +112,67 @@ std::vector<int64_t> costs_of(const std::vector<AttnItem>& items) {
   return c;
 }
 
+// Cuts the items' keys where that ends sooner on `ctas` CTAs (or pairs),
+// gives the parts their slots and join jobs and lists the items by CTA.
+// Returns the CTAs used.
+int32_t schedule(mla_prefill* P, const std::vector<AttnItem>& whole, int32_t ctas,
+                 std::vector<int32_t>* indptr) {
+  indptr->assign(1, static_cast<int32_t>(P->items.size()));
+  if (whole.empty()) return 0;
+  // Cut limit: the one whose longest-first assignment ends first.  With many
+  // more items than CTAs and none of them long, no cut can help.
+  int64_t total = 0, longest = 0, max_tiles = 0;
+  for (const AttnItem& w : whole) {
+    total += item_cost(w);
+    longest = std::max(longest, item_cost(w));
+    max_tiles = std::max(max_tiles, item_tiles(w));
+  }
+  int64_t best_limit = INT32_MAX;
+  if (2 * longest > std::max<int64_t>(1, total / ctas)) {
+    int64_t best = assign(whole, costs_of(whole), ctas, nullptr), seen = 0;
+    for (int64_t k = 2; k <= 64 && (max_tiles + k - 1) / k >= 4; ++k) {
+      const int64_t limit = (max_tiles + k - 1) / k;
+      if (limit == seen) continue;
+      seen = limit;
+      const std::vector<AttnItem> cut = cut_items(whole, limit);
+      if (cut.size() > whole.size() + 16u * ctas) break;
+      const int64_t most = assign(cut, costs_of(cut), ctas, nullptr) + kJoinCost;
+      if (most < best) {
+        best = most;
+        best_limit = limit;
+      }
+    }
+  }
+  std::vector<AttnItem> items = cut_items(whole, best_limit);
+  // slots, in item order: the parts of a whole item are neighbours
+  for (size_t i = 0; i < items.size();) {
+    size_t e = i + 1;
+    if (items[i].slot >= 0) {
+      while (e < items.size() && items[e].q_row == items[i].q_row &&
+             items[e].head == items[i].head)
+        ++e;
+      const int32_t span = (items[i].rows + mla::kPfRows - 1) / mla::kPfRows;
+      P->jobs.push_back(JoinJob{items[i].q_row, items[i].rows, items[i].head, P->num_partials,
+                                static_cast<int32_t>(e - i), items[i].vis0, span, 0});
+      for (size_t j = i; j < e; ++j) {
+        items[j].slot = P->num_partials;
+        P->num_partials += span;
+      }
+    }
+    i = e;
+  }
+  const int32_t used = static_cast<int32_t>(std::min<size_t>(ctas, items.size()));
+  std::vector<std::vector<int32_t>> of(used);
+  assign(items, costs_of(items), used, &of);
+  for (const std::vector<int32_t>& l : of) {
+    for (const int32_t i : l) P->items.push_back(items[i]);
+    indptr->push_back(static_cast<int32_t>(P->items.size()));
+  }
+  return used;
+}
+
 mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, const int32_t* last) {
-  std::vector<AttnItem> whole;
+  std::vector<AttnItem> singles, pairs;
   for (int32_t b = 0; b < P->bs; ++b) {
     const int64_t m = static_cast<int64_t>(qo[b + 1]) - qo[b];
     const int64_t np = static_cast<int64_t>(kvp[b + 1]) - kvp[b];
@@ -133,76 +195,30 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
       P->kx_rows += mla::kPfTile;
       if (P->kx_rows > INT32_MAX - mla::kPfTile) return MLA_ERR_INVALID_ARG;
     }
-    for (int64_t r0 = 0; r0 < m; r0 += mla::kPfRows) {
+    // Blocks of 512 rows go to pairs, what is left to CTAs on their own; a
+    // pair's second tile must be more than half full to be worth its CTAs.
+    for (int64_t r0 = 0; r0 < m;) {
+      const bool pair = m - r0 > kPairRows && P->num_sms >= 2;
       AttnItem w{};
       w.q_row = qo[b] + static_cast<int32_t>(r0);
-      w.rows = static_cast<int32_t>(std::min<int64_t>(mla::kPfRows, m - r0));
+      w.rows = static_cast<int32_t>(std::min<int64_t>((pair ? 2 : 1) * mla::kPfRows, m - r0));
       w.kv_row = static_cast<int32_t>(kv_row);
       w.vis0 = static_cast<int32_t>(n - m + 1 + r0);
       w.kv_end = std::max(0, w.vis0 + w.rows - 1);
       w.slot = -1;
       for (int32_t h = 0; h < P->heads; ++h) {
         w.head = h;
-        whole.push_back(w);
+        (pair ? pairs : singles).push_back(w);
       }
+      r0 += w.rows;
     }
   }
-  if (whole.size() > static_cast<size_t>(INT32_MAX / 64) ||
+  if (singles.size() + pairs.size() > static_cast<size_t>(INT32_MAX / 64) ||
       static_cast<int64_t>(P->tiles.size()) * P->heads > INT32_MAX)
     return MLA_ERR_INVALID_ARG;
   P->q_tokens = qo[P->bs];
-
-  // Cut limit: the one whose longest-first assignment ends first.  With many
-  // more items than CTAs and none of them long, no cut can help.
-  int64_t total = 0, longest = 0;
-  for (const AttnItem& w : whole) {
-    total += item_cost(w);
-    longest = std::max(longest, item_cost(w));
-  }
-  const int64_t mean = std::max<int64_t>(1, total / P->num_sms);
-  int64_t best_limit = INT32_MAX;
-  if (!whole.empty() && 2 * longest > mean) {
-    int64_t best = assign(whole, costs_of(whole), P->num_sms, nullptr);
-    int64_t max_tiles = 0;
-    for (const AttnItem& w : whole) max_tiles = std::max(max_tiles, item_tiles(w));
-    int64_t seen = 0;
-    for (int64_t k = 2; k <= 64 && (max_tiles + k - 1) / k >= 4; ++k) {
-      const int64_t limit = (max_tiles + k - 1) / k;
-      if (limit == seen) continue;
-      seen = limit;
-      const std::vector<AttnItem> cut = cut_items(whole, limit);
-      if (cut.size() > whole.size() + 16u * P->num_sms) break;
-      const int64_t most = assign(cut, costs_of(cut), P->num_sms, nullptr) + kJoinCost;
-      if (most < best) {
-        best = most;
-        best_limit = limit;
-      }
-    }
-  }
-  std::vector<AttnItem> items = cut_items(whole, best_limit);
-  // slots, in item order: the parts of a whole item are neighbours
-  for (size_t i = 0; i < items.size();) {
-    size_t e = i + 1;
-    if (items[i].slot >= 0) {
-      while (e < items.size() && items[e].q_row == items[i].q_row &&
-             items[e].head == items[i].head)
-        ++e;
-      P->jobs.push_back(JoinJob{items[i].q_row, items[i].rows, items[i].head, P->num_partials,
-                                static_cast<int32_t>(e - i), items[i].vis0, {0, 0}});
-      for (size_t j = i; j < e; ++j) items[j].slot = P->num_partials++;
-    }
-    i = e;
-  }
-  P->num_ctas = static_cast<int32_t>(std::min<size_t>(P->num_sms, items.size()));
-  P->cta_indptr.assign(1, 0);
-  if (P->num_ctas > 0) {
-    std::vector<std::vector<int32_t>> of(P->num_ctas);
-    assign(items, costs_of(items), P->num_ctas, &of);
-    for (const std::vector<int32_t>& l : of) {
-      for (const int32_t i : l) P->items.push_back(items[i]);
-      P->cta_indptr.push_back(static_cast<int32_t>(P->items.size()));
-    }
-  }
+  P->num_ctas = schedule(P, singles, P->num_sms, &P->cta_indptr);
+  P->num_pairs = schedule(P, pairs, P->num_sms / 2, &P->pair_indptr);
 
   size_t off = align256(sizeof(mla::WsHeader));
   auto take = [&](size_t bytes) {
@@ -212,11 +228,13 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   };
   P->off_tiles = take(sizeof(ExpandTile) * P->tiles.size());
   P->off_indptr = take(sizeof(int32_t) * P->cta_indptr.size());
+  P->off_pairs = take(sizeof(int32_t) * P->pair_indptr.size());
   P->off_items = take(sizeof(AttnItem) * P->items.size());
   P->off_jobs = take(sizeof(JoinJob) * P->jobs.size());
   P->table.assign(off, 0);
   P->off_kx = take(sizeof(uint16_t) * P->kx_rows * P->heads * mla::kWRows);
   P->off_kr = take(sizeof(uint16_t) * P->kx_rows * mla::kRope);
+  P->off_qr = take(sizeof(uint16_t) * P->q_tokens * P->heads * mla::kRope);
   P->off_part_o = take(sizeof(float) * P->num_partials * mla::kPfRows * mla::kVHead);
   P->off_part_lse = take(sizeof(float) * P->num_partials * mla::kPfRows);
   P->ws_bytes = off;
@@ -229,6 +247,7 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   put(0, &hdr, sizeof(hdr));
   put(P->off_tiles, P->tiles.data(), sizeof(ExpandTile) * P->tiles.size());
   put(P->off_indptr, P->cta_indptr.data(), sizeof(int32_t) * P->cta_indptr.size());
+  put(P->off_pairs, P->pair_indptr.data(), sizeof(int32_t) * P->pair_indptr.size());
   put(P->off_items, P->items.data(), sizeof(AttnItem) * P->items.size());
   put(P->off_jobs, P->jobs.data(), sizeof(JoinJob) * P->jobs.size());
   return MLA_OK;
@@ -293,7 +312,7 @@ mla_status mla_prefill_get_info(const mla_prefill* plan, mla_prefill_info* info)
   if (plan == nullptr || info == nullptr) return MLA_ERR_INVALID_ARG;
   info->batch_size = plan->bs;
   info->heads = plan->heads;
-  info->num_ctas = plan->num_ctas;
+  info->num_ctas = plan->num_ctas + 2 * plan->num_pairs;
   info->num_items = static_cast<int32_t>(plan->items.size());
   info->num_partials = plan->num_partials;
   info->query_tokens = plan->q_tokens;
@@ -347,6 +366,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
   int32_t* err = reinterpret_cast<int32_t*>(ws);
   uint16_t* kx = reinterpret_cast<uint16_t*>(ws + plan->off_kx);
   uint16_t* kr = reinterpret_cast<uint16_t*>(ws + plan->off_kr);
+  uint16_t* qr = reinterpret_cast<uint16_t*>(ws + plan->off_qr);
   float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
   float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
   if (!plan->tiles.empty()) {
@@ -377,8 +397,13 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.err = err;
     p.stamp = plan->stamp;
     if (mla::launch_expand(p, plan->num_sms, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    if (rot.cos_sin != nullptr) {
+      const mla::RotateParams r{static_cast<const uint16_t*>(q), q_token_stride, q_head_stride,
+                                plan->q_tokens, plan->heads, rot, qr, err, plan->stamp};
+      if (mla::launch_rotate(r, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    }
   }
-  if (plan->num_ctas > 0) {
+  if (plan->num_ctas > 0 || plan->num_pairs > 0) {
     if (plan->map_q_ptr != q || plan->map_q_ts != q_token_stride ||
         plan->map_q_hs != q_head_stride) {
       plan->map_q_ptr = nullptr;
@@ -401,26 +426,38 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
           (!make_map(&plan->map_kx, kx, {mla::kWRows, rows, static_cast<cuuint64_t>(plan->heads)},
                      {mla::kWRows * 2, rows * mla::kWRows * 2}, {64, 64, 1}) ||
            !make_map(&plan->map_kr, kr, {mla::kRope, rows, 1}, {mla::kRope * 2, rows * mla::kRope * 2},
-                     {64, 64, 1})))
+                     {64, 64, 1}) ||
+           !make_map(&plan->map_qr, qr,
+                     {mla::kRope, static_cast<cuuint64_t>(plan->heads),
+                      static_cast<cuuint64_t>(plan->q_tokens)},
+                     {mla::kRope * 2, static_cast<cuuint64_t>(plan->heads) * mla::kRope * 2},
+                     {64, 1, mla::kPfTile})))
         return MLA_ERR_CUDA;
       plan->map_ws = workspace;
     }
     mla::AttnParams p{};
     p.map_q = plan->map_q;
+    p.map_qr = rot.cos_sin != nullptr ? plan->map_qr : plan->map_q;
+    p.qr_x = rot.cos_sin != nullptr ? 0 : mla::kNope;
     p.map_kx = plan->map_kx;
     p.map_kr = plan->map_kr;
     p.items = reinterpret_cast<const AttnItem*>(ws + plan->off_items);
-    p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_indptr);
     p.heads = plan->heads;
     p.scale_log2 = sm_scale * mla::kLog2e;
-    p.rot = rot;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
     p.part_o = part_o;
     p.part_lse = part_lse;
     p.err = err;
     p.stamp = plan->stamp;
-    if (mla::launch_attn(p, plan->num_ctas, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    if (plan->num_pairs > 0) {
+      p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_pairs);
+      if (mla::launch_attn_pairs(p, plan->num_pairs, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    }
+    if (plan->num_ctas > 0) {
+      p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_indptr);
+      if (mla::launch_attn(p, plan->num_ctas, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    }
   }
   if (!plan->jobs.empty()) {
     const mla::JoinParams p{reinterpret_cast<const JoinJob*>(ws + plan->off_jobs),

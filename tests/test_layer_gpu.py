@@ -558,6 +558,20 @@ def test_prefill(mla, kv, q_lens, kv_lens, heads, page, rope, layout):
     check_prefill(mla, prefill_case(q_lens, kv_lens, heads, kv, page, rope, 31, layout))
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,heads,rope", [
+    ([512], [512], 1, "interleaved"), ([385], [385], 2, "half"), ([400, 1100], [5000, 1111], 1, None),
+    ([897, 3, 450], [1000, 300, 449], 2, "interleaved")])
+def test_prefill_blocks_of_512_rows(mla, q_lens, kv_lens, heads, rope):
+    # more than 384 rows: an item of two CTAs; the third case has a query without keys
+    check_prefill(mla, prefill_case(q_lens, kv_lens, heads, "bf16", 8, rope, 41))
+
+
+def test_prefill_blocks_of_512_rows_on_few_ctas(mla):
+    c = prefill_case([1500, 600], [1500, 2500], 2, "fp8", 16, "interleaved", 42)
+    for num_sms in (2, 5, 152):
+        check_prefill(mla, c, num_sms=num_sms)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8", "mxfp4"])
 def test_prefill_without_a_page_table(mla, kv):
     check_prefill(mla, prefill_case([70, 300], [200, 333], 2, kv, 1, "interleaved", 5, table=False))
