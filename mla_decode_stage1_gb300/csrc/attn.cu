@@ -170,8 +170,11 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
       }
     }
   };
+  // (the next item's description is loaded one item ahead, here and below)
+  AttnItem next = load_item(p.items + it0);
   for (int it = it0; it < it1 && ok; ++it) {
-    const AttnItem w = load_item(p.items + it);
+    const AttnItem w = next;
+    if (it + 1 < it1) next = load_item(p.items + it + 1);
     const int n0 = tile_steps<P>(w, 0), n1 = tile_steps<P>(w, 1), steps = max(n0, n1);
     if (steps == 0) continue;
     load_k(w, 0);
@@ -328,8 +331,10 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
         for (int i = 0; i < 2; ++i) commit<P>(&ms->empty[(k + i) % kSlots]);
     }
   };
+  AttnItem next = load_item(p.items + it0);
   for (int it = it0; it < it1; ++it) {
-    const AttnItem w = load_item(p.items + it);
+    const AttnItem w = next;
+    if (it + 1 < it1) next = load_item(p.items + it + 1);
     const int n0 = uniform(tile_steps<P>(w, 0)), n1 = uniform(tile_steps<P>(w, 1));
     const int steps = max(n0, n1);
     if (steps == 0) continue;
@@ -384,8 +389,10 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
   const uint32_t s_full = smem_u32(&ms->s_full[t]);
   uint32_t ns = 0, no = 0;
   const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2);
+  AttnItem next = load_item(p.items + it0);
   for (int it = it0; it < it1; ++it) {
-    const AttnItem w = load_item(p.items + it);
+    const AttnItem w = next;
+    if (it + 1 < it1) next = load_item(p.items + it + 1);
     const int n = tile_steps<P>(w, t);
     const int limit = min(w.kv_end, w.vis0 + row) - w.kv_begin;  // keys of this range it sees
     float m = -INFINITY, l = 0.0f;
@@ -479,35 +486,38 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
     const int64_t token = static_cast<int64_t>(w.q_row) + row;
     const int64_t part = static_cast<int64_t>(w.slot) * kPfRows + row;
     const int64_t at = token * p.heads + w.head;
-#pragma unroll 2
-    for (int q = 0; q < 8; ++q) {
-      float o[16];
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      uint32_t o[64];
       __syncwarp();
-      if (n > 0) {
-        tmem_ld16(to + 16 * q, o);
-        tmem_wait_ld();
-      }
+      tmem_ld32(to + 64 * half, o);              // (of an item without steps: not used)
+      tmem_ld32(to + 64 * half + 32, o + 32);
+      tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = seen ? o[i] * inv : 0.0f;
+      for (int i = 0; i < 64; ++i)
+        o[i] = seen ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
       if (!live) {
         // past the item's rows: nothing to write
       } else if (w.slot >= 0) {
-        uint32_t u[16];
+        float* dst = p.part_o + part * kVHead + 64 * half;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i]);
-        float* dst = p.part_o + part * kVHead + 16 * q;
-        st_global_32(dst, u);
-        st_global_32(dst + 8, u + 8);
+        for (int q = 0; q < 8; ++q) st_global_32(dst + 8 * q, o + 8 * q);
       } else {
-        uint32_t u[8];
+        uint16_t* dst = p.out + at * kVHead + 64 * half;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-          u[i] = *reinterpret_cast<const uint32_t*>(&v);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[16 * q + 2 * i]),
+                                                           __uint_as_float(o[16 * q + 2 * i + 1]));
+            u[i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          st_global_32(dst + 16 * q, u);
         }
-        st_global_32(p.out + at * kVHead + 16 * q, u);
       }
     }
+    tc_fence_before();
     if (live) {
       const float lse2 = seen ? m + __log2f(l) : -INFINITY;
       if (w.slot >= 0)
@@ -516,7 +526,6 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
         p.lse[at] = lse2 * kLn2;
     }
     __syncwarp();
-    tc_fence_before();
   }
 }
 
@@ -566,6 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   if (ms->ours) {
     const int at = P ? blockIdx.x / 2 : blockIdx.x;
     const int it0 = p.cta_indptr[at], it1 = p.cta_indptr[at + 1];
+    // Launched as a programmatic dependent: the kernels before it have to be
+    // through before their keys and queries are loaded, and, where it follows
+    // another attention kernel (`after_attn`), before it ends.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
       regs_raise<208>();
       run_softmax<P>(p, ms, tmem, it0, it1, rank, warp >> 2, warp & 3, lane);
@@ -573,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       regs_lower<88>();            // 2 x 208 + 88 = 3 x 168, the registers at launch
     }
     if (warp == 8) {
+      if (!p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
       if (lane == 0) run_loads<P>(p, ms, q_smem, ring, it0, it1, rank);
     } else if (warp == 9 && rank == 0) {
       run_products<P>(p, ms, q_smem, ring, tmem, uniform(it0), uniform(it1));
@@ -584,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     __syncwarp();
   }
+  if (p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if constexpr (P) {
@@ -605,11 +620,13 @@ cudaError_t launch(const AttnParams& p, int ctas, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {2, 1, 1};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = P ? 1 : 0;
+  cfg.numAttrs = P ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, attn_kernel<P>, p);
 }
 

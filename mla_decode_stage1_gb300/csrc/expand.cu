@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(ms->tmem);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (ms->ours) {
     const int64_t units = static_cast<int64_t>(p.num_tiles) * p.heads;
     const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
@@ -348,29 +349,42 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     }
     __syncwarp();
   }
+  // Nothing here needs the rotation of the queries; what follows needs both.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 13) tmem_dealloc(tmem, 512);
 }
 
 template <int KV>
-cudaError_t launch(const ExpandParams& p, int ctas, cudaStream_t stream) {
+cudaError_t launch(const ExpandParams& p, int ctas, bool dependent, cudaStream_t stream) {
   constexpr int bytes = kExpandSmem + 1024;
   const cudaError_t e =
       cudaFuncSetAttribute(expand_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  expand_kernel<KV><<<ctas, kExpandThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kExpandThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, expand_kernel<KV>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_expand(const ExpandParams& p, int num_ctas, cudaStream_t stream) {
+cudaError_t launch_expand(const ExpandParams& p, int num_ctas, bool dependent,
+                          cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(p.num_tiles) * p.heads;
   const int ctas = static_cast<int>(units < num_ctas ? units : num_ctas);
-  if (p.kv_dtype == MLA_DTYPE_BF16) return launch<MLA_DTYPE_BF16>(p, ctas, stream);
-  if (p.kv_dtype == MLA_DTYPE_FP8_E4M3) return launch<MLA_DTYPE_FP8_E4M3>(p, ctas, stream);
-  return launch<MLA_DTYPE_MXFP4>(p, ctas, stream);
+  if (p.kv_dtype == MLA_DTYPE_BF16) return launch<MLA_DTYPE_BF16>(p, ctas, dependent, stream);
+  if (p.kv_dtype == MLA_DTYPE_FP8_E4M3)
+    return launch<MLA_DTYPE_FP8_E4M3>(p, ctas, dependent, stream);
+  return launch<MLA_DTYPE_MXFP4>(p, ctas, dependent, stream);
 }
 
 }  // namespace mla

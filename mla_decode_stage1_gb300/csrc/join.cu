@@ -11,6 +11,7 @@ namespace {
 // out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max lse): one warp per
 // row of a job, four dims a lane.
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // a programmatic dependent
   if (reinterpret_cast<const WsHeader*>(p.err)->stamp != p.stamp) return;   // reported by attn_kernel
   const int lane = threadIdx.x & 31;
   const JoinJob j = p.jobs[blockIdx.x];
@@ -54,8 +55,16 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 }  // namespace
 
 cudaError_t launch_join(const JoinParams& p, cudaStream_t stream) {
-  join_kernel<<<dim3(p.num_jobs, 2 * kPfRows / 8), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_jobs, 2 * kPfRows / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, p);
 }
 
 }  // namespace mla

@@ -72,6 +72,7 @@ struct AttnParams {
   const int32_t* cta_indptr;
   int32_t heads;
   int32_t qr_x;
+  int32_t after_attn;          // 1: launched behind another attention kernel of the call
   float scale_log2;            // sm_scale * log2(e)
   uint16_t* out;
   float* lse;
@@ -92,7 +93,10 @@ struct JoinParams {
   uint64_t stamp;
 };
 
-cudaError_t launch_expand(const ExpandParams& p, int num_ctas, cudaStream_t stream);
+// The kernels of a call are programmatic dependents of one another, in the
+// order rotate, expand, attention (pairs, then single CTAs), join; the first
+// one launched is not (`dependent` for the expansion: the rotation precedes it).
+cudaError_t launch_expand(const ExpandParams& p, int num_ctas, bool dependent, cudaStream_t stream);
 cudaError_t launch_rotate(const RotateParams& p, cudaStream_t stream);
 cudaError_t launch_attn(const AttnParams& p, int num_ctas, cudaStream_t stream);
 cudaError_t launch_attn_pairs(const AttnParams& p, int num_pairs, cudaStream_t stream);

@@ -52,7 +52,9 @@ constexpr int64_t kFullCost = 10;     // both query tiles of an item at work
 constexpr int64_t kSingleCost = 6;    // one of them
 constexpr int64_t kItemCost = 15;     // prologue and epilogue of an item
 constexpr int64_t kJoinCost = 40;     // a join launch, once
-constexpr int64_t kPairRows = 384;    // more query rows than this left: a pair's item
+constexpr int64_t kLaunchCost = 40;   // a second attention kernel, once
+constexpr int64_t kPairRows = 384;    // a pair's item needs more query rows than this: half of
+                                      // its second tile must be there to be worth two CTAs
 
 int64_t item_tiles(const AttnItem& w) {
   return (static_cast<int64_t>(w.kv_end) - w.kv_begin + mla::kPfTile - 1) / mla::kPfTile;
@@ -112,13 +114,21 @@ std::vector<int64_t> costs_of(const std::vector<AttnItem>& items) {
   return c;
 }
 
-// Cuts the items' keys where that ends sooner on `ctas` CTAs (or pairs),
-// gives the parts their slots and join jobs and lists the items by CTA.
-// Returns the CTAs used.
-int32_t schedule(mla_prefill* P, const std::vector<AttnItem>& whole, int32_t ctas,
-                 std::vector<int32_t>* indptr) {
-  indptr->assign(1, static_cast<int32_t>(P->items.size()));
-  if (whole.empty()) return 0;
+// A list of items assigned to CTAs (or pairs).
+struct Schedule {
+  std::vector<AttnItem> items;      // by CTA
+  std::vector<int32_t> indptr{0};
+  std::vector<JoinJob> jobs;
+  int32_t ctas = 0, partials = 0;
+  int64_t most = 0;                 // the largest sum of costs
+};
+
+// Cuts the items' keys where that ends sooner on `ctas` CTAs (or pairs), gives
+// the parts their slots, from `slot0` on, and join jobs and lists the items by
+// CTA.
+Schedule schedule(const std::vector<AttnItem>& whole, int32_t ctas, int32_t slot0) {
+  Schedule S;
+  if (whole.empty()) return S;
   // Cut limit: the one whose longest-first assignment ends first.  With many
   // more items than CTAs and none of them long, no cut can help.
   int64_t total = 0, longest = 0, max_tiles = 0;
@@ -152,27 +162,49 @@ int32_t schedule(mla_prefill* P, const std::vector<AttnItem>& whole, int32_t cta
              items[e].head == items[i].head)
         ++e;
       const int32_t span = (items[i].rows + mla::kPfRows - 1) / mla::kPfRows;
-      P->jobs.push_back(JoinJob{items[i].q_row, items[i].rows, items[i].head, P->num_partials,
-                                static_cast<int32_t>(e - i), items[i].vis0, span, 0});
+      S.jobs.push_back(JoinJob{items[i].q_row, items[i].rows, items[i].head, slot0 + S.partials,
+                               static_cast<int32_t>(e - i), items[i].vis0, span, 0});
       for (size_t j = i; j < e; ++j) {
-        items[j].slot = P->num_partials;
-        P->num_partials += span;
+        items[j].slot = slot0 + S.partials;
+        S.partials += span;
       }
     }
     i = e;
   }
-  const int32_t used = static_cast<int32_t>(std::min<size_t>(ctas, items.size()));
-  std::vector<std::vector<int32_t>> of(used);
-  assign(items, costs_of(items), used, &of);
+  S.ctas = static_cast<int32_t>(std::min<size_t>(ctas, items.size()));
+  std::vector<std::vector<int32_t>> of(S.ctas);
+  S.most = assign(items, costs_of(items), S.ctas, &of) + (S.jobs.empty() ? 0 : kJoinCost);
   for (const std::vector<int32_t>& l : of) {
-    for (const int32_t i : l) P->items.push_back(items[i]);
-    indptr->push_back(static_cast<int32_t>(P->items.size()));
+    for (const int32_t i : l) S.items.push_back(items[i]);
+    S.indptr.push_back(static_cast<int32_t>(S.items.size()));
   }
-  return used;
+  return S;
+}
+
+// The items of a request's m query rows on one head each: blocks of 512 rows
+// for pairs while more than `pair_rows` are left, then of 256.
+void add_items(std::vector<AttnItem>* pairs, std::vector<AttnItem>* singles, int64_t pair_rows,
+               int32_t q_row, int64_t m, int64_t n, int64_t kv_row, int32_t heads) {
+  for (int64_t r0 = 0; r0 < m;) {
+    const bool pair = m - r0 > pair_rows;
+    AttnItem w{};
+    w.q_row = q_row + static_cast<int32_t>(r0);
+    w.rows = static_cast<int32_t>(std::min<int64_t>((pair ? 2 : 1) * mla::kPfRows, m - r0));
+    w.kv_row = static_cast<int32_t>(kv_row);
+    w.vis0 = static_cast<int32_t>(n - m + 1 + r0);
+    w.kv_end = std::max(0, w.vis0 + w.rows - 1);
+    w.slot = -1;
+    for (int32_t h = 0; h < heads; ++h) {
+      w.head = h;
+      (pair ? pairs : singles)->push_back(w);
+    }
+    r0 += w.rows;
+  }
 }
 
 mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, const int32_t* last) {
-  std::vector<AttnItem> singles, pairs;
+  // every row on CTAs on their own, or blocks of 512 rows on pairs and the rest so
+  std::vector<AttnItem> all, pairs, rest;
   for (int32_t b = 0; b < P->bs; ++b) {
     const int64_t m = static_cast<int64_t>(qo[b + 1]) - qo[b];
     const int64_t np = static_cast<int64_t>(kvp[b + 1]) - kvp[b];
@@ -195,30 +227,33 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
       P->kx_rows += mla::kPfTile;
       if (P->kx_rows > INT32_MAX - mla::kPfTile) return MLA_ERR_INVALID_ARG;
     }
-    // Blocks of 512 rows go to pairs, what is left to CTAs on their own; a
-    // pair's second tile must be more than half full to be worth its CTAs.
-    for (int64_t r0 = 0; r0 < m;) {
-      const bool pair = m - r0 > kPairRows && P->num_sms >= 2;
-      AttnItem w{};
-      w.q_row = qo[b] + static_cast<int32_t>(r0);
-      w.rows = static_cast<int32_t>(std::min<int64_t>((pair ? 2 : 1) * mla::kPfRows, m - r0));
-      w.kv_row = static_cast<int32_t>(kv_row);
-      w.vis0 = static_cast<int32_t>(n - m + 1 + r0);
-      w.kv_end = std::max(0, w.vis0 + w.rows - 1);
-      w.slot = -1;
-      for (int32_t h = 0; h < P->heads; ++h) {
-        w.head = h;
-        (pair ? pairs : singles).push_back(w);
-      }
-      r0 += w.rows;
+    add_items(nullptr, &all, INT64_MAX, qo[b], m, n, kv_row, P->heads);
+    add_items(&pairs, &rest, kPairRows, qo[b], m, n, kv_row, P->heads);
+    if (all.size() > static_cast<size_t>(INT32_MAX / 64)) return MLA_ERR_INVALID_ARG;
+  }
+  if (static_cast<int64_t>(P->tiles.size()) * P->heads > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  P->q_tokens = qo[P->bs];
+  // Pairs take nine tenths of the time of single CTAs for the same rows, but
+  // rows of both kinds run one after the other: whichever ends first.
+  Schedule single = schedule(all, P->num_sms, 0), pair;
+  if (!pairs.empty() && P->num_sms >= 2) {
+    Schedule a = schedule(pairs, P->num_sms / 2, 0);
+    Schedule b = schedule(rest, P->num_sms, a.partials);
+    if (9 * a.most / 10 + b.most + (b.ctas > 0 ? kLaunchCost : 0) < single.most) {
+      pair = std::move(a);
+      single = std::move(b);
     }
   }
-  if (singles.size() + pairs.size() > static_cast<size_t>(INT32_MAX / 64) ||
-      static_cast<int64_t>(P->tiles.size()) * P->heads > INT32_MAX)
-    return MLA_ERR_INVALID_ARG;
-  P->q_tokens = qo[P->bs];
-  P->num_ctas = schedule(P, singles, P->num_sms, &P->cta_indptr);
-  P->num_pairs = schedule(P, pairs, P->num_sms / 2, &P->pair_indptr);
+  P->num_ctas = single.ctas;
+  P->num_pairs = pair.ctas;
+  P->num_partials = single.partials + pair.partials;
+  P->items = single.items;
+  P->items.insert(P->items.end(), pair.items.begin(), pair.items.end());
+  P->cta_indptr = single.indptr;
+  P->pair_indptr = pair.indptr;
+  for (int32_t& i : P->pair_indptr) i += static_cast<int32_t>(single.items.size());
+  P->jobs = pair.jobs;
+  P->jobs.insert(P->jobs.end(), single.jobs.begin(), single.jobs.end());
 
   size_t off = align256(sizeof(mla::WsHeader));
   auto take = [&](size_t bytes) {
@@ -396,12 +431,13 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.kx_rows = plan->kx_rows;
     p.err = err;
     p.stamp = plan->stamp;
-    if (mla::launch_expand(p, plan->num_sms, stream) != cudaSuccess) return MLA_ERR_CUDA;
     if (rot.cos_sin != nullptr) {
       const mla::RotateParams r{static_cast<const uint16_t*>(q), q_token_stride, q_head_stride,
                                 plan->q_tokens, plan->heads, rot, qr, err, plan->stamp};
       if (mla::launch_rotate(r, stream) != cudaSuccess) return MLA_ERR_CUDA;
     }
+    if (mla::launch_expand(p, plan->num_sms, rot.cos_sin != nullptr, stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
   }
   if (plan->num_ctas > 0 || plan->num_pairs > 0) {
     if (plan->map_q_ptr != q || plan->map_q_ts != q_token_stride ||
@@ -456,6 +492,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     }
     if (plan->num_ctas > 0) {
       p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_indptr);
+      p.after_attn = plan->num_pairs > 0 ? 1 : 0;
       if (mla::launch_attn(p, plan->num_ctas, stream) != cudaSuccess) return MLA_ERR_CUDA;
     }
   }

@@ -21,6 +21,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 __global__ void __launch_bounds__(256) rotate_kernel(const RotateParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (reinterpret_cast<const WsHeader*>(p.err)->stamp != p.stamp) return;   // reported by the others
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x >> 2);
   if (r >= p.q_tokens * p.heads) return;
