@@ -6,11 +6,15 @@
 // into shared memory; nothing is written back in between.
 //
 // Bound: 2 x 512 x 256 flops per (token, head) against 512 bytes written; the
-// weights (256 KB a head) come from L2.  A CTA keeps 128 rows (128 KB of bf16)
-// in shared memory and runs heads over them, so rows are read and decoded
-// once per CTA that meets them; units (tile, head) are split evenly over the
-// CTAs.  Two 256-column accumulators let the epilogue of one head run under
-// the products of the next.
+// weights (256 KB a head) come from L2.  A pair of CTAs works on two 128-row
+// tiles with one product of M = 256, N = 256: each keeps its rows (128 KB of
+// bf16) in shared memory and streams half of each head's weights past them.
+// On its own a CTA would read 12 KB of operands a product (128 cycles) and
+// take in 8 KB of weights, 160 bytes a cycle of a shared memory that gives 128
+// (32,845 keys, 16 heads: 121 us; in pairs %EXP%).  Rows are read and decoded
+// once per pair that meets them; units (two tiles, head) are split evenly over
+// the pairs.  Two 256-column accumulators let the epilogue of one head run
+// under the products of the next.
 //
 // Roundings: e4m3 and e2m1 values with their block exponents are exact in
 // bf16; the per-tensor scale goes into the fp32 epilogue; keys and values are
@@ -32,14 +36,21 @@ namespace {
 
 constexpr int kExpandThreads = 448;        // 4 epilogue, 8 row, 1 weight, 1 product warps
 constexpr uint32_t kAChunk = 128 * 128;    // 128 rows x 64 bf16
-constexpr uint32_t kWChunk = 256 * 128;    // 256 weight rows x 64 bf16
+constexpr uint32_t kWChunk = 128 * 128;    // this CTA's 128 weight rows x 64 bf16
 constexpr int kChunks = kVDim / 64;
-constexpr int kWSlots = 3;
-constexpr int kAhead = 4;                  // row chunks loaded ahead of their use
-constexpr uint32_t kExpandSmem = kChunks * kAChunk + kWSlots * kWChunk;
+constexpr int kWSlots = 4;
+constexpr uint32_t kBox = 32 * 128;        // a warp's output box: 32 rows x 64 bf16, two a warp
+constexpr uint32_t kExpandSmem = kChunks * kAChunk + kWSlots * kWChunk + 4 * 2 * kBox;
+// Row chunks that a thread has in flight from memory.  The proxy fence behind a
+// chunk waits for all of the thread's loads, so none is issued between fences:
+// the chunks come in batches (registers: four of bf16, all of the others).
+template <int KV>
+constexpr int kBatch = KV == MLA_DTYPE_BF16 ? 4 : 8;
 
+// Barriers that the issuing (even) CTA waits on stand there; commits arrive in
+// both CTAs.
 struct ExpandMisc {
-  uint64_t a_full[kChunks], a_empty[kChunks];
+  uint64_t a_full[kChunks], a_peer[kChunks], a_empty[kChunks];
   uint64_t w_full[kWSlots], w_empty[kWSlots];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -117,15 +128,21 @@ __device__ __forceinline__ uint4 decode(const Raw<KV>& r, float sc) {
   }
 }
 
+// The tile of this CTA in tile pair `pair`; an odd last pair has an empty one.
+__device__ __forceinline__ ExpandTile tile_of(const ExpandParams& p, int pair, int rank) {
+  const int i = 2 * pair + rank;
+  return i < p.num_tiles ? p.tiles[i] : ExpandTile{0, 0, 0, -1};
+}
+
 template <int KV>
 __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem, int u0, int u1,
-                         int tid) {
+                         int rank, int tid) {
   const int g = tid & 7, r0 = tid >> 3;      // granule of a chunk; rows r0 + 32 i
   const float sc = KV == MLA_DTYPE_FP8_E4M3 ? *p.kv_scale : 1.0f;
   uint32_t lap = 0;
   for (int u = u0; u < u1; ++lap) {
-    const int tile = u / p.heads;
-    const ExpandTile t = p.tiles[tile];
+    const int pair = u / p.heads;
+    const ExpandTile t = tile_of(p, pair, rank);
     int64_t row[4];
     bool live[4];
 #pragma unroll
@@ -134,44 +151,62 @@ __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem,
       live[i] = tok < t.len;
       row[i] = live[i] ? pool_row(p, t.page_base, tok) : 0;
     }
-    Raw<KV> raw[kAhead][4];                  // chunks in flight from memory
-    auto fetch = [&](int c) {
+    Raw<KV> raw[kBatch<KV>][4];
+    Raw<KV> last[4];                         // chunk 8: the rotated dims
+    auto fetch = [&](Raw<KV>* r, int c) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (live[i]) raw[c % kAhead][i] = load_raw<KV>(p, row[i], 8 * c + g);
+        if (live[i]) r[i] = load_raw<KV>(p, row[i], 8 * c + g);
     };
 #pragma unroll
-    for (int c = 0; c < kAhead; ++c) fetch(c);
+    for (int b = 0; b < kChunks; b += kBatch<KV>) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      uint4 v[4];
+      for (int k = 0; k < kBatch<KV>; ++k) fetch(raw[k], b + k);
+      if (b + kBatch<KV> == kChunks) fetch(last, kChunks);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = live[i] ? decode<KV>(raw[c % kAhead][i], 1.0f) : make_uint4(0, 0, 0, 0);
-      if (c + kAhead <= kChunks) fetch(c + kAhead);     // chunk 8: the rotated dims
-      if (lap > 0 && !mbar_wait(smem_u32(&ms->a_empty[c]), (lap - 1) & 1, p.err, kErrProducer))
-        return;
+      for (int k = 0; k < kBatch<KV>; ++k) {
+        const int c = b + k;
+        if (lap > 0 && !mbar_wait(smem_u32(&ms->a_empty[c]), (lap - 1) & 1, p.err, kErrProducer))
+          return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 32 * i;
-        *reinterpret_cast<uint4*>(a_smem + c * kAChunk + r * 128 + ((g ^ (r & 7)) << 4)) = v[i];
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 32 * i;
+          *reinterpret_cast<uint4*>(a_smem + c * kAChunk + r * 128 + ((g ^ (r & 7)) << 4)) =
+              live[i] ? decode<KV>(raw[k][i], 1.0f) : make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&ms->a_full[c]));
       }
-      fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&ms->a_full[c]));
     }
-    if (u % p.heads == 0) {
+    if (u % p.heads == 0 && t.out_row >= 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4*>(p.kr + (static_cast<int64_t>(t.out_row) + r0 + 32 * i) * kRope +
                                   8 * g) =
-            live[i] ? decode<KV>(raw[kChunks % kAhead][i], sc) : make_uint4(0, 0, 0, 0);
+            live[i] ? decode<KV>(last[i], sc) : make_uint4(0, 0, 0, 0);
     }
-    u = min(u1, (tile + 1) * p.heads);
+    u = min(u1, (pair + 1) * p.heads);
   }
 }
 
-__device__ void run_weights(const ExpandParams& p, ExpandMisc* ms, uint32_t w_smem, int u0,
-                            int u1) {
+// In the odd CTA: passes the arrival of its rows on to the even one.  (The rows
+// are in this SM's shared memory, behind their writers' proxy fences, and only
+// this SM's tensor core reads them: a relaxed arrival does, where a release
+// for the cluster would hold up every chunk by about 1,500 cycles.)
+__device__ void run_relay(const ExpandParams& p, ExpandMisc* ms, int u0, int u1) {
+  uint32_t lap = 0;
+  for (int u = u0; u < u1; ++lap) {
+    for (int c = 0; c < kChunks; ++c) {
+      if (!mbar_wait(smem_u32(&ms->a_full[c]), lap & 1, p.err, kErrProducer)) return;
+      fence_proxy_async_smem();
+      mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->a_peer[c]), 0));
+    }
+    u = min(u1, (u / p.heads + 1) * p.heads);
+  }
+}
+
+__device__ void run_weights(const ExpandParams& p, ExpandMisc* ms, uint32_t w_smem, int u0, int u1,
+                            int rank) {
   const uint64_t keep = l2_policy_evict_normal();
   uint32_t n = 0;
   bool ok = true;
@@ -184,112 +219,142 @@ __device__ void run_weights(const ExpandParams& p, ExpandMisc* ms, uint32_t w_sm
         ok = false;
         break;
       }
-      mbar_arrive_expect_tx(smem_u32(&ms->w_full[s]), kWChunk);
-      tma_load_3d(w_smem + s * kWChunk, &p.map_w, smem_u32(&ms->w_full[s]), 64 * c, 0, h, keep);
+      if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ms->w_full[s]), 2 * kWChunk);
+      tma_load_3d_pair(w_smem + s * kWChunk, &p.map_w, dsmem_addr(smem_u32(&ms->w_full[s]), 0),
+                       64 * c, 128 * rank, h, keep);
     }
   }
-  if (!ok)      // a wait gave up: no copy may land after the CTA has gone
+  if (!ok && rank == 0)   // a wait gave up: no copy may land after the CTAs have gone
     for (uint32_t k = n > kWSlots ? n - kWSlots : 0; k < n; ++k)
       mbar_wait(smem_u32(&ms->w_full[k % kWSlots]), (k / kWSlots) & 1, p.err, kErrProducer);
 }
 
-// The whole warp walks the units; one lane issues.
+// The whole warp (of the even CTA) walks the units; one lane issues.
 __device__ void run_products(const ExpandParams& p, ExpandMisc* ms, uint32_t a_smem,
                              uint32_t w_smem, uint32_t tmem, int u0, int u1) {
-  constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, kWRows);
+  constexpr uint32_t idesc = make_idesc(1, 1, false, false, 256, kWRows);
   const uint64_t ad = smem_desc(a_smem, 16, 1024, kSwizzle128B);
   const uint64_t wd = smem_desc(w_smem, 16, 1024, kSwizzle128B);
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.err, kErrMma));
-  };
+  auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
   uint32_t slot = 0, phase = 0, lap = 0, k = 0;
+  bool w_ready = false;
   for (int u = u0; u < u1; ++u, ++k) {
-    const bool first = u == u0 || u % p.heads == 0;          // first unit of its tile here
+    const bool first = u == u0 || u % p.heads == 0;          // first unit of its tiles here
     const bool last = u + 1 == u1 || (u + 1) % p.heads == 0;
     const uint32_t buf = k & 1;
-    if (k >= 2 && !wait(&ms->acc_empty[buf], ((k >> 1) - 1) & 1)) return;
+    if (k >= 2 && !all(mbar_wait_cluster(smem_u32(&ms->acc_empty[buf]), ((k >> 1) - 1) & 1, p.err,
+                                         kErrMma)))
+      return;
     tc_fence_after();
     const uint32_t d = tmem + buf * kWRows;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      if (first && !wait(&ms->a_full[c], lap & 1)) return;
-      if (!wait(&ms->w_full[slot], phase)) return;
+      if (first) {
+        if (!all(mbar_wait(smem_u32(&ms->a_full[c]), lap & 1, p.err, kErrMma))) return;
+        if (!all(mbar_wait_cluster(smem_u32(&ms->a_peer[c]), lap & 1, p.err, kErrMma))) return;
+      }
+      if (!all(w_ready) &&
+          !all(mbar_wait_poll(smem_u32(&ms->w_full[slot]), phase, p.err, kErrMma)))
+        return;
       tc_fence_after();
       const uint64_t a = ad + ((c * kAChunk) >> 4), w = wd + ((slot * kWChunk) >> 4);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_f16(d, a + 2 * kk, w + 2 * kk, idesc, (c | kk) != 0);
-        tc_commit(smem_u32(&ms->w_empty[slot]));
-        if (last) tc_commit(smem_u32(&ms->a_empty[c]));
-      }
+      const uint32_t s = slot;
       if (++slot == kWSlots) {
         slot = 0;
         phase ^= 1;
       }
+      w_ready = mbar_test(smem_u32(&ms->w_full[slot]), phase);     // the next chunk's, ahead
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_pair(d, a + 2 * kk, w + 2 * kk, idesc, (c | kk) != 0);
+        tc_commit_pair(smem_u32(&ms->w_empty[s]));
+        if (last) tc_commit_pair(smem_u32(&ms->a_empty[c]));
+      }
     }
-    if (elect_one()) tc_commit(smem_u32(&ms->acc_full[buf]));
+    if (elect_one()) tc_commit_pair(smem_u32(&ms->acc_full[buf]));
     if (last) ++lap;
   }
 }
 
-__device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint32_t tmem, int u0, int u1,
-                             int warp, int lane) {
+// Accumulators to bf16 rows of kx, 64 columns at a time through a box in shared
+// memory and a bulk store: rows are 512 bytes apart, and a thread's own stores
+// (a sector each) took about 250 cycles an instruction.
+__device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* boxes, uint32_t tmem,
+                             int u0, int u1, int rank, int warp, int lane) {
   const float sc = p.kv_dtype == MLA_DTYPE_FP8_E4M3 ? *p.kv_scale : 1.0f;
+  uint8_t* box = boxes + warp * 2 * kBox;
   uint32_t k = 0;
   for (int u = u0; u < u1; ++u, ++k) {
     const uint32_t buf = k & 1;
-    const int tile = u / p.heads, h = u - tile * p.heads;
-    const int64_t row = static_cast<int64_t>(p.tiles[tile].out_row) + warp * 32 + lane;
-    uint16_t* dst = p.kx + (static_cast<int64_t>(h) * p.kx_rows + row) * kWRows;
+    const int pair = u / p.heads, h = u - pair * p.heads;
+    const int out_row = tile_of(p, pair, rank).out_row;      // -1: no tile here
     const bool ok = mbar_wait(smem_u32(&ms->acc_full[buf]), (k >> 1) & 1, p.err, kErrDrain);
-    if (!__all_sync(0xffffffffu, ok)) return;
+    if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
     const uint32_t acc = tmem + buf * kWRows + (static_cast<uint32_t>(warp) << 21);
+    // 64 columns from x on, rounded, as they go into box `b`
+    auto load = [&](int x, uint32_t (&v)[32]) {
+      uint32_t f[64];
+      tmem_ld32(acc + x, f);
+      tmem_ld32(acc + x + 32, f + 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = bf16x2(__uint_as_float(f[2 * i]) * sc, __uint_as_float(f[2 * i + 1]) * sc);
+    };
+    auto store = [&](int b, int x, const uint32_t (&v)[32]) {
+      // the box's last store has read it (one lane keeps the groups)
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+      uint8_t* at = box + b * kBox + lane * 128;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(at + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (out_row >= 0)
+          tma_store_3d(&p.map_kx, smem_u32(box + b * kBox), x, out_row + warp * 32, h);
+        bulk_commit();
+      }
+    };
     // values first: whether they are finite decides what the key becomes
-    uint32_t v[64];
+    uint32_t v0[32], v1[32];
+    load(kNope, v0);
+    load(kNope + 64, v1);
     __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t x[64];
-      tmem_ld32(acc + kNope + 64 * half, x);
-      tmem_ld32(acc + kNope + 64 * half + 32, x + 32);
-      tmem_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        v[32 * half + i] =
-            bf16x2(__uint_as_float(x[2 * i]) * sc, __uint_as_float(x[2 * i + 1]) * sc);
-        top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[32 * half + i])));
-      }
+    for (int i = 0; i < 32; ++i) {
+      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v0[i])));
+      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v1[i])));
     }
-    const bool finite = fmaxf(__low2float(top), __high2float(top)) < INFINITY &&
-                        !__isnanf(__low2float(top)) && !__isnanf(__high2float(top));
-    // (a sector per store: with 16-byte stores the write path was the limit)
+    const bool finite = __low2float(top) < INFINITY && __high2float(top) < INFINITY;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = finite ? v[i] : 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) st_global_32(dst + kNope + 16 * i, v + 8 * i);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t x[64];
-      tmem_ld32(acc + 64 * half, x);
-      tmem_ld32(acc + 64 * half + 32, x + 32);
-      tmem_wait_ld();
-      if (half == 1) {
-        tc_fence_before();
-        mbar_arrive(smem_u32(&ms->acc_empty[buf]));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          o[q] = finite ? bf16x2(__uint_as_float(x[16 * i + 2 * q]) * sc,
-                                 __uint_as_float(x[16 * i + 2 * q + 1]) * sc)
-                        : 0x7fc07fc0u;
-        st_global_32(dst + 64 * half + 16 * i, o);
-      }
+    for (int i = 0; i < 32; ++i) {
+      v0[i] = finite ? v0[i] : 0u;
+      v1[i] = finite ? v1[i] : 0u;
     }
+    store(0, kNope, v0);
+    store(1, kNope + 64, v1);
+    load(0, v0);
+    load(64, v1);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->acc_empty[buf]), 0));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v0[i] = finite ? v0[i] : 0x7fc07fc0u;
+      v1[i] = finite ? v1[i] : 0x7fc07fc0u;
+    }
+    store(0, 0, v0);
+    store(1, 64, v1);
   }
+  // the boxes stay until their stores are through, and the stores' rows are
+  // there before the kernel counts as ended
+  if (lane == 0) bulk_wait_all();
+  __syncwarp();
 }
 
 template <int KV>
@@ -302,9 +367,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t a_smem = smem_u32(smem), w_smem = a_smem + kChunks * kAChunk;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kChunks; ++i) {
       mbar_init(smem_u32(&ms->a_full[i]), 256);
+      mbar_init(smem_u32(&ms->a_peer[i]), 1);
       mbar_init(smem_u32(&ms->a_empty[i]), 1);
     }
     for (int i = 0; i < kWSlots; ++i) {
@@ -313,7 +380,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->acc_full[i]), 1);
-      mbar_init(smem_u32(&ms->acc_empty[i]), 128);
+      mbar_init(smem_u32(&ms->acc_empty[i]), 2 * 4);      // a warp's arrival each
     }
     mbar_init(smem_u32(&ms->drain), 1);
     fence_mbar_init();
@@ -321,31 +388,36 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     if (!ms->ours) atomicOr(p.err, kErrStale);
   }
   if (warp == 13) {
-    tmem_alloc(smem_u32(&ms->tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&ms->tmem), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                       // the other CTA's barriers are set up too
   tc_fence_after();
   const uint32_t tmem = uniform(ms->tmem);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (ms->ours) {
-    const int64_t units = static_cast<int64_t>(p.num_tiles) * p.heads;
-    const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
-    const int u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    const int64_t units = static_cast<int64_t>((p.num_tiles + 1) / 2) * p.heads;
+    const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int u0 = static_cast<int>(units * pair / pairs);
+    const int u1 = static_cast<int>(units * (pair + 1) / pairs);
     if (warp < 4) {
-      run_epilogue(p, ms, tmem, u0, u1, warp, lane);
+      run_epilogue(p, ms, smem + kChunks * kAChunk + kWSlots * kWChunk, tmem, u0, u1, rank, warp,
+                   lane);
     } else if (warp < 12) {
-      run_rows<KV>(p, ms, smem, u0, u1, threadIdx.x - 128);
+      run_rows<KV>(p, ms, smem, u0, u1, rank, threadIdx.x - 128);
     } else if (warp == 12) {
-      if (lane == 0) run_weights(p, ms, w_smem, u0, u1);
-    } else {
+      if (lane == 0) run_weights(p, ms, w_smem, u0, u1, rank);
+    } else if (rank == 0) {
       run_products(p, ms, a_smem, w_smem, tmem, uniform(u0), uniform(u1));
-      // no product may run on after the CTA has gone
+      // no product may run on after the CTAs have gone
       if (elect_one()) {
-        tc_commit(smem_u32(&ms->drain));
+        tc_commit_pair(smem_u32(&ms->drain));
         mbar_wait(smem_u32(&ms->drain), 0, p.err, kErrDrain);
       }
+    } else {
+      if (lane == 0) run_relay(p, ms, u0, u1);
     }
     __syncwarp();
   }
@@ -353,25 +425,28 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  cluster_sync();                       // nothing of the pair is under way any more
+  if (warp == 13) tmem_dealloc_pair(tmem, 512);
 }
 
 template <int KV>
-cudaError_t launch(const ExpandParams& p, int ctas, bool dependent, cudaStream_t stream) {
+cudaError_t launch(const ExpandParams& p, int pairs, bool dependent, cudaStream_t stream) {
   constexpr int bytes = kExpandSmem + 1024;
   const cudaError_t e =
       cudaFuncSetAttribute(expand_kernel<KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kExpandThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {2, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = dependent ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, expand_kernel<KV>, p);
 }
 
@@ -379,12 +454,13 @@ cudaError_t launch(const ExpandParams& p, int ctas, bool dependent, cudaStream_t
 
 cudaError_t launch_expand(const ExpandParams& p, int num_ctas, bool dependent,
                           cudaStream_t stream) {
-  const int64_t units = static_cast<int64_t>(p.num_tiles) * p.heads;
-  const int ctas = static_cast<int>(units < num_ctas ? units : num_ctas);
-  if (p.kv_dtype == MLA_DTYPE_BF16) return launch<MLA_DTYPE_BF16>(p, ctas, dependent, stream);
+  const int64_t units = static_cast<int64_t>((p.num_tiles + 1) / 2) * p.heads;
+  const int64_t most = num_ctas >= 2 ? num_ctas / 2 : 1;
+  const int pairs = static_cast<int>(units < most ? units : most);
+  if (p.kv_dtype == MLA_DTYPE_BF16) return launch<MLA_DTYPE_BF16>(p, pairs, dependent, stream);
   if (p.kv_dtype == MLA_DTYPE_FP8_E4M3)
-    return launch<MLA_DTYPE_FP8_E4M3>(p, ctas, dependent, stream);
-  return launch<MLA_DTYPE_MXFP4>(p, ctas, dependent, stream);
+    return launch<MLA_DTYPE_FP8_E4M3>(p, pairs, dependent, stream);
+  return launch<MLA_DTYPE_MXFP4>(p, pairs, dependent, stream);
 }
 
 }  // namespace mla

@@ -34,7 +34,8 @@ struct JoinJob {
 };
 
 struct ExpandParams {
-  CUtensorMap map_w;           // {512, 256, heads}, boxes {64, 256, 1}
+  CUtensorMap map_w;           // {512, 256, heads}, boxes {64, 128, 1}
+  CUtensorMap map_kx;          // {256, kx_rows, heads}, boxes {64, 32, 1}: keys' dims, then values'
   const ExpandTile* tiles;
   int32_t num_tiles, heads;
   const uint8_t* kv;
@@ -45,9 +46,7 @@ struct ExpandParams {
   const int32_t* kv_indices;   // null: identity
   int32_t page_size;
   int32_t kv_dtype;
-  uint16_t* kx;                // [heads][kx_rows][256]: keys' 128 dims, then values'
   uint16_t* kr;                // [kx_rows][64]: the keys' rotated dims
-  int64_t kx_rows;
   int32_t* err;                // workspace header
   uint64_t stamp;
 };

@@ -31,7 +31,7 @@ struct mla_prefill {
   uint64_t stamp = 0;
   // per-run caches: the workspace holding the table, the tensor maps and what they describe
   mutable void* uploaded_ws = nullptr;
-  CUtensorMap map_q, map_qr, map_kx, map_kr, map_w;
+  CUtensorMap map_q, map_qr, map_kx, map_kr, map_kx_out, map_w;
   const void* map_w_ptr = nullptr;
   const void* map_q_ptr = nullptr;
   int64_t map_q_ts = 0, map_q_hs = 0;
@@ -404,17 +404,35 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
   uint16_t* qr = reinterpret_cast<uint16_t*>(ws + plan->off_qr);
   float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
   float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
+  // (a plan without key rows has nothing to expand and no tile to load)
+  if (plan->kx_rows > 0 && plan->map_ws != workspace) {
+    const cuuint64_t rows = static_cast<cuuint64_t>(plan->kx_rows);
+    const cuuint64_t heads = static_cast<cuuint64_t>(plan->heads);
+    const cuuint64_t tokens = static_cast<cuuint64_t>(plan->q_tokens);
+    plan->map_ws = nullptr;
+    if (!make_map(&plan->map_kx, kx, {mla::kWRows, rows, heads},
+                  {mla::kWRows * 2, rows * mla::kWRows * 2}, {64, 64, 1}) ||
+        !make_map(&plan->map_kx_out, kx, {mla::kWRows, rows, heads},
+                  {mla::kWRows * 2, rows * mla::kWRows * 2}, {64, 32, 1}) ||
+        !make_map(&plan->map_kr, kr, {mla::kRope, rows, 1},
+                  {mla::kRope * 2, rows * mla::kRope * 2}, {64, 64, 1}) ||
+        !make_map(&plan->map_qr, qr, {mla::kRope, heads, tokens},
+                  {mla::kRope * 2, heads * mla::kRope * 2}, {64, 1, mla::kPfTile}))
+      return MLA_ERR_CUDA;
+    plan->map_ws = workspace;
+  }
   if (!plan->tiles.empty()) {
     if (plan->map_w_ptr != w) {
       plan->map_w_ptr = nullptr;
       if (!make_map(&plan->map_w, w,
                     {mla::kVDim, mla::kWRows, static_cast<cuuint64_t>(plan->heads)},
-                    {mla::kVDim * 2, mla::kVDim * mla::kWRows * 2}, {64, mla::kWRows, 1}))
+                    {mla::kVDim * 2, mla::kVDim * mla::kWRows * 2}, {64, 128, 1}))
         return MLA_ERR_CUDA;
       plan->map_w_ptr = w;
     }
     mla::ExpandParams p{};
     p.map_w = plan->map_w;
+    p.map_kx = plan->map_kx_out;
     p.tiles = reinterpret_cast<const ExpandTile*>(ws + plan->off_tiles);
     p.num_tiles = static_cast<int32_t>(plan->tiles.size());
     p.heads = plan->heads;
@@ -426,9 +444,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.kv_indices = kv_indices;
     p.page_size = plan->page_size;
     p.kv_dtype = plan->kv_dtype;
-    p.kx = kx;
     p.kr = kr;
-    p.kx_rows = plan->kx_rows;
     p.err = err;
     p.stamp = plan->stamp;
     if (rot.cos_sin != nullptr) {
@@ -453,23 +469,6 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
       plan->map_q_ptr = q;
       plan->map_q_ts = q_token_stride;
       plan->map_q_hs = q_head_stride;
-    }
-    if (plan->map_ws != workspace) {
-      // (a plan without key rows has no tile to load)
-      const cuuint64_t rows = static_cast<cuuint64_t>(std::max<int64_t>(plan->kx_rows, 1));
-      plan->map_ws = nullptr;
-      if (plan->kx_rows > 0 &&
-          (!make_map(&plan->map_kx, kx, {mla::kWRows, rows, static_cast<cuuint64_t>(plan->heads)},
-                     {mla::kWRows * 2, rows * mla::kWRows * 2}, {64, 64, 1}) ||
-           !make_map(&plan->map_kr, kr, {mla::kRope, rows, 1}, {mla::kRope * 2, rows * mla::kRope * 2},
-                     {64, 64, 1}) ||
-           !make_map(&plan->map_qr, qr,
-                     {mla::kRope, static_cast<cuuint64_t>(plan->heads),
-                      static_cast<cuuint64_t>(plan->q_tokens)},
-                     {mla::kRope * 2, static_cast<cuuint64_t>(plan->heads) * mla::kRope * 2},
-                     {64, 1, mla::kPfTile})))
-        return MLA_ERR_CUDA;
-      plan->map_ws = workspace;
     }
     mla::AttnParams p{};
     p.map_q = plan->map_q;
