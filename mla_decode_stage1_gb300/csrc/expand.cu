@@ -102,30 +102,32 @@ __device__ __forceinline__ Raw<KV> load_raw(const ExpandParams& p, int64_t row, 
   return r;
 }
 
-// The same values as bf16 (exactly; e4m3 without the per-tensor scale `sc`
-// unless it is given).
+// The same values as bf16, exactly (e4m3 without the per-tensor scale).
 template <int KV>
-__device__ __forceinline__ uint4 decode(const Raw<KV>& r, float sc) {
+__device__ __forceinline__ uint4 decode(const Raw<KV>& r) {
   if constexpr (KV == MLA_DTYPE_BF16) {
     return r.v;
-  } else {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h;
-      if constexpr (KV == MLA_DTYPE_FP8_E4M3)
-        h = e4m3x2_to_f16x2(static_cast<uint16_t>((i < 2 ? r.v.x : r.v.y) >> (16 * (i & 1))));
-      else
-        h = e2m1x2_to_f16x2((r.v >> (8 * i)) & 0xffu);
+  } else if constexpr (KV == MLA_DTYPE_FP8_E4M3) {
+    auto two = [](uint32_t v) {
+      const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(v));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      float m = sc;
-      if constexpr (KV == MLA_DTYPE_MXFP4)
-        m = r.e == 255u ? __uint_as_float(0x7fc00000u)
-                        : __uint_as_float(r.e > 0 ? r.e << 23 : 0x00400000u);
-      o[i] = bf16x2(f.x * m, f.y * m);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+      return bf16x2(f.x, f.y);
+    };
+    const uint4 o = make_uint4(two(r.v.x & 0xffffu), two(r.v.x >> 16), two(r.v.y & 0xffffu),
+                               two(r.v.y >> 16));
+    return o;
+  } else {
+    const uint32_t s = e8m0_to_bf16x2(r.e);
+    return make_uint4(e2m1x2_to_bf16(r.v & 0xffu, s), e2m1x2_to_bf16((r.v >> 8) & 0xffu, s),
+                      e2m1x2_to_bf16((r.v >> 16) & 0xffu, s), e2m1x2_to_bf16(r.v >> 24, s));
   }
+}
+// The same with the per-tensor scale, rounded.
+__device__ __forceinline__ uint4 scaled(const uint4& v, float sc) {
+  auto one = [&](uint32_t u) {
+    return bf16x2(__uint_as_float(u << 16) * sc, __uint_as_float(u & 0xffff0000u) * sc);
+  };
+  return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
 }
 
 // The tile of this CTA in tile pair `pair`; an odd last pair has an empty one.
@@ -172,18 +174,22 @@ __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem,
         for (int i = 0; i < 4; ++i) {
           const int r = r0 + 32 * i;
           *reinterpret_cast<uint4*>(a_smem + c * kAChunk + r * 128 + ((g ^ (r & 7)) << 4)) =
-              live[i] ? decode<KV>(raw[k][i], 1.0f) : make_uint4(0, 0, 0, 0);
+              live[i] ? decode<KV>(raw[k][i]) : make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
-        mbar_arrive(smem_u32(&ms->a_full[c]));
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(smem_u32(&ms->a_full[c]));
       }
     }
     if (u % p.heads == 0 && t.out_row >= 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live[i]) v = decode<KV>(last[i]);
+        if (KV == MLA_DTYPE_FP8_E4M3) v = scaled(v, sc);
         *reinterpret_cast<uint4*>(p.kr + (static_cast<int64_t>(t.out_row) + r0 + 32 * i) * kRope +
-                                  8 * g) =
-            live[i] ? decode<KV>(last[i], sc) : make_uint4(0, 0, 0, 0);
+                                  8 * g) = v;
+      }
     }
     u = min(u1, (pair + 1) * p.heads);
   }
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   const int rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kChunks; ++i) {
-      mbar_init(smem_u32(&ms->a_full[i]), 256);
+      mbar_init(smem_u32(&ms->a_full[i]), 8);             // a warp's arrival each
       mbar_init(smem_u32(&ms->a_peer[i]), 1);
       mbar_init(smem_u32(&ms->a_empty[i]), 1);
     }

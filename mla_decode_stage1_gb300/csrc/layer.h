@@ -145,6 +145,25 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t v) {
       : "r"(v));
   return r;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two e2m1 codes (a byte's low nibble first) times a power of two given as a
+// bf16 pair, exactly: a code's exponent and mantissa are put at the low end of
+// bf16's and the difference of the biases is multiplied in (a subnormal code
+// becomes a bf16 subnormal, so it comes out right too).
+__device__ __forceinline__ uint32_t e2m1x2_to_bf16(uint32_t byte, uint32_t scale) {
+  const uint32_t t = (byte & 0xfu) | ((byte & 0xf0u) << 12);
+  const uint32_t r = ((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6);
+  return mul_bf16x2(mul_bf16x2(r, 0x7e807e80u), scale);               // 2^126
+}
+// The power of two of an e8m0 byte as a bf16 pair (255: NaN).
+__device__ __forceinline__ uint32_t e8m0_to_bf16x2(uint32_t e) {
+  const uint32_t s = e == 255u ? 0x7fc0u : e > 0 ? e << 7 : 0x0040u;
+  return s | (s << 16);
+}
 #endif
 
 }  // namespace mla
