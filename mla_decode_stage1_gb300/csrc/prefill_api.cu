@@ -49,7 +49,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // Costs of the assignment, in tenths of one 128-key step of an item at full
 // width (256 rows on a CTA, 512 on a pair).
 constexpr int64_t kFullCost = 10;     // both query tiles of an item at work
-constexpr int64_t kSingleCost = 6;    // one of them
+constexpr int64_t kSingleCost = 10;   // one of them: nothing runs under its softmax
 constexpr int64_t kItemCost = 15;     // prologue and epilogue of an item
 constexpr int64_t kJoinCost = 40;     // a join launch, once
 constexpr int64_t kLaunchCost = 40;   // a second attention kernel, once
