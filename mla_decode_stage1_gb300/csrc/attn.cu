@@ -61,13 +61,28 @@ struct Misc {
   uint32_t ours;
 };
 
-// Key steps of tile t of an item: those with a key that the tile's last row sees.
+// What query tile t of an item works on: rows from `first` of the item on,
+// keys [begin, end).
+struct Stream {
+  int first, begin, end, slot;
+};
+template <bool P>
+__device__ __forceinline__ Stream stream_of(const AttnItem& w, int t) {
+  if (!P && halved(w)) {
+    const int mid = middle_key(w);
+    return Stream{0, t ? mid : w.kv_begin, t ? w.kv_end : mid, w.slot + t};
+  }
+  return Stream{t * kTileRows<P>, w.kv_begin, w.kv_end, w.slot};
+}
+
+// Key steps of query tile t: those with a key that the tile's last row sees.
 template <bool P>
 __device__ __forceinline__ int tile_steps(const AttnItem& w, int t) {
-  if (w.rows <= t * kTileRows<P>) return 0;
-  const int last = min(w.rows, (t + 1) * kTileRows<P>) - 1;
-  const int end = min(w.kv_end, w.vis0 + last);
-  return end > w.kv_begin ? (end - w.kv_begin + kPfTile - 1) / kPfTile : 0;
+  const Stream s = stream_of<P>(w, t);
+  if (w.rows <= s.first) return 0;
+  const int last = min(w.rows, s.first + kTileRows<P>) - 1;
+  const int end = min(s.end, w.vis0 + last);
+  return end > s.begin ? (end - s.begin + kPfTile - 1) / kPfTile : 0;
 }
 
 __device__ __forceinline__ AttnItem load_item(const AttnItem* p) {
@@ -125,8 +140,9 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
     else
       tma_load_3d(dst, map, smem_u32(bar), x, y, z, keep);
   };
-  auto load_k = [&](const AttnItem& w, int j) {
-    const int row = w.kv_row + w.kv_begin + j * kPfTile + 64 * rank;
+  // K and V tiles whose first key stands in workspace row `key`
+  auto load_k = [&](const AttnItem& w, int key) {
+    const int row = key + 64 * rank;
     if constexpr (P) {
       const uint32_t s = n % kStages;
       if (!open(s, n / kStages, 2 * 3 * kPieceBytes)) return;
@@ -148,8 +164,7 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
       }
     }
   };
-  auto load_v = [&](const AttnItem& w, int j) {
-    const int row = w.kv_row + w.kv_begin + j * kPfTile;
+  auto load_v = [&](const AttnItem& w, int row) {
     if constexpr (P) {
       const uint32_t s = nv % kStages;
       if (!open(kStages + s, nv / kStages, 2 * 2 * kPieceBytes)) return;
@@ -177,12 +192,17 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
     if (it + 1 < it1) next = load_item(p.items + it + 1);
     const int n0 = tile_steps<P>(w, 0), n1 = tile_steps<P>(w, 1), steps = max(n0, n1);
     if (steps == 0) continue;
-    load_k(w, 0);
+    const bool two = !P && halved(w);      // each query tile has keys of its own
+    const Stream s0 = stream_of<P>(w, 0), s1 = stream_of<P>(w, 1);
+    const int key0 = w.kv_row + s0.begin, key1 = w.kv_row + s1.begin;
+    if (!two || n0 > 0) load_k(w, key0);
     if (!ok) break;
     for (int t = 0; t < 2 && ok; ++t) {
       if ((t ? n1 : n0) == 0) continue;
+      if (two && t == 1) load_k(w, key1);
       const uint32_t k = t ? nq1 : nq0;
-      if (k > 0 && !mbar_wait_poll(smem_u32(&ms->q_empty[t]), (k - 1) & 1, p.err, kErrProducer)) {
+      if (!ok || (k > 0 && !mbar_wait_poll(smem_u32(&ms->q_empty[t]), (k - 1) & 1, p.err,
+                                           kErrProducer))) {
         ok = false;
         break;
       }
@@ -192,13 +212,18 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
       for (int ch = 0; ch < 3; ++ch)
         load(q_smem + t * kQTileBytes + ch * kChunkBytes, &ms->q_full[t],
              ch < 2 ? &p.map_q : &p.map_qr, ch < 2 ? ch * 64 : p.qr_x, w.head,
-             w.q_row + t * kTileRows<P> + rank * kPfTile);
+             w.q_row + (t ? s1.first : s0.first) + rank * kPfTile);
     }
-    if (!ok) break;
-    load_v(w, 0);
-    for (int j = 1; j < steps && ok; ++j) {
-      load_k(w, j);
-      if (ok) load_v(w, j);
+    for (int j = 0; j < steps && ok; ++j) {
+      if (!two) {
+        load_v(w, key0 + j * kPfTile);
+        if (ok && j + 1 < steps) load_k(w, key0 + (j + 1) * kPfTile);
+      } else {
+        if (j < n0) load_v(w, key0 + j * kPfTile);
+        if (ok && j + 1 < n0) load_k(w, key0 + (j + 1) * kPfTile);
+        if (ok && j < n1) load_v(w, key1 + j * kPfTile);
+        if (ok && j + 1 < n1) load_k(w, key1 + (j + 1) * kPfTile);
+      }
     }
   }
   if (!ok && rank == 0) {
@@ -338,6 +363,35 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
     const int n0 = uniform(tile_steps<P>(w, 0)), n1 = uniform(tile_steps<P>(w, 1));
     const int steps = max(n0, n1);
     if (steps == 0) continue;
+    if constexpr (!P) if (halved(w)) {
+      // the query tiles have keys of their own, in turn
+      for (int t = 0; t < 2; ++t) {
+        const int nt = t ? n1 : n0;
+        if (nt == 0) continue;
+        if (!wait(false, &ms->q_full[t], (t ? nq1++ : nq0++) & 1)) return;
+        tc_fence_after();
+        if (!qk(t, n, true, false, nt == 1)) return;
+        release_k(n);
+        n += 3;
+      }
+      for (int j = 0; j < steps; ++j)
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? n1 : n0;
+          if (j >= nt) continue;
+          bool k_ready = false;
+          if (!pv(t, n, (t ? np1++ : np0++) & 1, true, false, j == 0, n + 2, &k_ready)) return;
+          if (j + 1 == nt && elect_one()) commit<P>(&ms->o_full[t]);
+          release_v(n);
+          n += 2;
+          if (j + 1 < nt) {
+            if (!qk(t, n, true, k_ready, j + 2 == nt)) return;
+            release_k(n);
+            n += 3;
+          }
+        }
+      continue;
+    }
     if (n0 > 0) {
       if (!wait(false, &ms->q_full[0], nq0++ & 1)) return;
       tc_fence_after();
@@ -383,7 +437,6 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
 template <bool P>
 __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it0, int it1,
                             int rank, int t, int warp, int lane) {
-  const int row = t * kTileRows<P> + rank * kPfTile + warp * 32 + lane;     // of the item
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;      // TMEM lane 32 warp
   const uint32_t ts = tmem + lanes + kColS + 128 * t, to = tmem + lanes + kColO + 128 * t;
   const uint32_t s_full = smem_u32(&ms->s_full[t]);
@@ -393,8 +446,10 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
   for (int it = it0; it < it1; ++it) {
     const AttnItem w = next;
     if (it + 1 < it1) next = load_item(p.items + it + 1);
+    const Stream st = stream_of<P>(w, t);
     const int n = tile_steps<P>(w, t);
-    const int limit = min(w.kv_end, w.vis0 + row) - w.kv_begin;  // keys of this range it sees
+    const int row = st.first + rank * kPfTile + warp * 32 + lane;     // of the item
+    const int limit = min(st.end, w.vis0 + row) - st.begin;           // keys of this range it sees
     float m = -INFINITY, l = 0.0f;
     for (int j = 0; j < n; ++j) {
       if (!all_waited(mbar_wait_poll(s_full, ns & 1, p.err, kErrSoftmax))) return;
@@ -484,7 +539,7 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
     // a row that sees no key: zeros (one whose keys all score -inf: 0 / 0)
     const float inv = 1.0f / l;
     const int64_t token = static_cast<int64_t>(w.q_row) + row;
-    const int64_t part = static_cast<int64_t>(w.slot) * kPfRows + row;
+    const int64_t part = static_cast<int64_t>(st.slot) * kPfRows + row;
     const int64_t at = token * p.heads + w.head;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
@@ -575,10 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   if (ms->ours) {
     const int at = P ? blockIdx.x / 2 : blockIdx.x;
     const int it0 = p.cta_indptr[at], it1 = p.cta_indptr[at + 1];
-    // Launched as a programmatic dependent: the kernels before it have to be
-    // through before their keys and queries are loaded, and, where it follows
-    // another attention kernel (`after_attn`), before it ends.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
       regs_raise<208>();
       run_softmax<P>(p, ms, tmem, it0, it1, rank, warp >> 2, warp & 3, lane);
@@ -586,7 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       regs_lower<88>();            // 2 x 208 + 88 = 3 x 168, the registers at launch
     }
     if (warp == 8) {
+      // Launched as a programmatic dependent: the kernels before this one have
+      // to be through before their keys and queries are loaded.  The kernel
+      // after it is let go only then, so one that follows an attention kernel
+      // (`after_attn`) finds the expansion through when it starts, and waits
+      // for that attention kernel only before it ends.
       if (!p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       if (lane == 0) run_loads<P>(p, ms, q_smem, ring, it0, it1, rank);
     } else if (warp == 9 && rank == 0) {
       run_products<P>(p, ms, q_smem, ring, tmem, uniform(it0), uniform(it1));

@@ -20,12 +20,24 @@ static_assert(sizeof(ExpandTile) == 16, "an expansion tile is one int4");
 // Query rows q_row .. q_row + rows - 1 of one head against keys
 // [kv_begin, kv_end) of their request (kv_begin a multiple of 128).  Row i
 // sees the request's first vis0 + i keys.  slot < 0: out and lse are written;
-// else a partial result.
+// else a partial result.  Partial items of at most 128 rows are `halved`: their
+// rows fill both query tiles, tile 0 against the first half of the keys and
+// tile 1 against the second, with partial results slot and slot + 1.
 struct AttnItem {
   int32_t q_row, rows, head, kv_row;       // kv_row: workspace row of the request's key 0
   int32_t vis0, kv_begin, kv_end, slot;
 };
 static_assert(sizeof(AttnItem) == 32, "an attention item is two int4");
+
+__host__ __device__ inline bool halved(const AttnItem& w) {
+  return w.slot >= 0 && w.rows <= kPfTile;
+}
+// First key of the second half: whole tiles, the larger half first.
+__host__ __device__ inline int32_t middle_key(const AttnItem& w) {
+  const int32_t tiles = (w.kv_end - w.kv_begin + kPfTile - 1) / kPfTile;
+  const int32_t mid = w.kv_begin + (tiles + 1) / 2 * kPfTile;
+  return mid < w.kv_end ? mid : w.kv_end;
+}
 
 // Join of `count` consecutive partials, of `span` slots of 256 rows each, of
 // the same query rows and head.

