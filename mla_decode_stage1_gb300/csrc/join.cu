@@ -17,27 +17,40 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   const JoinJob j = p.jobs[blockIdx.x];
   const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (i >= j.rows) return;
+  // Weights first, a part per lane and 32 at a time, then the parts' rows,
+  // eight in flight.
   float M = -INFINITY;
   bool nan = false;
-  for (int s = 0; s < j.count; ++s) {
+  for (int s = lane; s < j.count; s += 32) {
     const float v = p.part_lse[static_cast<int64_t>(j.first + s * j.span) * kPfRows + i];
     nan |= v != v;
     M = fmaxf(M, v);
   }
-  if (nan) M = __uint_as_float(0x7fc00000u);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7fc00000u);
   float wsum = 0.0f;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int s = 0; s < j.count; ++s) {
-    const int64_t at = static_cast<int64_t>(j.first + s * j.span) * kPfRows + i;
-    const float v = p.part_lse[at];
-    if (v == -INFINITY) continue;          // no key of this range is seen
-    const float w = exp2f(v - M);
-    const float4 o = reinterpret_cast<const float4*>(p.part_o + at * kVHead)[lane];
-    wsum += w;
-    a.x += w * o.x;
-    a.y += w * o.y;
-    a.z += w * o.z;
-    a.w += w * o.w;
+  for (int s0 = 0; s0 < j.count; s0 += 8) {
+    float v[8];
+    float4 o[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = min(s0 + u, j.count - 1);
+      const int64_t at = static_cast<int64_t>(j.first + s * j.span) * kPfRows + i;
+      v[u] = s0 + u < j.count ? p.part_lse[at] : -INFINITY;
+      o[u] = reinterpret_cast<const float4*>(p.part_o + at * kVHead)[lane];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (v[u] == -INFINITY) continue;       // no key of this range is seen
+      const float w = exp2f(v[u] - M);
+      wsum += w;
+      a.x += w * o[u].x;
+      a.y += w * o[u].y;
+      a.z += w * o[u].z;
+      a.w += w * o[u].w;
+    }
   }
   // a row that sees no key at all is zero; one whose keys all score -inf is 0 / 0
   const float inv = j.vis0 + i <= 0 ? 0.0f : 1.0f / wsum;
