@@ -766,3 +766,18 @@ def test_both_forms_give_the_same_attention(mla, kv, q_dtype):
     mla.mla_absorb_out(lat, weights, out)
     # an e4m3 query moves scores of order one by 2^-4 / sqrt 3 of their terms
     assert torch.allclose(out.cpu().double(), o, atol=0.2 if fp8 else 3e-2, rtol=5e-2)
+
+
+# The cache's encoding sets the error: bf16 u / sqrt 3 a stage, e4m3 2^-4 / sqrt 3
+# of every stored value, e2m1 up to a quarter of one.
+@pytest.mark.parametrize("kv,limit", [("bf16", 1e-2), ("fp8", 6e-2), ("mxfp4", 2.5e-1)])
+def test_the_layer_example(mla, kv, limit):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for e in example.main([70, 3, 400], 3, kv):
+        assert e <= limit
