@@ -50,6 +50,9 @@ def _declare(lib):
 
 
 _declare(_lib)
+_cache_step, _cache_write, _absorb_q, _absorb_out, _prefill_run = (
+    _lib.mla_cache_step, _lib.mla_cache_write, _lib.mla_absorb_q, _lib.mla_absorb_out,
+    _lib.mla_prefill_run)
 
 # The handle of a device's current stream.  torch.cuda.current_stream builds a
 # Stream object first, 2.8 us a call on the Grace host against 0.1 us.
@@ -87,18 +90,25 @@ def _rotation(cos_sin, positions, tokens):
         return None, 0, None
     _need(cos_sin is not None and positions is not None,
           "cos_sin and positions go together (both or neither)")
-    if not (cos_sin.is_cuda and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2
-            and cos_sin.shape[1] == ROPE and cos_sin.is_contiguous()):
+    size = cos_sin.shape
+    if not (cos_sin.is_cuda and cos_sin.dtype is torch.float32 and len(size) == 2
+            and size[1] == ROPE and cos_sin.is_contiguous()):
         raise ValueError(f"cos_sin must be a contiguous CUDA tensor [positions, {ROPE}] of float32")
-    _vec("positions", positions, torch.int32, tokens)
-    return cos_sin.data_ptr(), cos_sin.shape[0], positions.data_ptr()
+    if not (positions.is_cuda and positions.dtype is torch.int32 and positions.is_contiguous()
+            and positions.numel() == tokens):
+        _vec("positions", positions, torch.int32, tokens)
+    return cos_sin.data_ptr(), size[0], positions.data_ptr()
+
+
+_POOLS = {"bf16": (ROW, torch.bfloat16), "fp8": (ROW, torch.uint8),
+          "mxfp4": (ROW // 2, torch.uint8)}
 
 
 def _pool(kv, kv_dtype, kv_scale, kv_e8m0):
     """(scale pointer, e8m0 pointer, e8m0 row stride) of a checked pool."""
-    width, dtype = {"bf16": (ROW, torch.bfloat16), "fp8": (ROW, torch.uint8),
-                    "mxfp4": (ROW // 2, torch.uint8)}[kv_dtype]
-    if not (kv.is_cuda and kv.dtype is dtype and kv.dim() == 2 and kv.shape[1] == width
+    width, dtype = _POOLS[kv_dtype]
+    size = kv.shape
+    if not (kv.is_cuda and kv.dtype is dtype and len(size) == 2 and size[1] == width
             and kv.is_contiguous()):
         raise ValueError(f"kv must be a contiguous CUDA tensor [rows, {width}] of {dtype}")
     if kv_dtype == "fp8":
@@ -115,27 +125,28 @@ def _pool(kv, kv_dtype, kv_scale, kv_e8m0):
 
 
 def _weights(w):
-    if not (w.is_cuda and w.dtype is torch.bfloat16 and w.dim() == 3
-            and w.shape[1] == NOPE + V_HEAD and w.shape[2] == LATENT and w.is_contiguous()):
+    size = w.shape
+    if not (w.is_cuda and w.dtype is torch.bfloat16 and len(size) == 3
+            and size[1] == NOPE + V_HEAD and size[2] == LATENT and w.is_contiguous()):
         raise ValueError(f"w must be a contiguous CUDA tensor [heads, {NOPE + V_HEAD}, {LATENT}] "
                          "of bfloat16")
-    return w.shape[0]
+    return size[0]
 
 
 def _query(q, heads):
     """(tokens, token stride, head stride) of q [tokens, heads, 192]; the
     stride of a dimension of size 1 is never used and takes its dense value."""
-    if not (q.is_cuda and q.dtype is torch.bfloat16 and q.dim() == 3 and q.shape[1] == heads
-            and q.shape[2] == NOPE + ROPE and q.stride(2) == 1):
+    size, strides = q.shape, q.stride()
+    if not (q.is_cuda and q.dtype is torch.bfloat16 and len(size) == 3 and size[1] == heads
+            and size[2] == NOPE + ROPE and strides[2] == 1):
         raise ValueError(f"q must be a CUDA tensor [tokens, {heads}, {NOPE + ROPE}] of bfloat16 "
                          "with a dense last dimension")
-    st, sh, _ = q.stride()
-    return (q.shape[0], st if q.shape[0] > 1 else heads * (NOPE + ROPE),
-            sh if heads > 1 else NOPE + ROPE)
+    return (size[0], strides[0] if size[0] > 1 else heads * (NOPE + ROPE),
+            strides[1] if heads > 1 else NOPE + ROPE)
 
 
 def _dense(name, t, dtype, shape):
-    if not (t.is_cuda and t.dtype is dtype and tuple(t.shape) == shape and t.is_contiguous()):
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype}")
 
 
@@ -154,30 +165,48 @@ def mla_cache_step(old_lens, new_lens, block_table, free_pages, *, page_size: in
     """
     i32 = torch.int32
     bs = old_lens.shape[0]
-    _vec("old_lens", old_lens, i32)
-    if new_lens is not None:
-        _vec("new_lens", new_lens, i32, bs)
-    if not (block_table.is_cuda and block_table.dtype is i32 and block_table.dim() == 2
-            and block_table.shape[0] == bs
-            and (block_table.shape[1] <= 1 or block_table.stride(1) == 1)):
-        raise ValueError(f"block_table must be a CUDA tensor [{bs}, columns] of torch.int32 with "
-                         "dense rows")
-    _vec("free_pages", free_pages, i32)
-    _vec("kv_indptr", kv_indptr, i32, bs + 1)
-    _vec("kv_last_page_len", kv_last_page_len, i32, bs)
-    _vec("kv_indices", kv_indices, i32)
-    _vec("qo_indptr", qo_indptr, i32, bs + 1)
-    _vec("slots", slots, torch.int64)
-    _vec("positions", positions, i32, slots.shape[0])
-    _word("pages_used", pages_used, i32)
-    _word("err", err, i32)
-    columns = block_table.shape[1]
-    status = _lib.mla_cache_step(
-        old_lens.data_ptr(), _ptr(new_lens), bs, page_size, block_table.data_ptr(),
-        block_table.stride(0) if bs > 1 else columns, columns, free_pages.data_ptr(),
-        free_pages.shape[0], kv_indptr.data_ptr(), kv_last_page_len.data_ptr(),
-        kv_indices.data_ptr(), kv_indices.shape[0], qo_indptr.data_ptr(), slots.data_ptr(),
-        positions.data_ptr(), slots.shape[0], _ptr(pages_used), _ptr(err), _stream(stream, old_lens))
+    # one pass over the common case; what is wrong is worked out only if it fails
+    if not (old_lens.dtype is i32 and old_lens.is_cuda and old_lens.is_contiguous()
+            and (new_lens is None or (new_lens.dtype is i32 and new_lens.is_cuda
+                                      and new_lens.is_contiguous() and new_lens.numel() == bs))
+            and block_table.dtype is i32 and block_table.is_cuda and block_table.dim() == 2
+            and free_pages.dtype is i32 and free_pages.is_cuda and free_pages.is_contiguous()
+            and kv_indptr.dtype is i32 and kv_indptr.is_cuda and kv_indptr.is_contiguous()
+            and kv_indptr.numel() == bs + 1
+            and kv_last_page_len.dtype is i32 and kv_last_page_len.is_cuda
+            and kv_last_page_len.is_contiguous() and kv_last_page_len.numel() == bs
+            and kv_indices.dtype is i32 and kv_indices.is_cuda and kv_indices.is_contiguous()
+            and qo_indptr.dtype is i32 and qo_indptr.is_cuda and qo_indptr.is_contiguous()
+            and qo_indptr.numel() == bs + 1
+            and slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous()
+            and positions.dtype is i32 and positions.is_cuda and positions.is_contiguous()
+            and positions.numel() == slots.numel()
+            and (pages_used is None or (pages_used.dtype is i32 and pages_used.is_cuda
+                                        and pages_used.numel() == 1))
+            and (err is None or (err.dtype is i32 and err.is_cuda and err.numel() == 1))):
+        _vec("old_lens", old_lens, i32)
+        if new_lens is not None:
+            _vec("new_lens", new_lens, i32, bs)
+        for name, x, n in (("free_pages", free_pages, None), ("kv_indptr", kv_indptr, bs + 1),
+                           ("kv_last_page_len", kv_last_page_len, bs),
+                           ("kv_indices", kv_indices, None), ("qo_indptr", qo_indptr, bs + 1)):
+            _vec(name, x, i32, n)
+        _vec("slots", slots, torch.int64)
+        _vec("positions", positions, i32, slots.numel())
+        _word("pages_used", pages_used, i32)
+        _word("err", err, i32)
+        raise ValueError("block_table must be a CUDA tensor [requests, columns] of torch.int32")
+    rows, columns = block_table.shape
+    stride, dense = block_table.stride()
+    if rows != bs or (columns > 1 and dense != 1):
+        raise ValueError(f"block_table must be [{bs}, columns] with dense rows")
+    status = _cache_step(
+        old_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(), bs, page_size,
+        block_table.data_ptr(), stride if bs > 1 else columns, columns, free_pages.data_ptr(),
+        free_pages.numel(), kv_indptr.data_ptr(), kv_last_page_len.data_ptr(),
+        kv_indices.data_ptr(), kv_indices.numel(), qo_indptr.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), slots.numel(), None if pages_used is None else pages_used.data_ptr(),
+        None if err is None else err.data_ptr(), _stream(stream, old_lens))
     if status:
         _check("mla_cache_step", status)
 
@@ -193,23 +222,31 @@ def mla_cache_write(latent, k_rope, kv, slots, *, kv_dtype: str, norm_weight=Non
     stored), kv the pool as mla_decode_run takes it, rows (optional) bf16
     [T,576]: the values that the stored encoding stands for.
     """
-    T = slots.shape[0]
-    _vec("slots", slots, torch.int64)
-    for name, x, n in (("latent", latent, LATENT), ("k_rope", k_rope, ROPE)):
-        if not (x.is_cuda and x.dtype is torch.bfloat16 and x.dim() == 2 and x.shape[0] == T
-                and x.shape[1] == n and x.stride(1) == 1):
-            raise ValueError(f"{name} must be a CUDA tensor [{T}, {n}] of bfloat16 with a dense "
-                             "last dimension")
-    if norm_weight is not None:
-        _vec("norm_weight", norm_weight, torch.bfloat16, LATENT)
+    T = slots.numel()
+    bf16 = torch.bfloat16
+    ls, rs = latent.stride(), k_rope.stride()
+    if not (slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous()
+            and latent.dtype is bf16 and latent.is_cuda and latent.shape == (T, LATENT)
+            and ls[1] == 1 and k_rope.dtype is bf16 and k_rope.is_cuda
+            and k_rope.shape == (T, ROPE) and rs[1] == 1
+            and (norm_weight is None
+                 or (norm_weight.dtype is bf16 and norm_weight.is_cuda
+                     and norm_weight.is_contiguous() and norm_weight.numel() == LATENT))
+            and (err is None or (err.dtype is torch.int32 and err.is_cuda and err.numel() == 1))):
+        _vec("slots", slots, torch.int64)
+        for name, x, n in (("latent", latent, LATENT), ("k_rope", k_rope, ROPE)):
+            _need(x.is_cuda and x.dtype is bf16 and tuple(x.shape) == (T, n) and x.stride(1) == 1,
+                  f"{name} must be a CUDA tensor [{T}, {n}] of bfloat16 with a dense last dimension")
+        if norm_weight is not None:
+            _vec("norm_weight", norm_weight, bf16, LATENT)
+        _word("err", err, torch.int32)
     if rows is not None:
-        _dense("rows", rows, torch.bfloat16, (T, ROW))
-    _word("err", err, torch.int32)
+        _dense("rows", rows, bf16, (T, ROW))
     scale, e8, e8_stride = _pool(kv, kv_dtype, kv_scale, kv_e8m0)
     cs, npos, pos = _rotation(cos_sin, positions, T)
-    status = _lib.mla_cache_write(
-        latent.data_ptr(), latent.stride(0) if T > 1 else LATENT, k_rope.data_ptr(),
-        k_rope.stride(0) if T > 1 else ROPE, _ptr(norm_weight), eps, cs, npos, pos, ROPES[rope],
+    status = _cache_write(
+        latent.data_ptr(), ls[0] if T > 1 else LATENT, k_rope.data_ptr(),
+        rs[0] if T > 1 else ROPE, _ptr(norm_weight), eps, cs, npos, pos, ROPES[rope],
         slots.data_ptr(), T, DTYPES[kv_dtype], kv.data_ptr(), scale, e8, e8_stride, kv.shape[0],
         _ptr(rows), _ptr(err), _stream(stream, slots))
     if status:
@@ -228,7 +265,7 @@ def mla_absorb_q(q, w, q_out, *, sm_scale: float, positions=None, cos_sin=None,
     _dense("q_out", q_out, torch.uint8 if fp8 else torch.bfloat16, (T, heads, ROW))
     _word("err", err, torch.int32)
     cs, npos, pos = _rotation(cos_sin, positions, T)
-    status = _lib.mla_absorb_q(q.data_ptr(), st, sh, w.data_ptr(), T, heads, sm_scale, cs, npos, pos,
+    status = _absorb_q(q.data_ptr(), st, sh, w.data_ptr(), T, heads, sm_scale, cs, npos, pos,
                                ROPES[rope], 1 if fp8 else 0, _ptr(q_scale), q_out.data_ptr(),
                                _ptr(err), _stream(stream, q))
     if status:
@@ -242,7 +279,7 @@ def mla_absorb_out(o, w, out, *, stream=None) -> None:
     T = o.shape[0]
     _dense("o", o, torch.bfloat16, (T, heads, LATENT))
     _dense("out", out, torch.bfloat16, (T, heads, V_HEAD))
-    status = _lib.mla_absorb_out(o.data_ptr(), w.data_ptr(), T, heads, out.data_ptr(),
+    status = _absorb_out(o.data_ptr(), w.data_ptr(), T, heads, out.data_ptr(),
                                  _stream(stream, o))
     if status:
         _check("mla_absorb_out", status)
@@ -311,7 +348,7 @@ def mla_prefill_run(plan: PrefillPlan, q, kv, w, out, *, workspace, sm_scale: fl
     _need(workspace.is_cuda and workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor")
     scale, e8, e8_stride = _pool(kv, plan.kv_dtype, kv_scale, kv_e8m0)
     cs, npos, pos = _rotation(cos_sin, positions, T)
-    status = _lib.mla_prefill_run(plan.handle, q.data_ptr(), st, sh, kv.data_ptr(), scale, e8,
+    status = _prefill_run(plan.handle, q.data_ptr(), st, sh, kv.data_ptr(), scale, e8,
                                   e8_stride, kv.shape[0], _ptr(kv_indices), w.data_ptr(), sm_scale,
                                   cs, npos, pos, ROPES[rope], workspace.data_ptr(),
                                   workspace.nbytes, out.data_ptr(), _ptr(lse), _stream(stream, q))
