@@ -44,6 +44,7 @@ constexpr uint32_t kExpandSmem = kChunks * kAChunk + kWSlots * kWChunk + 4 * 2 *
 // Row chunks that a thread has in flight from memory.  The proxy fence behind a
 // chunk waits for all of the thread's loads, so none is issued between fences:
 // the chunks come in batches (registers: four of bf16, all of the others).
+constexpr int kFenced = 4;                 // chunks handed over behind one proxy fence
 template <int KV>
 constexpr int kBatch = KV == MLA_DTYPE_BF16 ? 4 : 8;
 
@@ -77,34 +78,29 @@ __device__ __forceinline__ int64_t pool_row(const ExpandParams& p, int page_base
   return page * p.page_size + (tok - e * p.page_size);
 }
 
-// Eight consecutive stored values as they lie in memory.
+// 16 consecutive bytes of a stored row: 8 bf16, 16 e4m3 or 32 e2m1 values (a
+// block, with its exponent).
 template <int KV>
-struct Raw;
-template <>
-struct Raw<MLA_DTYPE_BF16> { uint4 v; };
-template <>
-struct Raw<MLA_DTYPE_FP8_E4M3> { uint2 v; };
-template <>
-struct Raw<MLA_DTYPE_MXFP4> { uint32_t v; uint32_t e; };
+constexpr int kPerLoad = KV == MLA_DTYPE_BF16 ? 8 : KV == MLA_DTYPE_FP8_E4M3 ? 16 : 32;
+struct Raw {
+  uint4 v;
+  uint32_t e;
+};
 
-// Values 8 g .. 8 g + 7 of a row (g = 0..71).
+// The g-th 16 bytes of a row.
 template <int KV>
-__device__ __forceinline__ Raw<KV> load_raw(const ExpandParams& p, int64_t row, int g) {
-  Raw<KV> r;
-  if constexpr (KV == MLA_DTYPE_BF16) {
-    r.v = *reinterpret_cast<const uint4*>(p.kv + row * (kQkDim * 2) + g * 16);
-  } else if constexpr (KV == MLA_DTYPE_FP8_E4M3) {
-    r.v = *reinterpret_cast<const uint2*>(p.kv + row * kQkDim + g * 8);
-  } else {
-    r.v = *reinterpret_cast<const uint32_t*>(p.kv + row * (kQkDim / 2) + g * 4);
-    r.e = p.e8m0[row * p.e8m0_stride + (g >> 2)];
-  }
+__device__ __forceinline__ Raw load_raw(const ExpandParams& p, int64_t row, int g) {
+  constexpr int kRow = kQkDim / kPerLoad<KV> * 16;
+  Raw r;
+  r.v = *reinterpret_cast<const uint4*>(p.kv + row * kRow + g * 16);
+  r.e = KV == MLA_DTYPE_MXFP4 ? p.e8m0[row * p.e8m0_stride + g] : 0;
   return r;
 }
 
-// The same values as bf16, exactly (e4m3 without the per-tensor scale).
+// Values 8 q .. 8 q + 7 of those, as bf16, exactly (e4m3 without the
+// per-tensor scale).
 template <int KV>
-__device__ __forceinline__ uint4 decode(const Raw<KV>& r) {
+__device__ __forceinline__ uint4 decode(const Raw& r, int q) {
   if constexpr (KV == MLA_DTYPE_BF16) {
     return r.v;
   } else if constexpr (KV == MLA_DTYPE_FP8_E4M3) {
@@ -113,13 +109,15 @@ __device__ __forceinline__ uint4 decode(const Raw<KV>& r) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
       return bf16x2(f.x, f.y);
     };
-    const uint4 o = make_uint4(two(r.v.x & 0xffffu), two(r.v.x >> 16), two(r.v.y & 0xffffu),
-                               two(r.v.y >> 16));
-    return o;
+    const uint32_t a = q ? r.v.z : r.v.x, b = q ? r.v.w : r.v.y;
+    return make_uint4(two(a & 0xffffu), two(a >> 16), two(b & 0xffffu), two(b >> 16));
   } else {
+    const uint32_t w = q == 0 ? r.v.x : q == 1 ? r.v.y : q == 2 ? r.v.z : r.v.w;
     const uint32_t s = e8m0_to_bf16x2(r.e);
-    return make_uint4(e2m1x2_to_bf16(r.v & 0xffu, s), e2m1x2_to_bf16((r.v >> 8) & 0xffu, s),
-                      e2m1x2_to_bf16((r.v >> 16) & 0xffu, s), e2m1x2_to_bf16(r.v >> 24, s));
+    uint4 o;
+    e2m1x4_to_bf16(w, s, o.x, o.y);
+    e2m1x4_to_bf16(w >> 16, s, o.z, o.w);
+    return o;
   }
 }
 // The same with the per-tensor scale, rounded.
@@ -139,26 +137,29 @@ __device__ __forceinline__ ExpandTile tile_of(const ExpandParams& p, int pair, i
 template <int KV>
 __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem, int u0, int u1,
                          int rank, int tid) {
-  const int g = tid & 7, r0 = tid >> 3;      // granule of a chunk; rows r0 + 32 i
+  // a chunk of a row is kLanes loads; this thread's rows are r0 + kStep i
+  constexpr int kLanes = 64 / kPerLoad<KV>, kStep = 256 / kLanes, kRows = kPfTile / kStep;
+  constexpr int kPieces = kPerLoad<KV> / 8;  // 16-byte pieces of bf16 that a load becomes
+  const int g = tid % kLanes, r0 = tid / kLanes;
   const float sc = KV == MLA_DTYPE_FP8_E4M3 ? *p.kv_scale : 1.0f;
   uint32_t lap = 0;
   for (int u = u0; u < u1; ++lap) {
     const int pair = u / p.heads;
     const ExpandTile t = tile_of(p, pair, rank);
-    int64_t row[4];
-    bool live[4];
+    int64_t row[kRows];
+    bool live[kRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = t.tok0 + r0 + 32 * i;
+    for (int i = 0; i < kRows; ++i) {
+      const int tok = t.tok0 + r0 + kStep * i;
       live[i] = tok < t.len;
       row[i] = live[i] ? pool_row(p, t.page_base, tok) : 0;
     }
-    Raw<KV> raw[kBatch<KV>][4];
-    Raw<KV> last[4];                         // chunk 8: the rotated dims
-    auto fetch = [&](Raw<KV>* r, int c) {
+    Raw raw[kBatch<KV>][kRows];
+    Raw last[kRows];                         // chunk 8: the rotated dims
+    auto fetch = [&](Raw* r, int c) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (live[i]) r[i] = load_raw<KV>(p, row[i], 8 * c + g);
+      for (int i = 0; i < kRows; ++i)
+        if (live[i]) r[i] = load_raw<KV>(p, row[i], kLanes * c + g);
     };
 #pragma unroll
     for (int b = 0; b < kChunks; b += kBatch<KV>) {
@@ -171,24 +172,33 @@ __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem,
         if (lap > 0 && !mbar_wait(smem_u32(&ms->a_empty[c]), (lap - 1) & 1, p.err, kErrProducer))
           return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r0 + 32 * i;
-          *reinterpret_cast<uint4*>(a_smem + c * kAChunk + r * 128 + ((g ^ (r & 7)) << 4)) =
-              live[i] ? decode<KV>(raw[k][i]) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kRows; ++i) {
+          const int r = r0 + kStep * i;
+#pragma unroll
+          for (int q = 0; q < kPieces; ++q)
+            *reinterpret_cast<uint4*>(a_smem + c * kAChunk + r * 128 +
+                                      (((g * kPieces + q) ^ (r & 7)) << 4)) =
+                live[i] ? decode<KV>(raw[k][i], q) : make_uint4(0, 0, 0, 0);
         }
+        if (c % kFenced != kFenced - 1) continue;
         fence_proxy_async_smem();
         __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(smem_u32(&ms->a_full[c]));
+        if ((tid & 31) == 0)
+          for (int d = c - kFenced + 1; d <= c; ++d) mbar_arrive(smem_u32(&ms->a_full[d]));
       }
     }
     if (u % p.heads == 0 && t.out_row >= 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live[i]) v = decode<KV>(last[i]);
-        if (KV == MLA_DTYPE_FP8_E4M3) v = scaled(v, sc);
-        *reinterpret_cast<uint4*>(p.kr + (static_cast<int64_t>(t.out_row) + r0 + 32 * i) * kRope +
-                                  8 * g) = v;
+      for (int i = 0; i < kRows; ++i) {
+        uint4* out = reinterpret_cast<uint4*>(
+            p.kr + (static_cast<int64_t>(t.out_row) + r0 + kStep * i) * kRope);
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live[i]) v = decode<KV>(last[i], q);
+          if (KV == MLA_DTYPE_FP8_E4M3) v = scaled(v, sc);
+          out[g * kPieces + q] = v;
+        }
       }
     }
     u = min(u1, (pair + 1) * p.heads);

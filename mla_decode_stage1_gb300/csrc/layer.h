@@ -150,14 +150,19 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Two e2m1 codes (a byte's low nibble first) times a power of two given as a
-// bf16 pair, exactly: a code's exponent and mantissa are put at the low end of
-// bf16's and the difference of the biases is multiplied in (a subnormal code
-// becomes a bf16 subnormal, so it comes out right too).
-__device__ __forceinline__ uint32_t e2m1x2_to_bf16(uint32_t byte, uint32_t scale) {
-  const uint32_t t = (byte & 0xfu) | ((byte & 0xf0u) << 12);
-  const uint32_t r = ((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6);
-  return mul_bf16x2(mul_bf16x2(r, 0x7e807e80u), scale);               // 2^126
+// Four e2m1 codes (the low 16 bits of x) times a power of two given as a bf16
+// pair, exactly: the magnitudes' bf16 bytes are looked up by byte permutes, the
+// code's three low bits being the selector.
+__device__ __forceinline__ void e2m1x4_to_bf16(uint32_t x, uint32_t scale, uint32_t& lo,
+                                               uint32_t& hi) {
+  const uint32_t sel = x & 0x7777u;
+  // 0, 0.5, 1, 1.5, 2, 3, 4, 6: high bytes, low bytes; selector bit 3 copies a
+  // byte's top bit, which makes 0xff of a negative code and 0x80 of another
+  uint32_t h = prmt(0x3f3f3f00u, 0x40404040u, sel);
+  const uint32_t l = prmt(0xc0800000u, 0xc0804000u, sel);
+  h |= (prmt(0x80808080u, 0x80808080u, x) << 7) & 0x80808080u;
+  lo = mul_bf16x2(prmt(l, h, 0x5140), scale);
+  hi = mul_bf16x2(prmt(l, h, 0x7362), scale);
 }
 // The power of two of an e8m0 byte as a bf16 pair (255: NaN).
 __device__ __forceinline__ uint32_t e8m0_to_bf16x2(uint32_t e) {
