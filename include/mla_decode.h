@@ -559,9 +559,10 @@ void mla_prefill_destroy(mla_prefill* plan);
 
 /*
  * mla_prefill_run -- one expanded-form attention call, enqueued on `stream`:
- * keys and values are expanded from the cached rows into the workspace
- * (rounded to bf16), then attended to in one pass over the keys; key ranges
- * that the plan split are joined by their log-sum-exp.
+ * keys and values are expanded from the cached rows into the workspace (keys
+ * rounded to bf16, values to fp16 or, where they are too large or small for
+ * it, to bf16), then attended to in one pass over the keys; key ranges that
+ * the plan split are joined by their log-sum-exp.
  *
  *   q          bf16 [query tokens][heads][192] with strides in elements, both
  *              multiples of 8 (and below 2^39); 16-byte aligned.

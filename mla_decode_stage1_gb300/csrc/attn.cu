@@ -22,11 +22,18 @@
 // filling and draining, 6 % each).  Against many keys and few rows HBM bounds
 // it: 77 rows, 32,845 keys: 54 us for 274 MB (5.1 TB/s).
 //
+// Probabilities are rounded to the type of the values that they meet, fp16 or
+// bf16 by groups of 32 keys (expand.cu); each 16-key product is of that type.
+// Sums, maxima and O are fp32.
+//
 // Roles (384 threads): warps 0-3 and 4-7 hold the softmax of tile 0 and 1, a
 // thread per row; warp 8 loads (TMA), warp 9 issues the products (warps 10 and
 // 11 only hold up the third warpgroup, whose registers the softmax takes).
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "prefill.h"
 #include "ptx.cuh"
@@ -56,10 +63,10 @@ constexpr int kStages = 3;
 constexpr uint32_t kPieceBytes = 64 * 128;         // 64 rows x 64 bf16
 constexpr uint32_t kVStages = kStages * 3 * kPieceBytes;      // V stages stand behind K's
 constexpr uint32_t kColS = 0, kColO = 256;         // tile t: + 128 t
-// A row's maximum is kept until a score exceeds it by a factor of 2^16: the
-// probabilities (bf16 has the exponent range of fp32) and their fp32 sums stay
-// far from overflow, no precision is lost, and rescaling O is rare.
-constexpr float kLag = 16.0f;
+// A row's maximum is kept until a score exceeds it by a factor of 2^12: the
+// probabilities stay inside fp16 (2^16), no precision is lost, and rescaling O
+// is rare.
+constexpr float kLag = 12.0f;
 
 struct Misc {
   uint64_t full[kSlots], empty[kSlots];            // units (a pair: K stages, then V stages)
@@ -98,6 +105,14 @@ __device__ __forceinline__ AttnItem load_item(const AttnItem* p) {
   const int4 a = reinterpret_cast<const int4*>(p)[0], b = reinterpret_cast<const int4*>(p)[1];
   return AttnItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
+
+// Types of the values of key step j of a query tile: a byte per 32 keys, 1 = fp16.
+__device__ __forceinline__ uint32_t value_types(const AttnParams& p, const AttnItem& w,
+                                                const Stream& s, int j) {
+  return __ldcg(reinterpret_cast<const uint32_t*>(
+      p.v_half + (w.head * p.kx_rows + w.kv_row + s.begin + j * kPfTile) / kPfGroup));
+}
+constexpr uint32_t kAllHalf = 0x01010101u;
 
 // A wait of the whole warp, which goes on (or gives up) together.
 __device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
@@ -256,6 +271,7 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
                              uint32_t tmem, int it0, int it1) {
   constexpr uint32_t idesc_qk = make_idesc(1, 1, false, false, kTileRows<P>, 128);
   constexpr uint32_t idesc_pv = make_idesc(1, 1, false, true, kTileRows<P>, 128);
+  constexpr uint32_t idesc_pv_half = make_idesc(0, 0, false, true, kTileRows<P>, 128);
   uint32_t n = 0;                   // chunks consumed (a pair: K tiles; its V tiles: nv)
   uint32_t nv = 0;
   uint32_t nq0 = 0, nq1 = 0;        // query tiles used of either kind
@@ -317,9 +333,16 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
   };
   // O_t (+)= P_t V with the V tile from unit k on, a half of 64 keys as soon as
   // its probabilities are there; looks at K's barrier k_next on the way
-  auto pv = [&](int t, uint32_t k, uint32_t parity, bool fresh, bool ready, bool first,
-                uint32_t k_next, bool* k_ready) {
+  auto pv = [&](int t, uint32_t k, uint32_t types, uint32_t parity, bool fresh, bool ready,
+                bool first, uint32_t k_next, bool* k_ready) {
     bool p_ready = false;
+    // Descriptors as uniform data.  (A branch to constant ones where all keys'
+    // values are fp16 cost 2.5 % of the long prompt's kernel with its test up
+    // here, 5 % with a test at each half.)
+    const uint32_t idesc0 = uniform(types & 0x1 ? idesc_pv_half : idesc_pv);
+    const uint32_t idesc1 = uniform(types & 0x100 ? idesc_pv_half : idesc_pv);
+    const uint32_t idesc2 = uniform(types & 0x10000 ? idesc_pv_half : idesc_pv);
+    const uint32_t idesc3 = uniform(types & 0x1000000 ? idesc_pv_half : idesc_pv);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       if (fresh && (half == 0 || !P))
@@ -335,14 +358,16 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
                             : ((k + half) % kSlots) * kChunkBytes;
       const uint64_t b = vd + (at >> 4);
       const uint32_t d = tmem + kColO + 128 * t, a = tmem + kColS + 128 * t + 32 * half;
+      const uint32_t first_pair = half ? idesc2 : idesc0, second_pair = half ? idesc3 : idesc1;
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const bool add = !(first && half == 0 && kk == 0);
+          const uint32_t idesc = kk < 2 ? first_pair : second_pair;
           if constexpr (P)
-            umma_f16_ta_pair(d, a + 8 * kk, b + 128 * kk, idesc_pv, add);
+            umma_f16_ta_pair(d, a + 8 * kk, b + 128 * kk, idesc, add);
           else
-            umma_f16_ta(d, a + 8 * kk, b + 128 * kk, idesc_pv, add);
+            umma_f16_ta(d, a + 8 * kk, b + 128 * kk, idesc, add);
         }
       }
     }
@@ -372,6 +397,13 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
     const int n0 = uniform(tile_steps<P>(w, 0)), n1 = uniform(tile_steps<P>(w, 1));
     const int steps = max(n0, n1);
     if (steps == 0) continue;
+    // types of the values, a step ahead (of either tile's keys)
+    const Stream s0 = stream_of<P>(w, 0), s1 = stream_of<P>(w, 1);
+    uint32_t types0 = n0 > 0 ? value_types(p, w, s0, 0) : 0;
+    uint32_t types1 = n1 > 0 ? value_types(p, w, s1, 0) : 0;
+    auto next_types = [&](const Stream& s, int j, int steps_of) {
+      return j + 1 < steps_of ? value_types(p, w, s, j + 1) : 0u;
+    };
     if constexpr (!P) if (halved(w)) {
       // the query tiles have keys of their own, in turn
       for (int t = 0; t < 2; ++t) {
@@ -389,7 +421,10 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
           const int nt = t ? n1 : n0;
           if (j >= nt) continue;
           bool k_ready = false;
-          if (!pv(t, n, (t ? np1++ : np0++) & 1, true, false, j == 0, n + 2, &k_ready)) return;
+          const uint32_t types = uniform(t ? types1 : types0);
+          if (t) types1 = next_types(s1, j, nt); else types0 = next_types(s0, j, nt);
+          if (!pv(t, n, types, (t ? np1++ : np0++) & 1, true, false, j == 0, n + 2, &k_ready))
+            return;
           if (j + 1 == nt && elect_one()) commit<P>(&ms->o_full[t]);
           release_v(n);
           n += 2;
@@ -417,8 +452,12 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
       const uint32_t v = P ? nv : n, k = P ? n : n + 2;
       bool fresh_v = true, fresh_k = true, k_ready = false;
       const bool v_ready = peek(v_bar(v), lap(v));
+      // (the tiles share their keys)
+      const uint32_t types = uniform(n1 > j ? types1 : types0);
+      types0 = next_types(s0, j, n0);
+      types1 = next_types(s1, j, n1);
       if (j < n0) {
-        if (!pv(0, v, np0++ & 1, true, v_ready, j == 0, k, &k_ready)) return;
+        if (!pv(0, v, types, np0++ & 1, true, v_ready, j == 0, k, &k_ready)) return;
         fresh_v = false;
         if (j + 1 == n0 && elect_one()) commit<P>(&ms->o_full[0]);
         if (j + 1 < n0) {
@@ -427,7 +466,7 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
         }
       }
       if (j < n1) {
-        if (!pv(1, v, np1++ & 1, fresh_v, v_ready, j == 0, k, &k_ready)) return;
+        if (!pv(1, v, types, np1++ & 1, fresh_v, v_ready, j == 0, k, &k_ready)) return;
         if (j + 1 == n1 && elect_one()) commit<P>(&ms->o_full[1]);
       }
       // the values are free before the next scores are through
@@ -443,6 +482,15 @@ __device__ void run_products(const AttnParams& p, Misc* ms, uint32_t q_smem, uin
 }
 
 // -------------------------------------------------------------- softmax
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <bool P>
 __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it0, int it1,
                             int rank, int t, int warp, int lane) {
@@ -460,7 +508,10 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
     const int row = st.first + rank * kPfTile + warp * 32 + lane;     // of the item
     const int limit = min(st.end, w.vis0 + row) - st.begin;           // keys of this range it sees
     float m = -INFINITY, l = 0.0f;
+    uint32_t next_types = n > 0 ? value_types(p, w, st, 0) : 0;
     for (int j = 0; j < n; ++j) {
+      const uint32_t types = next_types;
+      if (j + 1 < n) next_types = value_types(p, w, st, j + 1);
       if (!all_waited(mbar_wait_poll(s_full, ns & 1, p.err, kErrSoftmax))) return;
       ++ns;
       tc_fence_after();
@@ -484,10 +535,11 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
                            __uint_as_float(s[32 * q + i + 1]));
         }
       }
-      // Probabilities of 64 keys with the maximum so far, their sum, bf16 pairs.
+      // Probabilities of 64 keys with the maximum so far, their sum, and pairs
+      // in the values' types.
       uint64_t sum0 = 0, sum1 = 0;
       uint32_t pk[32];
-      auto exponents = [&](const uint32_t* v) {
+      auto exponents = [&](const uint32_t* v, auto all_half, uint32_t bits) {
         // a row that has seen no key keeps p = 2^(-inf) = 0
         const float off = m == -INFINITY ? 0.0f : -m;
         const uint64_t off2 = pack_f32x2(off, off);
@@ -501,9 +553,13 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
           x0 = ex2(x0); x1 = ex2(x1); x2 = ex2(x2); x3 = ex2(x3);
           sum0 = add_f32x2(sum0, pack_f32x2(x0, x1));
           sum1 = add_f32x2(sum1, pack_f32x2(x2, x3));
-          const __nv_bfloat162 c = __floats2bfloat162_rn(x0, x1), d = __floats2bfloat162_rn(x2, x3);
-          pk[i / 2] = *reinterpret_cast<const uint32_t*>(&c);
-          pk[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&d);
+          if (decltype(all_half)::value || ((bits >> (8 * (i / 32))) & 1)) {
+            pk[i / 2] = half2_of(x0, x1);
+            pk[i / 2 + 1] = half2_of(x2, x3);
+          } else {
+            pk[i / 2] = bf16x2_of(x0, x1);
+            pk[i / 2 + 1] = bf16x2_of(x2, x3);
+          }
         }
       };
       auto hand_over = [&](int half) {
@@ -531,10 +587,16 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
           }
         }
       }
-      exponents(s);
-      hand_over(0);
-      exponents(s + 64);
-      hand_over(1);
+      auto probabilities = [&](auto all_half) {
+        exponents(s, all_half, types);
+        hand_over(0);
+        exponents(s + 64, all_half, types >> 16);
+        hand_over(1);
+      };
+      if (__all_sync(0xffffffffu, types == kAllHalf))
+        probabilities(std::true_type());
+      else
+        probabilities(std::false_type());
       float u0, u1;
       unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
       l += u0 + u1;
@@ -639,6 +701,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   if (ms->ours) {
     const int at = P ? blockIdx.x / 2 : blockIdx.x;
     const int it0 = p.cta_indptr[at], it1 = p.cta_indptr[at + 1];
+    // Launched as a programmatic dependent: the kernels before this one have to
+    // be through before anything of theirs is read.  The kernel after it is let
+    // go only then, so one that follows an attention kernel (`after_attn`) finds
+    // the expansion through when it starts, and waits for that attention kernel
+    // only before it ends.
+    if (!p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
       regs_raise<208>();
       run_softmax<P>(p, ms, tmem, it0, it1, rank, warp >> 2, warp & 3, lane);
@@ -646,13 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
       regs_lower<88>();            // 2 x 208 + 88 = 3 x 168, the registers at launch
     }
     if (warp == 8) {
-      // Launched as a programmatic dependent: the kernels before this one have
-      // to be through before their keys and queries are loaded.  The kernel
-      // after it is let go only then, so one that follows an attention kernel
-      // (`after_attn`) finds the expansion through when it starts, and waits
-      // for that attention kernel only before it ends.
-      if (!p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
-      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       if (lane == 0) run_loads<P>(p, ms, q_smem, ring, it0, it1, rank);
     } else if (warp == 9 && rank == 0) {
       run_products<P>(p, ms, q_smem, ring, tmem, uniform(it0), uniform(it1));

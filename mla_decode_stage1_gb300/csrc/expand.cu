@@ -20,8 +20,11 @@
 // pass before the first product (page table, rows and weights from memory).
 //
 // Roundings: e4m3 and e2m1 values with their block exponents are exact in
-// bf16; the per-tensor scale goes into the fp32 epilogue; keys and values are
-// rounded to bf16 once, as operands of the attention's products.
+// bf16; the per-tensor scale goes into the fp32 epilogue.  Keys are rounded to
+// bf16 once, as operands of the attention's products, values to fp16 where the
+// 32 rows of a warp have their largest magnitude in [2^-6, 2^15] (three bits
+// more, far from fp16's ends: an error below 2^-25 is 2^-19 of that magnitude),
+// else to bf16; a flag per 32 rows and head says which.
 //
 // A value row that is not finite would reach every query through 0 x NaN in
 // the attention's product, also those that must not see the token.  Such a
@@ -30,6 +33,8 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "prefill.h"
 #include "ptx.cuh"
@@ -63,6 +68,10 @@ struct ExpandMisc {
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -312,16 +321,20 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* box
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
     const uint32_t acc = tmem + buf * kWRows + (static_cast<uint32_t>(warp) << 21);
-    // 64 columns from x on, rounded, as they go into box `b`
-    auto load = [&](int x, uint32_t (&v)[32]) {
+    // 64 columns from x on, scaled and rounded to fp16 or bf16
+    auto load = [&](auto half, int x, uint32_t (&v)[32]) {
       uint32_t f[64];
       tmem_ld32(acc + x, f);
       tmem_ld32(acc + x + 32, f + 32);
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        v[i] = bf16x2(__uint_as_float(f[2 * i]) * sc, __uint_as_float(f[2 * i + 1]) * sc);
+      for (int i = 0; i < 32; ++i) {
+        const float lo = __uint_as_float(f[2 * i]) * sc, hi = __uint_as_float(f[2 * i + 1]) * sc;
+        v[i] = decltype(half)::value ? half2_of(lo, hi) : bf16x2(lo, hi);
+      }
     };
+    const auto as_half = std::true_type();
+    const auto as_bf16 = std::false_type();
     auto store = [&](int b, int x, const uint32_t (&v)[32]) {
       // the box's last store has read it (one lane keeps the groups)
       if (lane == 0) bulk_wait_read<1>();
@@ -339,17 +352,35 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* box
         bulk_commit();
       }
     };
-    // values first: whether they are finite decides what the key becomes
+    // values first: whether they are finite decides what the key becomes, and
+    // how large they are which type the warp's 32 rows take
     uint32_t v0[32], v1[32];
-    load(kNope, v0);
-    load(kNope + 64, v1);
-    __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
+    load(as_half, kNope, v0);
+    load(as_half, kNope + 64, v1);
+    __half2 top2 = __floats2half2_rn(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v0[i])));
-      top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v1[i])));
+      top2 = __hmax2_nan(top2, __habs2(*reinterpret_cast<const __half2*>(&v0[i])));
+      top2 = __hmax2_nan(top2, __habs2(*reinterpret_cast<const __half2*>(&v1[i])));
     }
-    const bool finite = __low2float(top) < INFINITY && __high2float(top) < INFINITY;
+    // (bits of magnitudes have their order, infinity and NaN above all)
+    uint32_t top = *reinterpret_cast<const uint32_t*>(&top2);
+    top = __reduce_max_sync(0xffffffffu, max(top & 0x7fffu, (top >> 16) & 0x7fffu));
+    bool finite = true;
+    const bool half = top >= 0x2400u && top <= 0x7800u;      // 2^-6, 2^15
+    if (!half) {                             // not the common size (or no row): once more, to bf16
+      load(as_bf16, kNope, v0);
+      load(as_bf16, kNope + 64, v1);
+      __nv_bfloat162 most = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v0[i])));
+        most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v1[i])));
+      }
+      finite = __low2float(most) < INFINITY && __high2float(most) < INFINITY;
+    }
+    if (lane == 0 && out_row >= 0)
+      p.v_half[(static_cast<int64_t>(h) * p.kx_rows + out_row) / kPfGroup + warp] = half ? 1 : 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
       v0[i] = finite ? v0[i] : 0u;
@@ -357,8 +388,8 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* box
     }
     store(0, kNope, v0);
     store(1, kNope + 64, v1);
-    load(0, v0);
-    load(64, v1);
+    load(as_bf16, 0, v0);
+    load(as_bf16, 64, v1);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->acc_empty[buf]), 0));

@@ -9,6 +9,7 @@ namespace mla {
 constexpr int kPfRows = 256;     // query rows of a CTA's item (two 128-row matrix tiles); a pair's
                                  // item has up to twice as many
 constexpr int kPfTile = 128;     // keys of a tile
+constexpr int kPfGroup = 32;     // keys whose values share a type: fp16 (flag 1) or bf16 (0)
 
 // 128 consecutive cached tokens of one request, expanded into workspace rows
 // out_row .. out_row + 127 (rows past the request's end are written as zeros).
@@ -59,6 +60,8 @@ struct ExpandParams {
   int32_t page_size;
   int32_t kv_dtype;
   uint16_t* kr;                // [kx_rows][64]: the keys' rotated dims
+  uint8_t* v_half;             // [heads][kx_rows / 32]: type of the values of 32 rows
+  int64_t kx_rows;
   int32_t* err;                // workspace header
   uint64_t stamp;
 };
@@ -81,6 +84,8 @@ struct AttnParams {
   CUtensorMap map_kr;          // {64, kx_rows, 1}, boxes {64, 64, 1}
   const AttnItem* items;
   const int32_t* cta_indptr;
+  const uint8_t* v_half;       // [heads][kx_rows / 32]
+  int64_t kx_rows;
   int32_t heads;
   int32_t qr_x;
   int32_t after_attn;          // 1: launched behind another attention kernel of the call

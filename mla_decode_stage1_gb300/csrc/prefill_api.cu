@@ -25,7 +25,7 @@ struct mla_prefill {
   std::vector<int32_t> cta_indptr, pair_indptr;
   std::vector<mla::AttnItem> items;
   std::vector<mla::JoinJob> jobs;
-  size_t off_tiles = 0, off_indptr = 0, off_pairs = 0, off_items = 0, off_jobs = 0, off_kx = 0, off_kr = 0, off_qr = 0,
+  size_t off_tiles = 0, off_indptr = 0, off_pairs = 0, off_items = 0, off_jobs = 0, off_kx = 0, off_kr = 0, off_vh = 0, off_qr = 0,
          off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
   std::vector<uint8_t> table;
   uint64_t stamp = 0;
@@ -276,6 +276,7 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   P->table.assign(off, 0);
   P->off_kx = take(sizeof(uint16_t) * P->kx_rows * P->heads * mla::kWRows);
   P->off_kr = take(sizeof(uint16_t) * P->kx_rows * mla::kRope);
+  P->off_vh = take(static_cast<size_t>(P->kx_rows) / mla::kPfGroup * P->heads);
   P->off_qr = take(sizeof(uint16_t) * P->q_tokens * P->heads * mla::kRope);
   P->off_part_o = take(sizeof(float) * P->num_partials * mla::kPfRows * mla::kVHead);
   P->off_part_lse = take(sizeof(float) * P->num_partials * mla::kPfRows);
@@ -408,6 +409,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
   int32_t* err = reinterpret_cast<int32_t*>(ws);
   uint16_t* kx = reinterpret_cast<uint16_t*>(ws + plan->off_kx);
   uint16_t* kr = reinterpret_cast<uint16_t*>(ws + plan->off_kr);
+  uint8_t* v_half = ws + plan->off_vh;
   uint16_t* qr = reinterpret_cast<uint16_t*>(ws + plan->off_qr);
   float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
   float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
@@ -452,6 +454,8 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.page_size = plan->page_size;
     p.kv_dtype = plan->kv_dtype;
     p.kr = kr;
+    p.v_half = v_half;
+    p.kx_rows = plan->kx_rows;
     p.err = err;
     p.stamp = plan->stamp;
     if (rot.cos_sin != nullptr) {
@@ -484,6 +488,8 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.map_kx = plan->map_kx;
     p.map_kr = plan->map_kr;
     p.items = reinterpret_cast<const AttnItem*>(ws + plan->off_items);
+    p.v_half = v_half;
+    p.kx_rows = plan->kx_rows;
     p.heads = plan->heads;
     p.scale_log2 = sm_scale * mla::kLog2e;
     p.out = static_cast<uint16_t*>(out);

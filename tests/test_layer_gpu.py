@@ -617,6 +617,25 @@ def test_prefill_scores_that_grow_and_large_ones(mla):
     assert ((o - ref).abs() <= bound).all() and ((lse - ref_lse).abs() <= lse_bound).all()
 
 
+@pytest.mark.parametrize("q_lens,kv_lens", [([300], [640]), ([700], [1100]), ([40], [2000])])
+def test_prefill_values_of_any_size(mla, q_lens, kv_lens):
+    # values far above and below one (their type is chosen by groups of 32 keys):
+    # by head through the weights, and by key through short rows
+    c = prefill_case(q_lens, kv_lens, 6, "bf16", 8, "interleaved", 17)
+    for h, f in enumerate((1.0, 1e6, 1e-6, 3e4, 1e-12, 0.0)):
+        c["weights"][h, 128:] = (c["weights"][h, 128:].float() * f).bfloat16()
+    at = request_rows(c, 0)
+    short = torch.arange(len(at)) // 40 % 3 == 1
+    c["w"].kv[at[short], :512] = (c["w"].kv[at[short], :512].float() * 1e-3).bfloat16()
+    c["rows"] = c["w"].kv.double()
+    o, lse, _ = run_prefill(mla, c)
+    ref, ref_lse, bound, lse_bound = plain_prefill(c)
+    # (fp16 values: half a step of 2^-25 of 32 keys' largest magnitude; far below)
+    assert ((o - ref).abs() <= bound).all() and ((lse - ref_lse).abs() <= lse_bound).all()
+    for h in range(5):
+        assert (o[:, h] - ref[:, h]).norm() <= 1e-2 * ref[:, h].norm()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_prefill_values_that_are_not_finite(mla, kv):
     # request 0: token 150 is poisoned, seen by query rows 50.. only; request
