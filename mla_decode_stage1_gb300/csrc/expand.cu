@@ -266,9 +266,10 @@ __device__ void run_products(const ExpandParams& p, ExpandMisc* ms, uint32_t a_s
   auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
   uint32_t slot = 0, phase = 0, lap = 0, k = 0;
   bool w_ready = false;
+  int left = p.heads - uniform(u0 % p.heads);                // units of the present tiles
+  bool first = true;                                         // of the tiles, here
   for (int u = u0; u < u1; ++u, ++k) {
-    const bool first = u == u0 || u % p.heads == 0;          // first unit of its tiles here
-    const bool last = u + 1 == u1 || (u + 1) % p.heads == 0;
+    const bool last = u + 1 == u1 || left == 1;
     const uint32_t buf = k & 1;
     if (k >= 2 && !all(mbar_wait_cluster(smem_u32(&ms->acc_empty[buf]), ((k >> 1) - 1) & 1, p.err,
                                          kErrMma)))
@@ -302,6 +303,8 @@ __device__ void run_products(const ExpandParams& p, ExpandMisc* ms, uint32_t a_s
     }
     if (elect_one()) tc_commit_pair(smem_u32(&ms->acc_full[buf]));
     if (last) ++lap;
+    first = last;
+    left = left == 1 ? p.heads : left - 1;
   }
 }
 
