@@ -17,13 +17,16 @@
 // scores, all that its shared memory gives, and takes in its keys beside that:
 // a step takes about 3,700 cycles where the products need 2,560.  Two CTAs as a
 // pair (one product of M = 256, half of each key and value tile in either)
-// take 2,790: 8192 tokens, 16 heads, causal: 210 us on single CTAs, 194 us in
-// pairs (1.77 PFLOP/s, tensor pipe 78 % busy; what is left is 3 items a CTA
-// filling and draining, 6 % each).  Against many keys and few rows HBM bounds
-// it: 77 rows, 32,845 keys: 54 us for 274 MB (5.1 TB/s).
+// take 2,790: 8192 tokens, 16 heads, causal: 210 us on single CTAs, 196 us in
+// pairs (1.75 PFLOP/s, tensor pipe 79 % busy; what is left is 3 items a CTA
+// filling and draining, 5 % each).  Against many keys and few rows HBM bounds
+// it: 77 rows, 32,845 keys: 56 us for 274 MB (4.9 TB/s).
 //
 // Probabilities are rounded to the type of the values that they meet, fp16 or
 // bf16 by groups of 32 keys (expand.cu); each 16-key product is of that type.
+// (bf16 alone: 1 % faster in pairs and 5 % on single CTAs, but an error of the
+// output of 0.0026 to 0.0031 instead of 0.0021 to 0.0023, 0.0017 of it the
+// rounding of the output.)
 // Sums, maxima and O are fp32.
 //
 // Roles (384 threads): warps 0-3 and 4-7 hold the softmax of tile 0 and 1, a
