@@ -66,10 +66,12 @@ constexpr int kStages = 3;
 constexpr uint32_t kPieceBytes = 64 * 128;         // 64 rows x 64 bf16
 constexpr uint32_t kVStages = kStages * 3 * kPieceBytes;      // V stages stand behind K's
 constexpr uint32_t kColS = 0, kColO = 256;         // tile t: + 128 t
-// A row's maximum is kept until a score exceeds it by a factor of 2^12: the
-// probabilities stay inside fp16 (2^16), no precision is lost, and rescaling O
-// is rare.
-constexpr float kLag = 12.0f;
+// A row's maximum is kept until a score exceeds it by a factor of 2^8, so that
+// rescaling O is rare.  Probabilities are 2^7 times their value against that
+// maximum: at most 2^15 in fp16's 2^16, and down to 2^-21 of the largest with
+// all of fp16's bits, 2^-31 as its smallest (a first token with nearly all of
+// the weight and a small value leaves the output to such keys).
+constexpr float kLag = 8.0f, kLift = 7.0f;
 
 struct Misc {
   uint64_t full[kSlots], empty[kSlots];            // units (a pair: K stages, then V stages)
@@ -559,7 +561,7 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
       uint32_t pk[32];
       auto exponents = [&](const uint32_t* v, auto all_half, uint32_t bits) {
         // a row that has seen no key keeps p = 2^(-inf) = 0
-        const float off = m == -INFINITY ? 0.0f : -m;
+        const float off = m == -INFINITY ? 0.0f : kLift - m;
         const uint64_t off2 = pack_f32x2(off, off);
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
@@ -663,7 +665,7 @@ __device__ void run_softmax(const AttnParams& p, Misc* ms, uint32_t tmem, int it
     }
     tc_fence_before();
     if (live) {
-      const float lse2 = seen ? m + __log2f(l) : -INFINITY;
+      const float lse2 = seen ? m - kLift + __log2f(l) : -INFINITY;
       if (w.slot >= 0)
         p.part_lse[part] = lse2;
       else if (p.lse != nullptr)

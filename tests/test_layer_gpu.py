@@ -636,6 +636,26 @@ def test_prefill_values_of_any_size(mla, q_lens, kv_lens):
         assert (o[:, h] - ref[:, h]).norm() <= 1e-2 * ref[:, h].norm()
 
 
+@pytest.mark.parametrize("q_lens,kv_lens", [([40], [1500]), ([300], [1500]), ([600], [1500])])
+@pytest.mark.parametrize("at", [0, 700])
+def test_prefill_small_weights_count(mla, q_lens, kv_lens, at):
+    # one key takes nearly all of the weight and has no value: the output is what
+    # the others' weights of 2^-23.3 leave.  Scores are exact: 16 x 14 or zero.
+    c = prefill_case(q_lens, kv_lens, 2, "bf16", 8, None, 21)
+    rows = request_rows(c, 0)
+    c["w"].kv[rows, 512:] = 0
+    c["w"].kv[rows[at], :512] = 0
+    c["w"].kv[rows[at], 512] = 16
+    c["rows"] = c["w"].kv.double()
+    c["q"][:] = 0
+    c["q"][..., 128] = 14
+    o, lse, _ = run_prefill(mla, c)
+    ref, ref_lse, _, lse_bound = plain_prefill(c)
+    # the weights: half a step of 2^-24 on 2^-17 or more; values 2^-11, output 2^-8
+    assert (o - ref).norm() <= (2**-8 + 2**-11 + 2**-8) * ref.norm()
+    assert ((lse - ref_lse).abs() <= lse_bound).all()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_prefill_values_that_are_not_finite(mla, kv):
     # request 0: token 150 is poisoned, seen by query rows 50.. only; request
