@@ -820,3 +820,61 @@ def test_the_layer_example(mla, kv, limit):
     spec.loader.exec_module(example)
     for e in example.main([70, 3, 400], 3, kv):
         assert e <= limit
+
+
+def test_rows_past_4_gb_of_a_pool(mla):
+    # the same request in the last pages of a pool of 4.6 GB and in a small one
+    n, page = 200, 8
+    g = torch.Generator(device="cuda").manual_seed(31)
+    lat = torch.randn(n, 512, generator=g, device="cuda").bfloat16()
+    rope = torch.randn(n, 64, generator=g, device="cuda").bfloat16()
+    q = torch.randn(n, 2, 192, generator=g, device="cuda").bfloat16()
+    weights = make_w(2, gen(31)).cuda()
+    outs = []
+    for rows in (n, 4_000_000):
+        pool = torch.zeros(rows, 576, dtype=torch.bfloat16, device="cuda")
+        first = (rows - n) // page
+        mla.mla_cache_write(lat, rope, pool, first * page + torch.arange(n, device="cuda"),
+                            kv_dtype="bf16")
+        assert torch.equal(pool[-n:], torch.cat([lat, rope], 1))
+        assert rows == n or not pool[:n].any()
+        plan = mla.mla_prefill_plan([0, n], [0, n // page], page_size=page, heads=2,
+                                    kv_dtype="bf16")
+        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        out = torch.empty(n, 2, 128, dtype=torch.bfloat16, device="cuda")
+        mla.mla_prefill_run(plan, q, pool, weights, out, workspace=ws, sm_scale=SCALE,
+                            kv_indices=first + torch.arange(n // page, device="cuda").int())
+        mla.mla_prefill_check(plan, ws)
+        outs.append(out.clone())
+        del pool
+    assert torch.equal(outs[0], outs[1]) and outs[0].abs().sum() > 0
+
+
+def test_prefill_keys_past_4_gb_of_the_workspace(mla):
+    # 600,000 keys of 16 heads expand into 4.9 GB; the last heads stand behind 2^32
+    n, m, heads, page = 600_000, 5, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(32)
+    pages = n // page
+    pool = torch.randn(n, 576, generator=g, device="cuda").bfloat16()
+    table = torch.randperm(pages, generator=g, device="cuda").int()
+    q = torch.randn(m, heads, 192, generator=g, device="cuda").bfloat16()
+    weights = make_w(heads, gen(32)).cuda()
+    plan = mla.mla_prefill_plan([0, m], [0, pages], page_size=page, heads=heads, kv_dtype="bf16")
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = torch.empty(m, heads, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(m, heads, device="cuda")
+    mla.mla_prefill_run(plan, q, pool, weights, out, workspace=ws, sm_scale=SCALE,
+                        kv_indices=table, lse=lse)
+    mla.mla_prefill_check(plan, ws)
+    rows = pool.view(pages, page, 576)[table.long()].view(n, 576)
+    see = torch.arange(n, device="cuda")[None] < n - m + 1 + torch.arange(m, device="cuda")[:, None]
+    for h in (0, heads - 1):
+        x = rows[:, :512].double() @ weights[h].double().T
+        k = torch.cat([x[:, :128], rows[:, 512:].double()], 1)
+        s = (q[:, h].double() @ k.T * SCALE).masked_fill(~see, -math.inf)
+        mag = (q[:, h].double().abs() @ k.abs().T).amax() * SCALE
+        o = torch.softmax(s, -1) @ x[:, 128:]
+        # independent roundings, as for the other prefill tests; scores off by e
+        assert (out[:, h].double() - o).norm() <= 1e-2 * o.norm()
+        assert ((lse[:, h].double() - torch.logsumexp(s, -1)).abs() <= mag * (2 * U + 400 * F)
+                + (n + 64) * F).all()
