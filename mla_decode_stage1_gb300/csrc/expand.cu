@@ -62,7 +62,7 @@ constexpr int kBatch = KV == MLA_DTYPE_BF16 ? 4 : 8;
 // Barriers that the issuing (even) CTA waits on stand there; commits arrive in
 // both CTAs.
 struct ExpandMisc {
-  uint64_t a_full[kChunks], a_peer[kChunks], a_empty[kChunks];
+  uint64_t a_full[kChunks], a_peer[kChunks / kFenced], a_empty[kChunks];
   uint64_t w_full[kWSlots], w_empty[kWSlots];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -220,17 +220,20 @@ __device__ void run_rows(const ExpandParams& p, ExpandMisc* ms, uint8_t* a_smem,
   }
 }
 
-// In the odd CTA: passes the arrival of its rows on to the even one.  (The rows
-// are in this SM's shared memory, behind their writers' proxy fences, and only
-// this SM's tensor core reads them: a relaxed arrival does, where a release
-// for the cluster would hold up every chunk by about 1,500 cycles.)
+// In the odd CTA: passes the arrival of its rows on to the even one, whose
+// products read them.  Ordinary shared memory goes to another CTA, so this is a
+// release for the cluster, met by an acquire; a thread that does nothing else
+// issues it, once for the chunks behind one proxy fence (with eight relaxed
+// arrivals a tile the expansion took as long: 54 us of the ragged fp8 batch, 91
+// of 32,845 MXFP4 keys).
 __device__ void run_relay(const ExpandParams& p, ExpandMisc* ms, int u0, int u1) {
   uint32_t lap = 0;
   for (int u = u0; u < u1; ++lap) {
     for (int c = 0; c < kChunks; ++c) {
       if (!mbar_wait(smem_u32(&ms->a_full[c]), lap & 1, p.err, kErrProducer)) return;
+      if (c % kFenced != kFenced - 1) continue;
       fence_proxy_async_smem();
-      mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->a_peer[c]), 0));
+      mbar_arrive_cluster_release(dsmem_addr(smem_u32(&ms->a_peer[c / kFenced]), 0));
     }
     u = min(u1, (u / p.heads + 1) * p.heads);
   }
@@ -283,7 +286,10 @@ __device__ void run_products(const ExpandParams& p, ExpandMisc* ms, uint32_t a_s
     for (int c = 0; c < kChunks; ++c) {
       if (first) {
         if (!all(mbar_wait(smem_u32(&ms->a_full[c]), lap & 1, p.err, kErrMma))) return;
-        if (!all(mbar_wait_cluster(smem_u32(&ms->a_peer[c]), lap & 1, p.err, kErrMma))) return;
+        if (c % kFenced == 0 &&
+            !all(mbar_wait_cluster<true>(smem_u32(&ms->a_peer[c / kFenced]), lap & 1, p.err,
+                                         kErrMma)))
+          return;
       }
       if (!all(w_ready) &&
           !all(mbar_wait_poll(smem_u32(&ms->w_full[slot]), phase, p.err, kErrMma)))
@@ -427,9 +433,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kChunks; ++i) {
       mbar_init(smem_u32(&ms->a_full[i]), 8);             // a warp's arrival each
-      mbar_init(smem_u32(&ms->a_peer[i]), 1);
       mbar_init(smem_u32(&ms->a_empty[i]), 1);
     }
+    for (int i = 0; i < kChunks / kFenced; ++i) mbar_init(smem_u32(&ms->a_peer[i]), 1);
     for (int i = 0; i < kWSlots; ++i) {
       mbar_init(smem_u32(&ms->w_full[i]), 1);
       mbar_init(smem_u32(&ms->w_empty[i]), 1);

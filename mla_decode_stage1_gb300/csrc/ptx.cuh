@@ -459,31 +459,48 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
-// Arrival on a barrier of any CTA of the cluster, and its wait, for threads
-// that hand over tensor memory (ordered by the tcgen05 fences around the two)
-// and no other memory: a release for the whole cluster took about 1,500 cycles.
+// Arrival on a barrier of any CTA of the cluster, and its wait.  Relaxed: for
+// threads that hand over tensor memory (ordered by the tcgen05 fences around
+// the two) and no other memory.  Release and acquire: for everything else; the
+// release takes about 1,500 cycles, so it is for a thread that has nothing else
+// to do.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+template <bool kAcquire = false>
 __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (kAcquire)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
   return ok != 0;
 }
+template <bool kAcquire = false>
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int32_t* err,
                                                   int32_t code) {
 #pragma unroll 1
   for (int i = 0; i < kPolls; ++i)
-    if (mbar_test_cluster(bar, parity)) return true;
+    if (mbar_test_cluster<kAcquire>(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_test_cluster(bar, parity)) {
+  while (!mbar_test_cluster<kAcquire>(bar, parity)) {
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       atomicOr(err, code);
       return false;

@@ -878,3 +878,59 @@ def test_prefill_keys_past_4_gb_of_the_workspace(mla):
         assert (out[:, h].double() - o).norm() <= 1e-2 * o.norm()
         assert ((lse[:, h].double() - torch.logsumexp(s, -1)).abs() <= mag * (2 * U + 400 * F)
                 + (n + 64) * F).all()
+
+
+def prefill_calls(mla, cases, num_sms=0):
+    """Cases of the same lengths on the device: (plan, workspace, calls), a call
+    of case i being calls[i](out)."""
+    c = cases[0]
+    ws = [x["w"].to("cuda") for x in cases]
+    plan = mla.mla_prefill_plan(c["qo"], ws[0].kv_indptr, ws[0].kv_last_page_len,
+                                page_size=c["page"], heads=c["heads"], kv_dtype=ws[0].kv_dtype,
+                                num_sms=num_sms)
+    space = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+
+    def call(x, w):
+        q, weights = x["q"].cuda(), x["weights"].cuda()
+        rope = {} if not x["rope"] else dict(positions=x["pos"].cuda(), cos_sin=x["table"].cuda(),
+                                             rope=x["rope"])
+
+        def run(out, kv=w.kv, **kw):
+            mla.mla_prefill_run(plan, q, kv, weights, out, workspace=space, sm_scale=SCALE,
+                                kv_scale=w.kv_scale, kv_e8m0=w.kv_e8m0, kv_indices=w.kv_indices,
+                                **rope, **kw)
+        return run
+
+    return plan, space, [call(x, w) for x, w in zip(cases, ws)]
+
+
+def repeats(mla, cases, times, num_sms=0):
+    """Calls of the cases in turn, many times without a pause, give each case's
+    first output bit by bit: a row or a result of the call before would show."""
+    plan, space, calls = prefill_calls(mla, cases, num_sms)
+    shape = (cases[0]["qo"][-1], cases[0]["heads"], 128)
+    first = []
+    for run in calls:
+        out = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        run(out)
+        torch.cuda.synchronize()
+        first.append(out)
+    differing = torch.zeros(1, dtype=torch.int64, device="cuda")
+    out = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    for i in range(times):
+        out.fill_(7.0)
+        calls[i % len(calls)](out)
+        differing += (out.view(torch.int16) != first[i % len(calls)].view(torch.int16)).sum()
+    mla.mla_prefill_check(plan, space)
+    assert differing.item() == 0
+    return [f.cpu().double() for f in first]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "mxfp4"])
+def test_prefill_expansion_takes_every_new_row(mla, kv):
+    # few heads against many keys on few CTA pairs: rows are replaced every two
+    # units, in both CTAs of a pair, and the products wait for them each time
+    cases = [prefill_case([64], [6000], 2, kv, 8, "interleaved", s) for s in (51, 52)]
+    for c, o in zip(cases, repeats(mla, cases, 200, num_sms=8)):
+        ref, _, bound, _ = plain_prefill(c)
+        assert ((o - ref).abs() <= bound).all()
