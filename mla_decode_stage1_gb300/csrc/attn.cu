@@ -80,6 +80,7 @@ struct Misc {
   uint64_t drain;
   uint32_t tmem;
   uint32_t ours;
+  int32_t expanded;
 };
 
 // What query tile t of an item works on: rows from `first` of the item on,
@@ -154,6 +155,7 @@ __device__ void run_loads(const AttnParams& p, Misc* ms, uint32_t q_smem, uint32
   uint32_t nq0 = 0, nq1 = 0;        // query tiles loaded of either kind
   bool ok = true;
   const uint64_t keep = l2_policy_evict_normal();
+  fence_proxy_async();              // (behind the expansion, if word was left of it)
   // unit `s` is free in its lap; its bytes are announced (a pair's on the even
   // CTA, for both)
   auto open = [&](uint32_t s, uint32_t lap, uint32_t bytes) {
@@ -703,6 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     fence_mbar_init();
     ms->ours = reinterpret_cast<const WsHeader*>(p.err)->stamp == p.stamp ? 1 : 0;
     if (!ms->ours) atomicOr(p.err, kErrStale);
+    ms->expanded = p.after_attn ? ld_acquire_gpu(expanded_word(p.err)) : 0;
   }
   if (warp == 9) {
     if constexpr (P) {
@@ -722,11 +725,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     const int at = P ? blockIdx.x / 2 : blockIdx.x;
     const int it0 = p.cta_indptr[at], it1 = p.cta_indptr[at + 1];
     // Launched as a programmatic dependent: the kernels before this one have to
-    // be through before anything of theirs is read.  The kernel after it is let
-    // go only then, so one that follows an attention kernel (`after_attn`) finds
-    // the expansion through when it starts, and waits for that attention kernel
-    // only before it ends.
-    if (!p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // be through before anything of theirs is read.  One that follows an
+    // attention kernel (`after_attn`) reads nothing of that one, only of the
+    // expansion, which the first kernel has waited for before it lets this one
+    // go.  It leaves word of that, by a release here and an acquire there, so
+    // that this kernel may start beside the first one's last items and wait for
+    // it only before it ends (mixed batches: 2 to 7 % less than with the wait up
+    // here).  Without the word it waits.
+    if (!p.after_attn || !ms->expanded) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (P && threadIdx.x == 0) st_release_gpu(expanded_word(p.err), 1);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
       regs_raise<208>();
@@ -746,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
     }
     __syncwarp();
   }
-  if (p.after_attn) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if constexpr (P) {

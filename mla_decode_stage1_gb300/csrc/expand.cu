@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     fence_mbar_init();
     ms->ours = reinterpret_cast<const WsHeader*>(p.err)->stamp == p.stamp ? 1 : 0;
     if (!ms->ours) atomicOr(p.err, kErrStale);
+    else if (blockIdx.x == 0) *expanded_word(p.err) = 0;
   }
   if (warp == 13) {
     tmem_alloc_pair(smem_u32(&ms->tmem), 512);
@@ -483,7 +484,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     }
     __syncwarp();
   }
-  // Nothing here needs the rotation of the queries; what follows needs both.
+  // Nothing here needs the rotation of the queries (a launch in full stream
+  // order, behind everything that the expansion reads); what follows needs both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();

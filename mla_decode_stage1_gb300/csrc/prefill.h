@@ -11,6 +11,17 @@ constexpr int kPfRows = 256;     // query rows of a CTA's item (two 128-row matr
 constexpr int kPfTile = 128;     // keys of a tile
 constexpr int kPfGroup = 32;     // keys whose values share a type: fp16 (flag 1) or bf16 (0)
 
+// The workspace begins with WsHeader and, behind it, `expanded`: 0 from the
+// expansion on, 1 once the attention on pairs has found the expansion through.
+struct PrefillHeader {
+  WsHeader ws;
+  int32_t expanded;
+  int32_t pad[3];
+};
+__device__ __forceinline__ int32_t* expanded_word(int32_t* err) {
+  return &reinterpret_cast<PrefillHeader*>(err)->expanded;
+}
+
 // 128 consecutive cached tokens of one request, expanded into workspace rows
 // out_row .. out_row + 127 (rows past the request's end are written as zeros).
 struct ExpandTile {

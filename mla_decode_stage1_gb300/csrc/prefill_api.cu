@@ -262,7 +262,7 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   P->jobs = pair.jobs;
   P->jobs.insert(P->jobs.end(), single.jobs.begin(), single.jobs.end());
 
-  size_t off = align256(sizeof(mla::WsHeader));
+  size_t off = align256(sizeof(mla::PrefillHeader));
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off = align256(off + bytes);
@@ -282,8 +282,8 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   P->off_part_lse = take(sizeof(float) * P->num_partials * mla::kPfRows);
   P->ws_bytes = off;
   P->stamp = mla::new_plan_stamp();
-  mla::WsHeader hdr{};
-  hdr.stamp = P->stamp;
+  mla::PrefillHeader hdr{};
+  hdr.ws.stamp = P->stamp;
   auto put = [&](size_t at, const void* src, size_t bytes) {
     if (bytes > 0) std::memcpy(P->table.data() + at, src, bytes);
   };

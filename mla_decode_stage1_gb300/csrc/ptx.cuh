@@ -146,6 +146,20 @@ __device__ __forceinline__ void st_global_32(void* ptr, const uint32_t* v) {
                : "memory");
 }
 
+// A word that hands global memory over to another kernel, and the fence that
+// puts asynchronous copies behind what the acquire has seen.
+__device__ __forceinline__ void st_release_gpu(int32_t* ptr, int32_t v) {
+  asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(ptr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int32_t ld_acquire_gpu(const int32_t* ptr) {
+  int32_t v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+
 // ------------------------------------------------------------ cp.async rows
 // 16-byte asynchronous copy global -> shared (cached in L1, so that the other
 // 16-byte pieces of the same line hit there).

@@ -934,3 +934,17 @@ def test_prefill_expansion_takes_every_new_row(mla, kv):
     for c, o in zip(cases, repeats(mla, cases, 200, num_sms=8)):
         ref, _, bound, _ = plain_prefill(c)
         assert ((o - ref).abs() <= bound).all()
+
+
+def test_prefill_on_pairs_and_single_ctas_repeats(mla):
+    # blocks of 512 rows on CTA pairs and the rest on CTAs of their own, which
+    # start beside the pairs' last items: more CTAs in all than planned for
+    cases = [prefill_case([1300, 400, 900], [2300, 4400, 900], 2, "bf16", 8, "interleaved", s)
+             for s in (53, 54)]
+    plan = mla.mla_prefill_plan(cases[0]["qo"], cases[0]["w"].kv_indptr,
+                                cases[0]["w"].kv_last_page_len, page_size=8, heads=2,
+                                kv_dtype="bf16", num_sms=4)
+    assert plan.info().num_ctas > 4
+    for c, o in zip(cases, repeats(mla, cases, 200, num_sms=4)):
+        ref, _, bound, _ = plain_prefill(c)
+        assert ((o - ref).abs() <= bound).all()
