@@ -573,7 +573,10 @@ void mla_prefill_destroy(mla_prefill* plan);
  *              rotation of the queries' last 64 dims (cached rows hold rotated
  *              keys); positions [query tokens].
  *   workspace  mla_prefill_info.workspace_bytes device bytes, 256-byte
- *              aligned; its rules are those of mla_decode_run.
+ *              aligned; its rules are those of mla_decode_run.  Every record of
+ *              the work table in it is checked: one that something else has
+ *              overwritten since is not followed, and mla_prefill_check returns
+ *              MLA_ERR_WORKSPACE (the call's outputs are then not valid).
  *   out        bf16 [query tokens][heads][128] contiguous, 32-byte aligned.
  *   lse        fp32 [query tokens][heads], natural log, or NULL.
  * A cached token whose row holds a value that is not finite affects only the

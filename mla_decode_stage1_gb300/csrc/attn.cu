@@ -723,7 +723,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const __grid_constant
   const uint32_t tmem = uniform(ms->tmem);
   if (ms->ours) {
     const int at = P ? blockIdx.x / 2 : blockIdx.x;
-    const int it0 = p.cta_indptr[at], it1 = p.cta_indptr[at + 1];
+    // the CTA's items, all checked before the first is taken up (a pair's two
+    // CTAs check the same ones)
+    const int4 mine = reinterpret_cast<const int4*>(p.ctas)[at];
+    bool sound = check_of(CtaItems{mine.x, mine.y, 0u, 0}, p.stamp) ==
+                 static_cast<uint32_t>(mine.z);
+    const int it0 = sound ? mine.x : 0;
+    for (int it = it0 + static_cast<int>(threadIdx.x); sound && it < mine.y; it += kThreads)
+      sound = check_of(load_item(p.items + it), p.stamp) == p.item_checks[it];
+    sound = __syncthreads_and(sound);
+    if (!sound && threadIdx.x == 0) atomicOr(p.err, kErrStale);
+    const int it1 = uniform(sound ? mine.y : it0);
     // Launched as a programmatic dependent: the kernels before this one have to
     // be through before anything of theirs is read.  One that follows an
     // attention kernel (`after_attn`) reads nothing of that one, only of the

@@ -143,10 +143,17 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, float sc) {
   return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
 }
 
-// The tile of this CTA in tile pair `pair`; an odd last pair has an empty one.
+// The tile of this CTA in tile pair `pair`; an odd last pair has an empty one,
+// and so does a record that fails its check.
 __device__ __forceinline__ ExpandTile tile_of(const ExpandParams& p, int pair, int rank) {
   const int i = 2 * pair + rank;
-  return i < p.num_tiles ? p.tiles[i] : ExpandTile{0, 0, 0, -1};
+  const ExpandTile none{0, 0, 0, -1, 0u, {}};
+  if (i >= p.num_tiles) return none;
+  const int4 a = reinterpret_cast<const int4*>(p.tiles + i)[0];
+  const ExpandTile t{a.x, a.y, a.z, a.w, p.tiles[i].check, {}};
+  if (check_of(t, p.stamp) == t.check) return t;
+  atomicOr(p.err, kErrStale);
+  return none;
 }
 
 template <int KV>

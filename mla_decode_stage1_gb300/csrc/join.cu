@@ -16,6 +16,10 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   if (reinterpret_cast<const WsHeader*>(p.err)->stamp != p.stamp) return;   // reported by attn_kernel
   const int lane = threadIdx.x & 31;
   const JoinJob j = p.jobs[blockIdx.x];
+  if (check_of(j, p.stamp) != j.check) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrStale);
+    return;
+  }
   const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (i >= j.rows) return;
   // Weights first, a part per lane and 32 at a time, then the parts' rows,

@@ -22,12 +22,38 @@ __device__ __forceinline__ int32_t* expanded_word(int32_t* err) {
   return &reinterpret_cast<PrefillHeader*>(err)->expanded;
 }
 
+// Every record of the table carries a check word of the plan's stamp and its
+// own fields.  A record of another plan, one that something else has overwritten
+// in a workspace with the stamp still in place, or half of an upload (a run on a
+// second stream that does not wait for it) fails it, is reported as kErrStale
+// and stands for no work: nothing is read or written by what it says.
+__host__ __device__ inline uint32_t mix(uint32_t h, int32_t v) {
+  h = (h ^ static_cast<uint32_t>(v)) * 0x9e3779b1u;
+  return h ^ (h >> 15);
+}
+
 // 128 consecutive cached tokens of one request, expanded into workspace rows
 // out_row .. out_row + 127 (rows past the request's end are written as zeros).
 struct ExpandTile {
   int32_t page_base, tok0, len, out_row;   // first page-table entry, first token, request length
+  uint32_t check;
+  int32_t pad[3];
 };
-static_assert(sizeof(ExpandTile) == 16, "an expansion tile is one int4");
+static_assert(sizeof(ExpandTile) == 32, "an expansion tile is two int4");
+__host__ __device__ inline uint32_t check_of(const ExpandTile& t, uint64_t stamp) {
+  return mix(mix(mix(mix(static_cast<uint32_t>(stamp), t.page_base), t.tok0), t.len), t.out_row);
+}
+
+// The items of one CTA (or pair).
+struct CtaItems {
+  int32_t begin, end;
+  uint32_t check;
+  int32_t pad;
+};
+static_assert(sizeof(CtaItems) == 16, "a CTA's range is one int4");
+__host__ __device__ inline uint32_t check_of(const CtaItems& c, uint64_t stamp) {
+  return mix(mix(static_cast<uint32_t>(stamp), c.begin), c.end);
+}
 
 // Query rows q_row .. q_row + rows - 1 of one head against keys
 // [kv_begin, kv_end) of their request (kv_begin a multiple of 128).  Row i
@@ -35,11 +61,17 @@ static_assert(sizeof(ExpandTile) == 16, "an expansion tile is one int4");
 // else a partial result.  Partial items of at most 128 rows are `halved`: their
 // rows fill both query tiles, tile 0 against the first half of the keys and
 // tile 1 against the second, with partial results slot and slot + 1.
+// (Their check words stand in an array of their own: the attention kernel has no
+// register left for one.)
 struct AttnItem {
   int32_t q_row, rows, head, kv_row;       // kv_row: workspace row of the request's key 0
   int32_t vis0, kv_begin, kv_end, slot;
 };
 static_assert(sizeof(AttnItem) == 32, "an attention item is two int4");
+__host__ __device__ inline uint32_t check_of(const AttnItem& w, uint64_t stamp) {
+  const uint32_t h = mix(mix(mix(static_cast<uint32_t>(stamp), w.q_row), w.rows), w.head);
+  return mix(mix(mix(mix(mix(h, w.kv_row), w.vis0), w.kv_begin), w.kv_end), w.slot);
+}
 
 __host__ __device__ inline bool halved(const AttnItem& w) {
   return w.slot >= 0 && w.rows <= kPfTile;
@@ -54,8 +86,14 @@ __host__ __device__ inline int32_t middle_key(const AttnItem& w) {
 // Join of `count` consecutive partials, of `span` slots of 256 rows each, of
 // the same query rows and head.
 struct JoinJob {
-  int32_t q_row, rows, head, first, count, vis0, span, pad;
+  int32_t q_row, rows, head, first, count, vis0, span;
+  uint32_t check;
 };
+static_assert(sizeof(JoinJob) == 32, "a join job is two int4");
+__host__ __device__ inline uint32_t check_of(const JoinJob& j, uint64_t stamp) {
+  const uint32_t h = mix(mix(mix(static_cast<uint32_t>(stamp), j.q_row), j.rows), j.head);
+  return mix(mix(mix(mix(h, j.first), j.count), j.vis0), j.span);
+}
 
 struct ExpandParams {
   CUtensorMap map_w;           // {512, 256, heads}, boxes {64, 128, 1}
@@ -94,7 +132,8 @@ struct AttnParams {
   CUtensorMap map_kx;          // {256, kx_rows, heads}, boxes {64, 64, 1}
   CUtensorMap map_kr;          // {64, kx_rows, 1}, boxes {64, 64, 1}
   const AttnItem* items;
-  const int32_t* cta_indptr;
+  const uint32_t* item_checks;
+  const CtaItems* ctas;        // [CTAs] or [pairs]
   const uint8_t* v_half;       // [heads][kx_rows / 32]
   int64_t kx_rows;
   int32_t heads;

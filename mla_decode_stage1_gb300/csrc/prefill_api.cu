@@ -22,11 +22,12 @@ struct mla_prefill {
   int64_t q_tokens = 0, k_tokens = 0, kx_rows = 0, identity_rows = 0;
   std::vector<mla::ExpandTile> tiles;
   // items of CTAs on their own, then of CTA pairs, each list by CTA or pair
-  std::vector<int32_t> cta_indptr, pair_indptr;
+  std::vector<mla::CtaItems> cta_items, pair_items;
   std::vector<mla::AttnItem> items;
+  std::vector<uint32_t> item_checks;
   std::vector<mla::JoinJob> jobs;
-  size_t off_tiles = 0, off_indptr = 0, off_pairs = 0, off_items = 0, off_jobs = 0, off_kx = 0, off_kr = 0, off_vh = 0, off_qr = 0,
-         off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
+  size_t off_tiles = 0, off_ctas = 0, off_pairs = 0, off_items = 0, off_checks = 0,
+         off_jobs = 0, off_kx = 0, off_kr = 0, off_vh = 0, off_qr = 0, off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
   std::vector<uint8_t> table;
   uint64_t stamp = 0;
   // per-run caches: the workspace holding the table, the tensor maps and what they describe
@@ -41,6 +42,7 @@ struct mla_prefill {
 namespace {
 
 using mla::AttnItem;
+using mla::CtaItems;
 using mla::ExpandTile;
 using mla::JoinJob;
 
@@ -122,7 +124,7 @@ std::vector<int64_t> costs_of(const std::vector<AttnItem>& items) {
 // A list of items assigned to CTAs (or pairs).
 struct Schedule {
   std::vector<AttnItem> items;      // by CTA
-  std::vector<int32_t> indptr{0};
+  std::vector<CtaItems> of_cta;
   std::vector<JoinJob> jobs;
   int32_t ctas = 0, partials = 0;
   int64_t most = 0;                 // the largest sum of costs
@@ -170,7 +172,7 @@ Schedule schedule(const std::vector<AttnItem>& whole, int32_t ctas, int32_t slot
       const int32_t span = (items[i].rows + mla::kPfRows - 1) / mla::kPfRows;
       const int32_t each = mla::halved(items[i]) ? 2 : 1;
       S.jobs.push_back(JoinJob{items[i].q_row, items[i].rows, items[i].head, slot0 + S.partials,
-                               static_cast<int32_t>(e - i) * each, items[i].vis0, span, 0});
+                               static_cast<int32_t>(e - i) * each, items[i].vis0, span, 0u});
       for (size_t j = i; j < e; ++j) {
         items[j].slot = slot0 + S.partials;
         S.partials += span * each;
@@ -182,8 +184,9 @@ Schedule schedule(const std::vector<AttnItem>& whole, int32_t ctas, int32_t slot
   std::vector<std::vector<int32_t>> of(S.ctas);
   S.most = assign(items, costs_of(items), S.ctas, &of) + (S.jobs.empty() ? 0 : kJoinCost);
   for (const std::vector<int32_t>& l : of) {
+    const int32_t begin = static_cast<int32_t>(S.items.size());
     for (const int32_t i : l) S.items.push_back(items[i]);
-    S.indptr.push_back(static_cast<int32_t>(S.items.size()));
+    S.of_cta.push_back(CtaItems{begin, static_cast<int32_t>(S.items.size()), 0u, 0});
   }
   return S;
 }
@@ -230,7 +233,7 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
     const int64_t kv_row = P->kx_rows;
     for (int64_t t = 0; t < n; t += mla::kPfTile) {
       P->tiles.push_back(ExpandTile{kvp[b], static_cast<int32_t>(t), static_cast<int32_t>(n),
-                                    static_cast<int32_t>(P->kx_rows)});
+                                    static_cast<int32_t>(P->kx_rows), 0u, {}});
       P->kx_rows += mla::kPfTile;
       if (P->kx_rows > INT32_MAX - mla::kPfTile) return MLA_ERR_INVALID_ARG;
     }
@@ -256,9 +259,12 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   P->num_partials = single.partials + pair.partials;
   P->items = single.items;
   P->items.insert(P->items.end(), pair.items.begin(), pair.items.end());
-  P->cta_indptr = single.indptr;
-  P->pair_indptr = pair.indptr;
-  for (int32_t& i : P->pair_indptr) i += static_cast<int32_t>(single.items.size());
+  P->cta_items = single.of_cta;
+  P->pair_items = pair.of_cta;
+  for (CtaItems& c : P->pair_items) {
+    c.begin += static_cast<int32_t>(single.items.size());
+    c.end += static_cast<int32_t>(single.items.size());
+  }
   P->jobs = pair.jobs;
   P->jobs.insert(P->jobs.end(), single.jobs.begin(), single.jobs.end());
 
@@ -269,9 +275,10 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
     return at;
   };
   P->off_tiles = take(sizeof(ExpandTile) * P->tiles.size());
-  P->off_indptr = take(sizeof(int32_t) * P->cta_indptr.size());
-  P->off_pairs = take(sizeof(int32_t) * P->pair_indptr.size());
+  P->off_ctas = take(sizeof(CtaItems) * P->cta_items.size());
+  P->off_pairs = take(sizeof(CtaItems) * P->pair_items.size());
   P->off_items = take(sizeof(AttnItem) * P->items.size());
+  P->off_checks = take(sizeof(uint32_t) * P->items.size());
   P->off_jobs = take(sizeof(JoinJob) * P->jobs.size());
   P->table.assign(off, 0);
   P->off_kx = take(sizeof(uint16_t) * P->kx_rows * P->heads * mla::kWRows);
@@ -287,12 +294,18 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
   auto put = [&](size_t at, const void* src, size_t bytes) {
     if (bytes > 0) std::memcpy(P->table.data() + at, src, bytes);
   };
+  auto put_records = [&](size_t at, auto& records) {
+    for (auto& r : records) r.check = mla::check_of(r, P->stamp);
+    put(at, records.data(), sizeof(records[0]) * records.size());
+  };
+  for (const AttnItem& w : P->items) P->item_checks.push_back(mla::check_of(w, P->stamp));
   put(0, &hdr, sizeof(hdr));
-  put(P->off_tiles, P->tiles.data(), sizeof(ExpandTile) * P->tiles.size());
-  put(P->off_indptr, P->cta_indptr.data(), sizeof(int32_t) * P->cta_indptr.size());
-  put(P->off_pairs, P->pair_indptr.data(), sizeof(int32_t) * P->pair_indptr.size());
+  put_records(P->off_tiles, P->tiles);
+  put_records(P->off_ctas, P->cta_items);
+  put_records(P->off_pairs, P->pair_items);
   put(P->off_items, P->items.data(), sizeof(AttnItem) * P->items.size());
-  put(P->off_jobs, P->jobs.data(), sizeof(JoinJob) * P->jobs.size());
+  put(P->off_checks, P->item_checks.data(), sizeof(uint32_t) * P->item_checks.size());
+  put_records(P->off_jobs, P->jobs);
   return MLA_OK;
 }
 
@@ -488,6 +501,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.map_kx = plan->map_kx;
     p.map_kr = plan->map_kr;
     p.items = reinterpret_cast<const AttnItem*>(ws + plan->off_items);
+    p.item_checks = reinterpret_cast<const uint32_t*>(ws + plan->off_checks);
     p.v_half = v_half;
     p.kx_rows = plan->kx_rows;
     p.heads = plan->heads;
@@ -499,11 +513,11 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     p.err = err;
     p.stamp = plan->stamp;
     if (plan->num_pairs > 0) {
-      p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_pairs);
+      p.ctas = reinterpret_cast<const CtaItems*>(ws + plan->off_pairs);
       if (mla::launch_attn_pairs(p, plan->num_pairs, stream) != cudaSuccess) return MLA_ERR_CUDA;
     }
     if (plan->num_ctas > 0) {
-      p.cta_indptr = reinterpret_cast<const int32_t*>(ws + plan->off_indptr);
+      p.ctas = reinterpret_cast<const CtaItems*>(ws + plan->off_ctas);
       p.after_attn = plan->num_pairs > 0 ? 1 : 0;
       if (mla::launch_attn(p, plan->num_ctas, stream) != cudaSuccess) return MLA_ERR_CUDA;
     }

@@ -948,3 +948,35 @@ def test_prefill_on_pairs_and_single_ctas_repeats(mla):
     for c, o in zip(cases, repeats(mla, cases, 200, num_sms=4)):
         ref, _, bound, _ = plain_prefill(c)
         assert ((o - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,num_sms", [
+    ([130, 9, 300], [900, 6000, 400], 40), ([1300, 400, 900], [2300, 4400, 900], 4)])
+def test_prefill_notices_an_overwritten_work_table(mla, q_lens, kv_lens, num_sms):
+    # 256 bytes of the workspace at a time, the header with the plan's stamp left
+    # as it was: what the records say is not followed, and the next run is right
+    c = prefill_case(q_lens, kv_lens, 2, "bf16", 8, "interleaved", 55)
+    plan, space, (run,) = prefill_calls(mla, [c], num_sms)
+    out = torch.empty(c["qo"][-1], 2, 128, dtype=torch.bfloat16, device="cuda")
+    run(out)
+    mla.mla_prefill_check(plan, space)
+    clean = out.clone()
+    info = plan.info()
+    # tiles, CTAs, items (32 bytes each at least) are in there, each from 256 bytes on
+    records = sum(-(-n // 128) for n in kv_lens) + info.num_items
+    noticed = 0
+    for block in range(1, records * 32 // 256 + 8):
+        for value in (-1, 5):
+            space.view(torch.int32)[64 * block: 64 * block + 64] = value
+            out.fill_(7.0)
+            run(out)
+            try:
+                mla.mla_prefill_check(plan, space)
+                assert torch.equal(out, clean)        # behind the table: nothing is kept there
+            except mla.MlaError as e:
+                assert e.status == 3
+                noticed += 1
+            run(out)
+            mla.mla_prefill_check(plan, space)
+            assert torch.equal(out, clean)
+    assert noticed >= 2 * (records * 32 // 256)
