@@ -24,10 +24,11 @@
 //
 // Roundings: e4m3 and e2m1 values with their block exponents are exact in
 // bf16; the per-tensor scale goes into the fp32 epilogue.  Keys are rounded to
-// bf16 once, as operands of the attention's products, values to fp16 where the
-// 32 rows of a warp have their largest magnitude in [2^-6, 2^15] (three bits
+// bf16 once, as operands of the attention's products, values to fp16 where each of
+// the 32 rows of a warp has its largest magnitude in [2^-6, 2^15] (three bits
 // more, far from fp16's ends: an error below 2^-25 is 2^-19 of that magnitude),
-// else to bf16; a flag per 32 rows and head says which.
+// else to bf16; a flag per 32 rows and head says which.  (Each row, as a query may
+// see only the shortest of them; rows past the request's end do not count.)
 //
 // A value row that is not finite would reach every query through 0 x NaN in
 // the attention's product, also those that must not see the token.  Such a
@@ -335,7 +336,9 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* box
   for (int u = u0; u < u1; ++u, ++k) {
     const uint32_t buf = k & 1;
     const int pair = u / p.heads, h = u - pair * p.heads;
-    const int out_row = tile_of(p, pair, rank).out_row;      // -1: no tile here
+    const ExpandTile tile = tile_of(p, pair, rank);
+    const int out_row = tile.out_row;                        // -1: no tile here
+    const bool past = tile.tok0 + warp * 32 + lane >= tile.len;
     const bool ok = mbar_wait(smem_u32(&ms->acc_full[buf]), (k >> 1) & 1, p.err, kErrDrain);
     if (!__all_sync(0xffffffffu, ok)) break;
     tc_fence_after();
@@ -372,7 +375,7 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* box
       }
     };
     // values first: whether they are finite decides what the key becomes, and
-    // how large they are which type the warp's 32 rows take
+    // how large each row's are which type the warp's 32 rows take
     uint32_t v0[32], v1[32];
     load(as_half, kNope, v0);
     load(as_half, kNope + 64, v1);
@@ -384,10 +387,11 @@ __device__ void run_epilogue(const ExpandParams& p, ExpandMisc* ms, uint8_t* box
     }
     // (bits of magnitudes have their order, infinity and NaN above all)
     uint32_t top = *reinterpret_cast<const uint32_t*>(&top2);
-    top = __reduce_max_sync(0xffffffffu, max(top & 0x7fffu, (top >> 16) & 0x7fffu));
+    top = max(top & 0x7fffu, (top >> 16) & 0x7fffu);
     bool finite = true;
-    const bool half = top >= 0x2400u && top <= 0x7800u;      // 2^-6, 2^15
-    if (!half) {                             // not the common size (or no row): once more, to bf16
+    const uint32_t off = past ? 0u : top - 0x2400u;          // above 2^-6; below it wraps around
+    const bool half = __reduce_max_sync(0xffffffffu, off) <= 0x7800u - 0x2400u;   // 2^15
+    if (!half) {                             // not the common size: once more, to bf16
       load(as_bf16, kNope, v0);
       load(as_bf16, kNope + 64, v1);
       __nv_bfloat162 most = __floats2bfloat162_rn(0.0f, 0.0f);

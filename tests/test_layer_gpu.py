@@ -980,3 +980,20 @@ def test_prefill_notices_an_overwritten_work_table(mla, q_lens, kv_lens, num_sms
             mla.mla_prefill_check(plan, space)
             assert torch.equal(out, clean)
     assert noticed >= 2 * (records * 32 // 256)
+
+
+@pytest.mark.parametrize("f", [2.0**-9, 2.0**-16, 2.0**-22, 2.0**-40])
+@pytest.mark.parametrize("n", [40, 300, 700])
+def test_prefill_a_short_value_among_long_ones(mla, n, f):
+    # tokens 0 and 1 are far shorter than the 30 beside them, with which they
+    # share a type: query rows 0 and 1 see nothing else
+    c = prefill_case([n], [n], 2, "bf16", 8, "interleaved", 22)
+    at = request_rows(c, 0)
+    c["w"].kv[at[:2], :512] *= f
+    c["rows"] = c["w"].kv.double()
+    o, lse, _ = run_prefill(mla, c)
+    ref, ref_lse, bound, lse_bound = plain_prefill(c)
+    assert ((o - ref).abs() <= bound).all() and ((lse - ref_lse).abs() <= lse_bound).all()
+    # roundings of values, weights and output as independent errors, as elsewhere
+    for t in (0, 1):
+        assert (o[t] - ref[t]).norm() <= 1e-2 * ref[t].norm()
