@@ -363,7 +363,7 @@ extern "C" mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_
   if (q_dtype != MLA_DTYPE_BF16 && q_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
   if (q_dtype == MLA_DTYPE_FP8_E4M3 && q_scale == nullptr) return MLA_ERR_INVALID_ARG;
   const mla::Rotation rot{cos_sin, positions, max_positions, rope == MLA_ROPE_HALF ? 1 : 0};
-  if (!mla::rotation_ok(rot, rope) || !ptr_aligned(positions, 4) || !ptr_aligned(q_scale, 4) ||
+  if (!mla::rotation_ok(rot, rope, num_tokens) || !ptr_aligned(positions, 4) || !ptr_aligned(q_scale, 4) ||
       !ptr_aligned(err, 4))
     return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;

@@ -522,7 +522,7 @@ extern "C" mla_status mla_cache_write(const void* latent, int64_t latent_stride,
       !mla::ptr_aligned(err, 4))
     return MLA_ERR_INVALID_ARG;
   mla::Rotation rot{cos_sin, positions, max_positions, rope == MLA_ROPE_HALF ? 1 : 0};
-  if (!mla::rotation_ok(rot, rope) || !mla::ptr_aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
+  if (!mla::rotation_ok(rot, rope, num_tokens) || !mla::ptr_aligned(positions, 4)) return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (latent == nullptr || k_rope == nullptr || slots == nullptr) return MLA_ERR_INVALID_ARG;
   if (latent_stride < mla::kVDim || k_rope_stride < mla::kRope) return MLA_ERR_INVALID_ARG;

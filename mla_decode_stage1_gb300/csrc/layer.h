@@ -1,6 +1,7 @@
-// layer.h -- internal declarations shared by the operators around the decode
-// call (cache.cu, absorb.cu, prefill.cu): their geometry, the bits of their
-// device error word and the rotation of the 64 position dims.
+// layer.h -- internal declarations shared by the operators around the
+// decode call (cache.cu, absorb.cu, prefill_api.cu and its kernels): their
+// geometry, the bits of their device error word and the rotation of the 64
+// position dims.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,10 +43,12 @@ struct Rotation {
   int32_t half;                // 0: pairs (2i, 2i+1); 1: pairs (i, i + 32)
 };
 
-// Checks shared by the calls that rotate: both pointers or neither.
-inline bool rotation_ok(const Rotation& r, int rope) {
-  if ((r.cos_sin == nullptr) != (r.positions == nullptr)) return false;
+// Checks shared by the calls that rotate: both pointers or neither (the
+// positions of no token may be anywhere: an empty array often has no address).
+inline bool rotation_ok(const Rotation& r, int rope, int64_t tokens) {
   if (rope != MLA_ROPE_INTERLEAVED && rope != MLA_ROPE_HALF) return false;
+  if (tokens == 0) return true;
+  if ((r.cos_sin == nullptr) != (r.positions == nullptr)) return false;
   return r.cos_sin == nullptr || (r.max_positions >= 1 && ptr_aligned(r.cos_sin, 16));
 }
 

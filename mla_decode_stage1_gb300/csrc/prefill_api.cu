@@ -406,7 +406,7 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
     if (kv_e8m0_row_stride % 2 != 0 || !ptr_aligned(kv_e8m0, 2)) return MLA_ERR_UNSUPPORTED;
   }
   const mla::Rotation rot{cos_sin, positions, max_positions, rope == MLA_ROPE_HALF ? 1 : 0};
-  if (!mla::rotation_ok(rot, rope)) return MLA_ERR_INVALID_ARG;
+  if (!mla::rotation_ok(rot, rope, plan->q_tokens)) return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < plan->ws_bytes) return MLA_ERR_WORKSPACE;
   if (kv_indices == nullptr ? plan->identity_rows > kv_pool_rows
                             : kv_pool_rows % plan->page_size != 0)

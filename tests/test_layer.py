@@ -210,3 +210,12 @@ def test_bindings_refuse_host_tensors_and_types(mla):
         mla.mla_absorb_q(b, w, b, sm_scale=1.0)
     with pytest.raises(ValueError):
         mla.mla_absorb_out(b, w, b)
+
+
+def test_no_tokens_with_a_rotation(mla, mem):
+    # an empty tensor of positions has no address
+    none = dict(tokens=0, cs=mem, npos=8, pos=None)
+    assert mla._lib.mla_cache_write(*write_args(mem, slots=None, latent=None, rope=None, **none)) == 0
+    assert mla._lib.mla_absorb_q(*q_args(mem, q=None, out=None, **none)) == 0
+    assert mla._lib.mla_absorb_q(*q_args(mem, **dict(none, style=2))) == 1
+    assert mla._lib.mla_absorb_q(*q_args(mem, **dict(none, tokens=1))) == 1

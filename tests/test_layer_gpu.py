@@ -997,3 +997,30 @@ def test_prefill_a_short_value_among_long_ones(mla, n, f):
     # roundings of values, weights and output as independent errors, as elsewhere
     for t in (0, 1):
         assert (o[t] - ref[t]).norm() <= 1e-2 * ref[t].norm()
+
+
+def test_a_step_without_new_tokens(mla):
+    # every call of a step in which no request gets a token, rotation and all
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    rope = dict(positions=none, cos_sin=rotation_table(8).cuda())
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    err, w = word(), make_w(16, gen(1)).cuda()
+    o = dict(kv_indptr=i32([-9] * 3), kv_last_page_len=i32([-9] * 2), kv_indices=i32([-9] * 3),
+             qo_indptr=i32([-9] * 3), slots=torch.empty(0, dtype=torch.int64, device="cuda"),
+             positions=none)
+    mla.mla_cache_step(i32([3, 5]), i32([0, 0]), i32([[1, 0], [0, 2]]), i32([3]), page_size=4,
+                       err=err, **o)
+    assert o["kv_indptr"].tolist() == [0, 1, 3] and o["qo_indptr"].tolist() == [0, 0, 0]
+    assert o["kv_indices"].tolist() == [1, 0, 2] and o["kv_last_page_len"].tolist() == [3, 1]
+    pool, _ = new_pool("bf16", 16)
+    mla.mla_cache_write(torch.empty(0, 512, **bf16), torch.empty(0, 64, **bf16), pool, o["slots"],
+                        kv_dtype="bf16", err=err, **rope)
+    assert (pool == 7).all()
+    q = torch.empty(0, 16, 192, **bf16)
+    mla.mla_absorb_q(q, w, torch.empty(0, 16, 576, **bf16), sm_scale=SCALE, err=err, **rope)
+    mla.mla_absorb_out(torch.empty(0, 16, 512, **bf16), w, torch.empty(0, 16, 128, **bf16))
+    attend = mla.MlaPrefill([0, 0, 0], [0, 1, 3], [3, 1], page_size=4, kv_dtype="bf16")
+    attend(q, pool, w, torch.empty(0, 16, 128, **bf16), sm_scale=SCALE,
+           kv_indices=o["kv_indices"], **rope)
+    mla.mla_prefill_check(attend.plan, attend.workspace)
+    mla.mla_error_check(err)
