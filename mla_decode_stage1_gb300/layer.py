@@ -166,19 +166,24 @@ def mla_cache_step(old_lens, new_lens, block_table, free_pages, *, page_size: in
     i32 = torch.int32
     bs = old_lens.shape[0]
     # one pass over the common case; what is wrong is worked out only if it fails
+    # (arrays of a given length may have any shape, the others are lists)
     if not (old_lens.dtype is i32 and old_lens.is_cuda and old_lens.is_contiguous()
+            and old_lens.dim() == 1
             and (new_lens is None or (new_lens.dtype is i32 and new_lens.is_cuda
                                       and new_lens.is_contiguous() and new_lens.numel() == bs))
             and block_table.dtype is i32 and block_table.is_cuda and block_table.dim() == 2
             and free_pages.dtype is i32 and free_pages.is_cuda and free_pages.is_contiguous()
+            and free_pages.dim() == 1
             and kv_indptr.dtype is i32 and kv_indptr.is_cuda and kv_indptr.is_contiguous()
             and kv_indptr.numel() == bs + 1
             and kv_last_page_len.dtype is i32 and kv_last_page_len.is_cuda
             and kv_last_page_len.is_contiguous() and kv_last_page_len.numel() == bs
             and kv_indices.dtype is i32 and kv_indices.is_cuda and kv_indices.is_contiguous()
+            and kv_indices.dim() == 1
             and qo_indptr.dtype is i32 and qo_indptr.is_cuda and qo_indptr.is_contiguous()
             and qo_indptr.numel() == bs + 1
             and slots.dtype is torch.int64 and slots.is_cuda and slots.is_contiguous()
+            and slots.dim() == 1
             and positions.dtype is i32 and positions.is_cuda and positions.is_contiguous()
             and positions.numel() == slots.numel()
             and (pages_used is None or (pages_used.dtype is i32 and pages_used.is_cuda

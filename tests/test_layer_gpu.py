@@ -1024,3 +1024,23 @@ def test_a_step_without_new_tokens(mla):
            kv_indices=o["kv_indices"], **rope)
     mla.mla_prefill_check(attend.plan, attend.workspace)
     mla.mla_error_check(err)
+
+
+def test_cache_step_refuses_arrays_that_are_not_lists(mla):
+    # a [requests, k] tensor of lengths must not pass for its first entries
+    def call(**kw):
+        a = dict(old=i32([3, 5]), new=i32([1, 1]), table=i32([[1, 0], [0, 2]]), free=i32([3, 4]),
+                 idx=i32([0] * 4), slots=torch.zeros(2, dtype=torch.int64, device="cuda"),
+                 pos=i32([0] * 2))
+        a.update(kw)
+        mla.mla_cache_step(a["old"], a["new"], a["table"], a["free"], page_size=4,
+                           kv_indptr=i32([0] * 3), kv_last_page_len=i32([0] * 2),
+                           kv_indices=a["idx"], qo_indptr=i32([0] * 3), slots=a["slots"],
+                           positions=a["pos"])
+
+    call()
+    for bad in (dict(old=i32([[3, 5], [7, 9]])), dict(old=i32([[3], [5]])),
+                dict(free=i32([[3, 4]])), dict(idx=i32([[0, 0], [0, 0]])),
+                dict(slots=torch.zeros(2, 1, dtype=torch.int64, device="cuda"))):
+        with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+            call(**bad)
