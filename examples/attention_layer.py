@@ -125,7 +125,7 @@ def tokens(layer, cache, hidden):
     decode(q_lat, cache.pool, o, kv_indices=s["kv_indices"], **cache.format())
     mla.mla_decode_check(decode.plan, decode.workspace)
     out = torch.empty(bs, HEADS, 128, dtype=torch.bfloat16, device="cuda")
-    mla.mla_absorb_out(o, layer.up, out)
+    mla.mla_absorb_out(o, layer.up, out, err=cache.err)
     return out
 
 

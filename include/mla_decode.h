@@ -502,7 +502,9 @@ mla_status mla_cache_write(const void* latent, int64_t latent_stride, const void
  *   q_dtype  MLA_DTYPE_BF16 or MLA_DTYPE_FP8_E4M3 (the value divided by the
  *            device fp32 q_scale, saturating).
  *   q_out    [num_tokens][heads][576] contiguous, 32-byte aligned.
- * mla_decode_run takes heads = 16.  Sums are held in fp32.
+ * mla_decode_run takes heads = 16.  Sums are held in fp32.  Where a bounded
+ * wait on the device gives up, the tile's latent dims become NaN, also without
+ * an error word.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (q_dtype), MLA_ERR_CUDA.
  */
 mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -516,10 +518,29 @@ mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_st
  *     out[t,h,:] = w[h][128:256] o[t,h,:].
  *   o    bf16 [num_tokens][heads][512] contiguous, 16-byte aligned.
  *   out  bf16 [num_tokens][heads][128] contiguous, 32-byte aligned.
+ * mla_absorb_out_ex takes an error word as the other calls do; mla_absorb_out
+ * is that call without one.  Where a bounded wait on the device gives up, the
+ * tile's output becomes NaN, also without an error word.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
  */
 mla_status mla_absorb_out(const void* o, const void* w, int64_t num_tokens, int32_t heads,
                           void* out, mla_stream_t stream);
+mla_status mla_absorb_out_ex(const void* o, const void* w, int64_t num_tokens, int32_t heads,
+                             void* out, int32_t* err, mla_stream_t stream);
+
+/*
+ * mla_selftest_absorb_wait -- exercises the timeout path of the absorbed
+ * products on the GPU: mla_absorb_out_ex (to_out != 0) or mla_absorb_q (x dense,
+ * sm_scale 1, no rotation, e4m3 if q_scale is given) of these operands, in which
+ * the wait for operands runs out after limit_us microseconds (1 .. 20000).  The
+ * products come out as NaN, err (if given) gets the producer's bit, so that the
+ * next mla_error_check returns MLA_ERR_DEVICE_TIMEOUT, and the CUDA context stays
+ * usable.
+ * Errors: those of the two calls.
+ */
+mla_status mla_selftest_absorb_wait(const void* x, const void* w, int64_t num_tokens,
+                                    int32_t heads, const float* q_scale, void* y, int32_t to_out,
+                                    uint32_t limit_us, int32_t* err, mla_stream_t stream);
 
 /*
  * mla_prefill_plan -- plan of an expanded-form call over a ragged batch.

@@ -27,7 +27,8 @@ EXPORTS = ("mla_decode_plan", "mla_decode_plan_q", "mla_decode_plan_ex", "mla_pl
            "mla_decode_run_noalloc", "mla_selftest_bounded_wait", "mla_decode_autotune",
            "mla_autotune_select", "mla_cache_step", "mla_cache_write", "mla_absorb_q",
            "mla_absorb_out", "mla_prefill_plan", "mla_prefill_get_info", "mla_prefill_destroy",
-           "mla_prefill_run", "mla_prefill_check", "mla_error_check")
+           "mla_prefill_run", "mla_prefill_check", "mla_error_check", "mla_absorb_out_ex",
+           "mla_selftest_absorb_wait")
 
 
 class MlaError(RuntimeError):
@@ -339,7 +340,7 @@ class MlaDecoder:
 # are loaded when first asked for.
 LAYER = ("MlaPrefill", "PrefillInfo", "PrefillPlan", "mla_absorb_out", "mla_absorb_q",
          "mla_cache_step", "mla_cache_write", "mla_error_check", "mla_prefill_check",
-         "mla_prefill_plan", "mla_prefill_run")
+         "mla_prefill_plan", "mla_prefill_run", "mla_selftest_absorb_wait")
 
 
 def __getattr__(name):

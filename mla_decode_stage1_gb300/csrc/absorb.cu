@@ -12,6 +12,10 @@
 // the last token are computed from whatever the shared memory holds and never
 // written), the epilogue scales, rounds once and writes whole sectors.
 //
+// A wait that gives up is noted in the caller's error word, if there is one, and
+// in any case the tile's products are written as NaN: what the output held
+// before must not pass for a result.
+//
 // Measured (16 heads, kernel alone, warm L2): absorb_q 3.5 us for 4 tokens to
 // bf16 and 6.1 us for 256 to fp8; absorb_out 3.8 us for 61 tokens and 5.8 us
 // for 1024 (2.1 GFLOP, 23 MB: 4.0 TB/s).  Their bytes take 0.3, 0.9, 0.5 and
@@ -32,8 +36,12 @@ constexpr int kTokens = 128;                       // tokens of a CTA
 constexpr uint32_t kPanel = kTokens * 128;         // a row panel: 128 tokens x 64 bf16
 constexpr int kAbsorbThreads = 128;
 
-// Where a wait that gave up is noted when the caller has no error word.
-__device__ int32_t g_unreported;
+// The wait for operands: on their barrier, or (the self-test) on one that
+// nothing arrives on, with a limit of its own.
+struct OperandWait {
+  uint64_t limit_ns = kWaitLimitNs;
+  bool stalled = false;
+};
 
 struct AbsorbQParams {
   CUtensorMap map_q;           // {192, heads, tokens}, boxes {64, 1, box_rows}
@@ -48,6 +56,7 @@ struct AbsorbQParams {
   const float* q_scale;        // null: bf16 out
   void* out;
   int32_t* err;
+  OperandWait wait;
 };
 
 struct AbsorbOutParams {
@@ -57,6 +66,8 @@ struct AbsorbOutParams {
   int32_t heads;
   int32_t box_rows;
   uint16_t* out;
+  int32_t* err;
+  OperandWait wait;
 };
 
 __device__ __forceinline__ float bf16f(uint16_t v) {
@@ -94,19 +105,21 @@ __global__ void __launch_bounds__(kAbsorbThreads)
     absorb_q_kernel(const __grid_constant__ AbsorbQParams p) {
   constexpr int kSlices = kVDim / N;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full, done;
-  __shared__ uint32_t tmem_base;
+  __shared__ uint64_t full, done, never;
+  __shared__ uint32_t tmem_base, gave_up;
+  __shared__ int32_t unreported;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t a_smem = smem_u32(smem), b_smem = a_smem + 2 * kPanel;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int slice = blockIdx.x % kSlices, h = blockIdx.y;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / kSlices) * kTokens;
-  int32_t* err = p.err != nullptr ? p.err : &g_unreported;
+  int32_t* err = p.err != nullptr ? p.err : &unreported;
   if (warp == 0) {
     if (elect_one()) {
       mbar_init(smem_u32(&full), 1);
-      mbar_init(smem_u32(&done), 1);
+      mbar_init(smem_u32(&never), 1);
+      mbar_init(smem_u32(&done), 2);            // the products' commit, and `gave_up` is set
       fence_mbar_init();
       mbar_arrive_expect_tx(smem_u32(&full), 2 * p.box_rows * 128 + N / 64 * kPanel);
       const uint64_t keep = l2_policy_evict_normal();
@@ -152,9 +165,10 @@ __global__ void __launch_bounds__(kAbsorbThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(tmem_base);
-  bool ok = true;
   if (warp == 0) {
-    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full), 0, err, kErrProducer));
+    const bool ok = __all_sync(
+        0xffffffffu, mbar_wait_for(smem_u32(p.wait.stalled ? &never : &full), 0, err, kErrProducer,
+                                   p.wait.limit_ns));
     tc_fence_after();
     if (elect_one()) {
       if (ok) {
@@ -166,17 +180,28 @@ __global__ void __launch_bounds__(kAbsorbThreads)
           umma_f16(tmem, a + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), b + ((kk * 2048) >> 4),
                    idesc, kk != 0);
       }
+      gave_up = ok ? 0 : 1;
+      mbar_arrive(smem_u32(&done));
       tc_commit(smem_u32(&done));
     }
     __syncwarp();
+    // no copy may land after the CTA has gone
+    if (!ok) mbar_wait(smem_u32(&full), 0, err, kErrProducer);
   }
-  ok = mbar_wait(smem_u32(&done), 0, err, kErrDrain) && ok;
-  ok = __all_sync(0xffffffffu, ok);
+  bool ok = mbar_wait(smem_u32(&done), 0, err, kErrDrain);
+  ok = __all_sync(0xffffffffu, ok) && gave_up == 0;
   tc_fence_after();
   const int64_t t = t0 + warp * 32 + lane;
-  if (ok) {
+  const int64_t at = (t * p.heads + h) * kQkDim + slice * N;
+  if (!ok) {
+    const uint32_t nan = p.q_scale == nullptr ? 0x7fff7fffu : 0x7f7f7f7fu;
+    const uint32_t u[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+    const int size = p.q_scale == nullptr ? 2 : 1;
+    if (t < p.tokens)
+      for (int i = 0; i < N * size; i += 32)
+        st_global_32(static_cast<uint8_t*>(p.out) + at * size + i, u);
+  } else {
     const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
-    const int64_t at = (t * p.heads + h) * kQkDim + slice * N;
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) {
       uint32_t x[32], u[16];
@@ -215,14 +240,16 @@ __global__ void __launch_bounds__(kAbsorbThreads)
   constexpr uint32_t kStage = kPanel + N * 128;
   constexpr uint32_t kCols = N < 32 ? 32 : N;        // tensor memory comes in 32 columns
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[S], empty[S], done;
-  __shared__ uint32_t tmem_base;
+  __shared__ uint64_t full[S], empty[S], done, never;
+  __shared__ uint32_t tmem_base, gave_up;
+  __shared__ int32_t unreported;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_u32(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int slice = blockIdx.x % kSlices, h = blockIdx.y;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / kSlices) * kTokens;
+  int32_t* err = p.err != nullptr ? p.err : &unreported;
   const uint64_t keep = l2_policy_evict_normal();
   auto load = [&](int step) {
     const int s = step % S;
@@ -237,7 +264,8 @@ __global__ void __launch_bounds__(kAbsorbThreads)
         mbar_init(smem_u32(&full[s]), 1);
         mbar_init(smem_u32(&empty[s]), 1);
       }
-      mbar_init(smem_u32(&done), 1);
+      mbar_init(smem_u32(&never), 1);
+      mbar_init(smem_u32(&done), 2);            // the products' commit, and `gave_up` is set
       fence_mbar_init();
       for (int s = 0; s < S; ++s) load(s);
     }
@@ -249,44 +277,60 @@ __global__ void __launch_bounds__(kAbsorbThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(tmem_base);
-  bool ok = true;
   if (warp == 0) {
+    bool ok = true;
+    int seen = 0, issued = S;           // copies waited for, and under way
     constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, N);
     const uint64_t a0 = smem_desc(base, 16, 1024, kSwizzle128B);
 #pragma unroll
     for (int step = 0; step < kSteps; ++step) {
+      if (!ok) break;
       const int s = step % S;
-      // (every copy is waited for, also when an earlier wait gave up)
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[s]), (step / S) & 1, &g_unreported,
-                                             kErrProducer)) && ok;
+      ok = __all_sync(0xffffffffu, mbar_wait_for(smem_u32(p.wait.stalled ? &never : &full[s]),
+                                                 p.wait.stalled ? 0 : (step / S) & 1, err,
+                                                 kErrProducer, p.wait.limit_ns));
+      if (!ok) break;
+      ++seen;
       tc_fence_after();
       const uint64_t a = a0 + ((s * kStage) >> 4), b = a + (kPanel >> 4);
       if (elect_one()) {
-        if (ok) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16(tmem, a + 2 * kk, b + 2 * kk, idesc, (step | kk) != 0);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16(tmem, a + 2 * kk, b + 2 * kk, idesc, (step | kk) != 0);
         tc_commit(smem_u32(&empty[s]));
       }
       // refill the stage of the step before: its products are behind this one's
       if (step >= 1 && step - 1 + S < kSteps) {
         const int back = step - 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[back % S]), (back / S) & 1,
-                                               &g_unreported, kErrMma)) && ok;
-        if (elect_one()) load(back + S);
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[back % S]), (back / S) & 1, err,
+                                               kErrMma));
+        if (ok) {
+          ++issued;
+          if (elect_one()) load(back + S);
+        }
       }
     }
-    if (elect_one()) tc_commit(smem_u32(&done));
+    // a wait gave up: no copy may land after the CTA has gone
+    for (int k = seen; !ok && k < issued; ++k)
+      mbar_wait(smem_u32(&full[k % S]), (k / S) & 1, err, kErrProducer);
+    if (elect_one()) {
+      gave_up = ok ? 0 : 1;
+      mbar_arrive(smem_u32(&done));
+      tc_commit(smem_u32(&done));
+    }
     __syncwarp();
   }
-  ok = mbar_wait(smem_u32(&done), 0, &g_unreported, kErrDrain) && ok;
-  ok = __all_sync(0xffffffffu, ok);
+  bool ok = mbar_wait(smem_u32(&done), 0, err, kErrDrain);
+  ok = __all_sync(0xffffffffu, ok) && gave_up == 0;
   tc_fence_after();
   const int64_t t = t0 + warp * 32 + lane;
-  if (ok) {
+  uint16_t* out = p.out + (t * p.heads + h) * kVHead + slice * N;
+  if (!ok) {
+    const uint32_t nan = 0x7fff7fffu, u[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+    if (t < p.tokens)
+      for (int c = 0; c < N / 16; ++c) st_global_32(out + 16 * c, u);
+  } else {
     const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
-    uint16_t* out = p.out + (t * p.heads + h) * kVHead + slice * N;
 #pragma unroll
     for (int c = 0; c < N / 16; ++c) {
       float x[16];
@@ -347,38 +391,31 @@ cudaError_t launch_out(AbsorbOutParams& p, const void* w, int64_t tiles, cudaStr
   return cudaGetLastError();
 }
 
-}  // namespace
-}  // namespace mla
-
-extern "C" mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_stride,
-                                   const void* w, int64_t num_tokens, int32_t heads,
-                                   float sm_scale, const float* cos_sin, int64_t max_positions,
-                                   const int32_t* positions, mla_rope rope, mla_dtype q_dtype,
-                                   const float* q_scale, void* q_out, int32_t* err,
-                                   mla_stream_t stream) {
-  using mla::ptr_aligned;
+// Arguments as for mla_absorb_q and mla_absorb_out_ex.
+mla_status absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* w,
+                    int64_t num_tokens, int32_t heads, float sm_scale, const Rotation& rot,
+                    int rope, mla_dtype q_dtype, const float* q_scale, void* q_out, int32_t* err,
+                    const OperandWait& wait, cudaStream_t stream) {
   if (num_tokens < 0 || num_tokens > INT32_MAX || heads < 1 || heads > 1024 ||
       !(sm_scale > 0.0f) || !(sm_scale < 1e30f))
     return MLA_ERR_INVALID_ARG;
   if (q_dtype != MLA_DTYPE_BF16 && q_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
   if (q_dtype == MLA_DTYPE_FP8_E4M3 && q_scale == nullptr) return MLA_ERR_INVALID_ARG;
-  const mla::Rotation rot{cos_sin, positions, max_positions, rope == MLA_ROPE_HALF ? 1 : 0};
-  if (!mla::rotation_ok(rot, rope, num_tokens) || !ptr_aligned(positions, 4) || !ptr_aligned(q_scale, 4) ||
-      !ptr_aligned(err, 4))
+  if (!rotation_ok(rot, rope, num_tokens) || !ptr_aligned(rot.positions, 4) ||
+      !ptr_aligned(q_scale, 4) || !ptr_aligned(err, 4))
     return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (q == nullptr || w == nullptr || q_out == nullptr) return MLA_ERR_INVALID_ARG;
   if (!ptr_aligned(q, 16) || !ptr_aligned(w, 16) || !ptr_aligned(q_out, 32) ||
       q_token_stride >= (1LL << 39) || q_head_stride >= (1LL << 39) ||
-      q_token_stride < mla::kQHead || q_head_stride < mla::kQHead || q_token_stride % 8 != 0 ||
+      q_token_stride < kQHead || q_head_stride < kQHead || q_token_stride % 8 != 0 ||
       q_head_stride % 8 != 0)
     return MLA_ERR_INVALID_ARG;
-  mla::AbsorbQParams p{};
-  p.box_rows = mla::box_rows_for(num_tokens);
-  if (!mla::make_map(&p.map_q, q, mla::kQHead, heads, num_tokens, q_head_stride, q_token_stride, 1,
-                     p.box_rows) ||
-      !mla::make_map(&p.map_w, w, mla::kVDim, mla::kWRows, heads, mla::kVDim,
-                     mla::kVDim * mla::kWRows, mla::kNope, 1))
+  AbsorbQParams p{};
+  p.box_rows = box_rows_for(num_tokens);
+  if (!make_map(&p.map_q, q, kQHead, heads, num_tokens, q_head_stride, q_token_stride, 1,
+                p.box_rows) ||
+      !make_map(&p.map_w, w, kVDim, kWRows, heads, kVDim, kVDim * kWRows, kNope, 1))
     return MLA_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(q);
   p.token_stride = q_token_stride;
@@ -390,37 +427,81 @@ extern "C" mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_
   p.q_scale = q_dtype == MLA_DTYPE_FP8_E4M3 ? q_scale : nullptr;
   p.out = q_out;
   p.err = err;
-  const int64_t tiles = (num_tokens + mla::kTokens - 1) / mla::kTokens;
+  p.wait = wait;
+  const int64_t tiles = (num_tokens + kTokens - 1) / kTokens;
   // eight slices of 64 dims until the (head, token tile)s alone fill the SMs
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      tiles * heads < 76 ? mla::launch_q<64>(p, tiles, s) : mla::launch_q<128>(p, tiles, s);
+      tiles * heads < 76 ? launch_q<64>(p, tiles, stream) : launch_q<128>(p, tiles, stream);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-extern "C" mla_status mla_absorb_out(const void* o, const void* w, int64_t num_tokens,
-                                     int32_t heads, void* out, mla_stream_t stream) {
-  using mla::ptr_aligned;
-  if (num_tokens < 0 || num_tokens > INT32_MAX || heads < 1 || heads > 1024)
+mla_status absorb_out(const void* o, const void* w, int64_t num_tokens, int32_t heads, void* out,
+                      int32_t* err, const OperandWait& wait, cudaStream_t stream) {
+  if (num_tokens < 0 || num_tokens > INT32_MAX || heads < 1 || heads > 1024 ||
+      !ptr_aligned(err, 4))
     return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (o == nullptr || w == nullptr || out == nullptr || !ptr_aligned(o, 16) ||
       !ptr_aligned(w, 16) || !ptr_aligned(out, 32))
     return MLA_ERR_INVALID_ARG;
-  mla::AbsorbOutParams p{};
-  p.box_rows = mla::box_rows_for(num_tokens);
-  if (!mla::make_map(&p.map_o, o, mla::kVDim, heads, num_tokens, mla::kVDim,
-                     static_cast<int64_t>(heads) * mla::kVDim, 1, p.box_rows))
+  AbsorbOutParams p{};
+  p.box_rows = box_rows_for(num_tokens);
+  if (!make_map(&p.map_o, o, kVDim, heads, num_tokens, kVDim,
+                static_cast<int64_t>(heads) * kVDim, 1, p.box_rows))
     return MLA_ERR_CUDA;
   p.tokens = num_tokens;
   p.heads = heads;
   p.out = static_cast<uint16_t*>(out);
-  const int64_t tiles = (num_tokens + mla::kTokens - 1) / mla::kTokens, units = tiles * heads;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.err = err;
+  p.wait = wait;
+  const int64_t tiles = (num_tokens + kTokens - 1) / kTokens, units = tiles * heads;
   // narrower slices of the 128 output dims while there are few (head, token tile)s
-  const cudaError_t e = units < 24    ? mla::launch_out<16, 8>(p, w, tiles, s)
-                        : units < 48  ? mla::launch_out<32, 8>(p, w, tiles, s)
-                        : units < 96  ? mla::launch_out<64, 4>(p, w, tiles, s)
-                                      : mla::launch_out<128, 3>(p, w, tiles, s);
+  const cudaError_t e = units < 24    ? launch_out<16, 8>(p, w, tiles, stream)
+                        : units < 48  ? launch_out<32, 8>(p, w, tiles, stream)
+                        : units < 96  ? launch_out<64, 4>(p, w, tiles, stream)
+                                      : launch_out<128, 3>(p, w, tiles, stream);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
+
+}  // namespace
+}  // namespace mla
+
+extern "C" {
+
+mla_status mla_absorb_q(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const void* w, int64_t num_tokens, int32_t heads, float sm_scale,
+                        const float* cos_sin, int64_t max_positions, const int32_t* positions,
+                        mla_rope rope, mla_dtype q_dtype, const float* q_scale, void* q_out,
+                        int32_t* err, mla_stream_t stream) {
+  const mla::Rotation rot{cos_sin, positions, max_positions, rope == MLA_ROPE_HALF ? 1 : 0};
+  return mla::absorb_q(q, q_token_stride, q_head_stride, w, num_tokens, heads, sm_scale, rot, rope,
+                       q_dtype, q_scale, q_out, err, {}, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mla_status mla_absorb_out(const void* o, const void* w, int64_t num_tokens, int32_t heads,
+                          void* out, mla_stream_t stream) {
+  return mla_absorb_out_ex(o, w, num_tokens, heads, out, nullptr, stream);
+}
+
+mla_status mla_absorb_out_ex(const void* o, const void* w, int64_t num_tokens, int32_t heads,
+                             void* out, int32_t* err, mla_stream_t stream) {
+  return mla::absorb_out(o, w, num_tokens, heads, out, err, {},
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+mla_status mla_selftest_absorb_wait(const void* x, const void* w, int64_t num_tokens,
+                                    int32_t heads, const float* q_scale, void* y, int32_t to_out,
+                                    uint32_t limit_us, int32_t* err, mla_stream_t stream) {
+  if (limit_us == 0 || limit_us > 20000) return MLA_ERR_INVALID_ARG;
+  mla::OperandWait wait;
+  wait.limit_ns = static_cast<uint64_t>(limit_us) * 1000u;
+  wait.stalled = true;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (to_out != 0) return mla::absorb_out(x, w, num_tokens, heads, y, err, wait, st);
+  return mla::absorb_q(x, static_cast<int64_t>(heads) * mla::kQHead, mla::kQHead, w, num_tokens,
+                       heads, 1.0f, mla::Rotation{}, MLA_ROPE_HALF,
+                       q_scale != nullptr ? MLA_DTYPE_FP8_E4M3 : MLA_DTYPE_BF16, q_scale, y, err,
+                       wait, st);
+}
+
+}  // extern "C"

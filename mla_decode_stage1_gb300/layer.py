@@ -35,6 +35,8 @@ def _declare(lib):
                             P, P],
         "mla_absorb_q": [P, i64, i64, P, i64, i32, f32, P, i64, P, e, e, P, P, P, P],
         "mla_absorb_out": [P, P, i64, i32, P, P],
+        "mla_absorb_out_ex": [P, P, i64, i32, P, P, P],
+        "mla_selftest_absorb_wait": [P, P, i64, i32, P, P, i32, ctypes.c_uint32, P, P],
         "mla_prefill_plan": [P, P, P, i32, i32, i32, e, i32, ctypes.POINTER(P)],
         "mla_prefill_get_info": [P, ctypes.POINTER(PrefillInfo)],
         "mla_prefill_destroy": [P],
@@ -51,7 +53,7 @@ def _declare(lib):
 
 _declare(_lib)
 _cache_step, _cache_write, _absorb_q, _absorb_out, _prefill_run = (
-    _lib.mla_cache_step, _lib.mla_cache_write, _lib.mla_absorb_q, _lib.mla_absorb_out,
+    _lib.mla_cache_step, _lib.mla_cache_write, _lib.mla_absorb_q, _lib.mla_absorb_out_ex,
     _lib.mla_prefill_run)
 
 # The handle of a device's current stream.  torch.cuda.current_stream builds a
@@ -277,17 +279,35 @@ def mla_absorb_q(q, w, q_out, *, sm_scale: float, positions=None, cos_sin=None,
         _check("mla_absorb_q", status)
 
 
-def mla_absorb_out(o, w, out, *, stream=None) -> None:
+def mla_absorb_out(o, w, out, *, err=None, stream=None) -> None:
     """The layer's attention output bf16 [T, heads, 128] from the decode
     output o bf16 [T, heads, 512]."""
     heads = _weights(w)
     T = o.shape[0]
     _dense("o", o, torch.bfloat16, (T, heads, LATENT))
     _dense("out", out, torch.bfloat16, (T, heads, V_HEAD))
-    status = _absorb_out(o.data_ptr(), w.data_ptr(), T, heads, out.data_ptr(),
-                                 _stream(stream, o))
+    _word("err", err, torch.int32)
+    status = _absorb_out(o.data_ptr(), w.data_ptr(), T, heads, out.data_ptr(), _ptr(err),
+                         _stream(stream, o))
     if status:
         _check("mla_absorb_out", status)
+
+
+def mla_selftest_absorb_wait(x, w, y, *, q_scale=None, limit_us: int = 2000, err=None,
+                             stream=None) -> None:
+    """mla_absorb_out (y [T, heads, 128]) or mla_absorb_q (y [T, heads, 576]) in
+    which the waits for operands run out after limit_us: y's products become
+    NaN, and mla_error_check of err raises MlaError with status 5."""
+    heads = _weights(w)
+    T, to_out = x.shape[0], y.shape[-1] == V_HEAD
+    _word("q_scale", q_scale, torch.float32)
+    _word("err", err, torch.int32)
+    _dense("x", x, torch.bfloat16, (T, heads, LATENT if to_out else NOPE + ROPE))
+    _dense("y", y, torch.bfloat16 if q_scale is None else torch.uint8,
+           (T, heads, V_HEAD if to_out else ROW))
+    _check("mla_selftest_absorb_wait", _lib.mla_selftest_absorb_wait(
+        x.data_ptr(), w.data_ptr(), T, heads, _ptr(q_scale), y.data_ptr(), int(to_out),
+        int(limit_us), _ptr(err), _stream(stream, x)))
 
 
 class PrefillPlan:

@@ -219,3 +219,18 @@ def test_no_tokens_with_a_rotation(mla, mem):
     assert mla._lib.mla_absorb_q(*q_args(mem, q=None, out=None, **none)) == 0
     assert mla._lib.mla_absorb_q(*q_args(mem, **dict(none, style=2))) == 1
     assert mla._lib.mla_absorb_q(*q_args(mem, **dict(none, tokens=1))) == 1
+
+
+def test_absorb_out_ex_refuses(mla, mem):
+    f = mla._lib.mla_absorb_out_ex
+    assert f(mem, mem, 1, 16, None, mem, None) == 1
+    assert f(mem, mem, 0, 16, mem, mem + 2, None) == 1
+    assert f(mem, mem, 0, 16, mem, mem, None) == 0
+    g = mla._lib.mla_selftest_absorb_wait
+    assert g(mem, mem, 0, 16, None, mem, 0, 0, mem, None) == 1
+    assert g(mem, mem, 0, 16, None, mem, 1, 20001, mem, None) == 1
+    assert g(mem, mem, 1, 16, None, None, 1, 100, mem, None) == 1
+    import torch
+    b = torch.zeros(1, 16, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mla.mla_absorb_out(b, torch.zeros(16, 256, 512, dtype=torch.bfloat16), b, err=b)

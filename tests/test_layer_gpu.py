@@ -1044,3 +1044,43 @@ def test_cache_step_refuses_arrays_that_are_not_lists(mla):
                 dict(slots=torch.zeros(2, 1, dtype=torch.int64, device="cuda"))):
         with pytest.raises(ValueError, match="contiguous CUDA tensor"):
             call(**bad)
+
+
+@pytest.mark.parametrize("report", [True, False])
+@pytest.mark.parametrize("tokens,heads", [(5, 16), (130, 16), (300, 40)])
+def test_absorbed_products_whose_wait_gives_up(mla, tokens, heads, report):
+    # the waits for operands run out: nothing of the output before them is left,
+    # the error word says so, and the next call is right
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    w = make_w(heads, gen(tokens)).cuda()
+    q = torch.randn(tokens, heads, 192, generator=g, device="cuda").bfloat16()
+    o = torch.randn(tokens, heads, 512, generator=g, device="cuda").bfloat16()
+    err = word() if report else None
+    scale = torch.full((1,), 0.02, device="cuda")
+    outs = [torch.full((tokens + 2, heads, n), 7.0, dtype=torch.bfloat16, device="cuda")
+            for n in (576, 128)]
+    qa, out = (x[1:-1] for x in outs)
+    q8 = torch.full((tokens, heads, 576), 0x11, dtype=torch.uint8, device="cuda")
+    for x, y, s in ((q, qa, None), (q, q8, scale), (o, out, None)):
+        mla.mla_selftest_absorb_wait(x, w, y, q_scale=s, err=err)
+        if report:
+            with pytest.raises(mla.MlaError) as e:
+                mla.mla_error_check(err)
+            assert e.value.status == 5
+            mla.mla_error_check(err)
+    torch.cuda.synchronize()
+    assert torch.isnan(qa[..., :512]).all() and torch.isnan(out).all()
+    assert torch.isnan(q8.view(torch.float8_e4m3fn).float()[..., :512]).all()
+    assert all((x[[0, -1]] == 7).all() for x in outs)
+    # the rotated dims wait for nothing
+    assert torch.equal(qa[..., 512:], (q[..., 128:].float() * 24).bfloat16())
+    mla.mla_absorb_q(q, w, qa, sm_scale=1.0, err=err)
+    mla.mla_absorb_q(q, w, q8, sm_scale=1.0, q_scale=scale, err=err)
+    mla.mla_absorb_out(o, w, out, err=err)
+    if report:
+        mla.mla_error_check(err)
+    assert torch.isfinite(qa).all() and torch.isfinite(q8.view(torch.float8_e4m3fn).float()).all()
+    ref = torch.einsum("thc,hvc->thv", o.double(), w[:, 128:].double())
+    mag = torch.einsum("thc,hvc->thv", o.double().abs(), w[:, 128:].double().abs())
+    acc = 512 * F * mag
+    assert ((out.double() - ref).abs() <= acc + U * (ref.abs() + acc)).all()
