@@ -2,7 +2,7 @@
 write, the absorbed form's two products and the expanded form.
 
 Marshalling only, like the package's other calls.  Shapes, dtypes and devices
-are checked here (ValueError); everything else is checked by the library
+(the current one) are checked here (ValueError); everything else is checked by the library
 (MlaError).  Nothing synchronises but the ``_check`` calls.
 """
 from __future__ import annotations
@@ -65,6 +65,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 def _stream(stream, t):
     """The stream to enqueue on: the caller's, or the current one of t's device."""
     return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+# The library launches on the current device.  Only with several devices can a
+# tensor be on another one; asking each costs 0.5 us a call.
+_several_devices = torch.cuda.device_count() > 1
+_current_device = torch.cuda.current_device
+
+
+def _on_current_device(stream, *tensors):
+    dev = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current CUDA device, {dev}")
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream must be one of the current CUDA device, {dev}")
 
 
 def _need(ok: bool, what: str) -> None:
@@ -165,6 +180,10 @@ def mla_cache_step(old_lens, new_lens, block_table, free_pages, *, page_size: in
     token), positions int32 [capacity], pages_used int32 [1].  What went wrong
     on the device (pages ran out, ...) is in err, read by mla_error_check.
     """
+    if _several_devices:
+        _on_current_device(stream, old_lens, new_lens, block_table, free_pages, kv_indptr,
+                           kv_last_page_len, kv_indices, qo_indptr, slots, positions, pages_used,
+                           err)
     i32 = torch.int32
     bs = old_lens.shape[0]
     # one pass over the common case; what is wrong is worked out only if it fails
@@ -229,6 +248,9 @@ def mla_cache_write(latent, k_rope, kv, slots, *, kv_dtype: str, norm_weight=Non
     stored), kv the pool as mla_decode_run takes it, rows (optional) bf16
     [T,576]: the values that the stored encoding stands for.
     """
+    if _several_devices:
+        _on_current_device(stream, latent, k_rope, kv, slots, norm_weight, positions, cos_sin,
+                           kv_scale, kv_e8m0, rows, err)
     T = slots.numel()
     bf16 = torch.bfloat16
     ls, rs = latent.stride(), k_rope.stride()
@@ -265,6 +287,8 @@ def mla_absorb_q(q, w, q_out, *, sm_scale: float, positions=None, cos_sin=None,
     """The decode call's query from a layer's query q bf16 [T, heads, 192]:
     q_out [T, heads, 576], bf16, or uint8 (e4m3 bytes of the value divided by
     q_scale).  The decode call's scores then carry sm_scale."""
+    if _several_devices:
+        _on_current_device(stream, q, w, q_out, positions, cos_sin, q_scale, err)
     heads = _weights(w)
     T, st, sh = _query(q, heads)
     fp8 = q_scale is not None
@@ -282,6 +306,8 @@ def mla_absorb_q(q, w, q_out, *, sm_scale: float, positions=None, cos_sin=None,
 def mla_absorb_out(o, w, out, *, err=None, stream=None) -> None:
     """The layer's attention output bf16 [T, heads, 128] from the decode
     output o bf16 [T, heads, 512]."""
+    if _several_devices:
+        _on_current_device(stream, o, w, out, err)
     heads = _weights(w)
     T = o.shape[0]
     _dense("o", o, torch.bfloat16, (T, heads, LATENT))
@@ -298,6 +324,8 @@ def mla_selftest_absorb_wait(x, w, y, *, q_scale=None, limit_us: int = 2000, err
     """mla_absorb_out (y [T, heads, 128]) or mla_absorb_q (y [T, heads, 576]) in
     which the waits for operands run out after limit_us: y's products become
     NaN, and mla_error_check of err raises MlaError with status 5."""
+    if _several_devices:
+        _on_current_device(stream, x, w, y, q_scale, err)
     heads = _weights(w)
     T, to_out = x.shape[0], y.shape[-1] == V_HEAD
     _word("q_scale", q_scale, torch.float32)
@@ -359,6 +387,9 @@ def mla_prefill_run(plan: PrefillPlan, q, kv, w, out, *, workspace, sm_scale: fl
     pool as mla_decode_run takes it, w bf16 [heads, 256, 512], out bf16
     [T, heads, 128], lse fp32 [T, heads] or None, workspace a uint8 CUDA tensor
     of at least plan.workspace_bytes."""
+    if _several_devices:
+        _on_current_device(stream, q, kv, w, out, workspace, positions, cos_sin, kv_scale, kv_e8m0,
+                           kv_indices, lse)
     heads = _weights(w)
     _need(heads == plan.heads, f"w must have the plan's {plan.heads} heads")
     T, st, sh = _query(q, heads)
@@ -383,6 +414,8 @@ def mla_prefill_run(plan: PrefillPlan, q, kv, w, out, *, workspace, sm_scale: fl
 
 def mla_prefill_check(plan: PrefillPlan, workspace, stream=None) -> None:
     """mla_decode_check for a prefill plan's workspace."""
+    if _several_devices:
+        _on_current_device(stream, workspace)
     _check("mla_prefill_check", _lib.mla_prefill_check(plan.handle, workspace.data_ptr(),
                                                        _stream(stream, workspace)))
 
@@ -406,5 +439,7 @@ def mla_error_check(err, stream=None) -> None:
     """Synchronise, read and clear a device error word; raise MlaError if it
     was set: status 6 (pages or entries ran out), 1 (a length, page, slot or
     position out of range)."""
+    if _several_devices:
+        _on_current_device(stream, err)
     _word("err", err, torch.int32)
     _check("mla_error_check", _lib.mla_error_check(err.data_ptr(), _stream(stream, err)))

@@ -234,3 +234,101 @@ def test_absorb_out_ex_refuses(mla, mem):
     b = torch.zeros(1, 16, 512, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         mla.mla_absorb_out(b, torch.zeros(16, 256, 512, dtype=torch.bfloat16), b, err=b)
+
+
+class OnDevice:
+    """A host tensor that says that it is on CUDA device `dev`."""
+
+    is_cuda = True
+
+    def __init__(self, t, dev):
+        self.t, self.dev = t, dev
+
+    def get_device(self):
+        return self.dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def calls_of_the_layer(mla):
+    """name -> (call, its tensors), all of them with right shapes."""
+    import torch
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)          # noqa: E731
+    i64 = lambda *s: torch.zeros(*s, dtype=torch.int64)          # noqa: E731
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)        # noqa: E731
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)           # noqa: E731
+    f32 = lambda *s: torch.zeros(*s)                             # noqa: E731
+    rope = dict(positions=i32(2), cos_sin=f32(4, 64))
+    p = plan(mla, [0, 2], [0, 2], heads=2, kd="fp8")
+    return dict(
+        mla_cache_step=(lambda **a: mla.mla_cache_step(
+            a.pop("old"), a.pop("new"), a.pop("table"), a.pop("free"), page_size=1, **a), dict(
+            old=i32(2), new=i32(2), table=i32(2, 3), free=i32(4), kv_indptr=i32(3),
+            kv_last_page_len=i32(2), kv_indices=i32(4), qo_indptr=i32(3), slots=i64(4),
+            positions=i32(4), pages_used=i32(1), err=i32(1))),
+        mla_cache_write=(lambda **a: mla.mla_cache_write(
+            a.pop("latent"), a.pop("k_rope"), a.pop("kv"), a.pop("slots"), kv_dtype="fp8", **a),
+            dict(latent=bf(2, 512), k_rope=bf(2, 64), kv=u8(4, 576), slots=i64(2), err=i32(1),
+                 norm_weight=bf(512), kv_scale=f32(1), rows=bf(2, 576), **rope)),
+        mla_cache_write_mxfp4=(lambda **a: mla.mla_cache_write(
+            a.pop("latent"), a.pop("k_rope"), a.pop("kv"), a.pop("slots"), kv_dtype="mxfp4", **a),
+            dict(latent=bf(2, 512), k_rope=bf(2, 64), kv=u8(4, 288), slots=i64(2),
+                 kv_e8m0=u8(4, 18))),
+        mla_absorb_q=(lambda **a: mla.mla_absorb_q(
+            a.pop("q"), a.pop("w"), a.pop("q_out"), sm_scale=1.0, **a),
+            dict(q=bf(2, 2, 192), w=bf(2, 256, 512), q_out=u8(2, 2, 576), q_scale=f32(1),
+                 err=i32(1), **rope)),
+        mla_absorb_out=(lambda **a: mla.mla_absorb_out(a.pop("o"), a.pop("w"), a.pop("out"), **a),
+                        dict(o=bf(2, 2, 512), w=bf(2, 256, 512), out=bf(2, 2, 128), err=i32(1))),
+        mla_prefill_run=(lambda **a: mla.mla_prefill_run(
+            p, a.pop("q"), a.pop("kv"), a.pop("w"), a.pop("out"), sm_scale=1.0, **a),
+            dict(q=bf(2, 2, 192), kv=u8(2, 576), w=bf(2, 256, 512), out=bf(2, 2, 128),
+                 workspace=u8(256), kv_scale=f32(1), kv_indices=i32(2), lse=f32(2, 2), **rope)),
+        mla_prefill_check=(lambda workspace: mla.mla_prefill_check(p, workspace),
+                           dict(workspace=u8(256))),
+        mla_error_check=(mla.mla_error_check, dict(err=i32(1))))
+
+
+@pytest.mark.parametrize("name", ["mla_cache_step", "mla_cache_write", "mla_cache_write_mxfp4",
+                                  "mla_absorb_q", "mla_absorb_out", "mla_prefill_run",
+                                  "mla_prefill_check", "mla_error_check"])
+def test_tensors_of_another_device_are_refused(mla, monkeypatch, name):
+    # the library launches on the current device: every tensor has to be there
+    from mla_decode_stage1_gb300 import layer
+    call, tensors = calls_of_the_layer(mla)[name]
+    launched = []
+
+    def library(*args):
+        launched.append(args)
+        return 0
+
+    for f in ("_cache_step", "_cache_write", "_absorb_q", "_absorb_out", "_prefill_run"):
+        monkeypatch.setattr(layer, f, library)
+    monkeypatch.setattr(layer, "_lib", type("Library", (), dict(
+        mla_prefill_check=staticmethod(library), mla_error_check=staticmethod(library),
+        mla_prefill_destroy=staticmethod(library))))
+    monkeypatch.setattr(layer, "_raw_stream", lambda dev: 0)
+    current = [0]
+    monkeypatch.setattr(layer, "_current_device", lambda: current[0], raising=False)
+    monkeypatch.setattr(layer, "_several_devices", True, raising=False)
+    def on(dev, other=None):
+        return {k: OnDevice(t, 1 if k == other else dev) for k, t in tensors.items()}
+
+    call(**on(0))
+    assert len(launched) == 1
+    for other in tensors:
+        with pytest.raises(ValueError):
+            call(**on(0, other))
+    with pytest.raises(ValueError):
+        call(**on(1))
+    with pytest.raises(ValueError):
+        call(**tensors)                        # on the host
+    if "check" not in name:
+        with pytest.raises(ValueError):
+            call(**on(0), stream=type("Stream", (), dict(
+                device=type("Device", (), dict(index=1)), cuda_stream=0)))
+    assert len(launched) == 1
+    current[0] = 1
+    call(**on(1))
+    assert len(launched) == 2
