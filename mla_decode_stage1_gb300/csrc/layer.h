@@ -87,14 +87,15 @@ __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
 // A per-tensor scale.  x / sc as plain division rounds it, in three operations
 // where the division instruction's sequence takes about 80 cycles: q0 = x r
 // with r = 1 / sc rounded, then q0 + (x - q0 sc) r, which is the rounded
-// quotient while nothing over- or underflows (Markstein 1990).
+// quotient while nothing over- or underflows (Markstein 1990).  The negative of
+// it is computed and the codes' signs turned: x = -0 keeps its sign that way.
 struct Fp8Scale {
   float sc, r;
-  bool normal;                // 2^-60 < |sc| < 2^60
+  bool normal;                // 2^-60 < sc < 2^60
 };
 __device__ __forceinline__ Fp8Scale load_fp8_scale(const float* p) {
   const float sc = *p;
-  return Fp8Scale{sc, __fdiv_rn(1.0f, sc), fabsf(sc) > 0x1p-60f && fabsf(sc) < 0x1p60f};
+  return Fp8Scale{sc, __fdiv_rn(1.0f, sc), sc > 0x1p-60f && sc < 0x1p60f};
 }
 // N values divided by the scale to e4m3, four a word.  Values that are not
 // finite, or whose quotient is not, go through the division instruction.
@@ -104,13 +105,15 @@ __device__ __forceinline__ void to_e4m3(const float* y, const Fp8Scale& s, uint3
 #pragma unroll
   for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
   uint16_t c[N / 2];
-  if (s.normal && __uint_as_float(top) < 1e30f && __uint_as_float(top) * fabsf(s.r) < 1e30f) {
-    const uint64_t r2 = pack_f32x2(s.r, s.r), n2 = pack_f32x2(-s.sc, -s.sc);
+  const bool fast =
+      s.normal && __uint_as_float(top) < 1e30f && __uint_as_float(top) * s.r < 1e30f;
+  if (fast) {
+    const uint64_t n2 = pack_f32x2(-s.r, -s.r), s2 = pack_f32x2(s.sc, s.sc);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const uint64_t x = pack_f32x2(y[i], y[i + 1]), q0 = mul_f32x2(x, r2);
+      const uint64_t x = pack_f32x2(y[i], y[i + 1]), q0 = mul_f32x2(x, n2);
       float a, b;
-      unpack_f32x2(fma_f32x2(fma_f32x2(q0, n2, x), r2, q0), a, b);
+      unpack_f32x2(fma_f32x2(fma_f32x2(q0, s2, x), n2, q0), a, b);
       c[i / 2] = to_e4m3x2(a, b);
     }
   } else {
@@ -120,7 +123,8 @@ __device__ __forceinline__ void to_e4m3(const float* y, const Fp8Scale& s, uint3
   }
 #pragma unroll
   for (int i = 0; i < (N + 3) / 4; ++i)
-    out[i] = c[2 * i] | (N > 2 ? static_cast<uint32_t>(c[2 * i + 1]) << 16 : 0u);
+    out[i] = (c[2 * i] | (N > 2 ? static_cast<uint32_t>(c[2 * i + 1]) << 16 : 0u)) ^
+             (fast ? 0x80808080u : 0u);
 }
 // Two e4m3 codes as half precision (exact).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {

@@ -1084,3 +1084,29 @@ def test_absorbed_products_whose_wait_gives_up(mla, tokens, heads, report):
     mag = torch.einsum("thc,hvc->thv", o.double().abs(), w[:, 128:].double().abs())
     acc = 512 * F * mag
     assert ((out.double() - ref).abs() <= acc + U * (ref.abs() + acc)).all()
+
+
+@pytest.mark.parametrize("scale", [0.013, 1.0, 2.0**-59, 2.0**-61, 2.0**61, 3e-30, -0.5])
+@pytest.mark.parametrize("norm", [True, False])
+def test_cache_write_zeros_and_scales_of_any_size(mla, scale, norm):
+    # bytes of the plain 32-bit quotient: signed zeros, and scales on both sides
+    # of the range in which it is had without a division
+    g = gen(61)
+    latent = torch.randn(40, 512, generator=g).bfloat16()
+    k_rope = torch.randn(40, 64, generator=g).bfloat16()
+    for x in (latent, k_rope):
+        x[:, 0::7] = 0.0
+        x[:, 3::7] = -0.0
+        x[5] = -0.0
+        x[6, 1::2] *= 2.0**-30
+    weight = (1 + 0.2 * torch.randn(512, generator=g)).bfloat16() if norm else None
+    sc = torch.tensor([scale])
+    pool, _ = new_pool("fp8", 40)
+    out = torch.empty(40, 576, dtype=torch.bfloat16, device="cuda")
+    mla.mla_cache_write(latent.cuda(), k_rope.cuda(), pool, torch.arange(40, device="cuda"),
+                        kv_dtype="fp8", eps=1e-5, norm_weight=None if weight is None
+                        else weight.cuda(), kv_scale=sc.cuda(), rows=out)
+    y = plain_row(latent, k_rope, weight, 1e-5, None, None, None)
+    q = (y / sc).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert torch.equal(pool.cpu(), q.view(torch.uint8))
+    assert torch.equal(out.cpu().view(torch.int16), (q.float() * sc).bfloat16().view(torch.int16))
