@@ -555,7 +555,7 @@ mla_status mla_selftest_absorb_wait(const void* x, const void* w, int64_t num_to
  *   kv_dtype        MLA_DTYPE_BF16, MLA_DTYPE_FP8_E4M3 or MLA_DTYPE_MXFP4.
  *   num_sms         CTAs to plan for; 0 = the SM count of the current device.
  * The plan follows mla_plan's rules: library-owned, one host thread at a time,
- * one workspace per plan.
+ * one workspace per plan.  At most 2^25 - 1 blocks of 256 query rows and a head.
  * Errors: MLA_ERR_INVALID_ARG (also out of host memory), MLA_ERR_CUDA.
  */
 typedef struct mla_prefill mla_prefill;

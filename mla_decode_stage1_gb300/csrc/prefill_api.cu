@@ -58,6 +58,8 @@ constexpr int64_t kLaunchCost = 40;   // a second attention kernel, once
 constexpr int64_t kPairRows = 384;    // a pair's item needs more query rows than this: half of
                                       // its second tile must be there to be worth two CTAs
 
+constexpr int64_t kMaxItems = INT32_MAX / 64;   // whole items of a plan
+
 int64_t item_tiles(const AttnItem& w) {
   return (static_cast<int64_t>(w.kv_end) - w.kv_begin + mla::kPfTile - 1) / mla::kPfTile;
 }
@@ -230,6 +232,10 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
           std::max(P->identity_rows, static_cast<int64_t>(kvp[b]) * P->page_size + n);
     P->k_tokens += n;
     if (m == 0) continue;
+    // (before the lists are built: 2^31 rows of 1024 heads would be 8.6 G items)
+    const int64_t blocks = (m + mla::kPfRows - 1) / mla::kPfRows;
+    if (static_cast<int64_t>(all.size()) + blocks * P->heads > kMaxItems)
+      return MLA_ERR_INVALID_ARG;
     const int64_t kv_row = P->kx_rows;
     for (int64_t t = 0; t < n; t += mla::kPfTile) {
       P->tiles.push_back(ExpandTile{kvp[b], static_cast<int32_t>(t), static_cast<int32_t>(n),
@@ -239,7 +245,6 @@ mla_status make_plan(mla_prefill* P, const int32_t* qo, const int32_t* kvp, cons
     }
     add_items(nullptr, &all, INT64_MAX, qo[b], m, n, kv_row, P->heads);
     add_items(&pairs, &rest, kPairRows, qo[b], m, n, kv_row, P->heads);
-    if (all.size() > static_cast<size_t>(INT32_MAX / 64)) return MLA_ERR_INVALID_ARG;
   }
   if (static_cast<int64_t>(P->tiles.size()) * P->heads > INT32_MAX) return MLA_ERR_INVALID_ARG;
   P->q_tokens = qo[P->bs];

@@ -332,3 +332,15 @@ def test_tensors_of_another_device_are_refused(mla, monkeypatch, name):
     current[0] = 1
     call(**on(1))
     assert len(launched) == 2
+
+
+@pytest.mark.parametrize("qo,heads", [([0, 2 ** 31 - 1], 1024), ([0, 2 ** 30, 2 ** 31 - 1], 8),
+                                      ([0, 8 * 2 ** 20, 16 * 2 ** 20], 1024)])
+def test_prefill_plan_refuses_more_blocks_than_it_can_list(mla, qo, heads):
+    import resource
+    before = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+    with pytest.raises(mla.MlaError) as e:
+        plan(mla, qo, [0] * len(qo), heads=heads)
+    assert e.value.status == 1
+    # the first 2^25 items at most (1 GB a list) have been built
+    assert resource.getrusage(resource.RUSAGE_SELF).ru_maxrss - before < 5 * 2 ** 20
