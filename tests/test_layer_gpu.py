@@ -1110,3 +1110,157 @@ def test_cache_write_zeros_and_scales_of_any_size(mla, scale, norm):
     q = (y / sc).clamp(-448, 448).to(torch.float8_e4m3fn)
     assert torch.equal(pool.cpu(), q.view(torch.uint8))
     assert torch.equal(out.cpu().view(torch.int16), (q.float() * sc).bfloat16().view(torch.int16))
+
+
+# ------------------------------------- rows one by one, more heads, whole chains
+def row_errors(c):
+    """For every row (token, head): out and lse in 64 bits and the standard
+    deviation of their errors if every rounding is an error of its own, uniform
+    over its step: u / sqrt 3 for key, query, value, probability and output."""
+    q, w = c["q"].double(), c["weights"].double()
+    if c["rope"]:
+        q = torch.cat([q[..., :128], rotate(q[..., 128:], c["table"], c["pos"], c["rope"])], -1)
+    r = U / math.sqrt(3)
+    outs, lses, sd_o, sd_l = [], [], [], []
+    for b, (m, n) in enumerate(zip(c["q_lens"], c["kv_lens"])):
+        x = c["rows"][request_rows(c, b)]
+        qb = q[c["qo"][b]: c["qo"][b + 1]]
+        kv = torch.einsum("nc,hdc->hnd", x[:, :512], w)
+        k = torch.cat([kv[..., :128], x[:, 512:].expand(c["heads"], -1, -1)], -1)
+        s = torch.einsum("mhd,hnd->hmn", qb, k) * SCALE
+        see = torch.arange(n)[None] < (n - m + 1 + torch.arange(m))[:, None]
+        p = torch.softmax(s.masked_fill(~see, -math.inf), -1)
+        v = kv[..., 128:]
+        o = p @ v
+        # score: either factor of each product; (v - o): what a weight moves
+        var_s = 2 * r * r * SCALE ** 2 * torch.einsum("mhd,hnd->hmn", qb.square(), k.square())
+        far = v.square().sum(-1)[:, None] - 2 * o @ v.transpose(1, 2) + o.square().sum(-1)[..., None]
+        sd_o.append((torch.einsum("hmn,hmn->hm", p.square() * var_s, far)
+                     + 2 * r * r * torch.einsum("hmn,hn->hm", p.square(), v.square().sum(-1))
+                     + r * r * o.square().sum(-1)).sqrt().T)
+        sd_l.append((p.square() * var_s).sum(-1).sqrt().T)
+        outs.append(o.transpose(0, 1))
+        lses.append(torch.logsumexp(s.masked_fill(~see, -math.inf), -1).T)
+    return torch.cat(outs), torch.cat(lses), torch.cat(sd_o), torch.cat(sd_l)
+
+
+def check_rows(mla, c, num_sms=0):
+    o, lse, _ = run_prefill(mla, c, num_sms)
+    ref, ref_lse, sd_o, sd_l = row_errors(c)
+    # six standard deviations; sums, exponents and logarithms in fp32: 64 F each
+    off = (o - ref).norm(dim=-1) / (6 * sd_o + 64 * F * ref.norm(dim=-1))
+    assert off.max() <= 1, (off.max(), off.argmax())
+    off = (lse - ref_lse).abs() / (6 * sd_l + 64 * F * (1 + ref_lse.abs()))
+    assert off.max() <= 1, (off.max(), off.argmax())
+    return o
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,num_sms", [
+    ([300, 1, 40], [300, 200, 131], 0), ([70], [900], 0), ([70, 9], [900, 1300], 40),
+    ([600], [700], 0), ([900, 400], [1000, 400], 4)])
+@pytest.mark.parametrize("kv", ["bf16", "mxfp4"])
+def test_prefill_row_by_row(mla, kv, q_lens, kv_lens, num_sms):
+    # a row of its own, not the whole output: one lost key of 1000 would show
+    check_rows(mla, prefill_case(q_lens, kv_lens, 3, kv, 8, "interleaved", 71), num_sms)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads", [([33, 5], [33, 200], 33), ([520, 3], [520, 64], 20),
+                                                  ([17], [150], 128), ([3], [40], 1024)])
+def test_prefill_with_more_heads(mla, q_lens, kv_lens, heads):
+    check_rows(mla, prefill_case(q_lens, kv_lens, heads, "bf16", 8, "half", 72))
+
+
+@pytest.mark.parametrize("tokens,heads", [(1, 17), (5, 128), (130, 64), (2, 1024)])
+def test_absorbed_products_with_more_heads(mla, tokens, heads):
+    g = gen(heads)
+    q = torch.randn(tokens, heads, 192, generator=g).bfloat16()
+    o = torch.randn(tokens, heads, 512, generator=g).bfloat16()
+    w = make_w(heads, g).cuda()
+    qa = torch.full((tokens + 2, heads, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((tokens + 2, heads, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    mla.mla_absorb_q(q.cuda(), w, qa[1:-1], sm_scale=SCALE)
+    mla.mla_absorb_out(o.cuda(), w, out[1:-1])
+    f = 24 * SCALE
+    for got, x, y in ((qa[1:-1, :, :512], q[..., :128].double().cuda() * f, w[:, :128].double()),
+                      (out[1:-1], o.double().cuda(), w[:, 128:].double().transpose(1, 2))):
+        ref = torch.einsum("thk,hkn->thn", x, y)
+        # sums of at most 512 products and the factor; one rounding
+        acc = 516 * F * torch.einsum("thk,hkn->thn", x.abs(), y.abs())
+        assert ((got.double() - ref).abs() <= acc + U * (ref.abs() + acc)).all()
+    f32 = torch.tensor(24.0) * torch.tensor(SCALE)
+    assert torch.equal(qa[1:-1, :, 512:].cpu(), (q[..., 128:].float() * f32).bfloat16())
+    assert (qa[[0, -1]] == 7).all() and (out[[0, -1]] == 7).all()
+
+
+# Roundings of the absorbed chain as independent errors of u / sqrt 3 (query,
+# its low part, probabilities, latent output, output, key): sqrt 6 of them stay
+# near 0.6 %.  An e4m3 query moves a score by 2^-4 / sqrt 3 of its terms, which
+# are 0.87 x 1 / 24 in size and 576: 0.031, and the output by as much of its norm.
+@pytest.mark.parametrize("kv,q_dtype,limit", [("bf16", "bf16", 2e-2), ("fp8", "bf16", 2e-2),
+                                              ("fp8", "fp8", 1e-1), ("mxfp4", "bf16", 2e-2)])
+def test_absorbed_form_request_by_request(mla, kv, q_dtype, limit):
+    kv_lens = [5, 300, 1, 777, 130]
+    c = prefill_case([1] * 5, kv_lens, 16, kv, 8, "interleaved", 73)
+    ref = row_errors(c)[0]
+    w = c["w"].to("cuda")
+    fp8 = q_dtype == "fp8"
+    weights, err = c["weights"].cuda(), word()
+    qa = torch.empty(5, 16, 576, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    qs = torch.full((1,), 0.02, device="cuda") if fp8 else None
+    mla.mla_absorb_q(c["q"].cuda(), weights, qa, sm_scale=SCALE, positions=c["pos"].cuda(),
+                     cos_sin=c["table"].cuda(), q_scale=qs, err=err)
+    decode = mla.MlaDecoder(w.kv_indptr, w.kv_last_page_len, page_size=8, q_dtype=q_dtype,
+                            kv_dtype=kv)
+    lat = torch.empty(5, 16, 512, dtype=torch.bfloat16, device="cuda")
+    decode(qa, w.kv, lat, q_scale=qs, kv_scale=w.kv_scale, kv_e8m0=w.kv_e8m0,
+           kv_indices=w.kv_indices)
+    mla.mla_decode_check(decode.plan, decode.workspace)
+    out = torch.empty(5, 16, 128, dtype=torch.bfloat16, device="cuda")
+    mla.mla_absorb_out(lat, weights, out, err=err)
+    mla.mla_error_check(err)
+    for b in range(5):
+        off = out[b].cpu().double() - ref[b]
+        assert off.norm() <= limit * ref[b].norm(), (b, off.norm() / ref[b].norm())
+
+
+def test_replayed_calls_give_the_eager_bits(mla):
+    # a whole step in one graph: cache write, both forms, on new inputs each replay
+    c = prefill_case([150], [400], 16, "bf16", 8, "interleaved", 74)
+    w = c["w"].to("cuda")
+    weights, pos, table = c["weights"].cuda(), c["pos"].cuda(), c["table"].cuda()
+    attend = mla.MlaPrefill(c["qo"], w.kv_indptr, w.kv_last_page_len, page_size=8,
+                            kv_dtype="bf16")
+    slots = request_rows(c, 0)[250:].cuda()
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    q, latent, k_rope = (torch.zeros(150, *s, **bf16) for s in ((16, 192), (512,), (64,)))
+    lat = torch.zeros(150, 16, 512, **bf16)
+    outs = [torch.zeros(150, 16, n, **bf16) for n in (128, 576, 128)]
+    err = word()
+
+    def step():
+        mla.mla_cache_write(latent, k_rope, w.kv, slots, kv_dtype="bf16", positions=pos,
+                            cos_sin=table, err=err)
+        attend(q, w.kv, weights, outs[0], sm_scale=SCALE, positions=pos, cos_sin=table,
+               kv_indices=w.kv_indices)
+        mla.mla_absorb_q(q, weights, outs[1], sm_scale=SCALE, positions=pos, cos_sin=table, err=err)
+        mla.mla_absorb_out(lat, weights, outs[2], err=err)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (1, 2, 3):
+        r = torch.Generator(device="cuda").manual_seed(seed)
+        for x in (q, latent, k_rope, lat):
+            x.copy_(torch.randn(x.shape, generator=r, device="cuda"))
+        step()
+        eager = [x.clone() for x in outs]
+        for x in outs:
+            x.fill_(7.0)
+        w.kv[slots] = 7.0
+        g.replay()
+        torch.cuda.synchronize()
+        for x, e in zip(outs, eager):
+            assert torch.equal(x, e) and x.float().abs().sum() > 0
+    mla.mla_error_check(err)
+    mla.mla_prefill_check(attend.plan, attend.workspace)
