@@ -464,8 +464,9 @@ mla_status mla_cache_step(const int32_t* old_lens, const int32_t* new_lens, int3
  * dims and the pool's encoding in one pass.
  *
  *   latent        bf16 [num_tokens][512], row stride latent_stride elements (a
- *                 multiple of 8); 16-byte aligned.
- *   k_rope        bf16 [num_tokens][64], row stride k_rope_stride elements.
+ *                 multiple of 8, at least 512); 16-byte aligned.
+ *   k_rope        bf16 [num_tokens][64], row stride k_rope_stride elements (at
+ *                 least 64).
  *   norm_weight   bf16 [512], 16-byte aligned, or NULL: no norm.
  *   slots         int64 [num_tokens]: pool row of each token; -1: not stored.
  *                 Two tokens of a call must not share a slot.
@@ -497,7 +498,7 @@ mla_status mla_cache_write(const void* latent, int64_t latent_stride, const void
  * scores carry sm_scale.
  *
  *   q        bf16 [num_tokens][heads][192] with strides in elements, both
- *            multiples of 8 (and below 2^39); 16-byte aligned.
+ *            multiples of 8, at least 192 and below 2^39; 16-byte aligned.
  *   w        bf16 [heads][256][512] contiguous, 16-byte aligned.
  *   q_dtype  MLA_DTYPE_BF16 or MLA_DTYPE_FP8_E4M3 (the value divided by the
  *            device fp32 q_scale, saturating).
@@ -556,6 +557,11 @@ mla_status mla_selftest_absorb_wait(const void* x, const void* w, int64_t num_to
  *   num_sms         CTAs to plan for; 0 = the SM count of the current device.
  * The plan follows mla_plan's rules: library-owned, one host thread at a time,
  * one workspace per plan.  At most 2^25 - 1 blocks of 256 query rows and a head.
+ * The workspace holds the expanded keys and values of every request that has a
+ * query: (512 heads + 128 + heads / 32) bytes a cached token, its length rounded
+ * up to 128 (8.3 KB at 16 heads, 7 times a bf16 row), 128 heads bytes a query
+ * token and the partial results.  32 requests of 131,072 tokens take 35 GB at 16
+ * heads: plan so large a batch in several calls, one workspace's worth each.
  * Errors: MLA_ERR_INVALID_ARG (also out of host memory), MLA_ERR_CUDA.
  */
 typedef struct mla_prefill mla_prefill;
@@ -580,13 +586,20 @@ void mla_prefill_destroy(mla_prefill* plan);
 
 /*
  * mla_prefill_run -- one expanded-form attention call, enqueued on `stream`:
- * keys and values are expanded from the cached rows into the workspace (keys
- * rounded to bf16, values to fp16 or, where they are too large or small for
- * it, to bf16), then attended to in one pass over the keys; key ranges that
- * the plan split are joined by their log-sum-exp.
+ * keys and values are expanded from the cached rows into the workspace, then
+ * attended to in one pass over the keys; key ranges that the plan split are
+ * joined by their log-sum-exp.
+ *
+ * Sums, maxima, the softmax's statistics, partial outputs and their join are
+ * fp32.  Fewer bits have, as operands of the products: keys and the rotated
+ * query dims (bf16); the cached rotated dims of an e4m3 pool, after kv_scale
+ * (bf16); values (fp16, or bf16 for 32 tokens and a head where a token's largest
+ * value is outside [2^-6, 2^15]); probabilities (the type of the values that
+ * they meet; against fp16 values those below 2^-32 of the row's largest count
+ * as zero).
  *
  *   q          bf16 [query tokens][heads][192] with strides in elements, both
- *              multiples of 8 (and below 2^39); 16-byte aligned.
+ *              multiples of 8, at least 192 and below 2^39; 16-byte aligned.
  *   kv .. kv_pool_rows, kv_indices  the cache, as for mla_decode_run.
  *   w          bf16 [heads][256][512] contiguous, 16-byte aligned.
  *   sm_scale   softmax scale, finite and > 0.

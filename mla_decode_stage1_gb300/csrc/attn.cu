@@ -20,7 +20,7 @@
 // take 2,790: 8192 tokens, 16 heads, causal: 210 us on single CTAs, 196 us in
 // pairs (1.75 PFLOP/s, tensor pipe 79 % busy; what is left is 3 items a CTA
 // filling and draining, 5 % each).  Against many keys and few rows HBM bounds
-// it: 77 rows, 32,845 keys: 56 us for 274 MB (4.9 TB/s).
+// it: 77 rows, 32,845 keys: 57 us for 274 MB (4.8 TB/s).
 //
 // Probabilities are rounded to the type of the values that they meet, fp16 or
 // bf16 by groups of 32 keys (expand.cu); each 16-key product is of that type.

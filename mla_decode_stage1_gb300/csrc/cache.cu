@@ -169,9 +169,10 @@ __global__ void __launch_bounds__(kStepThreads) cache_step_kernel(const StepPara
 // One warp per token: y = x r g with r = 1 / sqrt(mean(x^2) + eps) over the
 // 512 latent dims, the 64 rotated dims behind them, encoded as the pool
 // stores them and written to the token's slot.  One pass: the row stays in
-// registers (16 latent dims and one rotation pair a lane).  Bound by memory
-// and, with about 480 instructions a token, by issue as much: 16,384 tokens to
-// fp8 10.0 us (3.3 TB/s, issue 48 % busy), 5003 to MXFP4 5.3 us, 32 2.2 us.
+// registers (16 latent dims and one rotation pair a lane).  16,384 tokens to fp8
+// take 9.9 us: neither memory (3.3 TB/s) nor issue (about 480 instructions a
+// token, 47 % busy) is full, but each of 2.7 waves loads, then computes, then
+// stores.  5003 to MXFP4 5.2 us, 32 to bf16 2.2 us.
 // Several tokens a warp with the next one's loads ahead took 13.9 us (90
 // registers, a quarter of the warps).
 //

@@ -11,14 +11,15 @@
 // bf16) in shared memory and streams half of each head's weights past them.
 // On its own a CTA would read 12 KB of operands a product (128 cycles) and
 // take in 8 KB of weights, 160 bytes a cycle of a shared memory that gives 128
-// (32,845 MXFP4 keys, 16 heads: 121 us; in pairs 94 us).  Rows are read and decoded
+// (32,845 MXFP4 keys, 16 heads: 121 us; in pairs 93 us).  Rows are read and decoded
 // once per pair that meets them; units (two tiles, head) are split evenly over
 // the pairs.  Two 256-column accumulators let the epilogue of one head run
 // under the products of the next.  Operand reads, weights and outputs still
 // take about 125 bytes a cycle at the products' full rate, and new rows of a
 // single buffer stop them for about 8,000 cycles a tile pair: the tensor pipe is
-// 60 % busy in the long run (1.47 PFLOP/s); 8192 bf16 keys take 31 us (1.1 PFLOP/s), of which about 8 us
-// pass before the first product (page table, rows and weights from memory).
+// 62 % busy in the long run (1.48 PFLOP/s); 8192 bf16 keys take 32 us (1.07
+// PFLOP/s), of which about 8 us pass before the first product (page table, rows
+// and weights from memory).
 // With the rows in tensor memory (bulk copies, decoded a lane a row, products of
 // N = 128) it took 90 / 33 us: faster on long rows, slower on short ones.
 //
