@@ -630,6 +630,181 @@ mla_status mla_prefill_run(mla_prefill* plan, const void* q, int64_t q_token_str
  * rotation table also gives MLA_ERR_INVALID_ARG. */
 mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Reading less of a long cache: a prefix that many requests share is read once
+ * for all of them, or each query reads only the pages that promise most.
+ */
+
+/*
+ * mla_shared_plan -- plan of a decode call over groups of requests that share a
+ * prefix.  Requests group_indptr[g] .. group_indptr[g+1]-1 attend to the pages
+ * of group g's prefix (all of them full), then to pages of their own:
+ *     out[b,t,h,:] = softmax over [prefix of b's group ; own tokens of b]
+ * with the scores, values and lse of mla_decode_run.  The prefix's rows are read
+ * and multiplied once for up to 128 query rows (8 query tokens of 16 heads).
+ *
+ *   group_indptr_host   host int32 [num_groups+1], non-decreasing from 0; its
+ *                       last entry is the batch size (at least 1).
+ *   prefix_indptr_host  host int32 [num_groups+1], non-decreasing, in pages:
+ *                       group g's prefix is entries prefix_indptr[g] ..
+ *                       prefix_indptr[g+1]-1 of the prefixes' page table.  A
+ *                       group may have no prefix.
+ *   kv_indptr_host, kv_last_page_len_host, page_size, q_dtype, kv_dtype
+ *                       the requests' own pages, as for mla_decode_plan (the
+ *                       same pairs of types).
+ *   q_len               query tokens per request (1 .. MLA_MAX_Q_LEN), the last
+ *                       positions of its own tokens: query token t sees the
+ *                       prefix and the first n - q_len + 1 + t of n own tokens.
+ *                       A request of a group with a prefix has at least
+ *                       q_len - 1 own tokens, so that each sees the whole prefix.
+ *   num_sms             CTAs to plan for; 0 = the SM count of the device.
+ * The plan follows mla_plan's rules: library-owned, one host thread at a time,
+ * one workspace per plan.  The workspace holds the prefixes' rows in bf16 (1,152
+ * bytes a token, the group's length rounded up to 128), the partial results (256
+ * KB for each of num_items, 32 KB and more for each range of own tokens) and the
+ * work tables.
+ * Errors: MLA_ERR_INVALID_ARG (also out of host memory), MLA_ERR_UNSUPPORTED (a
+ * pair of types), MLA_ERR_CUDA.
+ */
+typedef struct mla_shared mla_shared;
+
+typedef struct {
+  int32_t batch_size;
+  int32_t num_groups;
+  int32_t q_len;
+  int32_t num_pairs;         /* pairs of CTAs that work on the prefixes */
+  int32_t num_items;         /* (up to 128 query rows, range of their prefix) */
+  int64_t prefix_tokens;     /* of groups with requests, once each */
+  int64_t own_tokens;        /* as the decode kernel counts them: for each query token (or pair) */
+  size_t workspace_bytes;
+} mla_shared_info;
+
+mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* prefix_indptr_host,
+                           int32_t num_groups, const int32_t* kv_indptr_host,
+                           const int32_t* kv_last_page_len_host, int32_t q_len, int32_t page_size,
+                           mla_dtype q_dtype, mla_dtype kv_dtype, int32_t num_sms,
+                           mla_shared** plan_out);
+mla_status mla_shared_get_info(const mla_shared* plan, mla_shared_info* info);
+void mla_shared_destroy(mla_shared* plan);
+
+/*
+ * mla_shared_run -- one decode call of that plan, enqueued on `stream`.
+ *
+ * Sums, maxima, the softmax's statistics and partial outputs are fp32.  Against
+ * a prefix, probabilities are rounded to bf16 where they meet the values; the
+ * stored values and the queries are exact there.
+ *
+ *   q, q_scale, kv .. kv_pool_rows, out, lse   as for mla_decode_run with a plan
+ *                    of the same q_len.
+ *   prefix_indices   device int32 page table of the prefixes, indexed from
+ *                    prefix_indptr; NULL = the identity table.
+ *   kv_indices       device int32 page table of the requests' own pages, indexed
+ *                    from kv_indptr; NULL = the identity table.
+ *   workspace        mla_shared_info.workspace_bytes device bytes, 256-byte
+ *                    aligned; its rules are those of mla_decode_run.
+ * Errors: those of mla_decode_run.
+ */
+mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale, const void* kv,
+                          const float* kv_scale, const uint8_t* kv_e8m0, int64_t kv_e8m0_row_stride,
+                          int64_t kv_pool_rows, const int32_t* prefix_indices,
+                          const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
+                          void* out, float* lse, mla_stream_t stream);
+
+/* mla_decode_check for a shared plan's workspace. */
+mla_status mla_shared_check(const mla_shared* plan, void* workspace, mla_stream_t stream);
+
+/*
+ * Selected pages.  Three calls, in the order of a step, behind mla_cache_step and
+ * mla_cache_write: the bounds of the pages that got rows, the score of every page
+ * for every query, and the best pages as the page table of a decode call
+ * (mla_decode_plan with one query token, a "request" for each query token, whose
+ * length in pages is at most top_pages).  Pages are those of the pool: page_size
+ * is also the grain of the selection.  The block table is mla_cache_step's.
+ *
+ * mla_page_bounds -- the smallest and the largest of every dim over a page's
+ * rows, for the pages that hold tokens old_lens[b] .. old_lens[b] + new_lens[b] -
+ * 1 of a request.  A page with earlier tokens goes on from the bounds that it
+ * has; with old_lens 0 all pages are begun anew.
+ *
+ *   kv .. kv_pool_rows, page_size   the pool, as mla_decode_run reads it.
+ *   old_lens, new_lens  device int32 [batch_size]; new_lens NULL = 1 each.
+ *   block_table     device int32 [batch_size][table_stride], table_pages columns
+ *                   used; column j of row b is the page of tokens j*page_size .. .
+ *   bounds          bf16 [num_pages][2][576], 16-byte aligned: the smallest
+ *                   values, then the largest, exactly as stored (an e4m3 pool's
+ *                   values without kv_scale).  Both are NaN for a dim with a value
+ *                   that is not finite.
+ * Two requests of a call must not have new tokens in the same page.
+ * On the device: a negative length counts as 0, a page outside the pool or the
+ * bounds is skipped (mla_error_check: MLA_ERR_INVALID_ARG), as are pages beyond
+ * the table's columns (MLA_ERR_CAPACITY).
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
+ */
+mla_status mla_page_bounds(const void* kv, mla_dtype kv_dtype, const uint8_t* kv_e8m0,
+                           int64_t kv_e8m0_row_stride, int64_t kv_pool_rows, int32_t page_size,
+                           const int32_t* old_lens, const int32_t* new_lens, int32_t batch_size,
+                           const int32_t* block_table, int64_t table_stride, int32_t table_pages,
+                           void* bounds, int64_t num_pages, int32_t* err, mla_stream_t stream);
+
+/*
+ * mla_page_scores -- for every query token and page, an upper bound of the
+ * decode call's scores of the page's tokens, over all heads:
+ *     scores[r,j] = (q_scale kv_scale / sqrt(576))
+ *                   max_h sum_d max(q[r,h,d] lo_j[d], q[r,h,d] hi_j[d]).
+ * Query token t of a request with n tokens (row r = b * q_len + t) sees the first
+ * n - q_len + 1 + t; columns without a token that it sees are -inf.
+ *
+ *   q           [batch_size * q_len][16][576], bf16 or e4m3 (with q_scale), as
+ *               mla_decode_run takes it; 16-byte aligned.
+ *   q_scale, kv_scale  device fp32 [1], positive; NULL = 1 (q_scale is required
+ *               for an e4m3 query and ignored for a bf16 one).
+ *   bounds, num_pages, block_table .. table_pages   as above.
+ *   lens        device int32 [batch_size]: tokens of a request, new ones included.
+ *   scores      fp32 [batch_size * q_len], row stride scores_stride; table_pages
+ *               columns are written.
+ * A page with NaN bounds scores NaN.  Sums are fp32.  On the device: a negative
+ * length counts as 0, a page outside the bounds is read as page 0 (both
+ * MLA_ERR_INVALID_ARG); tokens beyond the table's columns do not count
+ * (MLA_ERR_CAPACITY).
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (q_dtype), MLA_ERR_CUDA.
+ */
+mla_status mla_page_scores(const void* q, mla_dtype q_dtype, const float* q_scale,
+                           const float* kv_scale, const void* bounds, int64_t num_pages,
+                           const int32_t* lens, int32_t batch_size, int32_t q_len,
+                           int32_t page_size, const int32_t* block_table, int64_t table_stride,
+                           int32_t table_pages, float* scores, int64_t scores_stride, int32_t* err,
+                           mla_stream_t stream);
+
+/*
+ * mla_page_select -- the page table of the best pages.  A row (as above) that
+ * sees at most top_pages pages keeps all; another keeps its first_pages first,
+ * its last_pages last, and of those between the ones with the largest scores, up
+ * to top_pages in all (ties: the lower column; NaN counts as the largest score,
+ * -0 as 0).  Kept pages stay in order.
+ *
+ *   scores, lens, block_table .. table_pages   as above; any scores will do.
+ *   top_pages, first_pages, last_pages   last_pages >= 1 (the last page may be
+ *                 part full), first_pages + last_pages <= top_pages.
+ *   kv_indptr     int32 [rows+1] out: kept pages before each row.
+ *   kv_last_page_len  int32 [rows] out: tokens that the row sees in its last
+ *                 page (0: none).
+ *   kv_indices    int32 [max_indices] out: the kept pages' table entries, row by
+ *                 row.  Entries past kv_indptr[rows] are left alone.
+ *   columns       int32 [rows][top_pages] out, or NULL: the kept columns, then -1.
+ * The host knows the counts without reading them back: min(top_pages, pages).
+ * On the device: a negative length counts as 0 (MLA_ERR_INVALID_ARG); tokens
+ * beyond the table's columns do not count, entries beyond max_indices are not
+ * written (MLA_ERR_CAPACITY).
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
+ */
+mla_status mla_page_select(const float* scores, int64_t scores_stride, const int32_t* lens,
+                           int32_t batch_size, int32_t q_len, int32_t page_size,
+                           const int32_t* block_table, int64_t table_stride, int32_t table_pages,
+                           int32_t top_pages, int32_t first_pages, int32_t last_pages,
+                           int32_t* kv_indptr, int32_t* kv_last_page_len, int32_t* kv_indices,
+                           int64_t max_indices, int32_t* columns, int32_t* err,
+                           mla_stream_t stream);
+
 /*
  * mla_error_check -- synchronises `stream`, reads the device error word `err`
  * and clears it.  MLA_OK; MLA_ERR_CAPACITY (nothing but pages, table columns

@@ -5,7 +5,9 @@ CUDA kernels.  The names mirror the C ABI in include/mla_decode.h:
 ``mla_decode_plan``, ``mla_decode_run``, ``mla_decode_check``,
 ``mla_status_string``.  The operators that make an attention layer of the
 decode call (``mla_cache_step``, ``mla_cache_write``, ``mla_absorb_q``,
-``mla_absorb_out``, ``mla_prefill_plan``, ``mla_prefill_run``) are in layer.py.  PyTorch tensors are accepted for device memory and
+``mla_absorb_out``, ``mla_prefill_plan``, ``mla_prefill_run``) are in layer.py,
+those that read less of a long cache (``mla_shared_plan``, ``mla_shared_run``,
+``mla_page_bounds``, ``mla_page_scores``, ``mla_page_select``) in longcache.py.  PyTorch tensors are accepted for device memory and
 ``torch.cuda`` streams; there is no CPU fallback -- importing this package
 fails loudly when the shared library has not been built.
 """
@@ -28,7 +30,9 @@ EXPORTS = ("mla_decode_plan", "mla_decode_plan_q", "mla_decode_plan_ex", "mla_pl
            "mla_autotune_select", "mla_cache_step", "mla_cache_write", "mla_absorb_q",
            "mla_absorb_out", "mla_prefill_plan", "mla_prefill_get_info", "mla_prefill_destroy",
            "mla_prefill_run", "mla_prefill_check", "mla_error_check", "mla_absorb_out_ex",
-           "mla_selftest_absorb_wait")
+           "mla_selftest_absorb_wait", "mla_shared_plan", "mla_shared_get_info",
+           "mla_shared_destroy", "mla_shared_run", "mla_shared_check", "mla_page_bounds",
+           "mla_page_scores", "mla_page_select")
 
 
 class MlaError(RuntimeError):
@@ -336,16 +340,20 @@ class MlaDecoder:
         return out
 
 
-# The operators around the decode call (layer.py) need torch at import; they
-# are loaded when first asked for.
+# The operators around the decode call (layer.py) and those that read less of a
+# long cache (longcache.py) need torch at import; they are loaded when first
+# asked for.
 LAYER = ("MlaPrefill", "PrefillInfo", "PrefillPlan", "mla_absorb_out", "mla_absorb_q",
          "mla_cache_step", "mla_cache_write", "mla_error_check", "mla_prefill_check",
          "mla_prefill_plan", "mla_prefill_run", "mla_selftest_absorb_wait")
+LONG_CACHE = ("MlaShared", "SharedInfo", "SharedPlan", "mla_page_bounds", "mla_page_scores",
+              "mla_page_select", "mla_shared_check", "mla_shared_plan", "mla_shared_run")
 
 
 def __getattr__(name):
-    if name in LAYER:
-        from . import layer
-        value = globals()[name] = getattr(layer, name)
+    if name in LAYER or name in LONG_CACHE:
+        from importlib import import_module
+        module = import_module("." + ("layer" if name in LAYER else "longcache"), __name__)
+        value = globals()[name] = getattr(module, name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

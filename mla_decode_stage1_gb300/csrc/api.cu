@@ -262,6 +262,19 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 namespace mla {
 uint64_t new_plan_stamp() { return next_stamp(); }
 TiledEncoder tiled_encoder() { return encode_fn(); }
+void plan_partials_only(mla_plan* P, std::vector<int32_t>* first, std::vector<int32_t>* count) {
+  first->assign(P->bs, 0);
+  count->assign(P->bs, 0);
+  for (const WorkItem& w : P->items) ++(*count)[w.b];
+  for (int32_t b = 1; b < P->bs; ++b) (*first)[b] = (*first)[b - 1] + (*count)[b - 1];
+  std::vector<int32_t> used(P->bs, 0);
+  for (WorkItem& w : P->items) w.slot = (*first)[w.b] + used[w.b]++;
+  P->num_partials = static_cast<int32_t>(P->items.size());
+  P->jobs.clear();
+  P->cluster = 0;
+  P->exact_q = 1;
+  layout_workspace(P);
+}
 }  // namespace mla
 
 extern "C" {
@@ -565,6 +578,7 @@ mla_status mla_decode_run(mla_plan* plan, const void* q, const float* q_scale, c
     p.kv_e8m0 = kv_e8m0;
     p.sc_stride = kv_e8m0_row_stride;
     p.cluster = cluster ? plan->cluster : 0;
+    p.exact_q = plan->exact_q;
     if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, stream) != cudaSuccess)
       return MLA_ERR_CUDA;
     if (mla::launch_stage1(plan->qmode, p, plan->num_ctas, stream) != cudaSuccess)

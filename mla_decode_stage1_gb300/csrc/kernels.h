@@ -110,6 +110,7 @@ struct Stage1Params {
   int64_t pool_rows;
   const uint8_t* kv_e8m0;       // MXFP4 only: e8m0 scale rows (18 bytes used per row)
   int64_t sc_stride;            // bytes between scale rows (even, >= 18)
+  int32_t exact_q;              // 1: bf16 q is split into two e4m3 terms without loss
 };
 
 struct Stage2Params {

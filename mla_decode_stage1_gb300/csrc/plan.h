@@ -22,6 +22,7 @@ struct mla_plan {
   int32_t unit_tokens = mla::kTile;   // tokens between the planner's possible cut points
   int32_t item_cost = 1;              // cost of an extra item in a CTA (balanced plan)
   int32_t num_sms = 0;                // CTAs the balanced plan was cut for
+  int32_t exact_q = 0;                // see Stage1Params
   int32_t cluster = 0;                // CTAs per cluster merging a request inside stage 1 (0: stage 2)
   int64_t total_tokens = 0, total_tiles = 0;
   int64_t identity_rows = 0;   // pool rows the requests reach without a page table
@@ -59,4 +60,9 @@ typedef CUresult (*TiledEncoder)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 TiledEncoder tiled_encoder();
+// Turns a new plan into one whose every item writes a partial result and whose
+// run merges nothing: request b's are slots first[b] .. first[b] + count[b] - 1.
+// Its run splits a bf16 query without loss where the decode call rounds it a
+// little (a log-sum-exp of few tokens was 3e-4 off).
+void plan_partials_only(mla_plan* P, std::vector<int32_t>* first, std::vector<int32_t>* count);
 }  // namespace mla

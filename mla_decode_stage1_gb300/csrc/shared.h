@@ -1,0 +1,87 @@
+// shared.h -- internal interface between the host side of the shared-prefix
+// decode (shared_api.cu) and its kernels (gather.cu, prefix.cu, meet.cu).
+#pragma once
+
+#include "prefill.h"
+
+namespace mla {
+
+constexpr int kSpRows = 128;     // query rows of a block: 8 tokens x 16 heads
+constexpr int kSpTile = 128;     // keys of a tile
+
+// Query rows q_row .. q_row + rows - 1 (row = token * 16 + head) of one group
+// against `keys` of its prefix's rows, from workspace row key0 on.
+struct PrefixItem {
+  int32_t q_row, rows, key0, keys, slot;   // slot: of the partial result, 128 rows each
+  uint32_t check;
+  int32_t pad[2];
+};
+static_assert(sizeof(PrefixItem) == 32, "a prefix item is two int4");
+__host__ __device__ inline uint32_t check_of(const PrefixItem& w, uint64_t stamp) {
+  const uint32_t h = mix(mix(mix(static_cast<uint32_t>(stamp), w.q_row), w.rows), w.key0);
+  return mix(mix(h, w.keys), w.slot);
+}
+
+// The partial results of one query token: `own_count` of the decode kernel from
+// own_first on (its 16 heads from row own_row of each), prefix_count of the
+// prefix kernel from prefix_first on (from row prefix_row of each).
+struct MeetJob {
+  int32_t own_first, own_count, own_row, prefix_first, prefix_count, prefix_row;
+  uint32_t check;
+  int32_t pad;
+};
+static_assert(sizeof(MeetJob) == 32, "a meeting is two int4");
+__host__ __device__ inline uint32_t check_of(const MeetJob& j, uint64_t stamp) {
+  const uint32_t h = mix(mix(mix(static_cast<uint32_t>(stamp), j.own_first), j.own_count), j.own_row);
+  return mix(mix(mix(h, j.prefix_first), j.prefix_count), j.prefix_row);
+}
+
+struct GatherParams {
+  const ExpandTile* tiles;     // 128 rows each
+  int32_t num_tiles;
+  const uint8_t* kv;
+  const uint8_t* e8m0;
+  int64_t e8m0_stride;
+  int64_t pool_rows;
+  const int32_t* indices;      // page table of the prefixes, or null: identity
+  int32_t page_size;
+  int32_t kv_dtype;
+  uint16_t* rows;              // [tiles * 128][576] bf16
+  int32_t* err;                // workspace header
+  uint64_t stamp;
+};
+
+struct PrefixParams {
+  CUtensorMap map_k;           // {64, rows, 9} of the gathered rows, boxes {64, 128, 1}
+  CUtensorMap map_v;           // the same, boxes {64, 64, 4}
+  const PrefixItem* items;
+  const CtaItems* pairs;
+  const void* q;               // [tokens * 16][576], bf16 or e4m3
+  int32_t q_fp8;
+  const float* q_scale;        // device [1], or null: 1
+  const float* kv_scale;       // device [1], or null: 1
+  float* part_o;               // [slots][128][512] fp32, normalised
+  float* part_lse;             // [slots][128], log2 domain
+  int32_t* err;
+  uint64_t stamp;
+};
+
+struct MeetParams {
+  const MeetJob* jobs;
+  int64_t tokens;
+  const float* own_o;          // [partials][own_rows][512]
+  const float* own_lse;
+  int32_t own_rows;
+  const float* prefix_o;       // [slots][128][512]
+  const float* prefix_lse;
+  uint16_t* out;
+  float* lse;
+  int32_t* err;
+  uint64_t stamp;
+};
+
+cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream);
+cudaError_t launch_prefix(const PrefixParams& p, int num_pairs, cudaStream_t stream);
+cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream);
+
+}  // namespace mla

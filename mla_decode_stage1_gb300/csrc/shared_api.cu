@@ -1,0 +1,402 @@
+// shared_api.cu -- host side of the shared-prefix decode: validation, the plan
+// (the decode kernel's work over the requests' own ends, the prefix kernel's
+// over the prefixes), workspace layout, tensor maps and launches.  The C
+// declarations and their contracts are in include/mla_decode.h.
+
+#include <algorithm>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "plan.h"
+#include "shared.h"
+
+using mla::CtaItems;
+using mla::ExpandTile;
+using mla::MeetJob;
+using mla::PrefixItem;
+
+struct mla_shared {
+  int32_t bs = 0, groups = 0, q_len = 1, page_size = 0, num_sms = 0;
+  int q_dtype = 0, kv_dtype = 0;
+  int32_t num_pairs = 0, num_slots = 0;
+  int64_t prefix_tokens = 0, identity_rows = 0;
+  mla_plan* own = nullptr;           // over the requests' own ends, partial results only
+  std::vector<ExpandTile> tiles;
+  std::vector<PrefixItem> items;
+  std::vector<CtaItems> pair_items;
+  std::vector<MeetJob> jobs;
+  size_t off_tiles = 0, off_pairs = 0, off_items = 0, off_jobs = 0, off_own = 0, off_rows = 0,
+         off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
+  std::vector<uint8_t> table;
+  uint64_t stamp = 0;
+  mutable void* uploaded_ws = nullptr;
+  void* map_ws = nullptr;
+  CUtensorMap map_k, map_v;
+  ~mla_shared() { mla_plan_destroy(own); }
+};
+
+namespace {
+
+constexpr int32_t kTokensPerBlock = mla::kSpRows / mla::kHeads;
+
+// What an item costs beside its tiles, in tiles: the queries' way into tensor
+// memory, the first scores and the last values without the other half's work
+// beside them, and the output.
+constexpr int64_t kItemCost = 2;
+
+struct Block {
+  int32_t q_row, rows, key0, keys;   // key0: workspace row of the group's first key
+};
+
+// The blocks' key tiles, in order, cut into at most `pairs` ranges of nearly
+// equal cost (kItemCost for each item, 1 for each tile).  The smallest largest
+// cost that greedy ranges reach is found by bisection.
+void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t pairs) {
+  int64_t total = 0;
+  for (const Block& b : blocks) total += (b.keys + mla::kSpTile - 1) / mla::kSpTile;
+  auto cut = [&](int64_t cap, auto&& emit) {
+    int64_t ranges = 0, left = 0;
+    for (size_t k = 0; k < blocks.size(); ++k) {
+      const int64_t tiles = (blocks[k].keys + mla::kSpTile - 1) / mla::kSpTile;
+      for (int64_t at = 0; at < tiles;) {
+        if (left <= kItemCost) {
+          left = cap;
+          ++ranges;
+        }
+        const int64_t take = std::min(left - kItemCost, tiles - at);
+        emit(k, at, take, ranges - 1);
+        left -= kItemCost + take;
+        at += take;
+      }
+    }
+    return ranges;
+  };
+  int64_t lo = kItemCost + 1, hi = kItemCost * (1 + static_cast<int64_t>(blocks.size())) + total;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (cut(mid, [](size_t, int64_t, int64_t, int64_t) {}) <= pairs) hi = mid; else lo = mid + 1;
+  }
+  int64_t last = -1;
+  cut(lo, [&](size_t k, int64_t at, int64_t take, int64_t range) {
+    const Block& b = blocks[k];
+    if (range != last) {
+      const int32_t n = static_cast<int32_t>(P->items.size());
+      if (last >= 0) P->pair_items.back().end = n;
+      P->pair_items.push_back(CtaItems{n, n, 0u, 0});
+      last = range;
+    }
+    PrefixItem w{};
+    w.q_row = b.q_row;
+    w.rows = b.rows;
+    w.key0 = static_cast<int32_t>(b.key0 + at * mla::kSpTile);
+    w.keys = static_cast<int32_t>(std::min<int64_t>(take * mla::kSpTile, b.keys - at * mla::kSpTile));
+    w.slot = static_cast<int32_t>(P->items.size());       // a block's are consecutive
+    P->items.push_back(w);
+  });
+  if (!P->pair_items.empty()) P->pair_items.back().end = static_cast<int32_t>(P->items.size());
+  P->num_pairs = static_cast<int32_t>(P->pair_items.size());
+  P->num_slots = static_cast<int32_t>(P->items.size());
+}
+
+mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
+                     const int32_t* kv_indptr, const int32_t* last_len) {
+  const int32_t t = P->q_len;
+  std::vector<Block> blocks;
+  std::vector<int32_t> block_of(P->bs, -1), first_of(P->bs, 0);   // first: the group's first token
+  int64_t rows = 0;
+  for (int32_t g = 0; g < P->groups; ++g) {
+    const int64_t np = static_cast<int64_t>(prefix_indptr[g + 1]) - prefix_indptr[g];
+    const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
+    if (np < 0 || b1 < b0) return MLA_ERR_INVALID_ARG;
+    const int64_t keys = np * P->page_size;
+    if (keys == 0) continue;
+    if (rows + keys > INT32_MAX - mla::kSpTile) return MLA_ERR_INVALID_ARG;
+    if (b1 == b0) continue;
+    P->identity_rows = std::max(P->identity_rows,
+                                (static_cast<int64_t>(prefix_indptr[g]) + np) * P->page_size);
+    P->prefix_tokens += keys;
+    for (int32_t b = b0; b < b1; ++b) {
+      // every query token sees the whole prefix
+      int64_t n = (static_cast<int64_t>(kv_indptr[b + 1]) - kv_indptr[b]) * P->page_size;
+      if (n > 0 && last_len != nullptr) n -= P->page_size - last_len[b];
+      if (n < t - 1) return MLA_ERR_INVALID_ARG;
+      block_of[b] = static_cast<int32_t>(blocks.size());
+      first_of[b] = b0 * t;
+    }
+    const int64_t tokens = static_cast<int64_t>(b1 - b0) * t;
+    for (int64_t a = 0; a < tokens; a += kTokensPerBlock) {
+      Block b;
+      b.q_row = static_cast<int32_t>((static_cast<int64_t>(b0) * t + a) * mla::kHeads);
+      b.rows = static_cast<int32_t>(std::min<int64_t>(kTokensPerBlock, tokens - a) * mla::kHeads);
+      b.key0 = static_cast<int32_t>(rows);
+      b.keys = static_cast<int32_t>(keys);
+      blocks.push_back(b);
+    }
+    for (int64_t k = 0; k < keys; k += mla::kSpTile) {
+      ExpandTile e{};
+      e.page_base = prefix_indptr[g];
+      e.tok0 = static_cast<int32_t>(k);
+      e.len = static_cast<int32_t>(keys);
+      e.out_row = static_cast<int32_t>(rows + k);
+      P->tiles.push_back(e);
+    }
+    rows += (keys + mla::kSpTile - 1) / mla::kSpTile * mla::kSpTile;
+  }
+  cut_blocks(P, blocks, std::max(1, P->num_sms / 2));
+  // partial results of every block, then of every query token
+  std::vector<int32_t> first_slot(blocks.size(), 0), slots(blocks.size(), 0);
+  {
+    size_t k = 0;
+    int64_t left = blocks.empty() ? 0 : blocks[0].keys;
+    for (size_t i = 0; i < P->items.size(); ++i) {
+      if (slots[k]++ == 0) first_slot[k] = static_cast<int32_t>(i);
+      left -= P->items[i].keys;
+      if (left == 0 && ++k < blocks.size()) left = blocks[k].keys;
+    }
+  }
+  std::vector<int32_t> own_first, own_count;
+  mla::plan_partials_only(P->own, &own_first, &own_count);
+  const bool two = P->own->rows == 2 * mla::kHeads;      // tokens of a request in pairs
+  for (int32_t b = 0; b < P->bs; ++b)
+    for (int32_t i = 0; i < t; ++i) {
+      MeetJob j{};
+      const int32_t r = two ? b * (t / 2) + i / 2 : b * t + i;
+      j.own_first = own_first[r];
+      j.own_count = own_count[r];
+      j.own_row = two ? i % 2 * mla::kHeads : 0;
+      if (block_of[b] >= 0) {
+        const int32_t in = b * t + i - first_of[b], k = block_of[b] + in / kTokensPerBlock;
+        j.prefix_first = first_slot[k];
+        j.prefix_count = slots[k];
+        j.prefix_row = in % kTokensPerBlock * mla::kHeads;
+      }
+      P->jobs.push_back(j);
+    }
+  size_t off = sizeof(mla::PrefillHeader);
+  auto take = [&](size_t bytes) {
+    const size_t at = (off + 255) & ~static_cast<size_t>(255);
+    off = (at + bytes + 255) & ~static_cast<size_t>(255);
+    return at;
+  };
+  P->off_tiles = take(sizeof(ExpandTile) * P->tiles.size());
+  P->off_pairs = take(sizeof(CtaItems) * P->pair_items.size());
+  P->off_items = take(sizeof(PrefixItem) * P->items.size());
+  P->off_jobs = take(sizeof(MeetJob) * P->jobs.size());
+  P->table.assign(off, 0);
+  P->off_own = take(P->own->ws_bytes);
+  P->off_rows = take(sizeof(uint16_t) * P->tiles.size() * mla::kSpTile * mla::kQkDim);
+  P->off_part_o = take(sizeof(float) * P->num_slots * mla::kSpRows * mla::kVDim);
+  P->off_part_lse = take(sizeof(float) * P->num_slots * mla::kSpRows);
+  P->ws_bytes = off;
+  P->stamp = mla::new_plan_stamp();
+  mla::PrefillHeader hdr{};
+  hdr.ws.stamp = P->stamp;
+  std::memcpy(P->table.data(), &hdr, sizeof(hdr));
+  auto put = [&](size_t at, auto& records) {
+    for (auto& r : records) r.check = mla::check_of(r, P->stamp);
+    if (!records.empty())
+      std::memcpy(P->table.data() + at, records.data(), sizeof(records[0]) * records.size());
+  };
+  put(P->off_tiles, P->tiles);
+  put(P->off_pairs, P->pair_items);
+  put(P->off_items, P->items);
+  put(P->off_jobs, P->jobs);
+  return MLA_OK;
+}
+
+// Gathered rows as {64 dims, rows, 9 panels} with the 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* rows, int64_t count, uint32_t box_rows,
+              uint32_t box_panels) {
+  const mla::TiledEncoder enc = mla::tiled_encoder();
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(count), mla::kQkDim / 64};
+  const cuuint64_t strides[2] = {mla::kQkDim * 2, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_panels}, one[3] = {1, 1, 1};
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* prefix_indptr_host,
+                           int32_t num_groups, const int32_t* kv_indptr_host,
+                           const int32_t* kv_last_page_len_host, int32_t q_len, int32_t page_size,
+                           mla_dtype q_dtype, mla_dtype kv_dtype, int32_t num_sms,
+                           mla_shared** plan_out) {
+  if (plan_out == nullptr) return MLA_ERR_INVALID_ARG;
+  *plan_out = nullptr;
+  if (group_indptr_host == nullptr || prefix_indptr_host == nullptr || kv_indptr_host == nullptr ||
+      num_groups < 1 || num_sms < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (group_indptr_host[0] != 0 || prefix_indptr_host[0] < 0) return MLA_ERR_INVALID_ARG;
+  for (int32_t g = 0; g < num_groups; ++g)
+    if (group_indptr_host[g + 1] < group_indptr_host[g]) return MLA_ERR_INVALID_ARG;
+  if (num_sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MLA_ERR_CUDA;
+  }
+  mla_shared* P = nullptr;
+  mla_status st = MLA_ERR_INVALID_ARG;
+  try {
+    P = new mla_shared();
+    P->bs = group_indptr_host[num_groups];
+    P->groups = num_groups;
+    P->q_len = q_len;
+    P->page_size = page_size;
+    P->num_sms = num_sms;
+    P->q_dtype = q_dtype;
+    P->kv_dtype = kv_dtype;
+    // (checks the batch's lengths, query tokens, page size and types)
+    const mla_plan_options o{0, num_sms, 0, 0, 1};
+    st = mla_decode_plan_ex(kv_indptr_host, kv_last_page_len_host, P->bs, q_len, page_size, q_dtype,
+                            kv_dtype, &o, &P->own);
+    if (st == MLA_OK)
+      st = make_plan(P, group_indptr_host, prefix_indptr_host, kv_indptr_host, kv_last_page_len_host);
+  } catch (...) {   // out of host memory
+    st = MLA_ERR_INVALID_ARG;
+  }
+  if (st != MLA_OK) {
+    delete P;
+    return st;
+  }
+  *plan_out = P;
+  return MLA_OK;
+}
+
+mla_status mla_shared_get_info(const mla_shared* plan, mla_shared_info* info) {
+  if (plan == nullptr || info == nullptr) return MLA_ERR_INVALID_ARG;
+  info->batch_size = plan->bs;
+  info->num_groups = plan->groups;
+  info->q_len = plan->q_len;
+  info->num_pairs = plan->num_pairs;
+  info->num_items = static_cast<int32_t>(plan->items.size());
+  info->prefix_tokens = plan->prefix_tokens;
+  info->own_tokens = plan->own->total_tokens;
+  info->workspace_bytes = plan->ws_bytes;
+  return MLA_OK;
+}
+
+void mla_shared_destroy(mla_shared* plan) { delete plan; }
+
+mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale, const void* kv,
+                          const float* kv_scale, const uint8_t* kv_e8m0, int64_t kv_e8m0_row_stride,
+                          int64_t kv_pool_rows, const int32_t* prefix_indices,
+                          const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
+                          void* out, float* lse, mla_stream_t stream_) {
+  using mla::ptr_aligned;
+  if (plan == nullptr || q == nullptr || kv == nullptr || out == nullptr || workspace == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (!ptr_aligned(workspace, 256) || !ptr_aligned(q, 16) || !ptr_aligned(kv, 16) ||
+      !ptr_aligned(out, 16) || !ptr_aligned(lse, 4) || !ptr_aligned(q_scale, 4) ||
+      !ptr_aligned(kv_scale, 4) || !ptr_aligned(prefix_indices, 4) || !ptr_aligned(kv_indices, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (kv_pool_rows < 1 || kv_pool_rows > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (plan->q_dtype == MLA_DTYPE_FP8_E4M3 && q_scale == nullptr) return MLA_ERR_INVALID_ARG;
+  if (plan->kv_dtype == MLA_DTYPE_FP8_E4M3 && kv_scale == nullptr) return MLA_ERR_INVALID_ARG;
+  if (plan->kv_dtype == MLA_DTYPE_MXFP4) {
+    if (kv_e8m0 == nullptr || kv_e8m0_row_stride < 18) return MLA_ERR_INVALID_ARG;
+    if (kv_e8m0_row_stride % 2 != 0 || !ptr_aligned(kv_e8m0, 2)) return MLA_ERR_UNSUPPORTED;
+  }
+  if (workspace_bytes < plan->ws_bytes) return MLA_ERR_WORKSPACE;
+  if (prefix_indices == nullptr ? plan->identity_rows > kv_pool_rows
+                                : kv_pool_rows % plan->page_size != 0)
+    return MLA_ERR_INVALID_ARG;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  // the requests' own ends, first: that call checks its arguments before it
+  // launches anything
+  const mla_status st = mla_decode_run(plan->own, q, q_scale, kv, kv_scale, kv_e8m0,
+                                       kv_e8m0_row_stride, kv_pool_rows, kv_indices,
+                                       ws + plan->off_own, plan->own->ws_bytes, out, nullptr, stream_);
+  if (st != MLA_OK) return st;
+  if (plan->uploaded_ws != workspace) {
+    if (cudaMemcpyAsync(ws, plan->table.data(), plan->table.size(), cudaMemcpyHostToDevice,
+                        stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    plan->uploaded_ws = workspace;
+  }
+  int32_t* err = reinterpret_cast<int32_t*>(ws);
+  uint16_t* rows = reinterpret_cast<uint16_t*>(ws + plan->off_rows);
+  float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
+  float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
+  if (plan->num_pairs > 0) {
+    if (plan->map_ws != workspace) {
+      const int64_t count = static_cast<int64_t>(plan->tiles.size()) * mla::kSpTile;
+      plan->map_ws = nullptr;
+      if (!make_map(&plan->map_k, rows, count, mla::kSpTile, 1) ||
+          !make_map(&plan->map_v, rows, count, 64, 4))
+        return MLA_ERR_CUDA;
+      plan->map_ws = workspace;
+    }
+    mla::GatherParams g{};
+    g.tiles = reinterpret_cast<const ExpandTile*>(ws + plan->off_tiles);
+    g.num_tiles = static_cast<int32_t>(plan->tiles.size());
+    g.kv = static_cast<const uint8_t*>(kv);
+    g.e8m0 = kv_e8m0;
+    g.e8m0_stride = kv_e8m0_row_stride;
+    g.pool_rows = kv_pool_rows;
+    g.indices = prefix_indices;
+    g.page_size = plan->page_size;
+    g.kv_dtype = plan->kv_dtype;
+    g.rows = rows;
+    g.err = err;
+    g.stamp = plan->stamp;
+    if (mla::launch_gather(g, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    mla::PrefixParams p{};
+    p.map_k = plan->map_k;
+    p.map_v = plan->map_v;
+    p.items = reinterpret_cast<const PrefixItem*>(ws + plan->off_items);
+    p.pairs = reinterpret_cast<const CtaItems*>(ws + plan->off_pairs);
+    p.q = q;
+    p.q_fp8 = plan->q_dtype == MLA_DTYPE_FP8_E4M3 ? 1 : 0;
+    p.q_scale = p.q_fp8 ? q_scale : nullptr;
+    p.kv_scale = plan->kv_dtype == MLA_DTYPE_FP8_E4M3 ? kv_scale : nullptr;
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    p.err = err;
+    p.stamp = plan->stamp;
+    if (mla::launch_prefix(p, plan->num_pairs, stream) != cudaSuccess) return MLA_ERR_CUDA;
+  }
+  mla::MeetParams m{};
+  m.jobs = reinterpret_cast<const MeetJob*>(ws + plan->off_jobs);
+  m.tokens = static_cast<int64_t>(plan->bs) * plan->q_len;
+  m.own_o = reinterpret_cast<const float*>(ws + plan->off_own + plan->own->off_part_o);
+  m.own_lse = reinterpret_cast<const float*>(ws + plan->off_own + plan->own->off_part_lse);
+  m.own_rows = plan->own->rows;
+  m.prefix_o = part_o;
+  m.prefix_lse = part_lse;
+  m.out = static_cast<uint16_t*>(out);
+  m.lse = lse;
+  m.err = err;
+  m.stamp = plan->stamp;
+  return mla::launch_meet(m, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+mla_status mla_shared_check(const mla_shared* plan, void* workspace, mla_stream_t stream_) {
+  if (plan == nullptr || workspace == nullptr) return MLA_ERR_INVALID_ARG;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const mla_status own =
+      mla_decode_check(plan->own, static_cast<uint8_t*>(workspace) + plan->off_own, stream_);
+  int32_t word = 0;
+  if (cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, stream) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  if (word == 0) return own;
+  if (cudaMemsetAsync(workspace, 0, sizeof(word), stream) != cudaSuccess) return MLA_ERR_CUDA;
+  if (word & mla::kErrStale) {
+    if (plan->uploaded_ws == workspace) plan->uploaded_ws = nullptr;
+    return MLA_ERR_WORKSPACE;
+  }
+  if (own != MLA_OK) return own;
+  return (word & mla::kErrTimeout) ? MLA_ERR_DEVICE_TIMEOUT : MLA_ERR_INVALID_ARG;
+}
+
+}  // extern "C"

@@ -670,6 +670,21 @@ __device__ __forceinline__ void q_fetch(const Stage1Params& p, Misc* ms, uint8_t
             L::kQSrcBytes, bar);
 }
 
+// The scale of the two terms, and 1 over it: the largest magnitude at e4m3's
+// largest value, or (exact_q) the next power of two.  With that, q / s_hi keeps
+// q's 8 bits: q_hi takes four, and what it leaves is at most 8 units of the last
+// place, which q_lo holds exactly (down to 2^-13 s_hi).
+__device__ __forceinline__ void q_term_scale(const Stage1Params& p, float amax, float& s_hi,
+                                             float& inv_hi) {
+  s_hi = amax / 448.0f;
+  inv_hi = 448.0f / amax;
+  if (p.exact_q) {
+    const uint32_t b = __float_as_uint(s_hi);
+    s_hi = __uint_as_float((b & 0x007fffffu) != 0 ? (b & 0x7f800000u) + 0x00800000u : b);
+    inv_hi = 1.0f / s_hi;
+  }
+}
+
 // Eight bf16 q values (vector `vid` of the [rows][576] q) -> their e4m3
 // q_hi = rn(q / s_hi) and q_lo = rn(16 (q - q_hi s_hi) / s_hi) bytes, stored
 // as rows h and rows + h of the K-major, 128-byte-swizzled q operand.
@@ -734,7 +749,8 @@ __device__ __forceinline__ void q_convert(const Stage1Params& p, Misc* ms, const
       for (int w = 0; w < n / 32; ++w) amax = fmaxf(amax, ms->qred[w]);
     }
     amax = fmaxf(amax, 1e-30f);
-    const float s_hi = amax / 448.0f, inv_hi = 448.0f / amax;
+    float s_hi, inv_hi;
+    q_term_scale(p, amax, s_hi, inv_hi);
     for (int v = i; v < kV; v += n)
       q_split_store(src[v], v, s_hi, inv_hi, dst, L::kQAtomBytes, L::kRows);
     const float kvs = (QM == kQBf16KvMx) ? 1.0f : __ldg(p.kv_scale);
@@ -811,7 +827,8 @@ __device__ __forceinline__ void q_convert_mx(const Stage1Params& p, Misc* ms, in
 #pragma unroll
   for (int w = 0; w < kN / 32; ++w) amax = fmaxf(amax, ms->qred[w]);
   amax = fmaxf(amax, 1e-30f);
-  const float s_hi = amax / 448.0f, inv_hi = 448.0f / amax;
+  float s_hi, inv_hi;
+  q_term_scale(p, amax, s_hi, inv_hi);
 #pragma unroll 1
   for (int u = 0; u < kPer; ++u) {
     const int v = i + kN * u;
