@@ -37,36 +37,37 @@ namespace {
 
 constexpr int kThreads = 320;
 constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 bf16 (or 64 keys)
-// even CTA: rotated query dims, probabilities of either half on their way, K ring
-constexpr uint32_t kQrAt = 0, kStageAt = kHalfBytes, kKRingAt = 3 * kHalfBytes;
-constexpr int kKSlots = 10;                        // 128 keys x 64 dims each
-constexpr uint32_t kSumAt = kKRingAt + kKSlots * kHalfBytes;      // the second half's sums
+// even CTA: probabilities of two tiles (each of two halves) on their way, rotated
+// query dims, K ring; odd CTA: the probabilities received, V ring
+constexpr uint32_t kPAt = 0, kQrAt = 4 * kHalfBytes, kKRingAt = 5 * kHalfBytes;
+constexpr int kKSlots = 9;                         // 128 keys x 64 dims each
 constexpr int kChunks = kQkDim / 64;
-// odd CTA: probabilities of either half, V ring
-constexpr uint32_t kPAt = 0, kVRingAt = 2 * kHalfBytes;
-constexpr int kVSlots = 6;                         // 64 keys x 256 dims each
+constexpr uint32_t kVRingAt = 4 * kHalfBytes;
+constexpr int kVSlots = 5;                         // 64 keys x 256 dims each
 constexpr uint32_t kVBytes = 64 * 256 * 2;
 constexpr uint32_t kSmemBytes = kVRingAt + kVSlots * kVBytes;
-static_assert(kSumAt + kSpRows * 4 <= kSmemBytes, "the even CTA's arrays fit");
+static_assert(kKRingAt + kKSlots * kHalfBytes <= kSmemBytes, "the even CTA's arrays fit");
 // even CTA: queries' dims 0-511, then two buffers of scores; odd CTA: the output
 constexpr uint32_t kColQ = 0, kColS = 256, kColO = 0;
-// A row's maximum is kept until a score exceeds it by a factor of 2^8.
+// A row's maximum, rounded up to a power of two, is kept until a score exceeds it
+// by a factor of 2^8.
 constexpr float kLag = 8.0f;
 
 struct Misc {
   uint64_t full[kKSlots], empty[kKSlots];          // K or V ring
   uint64_t q_ready;                                // even: the item's queries are in place
   uint64_t s_full[2], s_empty[2];                  // even: score buffers
-  uint64_t p_empty[2];                             // even: the odd CTA's P halves are free
-  uint64_t landed[2];                              // even: a half's copy has arrived there
+  uint64_t p_empty[4];                             // even: P buffers (tile & 1, half) are free
   uint64_t sum_full;                               // even: the second half's sums
-  uint64_t p_full[2];                              // odd: P halves (with half 0: factors)
-  uint64_t o_ready, pv_done;                       // odd: output rescaled; a tile's PV through
+  uint64_t p_full[4];                              // odd: P buffers (with half 0: factors)
+  uint64_t o_ready[2], pv_done;                    // odd: output rescaled (tiles in turn, as the
+                                                   // warps may be a tile ahead); a tile's PV through
   uint64_t fin_full[2];                            // odd: 1 / sums of an item
   uint64_t drain;
   uint32_t tmem;
-  alignas(16) float factor[kSpRows];               // odd: received; even: being sent
-  float fin[2][kSpRows];                           // the same, of items in turn
+  // of tiles, and of items, in turn; odd CTA: received, even CTA: being sent
+  alignas(16) uint8_t factor[2][kSpRows];          // rows are to be scaled by 2^-factor
+  alignas(16) float fin[2][kSpRows];               // 1 / sums (even CTA: first the half sums)
 };
 static_assert(sizeof(Misc) + kSmemBytes + 1024 <= 232448, "fits a CTA's shared memory");
 
@@ -182,7 +183,7 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
 }
 
 constexpr uint32_t kPHalfBytes = kHalfBytes;
-constexpr uint32_t kFactorBytes = kSpRows * 4;
+constexpr uint32_t kFactorBytes = kSpRows, kFinBytes = kSpRows * 4;
 
 __device__ void run_values(const PrefixParams& p, Misc* ms, uint32_t smem, uint32_t tmem, int it0,
                            int it1) {
@@ -196,16 +197,14 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
     for (int j = 0; j < tiles; ++j, ++tile) {
-      if (!wait(&ms->o_ready, tile & 1)) return;
+      if (!wait(&ms->o_ready[tile & 1], (tile >> 1) & 1)) return;
       for (int h = 0; h < 2; ++h) {
-        if (!wait(&ms->p_full[h], tile & 1)) return;
-        // word of it to the sender; and the next one's bytes, which cannot come
-        // before this half is given back
-        if (elect_one()) {
-          mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->landed[h]), 0));
-          mbar_arrive_expect_tx(smem_u32(&ms->p_full[h]), kPHalfBytes + (h == 0 ? kFactorBytes : 0));
-        }
-        const uint64_t a = pd + ((h * kHalfBytes) >> 4);
+        const uint32_t buf = 2 * (tile & 1) + h;
+        if (!wait(&ms->p_full[buf], (tile >> 1) & 1)) return;
+        // (the next one's bytes, which cannot come before this buffer is given back)
+        if (elect_one())
+          mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + (h == 0 ? kFactorBytes : 0));
+        const uint64_t a = pd + ((buf * kHalfBytes) >> 4);
         for (int half = 0; half < 2; ++half, ++n) {
           const uint32_t s = n % kVSlots;
           if (!wait(&ms->full[s], (n / kVSlots) & 1)) return;
@@ -217,7 +216,7 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
               umma_f16(tmem + kColO + 256 * half, a + 2 * kk, vb + 128 * kk, idesc,
                        (j | h | kk) != 0);
             tc_commit(smem_u32(&ms->empty[s]));
-            if (half == 1) commit_to_even(&ms->p_empty[h]);
+            if (half == 1) commit_to_even(&ms->p_empty[buf]);
             if (half == 1 && h == 1) tc_commit(smem_u32(&ms->pv_done));
           }
           __syncwarp();
@@ -238,13 +237,9 @@ __device__ __forceinline__ void st_shared_16(uint32_t at, uint32_t a, uint32_t b
                : "memory");
 }
 
-__device__ __forceinline__ void st_shared_f32(uint32_t at, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
-__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
+// 2^-drop (0 where that is no normal number).
+__device__ __forceinline__ float factor_of(uint32_t drop) {
+  return drop < 127 ? __uint_as_float((127u - drop) << 23) : 0.0f;
 }
 
 // 64 dims of a query row (zeros past the item's rows) as 32 bf16 pairs.
@@ -283,9 +278,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
   const int row = warp * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;      // TMEM lane 32 warp
   const uint32_t tq = tmem + lanes + kColQ, ts = tmem + lanes + kColS;
-  const uint32_t stage = smem + kStageAt + h * kHalfBytes + row * 128, turn = row & 7;
-  const uint32_t peer_p = dsmem_addr(smem + kPAt + h * kHalfBytes, 1);
-  const uint32_t peer_full = dsmem_addr(smem_u32(&ms->p_full[h]), 1);
+  const uint32_t turn = row & 7;
   const bool sender = warp == 0 && lane == 0;
   const float qs = p.q_scale != nullptr ? *p.q_scale : 1.0f;
   const float ks = p.kv_scale != nullptr ? *p.kv_scale : 1.0f;
@@ -358,11 +351,12 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
         }
       }
       const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
-      float f = 1.0f;
+      uint32_t drop = 0;
       if (top > m + kLag) {
-        f = ex2(m - top);                                // (the first tile: 0)
-        m = top;
-        l *= f;
+        const float nm = ceilf(top), d = nm - m;         // (the first tile: infinite)
+        drop = d < 200.0f ? static_cast<uint32_t>(d) : 200u;
+        m = nm;
+        l *= factor_of(drop);
       }
       // a row that has seen no score above -inf keeps p = 2^(-inf) = 0
       const float off = m == -INFINITY ? 0.0f : -m;
@@ -385,52 +379,55 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
       float u0, u1;
       unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
       l += u0 + u1;
-      // the staging buffer is free once its last copy has landed
-      if (sender && ok && tile > 0)
-        ok = mbar_wait_cluster<true>(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err, kErrSoftmax);
+      // both sides' buffers are free once the tile before the last is through PV
+      const uint32_t buf = 2 * b + h, stage = smem + kPAt + buf * kHalfBytes;
+      if (sender && ok && tile >= 2)
+        ok = mbar_wait_cluster<true>(smem_u32(&ms->p_empty[buf]), ((tile >> 1) - 1) & 1, p.err,
+                                     kErrSoftmax);
       if (named_bar_any(1 + h, 128, !ok)) return;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        st_shared_16(stage + ((i ^ turn) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
+        st_shared_16(stage + row * 128 + ((i ^ turn) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
                      pk[4 * i + 3]);
-      if (h == 0) ms->factor[row] = f;
+      if (h == 0) ms->factor[b][row] = static_cast<uint8_t>(drop);
       fence_proxy_async_smem();
       named_bar_sync(1 + h, 128);
       if (sender) {
-        ok = tile == 0 || mbar_wait_cluster<true>(smem_u32(&ms->p_empty[h]), (tile - 1) & 1, p.err,
-                                                  kErrSoftmax);
-        if (ok) {
-          bulk_to_peer(peer_p, smem + kStageAt + h * kHalfBytes, kPHalfBytes, peer_full);
-          if (h == 0)
-            bulk_to_peer(dsmem_addr(smem_u32(ms->factor), 1), smem_u32(ms->factor), kFactorBytes,
-                         peer_full);
-        }
+        const uint32_t full = dsmem_addr(smem_u32(&ms->p_full[buf]), 1);
+        bulk_to_peer(dsmem_addr(stage, 1), stage, kPHalfBytes, full);
+        if (h == 0)
+          bulk_to_peer(dsmem_addr(smem_u32(ms->factor[b]), 1), smem_u32(ms->factor[b]), kFactorBytes,
+                       full);
       }
       __syncwarp();
     }
-    // sums of both halves; 1 / sum (times the values' scale) to the odd CTA
+    // Sums of both halves; 1 / sum (times the values' scale) to the odd CTA.  The
+    // buffers on both sides are those of the item before the last: its output is
+    // written before the last item's PV begins, and that is through here.
     const uint32_t turn_of = (it - it0) & 1;
+    if (sender && ok && tile >= 2)
+      ok = mbar_wait_cluster<true>(smem_u32(&ms->p_empty[2 * (tile & 1) + h]),
+                                   ((tile - 2) >> 1) & 1, p.err, kErrSoftmax);
+    if (named_bar_any(1 + h, 128, !ok)) return;
     if (h == 1) {
-      st_shared_f32(smem + kSumAt + 4 * row, l);
+      ms->fin[turn_of][row] = l;
       arrive_warp(&ms->sum_full, lane);
     } else {
       ok = all_waited(ok && mbar_wait_poll(smem_u32(&ms->sum_full), turn_of, p.err, kErrSoftmax));
-      l += ld_shared_f32(smem + kSumAt + 4 * row);
+      l += ms->fin[turn_of][row];
       if (row < w.rows)
         p.part_lse[static_cast<int64_t>(w.slot) * kSpRows + row] = l == 0.0f ? -INFINITY : m + __log2f(l);
-      // (the copy that last read this buffer was of the item before the last,
-      // whose output was written before the last item's first PV)
       ms->fin[turn_of][row] = l == 0.0f ? 0.0f : ks / l;
       fence_proxy_async_smem();
       if (named_bar_any(1, 128, !ok)) return;
       if (sender)
         bulk_to_peer(dsmem_addr(smem_u32(ms->fin[turn_of]), 1), smem_u32(ms->fin[turn_of]),
-                     kFactorBytes, dsmem_addr(smem_u32(&ms->fin_full[turn_of]), 1));
+                     kFinBytes, dsmem_addr(smem_u32(&ms->fin_full[turn_of]), 1));
     }
   }
   // what was sent is there before either CTA goes
-  if (sender && tile > 0)
-    mbar_wait_cluster<true>(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err, kErrSoftmax);
+  for (uint32_t k = tile > 2 ? tile - 2 : 0; sender && k < tile; ++k)
+    mbar_wait_cluster<true>(smem_u32(&ms->p_empty[2 * (k & 1) + h]), (k >> 1) & 1, p.err, kErrSoftmax);
 }
 
 // --------------------------------------------------------------- output
@@ -444,10 +441,12 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
     for (int j = 0; j < tiles; ++j, ++tile) {
-      if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[0]), tile & 1, p.err, kErrDrain)))
+      if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[2 * (tile & 1)]), (tile >> 1) & 1, p.err,
+                                     kErrDrain)))
         return false;
-      const float f = ms->factor[row];
-      if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+      const uint32_t drop = ms->factor[tile & 1][row];
+      if (j > 0 && __any_sync(0xffffffffu, drop != 0)) {
+        const float f = factor_of(drop);
         if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done), (tile - 1) & 1, p.err, kErrDrain)))
           return false;
         tc_fence_after();
@@ -463,10 +462,13 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
         tmem_wait_st();
         tc_fence_before();
       }
-      arrive_warp(&ms->o_ready, lane);
+      arrive_warp(&ms->o_ready[tile & 1], lane);
     }
     const uint32_t turn_of = (it - it0) & 1;
-    if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done), (tile - 1) & 1, p.err, kErrDrain)) ||
+    // (P of the last tile came when the tile two before it was through: two
+    // phases may be left, of which a wait for the last alone would see neither)
+    if (!all_waited((tile < 2 || mbar_wait_poll(smem_u32(&ms->pv_done), tile & 1, p.err, kErrDrain)) &&
+                    mbar_wait_poll(smem_u32(&ms->pv_done), (tile - 1) & 1, p.err, kErrDrain)) ||
         !all_waited(mbar_wait_poll(smem_u32(&ms->fin_full[turn_of]), ((it - it0) >> 1) & 1, p.err,
                                    kErrDrain)))
       return false;
@@ -489,7 +491,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
     }
     tc_fence_before();
     // the odd CTA's thread re-arms the buffer for the item after the next
-    if (half == 0 && row == 0) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[turn_of]), kFactorBytes);
+    if (half == 0 && row == 0) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[turn_of]), kFinBytes);
   }
   return true;
 }
@@ -508,24 +510,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(smem_u32(&ms->empty[i]), 1);
     }
     mbar_init(smem_u32(&ms->q_ready), 8);
-    mbar_init(smem_u32(&ms->o_ready), 8);
     mbar_init(smem_u32(&ms->sum_full), 4);
     mbar_init(smem_u32(&ms->pv_done), 1);
     mbar_init(smem_u32(&ms->drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->s_full[i]), 1);
       mbar_init(smem_u32(&ms->s_empty[i]), 8);
-      mbar_init(smem_u32(&ms->p_empty[i]), 1);
-      mbar_init(smem_u32(&ms->p_full[i]), 1);
-      mbar_init(smem_u32(&ms->landed[i]), 1);
+      mbar_init(smem_u32(&ms->o_ready[i]), 8);
+      for (int b = i; b < 4; b += 2) {
+        mbar_init(smem_u32(&ms->p_empty[b]), 1);
+        mbar_init(smem_u32(&ms->p_full[b]), 1);
+      }
       mbar_init(smem_u32(&ms->fin_full[i]), 1);
     }
     fence_mbar_init();
     if (rank == 1) {
-      mbar_arrive_expect_tx(smem_u32(&ms->p_full[0]), kPHalfBytes + kFactorBytes);
-      mbar_arrive_expect_tx(smem_u32(&ms->p_full[1]), kPHalfBytes);
-      mbar_arrive_expect_tx(smem_u32(&ms->fin_full[0]), kFactorBytes);
-      mbar_arrive_expect_tx(smem_u32(&ms->fin_full[1]), kFactorBytes);
+      for (int b = 0; b < 4; ++b)
+        mbar_arrive_expect_tx(smem_u32(&ms->p_full[b]), kPHalfBytes + (b & 1 ? 0 : kFactorBytes));
+      mbar_arrive_expect_tx(smem_u32(&ms->fin_full[0]), kFinBytes);
+      mbar_arrive_expect_tx(smem_u32(&ms->fin_full[1]), kFinBytes);
     }
   }
   if (warp == 9) {
