@@ -23,10 +23,16 @@
 // sums that divide the output are of the unrounded ones.  Scores, sums, maxima
 // and outputs are fp32.
 //
-// Roles (320 threads): warps 0-3 and 4-7 of the even CTA hold the softmax, a
+// Roles (352 threads): warps 0-3 and 4-7 of the even CTA hold the softmax, a
 // thread per row and half of a tile's keys (both see the tile's maximum, so that
 // they keep the same m); of the odd CTA the output's dims 0-255 and 256-511.
-// Warp 8 loads, warp 9 issues the products.
+// Warp 8 (and in the even CTA warp 10) loads, warp 9 issues the products.
+//
+// What those single threads do for each piece counts: a wait that is over takes
+// 100 cycles, announcing bytes 25, issuing a copy 64.  With a loop over 9 chunks a
+// tile that waits for each, a tile took 4,900 cycles.  So key chunks are loaded by
+// two warps and waited for by threes, and a wait is looked at before the products
+// ahead of it are issued.
 
 #include <cuda_fp16.h>
 
@@ -35,26 +41,26 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 bf16 (or 64 keys)
 // even CTA: probabilities of two tiles (each of two halves) on their way, rotated
 // query dims, K ring; odd CTA: the probabilities received, V ring
 constexpr uint32_t kPAt = 0, kQrAt = 4 * kHalfBytes, kKRingAt = 5 * kHalfBytes;
-constexpr int kKSlots = 9;                         // 128 keys x 64 dims each
-constexpr int kChunks = kQkDim / 64;
+constexpr int kChunks = kQkDim / 64;               // of 128 keys x 64 dims: a tile fills the K ring
 constexpr uint32_t kVRingAt = 4 * kHalfBytes;
 constexpr int kVSlots = 5;                         // 64 keys x 256 dims each
 constexpr uint32_t kVBytes = 64 * 256 * 2;
 constexpr uint32_t kSmemBytes = kVRingAt + kVSlots * kVBytes;
-static_assert(kKRingAt + kKSlots * kHalfBytes <= kSmemBytes, "the even CTA's arrays fit");
+static_assert(kKRingAt + kChunks * kHalfBytes <= kSmemBytes, "the even CTA's arrays fit");
 // even CTA: queries' dims 0-511, then two buffers of scores; odd CTA: the output
 constexpr uint32_t kColQ = 0, kColS = 256, kColO = 0;
-// A row's maximum, rounded up to a power of two, is kept until a score exceeds it
-// by a factor of 2^8.
+// A row's maximum is kept until a score exceeds it by a factor of 2^8, and then
+// moves by a power of two, so that a byte tells the factor.
 constexpr float kLag = 8.0f;
 
 struct Misc {
-  uint64_t full[kKSlots], empty[kKSlots];          // K or V ring
+  uint64_t full[kVSlots], empty[kChunks];          // rings: even: three chunks' bytes, a chunk
+                                                   // is free; odd: a slot's
   uint64_t q_ready;                                // even: the item's queries are in place
   uint64_t s_full[2], s_empty[2];                  // even: score buffers
   uint64_t p_empty[4];                             // even: P buffers (tile & 1, half) are free
@@ -81,6 +87,11 @@ __device__ __forceinline__ PrefixItem load_item(const PrefixItem* p) {
 __device__ __forceinline__ int tiles_of(const PrefixItem& w) {
   return (w.keys + kSpTile - 1) / kSpTile;
 }
+// About a millisecond, in which every copy under way lands (a wait gave up).
+__device__ __forceinline__ void linger() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000) {}
+}
 __device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
   __syncwarp();
@@ -106,40 +117,68 @@ __device__ __forceinline__ void commit_to_even(uint64_t* bar) {
 }
 
 // ---------------------------------------------------------------- loads
-template <bool kEven>
-__device__ void run_loads(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1) {
-  constexpr int kSlots = kEven ? kKSlots : kVSlots;
-  constexpr uint32_t kBytes = kEven ? kHalfBytes : kVBytes;
-  uint32_t n = 0;
+//
+// Even CTA: chunks kFirst .. kLast - 1 of every key tile.  Chunks 3 u .. 3 u + 2 are
+// counted on one barrier, announced by who loads the first of them.
+template <int kFirst, int kLast>
+__device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1) {
+  uint32_t tile = 0;
   bool ok = true;
   const uint64_t keep = l2_policy_evict_normal();
+  const CUtensorMap* map = &p.map_k;
   fence_proxy_async();               // (the rows were written by another kernel)
-  auto load = [&](const CUtensorMap* map, int key, int panel) {
-    const uint32_t s = n % kSlots, lap = n / kSlots;
-    if (lap > 0 && !mbar_wait_poll(smem_u32(&ms->empty[s]), (lap - 1) & 1, p.err, kErrProducer)) {
-      ok = false;
-      return;
+  for (int it = it0; it < it1 && ok; ++it) {
+    const PrefixItem w = load_item(p.items + it);
+    const int tiles = tiles_of(w);
+    for (int j = 0; j < tiles && ok; ++j, ++tile) {
+      const int key = w.key0 + j * kSpTile;
+      const uint32_t parity = (tile - 1) & 1;
+      bool ready = tile == 0 || mbar_test(smem_u32(&ms->empty[kFirst]), parity);
+#pragma unroll
+      for (int ch = kFirst; ch < kLast; ++ch) {
+        if (!ready && !mbar_wait_poll(smem_u32(&ms->empty[ch]), parity, p.err, kErrProducer)) {
+          ok = false;
+          break;
+        }
+        if (ch + 1 < kLast) ready = tile == 0 || mbar_test(smem_u32(&ms->empty[ch + 1]), parity);
+        const uint32_t bar = smem_u32(&ms->full[ch / 3]);
+        if (ch % 3 == 0) mbar_arrive_expect_tx(bar, 3 * kHalfBytes);
+        tma_load_3d(ring + ch * kHalfBytes, map, bar, 0, key, ch, keep);
+      }
     }
-    mbar_arrive_expect_tx(smem_u32(&ms->full[s]), kBytes);
-    tma_load_3d(ring + s * kBytes, map, smem_u32(&ms->full[s]), 0, key, panel, keep);
-    ++n;
-  };
+  }
+  if (!ok) linger();                 // no copy may land after the CTA has gone
+}
+
+// Odd CTA: slots of 64 keys and 256 dims.
+__device__ void load_values(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1) {
+  uint32_t s = 0, parity = 1;        // (of the first lap: nothing to wait for)
+  bool ok = true;
+  const uint64_t keep = l2_policy_evict_normal();
+  const CUtensorMap* map = &p.map_v;
+  fence_proxy_async();
   for (int it = it0; it < it1 && ok; ++it) {
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
     for (int j = 0; j < tiles && ok; ++j) {
       const int key = w.key0 + j * kSpTile;
-      if constexpr (kEven) {
-        for (int ch = 0; ch < kChunks && ok; ++ch) load(&p.map_k, key, ch);
-      } else {
-        for (int u = 0; u < 4 && ok; ++u) load(&p.map_v, key + 64 * (u >> 1), 4 * (u & 1));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!mbar_wait_poll(smem_u32(&ms->empty[s]), parity, p.err, kErrProducer)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&ms->full[s]);
+        mbar_arrive_expect_tx(bar, kVBytes);
+        tma_load_3d(ring + s * kVBytes, map, bar, 0, key + 64 * (u >> 1), 4 * (u & 1), keep);
+        if (++s == kVSlots) {
+          s = 0;
+          parity ^= 1;
+        }
       }
     }
   }
-  // a wait gave up: no copy may land after the CTA has gone
-  if (!ok)
-    for (uint32_t k = n > kSlots ? n - kSlots : 0; k < n; ++k)
-      mbar_wait_poll(smem_u32(&ms->full[k % kSlots]), (k / kSlots) & 1, p.err, kErrProducer);
+  if (!ok) linger();
 }
 
 // ------------------------------------------------------------- products
@@ -148,33 +187,38 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
   constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, 128);
   const uint64_t qd = smem_desc(smem + kQrAt, 16, 1024, kSwizzle128B);
   const uint64_t kd = smem_desc(smem + kKRingAt, 16, 1024, kSwizzle128B);
-  uint32_t n = 0, tile = 0;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
+  uint32_t tile = 0;
+  auto wait = [&](bool ready, uint64_t* bar, uint32_t parity) {
+    return all_waited(ready) ||
+           all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
   };
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
-    if (!wait(&ms->q_ready, (it - it0) & 1)) return;
+    if (!wait(false, &ms->q_ready, (it - it0) & 1)) return;
     for (int j = 0; j < tiles; ++j, ++tile) {
-      const uint32_t b = tile & 1;
-      if (tile >= 2 && !wait(&ms->s_empty[b], ((tile >> 1) - 1) & 1)) return;
+      const uint32_t b = tile & 1, parity = tile & 1;
+      bool ready = mbar_test(smem_u32(&ms->full[0]), parity);
+      if (tile >= 2 && !wait(false, &ms->s_empty[b], ((tile >> 1) - 1) & 1)) return;
       const uint32_t d = tmem + kColS + 128 * b;
-      for (int ch = 0; ch < kChunks; ++ch, ++n) {
-        const uint32_t s = n % kKSlots;
-        if (!wait(&ms->full[s], (n / kKSlots) & 1)) return;
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        if (!wait(ready, &ms->full[u], parity)) return;
+        if (u < 2) ready = mbar_test(smem_u32(&ms->full[u + 1]), parity);
         tc_fence_after();
-        const uint64_t kb = kd + ((s * kHalfBytes) >> 4);
         if (elect_one()) {
-          if (ch < 8) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ta(d, tmem + kColQ + 32 * ch + 8 * kk, kb + 2 * kk, idesc, (ch | kk) != 0);
-          } else {
+          for (int ch = 3 * u; ch < 3 * u + 3; ++ch) {
+            const uint64_t kb = kd + ((ch * kHalfBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_f16(d, qd + 2 * kk, kb + 2 * kk, idesc, 1);
+            for (int kk = 0; kk < 4; ++kk) {
+              if (ch < 8)
+                umma_f16_ta(d, tmem + kColQ + 32 * ch + 8 * kk, kb + 2 * kk, idesc, (ch | kk) != 0);
+              else
+                umma_f16(d, qd + 2 * kk, kb + 2 * kk, idesc, 1);
+            }
+            tc_commit(smem_u32(&ms->empty[ch]));
           }
-          tc_commit(smem_u32(&ms->empty[s]));
-          if (ch == kChunks - 1) tc_commit(smem_u32(&ms->s_full[b]));
+          if (u == 2) tc_commit(smem_u32(&ms->s_full[b]));
         }
         __syncwarp();
       }
@@ -190,32 +234,44 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
   constexpr uint32_t idesc = make_idesc(1, 1, false, true, 128, 256);
   const uint64_t pd = smem_desc(smem + kPAt, 16, 1024, kSwizzle128B);
   const uint64_t vd = smem_desc(smem + kVRingAt, 64 * 128, 1024, kSwizzle128B);
-  uint32_t n = 0, tile = 0;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
+  uint32_t s = 0, lap = 0, tile = 0;
+  auto wait = [&](bool ready, uint64_t* bar, uint32_t parity) {
+    return all_waited(ready) ||
+           all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
   };
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
     for (int j = 0; j < tiles; ++j, ++tile) {
-      if (!wait(&ms->o_ready[tile & 1], (tile >> 1) & 1)) return;
+      const uint32_t turn = (tile >> 1) & 1;
+      bool p_ready = mbar_test(smem_u32(&ms->p_full[2 * (tile & 1)]), turn);
+      if (!wait(false, &ms->o_ready[tile & 1], turn)) return;
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t buf = 2 * (tile & 1) + h;
-        if (!wait(&ms->p_full[buf], (tile >> 1) & 1)) return;
+        bool v_ready = mbar_test(smem_u32(&ms->full[s]), lap);
+        if (!wait(p_ready, &ms->p_full[buf], turn)) return;
         // (the next one's bytes, which cannot come before this buffer is given back)
         if (elect_one())
           mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + (h == 0 ? kFactorBytes : 0));
         const uint64_t a = pd + ((buf * kHalfBytes) >> 4);
-        for (int half = 0; half < 2; ++half, ++n) {
-          const uint32_t s = n % kVSlots;
-          if (!wait(&ms->full[s], (n / kVSlots) & 1)) return;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(v_ready, &ms->full[s], lap)) return;
+          const uint32_t at = s;
+          if (++s == kVSlots) {
+            s = 0;
+            lap ^= 1;
+          }
+          if (half == 0) v_ready = mbar_test(smem_u32(&ms->full[s]), lap);
+          if (half == 1 && h == 0) p_ready = mbar_test(smem_u32(&ms->p_full[buf + 1]), turn);
           tc_fence_after();
-          const uint64_t vb = vd + ((s * kVBytes) >> 4);
+          const uint64_t vb = vd + ((at * kVBytes) >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_f16(tmem + kColO + 256 * half, a + 2 * kk, vb + 128 * kk, idesc,
                        (j | h | kk) != 0);
-            tc_commit(smem_u32(&ms->empty[s]));
+            tc_commit(smem_u32(&ms->empty[at]));
             if (half == 1) commit_to_even(&ms->p_empty[buf]);
             if (half == 1 && h == 1) tc_commit(smem_u32(&ms->pv_done));
           }
@@ -353,9 +409,9 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
       const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
       uint32_t drop = 0;
       if (top > m + kLag) {
-        const float nm = ceilf(top), d = nm - m;         // (the first tile: infinite)
+        const float d = ceilf(top - m);                  // (the first tile: infinite)
         drop = d < 200.0f ? static_cast<uint32_t>(d) : 200u;
-        m = nm;
+        m = m == -INFINITY ? top : m + d;
         l *= factor_of(drop);
       }
       // a row that has seen no score above -inf keeps p = 2^(-inf) = 0
@@ -505,10 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKSlots; ++i) {
-      mbar_init(smem_u32(&ms->full[i]), 1);
-      mbar_init(smem_u32(&ms->empty[i]), 1);
-    }
+    for (int i = 0; i < kVSlots; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
+    for (int i = 0; i < kChunks; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
     mbar_init(smem_u32(&ms->q_ready), 8);
     mbar_init(smem_u32(&ms->sum_full), 4);
     mbar_init(smem_u32(&ms->pv_done), 1);
@@ -557,17 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (rank == 0) {
       run_softmax(p, ms, smem, tmem, first, last, warp >> 2, warp & 3, lane);
     } else if (!run_output(p, ms, tmem, first, last, warp >> 2, warp & 3, lane)) {
-      // copies on their way land before this CTA goes
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000) {}
+      linger();                      // copies on their way land before this CTA goes
     }
   } else if (warp == 8) {
     if (lane == 0) {
       if (rank == 0)
-        run_loads<true>(p, ms, smem + kKRingAt, first, last);
+        load_keys<0, 5>(p, ms, smem + kKRingAt, first, last);
       else
-        run_loads<false>(p, ms, smem + kVRingAt, first, last);
+        load_values(p, ms, smem + kVRingAt, first, last);
     }
+  } else if (warp == 10) {
+    if (lane == 0 && rank == 0) load_keys<5, kChunks>(p, ms, smem + kKRingAt, first, last);
   } else {
     if (rank == 0)
       run_scores(p, ms, smem, tmem, first, last);
