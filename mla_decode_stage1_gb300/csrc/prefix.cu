@@ -32,7 +32,8 @@
 // 100 cycles, announcing bytes 25, issuing a copy 64.  With a loop over 9 chunks a
 // tile that waits for each, a tile took 4,900 cycles.  So key chunks are loaded by
 // two warps and waited for by threes, and a wait is looked at before the products
-// ahead of it are issued.
+// ahead of it are issued.  A chunk takes 1,800 to 2,500 cycles to come from L2:
+// eleven stand in the ring.
 
 #include <cuda_fp16.h>
 
@@ -43,15 +44,17 @@ namespace {
 
 constexpr int kThreads = 352;
 constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 bf16 (or 64 keys)
-// even CTA: probabilities of two tiles (each of two halves) on their way, rotated
-// query dims, K ring; odd CTA: the probabilities received, V ring
-constexpr uint32_t kPAt = 0, kQrAt = 4 * kHalfBytes, kKRingAt = 5 * kHalfBytes;
-constexpr int kChunks = kQkDim / 64;               // of 128 keys x 64 dims: a tile fills the K ring
-constexpr uint32_t kVRingAt = 4 * kHalfBytes;
+// even CTA: probabilities of either half of a tile on their way, rotated query
+// dims, K ring; odd CTA: the probabilities of two tiles received, V ring
+constexpr uint32_t kStageAt = 0, kQrAt = 2 * kHalfBytes, kKRingAt = 3 * kHalfBytes;
+constexpr int kChunks = kQkDim / 64;               // of a tile: 128 keys x 64 dims
+constexpr int kGroup = 3, kGroups = 4;             // chunks waited for together; groups under way
+constexpr uint32_t kKSlots = 11;
+constexpr uint32_t kPAt = 0, kVRingAt = 4 * kHalfBytes;
 constexpr int kVSlots = 5;                         // 64 keys x 256 dims each
 constexpr uint32_t kVBytes = 64 * 256 * 2;
 constexpr uint32_t kSmemBytes = kVRingAt + kVSlots * kVBytes;
-static_assert(kKRingAt + kChunks * kHalfBytes <= kSmemBytes, "the even CTA's arrays fit");
+static_assert(kKRingAt + kKSlots * kHalfBytes <= kSmemBytes, "the even CTA's arrays fit");
 // even CTA: queries' dims 0-511, then two buffers of scores; odd CTA: the output
 constexpr uint32_t kColQ = 0, kColS = 256, kColO = 0;
 // A row's maximum is kept until a score exceeds it by a factor of 2^8, and then
@@ -59,20 +62,21 @@ constexpr uint32_t kColQ = 0, kColS = 256, kColO = 0;
 constexpr float kLag = 8.0f;
 
 struct Misc {
-  uint64_t full[kVSlots], empty[kChunks];          // rings: even: three chunks' bytes, a chunk
-                                                   // is free; odd: a slot's
+  uint64_t full[kVSlots], empty[kKSlots];          // rings: even: a group's bytes, a chunk's
+                                                   // slot is free; odd: a slot's
   uint64_t q_ready;                                // even: the item's queries are in place
   uint64_t s_full[2], s_empty[2];                  // even: score buffers
   uint64_t p_empty[4];                             // even: P buffers (tile & 1, half) are free
+  uint64_t landed[2];                              // even: a half's copy has arrived
   uint64_t sum_full;                               // even: the second half's sums
-  uint64_t p_full[4];                              // odd: P buffers (with half 0: factors)
+  uint64_t p_full[4];                              // odd: P buffers and factors
   uint64_t o_ready[2], pv_done;                    // odd: output rescaled (tiles in turn, as the
                                                    // warps may be a tile ahead); a tile's PV through
   uint64_t fin_full[2];                            // odd: 1 / sums of an item
   uint64_t drain;
   uint32_t tmem;
   // of tiles, and of items, in turn; odd CTA: received, even CTA: being sent
-  alignas(16) uint8_t factor[2][kSpRows];          // rows are to be scaled by 2^-factor
+  alignas(16) uint8_t factor[4][kSpRows];          // rows are to be scaled by 2^-factor
   alignas(16) float fin[2][kSpRows];               // 1 / sums (even CTA: first the half sums)
 };
 static_assert(sizeof(Misc) + kSmemBytes + 1024 <= 232448, "fits a CTA's shared memory");
@@ -118,11 +122,11 @@ __device__ __forceinline__ void commit_to_even(uint64_t* bar) {
 
 // ---------------------------------------------------------------- loads
 //
-// Even CTA: chunks kFirst .. kLast - 1 of every key tile.  Chunks 3 u .. 3 u + 2 are
-// counted on one barrier, announced by who loads the first of them.
-template <int kFirst, int kLast>
-__device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1) {
-  uint32_t tile = 0;
+// Even CTA: every other group of three chunks, from `first` (0 or 1) on.
+__device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1, int first) {
+  // group of the whole walk, its barrier; the next chunk's slot and, of the slots
+  // from it on, the parity of the release to wait for
+  uint32_t g = 0, s = 0, parity = 1;
   bool ok = true;
   const uint64_t keep = l2_policy_evict_normal();
   const CUtensorMap* map = &p.map_k;
@@ -130,20 +134,34 @@ __device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it
   for (int it = it0; it < it1 && ok; ++it) {
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
-    for (int j = 0; j < tiles && ok; ++j, ++tile) {
+    for (int j = 0; j < tiles && ok; ++j) {
       const int key = w.key0 + j * kSpTile;
-      const uint32_t parity = (tile - 1) & 1;
-      bool ready = tile == 0 || mbar_test(smem_u32(&ms->empty[kFirst]), parity);
-#pragma unroll
-      for (int ch = kFirst; ch < kLast; ++ch) {
-        if (!ready && !mbar_wait_poll(smem_u32(&ms->empty[ch]), parity, p.err, kErrProducer)) {
-          ok = false;
-          break;
+      for (int ch = 0; ch < kChunks && ok; ch += kGroup, ++g) {
+        if ((g & 1) != static_cast<uint32_t>(first)) {
+          s += kGroup;
+          if (s >= kKSlots) {
+            s -= kKSlots;
+            parity ^= 1;
+          }
+          continue;
         }
-        if (ch + 1 < kLast) ready = tile == 0 || mbar_test(smem_u32(&ms->empty[ch + 1]), parity);
-        const uint32_t bar = smem_u32(&ms->full[ch / 3]);
-        if (ch % 3 == 0) mbar_arrive_expect_tx(bar, 3 * kHalfBytes);
-        tma_load_3d(ring + ch * kHalfBytes, map, bar, 0, key, ch, keep);
+        const uint32_t bar = smem_u32(&ms->full[g % kGroups]);
+        bool ready = mbar_test(smem_u32(&ms->empty[s]), parity);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          if (!ready && !mbar_wait_poll(smem_u32(&ms->empty[s]), parity, p.err, kErrProducer)) {
+            ok = false;
+            break;
+          }
+          if (i == 0) mbar_arrive_expect_tx(bar, kGroup * kHalfBytes);
+          const uint32_t at = s;
+          if (++s == kKSlots) {
+            s = 0;
+            parity ^= 1;
+          }
+          if (i + 1 < kGroup) ready = mbar_test(smem_u32(&ms->empty[s]), parity);
+          tma_load_3d(ring + at * kHalfBytes, map, bar, 0, key, ch + i, keep);
+        }
       }
     }
   }
@@ -187,28 +205,38 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
   constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, 128);
   const uint64_t qd = smem_desc(smem + kQrAt, 16, 1024, kSwizzle128B);
   const uint64_t kd = smem_desc(smem + kKRingAt, 16, 1024, kSwizzle128B);
-  uint32_t tile = 0;
+  uint32_t tile = 0, g = 0, s = 0;
   auto wait = [&](bool ready, uint64_t* bar, uint32_t parity) {
     return all_waited(ready) ||
            all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
+  };
+  auto group_ready = [&](uint32_t g) {
+    return mbar_test(smem_u32(&ms->full[g % kGroups]), (g / kGroups) & 1);
   };
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
     if (!wait(false, &ms->q_ready, (it - it0) & 1)) return;
     for (int j = 0; j < tiles; ++j, ++tile) {
-      const uint32_t b = tile & 1, parity = tile & 1;
-      bool ready = mbar_test(smem_u32(&ms->full[0]), parity);
+      const uint32_t b = tile & 1;
+      bool ready = group_ready(g);
       if (tile >= 2 && !wait(false, &ms->s_empty[b], ((tile >> 1) - 1) & 1)) return;
       const uint32_t d = tmem + kColS + 128 * b;
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        if (!wait(ready, &ms->full[u], parity)) return;
-        if (u < 2) ready = mbar_test(smem_u32(&ms->full[u + 1]), parity);
+      for (int u = 0; u < kChunks / kGroup; ++u, ++g) {
+        if (!wait(ready, &ms->full[g % kGroups], (g / kGroups) & 1)) return;
+        ready = group_ready(g + 1);
         tc_fence_after();
+        uint32_t at[kGroup];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          at[i] = s;
+          s = s + 1 == kKSlots ? 0 : s + 1;
+        }
         if (elect_one()) {
 #pragma unroll
-          for (int ch = 3 * u; ch < 3 * u + 3; ++ch) {
-            const uint64_t kb = kd + ((ch * kHalfBytes) >> 4);
+          for (int i = 0; i < kGroup; ++i) {
+            const int ch = kGroup * u + i;
+            const uint64_t kb = kd + ((at[i] * kHalfBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               if (ch < 8)
@@ -216,9 +244,9 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
               else
                 umma_f16(d, qd + 2 * kk, kb + 2 * kk, idesc, 1);
             }
-            tc_commit(smem_u32(&ms->empty[ch]));
+            tc_commit(smem_u32(&ms->empty[at[i]]));
           }
-          if (u == 2) tc_commit(smem_u32(&ms->s_full[b]));
+          if (u == kChunks / kGroup - 1) tc_commit(smem_u32(&ms->s_full[b]));
         }
         __syncwarp();
       }
@@ -252,7 +280,7 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
         if (!wait(p_ready, &ms->p_full[buf], turn)) return;
         // (the next one's bytes, which cannot come before this buffer is given back)
         if (elect_one())
-          mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + (h == 0 ? kFactorBytes : 0));
+          mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + kFactorBytes);
         const uint64_t a = pd + ((buf * kHalfBytes) >> 4);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -298,19 +326,20 @@ __device__ __forceinline__ float factor_of(uint32_t drop) {
   return drop < 127 ? __uint_as_float((127u - drop) << 23) : 0.0f;
 }
 
-// 64 dims of a query row (zeros past the item's rows) as 32 bf16 pairs.
+// kChunks64 x 64 dims of a query row (zeros past the item's rows) as bf16 pairs,
+// all loads in flight together.
+template <int kChunks64>
 __device__ __forceinline__ void load_query(const PrefixParams& p, int64_t row, bool live, int chunk,
                                            uint32_t* v) {
-  if (!live) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0u;
-  } else if (p.q_fp8) {
+  if (p.q_fp8) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
                                                       row * kQkDim + chunk * 64);
+    uint4 x[4 * kChunks64];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 x = src[i];
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < 4 * kChunks64; ++i) x[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4 * kChunks64; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1))));
@@ -322,8 +351,8 @@ __device__ __forceinline__ void load_query(const PrefixParams& p, int64_t row, b
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
                                                       row * kQkDim + chunk * 64);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 x = src[i];
+    for (int i = 0; i < 8 * kChunks64; ++i) {
+      const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
       v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
     }
   }
@@ -334,7 +363,10 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
   const int row = warp * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;      // TMEM lane 32 warp
   const uint32_t tq = tmem + lanes + kColQ, ts = tmem + lanes + kColS;
-  const uint32_t turn = row & 7;
+  const uint32_t stage = smem + kStageAt + h * kHalfBytes, turn = row & 7;
+  const uint32_t peer_p = dsmem_addr(smem + kPAt + h * kHalfBytes, 1);
+  const uint32_t peer_full = dsmem_addr(smem_u32(&ms->p_full[h]), 1);
+  const uint32_t peer_factor = dsmem_addr(smem_u32(ms->factor[h]), 1);
   const bool sender = warp == 0 && lane == 0;
   const float qs = p.q_scale != nullptr ? *p.q_scale : 1.0f;
   const float ks = p.kv_scale != nullptr ? *p.kv_scale : 1.0f;
@@ -350,19 +382,21 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
     {
       const int64_t q_row = static_cast<int64_t>(w.q_row) + row;
       const bool live = row < w.rows;
-      uint32_t v[32];
+      uint32_t r[32];
+      if (h == 0) load_query<1>(p, q_row, live, 8, r);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        load_query(p, q_row, live, 4 * h + c, v);
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t v[64];
+        load_query<2>(p, q_row, live, 4 * h + c, v);
         __syncwarp();
         tmem_st32(tq + 128 * h + 32 * c, v);
+        tmem_st32(tq + 128 * h + 32 * c + 32, v + 32);
       }
       if (h == 0) {
-        load_query(p, q_row, live, 8, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          st_shared_16(smem + kQrAt + row * 128 + ((i ^ turn) << 4), v[4 * i], v[4 * i + 1],
-                       v[4 * i + 2], v[4 * i + 3]);
+          st_shared_16(smem + kQrAt + row * 128 + ((i ^ turn) << 4), r[4 * i], r[4 * i + 1],
+                       r[4 * i + 2], r[4 * i + 3]);
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -406,6 +440,13 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
           tops[0] = fmaxf(tops[0], __uint_as_float(s[i]));
         }
       }
+      // The staging buffer is free once its last copy has landed, the odd CTA's once
+      // the tile before the last is through PV: looked at here, waited for below.
+      const uint32_t buf = 2 * b + h;
+      const bool landed =
+          tile < 1 || mbar_test_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1);
+      const bool taken =
+          tile < 2 || mbar_test_cluster(smem_u32(&ms->p_empty[buf]), ((tile >> 1) - 1) & 1);
       const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
       uint32_t drop = 0;
       if (top > m + kLag) {
@@ -435,25 +476,23 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
       float u0, u1;
       unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
       l += u0 + u1;
-      // both sides' buffers are free once the tile before the last is through PV
-      const uint32_t buf = 2 * b + h, stage = smem + kPAt + buf * kHalfBytes;
-      if (sender && ok && tile >= 2)
-        ok = mbar_wait_cluster<true>(smem_u32(&ms->p_empty[buf]), ((tile >> 1) - 1) & 1, p.err,
-                                     kErrSoftmax);
-      if (named_bar_any(1 + h, 128, !ok)) return;
+      if (!all_waited(landed))
+        ok = ok && all_waited(mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err,
+                                                kErrSoftmax));
+      if (!all_waited(taken))
+        ok = ok && all_waited(mbar_wait_cluster(smem_u32(&ms->p_empty[buf]), ((tile >> 1) - 1) & 1,
+                                                p.err, kErrSoftmax));
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         st_shared_16(stage + row * 128 + ((i ^ turn) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
                      pk[4 * i + 3]);
-      if (h == 0) ms->factor[b][row] = static_cast<uint8_t>(drop);
+      ms->factor[buf][row] = static_cast<uint8_t>(drop);
       fence_proxy_async_smem();
-      named_bar_sync(1 + h, 128);
+      if (named_bar_any(1 + h, 128, !ok)) return;
       if (sender) {
-        const uint32_t full = dsmem_addr(smem_u32(&ms->p_full[buf]), 1);
-        bulk_to_peer(dsmem_addr(stage, 1), stage, kPHalfBytes, full);
-        if (h == 0)
-          bulk_to_peer(dsmem_addr(smem_u32(ms->factor[b]), 1), smem_u32(ms->factor[b]), kFactorBytes,
-                       full);
+        bulk_to_peer(peer_p + b * 2 * kHalfBytes, stage, kPHalfBytes, peer_full + 16 * b);
+        bulk_to_peer(peer_factor + b * 2 * kSpRows, smem_u32(ms->factor[buf]), kFactorBytes,
+                     peer_full + 16 * b);
       }
       __syncwarp();
     }
@@ -482,8 +521,8 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
     }
   }
   // what was sent is there before either CTA goes
-  for (uint32_t k = tile > 2 ? tile - 2 : 0; sender && k < tile; ++k)
-    mbar_wait_cluster<true>(smem_u32(&ms->p_empty[2 * (k & 1) + h]), (k >> 1) & 1, p.err, kErrSoftmax);
+  if (sender && tile > 0)
+    mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err, kErrSoftmax);
 }
 
 // --------------------------------------------------------------- output
@@ -497,10 +536,11 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
     for (int j = 0; j < tiles; ++j, ++tile) {
-      if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[2 * (tile & 1)]), (tile >> 1) & 1, p.err,
-                                     kErrDrain)))
+      const uint32_t buf = 2 * (tile & 1) + half;
+      if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[buf]), (tile >> 1) & 1, p.err, kErrDrain)))
         return false;
-      const uint32_t drop = ms->factor[tile & 1][row];
+      if (warp == 0 && lane == 0) mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->landed[half]), 0));
+      const uint32_t drop = ms->factor[buf][row];
       if (j > 0 && __any_sync(0xffffffffu, drop != 0)) {
         const float f = factor_of(drop);
         if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done), (tile - 1) & 1, p.err, kErrDrain)))
@@ -562,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kVSlots; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
-    for (int i = 0; i < kChunks; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
+    for (uint32_t i = 0; i < kKSlots; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
     mbar_init(smem_u32(&ms->q_ready), 8);
     mbar_init(smem_u32(&ms->sum_full), 4);
     mbar_init(smem_u32(&ms->pv_done), 1);
@@ -570,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->s_full[i]), 1);
       mbar_init(smem_u32(&ms->s_empty[i]), 8);
+      mbar_init(smem_u32(&ms->landed[i]), 1);
       mbar_init(smem_u32(&ms->o_ready[i]), 8);
       for (int b = i; b < 4; b += 2) {
         mbar_init(smem_u32(&ms->p_empty[b]), 1);
@@ -580,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fence_mbar_init();
     if (rank == 1) {
       for (int b = 0; b < 4; ++b)
-        mbar_arrive_expect_tx(smem_u32(&ms->p_full[b]), kPHalfBytes + (b & 1 ? 0 : kFactorBytes));
+        mbar_arrive_expect_tx(smem_u32(&ms->p_full[b]), kPHalfBytes + kFactorBytes);
       mbar_arrive_expect_tx(smem_u32(&ms->fin_full[0]), kFinBytes);
       mbar_arrive_expect_tx(smem_u32(&ms->fin_full[1]), kFinBytes);
     }
@@ -616,12 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 8) {
     if (lane == 0) {
       if (rank == 0)
-        load_keys<0, 5>(p, ms, smem + kKRingAt, first, last);
+        load_keys(p, ms, smem + kKRingAt, first, last, 0);
       else
         load_values(p, ms, smem + kVRingAt, first, last);
     }
   } else if (warp == 10) {
-    if (lane == 0 && rank == 0) load_keys<5, kChunks>(p, ms, smem + kKRingAt, first, last);
+    if (lane == 0 && rank == 0) load_keys(p, ms, smem + kKRingAt, first, last, 1);
   } else {
     if (rank == 0)
       run_scores(p, ms, smem, tmem, first, last);
