@@ -277,6 +277,140 @@ void plan_partials_only(mla_plan* P, std::vector<int32_t>* first, std::vector<in
 }
 }  // namespace mla
 
+namespace mla {
+
+// mla_decode_run in two steps: everything that can be refused, with the table's
+// upload, and the launches.
+mla_status decode_prepare(mla_plan* plan, const void* q, const float* q_scale, const void* kv,
+                          const float* kv_scale, const uint8_t* kv_e8m0,
+                          int64_t kv_e8m0_row_stride, int64_t kv_pool_rows,
+                          const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
+                          void* out, float* lse, cudaStream_t stream, DecodeLaunch* launch) {
+  if (plan == nullptr || q == nullptr || kv == nullptr || out == nullptr || workspace == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(workspace, 256))
+    return MLA_ERR_INVALID_ARG;
+  if (kv_pool_rows < 1 || kv_pool_rows > INT32_MAX) return MLA_ERR_INVALID_ARG;
+  if (plan->q_dtype == MLA_DTYPE_FP8_E4M3 && q_scale == nullptr) return MLA_ERR_INVALID_ARG;
+  if (plan->kv_dtype == MLA_DTYPE_FP8_E4M3 && kv_scale == nullptr) return MLA_ERR_INVALID_ARG;
+  if (plan->kv_dtype == MLA_DTYPE_MXFP4) {
+    if (kv_e8m0 == nullptr || kv_e8m0_row_stride < 18) return MLA_ERR_INVALID_ARG;
+    // scale rows are read two bytes at a time
+    if (kv_e8m0_row_stride % 2 != 0 || !aligned(kv_e8m0, 2)) return MLA_ERR_UNSUPPORTED;
+  }
+  if (workspace_bytes < plan->ws_bytes) return MLA_ERR_WORKSPACE;
+  // without a page table, request b's rows follow from kv_indptr: all of them
+  // must lie inside the pool
+  if (kv_indices == nullptr && plan->identity_rows > kv_pool_rows) return MLA_ERR_INVALID_ARG;
+  // Identity table: one TMA box of 128 rows per tile.  Page table with a
+  // page size that is a multiple of 8: one box per 8-row group (a group never
+  // straddles a page).  Other page sizes (bf16 / fp8 KV): every row is
+  // gathered on its own (cp.async), laid out as for the identity table.
+  // MXFP4 rows are loaded by the dequantising threads themselves (no tensor
+  // map) and written in the 8-row-group layout, for any page size.
+  const bool mx = plan->kv_dtype == MLA_DTYPE_MXFP4;
+  int box_rows = mla::kTile;
+  int gather = 0;
+  if (kv_indices != nullptr) {
+    if (kv_pool_rows % plan->page_size != 0) return MLA_ERR_INVALID_ARG;
+    if (plan->page_size % 8 == 0 || mx)
+      box_rows = 8;
+    else
+      gather = 1;
+  }
+  // MXFP4, and plans cut below whole tiles (a CTA's rows are then fewer
+  // than 128): 8-row groups
+  if (mx || plan->unit_tokens < mla::kTile) box_rows = 8;
+  // bytes per row of the tile the UMMAs read (MXFP4 is dequantised to e4m3)
+  const uint32_t row_bytes = mla::kQkDim * (plan->kv_dtype == MLA_DTYPE_BF16 ? 2 : 1);
+  if (!mx && (plan->tmap_ptr != kv || plan->tmap_rows != kv_pool_rows ||
+              plan->tmap_box_rows != box_rows)) {
+    if (!make_kv_map(&plan->tmap, kv, plan->kv_dtype, kv_pool_rows, box_rows)) return MLA_ERR_CUDA;
+    plan->tmap_ptr = kv;
+    plan->tmap_rows = kv_pool_rows;
+    plan->tmap_box_rows = box_rows;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (plan->uploaded_ws != workspace) {
+    if (cudaMemcpyAsync(ws, plan->table.data(), plan->table.size(), cudaMemcpyHostToDevice,
+                        stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    plan->uploaded_ws = workspace;
+  }
+  float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
+  float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
+  int32_t* err = reinterpret_cast<int32_t*>(ws + plan->off_err);
+  // cluster merge when the plan allows it and this device can hold such a
+  // cluster (checked once per plan and device); otherwise stage 2 merges
+  bool cluster = false;
+  if (plan->cluster > 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+    if (plan->cluster_dev != dev) {
+      plan->cluster_fits = mla::stage1_cluster_fits(plan->qmode, plan->cluster);
+      plan->cluster_dev = dev;
+    }
+    cluster = plan->cluster_fits;
+  }
+  if (plan->num_ctas > 0) {
+    mla::Stage1Params& p = launch->stage1;
+    p.tmap_kv = plan->tmap;
+    p.q = q;
+    p.q_scale = q_scale;
+    p.kv_scale = kv_scale;
+    p.kv_indices = kv_indices;
+    p.items = reinterpret_cast<const WorkItem*>(ws + plan->off_items);
+    p.heads = reinterpret_cast<const CtaHead*>(ws + plan->off_indptr);
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.err = err;
+    p.stamp = plan->stamp;
+    p.page_size = plan->page_size;
+    p.box_rows = box_rows;
+    p.gather = gather;
+    p.kv = static_cast<const uint8_t*>(kv);
+    p.chunk_stride = static_cast<uint32_t>(box_rows) * 64u;    // [group][chunk][rows][64 B]
+    p.group_stride = box_rows == 8 ? row_bytes * 8u : 512u;
+    p.pool_rows = kv_pool_rows;
+    p.kv_e8m0 = kv_e8m0;
+    p.sc_stride = kv_e8m0_row_stride;
+    p.cluster = cluster ? plan->cluster : 0;
+    p.exact_q = plan->exact_q;
+  }
+  if (!plan->jobs.empty() && !cluster) {
+    mla::Stage2Params& s = launch->stage2;
+    launch->merge = true;
+    s.jobs = reinterpret_cast<const MergeJob*>(ws + plan->off_jobs);
+    s.err = err;
+    s.stamp = plan->stamp;
+    s.part_o = part_o;
+    s.part_lse = part_lse;
+    s.out = static_cast<uint16_t*>(out);
+    s.lse = lse;
+    s.num_jobs = static_cast<int32_t>(plan->jobs.size());
+    s.rows = plan->rows;
+    s.wide = plan->max_parts > 4 ? 1 : 0;   // the narrow merge takes up to 4 partials per round trip
+  }
+  return MLA_OK;
+}
+
+mla_status decode_launch(const mla_plan* plan, const DecodeLaunch& launch, cudaStream_t stream) {
+  if (plan->num_ctas > 0) {
+    if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    if (launch_stage1(plan->qmode, launch.stage1, plan->num_ctas, stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    if (plan->ev_after != nullptr && cudaEventRecord(plan->ev_after, stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
+  }
+  if (launch.merge && launch_stage2(launch.stage2, stream) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+}  // namespace mla
+
 extern "C" {
 
 // Split requests can be merged inside stage 1 when the CTAs of every
@@ -486,121 +620,12 @@ mla_status mla_decode_run(mla_plan* plan, const void* q, const float* q_scale, c
                           int64_t kv_e8m0_row_stride, int64_t kv_pool_rows,
                           const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
                           void* out, float* lse, mla_stream_t stream_) {
-  if (plan == nullptr || q == nullptr || kv == nullptr || out == nullptr || workspace == nullptr)
-    return MLA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(workspace, 256))
-    return MLA_ERR_INVALID_ARG;
-  if (kv_pool_rows < 1 || kv_pool_rows > INT32_MAX) return MLA_ERR_INVALID_ARG;
-  if (plan->q_dtype == MLA_DTYPE_FP8_E4M3 && q_scale == nullptr) return MLA_ERR_INVALID_ARG;
-  if (plan->kv_dtype == MLA_DTYPE_FP8_E4M3 && kv_scale == nullptr) return MLA_ERR_INVALID_ARG;
-  if (plan->kv_dtype == MLA_DTYPE_MXFP4) {
-    if (kv_e8m0 == nullptr || kv_e8m0_row_stride < 18) return MLA_ERR_INVALID_ARG;
-    // scale rows are read two bytes at a time
-    if (kv_e8m0_row_stride % 2 != 0 || !aligned(kv_e8m0, 2)) return MLA_ERR_UNSUPPORTED;
-  }
-  if (workspace_bytes < plan->ws_bytes) return MLA_ERR_WORKSPACE;
-  // without a page table, request b's rows follow from kv_indptr: all of them
-  // must lie inside the pool
-  if (kv_indices == nullptr && plan->identity_rows > kv_pool_rows) return MLA_ERR_INVALID_ARG;
-  // Identity table: one TMA box of 128 rows per tile.  Page table with a
-  // page size that is a multiple of 8: one box per 8-row group (a group never
-  // straddles a page).  Other page sizes (bf16 / fp8 KV): every row is
-  // gathered on its own (cp.async), laid out as for the identity table.
-  // MXFP4 rows are loaded by the dequantising threads themselves (no tensor
-  // map) and written in the 8-row-group layout, for any page size.
-  const bool mx = plan->kv_dtype == MLA_DTYPE_MXFP4;
-  int box_rows = mla::kTile;
-  int gather = 0;
-  if (kv_indices != nullptr) {
-    if (kv_pool_rows % plan->page_size != 0) return MLA_ERR_INVALID_ARG;
-    if (plan->page_size % 8 == 0 || mx)
-      box_rows = 8;
-    else
-      gather = 1;
-  }
-  // MXFP4, and plans cut below whole tiles (a CTA's rows are then fewer
-  // than 128): 8-row groups
-  if (mx || plan->unit_tokens < mla::kTile) box_rows = 8;
-  // bytes per row of the tile the UMMAs read (MXFP4 is dequantised to e4m3)
-  const uint32_t row_bytes = mla::kQkDim * (plan->kv_dtype == MLA_DTYPE_BF16 ? 2 : 1);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  if (!mx && (plan->tmap_ptr != kv || plan->tmap_rows != kv_pool_rows ||
-              plan->tmap_box_rows != box_rows)) {
-    if (!make_kv_map(&plan->tmap, kv, plan->kv_dtype, kv_pool_rows, box_rows)) return MLA_ERR_CUDA;
-    plan->tmap_ptr = kv;
-    plan->tmap_rows = kv_pool_rows;
-    plan->tmap_box_rows = box_rows;
-  }
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (plan->uploaded_ws != workspace) {
-    if (cudaMemcpyAsync(ws, plan->table.data(), plan->table.size(), cudaMemcpyHostToDevice,
-                        stream) != cudaSuccess)
-      return MLA_ERR_CUDA;
-    plan->uploaded_ws = workspace;
-  }
-  float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
-  float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
-  int32_t* err = reinterpret_cast<int32_t*>(ws + plan->off_err);
-  // cluster merge when the plan allows it and this device can hold such a
-  // cluster (checked once per plan and device); otherwise stage 2 merges
-  bool cluster = false;
-  if (plan->cluster > 0) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
-    if (plan->cluster_dev != dev) {
-      plan->cluster_fits = mla::stage1_cluster_fits(plan->qmode, plan->cluster);
-      plan->cluster_dev = dev;
-    }
-    cluster = plan->cluster_fits;
-  }
-  if (plan->num_ctas > 0) {
-    mla::Stage1Params p{};
-    p.tmap_kv = plan->tmap;
-    p.q = q;
-    p.q_scale = q_scale;
-    p.kv_scale = kv_scale;
-    p.kv_indices = kv_indices;
-    p.items = reinterpret_cast<const WorkItem*>(ws + plan->off_items);
-    p.heads = reinterpret_cast<const CtaHead*>(ws + plan->off_indptr);
-    p.part_o = part_o;
-    p.part_lse = part_lse;
-    p.out = static_cast<uint16_t*>(out);
-    p.lse = lse;
-    p.err = err;
-    p.stamp = plan->stamp;
-    p.page_size = plan->page_size;
-    p.box_rows = box_rows;
-    p.gather = gather;
-    p.kv = static_cast<const uint8_t*>(kv);
-    p.chunk_stride = static_cast<uint32_t>(box_rows) * 64u;    // [group][chunk][rows][64 B]
-    p.group_stride = box_rows == 8 ? row_bytes * 8u : 512u;
-    p.pool_rows = kv_pool_rows;
-    p.kv_e8m0 = kv_e8m0;
-    p.sc_stride = kv_e8m0_row_stride;
-    p.cluster = cluster ? plan->cluster : 0;
-    p.exact_q = plan->exact_q;
-    if (plan->ev_before != nullptr && cudaEventRecord(plan->ev_before, stream) != cudaSuccess)
-      return MLA_ERR_CUDA;
-    if (mla::launch_stage1(plan->qmode, p, plan->num_ctas, stream) != cudaSuccess)
-      return MLA_ERR_CUDA;
-    if (plan->ev_after != nullptr && cudaEventRecord(plan->ev_after, stream) != cudaSuccess)
-      return MLA_ERR_CUDA;
-  }
-  if (!plan->jobs.empty() && !cluster) {
-    mla::Stage2Params s{};
-    s.jobs = reinterpret_cast<const MergeJob*>(ws + plan->off_jobs);
-    s.err = err;
-    s.stamp = plan->stamp;
-    s.part_o = part_o;
-    s.part_lse = part_lse;
-    s.out = static_cast<uint16_t*>(out);
-    s.lse = lse;
-    s.num_jobs = static_cast<int32_t>(plan->jobs.size());
-    s.rows = plan->rows;
-    s.wide = plan->max_parts > 4 ? 1 : 0;   // the narrow merge takes up to 4 partials per round trip
-    if (mla::launch_stage2(s, stream) != cudaSuccess) return MLA_ERR_CUDA;
-  }
-  return MLA_OK;
+  mla::DecodeLaunch launch{};
+  const mla_status st = mla::decode_prepare(plan, q, q_scale, kv, kv_scale, kv_e8m0,
+                                            kv_e8m0_row_stride, kv_pool_rows, kv_indices, workspace,
+                                            workspace_bytes, out, lse, stream, &launch);
+  return st != MLA_OK ? st : mla::decode_launch(plan, launch, stream);
 }
 
 mla_status mla_decode_check(const mla_plan* plan, void* workspace, mla_stream_t stream_) {

@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
   constexpr int kPieces = KV == MLA_DTYPE_BF16 ? 72 : KV == MLA_DTYPE_FP8_E4M3 ? 36 : 18;
   constexpr int kStep = kThreads / kPieces, kSteps = kRowsPerCta / kStep;
   constexpr int kRowBytes = kPieces * 16;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const ExpandTile t = p.tiles[blockIdx.x / kParts];
   if (reinterpret_cast<const WsHeader*>(p.err)->stamp != p.stamp || check_of(t, p.stamp) != t.check) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrStale);

@@ -52,6 +52,19 @@ namespace mla {
 mla_status static_workspace(void** out);
 constexpr size_t kStaticWorkspaceBytes = size_t(16) << 20;
 
+// The two steps of mla_decode_run (api.cu).
+struct DecodeLaunch {
+  Stage1Params stage1;
+  Stage2Params stage2;
+  bool merge;
+};
+mla_status decode_prepare(mla_plan* plan, const void* q, const float* q_scale, const void* kv,
+                          const float* kv_scale, const uint8_t* kv_e8m0,
+                          int64_t kv_e8m0_row_stride, int64_t kv_pool_rows,
+                          const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
+                          void* out, float* lse, cudaStream_t stream, DecodeLaunch* launch);
+mla_status decode_launch(const mla_plan* plan, const DecodeLaunch& launch, cudaStream_t stream);
+
 // What the other host files take from api.cu: a process-wide unique stamp for
 // a new plan, and the driver's cuTensorMapEncodeTiled (null if not found).
 uint64_t new_plan_stamp();

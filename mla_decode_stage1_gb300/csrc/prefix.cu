@@ -382,8 +382,13 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
     {
       const int64_t q_row = static_cast<int64_t>(w.q_row) + row;
       const bool live = row < w.rows;
-      uint32_t r[32];
-      if (h == 0) load_query<1>(p, q_row, live, 8, r);
+      // (the lines of the second step, on their way beside the first one's)
+      if (live) {
+        const char* line = static_cast<const char*>(p.q) + q_row * kQkDim * (p.q_fp8 ? 1 : 2);
+        const int bytes = 64 * (p.q_fp8 ? 1 : 2);
+        for (int c = 2; c < 5; ++c)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(line + (c < 4 ? 4 * h + c : 8) * bytes));
+      }
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
         uint32_t v[64];
@@ -393,6 +398,8 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
         tmem_st32(tq + 128 * h + 32 * c + 32, v + 32);
       }
       if (h == 0) {
+        uint32_t r[32];
+        load_query<1>(p, q_row, live, 8, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           st_shared_16(smem + kQrAt + row * 128 + ((i ^ turn) << 4), r[4 * i], r[4 * i + 1],
@@ -648,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(ms->tmem);
   const int first = uniform(it0), last = uniform(sound ? mine.y : it0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp < 8) {
     if (rank == 0) {
       run_softmax(p, ms, smem, tmem, first, last, warp >> 2, warp & 3, lane);
@@ -656,13 +664,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 8) {
     if (lane == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");      // the gathered rows are there
       if (rank == 0)
         load_keys(p, ms, smem + kKRingAt, first, last, 0);
       else
         load_values(p, ms, smem + kVRingAt, first, last);
     }
   } else if (warp == 10) {
-    if (lane == 0 && rank == 0) load_keys(p, ms, smem + kKRingAt, first, last, 1);
+    if (lane == 0 && rank == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      load_keys(p, ms, smem + kKRingAt, first, last, 1);
+    }
   } else {
     if (rank == 0)
       run_scores(p, ms, smem, tmem, first, last);
@@ -688,8 +700,17 @@ cudaError_t launch_prefix(const PrefixParams& p, int num_pairs, cudaStream_t str
   const cudaError_t e =
       cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  prefix_kernel<<<2 * num_pairs, kThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * num_pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_kernel, p);
 }
 
 }  // namespace mla

@@ -80,6 +80,11 @@ struct MeetParams {
   uint64_t stamp;
 };
 
+// The kernels of a call are chained as programmatic dependents, in the order
+// gather, prefix, the decode kernel over the own ends, meet.  The prefix kernel
+// waits for the gathered rows only before it loads them; the decode kernel reads
+// nothing of the others and runs on the SMs that they leave; each ends after the
+// one before it, so that the last one waits for all.
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_prefix(const PrefixParams& p, int num_pairs, cudaStream_t stream);
 cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream);

@@ -310,11 +310,12 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     return MLA_ERR_INVALID_ARG;
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  // the requests' own ends, first: that call checks its arguments before it
-  // launches anything
-  const mla_status st = mla_decode_run(plan->own, q, q_scale, kv, kv_scale, kv_e8m0,
-                                       kv_e8m0_row_stride, kv_pool_rows, kv_indices,
-                                       ws + plan->off_own, plan->own->ws_bytes, out, nullptr, stream_);
+  // the requests' own ends: everything that can be refused comes before the
+  // first launch
+  mla::DecodeLaunch own{};
+  const mla_status st = mla::decode_prepare(
+      plan->own, q, q_scale, kv, kv_scale, kv_e8m0, kv_e8m0_row_stride, kv_pool_rows, kv_indices,
+      ws + plan->off_own, plan->own->ws_bytes, out, nullptr, stream, &own);
   if (st != MLA_OK) return st;
   if (plan->uploaded_ws != workspace) {
     if (cudaMemcpyAsync(ws, plan->table.data(), plan->table.size(), cudaMemcpyHostToDevice,
@@ -363,7 +364,9 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     p.err = err;
     p.stamp = plan->stamp;
     if (mla::launch_prefix(p, plan->num_pairs, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    own.stage1.beside = 1;
   }
+  if (mla::decode_launch(plan->own, own, stream) != MLA_OK) return MLA_ERR_CUDA;
   mla::MeetParams m{};
   m.jobs = reinterpret_cast<const MeetJob*>(ws + plan->off_jobs);
   m.tokens = static_cast<int64_t>(plan->bs) * plan->q_len;

@@ -1645,6 +1645,9 @@ __global__ void __launch_bounds__(Layout<QM>::kThreads, 1) mla_stage1_kernel(con
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+  // launched beside the kernel before it, on the SMs that one leaves: through
+  // only when that one is
+  if (p.beside && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 int stage1_smem_bytes(int qmode) {
@@ -1686,6 +1689,19 @@ static cudaError_t launch_t(const Stage1Params& p, int num_ctas, cudaStream_t st
     attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mla_stage1_kernel<QM>, p);
+  }
+  if (p.beside) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_ctas);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, mla_stage1_kernel<QM>, p);
