@@ -641,7 +641,7 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  * of group g's prefix (all of them full), then to pages of their own:
  *     out[b,t,h,:] = softmax over [prefix of b's group ; own tokens of b]
  * with the scores, values and lse of mla_decode_run.  The prefix's rows are read
- * and multiplied once for up to 128 query rows (8 query tokens of 16 heads).
+ * and multiplied once for up to 256 query rows (16 query tokens of 16 heads).
  *
  *   group_indptr_host   host int32 [num_groups+1], non-decreasing from 0; its
  *                       last entry is the batch size (at least 1).
@@ -660,8 +660,9 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  *   num_sms             CTAs to plan for; 0 = the SM count of the device.
  * The plan follows mla_plan's rules: library-owned, one host thread at a time,
  * one workspace per plan.  The workspace holds the prefixes' rows in bf16 (1,152
- * bytes a token, the group's length rounded up to 128), the partial results (256
- * KB for each of num_items, 32 KB and more for each range of own tokens) and the
+ * bytes a token, the group's length rounded up to 128; not of a bf16 pool in pages
+ * of a multiple of 64, which is read where it stands), the partial results (2 KB a
+ * row of each of num_items, 32 KB and more for each range of own tokens) and the
  * work tables.
  * Errors: MLA_ERR_INVALID_ARG (also out of host memory), MLA_ERR_UNSUPPORTED (a
  * pair of types), MLA_ERR_CUDA.
@@ -672,8 +673,9 @@ typedef struct {
   int32_t batch_size;
   int32_t num_groups;
   int32_t q_len;
-  int32_t num_pairs;         /* pairs of CTAs that work on the prefixes */
-  int32_t num_items;         /* (up to 128 query rows, range of their prefix) */
+  int32_t num_clusters;      /* clusters of CTAs that work on the prefixes */
+  int32_t block_rows;        /* query rows of such a cluster: 128 or 256 */
+  int32_t num_items;         /* (up to block_rows query rows, range of their prefix) */
   int64_t prefix_tokens;     /* of groups with requests, once each */
   int64_t own_tokens;        /* as the decode kernel counts them: for each query token (or pair) */
   size_t workspace_bytes;

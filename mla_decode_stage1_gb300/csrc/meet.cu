@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(128) meet_kernel(const MeetParams p) {
   auto at = [&](int s) {
     return s < j.own_count
                ? static_cast<int64_t>(j.own_first + s) * p.own_rows + j.own_row + h
-               : static_cast<int64_t>(j.prefix_first + s - j.own_count) * kSpRows + j.prefix_row + h;
+               : (j.prefix_first + static_cast<int64_t>(s - j.own_count) * p.blocks) * kSpRows + j.prefix_row + h;
   };
   auto lse_of = [&](int s) { return (s < j.own_count ? p.own_lse : p.prefix_lse)[at(s)]; };
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are there

@@ -8,25 +8,31 @@
 //
 // Bound: matrix products, 2 (576 + 512) flops per (row, key).
 //
-// Two CTAs of a cluster work on one item.  The output of 128 rows alone fills
-// the 512 columns of a CTA's tensor memory, so the scores stand in the other
-// CTA's.  The even CTA holds the queries (512 dims in tensor memory, 64 in
-// shared memory) and streams key tiles through QK^T; eight warps make
-// probabilities of its scores and send them to the odd CTA's shared memory (bulk
-// copies, 64 keys at a time), with the factors by which the output's rows are to
-// be rescaled.  The odd CTA streams value tiles through PV; its eight warps
-// rescale the output, rarely, and write it.  The two halves' work is nearly equal: a
-// tile of 128 keys takes 36 K steps of N = 128 in the even CTA (2,304 cycles)
-// and 16 of N = 256 in the odd one (2,048).
+// The output of 128 rows alone fills the 512 columns of a CTA's tensor memory, so
+// the scores stand in another CTA's.  A score CTA holds 128 query rows (512 dims
+// in tensor memory, 64 in shared memory) and streams key tiles through QK^T; eight
+// warps make probabilities of its scores and send them to a value CTA's shared
+// memory (bulk copies, 64 keys at a time), with the factors by which the output's
+// rows are to be rescaled.  The value CTA streams the keys' first 512 dims through
+// PV; its eight warps rescale the output, rarely, and write it.  The work of the two
+// is nearly equal: a tile of 128 keys takes 36 K steps of N = 128 of the one (2,304
+// cycles) and 16 of N = 256 of the other (2,048).
+//
+// A cluster is a score and a value CTA, or two of each (kPaired) for 256 rows,
+// whose products are those of a pair of CTAs (M = 256): either holds half of a
+// tile's keys (of the values: half of their dims).  On their own the two kinds read
+// and write 350 KB of shared memory a tile, 2,800 cycles' worth, and a tile took
+// 3,150 cycles; paired, each moves half of the keys.
 //
 // Probabilities are rounded to bf16, the type of the values that they meet; the
 // sums that divide the output are of the unrounded ones.  Scores, sums, maxima
 // and outputs are fp32.
 //
-// Roles (352 threads): warps 0-3 and 4-7 of the even CTA hold the softmax, a
+// Roles (352 threads): warps 0-3 and 4-7 of a score CTA hold the softmax, a
 // thread per row and half of a tile's keys (both see the tile's maximum, so that
-// they keep the same m); of the odd CTA the output's dims 0-255 and 256-511.
-// Warp 8 (and in the even CTA warp 10) loads, warp 9 issues the products.
+// they keep the same m); of a value CTA the output's dims 0-255 and 256-511.
+// Warp 8 (and in a score CTA warp 10) loads, warp 9 issues the products, in the
+// first CTA of a pair for both.
 //
 // What those single threads do for each piece counts: a wait that is over takes
 // 100 cycles, announcing bytes 25, issuing a copy 64.  With a loop over 9 chunks a
@@ -43,50 +49,71 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 352;
-constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 bf16 (or 64 keys)
-// even CTA: probabilities of either half of a tile on their way, rotated query
-// dims, K ring; odd CTA: the probabilities of two tiles received, V ring
+constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 keys of P (or 64 dims)
+constexpr uint32_t kPanelBytes = 64 * 128;         // 64 keys x 64 dims
+// score CTA: probabilities of either half of a tile on their way, rotated query
+// dims, K ring; value CTA: the probabilities of two tiles received, V ring
 constexpr uint32_t kStageAt = 0, kQrAt = 2 * kHalfBytes, kKRingAt = 3 * kHalfBytes;
-constexpr int kChunks = kQkDim / 64;               // of a tile: 128 keys x 64 dims
-constexpr int kGroup = 3, kGroups = 4;             // chunks waited for together; groups under way
-constexpr uint32_t kKSlots = 11;
 constexpr uint32_t kPAt = 0, kVRingAt = 4 * kHalfBytes;
-constexpr int kVSlots = 5;                         // 64 keys x 256 dims each
-constexpr uint32_t kVBytes = 64 * 256 * 2;
-constexpr uint32_t kSmemBytes = kVRingAt + kVSlots * kVBytes;
-static_assert(kKRingAt + kKSlots * kHalfBytes <= kSmemBytes, "the even CTA's arrays fit");
-// even CTA: queries' dims 0-511, then two buffers of scores; odd CTA: the output
+constexpr uint32_t kSmemBytes = 14 * kHalfBytes;
+constexpr int kChunks = kQkDim / 64;               // of a tile: its keys' dims by 64
+constexpr int kGroup = 3;                          // chunks that are waited for together
+
+// What a CTA holds of a tile.  K: 64 or 128 keys and 64 dims a slot; V: 64 keys and
+// 128 or 256 dims a slot.
+template <bool kPaired>
+struct Ring {
+  static constexpr uint32_t kPanels = kPaired ? 1 : 2;          // of a K slot, 64 keys each
+  static constexpr uint32_t kKBytes = kPanels * kPanelBytes;
+  static constexpr uint32_t kKSlots = kPaired ? 22 : 11;
+  static constexpr uint32_t kGroups = kPaired ? 8 : 4;          // of chunks, under way
+  static constexpr uint32_t kVPanels = kPaired ? 2 : 4;         // of a V slot, 64 dims each
+  static constexpr uint32_t kVBytes = kVPanels * kPanelBytes;
+  static constexpr uint32_t kVSlots = kPaired ? 10 : 5;
+  static constexpr int kCtas = kPaired ? 2 : 1;                 // of either kind in a cluster
+  static_assert(kKRingAt + kKSlots * kKBytes <= kSmemBytes, "the score CTA's arrays fit");
+  static_assert(kVRingAt + kVSlots * kVBytes <= kSmemBytes, "the value CTA's arrays fit");
+  // (a group's barrier is used again once its chunks have left the ring)
+  static_assert(kGroups * kGroup > kKSlots, "groups under way");
+};
+// score CTA: queries' dims 0-511, then two buffers of scores; value CTA: the output
 constexpr uint32_t kColQ = 0, kColS = 256, kColO = 0;
 // A row's maximum is kept until a score exceeds it by a factor of 2^8, and then
 // moves by a power of two, so that a byte tells the factor.
 constexpr float kLag = 8.0f;
+constexpr uint32_t kPHalfBytes = kHalfBytes;
+constexpr uint32_t kFactorBytes = kSpRows, kFinBytes = kSpRows * 4;
 
 struct Misc {
-  uint64_t full[kVSlots], empty[kKSlots];          // rings: even: a group's bytes, a chunk's
-                                                   // slot is free; odd: a slot's
-  uint64_t q_ready;                                // even: the item's queries are in place
-  uint64_t s_full[2], s_empty[2];                  // even: score buffers
-  uint64_t p_empty[4];                             // even: P buffers (tile & 1, half) are free
-  uint64_t landed[2];                              // even: a half's copy has arrived
-  uint64_t sum_full;                               // even: the second half's sums
-  uint64_t p_full[4];                              // odd: P buffers and factors
-  uint64_t o_ready[2], pv_done;                    // odd: output rescaled (tiles in turn, as the
-                                                   // warps may be a tile ahead); a tile's PV through
-  uint64_t fin_full[2];                            // odd: 1 / sums of an item
+  uint64_t full[10], empty[22];                    // rings: score: a group's bytes, a chunk's
+                                                   // slot is free; value: a slot's
+  union {
+    struct {                                       // score CTA
+      uint64_t q_ready;                            // the item's queries are in place
+      uint64_t s_full[2], s_empty[2];              // score buffers
+      uint64_t p_empty[4];                         // P buffers (tile & 1, half) are free
+      uint64_t landed[2];                          // a half's copy has arrived
+      uint64_t sum_full;                           // the second half's sums
+    };
+    struct {                                       // value CTA
+      uint64_t p_full[4];                          // P buffers and factors
+      uint64_t o_ready[2];                         // P is there, the output rescaled (tiles in
+                                                   // turn, as the warps may be a tile ahead)
+      uint64_t pv_done;                            // a tile's PV through
+      uint64_t fin_full[2];                        // 1 / sums of an item
+    };
+  };
   uint64_t drain;
   uint32_t tmem;
-  // of tiles, and of items, in turn; odd CTA: received, even CTA: being sent
+  // of tiles, and of items, in turn; value CTA: received, score CTA: being sent
   alignas(16) uint8_t factor[4][kSpRows];          // rows are to be scaled by 2^-factor
-  alignas(16) float fin[2][kSpRows];               // 1 / sums (even CTA: first the half sums)
+  alignas(16) float fin[2][kSpRows];               // 1 / sums (score CTA: first the half sums)
 };
 static_assert(sizeof(Misc) + kSmemBytes + 1024 <= 232448, "fits a CTA's shared memory");
 
 __device__ __forceinline__ PrefixItem load_item(const PrefixItem* p) {
   const int4 a = reinterpret_cast<const int4*>(p)[0], b = reinterpret_cast<const int4*>(p)[1];
-  PrefixItem w{};
-  w.q_row = a.x; w.rows = a.y; w.key0 = a.z; w.keys = a.w;
-  w.slot = b.x; w.check = static_cast<uint32_t>(b.y);
-  return w;
+  return PrefixItem{a.x, a.y, a.z, a.w, b.x, b.y, static_cast<uint32_t>(b.z), 0};
 }
 __device__ __forceinline__ int tiles_of(const PrefixItem& w) {
   return (w.keys + kSpTile - 1) / kSpTile;
@@ -97,11 +124,40 @@ __device__ __forceinline__ void linger() {
   while (globaltimer_ns() - t0 < 1000000) {}
 }
 __device__ __forceinline__ bool all_waited(bool ok) { return __all_sync(0xffffffffu, ok); }
-__device__ __forceinline__ void arrive_warp(uint64_t* bar, int lane) {
+
+// This CTA's place: its kind, and which of its kind.  The first of a kind issues
+// the products and holds the barriers that they wait for.
+struct Place {
+  int kind, half;                                  // kind 0: scores, 1: values
+  uint32_t first;                                  // rank of the first CTA of this kind
+  uint32_t peer;                                   // rank of the other kind's CTA of these rows
+};
+
+// One arrival of the (converged) warp at the first CTA's barrier.  kRelease: it
+// hands over shared memory, or data that came there; else tensor memory alone,
+// which the tcgen05 fences order.
+template <bool kPaired, bool kRelease>
+__device__ __forceinline__ void arrive_at_first(const Place& at, uint64_t* bar, int lane) {
   __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(bar));
+  if (lane != 0) return;
+  if constexpr (!kPaired) {
+    mbar_arrive(smem_u32(bar));
+  } else {
+    const uint32_t there = dsmem_addr(smem_u32(bar), at.first);
+    if constexpr (kRelease)
+      mbar_arrive_cluster_release(there);
+    else
+      mbar_arrive_cluster_relaxed(there);
+  }
 }
-// Copy of this CTA's shared memory to the other's, counted on a barrier there.
+template <bool kPaired>
+__device__ __forceinline__ void commit(const Place& at, uint64_t* bar) {
+  if constexpr (kPaired)
+    tc_commit_mask<true>(smem_u32(bar), static_cast<uint16_t>(3u << at.first));
+  else
+    tc_commit(smem_u32(bar));
+}
+// Copy of this CTA's shared memory to another's, counted on a barrier there.
 __device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_t bytes,
                                              uint32_t bar) {
   asm volatile(
@@ -109,43 +165,67 @@ __device__ __forceinline__ void bulk_to_peer(uint32_t dst, uint32_t src, uint32_
       "r"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-// One arrival on the even CTA's barrier of that name once every product that
-// this thread has issued is through.
-__device__ __forceinline__ void commit_to_even(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b16 even;\n\t"
-      "mov.b16 even, 1;\n\t"
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], even;\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
 
 // ---------------------------------------------------------------- loads
-//
-// Even CTA: every other group of three chunks, from `first` (0 or 1) on.
-__device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1, int first) {
+template <bool kPaired>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row,
+                                         int panel, uint64_t policy) {
+  if constexpr (kPaired)
+    tma_load_3d_pair(dst, map, bar, 0, row, panel, policy);
+  else
+    tma_load_3d(dst, map, bar, 0, row, panel, policy);
+}
+
+// Row of the tensor map of 64 keys of the item's group, from key `key` on.  In the
+// pool itself (`direct`), behind the group's last key it is that of the last 64 keys:
+// such keys have no weight, but what stands in their place must not be NaN.
+__device__ __forceinline__ int key_row(const PrefixParams& p, const PrefixItem& w, int key) {
+  if (!p.direct) return key;
+  key = min(key, w.key0 + (w.keys - 1) / 64 * 64);
+  int64_t page = w.page_base + key / p.page_size;
+  if (p.indices != nullptr) page = p.indices[page];
+  const int64_t row = page * p.page_size + key % p.page_size;
+  if (page < 0 || row + 64 > p.pool_rows) {
+    atomicOr(p.err, kErrBadPage);
+    return 0;
+  }
+  return static_cast<int>(row);
+}
+
+// Score CTA: every other group of three chunks, from `first` (0 or 1) on.
+template <bool kPaired>
+__device__ void load_keys(const PrefixParams& p, Misc* ms, const Place& at, uint32_t ring, int it0,
+                          int it1, int first) {
+  using R = Ring<kPaired>;
   // group of the whole walk, its barrier; the next chunk's slot and, of the slots
   // from it on, the parity of the release to wait for
   uint32_t g = 0, s = 0, parity = 1;
   bool ok = true;
   const uint64_t keep = l2_policy_evict_normal();
   const CUtensorMap* map = &p.map_k;
+  const uint32_t full = kPaired ? dsmem_addr(smem_u32(ms->full), at.first) : smem_u32(ms->full);
   fence_proxy_async();               // (the rows were written by another kernel)
   for (int it = it0; it < it1 && ok; ++it) {
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
+    const int mine = w.key0 + (kPaired ? 64 * at.half : 0);
+    int next0 = key_row(p, w, mine), next1 = kPaired ? 0 : key_row(p, w, mine + 64);
     for (int j = 0; j < tiles && ok; ++j) {
-      const int key = w.key0 + j * kSpTile;
+      const int row0 = next0, row1 = next1;
+      if (j + 1 < tiles) {
+        next0 = key_row(p, w, mine + (j + 1) * kSpTile);
+        if (!kPaired) next1 = key_row(p, w, mine + (j + 1) * kSpTile + 64);
+      }
       for (int ch = 0; ch < kChunks && ok; ch += kGroup, ++g) {
         if ((g & 1) != static_cast<uint32_t>(first)) {
           s += kGroup;
-          if (s >= kKSlots) {
-            s -= kKSlots;
+          if (s >= R::kKSlots) {
+            s -= R::kKSlots;
             parity ^= 1;
           }
           continue;
         }
-        const uint32_t bar = smem_u32(&ms->full[g % kGroups]);
+        const uint32_t bar = full + 8 * (g % R::kGroups);
         bool ready = mbar_test(smem_u32(&ms->empty[s]), parity);
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
@@ -153,14 +233,16 @@ __device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it
             ok = false;
             break;
           }
-          if (i == 0) mbar_arrive_expect_tx(bar, kGroup * kHalfBytes);
-          const uint32_t at = s;
-          if (++s == kKSlots) {
+          if (i == 0 && at.half == 0)
+            mbar_arrive_expect_tx(smem_u32(&ms->full[g % R::kGroups]), R::kCtas * kGroup * R::kKBytes);
+          const uint32_t dst = ring + s * R::kKBytes;
+          if (++s == R::kKSlots) {
             s = 0;
             parity ^= 1;
           }
           if (i + 1 < kGroup) ready = mbar_test(smem_u32(&ms->empty[s]), parity);
-          tma_load_3d(ring + at * kHalfBytes, map, bar, 0, key, ch + i, keep);
+          load_box<kPaired>(dst, map, bar, row0, ch + i, keep);
+          if (!kPaired) load_box<kPaired>(dst + kPanelBytes, map, bar, row1, ch + i, keep);
         }
       }
     }
@@ -168,28 +250,40 @@ __device__ void load_keys(const PrefixParams& p, Misc* ms, uint32_t ring, int it
   if (!ok) linger();                 // no copy may land after the CTA has gone
 }
 
-// Odd CTA: slots of 64 keys and 256 dims.
-__device__ void load_values(const PrefixParams& p, Misc* ms, uint32_t ring, int it0, int it1) {
+// Value CTA: for each 64 keys the output's dims 0-255 and 256-511 (of a pair:
+// this CTA's half of either).
+template <bool kPaired>
+__device__ void load_values(const PrefixParams& p, Misc* ms, const Place& at, uint32_t ring, int it0,
+                            int it1) {
+  using R = Ring<kPaired>;
   uint32_t s = 0, parity = 1;        // (of the first lap: nothing to wait for)
   bool ok = true;
   const uint64_t keep = l2_policy_evict_normal();
   const CUtensorMap* map = &p.map_v;
+  const uint32_t full = kPaired ? dsmem_addr(smem_u32(ms->full), at.first) : smem_u32(ms->full);
   fence_proxy_async();
   for (int it = it0; it < it1 && ok; ++it) {
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
+    int next0 = key_row(p, w, w.key0), next1 = key_row(p, w, w.key0 + 64);
     for (int j = 0; j < tiles && ok; ++j) {
-      const int key = w.key0 + j * kSpTile;
+      const int row0 = next0, row1 = next1;
+      if (j + 1 < tiles) {
+        next0 = key_row(p, w, w.key0 + (j + 1) * kSpTile);
+        next1 = key_row(p, w, w.key0 + (j + 1) * kSpTile + 64);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (!mbar_wait_poll(smem_u32(&ms->empty[s]), parity, p.err, kErrProducer)) {
           ok = false;
           break;
         }
-        const uint32_t bar = smem_u32(&ms->full[s]);
-        mbar_arrive_expect_tx(bar, kVBytes);
-        tma_load_3d(ring + s * kVBytes, map, bar, 0, key + 64 * (u >> 1), 4 * (u & 1), keep);
-        if (++s == kVSlots) {
+        if (at.half == 0) mbar_arrive_expect_tx(smem_u32(&ms->full[s]), R::kCtas * R::kVBytes);
+        const int row = u < 2 ? row0 : row1, panel = 4 * (u & 1) + 2 * at.half;
+        const uint32_t dst = ring + s * R::kVBytes, bar = full + 8 * s;
+        load_box<kPaired>(dst, map, bar, row, panel, keep);
+        if (!kPaired) load_box<kPaired>(dst + 2 * kPanelBytes, map, bar, row, panel + 2, keep);
+        if (++s == R::kVSlots) {
           s = 0;
           parity ^= 1;
         }
@@ -200,9 +294,11 @@ __device__ void load_values(const PrefixParams& p, Misc* ms, uint32_t ring, int 
 }
 
 // ------------------------------------------------------------- products
-__device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint32_t tmem, int it0,
-                           int it1) {
-  constexpr uint32_t idesc = make_idesc(1, 1, false, false, 128, 128);
+template <bool kPaired>
+__device__ void run_scores(const PrefixParams& p, Misc* ms, const Place& at, uint32_t smem,
+                           uint32_t tmem, int it0, int it1) {
+  using R = Ring<kPaired>;
+  constexpr uint32_t idesc = make_idesc(1, 1, false, false, kPaired ? 256 : 128, 128);
   const uint64_t qd = smem_desc(smem + kQrAt, 16, 1024, kSwizzle128B);
   const uint64_t kd = smem_desc(smem + kKRingAt, 16, 1024, kSwizzle128B);
   uint32_t tile = 0, g = 0, s = 0;
@@ -210,43 +306,61 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
     return all_waited(ready) ||
            all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
   };
+  // (arrivals of both CTAs' threads)
+  auto wait_queries = [&](uint32_t parity) {
+    return all_waited(kPaired ? mbar_wait_cluster<true>(smem_u32(&ms->q_ready), parity, p.err, kErrMma)
+                              : mbar_wait_poll(smem_u32(&ms->q_ready), parity, p.err, kErrMma));
+  };
+  auto wait_buffer = [&](uint32_t b, uint32_t parity) {
+    return all_waited(kPaired ? mbar_wait_cluster(smem_u32(&ms->s_empty[b]), parity, p.err, kErrMma)
+                              : mbar_wait_poll(smem_u32(&ms->s_empty[b]), parity, p.err, kErrMma));
+  };
   auto group_ready = [&](uint32_t g) {
-    return mbar_test(smem_u32(&ms->full[g % kGroups]), (g / kGroups) & 1);
+    return mbar_test(smem_u32(&ms->full[g % R::kGroups]), (g / R::kGroups) & 1);
   };
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
-    if (!wait(false, &ms->q_ready, (it - it0) & 1)) return;
+    if (!wait_queries((it - it0) & 1)) return;
+    if constexpr (kPaired) fence_proxy_async();      // (the other CTA's rotated query dims)
     for (int j = 0; j < tiles; ++j, ++tile) {
       const uint32_t b = tile & 1;
       bool ready = group_ready(g);
-      if (tile >= 2 && !wait(false, &ms->s_empty[b], ((tile >> 1) - 1) & 1)) return;
+      if (tile >= 2 && !wait_buffer(b, ((tile >> 1) - 1) & 1)) return;
       const uint32_t d = tmem + kColS + 128 * b;
 #pragma unroll
       for (int u = 0; u < kChunks / kGroup; ++u, ++g) {
-        if (!wait(ready, &ms->full[g % kGroups], (g / kGroups) & 1)) return;
+        if (!wait(ready, &ms->full[g % R::kGroups], (g / R::kGroups) & 1)) return;
         ready = group_ready(g + 1);
         tc_fence_after();
-        uint32_t at[kGroup];
+        uint32_t slot[kGroup];
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          at[i] = s;
-          s = s + 1 == kKSlots ? 0 : s + 1;
+          slot[i] = s;
+          s = s + 1 == R::kKSlots ? 0 : s + 1;
         }
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kGroup; ++i) {
             const int ch = kGroup * u + i;
-            const uint64_t kb = kd + ((at[i] * kHalfBytes) >> 4);
+            const uint64_t kb = kd + ((slot[i] * R::kKBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if (ch < 8)
-                umma_f16_ta(d, tmem + kColQ + 32 * ch + 8 * kk, kb + 2 * kk, idesc, (ch | kk) != 0);
-              else
-                umma_f16(d, qd + 2 * kk, kb + 2 * kk, idesc, 1);
+              const uint32_t qa = tmem + kColQ + 32 * ch + 8 * kk;
+              if constexpr (kPaired) {
+                if (ch < 8)
+                  umma_f16_ta_pair(d, qa, kb + 2 * kk, idesc, (ch | kk) != 0);
+                else
+                  umma_f16_pair(d, qd + 2 * kk, kb + 2 * kk, idesc, 1);
+              } else {
+                if (ch < 8)
+                  umma_f16_ta(d, qa, kb + 2 * kk, idesc, (ch | kk) != 0);
+                else
+                  umma_f16(d, qd + 2 * kk, kb + 2 * kk, idesc, 1);
+              }
             }
-            tc_commit(smem_u32(&ms->empty[at[i]]));
+            commit<kPaired>(at, &ms->empty[slot[i]]);
           }
-          if (u == kChunks / kGroup - 1) tc_commit(smem_u32(&ms->s_full[b]));
+          if (u == kChunks / kGroup - 1) commit<kPaired>(at, &ms->s_full[b]);
         }
         __syncwarp();
       }
@@ -254,57 +368,55 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, uint32_t smem, uint3
   }
 }
 
-constexpr uint32_t kPHalfBytes = kHalfBytes;
-constexpr uint32_t kFactorBytes = kSpRows, kFinBytes = kSpRows * 4;
-
-__device__ void run_values(const PrefixParams& p, Misc* ms, uint32_t smem, uint32_t tmem, int it0,
-                           int it1) {
-  constexpr uint32_t idesc = make_idesc(1, 1, false, true, 128, 256);
+template <bool kPaired>
+__device__ void run_values(const PrefixParams& p, Misc* ms, const Place& at, uint32_t smem,
+                           uint32_t tmem, int it0, int it1) {
+  using R = Ring<kPaired>;
+  constexpr uint32_t idesc = make_idesc(1, 1, false, true, kPaired ? 256 : 128, 256);
+  // (the score CTAs of these rows: those before the value CTAs)
+  const uint16_t scores = kPaired ? 3 : 1;
   const uint64_t pd = smem_desc(smem + kPAt, 16, 1024, kSwizzle128B);
-  const uint64_t vd = smem_desc(smem + kVRingAt, 64 * 128, 1024, kSwizzle128B);
+  const uint64_t vd = smem_desc(smem + kVRingAt, kPanelBytes, 1024, kSwizzle128B);
   uint32_t s = 0, lap = 0, tile = 0;
-  auto wait = [&](bool ready, uint64_t* bar, uint32_t parity) {
-    return all_waited(ready) ||
-           all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrMma));
-  };
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
     for (int j = 0; j < tiles; ++j, ++tile) {
       const uint32_t turn = (tile >> 1) & 1;
-      bool p_ready = mbar_test(smem_u32(&ms->p_full[2 * (tile & 1)]), turn);
-      if (!wait(false, &ms->o_ready[tile & 1], turn)) return;
+      bool ready = mbar_test(smem_u32(&ms->full[s]), lap);
+      uint64_t* o_ready = &ms->o_ready[tile & 1];
+      if (!all_waited(kPaired ? mbar_wait_cluster<true>(smem_u32(o_ready), turn, p.err, kErrMma)
+                              : mbar_wait_poll(smem_u32(o_ready), turn, p.err, kErrMma)))
+        return;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int u = 0; u < 4; ++u) {
+        const int h = u >> 1, dims = u & 1;
         const uint32_t buf = 2 * (tile & 1) + h;
-        bool v_ready = mbar_test(smem_u32(&ms->full[s]), lap);
-        if (!wait(p_ready, &ms->p_full[buf], turn)) return;
-        // (the next one's bytes, which cannot come before this buffer is given back)
-        if (elect_one())
-          mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + kFactorBytes);
         const uint64_t a = pd + ((buf * kHalfBytes) >> 4);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait(v_ready, &ms->full[s], lap)) return;
-          const uint32_t at = s;
-          if (++s == kVSlots) {
-            s = 0;
-            lap ^= 1;
-          }
-          if (half == 0) v_ready = mbar_test(smem_u32(&ms->full[s]), lap);
-          if (half == 1 && h == 0) p_ready = mbar_test(smem_u32(&ms->p_full[buf + 1]), turn);
-          tc_fence_after();
-          const uint64_t vb = vd + ((at * kVBytes) >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16(tmem + kColO + 256 * half, a + 2 * kk, vb + 128 * kk, idesc,
-                       (j | h | kk) != 0);
-            tc_commit(smem_u32(&ms->empty[at]));
-            if (half == 1) commit_to_even(&ms->p_empty[buf]);
-            if (half == 1 && h == 1) tc_commit(smem_u32(&ms->pv_done));
-          }
-          __syncwarp();
+        if (!all_waited(ready) &&
+            !all_waited(mbar_wait_poll(smem_u32(&ms->full[s]), lap, p.err, kErrMma)))
+          return;
+        const uint32_t slot = s;
+        if (++s == R::kVSlots) {
+          s = 0;
+          lap ^= 1;
         }
+        if (u < 3) ready = mbar_test(smem_u32(&ms->full[s]), lap);
+        tc_fence_after();
+        const uint64_t vb = vd + ((slot * R::kVBytes) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t d = tmem + kColO + 256 * dims;
+            if constexpr (kPaired)
+              umma_f16_pair(d, a + 2 * kk, vb + 128 * kk, idesc, (j | h | kk) != 0);
+            else
+              umma_f16(d, a + 2 * kk, vb + 128 * kk, idesc, (j | h | kk) != 0);
+          }
+          commit<kPaired>(at, &ms->empty[slot]);
+          if (dims == 1) tc_commit_mask<kPaired>(smem_u32(&ms->p_empty[buf]), scores);
+          if (u == 3) commit<kPaired>(at, &ms->pv_done);
+        }
+        __syncwarp();
       }
     }
   }
@@ -358,15 +470,16 @@ __device__ __forceinline__ void load_query(const PrefixParams& p, int64_t row, b
   }
 }
 
-__device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint32_t tmem, int it0,
-                            int it1, int h, int warp, int lane) {
-  const int row = warp * 32 + lane;
+template <bool kPaired>
+__device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, uint32_t smem,
+                            uint32_t tmem, int it0, int it1, int h, int warp, int lane) {
+  const int row = warp * 32 + lane, item_row = at.half * kSpRows + row;
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;      // TMEM lane 32 warp
   const uint32_t tq = tmem + lanes + kColQ, ts = tmem + lanes + kColS;
   const uint32_t stage = smem + kStageAt + h * kHalfBytes, turn = row & 7;
-  const uint32_t peer_p = dsmem_addr(smem + kPAt + h * kHalfBytes, 1);
-  const uint32_t peer_full = dsmem_addr(smem_u32(&ms->p_full[h]), 1);
-  const uint32_t peer_factor = dsmem_addr(smem_u32(ms->factor[h]), 1);
+  const uint32_t peer_p = dsmem_addr(smem + kPAt + h * kHalfBytes, at.peer);
+  const uint32_t peer_full = dsmem_addr(smem_u32(&ms->p_full[h]), at.peer);
+  const uint32_t peer_factor = dsmem_addr(smem_u32(ms->factor[h]), at.peer);
   const bool sender = warp == 0 && lane == 0;
   const float qs = p.q_scale != nullptr ? *p.q_scale : 1.0f;
   const float ks = p.kv_scale != nullptr ? *p.kv_scale : 1.0f;
@@ -380,8 +493,8 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
     {
-      const int64_t q_row = static_cast<int64_t>(w.q_row) + row;
-      const bool live = row < w.rows;
+      const int64_t q_row = static_cast<int64_t>(w.q_row) + item_row;
+      const bool live = item_row < w.rows;
       // (the lines of the second step, on their way beside the first one's)
       if (live) {
         const char* line = static_cast<const char*>(p.q) + q_row * kQkDim * (p.q_fp8 ? 1 : 2);
@@ -409,7 +522,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
       __syncwarp();
       tmem_wait_st();
       tc_fence_before();
-      arrive_warp(&ms->q_ready, lane);
+      arrive_at_first<kPaired, true>(at, &ms->q_ready, lane);
     }
     float m = -INFINITY, l = 0.0f;
     for (int j = 0; j < tiles; ++j, ++tile) {
@@ -434,7 +547,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
       tops[1] = tmem_ld32_max(mine + 32, s + 32);
       tmem_wait_ld();
       tc_fence_before();
-      arrive_warp(&ms->s_empty[b], lane);
+      arrive_at_first<kPaired, false>(at, &ms->s_empty[b], lane);
       if (left < kSpTile) {
         tops[0] = tops[1] = tops[3] = -INFINITY;
 #pragma unroll
@@ -447,7 +560,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
           tops[0] = fmaxf(tops[0], __uint_as_float(s[i]));
         }
       }
-      // The staging buffer is free once its last copy has landed, the odd CTA's once
+      // The staging buffer is free once its last copy has landed, the value CTA's once
       // the tile before the last is through PV: looked at here, waited for below.
       const uint32_t buf = 2 * b + h;
       const bool landed =
@@ -503,7 +616,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
       }
       __syncwarp();
     }
-    // Sums of both halves; 1 / sum (times the values' scale) to the odd CTA.  The
+    // Sums of both halves; 1 / sum (times the values' scale) to the value CTA.  The
     // buffers on both sides are those of the item before the last: its output is
     // written before the last item's PV begins, and that is through here.
     const uint32_t turn_of = (it - it0) & 1;
@@ -513,18 +626,20 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
     if (named_bar_any(1 + h, 128, !ok)) return;
     if (h == 1) {
       ms->fin[turn_of][row] = l;
-      arrive_warp(&ms->sum_full, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->sum_full));
     } else {
       ok = all_waited(ok && mbar_wait_poll(smem_u32(&ms->sum_full), turn_of, p.err, kErrSoftmax));
       l += ms->fin[turn_of][row];
-      if (row < w.rows)
-        p.part_lse[static_cast<int64_t>(w.slot) * kSpRows + row] = l == 0.0f ? -INFINITY : m + __log2f(l);
+      if (item_row < w.rows)
+        p.part_lse[(static_cast<int64_t>(w.slot) * Ring<kPaired>::kCtas + at.half) * kSpRows + row] =
+            l == 0.0f ? -INFINITY : m + __log2f(l);
       ms->fin[turn_of][row] = l == 0.0f ? 0.0f : ks / l;
       fence_proxy_async_smem();
       if (named_bar_any(1, 128, !ok)) return;
       if (sender)
-        bulk_to_peer(dsmem_addr(smem_u32(ms->fin[turn_of]), 1), smem_u32(ms->fin[turn_of]),
-                     kFinBytes, dsmem_addr(smem_u32(&ms->fin_full[turn_of]), 1));
+        bulk_to_peer(dsmem_addr(smem_u32(ms->fin[turn_of]), at.peer), smem_u32(ms->fin[turn_of]),
+                     kFinBytes, dsmem_addr(smem_u32(&ms->fin_full[turn_of]), at.peer));
     }
   }
   // what was sent is there before either CTA goes
@@ -534,10 +649,13 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, uint32_t smem, uint
 
 // --------------------------------------------------------------- output
 // (false: a wait gave up)
-__device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int it0, int it1, int half,
-                           int warp, int lane) {
-  const int row = warp * 32 + lane;
+template <bool kPaired>
+__device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uint32_t tmem, int it0,
+                           int it1, int half, int warp, int lane) {
+  const int row = warp * 32 + lane, item_row = at.half * kSpRows + row;
   const uint32_t to = tmem + (static_cast<uint32_t>(warp) << 21) + kColO + 256 * half;
+  const uint32_t landed = dsmem_addr(smem_u32(&ms->landed[half]), at.peer);
+  const bool speaker = warp == 0 && lane == 0;
   uint32_t tile = 0;
   for (int it = it0; it < it1; ++it) {
     const PrefixItem w = load_item(p.items + it);
@@ -546,7 +664,12 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
       const uint32_t buf = 2 * (tile & 1) + half;
       if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[buf]), (tile >> 1) & 1, p.err, kErrDrain)))
         return false;
-      if (warp == 0 && lane == 0) mbar_arrive_cluster_relaxed(dsmem_addr(smem_u32(&ms->landed[half]), 0));
+      if (speaker) {
+        // word of it to the sender; and the next one's bytes, which cannot come
+        // before this buffer is given back
+        mbar_arrive_cluster_relaxed(landed);
+        mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + kFactorBytes);
+      }
       const uint32_t drop = ms->factor[buf][row];
       if (j > 0 && __any_sync(0xffffffffu, drop != 0)) {
         const float f = factor_of(drop);
@@ -565,7 +688,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
         tmem_wait_st();
         tc_fence_before();
       }
-      arrive_warp(&ms->o_ready[tile & 1], lane);
+      arrive_at_first<kPaired, true>(at, &ms->o_ready[tile & 1], lane);
     }
     const uint32_t turn_of = (it - it0) & 1;
     // (P of the last tile came when the tile two before it was through: two
@@ -577,7 +700,9 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
       return false;
     tc_fence_after();
     const float inv = ms->fin[turn_of][row];
-    float* dst = p.part_o + (static_cast<int64_t>(w.slot) * kSpRows + row) * kVDim + 256 * half;
+    float* dst = p.part_o +
+                 ((static_cast<int64_t>(w.slot) * Ring<kPaired>::kCtas + at.half) * kSpRows + row) * kVDim +
+                 256 * half;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[64];
@@ -585,7 +710,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
       tmem_ld32(to + 64 * c, o);
       tmem_ld32(to + 64 * c + 32, o + 32);
       tmem_wait_ld();
-      if (row < w.rows) {
+      if (item_row < w.rows) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
 #pragma unroll
@@ -593,53 +718,66 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, uint32_t tmem, int i
       }
     }
     tc_fence_before();
-    // the odd CTA's thread re-arms the buffer for the item after the next
-    if (half == 0 && row == 0) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[turn_of]), kFinBytes);
+    // (re-armed for the item after the next)
+    if (half == 0 && speaker) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[turn_of]), kFinBytes);
   }
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    prefix_kernel(const __grid_constant__ PrefixParams p) {
+template <bool kPaired>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using R = Ring<kPaired>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(16) Misc misc;
   Misc* ms = &misc;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
+  const uint32_t rank = cluster_ctarank();
+  Place at;
+  at.kind = static_cast<int>(rank) / R::kCtas;
+  at.half = static_cast<int>(rank) % R::kCtas;
+  at.first = static_cast<uint32_t>(at.kind * R::kCtas);
+  at.peer = rank ^ R::kCtas;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kVSlots; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
-    for (uint32_t i = 0; i < kKSlots; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
-    mbar_init(smem_u32(&ms->q_ready), 8);
-    mbar_init(smem_u32(&ms->sum_full), 4);
-    mbar_init(smem_u32(&ms->pv_done), 1);
+    for (int i = 0; i < 10; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
+    for (int i = 0; i < 22; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
     mbar_init(smem_u32(&ms->drain), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ms->s_full[i]), 1);
-      mbar_init(smem_u32(&ms->s_empty[i]), 8);
-      mbar_init(smem_u32(&ms->landed[i]), 1);
-      mbar_init(smem_u32(&ms->o_ready[i]), 8);
-      for (int b = i; b < 4; b += 2) {
-        mbar_init(smem_u32(&ms->p_empty[b]), 1);
-        mbar_init(smem_u32(&ms->p_full[b]), 1);
+    if (at.kind == 0) {
+      mbar_init(smem_u32(&ms->q_ready), 8 * R::kCtas);
+      mbar_init(smem_u32(&ms->sum_full), 4);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&ms->s_full[i]), 1);
+        mbar_init(smem_u32(&ms->s_empty[i]), 8 * R::kCtas);
+        mbar_init(smem_u32(&ms->landed[i]), 1);
       }
-      mbar_init(smem_u32(&ms->fin_full[i]), 1);
+      for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&ms->p_empty[b]), 1);
+    } else {
+      mbar_init(smem_u32(&ms->pv_done), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&ms->o_ready[i]), 8 * R::kCtas);
+        mbar_init(smem_u32(&ms->fin_full[i]), 1);
+      }
+      for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&ms->p_full[b]), 1);
     }
     fence_mbar_init();
-    if (rank == 1) {
+    if (at.kind == 1) {
       for (int b = 0; b < 4; ++b)
         mbar_arrive_expect_tx(smem_u32(&ms->p_full[b]), kPHalfBytes + kFactorBytes);
-      mbar_arrive_expect_tx(smem_u32(&ms->fin_full[0]), kFinBytes);
-      mbar_arrive_expect_tx(smem_u32(&ms->fin_full[1]), kFinBytes);
+      for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[i]), kFinBytes);
     }
   }
   if (warp == 9) {
-    tmem_alloc(smem_u32(&ms->tmem), 512);
-    tmem_relinquish();
+    if constexpr (kPaired) {
+      tmem_alloc_pair(smem_u32(&ms->tmem), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&ms->tmem), 512);
+      tmem_relinquish();
+    }
   }
-  // the pair's items, all checked before the first is taken up (both CTAs check
+  // the cluster's items, all checked before the first is taken up (its CTAs check
   // the same ones)
-  const int4 mine = reinterpret_cast<const int4*>(p.pairs)[blockIdx.x / 2];
+  const int4 mine = reinterpret_cast<const int4*>(p.clusters)[blockIdx.x / (2 * R::kCtas)];
   bool sound = reinterpret_cast<const WsHeader*>(p.err)->stamp == p.stamp &&
                check_of(CtaItems{mine.x, mine.y, 0u, 0}, p.stamp) == static_cast<uint32_t>(mine.z);
   const int it0 = sound ? mine.x : 0;
@@ -651,66 +789,86 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (!sound && threadIdx.x == 0) atomicOr(p.err, kErrStale);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                    // the other CTA's barriers are set up too
+  cluster_sync();                    // the other CTAs' barriers are set up too
   tc_fence_after();
   const uint32_t tmem = uniform(ms->tmem);
   const int first = uniform(it0), last = uniform(sound ? mine.y : it0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp < 8) {
-    if (rank == 0) {
-      run_softmax(p, ms, smem, tmem, first, last, warp >> 2, warp & 3, lane);
-    } else if (!run_output(p, ms, tmem, first, last, warp >> 2, warp & 3, lane)) {
+    if (at.kind == 0)
+      run_softmax<kPaired>(p, ms, at, smem, tmem, first, last, warp >> 2, warp & 3, lane);
+    else if (!run_output<kPaired>(p, ms, at, tmem, first, last, warp >> 2, warp & 3, lane))
       linger();                      // copies on their way land before this CTA goes
-    }
-  } else if (warp == 8) {
-    if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");      // the gathered rows are there
-      if (rank == 0)
-        load_keys(p, ms, smem + kKRingAt, first, last, 0);
+  } else if (warp == 9) {
+    if (at.half == 0) {
+      if (at.kind == 0)
+        run_scores<kPaired>(p, ms, at, smem, tmem, first, last);
       else
-        load_values(p, ms, smem + kVRingAt, first, last);
+        run_values<kPaired>(p, ms, at, smem, tmem, first, last);
+      // no product may run on after the CTAs have gone
+      if (elect_one()) {
+        commit<kPaired>(at, &ms->drain);
+        mbar_wait_poll(smem_u32(&ms->drain), 0, p.err, kErrDrain);
+      }
     }
-  } else if (warp == 10) {
-    if (lane == 0 && rank == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      load_keys(p, ms, smem + kKRingAt, first, last, 1);
-    }
-  } else {
-    if (rank == 0)
-      run_scores(p, ms, smem, tmem, first, last);
-    else
-      run_values(p, ms, smem, tmem, first, last);
-    // no product may run on after the CTAs have gone
-    if (elect_one()) {
-      tc_commit(smem_u32(&ms->drain));
-      mbar_wait_poll(smem_u32(&ms->drain), 0, p.err, kErrDrain);
-    }
+  } else if (lane == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");        // the gathered rows are there
+    if (at.kind == 0)
+      load_keys<kPaired>(p, ms, at, smem + kKRingAt, first, last, warp == 8 ? 0 : 1);
+    else if (warp == 8)
+      load_values<kPaired>(p, ms, at, smem + kVRingAt, first, last);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                    // nothing of the pair is under way any more
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  cluster_sync();                    // nothing of the cluster is under way any more
+  if (warp == 9) {
+    if constexpr (kPaired)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kPaired>
+cudaError_t configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int clusters,
+                      cudaStream_t stream) {
+  constexpr int bytes = kSmemBytes + 1024, ctas = 2 * Ring<kPaired>::kCtas;
+  cfg->gridDim = dim3(ctas * clusters);
+  cfg->blockDim = dim3(kThreads);
+  cfg->dynamicSmemBytes = bytes;
+  cfg->stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {ctas, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+  return cudaFuncSetAttribute(prefix_kernel<kPaired>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              bytes);
+}
+template <bool kPaired>
+cudaError_t launch(const PrefixParams& p, int clusters, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  const cudaError_t e = configure<kPaired>(&cfg, attr, clusters, stream);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, prefix_kernel<kPaired>, p);
+}
+template <bool kPaired>
+int fitting() {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (configure<kPaired>(&cfg, attr, 1, nullptr) != cudaSuccess) return 0;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(&n, prefix_kernel<kPaired>, &cfg) == cudaSuccess ? n : 0;
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const PrefixParams& p, int num_pairs, cudaStream_t stream) {
-  constexpr int bytes = kSmemBytes + 1024;
-  const cudaError_t e =
-      cudaFuncSetAttribute(prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * num_pairs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_kernel, p);
+cudaError_t launch_prefix(const PrefixParams& p, bool paired, int clusters, cudaStream_t stream) {
+  return paired ? launch<true>(p, clusters, stream) : launch<false>(p, clusters, stream);
 }
+int prefix_clusters(bool paired) { return paired ? fitting<true>() : fitting<false>(); }
 
 }  // namespace mla

@@ -444,6 +444,21 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
       "[%0], both;\n\t}" ::"r"(bar)
       : "memory");
 }
+// The same arrival on the barrier at that offset in every CTA of `mask`, for
+// products of one CTA, or of a pair.
+template <bool kPair>
+__device__ __forceinline__ void tc_commit_mask(uint32_t bar, uint16_t mask) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar), "h"(mask)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar), "h"(mask)
+        : "memory");
+}
 __device__ __forceinline__ void umma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -6,25 +6,27 @@
 
 namespace mla {
 
-constexpr int kSpRows = 128;     // query rows of a block: 8 tokens x 16 heads
+constexpr int kSpRows = 128;     // query rows of a CTA: 8 tokens x 16 heads
 constexpr int kSpTile = 128;     // keys of a tile
 
-// Query rows q_row .. q_row + rows - 1 (row = token * 16 + head) of one group
-// against `keys` of its prefix's rows, from workspace row key0 on.
+// Query rows q_row .. q_row + rows - 1 (row = token * 16 + head) of one group, up
+// to 128 or (paired) 256, against `keys` of its prefix's rows from key0 on: a row of
+// the workspace, or a key of the group, whose page table begins at page_base.
 struct PrefixItem {
-  int32_t q_row, rows, key0, keys, slot;   // slot: of the partial result, 128 rows each
+  int32_t q_row, rows, key0, keys, slot, page_base;   // slot: of the partial result
   uint32_t check;
-  int32_t pad[2];
+  int32_t pad;
 };
 static_assert(sizeof(PrefixItem) == 32, "a prefix item is two int4");
 __host__ __device__ inline uint32_t check_of(const PrefixItem& w, uint64_t stamp) {
   const uint32_t h = mix(mix(mix(static_cast<uint32_t>(stamp), w.q_row), w.rows), w.key0);
-  return mix(mix(h, w.keys), w.slot);
+  return mix(mix(mix(h, w.keys), w.slot), w.page_base);
 }
 
 // The partial results of one query token: `own_count` of the decode kernel from
 // own_first on (its 16 heads from row own_row of each), prefix_count of the
-// prefix kernel from prefix_first on (from row prefix_row of each).
+// prefix kernel from block prefix_first on, a block of 128 rows in each slot (from
+// row prefix_row of it).
 struct MeetJob {
   int32_t own_first, own_count, own_row, prefix_first, prefix_count, prefix_row;
   uint32_t check;
@@ -52,16 +54,20 @@ struct GatherParams {
 };
 
 struct PrefixParams {
-  CUtensorMap map_k;           // {64, rows, 9} of the gathered rows, boxes {64, 128, 1}
-  CUtensorMap map_v;           // the same, boxes {64, 64, 4}
+  CUtensorMap map_k;           // {64, rows, 9} of the rows, boxes {64, 64, 1}
+  CUtensorMap map_v;           // the same, boxes {64, 64, 2}
   const PrefixItem* items;
-  const CtaItems* pairs;
+  const CtaItems* clusters;
+  int32_t direct;              // 1: the rows are a bf16 pool's, in pages of a multiple of 64
+  int32_t page_size;
+  const int32_t* indices;      // page table of the prefixes, or null: identity
+  int64_t pool_rows;
   const void* q;               // [tokens * 16][576], bf16 or e4m3
   int32_t q_fp8;
   const float* q_scale;        // device [1], or null: 1
   const float* kv_scale;       // device [1], or null: 1
-  float* part_o;               // [slots][128][512] fp32, normalised
-  float* part_lse;             // [slots][128], log2 domain
+  float* part_o;               // [slots][blocks][128][512] fp32, normalised
+  float* part_lse;             // [slots][blocks][128], log2 domain
   int32_t* err;
   uint64_t stamp;
 };
@@ -72,7 +78,8 @@ struct MeetParams {
   const float* own_o;          // [partials][own_rows][512]
   const float* own_lse;
   int32_t own_rows;
-  const float* prefix_o;       // [slots][128][512]
+  int32_t blocks;              // of 128 rows in a slot of the prefix kernel
+  const float* prefix_o;       // [slots][blocks][128][512]
   const float* prefix_lse;
   uint16_t* out;
   float* lse;
@@ -86,7 +93,9 @@ struct MeetParams {
 // nothing of the others and runs on the SMs that they leave; each ends after the
 // one before it, so that the last one waits for all.
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream);
-cudaError_t launch_prefix(const PrefixParams& p, int num_pairs, cudaStream_t stream);
+cudaError_t launch_prefix(const PrefixParams& p, bool paired, int clusters, cudaStream_t stream);
+// Clusters of the prefix kernel that the current device holds at a time (0: unknown).
+int prefix_clusters(bool paired);
 cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream);
 
 }  // namespace mla

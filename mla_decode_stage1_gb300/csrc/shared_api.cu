@@ -4,6 +4,7 @@
 // declarations and their contracts are in include/mla_decode.h.
 
 #include <algorithm>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -19,19 +20,23 @@ using mla::PrefixItem;
 struct mla_shared {
   int32_t bs = 0, groups = 0, q_len = 1, page_size = 0, num_sms = 0;
   int q_dtype = 0, kv_dtype = 0;
-  int32_t num_pairs = 0, num_slots = 0;
+  bool paired = false;               // clusters of two score and two value CTAs, 256 rows
+  bool direct = false;               // the prefix kernel reads the pool itself
+  int32_t blocks = 1;                // of 128 rows in an item
+  int32_t num_clusters = 0, num_slots = 0;
   int64_t prefix_tokens = 0, identity_rows = 0;
   mla_plan* own = nullptr;           // over the requests' own ends, partial results only
   std::vector<ExpandTile> tiles;
   std::vector<PrefixItem> items;
-  std::vector<CtaItems> pair_items;
+  std::vector<CtaItems> cluster_items;
   std::vector<MeetJob> jobs;
-  size_t off_tiles = 0, off_pairs = 0, off_items = 0, off_jobs = 0, off_own = 0, off_rows = 0,
+  size_t off_tiles = 0, off_clusters = 0, off_items = 0, off_jobs = 0, off_own = 0, off_rows = 0,
          off_part_o = 0, off_part_lse = 0, ws_bytes = 0;
   std::vector<uint8_t> table;
   uint64_t stamp = 0;
   mutable void* uploaded_ws = nullptr;
-  void* map_ws = nullptr;
+  const void* map_ptr = nullptr;     // rows of the tensor maps
+  int64_t map_count = 0;
   CUtensorMap map_k, map_v;
   ~mla_shared() { mla_plan_destroy(own); }
 };
@@ -46,13 +51,14 @@ constexpr int32_t kTokensPerBlock = mla::kSpRows / mla::kHeads;
 constexpr int64_t kItemCost = 2;
 
 struct Block {
-  int32_t q_row, rows, key0, keys;   // key0: workspace row of the group's first key
+  int32_t q_row, rows, key0, keys;   // key0: row or key of the group's first key
+  int32_t page_base;
 };
 
-// The blocks' key tiles, in order, cut into at most `pairs` ranges of nearly
+// The blocks' key tiles, in order, cut into at most `clusters` ranges of nearly
 // equal cost (kItemCost for each item, 1 for each tile).  The smallest largest
 // cost that greedy ranges reach is found by bisection.
-void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t pairs) {
+void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t clusters) {
   int64_t total = 0;
   for (const Block& b : blocks) total += (b.keys + mla::kSpTile - 1) / mla::kSpTile;
   auto cut = [&](int64_t cap, auto&& emit) {
@@ -75,15 +81,15 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t pairs) 
   int64_t lo = kItemCost + 1, hi = kItemCost * (1 + static_cast<int64_t>(blocks.size())) + total;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
-    if (cut(mid, [](size_t, int64_t, int64_t, int64_t) {}) <= pairs) hi = mid; else lo = mid + 1;
+    if (cut(mid, [](size_t, int64_t, int64_t, int64_t) {}) <= clusters) hi = mid; else lo = mid + 1;
   }
   int64_t last = -1;
   cut(lo, [&](size_t k, int64_t at, int64_t take, int64_t range) {
     const Block& b = blocks[k];
     if (range != last) {
       const int32_t n = static_cast<int32_t>(P->items.size());
-      if (last >= 0) P->pair_items.back().end = n;
-      P->pair_items.push_back(CtaItems{n, n, 0u, 0});
+      if (last >= 0) P->cluster_items.back().end = n;
+      P->cluster_items.push_back(CtaItems{n, n, 0u, 0});
       last = range;
     }
     PrefixItem w{};
@@ -92,16 +98,42 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t pairs) 
     w.key0 = static_cast<int32_t>(b.key0 + at * mla::kSpTile);
     w.keys = static_cast<int32_t>(std::min<int64_t>(take * mla::kSpTile, b.keys - at * mla::kSpTile));
     w.slot = static_cast<int32_t>(P->items.size());       // a block's are consecutive
+    w.page_base = b.page_base;
     P->items.push_back(w);
   });
-  if (!P->pair_items.empty()) P->pair_items.back().end = static_cast<int32_t>(P->items.size());
-  P->num_pairs = static_cast<int32_t>(P->pair_items.size());
+  if (!P->cluster_items.empty()) P->cluster_items.back().end = static_cast<int32_t>(P->items.size());
+  P->num_clusters = static_cast<int32_t>(P->cluster_items.size());
   P->num_slots = static_cast<int32_t>(P->items.size());
+}
+
+// Whether to work in blocks of 256 rows, and on how many clusters.  A tile takes
+// 2,400 cycles on a paired cluster and 3,150 on another, but blocks of 256 rows may
+// leave half of one empty, and fewer CTAs have a place in clusters of four.
+void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
+                 bool whole_device) {
+  int32_t on_device[2] = {P->num_sms / 2, P->num_sms / 4};
+  if (whole_device)
+    for (int k = 0; k < 2; ++k) {
+      const int32_t n = mla::prefix_clusters(k == 1);
+      if (n > 0) on_device[k] = std::min(on_device[k], n);
+    }
+  double time[2] = {0, 0};
+  for (int32_t g = 0; g < P->groups; ++g) {
+    const int64_t keys = (static_cast<int64_t>(prefix_indptr[g + 1]) - prefix_indptr[g]) * P->page_size;
+    const int64_t tokens = static_cast<int64_t>(group_indptr[g + 1] - group_indptr[g]) * P->q_len;
+    const double tiles = static_cast<double>((keys + mla::kSpTile - 1) / mla::kSpTile);
+    time[0] += tiles * static_cast<double>((tokens + kTokensPerBlock - 1) / kTokensPerBlock) * 3150;
+    time[1] += tiles * static_cast<double>((tokens + 2 * kTokensPerBlock - 1) / (2 * kTokensPerBlock)) * 2400;
+  }
+  P->paired = on_device[1] > 0 && time[1] / std::max(1, on_device[1]) < time[0] / std::max(1, on_device[0]);
+  if (const char* e = getenv("MLA_PAIRED")) P->paired = atoi(e) != 0;
+  P->blocks = P->paired ? 2 : 1;
+  P->num_clusters = std::max(1, on_device[P->paired]);
 }
 
 mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
                      const int32_t* kv_indptr, const int32_t* last_len) {
-  const int32_t t = P->q_len;
+  const int32_t t = P->q_len, per_block = P->blocks * kTokensPerBlock;
   std::vector<Block> blocks;
   std::vector<int32_t> block_of(P->bs, -1), first_of(P->bs, 0);   // first: the group's first token
   int64_t rows = 0;
@@ -125,14 +157,16 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
       first_of[b] = b0 * t;
     }
     const int64_t tokens = static_cast<int64_t>(b1 - b0) * t;
-    for (int64_t a = 0; a < tokens; a += kTokensPerBlock) {
+    for (int64_t a = 0; a < tokens; a += per_block) {
       Block b;
       b.q_row = static_cast<int32_t>((static_cast<int64_t>(b0) * t + a) * mla::kHeads);
-      b.rows = static_cast<int32_t>(std::min<int64_t>(kTokensPerBlock, tokens - a) * mla::kHeads);
-      b.key0 = static_cast<int32_t>(rows);
+      b.rows = static_cast<int32_t>(std::min<int64_t>(per_block, tokens - a) * mla::kHeads);
+      b.key0 = P->direct ? 0 : static_cast<int32_t>(rows);
+      b.page_base = prefix_indptr[g];
       b.keys = static_cast<int32_t>(keys);
       blocks.push_back(b);
     }
+    if (P->direct) continue;
     for (int64_t k = 0; k < keys; k += mla::kSpTile) {
       ExpandTile e{};
       e.page_base = prefix_indptr[g];
@@ -143,7 +177,7 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
     }
     rows += (keys + mla::kSpTile - 1) / mla::kSpTile * mla::kSpTile;
   }
-  cut_blocks(P, blocks, std::max(1, P->num_sms / 2));
+  cut_blocks(P, blocks, P->num_clusters);
   // partial results of every block, then of every query token
   std::vector<int32_t> first_slot(blocks.size(), 0), slots(blocks.size(), 0);
   {
@@ -166,8 +200,8 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
       j.own_count = own_count[r];
       j.own_row = two ? i % 2 * mla::kHeads : 0;
       if (block_of[b] >= 0) {
-        const int32_t in = b * t + i - first_of[b], k = block_of[b] + in / kTokensPerBlock;
-        j.prefix_first = first_slot[k];
+        const int32_t in = b * t + i - first_of[b], k = block_of[b] + in / per_block;
+        j.prefix_first = first_slot[k] * P->blocks + in % per_block / kTokensPerBlock;
         j.prefix_count = slots[k];
         j.prefix_row = in % kTokensPerBlock * mla::kHeads;
       }
@@ -180,14 +214,14 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
     return at;
   };
   P->off_tiles = take(sizeof(ExpandTile) * P->tiles.size());
-  P->off_pairs = take(sizeof(CtaItems) * P->pair_items.size());
+  P->off_clusters = take(sizeof(CtaItems) * P->cluster_items.size());
   P->off_items = take(sizeof(PrefixItem) * P->items.size());
   P->off_jobs = take(sizeof(MeetJob) * P->jobs.size());
   P->table.assign(off, 0);
   P->off_own = take(P->own->ws_bytes);
   P->off_rows = take(sizeof(uint16_t) * P->tiles.size() * mla::kSpTile * mla::kQkDim);
-  P->off_part_o = take(sizeof(float) * P->num_slots * mla::kSpRows * mla::kVDim);
-  P->off_part_lse = take(sizeof(float) * P->num_slots * mla::kSpRows);
+  P->off_part_o = take(sizeof(float) * P->num_slots * P->blocks * mla::kSpRows * mla::kVDim);
+  P->off_part_lse = take(sizeof(float) * P->num_slots * P->blocks * mla::kSpRows);
   P->ws_bytes = off;
   P->stamp = mla::new_plan_stamp();
   mla::PrefillHeader hdr{};
@@ -199,19 +233,18 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
       std::memcpy(P->table.data() + at, records.data(), sizeof(records[0]) * records.size());
   };
   put(P->off_tiles, P->tiles);
-  put(P->off_pairs, P->pair_items);
+  put(P->off_clusters, P->cluster_items);
   put(P->off_items, P->items);
   put(P->off_jobs, P->jobs);
   return MLA_OK;
 }
 
-// Gathered rows as {64 dims, rows, 9 panels} with the 128-byte swizzle.
-bool make_map(CUtensorMap* map, const void* rows, int64_t count, uint32_t box_rows,
-              uint32_t box_panels) {
+// bf16 rows as {64 dims, rows, 9 panels} with the 128-byte swizzle, 64 rows a box.
+bool make_map(CUtensorMap* map, const void* rows, int64_t count, uint32_t box_panels) {
   const mla::TiledEncoder enc = mla::tiled_encoder();
   const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(count), mla::kQkDim / 64};
   const cuuint64_t strides[2] = {mla::kQkDim * 2, 128};
-  const cuuint32_t box[3] = {64, box_rows, box_panels}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 64, box_panels}, one[3] = {1, 1, 1};
   return enc != nullptr &&
          enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box,
              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -236,7 +269,8 @@ mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* pref
   if (group_indptr_host[0] != 0 || prefix_indptr_host[0] < 0) return MLA_ERR_INVALID_ARG;
   for (int32_t g = 0; g < num_groups; ++g)
     if (group_indptr_host[g + 1] < group_indptr_host[g]) return MLA_ERR_INVALID_ARG;
-  if (num_sms == 0) {
+  const bool whole_device = num_sms == 0;
+  if (whole_device) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -253,12 +287,16 @@ mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* pref
     P->num_sms = num_sms;
     P->q_dtype = q_dtype;
     P->kv_dtype = kv_dtype;
+    // (its rows are the tensor map's, 64 of them always on one page)
+    P->direct = kv_dtype == MLA_DTYPE_BF16 && page_size % 64 == 0;
     // (checks the batch's lengths, query tokens, page size and types)
     const mla_plan_options o{0, num_sms, 0, 0, 1};
     st = mla_decode_plan_ex(kv_indptr_host, kv_last_page_len_host, P->bs, q_len, page_size, q_dtype,
                             kv_dtype, &o, &P->own);
-    if (st == MLA_OK)
+    if (st == MLA_OK) {
+      choose_form(P, group_indptr_host, prefix_indptr_host, whole_device);
       st = make_plan(P, group_indptr_host, prefix_indptr_host, kv_indptr_host, kv_last_page_len_host);
+    }
   } catch (...) {   // out of host memory
     st = MLA_ERR_INVALID_ARG;
   }
@@ -275,7 +313,8 @@ mla_status mla_shared_get_info(const mla_shared* plan, mla_shared_info* info) {
   info->batch_size = plan->bs;
   info->num_groups = plan->groups;
   info->q_len = plan->q_len;
-  info->num_pairs = plan->num_pairs;
+  info->num_clusters = plan->num_clusters;
+  info->block_rows = plan->blocks * mla::kSpRows;
   info->num_items = static_cast<int32_t>(plan->items.size());
   info->prefix_tokens = plan->prefix_tokens;
   info->own_tokens = plan->own->total_tokens;
@@ -327,14 +366,16 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
   uint16_t* rows = reinterpret_cast<uint16_t*>(ws + plan->off_rows);
   float* part_o = reinterpret_cast<float*>(ws + plan->off_part_o);
   float* part_lse = reinterpret_cast<float*>(ws + plan->off_part_lse);
-  if (plan->num_pairs > 0) {
-    if (plan->map_ws != workspace) {
-      const int64_t count = static_cast<int64_t>(plan->tiles.size()) * mla::kSpTile;
-      plan->map_ws = nullptr;
-      if (!make_map(&plan->map_k, rows, count, mla::kSpTile, 1) ||
-          !make_map(&plan->map_v, rows, count, 64, 4))
+  if (plan->num_clusters > 0) {
+    const void* map_rows = plan->direct ? kv : rows;
+    const int64_t count = plan->direct ? kv_pool_rows
+                                       : static_cast<int64_t>(plan->tiles.size()) * mla::kSpTile;
+    if (plan->map_ptr != map_rows || plan->map_count != count) {
+      plan->map_ptr = nullptr;
+      if (!make_map(&plan->map_k, map_rows, count, 1) || !make_map(&plan->map_v, map_rows, count, 2))
         return MLA_ERR_CUDA;
-      plan->map_ws = workspace;
+      plan->map_ptr = map_rows;
+      plan->map_count = count;
     }
     mla::GatherParams g{};
     g.tiles = reinterpret_cast<const ExpandTile*>(ws + plan->off_tiles);
@@ -349,12 +390,16 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     g.rows = rows;
     g.err = err;
     g.stamp = plan->stamp;
-    if (mla::launch_gather(g, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    if (!plan->direct && mla::launch_gather(g, stream) != cudaSuccess) return MLA_ERR_CUDA;
     mla::PrefixParams p{};
     p.map_k = plan->map_k;
     p.map_v = plan->map_v;
     p.items = reinterpret_cast<const PrefixItem*>(ws + plan->off_items);
-    p.pairs = reinterpret_cast<const CtaItems*>(ws + plan->off_pairs);
+    p.clusters = reinterpret_cast<const CtaItems*>(ws + plan->off_clusters);
+    p.direct = plan->direct ? 1 : 0;
+    p.page_size = plan->page_size;
+    p.indices = prefix_indices;
+    p.pool_rows = kv_pool_rows;
     p.q = q;
     p.q_fp8 = plan->q_dtype == MLA_DTYPE_FP8_E4M3 ? 1 : 0;
     p.q_scale = p.q_fp8 ? q_scale : nullptr;
@@ -363,7 +408,7 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     p.part_lse = part_lse;
     p.err = err;
     p.stamp = plan->stamp;
-    if (mla::launch_prefix(p, plan->num_pairs, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    if (mla::launch_prefix(p, plan->paired, plan->num_clusters, stream) != cudaSuccess) return MLA_ERR_CUDA;
     own.stage1.beside = 1;
   }
   if (mla::decode_launch(plan->own, own, stream) != MLA_OK) return MLA_ERR_CUDA;
@@ -373,6 +418,7 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
   m.own_o = reinterpret_cast<const float*>(ws + plan->off_own + plan->own->off_part_o);
   m.own_lse = reinterpret_cast<const float*>(ws + plan->off_own + plan->own->off_part_lse);
   m.own_rows = plan->own->rows;
+  m.blocks = plan->blocks;
   m.prefix_o = part_o;
   m.prefix_lse = part_lse;
   m.out = static_cast<uint16_t*>(out);

@@ -18,8 +18,9 @@ from .layer import (_dense, _need, _on_current_device, _pool, _POOLS, _several_d
 
 class SharedInfo(ctypes.Structure):
     _fields_ = [("batch_size", ctypes.c_int32), ("num_groups", ctypes.c_int32),
-                ("q_len", ctypes.c_int32), ("num_pairs", ctypes.c_int32),
-                ("num_items", ctypes.c_int32), ("prefix_tokens", ctypes.c_int64),
+                ("q_len", ctypes.c_int32), ("num_clusters", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("num_items", ctypes.c_int32),
+                ("prefix_tokens", ctypes.c_int64),
                 ("own_tokens", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
 
 

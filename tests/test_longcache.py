@@ -83,21 +83,32 @@ def test_shared_plan_sizes(mla):
     assert (info.batch_size, info.num_groups, info.q_len) == (30, 3, 1)
     assert info.prefix_tokens == 113 * 8 and info.own_tokens == 30 * 8
     # 4 and 4 tiles of 128 keys: 2 x 4 + 3 x 4 of them at most
-    assert 5 <= info.num_items <= 20 and info.num_pairs <= 76
-    assert p.query_tokens == 30
-    assert p.workspace_bytes >= 8 * 128 * 1152 + info.num_items * 128 * 2052
+    assert 3 <= info.num_items <= 20 and info.num_clusters <= 76
+    assert info.block_rows in (128, 256) and p.query_tokens == 30
+    assert p.workspace_bytes >= 8 * 128 * 1152 + info.num_items * info.block_rows * 2052
+    # a bf16 pool in pages of a multiple of 64 is not gathered, others are
+    size = [plan(mla, [0, 2], [0, 1000], [0, 1, 2], ps=ps, kd=kd).workspace_bytes
+            for ps, kd in ((64, "bf16"), (64, "fp8"), (32, "bf16"))]
+    assert size[0] < 64000 * 1152 < size[1] and size[2] > 32000 * 1152
     # prefixes of groups without requests are not gathered
     assert plan(mla, [0, 0, 2], [0, 50, 60], [0, 1, 2]).info().prefix_tokens == 80
     assert plan(mla, [0, 2], [0, 0], [0, 1, 2]).info().num_items == 0
 
 
-@pytest.mark.parametrize("sms", [1, 2, 3, 7, 64, 152])
-def test_shared_plan_uses_the_pairs(mla, sms):
+@pytest.mark.parametrize("sms", [1, 2, 3, 4, 7, 64, 152])
+def test_shared_plan_uses_the_clusters(mla, sms):
     p = plan(mla, [0, 40], [0, 1000], list(range(41)), sms=sms).info()
-    pairs = max(1, sms // 2)
-    # 5 blocks of 63 tiles
-    assert p.num_pairs <= pairs and p.num_pairs >= min(pairs, 5) * 3 // 4
-    assert 5 <= p.num_items <= 5 + pairs
+    clusters = max(1, sms // (2 if p.block_rows == 128 else 4))
+    # 640 rows, 63 tiles
+    blocks = -(-640 // p.block_rows)
+    assert p.num_clusters <= clusters and p.num_clusters >= min(clusters, blocks) * 3 // 4
+    assert blocks <= p.num_items <= blocks + clusters
+
+
+def test_shared_plan_takes_blocks_of_256_rows_where_they_fill(mla):
+    assert plan(mla, [0, 256], [0, 1000], list(range(257))).info().block_rows == 256
+    assert plan(mla, [0, 8], [0, 1000], list(range(9))).info().block_rows == 128
+    assert plan(mla, [0, 256], [0, 1000], list(range(257)), sms=3).info().block_rows == 128
 
 
 def run_args(p, a, **kw):

@@ -358,10 +358,10 @@ def test_shared_notices_an_overwritten_work_table(mla):
     plan = c.plan(mla)
     ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
     clean = c.run(mla, plan=plan, ws=ws)[0].clone()
-    # behind the header: tiles of 128 gathered rows, pairs' ranges, items, tokens' jobs
+    # behind the header: tiles of 128 gathered rows, clusters' ranges, items, tokens' jobs
     info = plan.info()
     at = 256
-    for size, count in ((32, 7 + 2), (16, info.num_pairs), (32, info.num_items), (32, 23)):
+    for size, count in ((32, 7 + 2), (16, info.num_clusters), (32, info.num_items), (32, 23)):
         for k in {0, count // 2, count - 1}:
             for word in range(3):
                 field = ws[at + k * size + 4 * word: at + k * size + 4 * word + 4]
@@ -451,9 +451,11 @@ def test_shared_refuses_tensors_that_do_not_fit(mla):
     assert e.value.status == 3
 
 
-def test_shared_pool_rows_and_gathered_rows_past_4_gb(mla):
-    """One request on 3.8 million tokens, in reverse order of the pool's pages."""
-    n, page = 3_800_064, 64
+@pytest.mark.parametrize("page,own", [(64, 40), (32, 30)])
+def test_shared_pool_rows_and_gathered_rows_past_4_gb(mla, page, own):
+    """Two requests on 3.8 million tokens, in reverse order of the pool's pages, which
+    are read where they stand or gathered."""
+    n = 3_800_064
     pages = n // page + 1
     kv = torch.empty(pages * page, 576, dtype=torch.bfloat16, device="cuda")
     g = gen(11)
@@ -461,9 +463,9 @@ def test_shared_pool_rows_and_gathered_rows_past_4_gb(mla):
         kv[i: i + (1 << 19)] = torch.randn(len(kv[i: i + (1 << 19)]), 576, generator=g, device="cuda").bfloat16()
     ids = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device="cuda")
     q = (2 * torch.randn(2, 16, 576, generator=g, device="cuda")).bfloat16()
-    plan = mla.mla_shared_plan([0, 2], [0, pages - 1], [0, 1, 1], [40, 0], page_size=page,
+    plan = mla.mla_shared_plan([0, 2], [0, pages - 1], [0, 1, 1], [own, 0], page_size=page,
                                q_dtype="bf16", kv_dtype="bf16")
-    assert plan.workspace_bytes > 1 << 32
+    assert page == 64 or plan.workspace_bytes > 1 << 32
     ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
     out = torch.empty(2, 16, 512, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(2, 16, device="cuda")
@@ -476,8 +478,8 @@ def test_shared_pool_rows_and_gathered_rows_past_4_gb(mla):
     for i in list(range(0, len(kv), 1 << 17)):
         k = kv[i: i + (1 << 17)].double()
         s = q.double() @ k.T / 24
-        if i < page:                          # page 0: request 0's own 40 tokens
-            s[0, :, 40:page] = -INF
+        if i < page:                          # page 0: request 0's own tokens
+            s[0, :, own:page] = -INF
             s[1, :, :page] = -INF
         top = torch.maximum(top, s.masked_fill(s == -INF, 0).abs().amax(-1))
         nm = torch.maximum(m, s.amax(-1))
