@@ -28,11 +28,11 @@
 // sums that divide the output are of the unrounded ones.  Scores, sums, maxima
 // and outputs are fp32.
 //
-// Roles (352 threads): warps 0-3 and 4-7 of a score CTA hold the softmax, a
+// Roles (384 threads): warps 0-3 and 4-7 of a score CTA hold the softmax, a
 // thread per row and half of a tile's keys (both see the tile's maximum, so that
 // they keep the same m); of a value CTA the output's dims 0-255 and 256-511.
 // Warp 8 (and in a score CTA warp 10) loads, warp 9 issues the products, in the
-// first CTA of a pair for both.
+// first CTA of a pair for both; warp 11 of a score CTA sends.
 //
 // What those single threads do for each piece counts: a wait that is over takes
 // 100 cycles, announcing bytes 25, issuing a copy 64.  With a loop over 9 chunks a
@@ -48,13 +48,13 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 keys of P (or 64 dims)
 constexpr uint32_t kPanelBytes = 64 * 128;         // 64 keys x 64 dims
 // score CTA: probabilities of either half of a tile on their way, rotated query
-// dims, K ring; value CTA: the probabilities of two tiles received, V ring
+// dims, K ring; value CTA: the probabilities of some tiles received, V ring
 constexpr uint32_t kStageAt = 0, kQrAt = 2 * kHalfBytes, kKRingAt = 3 * kHalfBytes;
-constexpr uint32_t kPAt = 0, kVRingAt = 4 * kHalfBytes;
+constexpr uint32_t kPAt = 0;
 constexpr uint32_t kSmemBytes = 14 * kHalfBytes;
 constexpr int kChunks = kQkDim / 64;               // of a tile: its keys' dims by 64
 constexpr int kGroup = 3;                          // chunks that are waited for together
@@ -69,7 +69,12 @@ struct Ring {
   static constexpr uint32_t kGroups = kPaired ? 8 : 4;          // of chunks, under way
   static constexpr uint32_t kVPanels = kPaired ? 2 : 4;         // of a V slot, 64 dims each
   static constexpr uint32_t kVBytes = kVPanels * kPanelBytes;
-  static constexpr uint32_t kVSlots = kPaired ? 10 : 5;
+  static constexpr uint32_t kVSlots = kPaired ? 8 : 5;
+  // tiles of P in the value CTA: the word that one is there takes 1,500 cycles to
+  // the other CTA of a pair
+  static constexpr uint32_t kPTiles = kPaired ? 3 : 2;
+  static_assert(kPTiles == 2 || kPTiles == 3, "buffers of P");
+  static constexpr uint32_t kVRingAt = kPAt + kPTiles * 2 * kHalfBytes;
   static constexpr int kCtas = kPaired ? 2 : 1;                 // of either kind in a cluster
   static_assert(kKRingAt + kKSlots * kKBytes <= kSmemBytes, "the score CTA's arrays fit");
   static_assert(kVRingAt + kVSlots * kVBytes <= kSmemBytes, "the value CTA's arrays fit");
@@ -85,31 +90,44 @@ constexpr uint32_t kPHalfBytes = kHalfBytes;
 constexpr uint32_t kFactorBytes = kSpRows, kFinBytes = kSpRows * 4;
 
 struct Misc {
-  uint64_t full[10], empty[22];                    // rings: score: a group's bytes, a chunk's
+  uint64_t full[8], empty[22];                     // rings: score: a group's bytes, a chunk's
                                                    // slot is free; value: a slot's
   union {
     struct {                                       // score CTA
       uint64_t q_ready;                            // the item's queries are in place
       uint64_t s_full[2], s_empty[2];              // score buffers
-      uint64_t p_empty[4];                         // P buffers (tile & 1, half) are free
-      uint64_t landed[2];                          // a half's copy has arrived
-      uint64_t sum_full;                           // the second half's sums
+      uint64_t staged[2];                          // a half's probabilities are to be sent
+      uint64_t landed[2];                          // they have arrived
+      uint64_t p_empty[6];                         // the value CTA's P buffers are free
+      uint64_t sum_full, fin_staged;               // the second half's sums; 1 / sums
     };
     struct {                                       // value CTA
-      uint64_t p_full[4];                          // P buffers and factors
-      uint64_t o_ready[2];                         // P is there, the output rescaled (tiles in
-                                                   // turn, as the warps may be a tile ahead)
-      uint64_t pv_done;                            // a tile's PV through
+      uint64_t p_full[6];                          // P buffers and factors
+      uint64_t o_ready[3];                         // a tile's P is there, the output rescaled
+      uint64_t pv_done[3];                         // its PV is through
       uint64_t fin_full[2];                        // 1 / sums of an item
     };
   };
   uint64_t drain;
   uint32_t tmem;
   // of tiles, and of items, in turn; value CTA: received, score CTA: being sent
-  alignas(16) uint8_t factor[4][kSpRows];          // rows are to be scaled by 2^-factor
+  alignas(16) uint8_t factor[6][kSpRows];          // rows are to be scaled by 2^-factor
   alignas(16) float fin[2][kSpRows];               // 1 / sums (score CTA: first the half sums)
 };
-static_assert(sizeof(Misc) + kSmemBytes + 1024 <= 232448, "fits a CTA's shared memory");
+static_assert(kSmemBytes + sizeof(Misc) <= 232448, "fits a CTA's shared memory");
+
+// Buffer of a tile in a ring of N, and how often the ring has gone round (its
+// lowest bit).
+template <uint32_t N>
+struct Turn {
+  uint32_t at = 0, lap = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      lap ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ PrefixItem load_item(const PrefixItem* p) {
   const int4 a = reinterpret_cast<const int4*>(p)[0], b = reinterpret_cast<const int4*>(p)[1];
@@ -376,21 +394,21 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, const Place& at, uin
   // (the score CTAs of these rows: those before the value CTAs)
   const uint16_t scores = kPaired ? 3 : 1;
   const uint64_t pd = smem_desc(smem + kPAt, 16, 1024, kSwizzle128B);
-  const uint64_t vd = smem_desc(smem + kVRingAt, kPanelBytes, 1024, kSwizzle128B);
-  uint32_t s = 0, lap = 0, tile = 0;
+  const uint64_t vd = smem_desc(smem + R::kVRingAt, kPanelBytes, 1024, kSwizzle128B);
+  uint32_t s = 0, lap = 0;
+  Turn<R::kPTiles> turn;
   for (int it = it0; it < it1; ++it) {
     const int tiles = uniform(tiles_of(load_item(p.items + it)));
-    for (int j = 0; j < tiles; ++j, ++tile) {
-      const uint32_t turn = (tile >> 1) & 1;
+    for (int j = 0; j < tiles; ++j, turn.next()) {
       bool ready = mbar_test(smem_u32(&ms->full[s]), lap);
-      uint64_t* o_ready = &ms->o_ready[tile & 1];
-      if (!all_waited(kPaired ? mbar_wait_cluster<true>(smem_u32(o_ready), turn, p.err, kErrMma)
-                              : mbar_wait_poll(smem_u32(o_ready), turn, p.err, kErrMma)))
+      uint64_t* o_ready = &ms->o_ready[turn.at];
+      if (!all_waited(kPaired ? mbar_wait_cluster<true>(smem_u32(o_ready), turn.lap, p.err, kErrMma)
+                              : mbar_wait_poll(smem_u32(o_ready), turn.lap, p.err, kErrMma)))
         return;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int h = u >> 1, dims = u & 1;
-        const uint32_t buf = 2 * (tile & 1) + h;
+        const uint32_t buf = 2 * turn.at + h;
         const uint64_t a = pd + ((buf * kHalfBytes) >> 4);
         if (!all_waited(ready) &&
             !all_waited(mbar_wait_poll(smem_u32(&ms->full[s]), lap, p.err, kErrMma)))
@@ -414,7 +432,7 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, const Place& at, uin
           }
           commit<kPaired>(at, &ms->empty[slot]);
           if (dims == 1) tc_commit_mask<kPaired>(smem_u32(&ms->p_empty[buf]), scores);
-          if (u == 3) commit<kPaired>(at, &ms->pv_done);
+          if (u == 3) commit<kPaired>(at, &ms->pv_done[turn.at]);
         }
         __syncwarp();
       }
@@ -476,19 +494,16 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
   const int row = warp * 32 + lane, item_row = at.half * kSpRows + row;
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;      // TMEM lane 32 warp
   const uint32_t tq = tmem + lanes + kColQ, ts = tmem + lanes + kColS;
-  const uint32_t stage = smem + kStageAt + h * kHalfBytes, turn = row & 7;
-  const uint32_t peer_p = dsmem_addr(smem + kPAt + h * kHalfBytes, at.peer);
-  const uint32_t peer_full = dsmem_addr(smem_u32(&ms->p_full[h]), at.peer);
-  const uint32_t peer_factor = dsmem_addr(smem_u32(ms->factor[h]), at.peer);
-  const bool sender = warp == 0 && lane == 0;
+  const uint32_t stage = smem + kStageAt + h * kHalfBytes + row * 128, swizzle = row & 7;
   const float qs = p.q_scale != nullptr ? *p.q_scale : 1.0f;
   const float ks = p.kv_scale != nullptr ? *p.kv_scale : 1.0f;
   const float scale = qs * ks * (kLog2e / 24.0f);
   const uint64_t scale2 = pack_f32x2(scale, scale);
   uint32_t tile = 0;
-  // A wait that gave up is kept until the warpgroup's next barrier, where its
-  // four warps leave together: none is left alone at one.
-  bool ok = true;
+  Turn<Ring<kPaired>::kPTiles> turn;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrSoftmax));
+  };
   for (int it = it0; it < it1; ++it) {
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
@@ -515,7 +530,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
         load_query<1>(p, q_row, live, 8, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          st_shared_16(smem + kQrAt + row * 128 + ((i ^ turn) << 4), r[4 * i], r[4 * i + 1],
+          st_shared_16(smem + kQrAt + row * 128 + ((i ^ swizzle) << 4), r[4 * i], r[4 * i + 1],
                        r[4 * i + 2], r[4 * i + 3]);
         fence_proxy_async_smem();
       }
@@ -525,48 +540,37 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       arrive_at_first<kPaired, true>(at, &ms->q_ready, lane);
     }
     float m = -INFINITY, l = 0.0f;
-    for (int j = 0; j < tiles; ++j, ++tile) {
+    for (int j = 0; j < tiles; ++j, ++tile, turn.next()) {
       const uint32_t b = tile & 1;
-      ok = all_waited(ok && mbar_wait_poll(smem_u32(&ms->s_full[b]), (tile >> 1) & 1, p.err, kErrSoftmax));
+      if (!wait(&ms->s_full[b], (tile >> 1) & 1)) return;
       tc_fence_after();
       // the scores of this half, and the maxima of both
-      uint32_t s[64], other[32];
+      uint32_t s[64], other[64];
       const uint32_t mine = ts + 128 * b + 64 * h, theirs = ts + 128 * b + 64 * (1 - h);
       float tops[4];
-      const int left = w.keys - j * kSpTile;             // keys of this tile
-      tops[2] = tmem_ld32_max(theirs, other);
-      tmem_wait_ld();
-      if (left < kSpTile) {
-        tops[2] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          tops[2] = fmaxf(tops[2], 64 * (1 - h) + i < left ? __uint_as_float(other[i]) : -INFINITY);
-      }
-      tops[3] = tmem_ld32_max(theirs + 32, other);
       tops[0] = tmem_ld32_max(mine, s);
       tops[1] = tmem_ld32_max(mine + 32, s + 32);
+      tops[2] = tmem_ld32_max(theirs, other);
+      tops[3] = tmem_ld32_max(theirs + 32, other + 32);
       tmem_wait_ld();
       tc_fence_before();
       arrive_at_first<kPaired, false>(at, &ms->s_empty[b], lane);
+      // The staging buffer is free once its last copy has landed, the value CTA's once
+      // its last tile is through PV: looked at here, waited for below.
+      const uint32_t buf = 2 * turn.at + h;
+      const bool landed = tile < 1 || mbar_test_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1);
+      const bool taken = tile < Ring<kPaired>::kPTiles ||
+                         mbar_test_cluster(smem_u32(&ms->p_empty[buf]), turn.lap ^ 1);
+      const int left = w.keys - j * kSpTile;             // keys of this tile
       if (left < kSpTile) {
-        tops[0] = tops[1] = tops[3] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          tops[3] = fmaxf(tops[3],
-                          64 * (1 - h) + 32 + i < left ? __uint_as_float(other[i]) : -INFINITY);
+        tops[0] = tops[1] = tops[2] = tops[3] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           s[i] = 64 * h + i < left ? s[i] : 0xff800000u;
           tops[0] = fmaxf(tops[0], __uint_as_float(s[i]));
+          tops[2] = fmaxf(tops[2], 64 * (1 - h) + i < left ? __uint_as_float(other[i]) : -INFINITY);
         }
       }
-      // The staging buffer is free once its last copy has landed, the value CTA's once
-      // the tile before the last is through PV: looked at here, waited for below.
-      const uint32_t buf = 2 * b + h;
-      const bool landed =
-          tile < 1 || mbar_test_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1);
-      const bool taken =
-          tile < 2 || mbar_test_cluster(smem_u32(&ms->p_empty[buf]), ((tile >> 1) - 1) & 1);
       const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * scale;
       uint32_t drop = 0;
       if (top > m + kLag) {
@@ -596,55 +600,88 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       float u0, u1;
       unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
       l += u0 + u1;
-      if (!all_waited(landed))
-        ok = ok && all_waited(mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err,
-                                                kErrSoftmax));
-      if (!all_waited(taken))
-        ok = ok && all_waited(mbar_wait_cluster(smem_u32(&ms->p_empty[buf]), ((tile >> 1) - 1) & 1,
-                                                p.err, kErrSoftmax));
+      if (!all_waited(landed) && !all_waited(mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1,
+                                                               p.err, kErrSoftmax)))
+        return;
+      if (!all_waited(taken) && !all_waited(mbar_wait_cluster(smem_u32(&ms->p_empty[buf]), turn.lap ^ 1,
+                                                              p.err, kErrSoftmax)))
+        return;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        st_shared_16(stage + row * 128 + ((i ^ turn) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
+        st_shared_16(stage + ((i ^ swizzle) << 4), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2],
                      pk[4 * i + 3]);
       ms->factor[buf][row] = static_cast<uint8_t>(drop);
       fence_proxy_async_smem();
-      if (named_bar_any(1 + h, 128, !ok)) return;
-      if (sender) {
-        bulk_to_peer(peer_p + b * 2 * kHalfBytes, stage, kPHalfBytes, peer_full + 16 * b);
-        bulk_to_peer(peer_factor + b * 2 * kSpRows, smem_u32(ms->factor[buf]), kFactorBytes,
-                     peer_full + 16 * b);
-      }
       __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->staged[h]));
     }
     // Sums of both halves; 1 / sum (times the values' scale) to the value CTA.  The
-    // buffers on both sides are those of the item before the last: its output is
-    // written before the last item's PV begins, and that is through here.
-    const uint32_t turn_of = (it - it0) & 1;
-    if (sender && ok && tile >= 2)
-      ok = mbar_wait_cluster<true>(smem_u32(&ms->p_empty[2 * (tile & 1) + h]),
-                                   ((tile - 2) >> 1) & 1, p.err, kErrSoftmax);
-    if (named_bar_any(1 + h, 128, !ok)) return;
+    // buffers on both sides are those of the item before the last: its output was
+    // written before the first PV of the last item, so before the PV of the tile
+    // before this item's last one was through.
+    const uint32_t side = (it - it0) & 1;
+    if (tile >= 2) {
+      Turn<Ring<kPaired>::kPTiles> before = turn;        // (the tile before the last)
+      if constexpr (Ring<kPaired>::kPTiles == 3) before.next();
+      const uint32_t lap = before.at < turn.at ? turn.lap : turn.lap ^ 1;
+      if (!all_waited(mbar_wait_cluster(smem_u32(&ms->p_empty[2 * before.at + h]), lap, p.err,
+                                        kErrSoftmax)))
+        return;
+    }
     if (h == 1) {
-      ms->fin[turn_of][row] = l;
+      ms->fin[side][row] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->sum_full));
     } else {
-      ok = all_waited(ok && mbar_wait_poll(smem_u32(&ms->sum_full), turn_of, p.err, kErrSoftmax));
-      l += ms->fin[turn_of][row];
+      if (!wait(&ms->sum_full, side)) return;
+      l += ms->fin[side][row];
       if (item_row < w.rows)
         p.part_lse[(static_cast<int64_t>(w.slot) * Ring<kPaired>::kCtas + at.half) * kSpRows + row] =
             l == 0.0f ? -INFINITY : m + __log2f(l);
-      ms->fin[turn_of][row] = l == 0.0f ? 0.0f : ks / l;
+      ms->fin[side][row] = l == 0.0f ? 0.0f : ks / l;
       fence_proxy_async_smem();
-      if (named_bar_any(1, 128, !ok)) return;
-      if (sender)
-        bulk_to_peer(dsmem_addr(smem_u32(ms->fin[turn_of]), at.peer), smem_u32(ms->fin[turn_of]),
-                     kFinBytes, dsmem_addr(smem_u32(&ms->fin_full[turn_of]), at.peer));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->fin_staged));
     }
   }
+}
+
+// What the softmax has staged goes to the value CTA (one thread).
+template <bool kPaired>
+__device__ void run_sends(const PrefixParams& p, Misc* ms, const Place& at, uint32_t smem, int it0,
+                          int it1) {
+  const uint32_t peer_p = dsmem_addr(smem + kPAt, at.peer);
+  const uint32_t peer_full = dsmem_addr(smem_u32(ms->p_full), at.peer);
+  const uint32_t peer_factor = dsmem_addr(smem_u32(ms->factor), at.peer);
+  const uint32_t peer_fin = dsmem_addr(smem_u32(ms->fin), at.peer);
+  const uint32_t peer_fin_full = dsmem_addr(smem_u32(ms->fin_full), at.peer);
+  uint32_t tile = 0;
+  Turn<Ring<kPaired>::kPTiles> turn;
+  bool ok = true;
+  for (int it = it0; it < it1 && ok; ++it) {
+    const int tiles = tiles_of(load_item(p.items + it));
+    for (int j = 0; j < tiles && ok; ++j, ++tile, turn.next()) {
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h) {
+        ok = ok && mbar_wait_poll(smem_u32(&ms->staged[h]), tile & 1, p.err, kErrSoftmax);
+        if (!ok) break;
+        const uint32_t buf = 2 * turn.at + h;
+        bulk_to_peer(peer_p + buf * kHalfBytes, smem + kStageAt + h * kHalfBytes, kPHalfBytes,
+                     peer_full + 8 * buf);
+        bulk_to_peer(peer_factor + buf * kFactorBytes, smem_u32(ms->factor[buf]), kFactorBytes,
+                     peer_full + 8 * buf);
+      }
+    }
+    const uint32_t side = (it - it0) & 1;
+    ok = ok && mbar_wait_poll(smem_u32(&ms->fin_staged), side, p.err, kErrSoftmax);
+    if (ok)
+      bulk_to_peer(peer_fin + side * kFinBytes, smem_u32(ms->fin[side]), kFinBytes,
+                   peer_fin_full + 8 * side);
+  }
   // what was sent is there before either CTA goes
-  if (sender && tile > 0)
-    mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err, kErrSoftmax);
+  for (int h = 0; h < 2 && ok && tile > 0; ++h)
+    ok = mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err, kErrSoftmax);
+  if (!ok) linger();
 }
 
 // --------------------------------------------------------------- output
@@ -656,13 +693,13 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
   const uint32_t to = tmem + (static_cast<uint32_t>(warp) << 21) + kColO + 256 * half;
   const uint32_t landed = dsmem_addr(smem_u32(&ms->landed[half]), at.peer);
   const bool speaker = warp == 0 && lane == 0;
-  uint32_t tile = 0;
+  Turn<Ring<kPaired>::kPTiles> turn, last;               // last: the tile before
   for (int it = it0; it < it1; ++it) {
     const PrefixItem w = load_item(p.items + it);
     const int tiles = tiles_of(w);
-    for (int j = 0; j < tiles; ++j, ++tile) {
-      const uint32_t buf = 2 * (tile & 1) + half;
-      if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[buf]), (tile >> 1) & 1, p.err, kErrDrain)))
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t buf = 2 * turn.at + half;
+      if (!all_waited(mbar_wait_poll(smem_u32(&ms->p_full[buf]), turn.lap, p.err, kErrDrain)))
         return false;
       if (speaker) {
         // word of it to the sender; and the next one's bytes, which cannot come
@@ -673,7 +710,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
       const uint32_t drop = ms->factor[buf][row];
       if (j > 0 && __any_sync(0xffffffffu, drop != 0)) {
         const float f = factor_of(drop);
-        if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done), (tile - 1) & 1, p.err, kErrDrain)))
+        if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done[last.at]), last.lap, p.err, kErrDrain)))
           return false;
         tc_fence_after();
 #pragma unroll 1
@@ -688,18 +725,17 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
         tmem_wait_st();
         tc_fence_before();
       }
-      arrive_at_first<kPaired, true>(at, &ms->o_ready[tile & 1], lane);
+      arrive_at_first<kPaired, true>(at, &ms->o_ready[turn.at], lane);
+      last = turn;
+      turn.next();
     }
-    const uint32_t turn_of = (it - it0) & 1;
-    // (P of the last tile came when the tile two before it was through: two
-    // phases may be left, of which a wait for the last alone would see neither)
-    if (!all_waited((tile < 2 || mbar_wait_poll(smem_u32(&ms->pv_done), tile & 1, p.err, kErrDrain)) &&
-                    mbar_wait_poll(smem_u32(&ms->pv_done), (tile - 1) & 1, p.err, kErrDrain)) ||
-        !all_waited(mbar_wait_poll(smem_u32(&ms->fin_full[turn_of]), ((it - it0) >> 1) & 1, p.err,
+    const uint32_t side = (it - it0) & 1;
+    if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done[last.at]), last.lap, p.err, kErrDrain)) ||
+        !all_waited(mbar_wait_poll(smem_u32(&ms->fin_full[side]), ((it - it0) >> 1) & 1, p.err,
                                    kErrDrain)))
       return false;
     tc_fence_after();
-    const float inv = ms->fin[turn_of][row];
+    const float inv = ms->fin[side][row];
     float* dst = p.part_o +
                  ((static_cast<int64_t>(w.slot) * Ring<kPaired>::kCtas + at.half) * kSpRows + row) * kVDim +
                  256 * half;
@@ -719,7 +755,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
     }
     tc_fence_before();
     // (re-armed for the item after the next)
-    if (half == 0 && speaker) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[turn_of]), kFinBytes);
+    if (half == 0 && speaker) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[side]), kFinBytes);
   }
   return true;
 }
@@ -727,10 +763,13 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
 template <bool kPaired>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
   using R = Ring<kPaired>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(16) Misc misc;
-  Misc* ms = &misc;
-  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Misc* ms = reinterpret_cast<Misc*>(smem_raw + kSmemBytes);
+  const uint32_t smem = smem_u32(smem_raw);
+  if ((smem & 1023u) != 0) {         // (the swizzled tiles need it; there is no room to move)
+    if (threadIdx.x == 0) atomicOr(p.err, kErrProducer);
+    return;
+  }
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   Place at;
@@ -739,29 +778,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   at.first = static_cast<uint32_t>(at.kind * R::kCtas);
   at.peer = rank ^ R::kCtas;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
     for (int i = 0; i < 22; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
     mbar_init(smem_u32(&ms->drain), 1);
     if (at.kind == 0) {
       mbar_init(smem_u32(&ms->q_ready), 8 * R::kCtas);
       mbar_init(smem_u32(&ms->sum_full), 4);
+      mbar_init(smem_u32(&ms->fin_staged), 4);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&ms->s_full[i]), 1);
         mbar_init(smem_u32(&ms->s_empty[i]), 8 * R::kCtas);
+        mbar_init(smem_u32(&ms->staged[i]), 4);
         mbar_init(smem_u32(&ms->landed[i]), 1);
       }
-      for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&ms->p_empty[b]), 1);
+      for (int b = 0; b < 6; ++b) mbar_init(smem_u32(&ms->p_empty[b]), 1);
     } else {
-      mbar_init(smem_u32(&ms->pv_done), 1);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
         mbar_init(smem_u32(&ms->o_ready[i]), 8 * R::kCtas);
-        mbar_init(smem_u32(&ms->fin_full[i]), 1);
+        mbar_init(smem_u32(&ms->pv_done[i]), 1);
       }
-      for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&ms->p_full[b]), 1);
+      for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ms->fin_full[i]), 1);
+      for (int b = 0; b < 6; ++b) mbar_init(smem_u32(&ms->p_full[b]), 1);
     }
     fence_mbar_init();
     if (at.kind == 1) {
-      for (int b = 0; b < 4; ++b)
+      for (uint32_t b = 0; b < 2 * R::kPTiles; ++b)
         mbar_arrive_expect_tx(smem_u32(&ms->p_full[b]), kPHalfBytes + kFactorBytes);
       for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(smem_u32(&ms->fin_full[i]), kFinBytes);
     }
@@ -811,12 +852,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         mbar_wait_poll(smem_u32(&ms->drain), 0, p.err, kErrDrain);
       }
     }
+  } else if (warp == 11) {
+    if (lane == 0 && at.kind == 0) run_sends<kPaired>(p, ms, at, smem, first, last);
   } else if (lane == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");        // the gathered rows are there
     if (at.kind == 0)
       load_keys<kPaired>(p, ms, at, smem + kKRingAt, first, last, warp == 8 ? 0 : 1);
     else if (warp == 8)
-      load_values<kPaired>(p, ms, at, smem + kVRingAt, first, last);
+      load_values<kPaired>(p, ms, at, smem + R::kVRingAt, first, last);
   }
   __syncwarp();
   tc_fence_before();
@@ -833,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 template <bool kPaired>
 cudaError_t configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int clusters,
                       cudaStream_t stream) {
-  constexpr int bytes = kSmemBytes + 1024, ctas = 2 * Ring<kPaired>::kCtas;
+  constexpr int bytes = kSmemBytes + sizeof(Misc), ctas = 2 * Ring<kPaired>::kCtas;
   cfg->gridDim = dim3(ctas * clusters);
   cfg->blockDim = dim3(kThreads);
   cfg->dynamicSmemBytes = bytes;
