@@ -9,15 +9,15 @@
 // whose lse is NaN makes the row NaN.
 //
 // Bound: latency, and memory for many rows.  A CTA per row, a warp per 128 of the
-// 512 dims, the loads of up to 16 partials in flight.
+// 512 dims, the loads of up to 16 partials in flight (4 where no row has more:
+// registers for twice as many CTAs an SM).
 
 #include "shared.h"
 
 namespace mla {
 namespace {
 
-constexpr int kAhead = 16;
-
+template <int kAhead>
 __global__ void __launch_bounds__(128) meet_kernel(const MeetParams p) {
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x & 31;
@@ -98,7 +98,9 @@ cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, meet_kernel, p);
+  return p.most <= 4   ? cudaLaunchKernelEx(&cfg, meet_kernel<4>, p)
+         : p.most <= 8 ? cudaLaunchKernelEx(&cfg, meet_kernel<8>, p)
+                       : cudaLaunchKernelEx(&cfg, meet_kernel<16>, p);
 }
 
 }  // namespace mla

@@ -51,10 +51,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr uint32_t kHalfBytes = 128 * 128;         // 128 rows x 64 keys of P (or 64 dims)
 constexpr uint32_t kPanelBytes = 64 * 128;         // 64 keys x 64 dims
-// score CTA: probabilities of either half of a tile on their way, rotated query
-// dims, K ring; value CTA: the probabilities of some tiles received, V ring
-constexpr uint32_t kStageAt = 0, kQrAt = 2 * kHalfBytes, kKRingAt = 3 * kHalfBytes;
-constexpr uint32_t kPAt = 0;
+// score CTA: probabilities of either half of a tile or two on their way, rotated
+// query dims, K ring; value CTA: the probabilities of some tiles received, V ring
+constexpr uint32_t kStageAt = 0, kPAt = 0;
 constexpr uint32_t kSmemBytes = 14 * kHalfBytes;
 constexpr int kChunks = kQkDim / 64;               // of a tile: its keys' dims by 64
 constexpr int kGroup = 3;                          // chunks that are waited for together
@@ -65,7 +64,11 @@ template <bool kPaired>
 struct Ring {
   static constexpr uint32_t kPanels = kPaired ? 1 : 2;          // of a K slot, 64 keys each
   static constexpr uint32_t kKBytes = kPanels * kPanelBytes;
-  static constexpr uint32_t kKSlots = kPaired ? 22 : 11;
+  // tiles of P on their way: a copy lands 2,000 cycles after its tile was staged,
+  // and chunks take as long to come from L2, which a CTA on its own has less room for
+  static constexpr uint32_t kStages = kPaired ? 2 : 1;
+  static constexpr uint32_t kQrAt = kStages * 2 * kHalfBytes, kKRingAt = kQrAt + kHalfBytes;
+  static constexpr uint32_t kKSlots = kPaired ? 18 : 11;
   static constexpr uint32_t kGroups = kPaired ? 8 : 4;          // of chunks, under way
   static constexpr uint32_t kVPanels = kPaired ? 2 : 4;         // of a V slot, 64 dims each
   static constexpr uint32_t kVBytes = kVPanels * kPanelBytes;
@@ -97,7 +100,7 @@ struct Misc {
       uint64_t q_ready;                            // the item's queries are in place
       uint64_t s_full[2], s_empty[2];              // score buffers
       uint64_t staged[2];                          // a half's probabilities are to be sent
-      uint64_t landed[2];                          // they have arrived
+      uint64_t landed[4];                          // they have arrived (tiles in turn)
       uint64_t p_empty[6];                         // the value CTA's P buffers are free
       uint64_t sum_full, fin_staged;               // the second half's sums; 1 / sums
     };
@@ -199,7 +202,7 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
 // such keys have no weight, but what stands in their place must not be NaN.
 __device__ __forceinline__ int key_row(const PrefixParams& p, const PrefixItem& w, int key) {
   if (!p.direct) return key;
-  key = min(key, w.key0 + (w.keys - 1) / 64 * 64);
+  key = min(key, w.key0 + (w.keys - 1) / 64 * 64);       // (with boxes of 128 keys: a whole tile)
   int64_t page = w.page_base + key / p.page_size;
   if (p.indices != nullptr) page = p.indices[page];
   const int64_t row = page * p.page_size + key % p.page_size;
@@ -260,7 +263,7 @@ __device__ void load_keys(const PrefixParams& p, Misc* ms, const Place& at, uint
           }
           if (i + 1 < kGroup) ready = mbar_test(smem_u32(&ms->empty[s]), parity);
           load_box<kPaired>(dst, map, bar, row0, ch + i, keep);
-          if (!kPaired) load_box<kPaired>(dst + kPanelBytes, map, bar, row1, ch + i, keep);
+          if (!kPaired && !p.tall) load_box<kPaired>(dst + kPanelBytes, map, bar, row1, ch + i, keep);
         }
       }
     }
@@ -300,7 +303,6 @@ __device__ void load_values(const PrefixParams& p, Misc* ms, const Place& at, ui
         const int row = u < 2 ? row0 : row1, panel = 4 * (u & 1) + 2 * at.half;
         const uint32_t dst = ring + s * R::kVBytes, bar = full + 8 * s;
         load_box<kPaired>(dst, map, bar, row, panel, keep);
-        if (!kPaired) load_box<kPaired>(dst + 2 * kPanelBytes, map, bar, row, panel + 2, keep);
         if (++s == R::kVSlots) {
           s = 0;
           parity ^= 1;
@@ -317,8 +319,8 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, const Place& at, uin
                            uint32_t tmem, int it0, int it1) {
   using R = Ring<kPaired>;
   constexpr uint32_t idesc = make_idesc(1, 1, false, false, kPaired ? 256 : 128, 128);
-  const uint64_t qd = smem_desc(smem + kQrAt, 16, 1024, kSwizzle128B);
-  const uint64_t kd = smem_desc(smem + kKRingAt, 16, 1024, kSwizzle128B);
+  const uint64_t qd = smem_desc(smem + R::kQrAt, 16, 1024, kSwizzle128B);
+  const uint64_t kd = smem_desc(smem + R::kKRingAt, 16, 1024, kSwizzle128B);
   uint32_t tile = 0, g = 0, s = 0;
   auto wait = [&](bool ready, uint64_t* bar, uint32_t parity) {
     return all_waited(ready) ||
@@ -494,13 +496,14 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
   const int row = warp * 32 + lane, item_row = at.half * kSpRows + row;
   const uint32_t lanes = static_cast<uint32_t>(warp) << 21;      // TMEM lane 32 warp
   const uint32_t tq = tmem + lanes + kColQ, ts = tmem + lanes + kColS;
-  const uint32_t stage = smem + kStageAt + h * kHalfBytes + row * 128, swizzle = row & 7;
+  const uint32_t stage0 = smem + kStageAt + h * kHalfBytes + row * 128, swizzle = row & 7;
   const float qs = p.q_scale != nullptr ? *p.q_scale : 1.0f;
   const float ks = p.kv_scale != nullptr ? *p.kv_scale : 1.0f;
   const float scale = qs * ks * (kLog2e / 24.0f);
   const uint64_t scale2 = pack_f32x2(scale, scale);
   uint32_t tile = 0;
   Turn<Ring<kPaired>::kPTiles> turn;
+  Turn<Ring<kPaired>::kStages> side_of;                  // staging buffers
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrSoftmax));
   };
@@ -530,7 +533,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
         load_query<1>(p, q_row, live, 8, r);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          st_shared_16(smem + kQrAt + row * 128 + ((i ^ swizzle) << 4), r[4 * i], r[4 * i + 1],
+          st_shared_16(smem + Ring<kPaired>::kQrAt + row * 128 + ((i ^ swizzle) << 4), r[4 * i], r[4 * i + 1],
                        r[4 * i + 2], r[4 * i + 3]);
         fence_proxy_async_smem();
       }
@@ -540,7 +543,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       arrive_at_first<kPaired, true>(at, &ms->q_ready, lane);
     }
     float m = -INFINITY, l = 0.0f;
-    for (int j = 0; j < tiles; ++j, ++tile, turn.next()) {
+    for (int j = 0; j < tiles; ++j, ++tile, turn.next(), side_of.next()) {
       const uint32_t b = tile & 1;
       if (!wait(&ms->s_full[b], (tile >> 1) & 1)) return;
       tc_fence_after();
@@ -558,7 +561,8 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       // The staging buffer is free once its last copy has landed, the value CTA's once
       // its last tile is through PV: looked at here, waited for below.
       const uint32_t buf = 2 * turn.at + h;
-      const bool landed = tile < 1 || mbar_test_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1);
+      const uint32_t landed_bar = smem_u32(&ms->landed[2 * side_of.at + h]);
+      const bool landed = tile < Ring<kPaired>::kStages || mbar_test_cluster(landed_bar, side_of.lap ^ 1);
       const bool taken = tile < Ring<kPaired>::kPTiles ||
                          mbar_test_cluster(smem_u32(&ms->p_empty[buf]), turn.lap ^ 1);
       const int left = w.keys - j * kSpTile;             // keys of this tile
@@ -600,9 +604,10 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       float u0, u1;
       unpack_f32x2(add_f32x2(sum0, sum1), u0, u1);
       l += u0 + u1;
-      if (!all_waited(landed) && !all_waited(mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1,
-                                                               p.err, kErrSoftmax)))
+      if (!all_waited(landed) &&
+          !all_waited(mbar_wait_cluster(landed_bar, side_of.lap ^ 1, p.err, kErrSoftmax)))
         return;
+      const uint32_t stage = stage0 + side_of.at * 2 * kHalfBytes;
       if (!all_waited(taken) && !all_waited(mbar_wait_cluster(smem_u32(&ms->p_empty[buf]), turn.lap ^ 1,
                                                               p.err, kErrSoftmax)))
         return;
@@ -657,16 +662,17 @@ __device__ void run_sends(const PrefixParams& p, Misc* ms, const Place& at, uint
   const uint32_t peer_fin_full = dsmem_addr(smem_u32(ms->fin_full), at.peer);
   uint32_t tile = 0;
   Turn<Ring<kPaired>::kPTiles> turn;
+  Turn<Ring<kPaired>::kStages> side_of, last;            // staging buffers
   bool ok = true;
   for (int it = it0; it < it1 && ok; ++it) {
     const int tiles = tiles_of(load_item(p.items + it));
-    for (int j = 0; j < tiles && ok; ++j, ++tile, turn.next()) {
+    for (int j = 0; j < tiles && ok; ++j, ++tile, turn.next(), last = side_of, side_of.next()) {
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
         ok = ok && mbar_wait_poll(smem_u32(&ms->staged[h]), tile & 1, p.err, kErrSoftmax);
         if (!ok) break;
         const uint32_t buf = 2 * turn.at + h;
-        bulk_to_peer(peer_p + buf * kHalfBytes, smem + kStageAt + h * kHalfBytes, kPHalfBytes,
+        bulk_to_peer(peer_p + buf * kHalfBytes, smem + kStageAt + (2 * side_of.at + h) * kHalfBytes, kPHalfBytes,
                      peer_full + 8 * buf);
         bulk_to_peer(peer_factor + buf * kFactorBytes, smem_u32(ms->factor[buf]), kFactorBytes,
                      peer_full + 8 * buf);
@@ -679,8 +685,10 @@ __device__ void run_sends(const PrefixParams& p, Misc* ms, const Place& at, uint
                    peer_fin_full + 8 * side);
   }
   // what was sent is there before either CTA goes
+  // (of two tiles on their way the earlier one before the later one: landed words
+  // come in the order of the tiles)
   for (int h = 0; h < 2 && ok && tile > 0; ++h)
-    ok = mbar_wait_cluster(smem_u32(&ms->landed[h]), (tile - 1) & 1, p.err, kErrSoftmax);
+    ok = mbar_wait_cluster(smem_u32(&ms->landed[2 * last.at + h]), last.lap, p.err, kErrSoftmax);
   if (!ok) linger();
 }
 
@@ -692,6 +700,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
   const int row = warp * 32 + lane, item_row = at.half * kSpRows + row;
   const uint32_t to = tmem + (static_cast<uint32_t>(warp) << 21) + kColO + 256 * half;
   const uint32_t landed = dsmem_addr(smem_u32(&ms->landed[half]), at.peer);
+  uint32_t side_of = 0;                                  // the sender's staging buffer
   const bool speaker = warp == 0 && lane == 0;
   Turn<Ring<kPaired>::kPTiles> turn, last;               // last: the tile before
   for (int it = it0; it < it1; ++it) {
@@ -704,7 +713,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
       if (speaker) {
         // word of it to the sender; and the next one's bytes, which cannot come
         // before this buffer is given back
-        mbar_arrive_cluster_relaxed(landed);
+        mbar_arrive_cluster_relaxed(landed + 16 * side_of);
         mbar_arrive_expect_tx(smem_u32(&ms->p_full[buf]), kPHalfBytes + kFactorBytes);
       }
       const uint32_t drop = ms->factor[buf][row];
@@ -728,6 +737,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
       arrive_at_first<kPaired, true>(at, &ms->o_ready[turn.at], lane);
       last = turn;
       turn.next();
+      side_of = side_of + 1 == Ring<kPaired>::kStages ? 0 : side_of + 1;
     }
     const uint32_t side = (it - it0) & 1;
     if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done[last.at]), last.lap, p.err, kErrDrain)) ||
@@ -790,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         mbar_init(smem_u32(&ms->s_empty[i]), 8 * R::kCtas);
         mbar_init(smem_u32(&ms->staged[i]), 4);
         mbar_init(smem_u32(&ms->landed[i]), 1);
+        mbar_init(smem_u32(&ms->landed[2 + i]), 1);
       }
       for (int b = 0; b < 6; ++b) mbar_init(smem_u32(&ms->p_empty[b]), 1);
     } else {
@@ -857,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   } else if (lane == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");        // the gathered rows are there
     if (at.kind == 0)
-      load_keys<kPaired>(p, ms, at, smem + kKRingAt, first, last, warp == 8 ? 0 : 1);
+      load_keys<kPaired>(p, ms, at, smem + R::kKRingAt, first, last, warp == 8 ? 0 : 1);
     else if (warp == 8)
       load_values<kPaired>(p, ms, at, smem + R::kVRingAt, first, last);
   }
@@ -875,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 
 template <bool kPaired>
 cudaError_t configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int clusters,
-                      cudaStream_t stream) {
+                      bool dependent, cudaStream_t stream) {
   constexpr int bytes = kSmemBytes + sizeof(Misc), ctas = 2 * Ring<kPaired>::kCtas;
   cfg->gridDim = dim3(ctas * clusters);
   cfg->blockDim = dim3(kThreads);
@@ -886,7 +897,7 @@ cudaError_t configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], i
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg->attrs = attr;
-  cfg->numAttrs = 2;
+  cfg->numAttrs = dependent ? 2 : 1;
   return cudaFuncSetAttribute(prefix_kernel<kPaired>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               bytes);
 }
@@ -894,7 +905,8 @@ template <bool kPaired>
 cudaError_t launch(const PrefixParams& p, int clusters, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  const cudaError_t e = configure<kPaired>(&cfg, attr, clusters, stream);
+  // (with nothing of the call before it, it follows what the caller has launched)
+  const cudaError_t e = configure<kPaired>(&cfg, attr, clusters, !p.direct, stream);
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, prefix_kernel<kPaired>, p);
 }
 template <bool kPaired>
@@ -902,8 +914,7 @@ int fitting() {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   int n = 0;
-  if (configure<kPaired>(&cfg, attr, 1, nullptr) != cudaSuccess) return 0;
-  cfg.numAttrs = 1;
+  if (configure<kPaired>(&cfg, attr, 1, false, nullptr) != cudaSuccess) return 0;
   return cudaOccupancyMaxActiveClusters(&n, prefix_kernel<kPaired>, &cfg) == cudaSuccess ? n : 0;
 }
 

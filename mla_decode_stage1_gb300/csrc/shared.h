@@ -54,11 +54,12 @@ struct GatherParams {
 };
 
 struct PrefixParams {
-  CUtensorMap map_k;           // {64, rows, 9} of the rows, boxes {64, 64, 1}
-  CUtensorMap map_v;           // the same, boxes {64, 64, 2}
+  CUtensorMap map_k;           // {64, rows, 9} of the rows, boxes {64, 64, 1} or (tall) {64, 128, 1}
+  CUtensorMap map_v;           // the same, boxes {64, 64, 4} or (paired) {64, 64, 2}
   const PrefixItem* items;
   const CtaItems* clusters;
   int32_t direct;              // 1: the rows are a bf16 pool's, in pages of a multiple of 64
+  int32_t tall;                // 1: tiles of 128 keys stand together (not paired)
   int32_t page_size;
   const int32_t* indices;      // page table of the prefixes, or null: identity
   int64_t pool_rows;
@@ -79,6 +80,7 @@ struct MeetParams {
   const float* own_lse;
   int32_t own_rows;
   int32_t blocks;              // of 128 rows in a slot of the prefix kernel
+  int32_t most;                // partial results of a token, at most
   const float* prefix_o;       // [slots][blocks][128][512]
   const float* prefix_lse;
   uint16_t* out;

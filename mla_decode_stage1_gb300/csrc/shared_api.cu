@@ -22,6 +22,8 @@ struct mla_shared {
   int q_dtype = 0, kv_dtype = 0;
   bool paired = false;               // clusters of two score and two value CTAs, 256 rows
   bool direct = false;               // the prefix kernel reads the pool itself
+  bool tall = false;                 // a tile's 128 keys stand together there
+  int32_t most = 0;                  // partial results of a token, at most
   int32_t blocks = 1;                // of 128 rows in an item
   int32_t num_clusters = 0, num_slots = 0;
   int64_t prefix_tokens = 0, identity_rows = 0;
@@ -128,6 +130,7 @@ void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* pref
   P->paired = on_device[1] > 0 && time[1] / std::max(1, on_device[1]) < time[0] / std::max(1, on_device[0]);
   if (const char* e = getenv("MLA_PAIRED")) P->paired = atoi(e) != 0;
   P->blocks = P->paired ? 2 : 1;
+  P->tall = !P->paired && (!P->direct || P->page_size % mla::kSpTile == 0);
   P->num_clusters = std::max(1, on_device[P->paired]);
 }
 
@@ -205,6 +208,7 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
         j.prefix_count = slots[k];
         j.prefix_row = in % kTokensPerBlock * mla::kHeads;
       }
+      P->most = std::max(P->most, j.own_count + j.prefix_count);
       P->jobs.push_back(j);
     }
   size_t off = sizeof(mla::PrefillHeader);
@@ -239,12 +243,13 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
   return MLA_OK;
 }
 
-// bf16 rows as {64 dims, rows, 9 panels} with the 128-byte swizzle, 64 rows a box.
-bool make_map(CUtensorMap* map, const void* rows, int64_t count, uint32_t box_panels) {
+// bf16 rows as {64 dims, rows, 9 panels} with the 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* rows, int64_t count, uint32_t box_rows,
+              uint32_t box_panels) {
   const mla::TiledEncoder enc = mla::tiled_encoder();
   const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(count), mla::kQkDim / 64};
   const cuuint64_t strides[2] = {mla::kQkDim * 2, 128};
-  const cuuint32_t box[3] = {64, 64, box_panels}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, box_rows, box_panels}, one[3] = {1, 1, 1};
   return enc != nullptr &&
          enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box,
              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -372,7 +377,8 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
                                        : static_cast<int64_t>(plan->tiles.size()) * mla::kSpTile;
     if (plan->map_ptr != map_rows || plan->map_count != count) {
       plan->map_ptr = nullptr;
-      if (!make_map(&plan->map_k, map_rows, count, 1) || !make_map(&plan->map_v, map_rows, count, 2))
+      if (!make_map(&plan->map_k, map_rows, count, plan->tall ? 128 : 64, 1) ||
+          !make_map(&plan->map_v, map_rows, count, 64, plan->paired ? 2 : 4))
         return MLA_ERR_CUDA;
       plan->map_ptr = map_rows;
       plan->map_count = count;
@@ -397,6 +403,7 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     p.items = reinterpret_cast<const PrefixItem*>(ws + plan->off_items);
     p.clusters = reinterpret_cast<const CtaItems*>(ws + plan->off_clusters);
     p.direct = plan->direct ? 1 : 0;
+    p.tall = plan->tall ? 1 : 0;
     p.page_size = plan->page_size;
     p.indices = prefix_indices;
     p.pool_rows = kv_pool_rows;
@@ -419,6 +426,7 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
   m.own_lse = reinterpret_cast<const float*>(ws + plan->off_own + plan->own->off_part_lse);
   m.own_rows = plan->own->rows;
   m.blocks = plan->blocks;
+  m.most = plan->most;
   m.prefix_o = part_o;
   m.prefix_lse = part_lse;
   m.out = static_cast<uint16_t*>(out);
