@@ -113,6 +113,7 @@ struct Misc {
   };
   uint64_t drain;
   uint32_t tmem;
+  PrefixItem first;                                // the cluster's first item
   // of tiles, and of items, in turn; value CTA: received, score CTA: being sent
   alignas(16) uint8_t factor[6][kSpRows];          // rows are to be scaled by 2^-factor
   alignas(16) float fin[2][kSpRows];               // 1 / sums (score CTA: first the half sums)
@@ -135,6 +136,10 @@ struct Turn {
 __device__ __forceinline__ PrefixItem load_item(const PrefixItem* p) {
   const int4 a = reinterpret_cast<const int4*>(p)[0], b = reinterpret_cast<const int4*>(p)[1];
   return PrefixItem{a.x, a.y, a.z, a.w, b.x, b.y, static_cast<uint32_t>(b.z), 0};
+}
+// Item `it` of a cluster's items from `it0` on.
+__device__ __forceinline__ PrefixItem item_at(const PrefixParams& p, const Misc* ms, int it, int it0) {
+  return it == it0 ? ms->first : load_item(p.items + it);
 }
 __device__ __forceinline__ int tiles_of(const PrefixItem& w) {
   return (w.keys + kSpTile - 1) / kSpTile;
@@ -225,9 +230,8 @@ __device__ void load_keys(const PrefixParams& p, Misc* ms, const Place& at, uint
   const uint64_t keep = l2_policy_evict_normal();
   const CUtensorMap* map = &p.map_k;
   const uint32_t full = kPaired ? dsmem_addr(smem_u32(ms->full), at.first) : smem_u32(ms->full);
-  fence_proxy_async();               // (the rows were written by another kernel)
   for (int it = it0; it < it1 && ok; ++it) {
-    const PrefixItem w = load_item(p.items + it);
+    const PrefixItem w = item_at(p, ms, it, it0);
     const int tiles = tiles_of(w);
     const int mine = w.key0 + (kPaired ? 64 * at.half : 0);
     int next0 = key_row(p, w, mine), next1 = kPaired ? 0 : key_row(p, w, mine + 64);
@@ -282,9 +286,8 @@ __device__ void load_values(const PrefixParams& p, Misc* ms, const Place& at, ui
   const uint64_t keep = l2_policy_evict_normal();
   const CUtensorMap* map = &p.map_v;
   const uint32_t full = kPaired ? dsmem_addr(smem_u32(ms->full), at.first) : smem_u32(ms->full);
-  fence_proxy_async();
   for (int it = it0; it < it1 && ok; ++it) {
-    const PrefixItem w = load_item(p.items + it);
+    const PrefixItem w = item_at(p, ms, it, it0);
     const int tiles = tiles_of(w);
     int next0 = key_row(p, w, w.key0), next1 = key_row(p, w, w.key0 + 64);
     for (int j = 0; j < tiles && ok; ++j) {
@@ -339,7 +342,7 @@ __device__ void run_scores(const PrefixParams& p, Misc* ms, const Place& at, uin
     return mbar_test(smem_u32(&ms->full[g % R::kGroups]), (g / R::kGroups) & 1);
   };
   for (int it = it0; it < it1; ++it) {
-    const int tiles = uniform(tiles_of(load_item(p.items + it)));
+    const int tiles = uniform(tiles_of(item_at(p, ms, it, it0)));
     if (!wait_queries((it - it0) & 1)) return;
     if constexpr (kPaired) fence_proxy_async();      // (the other CTA's rotated query dims)
     for (int j = 0; j < tiles; ++j, ++tile) {
@@ -400,7 +403,7 @@ __device__ void run_values(const PrefixParams& p, Misc* ms, const Place& at, uin
   uint32_t s = 0, lap = 0;
   Turn<R::kPTiles> turn;
   for (int it = it0; it < it1; ++it) {
-    const int tiles = uniform(tiles_of(load_item(p.items + it)));
+    const int tiles = uniform(tiles_of(item_at(p, ms, it, it0)));
     for (int j = 0; j < tiles; ++j, turn.next()) {
       bool ready = mbar_test(smem_u32(&ms->full[s]), lap);
       uint64_t* o_ready = &ms->o_ready[turn.at];
@@ -458,36 +461,90 @@ __device__ __forceinline__ float factor_of(uint32_t drop) {
   return drop < 127 ? __uint_as_float((127u - drop) << 23) : 0.0f;
 }
 
-// kChunks64 x 64 dims of a query row (zeros past the item's rows) as bf16 pairs,
-// all loads in flight together.
-template <int kChunks64>
-__device__ __forceinline__ void load_query(const PrefixParams& p, int64_t row, bool live, int chunk,
-                                           uint32_t* v) {
-  if (p.q_fp8) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) +
-                                                      row * kQkDim + chunk * 64);
-    uint4 x[4 * kChunks64];
+// 64 dims of a warp's 32 query rows (zeros past the item's `live` rows) on their
+// way, whole lines at a time: a lane holds 16 bytes of bf16 in steps of 4 rows, or of
+// e4m3 in steps of 8.  `src`: the lane's piece of its first row.
+template <bool kFp8>
+__device__ __forceinline__ void fetch_query(const uint8_t* src, int live, int lane,
+                                            uint4 (&x)[kFp8 ? 4 : 8]) {
+  constexpr int kLanes = kFp8 ? 4 : 8;                   // of a row
 #pragma unroll
-    for (int i = 0; i < 4 * kChunks64; ++i) x[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = 32 / kLanes * i + lane / kLanes;
+    x[i] = r < live ? __ldg(reinterpret_cast<const uint4*>(src + 32 / kLanes * i * kQkDim * (kFp8 ? 1 : 2)))
+                    : make_uint4(0, 0, 0, 0);
+  }
+}
+// The same as bf16 rows of 128 bytes at `dst` (row 0 of the warp, a multiple of 8
+// rows behind a 1,024-byte boundary), in the 128-byte swizzle.
+template <bool kFp8>
+__device__ __forceinline__ void stage_query(const uint4 (&x)[kFp8 ? 4 : 8], uint32_t dst, int lane) {
+  constexpr int kLanes = kFp8 ? 4 : 8;
 #pragma unroll
-    for (int i = 0; i < 4 * kChunks64; ++i) {
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = 32 / kLanes * i + lane / kLanes;
+    const uint32_t at = dst + r * 128;
+    if constexpr (kFp8) {
+      const int piece = 2 * (lane & 3);
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1))));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        v[8 * i + k] = bf16x2_of(f.x, f.y);
+        v[k] = bf16x2_of(f.x, f.y);
       }
-    }
-  } else {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                      row * kQkDim + chunk * 64);
-#pragma unroll
-    for (int i = 0; i < 8 * kChunks64; ++i) {
-      const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-      v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+      st_shared_16(at + ((piece ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+      st_shared_16(at + (((piece + 1) ^ (r & 7)) << 4), v[4], v[5], v[6], v[7]);
+    } else {
+      st_shared_16(at + (((lane & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
     }
   }
+}
+// A lane's own row of it, as bf16 pairs.
+__device__ __forceinline__ void own_query(uint32_t src, int lane, uint32_t* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[4 * i]), "=r"(v[4 * i + 1]), "=r"(v[4 * i + 2]), "=r"(v[4 * i + 3])
+                 : "r"(src + lane * 128 + ((i ^ (lane & 7)) << 4))
+                 : "memory");
+}
+
+// A warp's 32 query rows: dims 256 h .. 256 h + 255 to tensor memory (a row a lane),
+// by way of 4 KB of shared memory; with h = 0 the rotated ones to shared memory.
+template <bool kFp8>
+__device__ __forceinline__ void load_queries(const void* q, int64_t row0, int live, int h,
+                                             uint32_t via, uint32_t tmem, uint32_t rotated, int lane) {
+  constexpr int kRowBytes = kQkDim * (kFp8 ? 1 : 2), kChunkBytes = kRowBytes / kChunks;
+  constexpr int kLanes = kFp8 ? 4 : 8;
+  const uint8_t* rows = static_cast<const uint8_t*>(q) + row0 * kRowBytes;
+  if (lane < live) {
+    // all lines of the lane's row, so that the chunks behind the first one wait less
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + lane * kRowBytes +
+                                                    (i < 4 ? 4 * h + i : 8) * kChunkBytes));
+  }
+  const uint8_t* src = rows + lane / kLanes * kRowBytes + lane % kLanes * 16 + 4 * h * kChunkBytes;
+  uint4 x[kLanes];
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    fetch_query<kFp8>(src + c * kChunkBytes, live, lane, x);
+    stage_query<kFp8>(x, via, lane);
+    __syncwarp();
+    own_query(via, lane, v);
+    __syncwarp();
+    tmem_st32(tmem + 32 * c, v);
+  }
+  if (h == 0) {
+    fetch_query<kFp8>(src + 8 * kChunkBytes, live, lane, x);
+    stage_query<kFp8>(x, rotated, lane);
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  tmem_wait_st();
 }
 
 template <bool kPaired>
@@ -508,37 +565,25 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
     return all_waited(mbar_wait_poll(smem_u32(bar), parity, p.err, kErrSoftmax));
   };
   for (int it = it0; it < it1; ++it) {
-    const PrefixItem w = load_item(p.items + it);
+    const PrefixItem w = item_at(p, ms, it, it0);
     const int tiles = tiles_of(w);
     {
-      const int64_t q_row = static_cast<int64_t>(w.q_row) + item_row;
-      const bool live = item_row < w.rows;
-      // (the lines of the second step, on their way beside the first one's)
-      if (live) {
-        const char* line = static_cast<const char*>(p.q) + q_row * kQkDim * (p.q_fp8 ? 1 : 2);
-        const int bytes = 64 * (p.q_fp8 ? 1 : 2);
-        for (int c = 2; c < 5; ++c)
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(line + (c < 4 ? 4 * h + c : 8) * bytes));
-      }
-#pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t v[64];
-        load_query<2>(p, q_row, live, 4 * h + c, v);
-        __syncwarp();
-        tmem_st32(tq + 128 * h + 32 * c, v);
-        tmem_st32(tq + 128 * h + 32 * c + 32, v + 32);
-      }
-      if (h == 0) {
-        uint32_t r[32];
-        load_query<1>(p, q_row, live, 8, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          st_shared_16(smem + Ring<kPaired>::kQrAt + row * 128 + ((i ^ swizzle) << 4), r[4 * i], r[4 * i + 1],
-                       r[4 * i + 2], r[4 * i + 3]);
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      tmem_wait_st();
+      // Queries, a row a lane of tensor memory, by way of the warp's part of its
+      // staging buffer 0 (once the last copy from there has landed).
+      const int row0 = at.half * kSpRows + warp * 32;
+      const int64_t q_row0 = static_cast<int64_t>(w.q_row) + row0;
+      const int live = w.rows - row0;
+      const uint32_t via = smem + kStageAt + h * kHalfBytes + warp * 4096;
+      constexpr uint32_t kStages = Ring<kPaired>::kStages;
+      const uint32_t uses = (tile + kStages - 1) / kStages;
+      if (uses > 0 && !all_waited(mbar_wait_cluster(smem_u32(&ms->landed[h]), (uses - 1) & 1, p.err,
+                                                    kErrSoftmax)))
+        return;
+      const uint32_t rotated = smem + Ring<kPaired>::kQrAt + warp * 4096;
+      if (p.q_fp8)
+        load_queries<true>(p.q, q_row0, live, h, via, tq + 128 * h, rotated, lane);
+      else
+        load_queries<false>(p.q, q_row0, live, h, via, tq + 128 * h, rotated, lane);
       tc_fence_before();
       arrive_at_first<kPaired, true>(at, &ms->q_ready, lane);
     }
@@ -665,7 +710,7 @@ __device__ void run_sends(const PrefixParams& p, Misc* ms, const Place& at, uint
   Turn<Ring<kPaired>::kStages> side_of, last;            // staging buffers
   bool ok = true;
   for (int it = it0; it < it1 && ok; ++it) {
-    const int tiles = tiles_of(load_item(p.items + it));
+    const int tiles = tiles_of(item_at(p, ms, it, it0));
     for (int j = 0; j < tiles && ok; ++j, ++tile, turn.next(), last = side_of, side_of.next()) {
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
@@ -704,7 +749,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
   const bool speaker = warp == 0 && lane == 0;
   Turn<Ring<kPaired>::kPTiles> turn, last;               // last: the tile before
   for (int it = it0; it < it1; ++it) {
-    const PrefixItem w = load_item(p.items + it);
+    const PrefixItem w = item_at(p, ms, it, it0);
     const int tiles = tiles_of(w);
     for (int j = 0; j < tiles; ++j) {
       const uint32_t buf = 2 * turn.at + half;
@@ -746,9 +791,10 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
       return false;
     tc_fence_after();
     const float inv = ms->fin[side][row];
+    // [dims / 8][row][8]: 32 bytes a lane, a kilobyte a warp
     float* dst = p.part_o +
-                 ((static_cast<int64_t>(w.slot) * Ring<kPaired>::kCtas + at.half) * kSpRows + row) * kVDim +
-                 256 * half;
+                 (static_cast<int64_t>(w.slot) * Ring<kPaired>::kCtas + at.half) * kSpRows * kVDim +
+                 (32 * half * kSpRows + row) * 8;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[64];
@@ -760,7 +806,7 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
 #pragma unroll
         for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st_global_32(dst + 64 * c + 8 * i, o + 8 * i);
+        for (int i = 0; i < 8; ++i) st_global_32(dst + (8 * c + i) * kSpRows * 8, o + 8 * i);
       }
     }
     tc_fence_before();
@@ -836,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   for (int it = it0 + static_cast<int>(threadIdx.x); sound && it < mine.y; it += kThreads) {
     const PrefixItem w = load_item(p.items + it);
     sound = check_of(w, p.stamp) == w.check;
+    if (it == it0) ms->first = w;
   }
   sound = __syncthreads_and(sound);
   if (!sound && threadIdx.x == 0) atomicOr(p.err, kErrStale);

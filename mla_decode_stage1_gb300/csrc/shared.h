@@ -67,7 +67,7 @@ struct PrefixParams {
   int32_t q_fp8;
   const float* q_scale;        // device [1], or null: 1
   const float* kv_scale;       // device [1], or null: 1
-  float* part_o;               // [slots][blocks][128][512] fp32, normalised
+  float* part_o;               // [slots][blocks][64][128][8] fp32, normalised: dim / 8, row, dim % 8
   float* part_lse;             // [slots][blocks][128], log2 domain
   int32_t* err;
   uint64_t stamp;
@@ -81,7 +81,7 @@ struct MeetParams {
   int32_t own_rows;
   int32_t blocks;              // of 128 rows in a slot of the prefix kernel
   int32_t most;                // partial results of a token, at most
-  const float* prefix_o;       // [slots][blocks][128][512]
+  const float* prefix_o;       // [slots][blocks][64][128][8]
   const float* prefix_lse;
   uint16_t* out;
   float* lse;
