@@ -99,8 +99,8 @@ struct Misc {
     struct {                                       // score CTA
       uint64_t q_ready;                            // the item's queries are in place
       uint64_t s_full[2], s_empty[2];              // score buffers
-      uint64_t staged[2];                          // a half's probabilities are to be sent
-      uint64_t landed[4];                          // they have arrived (tiles in turn)
+      uint64_t staged[4];                          // a half's probabilities are to be sent
+      uint64_t landed[4];                          // they have arrived (both: tiles in turn)
       uint64_t p_empty[6];                         // the value CTA's P buffers are free
       uint64_t sum_full, fin_staged;               // the second half's sums; 1 / sums
     };
@@ -663,7 +663,7 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       ms->factor[buf][row] = static_cast<uint8_t>(drop);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->staged[h]));
+      if (lane == 0) mbar_arrive(smem_u32(&ms->staged[2 * side_of.at + h]));
     }
     // Sums of both halves; 1 / sum (times the values' scale) to the value CTA.  The
     // buffers on both sides are those of the item before the last: its output was
@@ -714,11 +714,12 @@ __device__ void run_sends(const PrefixParams& p, Misc* ms, const Place& at, uint
     for (int j = 0; j < tiles && ok; ++j, ++tile, turn.next(), last = side_of, side_of.next()) {
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
-        ok = ok && mbar_wait_poll(smem_u32(&ms->staged[h]), tile & 1, p.err, kErrSoftmax);
+        ok = ok && mbar_wait_poll(smem_u32(&ms->staged[2 * side_of.at + h]), side_of.lap, p.err,
+                                  kErrSoftmax);
         if (!ok) break;
         const uint32_t buf = 2 * turn.at + h;
-        bulk_to_peer(peer_p + buf * kHalfBytes, smem + kStageAt + (2 * side_of.at + h) * kHalfBytes, kPHalfBytes,
-                     peer_full + 8 * buf);
+        bulk_to_peer(peer_p + buf * kHalfBytes, smem + kStageAt + (2 * side_of.at + h) * kHalfBytes,
+                     kPHalfBytes, peer_full + 8 * buf);
         bulk_to_peer(peer_factor + buf * kFactorBytes, smem_u32(ms->factor[buf]), kFactorBytes,
                      peer_full + 8 * buf);
       }
@@ -747,7 +748,8 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
   const uint32_t landed = dsmem_addr(smem_u32(&ms->landed[half]), at.peer);
   uint32_t side_of = 0;                                  // the sender's staging buffer
   const bool speaker = warp == 0 && lane == 0;
-  Turn<Ring<kPaired>::kPTiles> turn, last;               // last: the tile before
+  Turn<Ring<kPaired>::kPTiles> turn, last, earlier;      // the two tiles before
+  bool second = false;                                   // (there is one)
   for (int it = it0; it < it1; ++it) {
     const PrefixItem w = item_at(p, ms, it, it0);
     const int tiles = tiles_of(w);
@@ -780,12 +782,19 @@ __device__ bool run_output(const PrefixParams& p, Misc* ms, const Place& at, uin
         tc_fence_before();
       }
       arrive_at_first<kPaired, true>(at, &ms->o_ready[turn.at], lane);
+      second = it > it0 || j > 0;
+      earlier = last;
       last = turn;
       turn.next();
       side_of = side_of + 1 == Ring<kPaired>::kStages ? 0 : side_of + 1;
     }
+    // The last PV; first the one before it, since this half's P may be there before
+    // the other half of an earlier tile in the same buffer is through, and the
+    // parities of two laps of a barrier are not to be mixed up.
     const uint32_t side = (it - it0) & 1;
-    if (!all_waited(mbar_wait_poll(smem_u32(&ms->pv_done[last.at]), last.lap, p.err, kErrDrain)) ||
+    if ((second && !all_waited(mbar_wait_poll(smem_u32(&ms->pv_done[earlier.at]), earlier.lap, p.err,
+                                              kErrDrain))) ||
+        !all_waited(mbar_wait_poll(smem_u32(&ms->pv_done[last.at]), last.lap, p.err, kErrDrain)) ||
         !all_waited(mbar_wait_poll(smem_u32(&ms->fin_full[side]), ((it - it0) >> 1) & 1, p.err,
                                    kErrDrain)))
       return false;
@@ -845,6 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         mbar_init(smem_u32(&ms->s_full[i]), 1);
         mbar_init(smem_u32(&ms->s_empty[i]), 8 * R::kCtas);
         mbar_init(smem_u32(&ms->staged[i]), 4);
+        mbar_init(smem_u32(&ms->staged[2 + i]), 4);
         mbar_init(smem_u32(&ms->landed[i]), 1);
         mbar_init(smem_u32(&ms->landed[2 + i]), 1);
       }

@@ -392,6 +392,30 @@ def test_shared_repeats_bit_by_bit(mla):
         mla.mla_shared_check(p, w)
 
 
+@pytest.mark.parametrize("per,q", [(1, "bf16"), (1, "fp8"), (16, "fp8"), (33, "bf16")])
+def test_shared_first_calls_of_plans_on_cold_memory(mla, per, q):
+    """Loads of very different latencies: new workspaces, tables and caches without any
+    of it, the call's kernels all enqueued before the first begins."""
+    c = Case([per], [3001], [17] * per, 8, q, "fp8")
+    rows = c.bs
+    plans = [c.plan(mla) for _ in range(12)]
+    wss = [torch.full((p.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda") for p in plans]
+    outs = [torch.zeros(rows, 16, 512, dtype=torch.bfloat16, device="cuda") for _ in plans]
+    lses = [torch.zeros(rows, 16, device="cuda") for _ in plans]
+    other = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for p, w, o, lse in zip(plans, wss, outs, lses):
+        other.fill_(1)
+        mla.mla_shared_run(p, c.query["q"], c.pool["kv"], o, workspace=w, lse=lse,
+                           q_scale=c.query.get("q_scale"), kv_scale=c.pool["kv_scale"],
+                           prefix_indices=c.prefix_ids, kv_indices=c.own_ids)
+    ref, ref_lse, bound, lse_bound, _ = c.reference()
+    for p, w, o, lse in zip(plans, wss, outs, lses):
+        mla.mla_shared_check(p, w)
+        assert ((o.double() - ref).abs() <= bound).all()
+        assert ((lse.double() - ref_lse).abs() <= lse_bound).all()
+        assert torch.equal(o, outs[0]) and torch.equal(lse, lses[0])
+
+
 def test_shared_captured_and_on_another_stream(mla):
     c = Case([9, 3], [77, 12], [(5 * i) % 40 for i in range(12)], 16, "bf16", "fp8")
     plan = c.plan(mla)
