@@ -732,11 +732,12 @@ mla_status mla_shared_check(const mla_shared* plan, void* workspace, mla_stream_
  *   old_lens, new_lens  device int32 [batch_size]; new_lens NULL = 1 each.
  *   block_table     device int32 [batch_size][table_stride], table_pages columns
  *                   used; column j of row b is the page of tokens j*page_size .. .
- *   bounds          bf16 [num_pages][2][576], 16-byte aligned: the smallest
+ *   bounds          bf16 [num_pages][2][576], 32-byte aligned: the smallest
  *                   values, then the largest, exactly as stored (an e4m3 pool's
  *                   values without kv_scale).  Both are NaN for a dim with a value
  *                   that is not finite.
- * Two requests of a call must not have new tokens in the same page.
+ * A page must not get new tokens from two places of a call (two requests, or two
+ * columns of one).  batch_size x table_pages is below 2^31.
  * On the device: a negative length counts as 0, a page outside the pool or the
  * bounds is skipped (mla_error_check: MLA_ERR_INVALID_ARG), as are pages beyond
  * the table's columns (MLA_ERR_CAPACITY).

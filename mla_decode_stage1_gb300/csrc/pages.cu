@@ -40,7 +40,9 @@ __device__ __forceinline__ void report(int32_t* err, int32_t bits) {
 // A page that had rows before goes on from its bounds, so a step reads its new
 // rows only.
 //
-// Bound: memory, one pass over the new rows; latency for a step of one token.
+// Bound: memory, one pass over the new rows; latency for a step of one token.  The
+// pages of all requests are one list (every CTA adds up the requests' counts, from
+// L2), handed out to the CTAs in turn, so that requests of any lengths are even work.
 
 constexpr uint32_t kPosInf2 = 0x7f807f80u, kNegInf2 = 0xff80ff80u, kNan2 = 0x7fff7fffu;
 constexpr int kBoundThreads = 288;
@@ -57,107 +59,144 @@ struct BoundsParams {
   int32_t table_pages;
   const int32_t* old_lens;
   const int32_t* new_lens;      // null: one new token per request
-  int32_t page_size;
+  int32_t bs, page_size;
   int32_t* err;
 };
 
 template <int KV>
-__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kBoundThreads, KV == MLA_DTYPE_BF16 ? 4 : 3) page_bounds_kernel(const BoundsParams p) {
   constexpr int kPieces = KV == MLA_DTYPE_BF16 ? 72 : KV == MLA_DTYPE_FP8_E4M3 ? 36 : 18;
   constexpr int kRows = kBoundThreads / kPieces;        // rows at a time
   constexpr int kWords = kQkDim / 2 / kPieces;          // bf16 pairs of a piece
-  constexpr int kAhead = KV == MLA_DTYPE_MXFP4 ? 2 : 4;
+  constexpr int kAhead = KV == MLA_DTYPE_BF16 ? 8 : KV == MLA_DTYPE_FP8_E4M3 ? 4 : 2;  // 8: 11.2 us, 4: 12.0
   __shared__ uint32_t part[2][kRows][kQkDim / 2];
-  const int b = blockIdx.x;
-  int64_t old_len = p.old_lens[b], new_len = p.new_lens != nullptr ? p.new_lens[b] : 1;
-  if (old_len < 0 || new_len < 0) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) report(p.err, kErrBadLength);
-    old_len = old_len < 0 ? 0 : old_len;
-    new_len = new_len < 0 ? 0 : new_len;
-  }
-  if (new_len == 0) return;
-  const int64_t len = old_len + new_len;
-  const int64_t first = old_len / p.page_size, end = (len + p.page_size - 1) / p.page_size;
-  if (end > p.table_pages && threadIdx.x == 0 && blockIdx.y == 0) report(p.err, kErrCapacity);
+  __shared__ uint32_t ends[kBoundThreads];               // pages of the requests up to each
+  __shared__ uint32_t warp_sum[kBoundThreads / 32];
   const int piece = threadIdx.x % kPieces, group = threadIdx.x / kPieces;
-  for (int64_t j = first + blockIdx.y; j < end && j < p.table_pages; j += gridDim.y) {
-    const int64_t page = p.table[b * p.table_stride + j];
-    if (page < 0 || page >= p.pages || (page + 1) * p.page_size > p.pool_rows) {
-      if (threadIdx.x == 0) report(p.err, kErrBadPage);
-      continue;
-    }
-    const int r0 = static_cast<int>(j == first ? old_len % p.page_size : 0);
-    const int r1 = static_cast<int>(len - j * p.page_size < p.page_size ? len - j * p.page_size
-                                                                        : p.page_size);
-    uint32_t lo[kWords], hi[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) lo[i] = kPosInf2, hi[i] = kNegInf2;
-    const int64_t row0 = page * p.page_size;
-    for (int r = r0 + group; r < r1; r += kRows * kAhead) {
-      uint4 v[kAhead];
-      uint32_t e[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        // (past the end: this thread's first row again)
-        const int64_t row = row0 + (r + u * kRows < r1 ? r + u * kRows : r);
-        v[u] = ld_nc_na_v4(p.kv + (row * kPieces + piece) * 16);
-        if constexpr (KV == MLA_DTYPE_MXFP4)
-          e[u] = ld_nc_u8_early(p.e8m0 + row * p.e8m0_stride + piece);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t page_size = p.page_size;
+  auto lengths = [&](int b, uint32_t& old_len, uint32_t& new_len) {
+    const int32_t o = p.old_lens[b], n = p.new_lens != nullptr ? p.new_lens[b] : 1;
+    old_len = o < 0 ? 0 : o;
+    new_len = n < 0 ? 0 : n;
+    return o < 0 || n < 0 ? kErrBadLength : 0;
+  };
+  uint32_t mine = blockIdx.x;                            // the next page of the list to do
+  uint32_t before = 0;                                   // pages of the chunks before
+  for (int b0 = 0; b0 < p.bs; b0 += kBoundThreads) {
+    uint32_t count = 0, old_len, new_len;
+    if (b0 + static_cast<int>(threadIdx.x) < p.bs) {
+      int32_t bad = lengths(b0 + threadIdx.x, old_len, new_len);
+      // (their sum may be beyond 31 bits, not beyond 32)
+      const uint32_t end = (old_len + new_len - 1) / page_size + 1;
+      if (new_len > 0) {
+        if (end > static_cast<uint32_t>(p.table_pages)) bad |= kErrCapacity;
+        const uint32_t first = old_len / page_size, last = min(end, static_cast<uint32_t>(p.table_pages));
+        count = last > first ? last - first : 0;
       }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t x[kWords];
-        if constexpr (KV == MLA_DTYPE_BF16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = w[i];
-        } else if constexpr (KV == MLA_DTYPE_FP8_E4M3) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            const __nv_bfloat162 o = __floats2bfloat162_rn(f.x, f.y);
-            x[i] = *reinterpret_cast<const uint32_t*>(&o);
-          }
-        } else {
-          const uint32_t scale = e8m0_to_bf16x2(e[u]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e2m1x4_to_bf16(w[i], scale, x[4 * i], x[4 * i + 1]);
-            e2m1x4_to_bf16(w[i] >> 16, scale, x[4 * i + 2], x[4 * i + 3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          lo[i] = min_nan_bf16x2(lo[i], x[i]);
-          hi[i] = max_nan_bf16x2(hi[i], x[i]);
-        }
-      }
+      if (bad && blockIdx.x == 0) report(p.err, bad);
     }
+    uint32_t sum = count;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      part[0][group][piece * kWords + i] = lo[i];
-      part[1][group][piece * kWords + i] = hi[i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
     }
     __syncthreads();
-    // a thread per pair of dims
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds + page * 2 * kQkDim) + threadIdx.x;
-    uint32_t a = r0 > 0 ? out[0] : kPosInf2, c = r0 > 0 ? out[kQkDim / 2] : kNegInf2;
-#pragma unroll
-    for (int g = 0; g < kRows; ++g) {
-      a = min_nan_bf16x2(a, part[0][g][threadIdx.x]);
-      c = max_nan_bf16x2(c, part[1][g][threadIdx.x]);
-    }
-    // both bounds NaN where either is not finite
-#pragma unroll
-    for (int s = 0; s < 32; s += 16)
-      if (((a >> s) & 0x7f80u) == 0x7f80u || ((c >> s) & 0x7f80u) == 0x7f80u) {
-        a = (a & ~(0xffffu << s)) | (kNan2 & (0xffffu << s));
-        c = (c & ~(0xffffu << s)) | (kNan2 & (0xffffu << s));
-      }
-    out[0] = a;
-    out[kQkDim / 2] = c;
+    if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+    ends[threadIdx.x] = sum;
+    __syncthreads();
+    const uint32_t total = ends[kBoundThreads - 1];
+    for (; mine - before < total; mine += gridDim.x) {
+      // request and column of the page
+      uint32_t at = 0;
+#pragma unroll
+      for (uint32_t step = 256; step > 0; step >>= 1)
+        if (at + step <= kBoundThreads && ends[at + step - 1] <= mine - before) at += step;
+      const int b = b0 + static_cast<int>(at);
+      lengths(b, old_len, new_len);
+      const uint32_t first = old_len / page_size;
+      const uint32_t j = first + mine - before - (at > 0 ? ends[at - 1] : 0);
+      const int64_t page = p.table[b * p.table_stride + j];
+      if (page < 0 || page >= p.pages || (page + 1) * p.page_size > p.pool_rows) {
+        if (threadIdx.x == 0) report(p.err, kErrBadPage);
+        continue;
+      }
+      const int r0 = static_cast<int>(j == first ? old_len % page_size : 0);
+      const int r1 = static_cast<int>(min(old_len + new_len - j * page_size, page_size));
+      uint32_t lo[kWords], hi[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) lo[i] = kPosInf2, hi[i] = kNegInf2;
+      const int64_t row0 = page * p.page_size;
+      for (int r = r0 + group; r < r1; r += kRows * kAhead) {
+        uint4 v[kAhead];
+        uint32_t e[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          // (past the end: this thread's first row again)
+          const int64_t row = row0 + (r + u * kRows < r1 ? r + u * kRows : r);
+          v[u] = ld_nc_na_v4(p.kv + (row * kPieces + piece) * 16);
+          if constexpr (KV == MLA_DTYPE_MXFP4)
+            e[u] = ld_nc_u8_early(p.e8m0 + row * p.e8m0_stride + piece);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          uint32_t x[kWords];
+          if constexpr (KV == MLA_DTYPE_BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = w[i];
+          } else if constexpr (KV == MLA_DTYPE_FP8_E4M3) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))));
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+              const __nv_bfloat162 o = __floats2bfloat162_rn(f.x, f.y);
+              x[i] = *reinterpret_cast<const uint32_t*>(&o);
+            }
+          } else {
+            const uint32_t scale = e8m0_to_bf16x2(e[u]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e2m1x4_to_bf16(w[i], scale, x[4 * i], x[4 * i + 1]);
+              e2m1x4_to_bf16(w[i] >> 16, scale, x[4 * i + 2], x[4 * i + 3]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            lo[i] = min_nan_bf16x2(lo[i], x[i]);
+            hi[i] = max_nan_bf16x2(hi[i], x[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        part[0][group][piece * kWords + i] = lo[i];
+        part[1][group][piece * kWords + i] = hi[i];
+      }
+      __syncthreads();
+      // a thread per pair of dims
+      uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds + page * 2 * kQkDim) + threadIdx.x;
+      uint32_t a = r0 > 0 ? out[0] : kPosInf2, c = r0 > 0 ? out[kQkDim / 2] : kNegInf2;
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) {
+        a = min_nan_bf16x2(a, part[0][g][threadIdx.x]);
+        c = max_nan_bf16x2(c, part[1][g][threadIdx.x]);
+      }
+      // both bounds NaN where either is not finite
+#pragma unroll
+      for (int s = 0; s < 32; s += 16)
+        if (((a >> s) & 0x7f80u) == 0x7f80u || ((c >> s) & 0x7f80u) == 0x7f80u) {
+          a = (a & ~(0xffffu << s)) | (kNan2 & (0xffffu << s));
+          c = (c & ~(0xffffu << s)) | (kNan2 & (0xffffu << s));
+        }
+      out[0] = a;
+      out[kQkDim / 2] = c;
+      __syncthreads();
+    }
+    before += total;
   }
 }
 
@@ -170,10 +209,11 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Bounds
 // a matrix instruction) and 1,152 columns for every page.  No score of a token
 // of the page exceeds it.
 //
-// Bound: memory, 2,304 bytes a page.  A warp holds 8 kTiles pages; a lane loads
-// 16 bytes (8 dims) of a page's bounds, which are its share of two instructions:
-// the order of the sum over d is free, so lane c of a quad takes dims
-// 8 c .. 8 c + 7 of 32, for the queries as well.
+// Bound: memory, 2,304 bytes a page.  A warp holds 8 kTiles pages; a lane loads 32
+// bytes (16 dims) of a page's bounds, a quad whole lines, kAhead steps of 64 dims
+// ahead of their use.  They are its share of four instructions: the order of the sum over d is
+// free, so lane c of a quad takes dims 16 c .. 16 c + 15 of 64, for the queries as
+// well.
 
 constexpr int kScoreWarps = 4;
 constexpr int kQPitch = kQkDim + 8;           // bf16 elements: rows start 4 banks apart
@@ -204,13 +244,21 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 32 bytes, not kept in L1 (read once).
+__device__ __forceinline__ void ld_na_32(const void* ptr, uint32_t (&v)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                 "=r"(v[7])
+               : "l"(ptr));
+}
+
 // Tokens that query token t of a request with n cached tokens sees.
 __device__ __forceinline__ int64_t seen_by(int64_t n, int q_len, int t) {
   const int64_t s = n - q_len + 1 + t;
   return s < 0 ? 0 : s;
 }
 
-template <int kTiles>
+template <int kTiles, int kAhead>
 __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const ScoresParams p) {
   __shared__ __align__(16) uint16_t qs[kHeads * kQPitch];
   const int b = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks, t = blockIdx.y;
@@ -234,6 +282,30 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
       if (cta0 + i < p.columns) out[cta0 + i] = -INFINITY;
     return;
   }
+  const int64_t page0 = cta0 + warp * (8 * kTiles);
+  const int g = lane >> 2, c = lane & 3;
+  const uint16_t* src[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    // (columns past the last: its page again)
+    const int64_t col = page0 + 8 * i + g;
+    int64_t page = p.table[b * p.table_stride + (col < pages ? col : pages - 1)];
+    if (page < 0 || page >= p.pages) {
+      if (c == 0 && col < pages) report(p.err, kErrBadPage);
+      page = 0;
+    }
+    src[i] = p.bounds + page * 2 * kQkDim + 16 * c;
+  }
+  uint32_t lo[kAhead][kTiles][8], hi[kAhead][kTiles][8];
+  auto fetch = [&](int d, int at) {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      ld_na_32(src[i] + 64 * d, lo[at][i]);
+      ld_na_32(src[i] + kQkDim + 64 * d, hi[at][i]);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) fetch(d, d);
   for (int i = threadIdx.x; i < kHeads * kQkDim / 16; i += 32 * kScoreWarps) {
     const int h = i / (kQkDim / 16), d = i % (kQkDim / 16) * 16;
     uint32_t v[8];
@@ -260,58 +332,48 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
     dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
   __syncthreads();
-  const int64_t page0 = cta0 + warp * (8 * kTiles);
-  const int g = lane >> 2, c = lane & 3;
-  const uint4* src[kTiles];
-#pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
-    // (columns past the last: its page again)
-    const int64_t col = page0 + 8 * i + g;
-    int64_t page = p.table[b * p.table_stride + (col < pages ? col : pages - 1)];
-    if (page < 0 || page >= p.pages) {
-      if (c == 0 && col < pages) report(p.err, kErrBadPage);
-      page = 0;
-    }
-    src[i] = reinterpret_cast<const uint4*>(p.bounds + page * 2 * kQkDim) + c;
-  }
-  // The instruction's own sums round towards zero: 12 in a row, then one rounded
+  // The instruction's own sums round towards zero: 8 in a row, then one rounded
   // addition (72 in a row were 1.2e-6 off, against 2e-7).
-  float sum[kTiles][4], acc[kTiles][4];
+  float sum[kTiles][4];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum[i][k] = acc[i][k] = 0.0f;
-  const uint16_t* qa = qs + g * kQPitch + 8 * c;
-#pragma unroll 3
-  for (int d = 0; d < kQkDim / 32; ++d) {
-    uint4 lo[kTiles], hi[kTiles];
+    for (int k = 0; k < 4; ++k) sum[i][k] = 0.0f;
+  const uint16_t* qa = qs + g * kQPitch + 16 * c;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      lo[i] = ld_nc_na_v4(src[i] + 4 * d);
-      hi[i] = ld_nc_na_v4(src[i] + kQkDim / 8 + 4 * d);
+  for (int d = 0; d < kQkDim / 64; ++d) {
+    const int at = d % kAhead;
+    float acc[kTiles][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint4 x = *reinterpret_cast<const uint4*>(qa + 64 * d + 8 * half);
+      const uint4 y = *reinterpret_cast<const uint4*>(qa + 8 * kQPitch + 64 * d + 8 * half);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      uint32_t xp[4], xn[4], yp[4], yn[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        xp[k] = max_nan_bf16x2(xs[k], 0u); xn[k] = min_nan_bf16x2(xs[k], 0u);
+        yp[k] = max_nan_bf16x2(ys[k], 0u); yn[k] = min_nan_bf16x2(ys[k], 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        const uint32_t* h = hi[at][i] + 4 * half;
+        const uint32_t* l = lo[at][i] + 4 * half;
+        mma_16816(acc[i], xp[0], yp[0], xp[1], yp[1], h[0], h[1]);
+        mma_16816(acc[i], xp[2], yp[2], xp[3], yp[3], h[2], h[3]);
+        mma_16816(acc[i], xn[0], yn[0], xn[1], yn[1], l[0], l[1]);
+        mma_16816(acc[i], xn[2], yn[2], xn[3], yn[3], l[2], l[3]);
+      }
     }
-    const uint4 x = *reinterpret_cast<const uint4*>(qa + 32 * d);
-    const uint4 y = *reinterpret_cast<const uint4*>(qa + 8 * kQPitch + 32 * d);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-    uint32_t xp[4], xn[4], yp[4], yn[4];
+    if (d + kAhead < kQkDim / 64) fetch(d + kAhead, at);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      xp[k] = max_nan_bf16x2(xs[k], 0u); xn[k] = min_nan_bf16x2(xs[k], 0u);
-      yp[k] = max_nan_bf16x2(ys[k], 0u); yn[k] = min_nan_bf16x2(ys[k], 0u);
-    }
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      mma_16816(acc[i], xp[0], yp[0], xp[1], yp[1], hi[i].x, hi[i].y);
-      mma_16816(acc[i], xp[2], yp[2], xp[3], yp[3], hi[i].z, hi[i].w);
-      mma_16816(acc[i], xn[0], yn[0], xn[1], yn[1], lo[i].x, lo[i].y);
-      mma_16816(acc[i], xn[2], yn[2], xn[3], yn[3], lo[i].z, lo[i].w);
-      if (d % 3 == 2)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sum[i][k] += acc[i][k];
-          acc[i][k] = 0.0f;
-        }
-    }
+      for (int k = 0; k < 4; ++k) sum[i][k] += acc[i][k];
   }
   float scale = 1.0f / 24.0f;
   if (p.q_scale != nullptr) scale *= *p.q_scale;
@@ -341,13 +403,13 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
 // Kept pages are written in ascending order, from the sum of the earlier rows'
 // counts on.
 //
-// The smallest kept score is found by its 32 bits, 8 at a time from the top: a
-// histogram of the scores that agree with what is known so far says which byte
-// comes next.  A thread holds consecutive columns, so that one scan of the
-// threads' counts places every kept page.  Latency-bound: 4 histograms, 2 scans.
-
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+// A CTA per row.  Up to 512 columns: every score's rank by comparison with all
+// others (in shared memory), which takes fewer steps than anything with a barrier
+// between them.  Beyond: the range of the keys that holds the smallest kept one is
+// cut into 2,048 bins again and again, the scores in it counted, until what is in a
+// bin is kept whole or has one key (2 rounds for scores that are spread, 3 at most).
+// A thread then holds consecutive columns, so that one scan of the threads' counts
+// places every kept page.  Latency-bound.
 
 struct SelectParams {
   const float* scores;
@@ -374,25 +436,15 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-struct SelectShared {
-  uint32_t hist[256];
-  uint32_t warp_sum[2][kSelWarps];
-  uint32_t byte, above;
-  int64_t before;
-};
-
 // Pages that row r sees, with what is wrong with its length.
-__device__ __forceinline__ int64_t pages_of_row(const SelectParams& p, int64_t r, int64_t* seen,
-                                                int32_t* bad) {
-  int64_t n = p.lens[r / p.q_len];
-  *bad = 0;
-  if (n < 0) {
-    *bad = kErrBadLength;
-    n = 0;
-  }
-  int64_t s = seen_by(n, p.q_len, static_cast<int>(r % p.q_len));
-  int64_t pages = (s + p.page_size - 1) / p.page_size;
-  if (pages > p.columns) {
+__device__ __forceinline__ uint32_t pages_of_row(const SelectParams& p, uint32_t r, uint32_t* seen,
+                                                 int32_t* bad) {
+  const uint32_t b = r / p.q_len, t = r % p.q_len;
+  const int32_t n = p.lens[b];
+  *bad = n < 0 ? kErrBadLength : 0;
+  uint32_t s = static_cast<uint32_t>(seen_by(n < 0 ? 0 : n, p.q_len, t));
+  uint32_t pages = (s + p.page_size - 1) / p.page_size;
+  if (pages > static_cast<uint32_t>(p.columns)) {
     *bad = kErrCapacity;
     pages = p.columns;
     s = pages * p.page_size;
@@ -401,9 +453,20 @@ __device__ __forceinline__ int64_t pages_of_row(const SelectParams& p, int64_t r
   return pages;
 }
 
-// Exclusive sums over the CTA of two counts, and their totals.
-__device__ __forceinline__ void scan2(SelectShared& sh, uint32_t a, uint32_t b, uint32_t& ea,
-                                      uint32_t& eb, uint32_t& ta, uint32_t& tb) {
+template <int kThreads>
+struct SelectShared {
+  static constexpr int kBins = 2048;
+  uint32_t hist[kBins];
+  uint32_t warp_sum[2][32];
+  uint32_t least, most, bin, above, inside;
+  unsigned long long before;
+};
+
+// Exclusive sums over the CTA of two counts.
+template <int kThreads>
+__device__ __forceinline__ void scan2(SelectShared<kThreads>& sh, uint32_t a, uint32_t b,
+                                      uint32_t& ea, uint32_t& eb) {
+  constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t ia = a, ib = b;
 #pragma unroll
@@ -411,115 +474,213 @@ __device__ __forceinline__ void scan2(SelectShared& sh, uint32_t a, uint32_t b, 
     const uint32_t x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ib, o);
     if (lane >= o) ia += x, ib += y;
   }
-  __syncthreads();
   if (lane == 31) sh.warp_sum[0][warp] = ia, sh.warp_sum[1][warp] = ib;
   __syncthreads();
-  ta = tb = 0;
-  ea = ia - a;
-  eb = ib - b;
+  // every warp adds up the warps before it
+  uint32_t x = lane < warp ? sh.warp_sum[0][lane] : 0, y = lane < warp ? sh.warp_sum[1][lane] : 0;
+  static_assert(kWarps <= 32, "a lane per warp");
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    if (w < warp) ea += sh.warp_sum[0][w], eb += sh.warp_sum[1][w];
-    ta += sh.warp_sum[0][w];
-    tb += sh.warp_sum[1][w];
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
   }
+  ea = x + ia - a;
+  eb = y + ib - b;
 }
 
-__global__ void __launch_bounds__(kSelThreads) page_select_kernel(const SelectParams p) {
-  __shared__ SelectShared sh;
-  const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x;
-  int64_t seen;
+// Columns that the counting form takes.
+constexpr uint32_t kCountColumns = 512;
+constexpr uint32_t kKeysInShared = 32768;      // 128 KB
+
+template <int kThreads, bool kCount>
+__global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectParams p) {
+  using Sh = SelectShared<kThreads>;
+  __shared__ Sh sh;
+  extern __shared__ uint32_t keys[];           // of the columns between, while they fit
+  const uint32_t r = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t seen;
   int32_t bad;
-  const int64_t n = pages_of_row(p, r, &seen, &bad);
-  if (bad && tid == 0) report(p.err, bad);
-  const int64_t kept = n < p.top ? n : p.top;
-  // entries of the rows before
-  if (tid == 0) sh.before = 0;
+  const uint32_t n = pages_of_row(p, r, &seen, &bad);
+  const uint32_t top = p.top, kept = n < top ? n : top;
+  const uint32_t lo = p.first, hi = n - p.last;          // the columns between (of n > top)
+  const uint32_t m = n > top ? hi - lo : 0;
+  const float* scores = p.scores + r * p.scores_stride;
+  if (tid == 0) {
+    sh.before = 0;
+    sh.least = 0xffffffffu;
+    sh.most = 0;
+    if (bad) report(p.err, bad);
+  }
+  if constexpr (!kCount)
+    for (int i = tid; i < Sh::kBins; i += kThreads) sh.hist[i] = 0;
   __syncthreads();
+  // entries of the rows before
   {
-    int64_t mine = 0;
-    for (int64_t i = tid; i < r; i += kSelThreads) {
-      int64_t s;
+    uint32_t mine = 0;
+    for (uint32_t i = tid; i < r; i += kThreads) {
+      uint32_t s;
       int32_t w;
-      const int64_t m = pages_of_row(p, i, &s, &w);
-      mine += m < p.top ? m : p.top;
+      const uint32_t k = pages_of_row(p, i, &s, &w);
+      mine += k < top ? k : top;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if ((tid & 31) == 0 && mine)
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.before), static_cast<unsigned long long>(mine));
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0 && mine) atomicAdd(&sh.before, static_cast<unsigned long long>(mine));
+  }
+  // the keys, and their range
+  const bool held = kCount || m <= kKeysInShared;
+  {
+    uint32_t least = 0xffffffffu, most = 0;
+    for (uint32_t i = tid; i < m; i += kThreads) {
+      const uint32_t k = key_of(scores[lo + i]);
+      if (held) keys[i] = k;
+      least = min(least, k);
+      most = max(most, k);
+    }
+    if constexpr (!kCount) {
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) {
+        atomicMin(&sh.least, least);
+        atomicMax(&sh.most, most);
+      }
+    }
   }
   __syncthreads();
-  const int64_t before = sh.before;
+  const int64_t before = static_cast<int64_t>(sh.before);
   if (tid == 0) {
     if (r == 0) p.kv_indptr[0] = 0;
     p.kv_indptr[r + 1] = static_cast<int32_t>(before + kept);
     p.last_page[r] = static_cast<int32_t>(n > 0 ? seen - (n - 1) * p.page_size : 0);
     if (before + kept > p.max_indices) report(p.err, kErrCapacity);
   }
-  const float* scores = p.scores + r * p.scores_stride;
   const int32_t* table = p.table + r / p.q_len * p.table_stride;
-  int32_t* cols = p.kept_columns != nullptr ? p.kept_columns + r * p.top : nullptr;
-  auto put = [&](int64_t rank, int64_t col) {
+  int32_t* cols = p.kept_columns != nullptr ? p.kept_columns + static_cast<int64_t>(r) * top : nullptr;
+  auto put = [&](uint32_t rank, uint32_t col) {
     if (before + rank < p.max_indices) p.kv_indices[before + rank] = table[col];
     if (cols != nullptr) cols[rank] = static_cast<int32_t>(col);
   };
   if (cols != nullptr)
-    for (int64_t i = kept + tid; i < p.top; i += kSelThreads) cols[i] = -1;
-  if (n <= p.top) {
-    for (int64_t i = tid; i < n; i += kSelThreads) put(i, i);
+    for (uint32_t i = kept + tid; i < top; i += kThreads) cols[i] = -1;
+  if (n <= top) {
+    for (uint32_t i = tid; i < n; i += kThreads) put(i, i);
     return;
   }
-  const int64_t lo = p.first, hi = n - p.last;
-  uint32_t need = static_cast<uint32_t>(p.top - p.first - p.last);     // of the columns between
-  uint32_t prefix = 0;
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) sh.hist[i] = 0;
-    __syncthreads();
-    for (int64_t i = lo + tid; i < hi; i += kSelThreads) {
-      const uint32_t k = key_of(scores[i]);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+  const uint32_t need = top - p.first - p.last;          // of the columns between
+  for (uint32_t i = tid; i < lo; i += kThreads) put(i, i);
+  for (uint32_t i = hi + tid; i < n; i += kThreads) put(top - n + i, i);
+  if (need == 0) return;
+  if constexpr (kCount) {
+    // a thread for two columns: how many keys are larger, or equal and before it
+    constexpr uint32_t kPer = kCountColumns / kThreads;
+    uint32_t k[kPer], rank[kPer];
+#pragma unroll
+    for (uint32_t u = 0; u < kPer; ++u) {
+      const uint32_t i = kPer * tid + u;
+      k[u] = i < m ? keys[i] : 0u;
+      rank[u] = 0;
     }
-    __syncthreads();
-    // byte v: fewer than `need` scores lie above it, at least `need` from it on
-    uint32_t ea, eb, ta, tb;
-    const uint32_t mine = sh.hist[255 - tid];              // thread t: byte 255 - t
-    scan2(sh, mine, 0, ea, eb, ta, tb);
-    if (ea < need && ea + mine >= need) {
-      sh.byte = 255 - tid;
-      sh.above = ea;
+    const uint32_t mine = kPer * tid;
+#pragma unroll 8
+    for (uint32_t i = 0; i < m; ++i) {
+      const uint32_t x = keys[i];
+#pragma unroll
+      for (uint32_t u = 0; u < kPer; ++u) rank[u] += x > k[u] || (x == k[u] && i < mine + u);
     }
-    __syncthreads();
-    prefix |= sh.byte << shift;
-    need -= sh.above;
-    __syncthreads();
+    uint32_t take = 0;
+#pragma unroll
+    for (uint32_t u = 0; u < kPer; ++u) take += mine + u < m && rank[u] < need;
+    uint32_t at, none;
+    scan2(sh, take, 0, at, none);
+    at += lo;
+#pragma unroll
+    for (uint32_t u = 0; u < kPer; ++u)
+      if (mine + u < m && rank[u] < need) put(at++, lo + mine + u);
+    return;
   }
-  // `need` of the columns with the key `prefix` are kept, and all above it
-  // (need 0 from the start: none)
-  const bool none = p.top == p.first + p.last;
-  uint32_t run_above = 0, run_equal = 0;
-  for (int64_t base = 0; base < n; base += kSelThreads) {
-    const int64_t i = base + tid;
-    uint32_t above = 0, equal = 0;
-    if (i < n) {
-      if (i < lo || i >= hi) {
-        above = 1;
-      } else if (!none) {
-        const uint32_t k = key_of(scores[i]);
-        above = k > prefix;
-        equal = k == prefix;
+  auto key = [&](uint32_t i) { return held ? keys[i] : key_of(scores[lo + i]); };
+  // All keys above b are kept, and `left` of those in [a, b].
+  uint32_t a = sh.least, b = sh.most, left = need;
+  bool whole = left == m;                                // those in [a, b] all are
+  while (!whole && a < b) {
+    const int shift = max(0, 21 - __clz(b - a));         // (b - a) >> shift < 2048
+    for (uint32_t i = tid; i < m; i += kThreads) {
+      const uint32_t k = key(i);
+      if (k >= a && k <= b) atomicAdd(&sh.hist[(k - a) >> shift], 1u);
+    }
+    __syncthreads();
+    // bins from the top: thread t holds the t-th part of them
+    constexpr int kPer = Sh::kBins / kThreads;
+    uint32_t c[kPer], sum = 0, above, none;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      c[u] = sh.hist[Sh::kBins - 1 - (kPer * tid + u)];
+      sum += c[u];
+    }
+    scan2(sh, sum, 0, above, none);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      if (above < left && above + c[u] >= left) {
+        sh.bin = Sh::kBins - 1 - (kPer * tid + u);
+        sh.above = above;
+        sh.inside = c[u];
       }
+      above += c[u];
+      sh.hist[Sh::kBins - 1 - (kPer * tid + u)] = 0;
     }
-    uint32_t ea, eb, ta, tb;
-    scan2(sh, above, equal, ea, eb, ta, tb);
-    ea += run_above;
-    eb += run_equal;
-    if (above || (equal && eb < need)) put(ea + (eb < need ? eb : need), i);
-    run_above += ta;
-    run_equal += tb;
+    __syncthreads();
+    a += sh.bin << shift;
+    if (b - a >= (1u << shift)) b = a + (1u << shift) - 1;
+    left -= sh.above;
+    whole = sh.inside == left;
+    __syncthreads();
   }
+  // Kept: keys above b, and in [a, b] all, or the first `left` of one key.
+  uint32_t run_above = 0, run_in = 0;
+  for (uint32_t base = 0; base < m; base += kThreads * 32) {
+    // consecutive columns of a thread, an odd number (banks)
+    const uint32_t count = min(m - base, static_cast<uint32_t>(kThreads * 32));
+    const uint32_t per = min(((count + kThreads - 1) / kThreads) | 1u, 33u);
+    const uint32_t i0 = base + per * tid, i1 = min(i0 + per, base + count);
+    uint32_t na = 0, ni = 0;
+    for (uint32_t i = i0; i < i1; ++i) {
+      const uint32_t k = key(i);
+      na += k > b;
+      ni += k >= a && k <= b;
+    }
+    uint32_t ea, ei;
+    scan2(sh, na, ni, ea, ei);
+    ea += run_above;
+    ei += run_in;
+    for (uint32_t i = i0; i < i1; ++i) {
+      const uint32_t k = key(i);
+      const bool in = k >= a && k <= b;
+      if (k > b || (in && ei < left)) put(lo + ea + min(ei, left), lo + i);
+      ea += k > b;
+      ei += in;
+    }
+    if (base + count < m) {
+      // totals, for the next part
+      __syncthreads();
+      if (tid == kThreads - 1) sh.above = ea, sh.inside = ei;
+      __syncthreads();
+      run_above = sh.above;
+      run_in = sh.inside;
+    }
+  }
+}
+
+template <int kThreads, bool kCount>
+cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
+  const uint32_t between = p.columns;
+  const uint32_t bytes = 4 * (kCount ? kCountColumns : std::min(between, kKeysInShared));
+  if (bytes > 32768) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        page_select_kernel<kThreads, kCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kKeysInShared);
+    if (e != cudaSuccess) return e;
+  }
+  page_select_kernel<kThreads, kCount><<<static_cast<unsigned>(p.rows), kThreads, bytes, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -545,15 +706,17 @@ extern "C" mla_status mla_page_bounds(const void* kv, mla_dtype kv_dtype, const 
     return MLA_ERR_INVALID_ARG;
   if (kv_dtype == MLA_DTYPE_MXFP4 && (kv_e8m0 == nullptr || kv_e8m0_row_stride < 18))
     return MLA_ERR_INVALID_ARG;
-  if (!mla::ptr_aligned(kv, 16) || !mla::ptr_aligned(bounds, 16) || !mla::ptr_aligned(old_lens, 4) ||
+  if (!mla::ptr_aligned(kv, 16) || !mla::ptr_aligned(bounds, 32) || !mla::ptr_aligned(old_lens, 4) ||
       !mla::ptr_aligned(new_lens, 4) || !mla::ptr_aligned(err, 4))
     return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(batch_size) * table_pages > INT32_MAX) return MLA_ERR_INVALID_ARG;
   if (table_pages == 0) table_stride = 0;
   mla::BoundsParams p{static_cast<const uint8_t*>(kv), kv_e8m0, kv_e8m0_row_stride, kv_pool_rows,
                       static_cast<uint16_t*>(bounds), num_pages, block_table, table_stride,
-                      table_pages, old_lens, new_lens, page_size, err};
-  const int32_t slices = std::max(1, std::min(table_pages, 1216 / std::min(batch_size, 1216)));
-  const dim3 grid(batch_size, slices);
+                      table_pages, old_lens, new_lens, batch_size, page_size, err};
+  // (at most 8 CTAs an SM; the number of pages is known on the device only)
+  const int64_t most = static_cast<int64_t>(batch_size) * std::max(table_pages, 1);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, 1216)));
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (kv_dtype == MLA_DTYPE_BF16)
     mla::page_bounds_kernel<MLA_DTYPE_BF16><<<grid, mla::kBoundThreads, 0, stream>>>(p);
@@ -576,25 +739,27 @@ extern "C" mla_status mla_page_scores(const void* q, mla_dtype q_dtype, const fl
     return MLA_ERR_INVALID_ARG;
   if (q_dtype != MLA_DTYPE_BF16 && q_dtype != MLA_DTYPE_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
   if (q_dtype == MLA_DTYPE_FP8_E4M3 && q_scale == nullptr) return MLA_ERR_INVALID_ARG;
-  if (!mla::ptr_aligned(q, 16) || !mla::ptr_aligned(bounds, 16) || !mla::ptr_aligned(lens, 4) ||
+  if (!mla::ptr_aligned(q, 16) || !mla::ptr_aligned(bounds, 32) || !mla::ptr_aligned(lens, 4) ||
       !mla::ptr_aligned(scores, 4) || !mla::ptr_aligned(q_scale, 4) ||
       !mla::ptr_aligned(kv_scale, 4) || !mla::ptr_aligned(err, 4))
     return MLA_ERR_INVALID_ARG;
   if (table_pages == 0) return MLA_OK;
-  mla::ScoresParams p{q, q_dtype == MLA_DTYPE_FP8_E4M3 ? 1 : 0, q_dtype == MLA_DTYPE_FP8_E4M3 ? q_scale : nullptr,
-                      kv_scale, static_cast<const uint16_t*>(bounds), num_pages, block_table,
+  const bool fp8 = q_dtype == MLA_DTYPE_FP8_E4M3;
+  mla::ScoresParams p{q, fp8 ? 1 : 0, fp8 ? q_scale : nullptr, kv_scale, static_cast<const uint16_t*>(bounds), num_pages, block_table,
                       table_stride, table_pages, lens, page_size, q_len, scores, scores_stride, 0, err};
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   constexpr int32_t kPages = mla::kScoreWarps * 8;
   const int64_t rows = static_cast<int64_t>(batch_size) * q_len;
-  const bool wide = rows * table_pages >= 152 * 8 * kPages;
+  // A tile a warp while all CTAs are on the machine at once (4 an SM): 32,768 pages
+  // take 18.7 us in 1,024 such CTAs, 16.4 in 256 of four tiles a warp (two an SM).
+  const bool wide = rows * ((table_pages - 1) / kPages + 1) > 4 * 152;
   p.chunks = (table_pages - 1) / (wide ? 4 * kPages : kPages) + 1;
   if (static_cast<int64_t>(p.chunks) * batch_size > INT32_MAX) return MLA_ERR_INVALID_ARG;
   const dim3 grid(p.chunks * batch_size, q_len);
   if (wide)
-    mla::page_scores_kernel<4><<<grid, 32 * mla::kScoreWarps, 0, stream>>>(p);
+    mla::page_scores_kernel<4, 3><<<grid, 32 * mla::kScoreWarps, 0, stream>>>(p);
   else
-    mla::page_scores_kernel<1><<<grid, 32 * mla::kScoreWarps, 0, stream>>>(p);
+    mla::page_scores_kernel<1, 4><<<grid, 32 * mla::kScoreWarps, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
@@ -622,7 +787,10 @@ extern "C" mla_status mla_page_select(const float* scores, int64_t scores_stride
   mla::SelectParams p{scores, scores_stride, block_table, table_stride, table_pages, lens,
                       page_size, q_len, rows, top_pages, first_pages, last_pages, kv_indptr,
                       kv_last_page_len, kv_indices, max_indices, columns, err};
-  mla::page_select_kernel<<<static_cast<unsigned>(rows), mla::kSelThreads, 0,
-                            reinterpret_cast<cudaStream_t>(stream_)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const cudaError_t e = table_pages <= static_cast<int32_t>(mla::kCountColumns)
+                            ? mla::launch_select<256, true>(p, stream)
+                        : table_pages <= 4096 ? mla::launch_select<256, false>(p, stream)
+                                              : mla::launch_select<1024, false>(p, stream);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

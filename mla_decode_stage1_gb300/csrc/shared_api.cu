@@ -4,7 +4,6 @@
 // declarations and their contracts are in include/mla_decode.h.
 
 #include <algorithm>
-#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -49,8 +48,9 @@ constexpr int32_t kTokensPerBlock = mla::kSpRows / mla::kHeads;
 
 // What an item costs beside its tiles, in tiles: the queries' way into tensor
 // memory, the first scores and the last values without the other half's work
-// beside them, and the output.
-constexpr int64_t kItemCost = 2;
+// beside them, and the output take 20,000 cycles.  (256 requests on 8192 tokens:
+// 87 us with 2, 85 with 5, 83 with 8.)
+constexpr int64_t kItemCost = 8;
 
 struct Block {
   int32_t q_row, rows, key0, keys;   // key0: row or key of the group's first key
@@ -108,9 +108,11 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t cluster
   P->num_slots = static_cast<int32_t>(P->items.size());
 }
 
-// Whether to work in blocks of 256 rows, and on how many clusters.  A tile takes
-// 2,400 cycles on a paired cluster and 3,150 on another, but blocks of 256 rows may
-// leave half of one empty, and fewer CTAs have a place in clusters of four.
+// Whether to work in blocks of 256 rows, and on how many clusters.  A tile of 128
+// keys takes 2,600 cycles on a paired cluster and 3,300 on another (3,900 with boxes
+// of 64 keys), but blocks of 256 rows may leave half of one empty, and 36 clusters of
+// four have a place where 76 of two have.  64 requests of a 32,768-token prefix: 73 us
+// paired, 87 not; 5 to 19 requests of three prefixes: 40 us paired, 39 not.
 void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
                  bool whole_device) {
   int32_t on_device[2] = {P->num_sms / 2, P->num_sms / 4};
@@ -124,11 +126,11 @@ void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* pref
     const int64_t keys = (static_cast<int64_t>(prefix_indptr[g + 1]) - prefix_indptr[g]) * P->page_size;
     const int64_t tokens = static_cast<int64_t>(group_indptr[g + 1] - group_indptr[g]) * P->q_len;
     const double tiles = static_cast<double>((keys + mla::kSpTile - 1) / mla::kSpTile);
-    time[0] += tiles * static_cast<double>((tokens + kTokensPerBlock - 1) / kTokensPerBlock) * 3150;
-    time[1] += tiles * static_cast<double>((tokens + 2 * kTokensPerBlock - 1) / (2 * kTokensPerBlock)) * 2400;
+    time[0] += tiles * static_cast<double>((tokens + kTokensPerBlock - 1) / kTokensPerBlock) *
+               (P->direct && P->page_size % mla::kSpTile != 0 ? 3900 : 3300);
+    time[1] += tiles * static_cast<double>((tokens + 2 * kTokensPerBlock - 1) / (2 * kTokensPerBlock)) * 2600;
   }
   P->paired = on_device[1] > 0 && time[1] / std::max(1, on_device[1]) < time[0] / std::max(1, on_device[0]);
-  if (const char* e = getenv("MLA_PAIRED")) P->paired = atoi(e) != 0;
   P->blocks = P->paired ? 2 : 1;
   P->tall = !P->paired && (!P->direct || P->page_size % mla::kSpTile == 0);
   P->num_clusters = std::max(1, on_device[P->paired]);
