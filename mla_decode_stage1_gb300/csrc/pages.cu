@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kBoundThreads, KV == MLA_DTYPE_BF16 ? 4 : 3) p
         part[1][group][piece * kWords + i] = hi[i];
       }
       __syncthreads();
-      // a thread per pair of dims
+      // a thread per pair of dims for what the page has
       uint32_t* out = reinterpret_cast<uint32_t*>(p.bounds + page * 2 * kQkDim) + threadIdx.x;
       uint32_t a = r0 > 0 ? out[0] : kPosInf2, c = r0 > 0 ? out[kQkDim / 2] : kNegInf2;
 #pragma unroll
@@ -264,6 +264,14 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
   const int b = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks, t = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(b) * p.q_len + t;
+  const int64_t cta0 = static_cast<int64_t>(chunk) * (kScoreWarps * 8 * kTiles);
+  const int64_t page0 = cta0 + warp * (8 * kTiles);
+  const int g = lane >> 2, c = lane & 3;
+  // (read beside the length; what is behind it is not looked at)
+  int32_t entry[kTiles];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+    entry[i] = p.table[b * p.table_stride + min(page0 + 8 * i + g, static_cast<int64_t>(p.columns - 1))];
   int64_t n = p.lens[b];
   const bool first_cta = chunk == 0 && t == 0 && threadIdx.x == 0;
   if (n < 0) {
@@ -276,32 +284,28 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
     pages = p.columns;
   }
   float* out = p.scores + row * p.scores_stride;
-  const int64_t cta0 = static_cast<int64_t>(chunk) * (kScoreWarps * 8 * kTiles);
   if (cta0 >= pages) {
     for (int i = threadIdx.x; i < kScoreWarps * 8 * kTiles; i += 32 * kScoreWarps)
       if (cta0 + i < p.columns) out[cta0 + i] = -INFINITY;
     return;
   }
-  const int64_t page0 = cta0 + warp * (8 * kTiles);
-  const int g = lane >> 2, c = lane & 3;
-  const uint16_t* src[kTiles];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    // (columns past the last: its page again)
-    const int64_t col = page0 + 8 * i + g;
-    int64_t page = p.table[b * p.table_stride + (col < pages ? col : pages - 1)];
-    if (page < 0 || page >= p.pages) {
-      if (c == 0 && col < pages) report(p.err, kErrBadPage);
-      page = 0;
+    // (columns past the last: page 0)
+    if (page0 + 8 * i + g >= pages) entry[i] = 0;
+    if (entry[i] < 0 || entry[i] >= p.pages) {
+      if (c == 0) report(p.err, kErrBadPage);
+      entry[i] = 0;
     }
-    src[i] = p.bounds + page * 2 * kQkDim + 16 * c;
   }
+  const uint16_t* bounds = p.bounds + 16 * c;
   uint32_t lo[kAhead][kTiles][8], hi[kAhead][kTiles][8];
   auto fetch = [&](int d, int at) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
-      ld_na_32(src[i] + 64 * d, lo[at][i]);
-      ld_na_32(src[i] + kQkDim + 64 * d, hi[at][i]);
+      const uint16_t* src = bounds + static_cast<int64_t>(entry[i]) * (2 * kQkDim) + 64 * d;
+      ld_na_32(src, lo[at][i]);
+      ld_na_32(src + kQkDim, hi[at][i]);
     }
   };
 #pragma unroll
@@ -403,13 +407,18 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
 // Kept pages are written in ascending order, from the sum of the earlier rows'
 // counts on.
 //
-// A CTA per row.  Up to 512 columns: every score's rank by comparison with all
+// A CTA per row.  Up to 256 columns: every score's rank by comparison with all
 // others (in shared memory), which takes fewer steps than anything with a barrier
 // between them.  Beyond: the range of the keys that holds the smallest kept one is
 // cut into 2,048 bins again and again, the scores in it counted, until what is in a
 // bin is kept whole or has one key (2 rounds for scores that are spread, 3 at most).
 // A thread then holds consecutive columns, so that one scan of the threads' counts
-// places every kept page.  Latency-bound.
+// places every kept column, in the pages' place; their pages come last, with all
+// loads of them under way at once.
+//
+// Bound: latency, of loads that wait for one another above all: the scores (and for
+// short rows the pages) are read beside the lengths.  256 rows of 128 columns 5.6 us,
+// one of 16,384 15 us (2 us of either is the launch).
 
 struct SelectParams {
   const float* scores;
@@ -453,13 +462,14 @@ __device__ __forceinline__ uint32_t pages_of_row(const SelectParams& p, uint32_t
   return pages;
 }
 
+constexpr int kBins = 2048;
 template <int kThreads>
 struct SelectShared {
-  static constexpr int kBins = 2048;
-  uint32_t hist[kBins];
   uint32_t warp_sum[2][32];
-  uint32_t least, most, bin, above, inside;
-  unsigned long long before;
+  // per warp: smallest and largest key, entries of the rows before
+  uint32_t least[kThreads / 32], most[kThreads / 32];
+  unsigned long long before[kThreads / 32];
+  uint32_t bin, above, inside;
 };
 
 // Exclusive sums over the CTA of two counts.
@@ -489,32 +499,40 @@ __device__ __forceinline__ void scan2(SelectShared<kThreads>& sh, uint32_t a, ui
 }
 
 // Columns that the counting form takes.
-constexpr uint32_t kCountColumns = 512;
+constexpr uint32_t kCountColumns = 256;
 constexpr uint32_t kKeysInShared = 32768;      // 128 KB
 
 template <int kThreads, bool kCount>
 __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectParams p) {
-  using Sh = SelectShared<kThreads>;
-  __shared__ Sh sh;
-  extern __shared__ uint32_t keys[];           // of the columns between, while they fit
+  constexpr uint32_t kEarly = kCount ? kCountColumns / kThreads : 8;
+  constexpr int kWarps = kThreads / 32;
+  __shared__ SelectShared<kThreads> sh;
+  extern __shared__ __align__(16) uint32_t dynamic[];
+  uint32_t* hist = dynamic;
+  uint32_t* keys = dynamic + (kCount ? 0 : kBins);       // of the columns, while they fit
   const uint32_t r = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float* scores = p.scores + r * p.scores_stride;
+  const int32_t* table = p.table + r / p.q_len * p.table_stride;
+  const uint32_t columns = p.columns;
+  // The first columns of a thread, read beside the length: what is behind it is not
+  // looked at.
+  float early[kEarly];
+  int32_t entry[kEarly];
+#pragma unroll
+  for (uint32_t u = 0; u < kEarly; ++u) {
+    const uint32_t i = tid + u * kThreads;
+    early[u] = i < columns ? scores[i] : 0.0f;
+    if constexpr (kCount) entry[u] = i < columns ? table[i] : 0;
+  }
   uint32_t seen;
   int32_t bad;
   const uint32_t n = pages_of_row(p, r, &seen, &bad);
   const uint32_t top = p.top, kept = n < top ? n : top;
-  const uint32_t lo = p.first, hi = n - p.last;          // the columns between (of n > top)
-  const uint32_t m = n > top ? hi - lo : 0;
-  const float* scores = p.scores + r * p.scores_stride;
-  if (tid == 0) {
-    sh.before = 0;
-    sh.least = 0xffffffffu;
-    sh.most = 0;
-    if (bad) report(p.err, bad);
-  }
-  if constexpr (!kCount)
-    for (int i = tid; i < Sh::kBins; i += kThreads) sh.hist[i] = 0;
-  __syncthreads();
+  const bool all = n <= top;
+  // the columns between (of n > top)
+  const uint32_t lo = all ? 0 : p.first, hi = all ? 0 : n - p.last, m = hi - lo;
+  if (tid == 0 && bad) report(p.err, bad);
   // entries of the rows before
   {
     uint32_t mine = 0;
@@ -525,158 +543,236 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectParam
       mine += k < top ? k : top;
     }
     mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0 && mine) atomicAdd(&sh.before, static_cast<unsigned long long>(mine));
+    if (lane == 0) sh.before[warp] = mine;
   }
-  // the keys, and their range
-  const bool held = kCount || m <= kKeysInShared;
-  {
+  // the keys, and the range of those between
+  const bool held = kCount || n <= kKeysInShared;
+  if constexpr (kCount) {
+#pragma unroll
+    for (uint32_t u = 0; u < kEarly; ++u) {
+      const uint32_t i = tid + u * kThreads;
+      keys[i] = i >= lo && i < hi ? key_of(early[u]) : 0u;    // (no score's key)
+    }
+  } else {
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     uint32_t least = 0xffffffffu, most = 0;
-    for (uint32_t i = tid; i < m; i += kThreads) {
-      const uint32_t k = key_of(scores[lo + i]);
-      if (held) keys[i] = k;
-      least = min(least, k);
-      most = max(most, k);
-    }
-    if constexpr (!kCount) {
-      least = __reduce_min_sync(0xffffffffu, least);
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (lane == 0) {
-        atomicMin(&sh.least, least);
-        atomicMax(&sh.most, most);
+    auto take = [&](uint32_t i, float s) {
+      const uint32_t k = key_of(s);
+      if (held && i < n) keys[i] = k;
+      if (i >= lo && i < hi) {
+        least = min(least, k);
+        most = max(most, k);
       }
+    };
+#pragma unroll
+    for (uint32_t u = 0; u < kEarly; ++u) take(tid + u * kThreads, early[u]);
+    for (uint32_t i = tid + kEarly * kThreads; i < hi; i += 8 * kThreads) {
+      float s[8];
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u) s[u] = i + u * kThreads < n ? scores[i + u * kThreads] : 0.0f;
+#pragma unroll
+      for (uint32_t u = 0; u < 8; ++u) take(i + u * kThreads, s[u]);
     }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) sh.least[warp] = least, sh.most[warp] = most;
   }
   __syncthreads();
-  const int64_t before = static_cast<int64_t>(sh.before);
+  int64_t before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) before += sh.before[w];
   if (tid == 0) {
     if (r == 0) p.kv_indptr[0] = 0;
     p.kv_indptr[r + 1] = static_cast<int32_t>(before + kept);
     p.last_page[r] = static_cast<int32_t>(n > 0 ? seen - (n - 1) * p.page_size : 0);
     if (before + kept > p.max_indices) report(p.err, kErrCapacity);
   }
-  const int32_t* table = p.table + r / p.q_len * p.table_stride;
   int32_t* cols = p.kept_columns != nullptr ? p.kept_columns + static_cast<int64_t>(r) * top : nullptr;
-  auto put = [&](uint32_t rank, uint32_t col) {
-    if (before + rank < p.max_indices) p.kv_indices[before + rank] = table[col];
-    if (cols != nullptr) cols[rank] = static_cast<int32_t>(col);
-  };
   if (cols != nullptr)
     for (uint32_t i = kept + tid; i < top; i += kThreads) cols[i] = -1;
-  if (n <= top) {
-    for (uint32_t i = tid; i < n; i += kThreads) put(i, i);
+  const uint32_t need = top - p.first - p.last;          // of the columns between (n > top)
+  if constexpr (kCount) {
+    // a column's rank: how many of those between have a larger key, or an equal one and
+    // stand before it; 32 columns at a time, which but for a warp's own are all before
+    // it or all behind
+    uint32_t rank[kEarly];
+#pragma unroll
+    for (uint32_t u = 0; u < kEarly; ++u) {
+      uint32_t part[4] = {0, 0, 0, 0};
+      rank[u] = 0;
+      const uint32_t own = warp + u * kWarps;
+      if (all || 32 * own >= hi || 32 * own + 32 <= lo) continue;
+      const uint32_t k = keys[tid + u * kThreads], below = k - 1;
+      for (uint32_t g = lo / 32; 32 * g < hi; ++g) {
+        const uint4* x = reinterpret_cast<const uint4*>(keys + 32 * g);
+        if (g == own) {
+#pragma unroll
+          for (uint32_t i = 0; i < 32; ++i) part[i % 4] += keys[32 * g + i] > (i < lane ? below : k);
+        } else {
+          const uint32_t limit = g < own ? below : k;
+#pragma unroll
+          for (uint32_t i = 0; i < 8; ++i) {
+            const uint4 v = x[i];
+            part[0] += v.x > limit;
+            part[1] += v.y > limit;
+            part[2] += v.z > limit;
+            part[3] += v.w > limit;
+          }
+        }
+      }
+      rank[u] = part[0] + part[1] + part[2] + part[3];
+    }
+    uint32_t mask[kEarly];
+#pragma unroll
+    for (uint32_t u = 0; u < kEarly; ++u) {
+      const uint32_t i = tid + u * kThreads;
+      const bool stays = i < n && (all || i < lo || i >= hi || rank[u] < need);
+      mask[u] = __ballot_sync(0xffffffffu, stays);
+      if (lane == 0) sh.warp_sum[0][warp + u * kWarps] = __popc(mask[u]);
+    }
+    __syncthreads();
+    // (the 32 columns of a warp stand together: one count for each)
+    static_assert(kCountColumns / 32 <= 32, "a lane for 32 columns");
+    const uint32_t count = sh.warp_sum[0][lane];
+#pragma unroll
+    for (uint32_t u = 0; u < kEarly; ++u) {
+      const uint32_t i = tid + u * kThreads, w = i / 32;
+      const uint32_t at = __reduce_add_sync(0xffffffffu, lane < w ? count : 0u) +
+                          __popc(mask[u] & ((1u << lane) - 1));
+      if (mask[u] >> lane & 1) {
+        if (before + at < p.max_indices) p.kv_indices[before + at] = entry[u];
+        if (cols != nullptr) cols[at] = static_cast<int32_t>(i);
+      }
+    }
     return;
   }
-  const uint32_t need = top - p.first - p.last;          // of the columns between
+  // Columns first, in the place of the pages (those past max_indices: nowhere).
+  auto put = [&](uint32_t rank, uint32_t col) {
+    if (before + rank < p.max_indices) p.kv_indices[before + rank] = static_cast<int32_t>(col);
+    if (cols != nullptr) cols[rank] = static_cast<int32_t>(col);
+  };
+  if (all) {
+    for (uint32_t i = tid; i < n; i += kThreads) {
+      if (before + i < p.max_indices) p.kv_indices[before + i] = table[i];
+      if (cols != nullptr) cols[i] = static_cast<int32_t>(i);
+    }
+    return;
+  }
   for (uint32_t i = tid; i < lo; i += kThreads) put(i, i);
   for (uint32_t i = hi + tid; i < n; i += kThreads) put(top - n + i, i);
-  if (need == 0) return;
-  if constexpr (kCount) {
-    // a thread for two columns: how many keys are larger, or equal and before it
-    constexpr uint32_t kPer = kCountColumns / kThreads;
-    uint32_t k[kPer], rank[kPer];
-#pragma unroll
-    for (uint32_t u = 0; u < kPer; ++u) {
-      const uint32_t i = kPer * tid + u;
-      k[u] = i < m ? keys[i] : 0u;
-      rank[u] = 0;
-    }
-    const uint32_t mine = kPer * tid;
+  if (need > 0) {
+    auto key = [&](uint32_t i) { return held ? keys[i] : key_of(scores[i]); };
+    // All keys above b are kept, and `left` of those in [a, b].
+    uint32_t a = __reduce_min_sync(0xffffffffu, sh.least[lane % kWarps]);
+    uint32_t b = __reduce_max_sync(0xffffffffu, sh.most[lane % kWarps]);
+    uint32_t left = need;
+    bool whole = left == m;                              // those in [a, b] all are
+    while (!whole && a < b) {
+      const int shift = max(0, 21 - __clz(b - a));       // (b - a) >> shift < 2048
 #pragma unroll 8
-    for (uint32_t i = 0; i < m; ++i) {
-      const uint32_t x = keys[i];
-#pragma unroll
-      for (uint32_t u = 0; u < kPer; ++u) rank[u] += x > k[u] || (x == k[u] && i < mine + u);
-    }
-    uint32_t take = 0;
-#pragma unroll
-    for (uint32_t u = 0; u < kPer; ++u) take += mine + u < m && rank[u] < need;
-    uint32_t at, none;
-    scan2(sh, take, 0, at, none);
-    at += lo;
-#pragma unroll
-    for (uint32_t u = 0; u < kPer; ++u)
-      if (mine + u < m && rank[u] < need) put(at++, lo + mine + u);
-    return;
-  }
-  auto key = [&](uint32_t i) { return held ? keys[i] : key_of(scores[lo + i]); };
-  // All keys above b are kept, and `left` of those in [a, b].
-  uint32_t a = sh.least, b = sh.most, left = need;
-  bool whole = left == m;                                // those in [a, b] all are
-  while (!whole && a < b) {
-    const int shift = max(0, 21 - __clz(b - a));         // (b - a) >> shift < 2048
-    for (uint32_t i = tid; i < m; i += kThreads) {
-      const uint32_t k = key(i);
-      if (k >= a && k <= b) atomicAdd(&sh.hist[(k - a) >> shift], 1u);
-    }
-    __syncthreads();
-    // bins from the top: thread t holds the t-th part of them
-    constexpr int kPer = Sh::kBins / kThreads;
-    uint32_t c[kPer], sum = 0, above, none;
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      c[u] = sh.hist[Sh::kBins - 1 - (kPer * tid + u)];
-      sum += c[u];
-    }
-    scan2(sh, sum, 0, above, none);
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      if (above < left && above + c[u] >= left) {
-        sh.bin = Sh::kBins - 1 - (kPer * tid + u);
-        sh.above = above;
-        sh.inside = c[u];
+      for (uint32_t i = lo + tid; i < hi; i += kThreads) {
+        const uint32_t k = key(i);
+        if (k >= a && k <= b) atomicAdd(&hist[(k - a) >> shift], 1u);
       }
-      above += c[u];
-      sh.hist[Sh::kBins - 1 - (kPer * tid + u)] = 0;
+      __syncthreads();
+      // bins from the top: thread t holds the t-th part of them
+      constexpr int kPer = kBins / kThreads;
+      uint32_t c[kPer], sum = 0, above, none;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        uint32_t& bin = hist[kBins - 1 - (kPer * tid + u)];
+        c[u] = bin;
+        bin = 0;
+        sum += c[u];
+      }
+      scan2(sh, sum, 0, above, none);
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        if (above < left && above + c[u] >= left) {
+          sh.bin = kBins - 1 - (kPer * tid + u);
+          sh.above = above;
+          sh.inside = c[u];
+        }
+        above += c[u];
+      }
+      __syncthreads();
+      a += sh.bin << shift;
+      if (b - a >= (1u << shift)) b = a + (1u << shift) - 1;
+      left -= sh.above;
+      whole = sh.inside == left;
+      __syncthreads();
     }
-    __syncthreads();
-    a += sh.bin << shift;
-    if (b - a >= (1u << shift)) b = a + (1u << shift) - 1;
-    left -= sh.above;
-    whole = sh.inside == left;
-    __syncthreads();
+    // Kept: keys above b, and in [a, b] all, or the first `left` of one key.
+    uint32_t run_above = 0, run_in = 0;
+    for (uint32_t base = lo; base < hi; base += kThreads * 32) {
+      // consecutive columns of a thread, an odd number (banks)
+      const uint32_t count = min(hi - base, static_cast<uint32_t>(kThreads * 32));
+      const uint32_t per = min(((count + kThreads - 1) / kThreads) | 1u, 33u);
+      const uint32_t i0 = base + per * tid, i1 = min(i0 + per, base + count);
+      uint32_t na = 0, ni = 0;
+      const uint32_t* part = keys;
+      if (!held) {
+        // (whole lines, to where a thread can walk along them)
+        __syncthreads();
+#pragma unroll 8
+        for (uint32_t i = tid; i < count; i += kThreads) keys[i] = key_of(scores[base + i]);
+        __syncthreads();
+        part = keys - base;
+      }
+#pragma unroll 4
+      for (uint32_t i = i0; i < i1; ++i) {
+        const uint32_t k = part[i];
+        na += k > b;
+        ni += k >= a && k <= b;
+      }
+      uint32_t ea, ei;
+      scan2(sh, na, ni, ea, ei);
+      ea += run_above;
+      ei += run_in;
+#pragma unroll 4
+      for (uint32_t i = i0; i < i1; ++i) {
+        const uint32_t k = part[i];
+        const bool in = k >= a && k <= b;
+        if (k > b || (in && ei < left)) put(lo + ea + min(ei, left), i);
+        ea += k > b;
+        ei += in;
+      }
+      if (base + count < hi) {
+        // totals, for the next part
+        __syncthreads();
+        if (tid == kThreads - 1) sh.above = ea, sh.inside = ei;
+        __syncthreads();
+        run_above = sh.above;
+        run_in = sh.inside;
+      }
+    }
   }
-  // Kept: keys above b, and in [a, b] all, or the first `left` of one key.
-  uint32_t run_above = 0, run_in = 0;
-  for (uint32_t base = 0; base < m; base += kThreads * 32) {
-    // consecutive columns of a thread, an odd number (banks)
-    const uint32_t count = min(m - base, static_cast<uint32_t>(kThreads * 32));
-    const uint32_t per = min(((count + kThreads - 1) / kThreads) | 1u, 33u);
-    const uint32_t i0 = base + per * tid, i1 = min(i0 + per, base + count);
-    uint32_t na = 0, ni = 0;
-    for (uint32_t i = i0; i < i1; ++i) {
-      const uint32_t k = key(i);
-      na += k > b;
-      ni += k >= a && k <= b;
-    }
-    uint32_t ea, ei;
-    scan2(sh, na, ni, ea, ei);
-    ea += run_above;
-    ei += run_in;
-    for (uint32_t i = i0; i < i1; ++i) {
-      const uint32_t k = key(i);
-      const bool in = k >= a && k <= b;
-      if (k > b || (in && ei < left)) put(lo + ea + min(ei, left), lo + i);
-      ea += k > b;
-      ei += in;
-    }
-    if (base + count < m) {
-      // totals, for the next part
-      __syncthreads();
-      if (tid == kThreads - 1) sh.above = ea, sh.inside = ei;
-      __syncthreads();
-      run_above = sh.above;
-      run_in = sh.inside;
-    }
+  // then their pages
+  __syncthreads();
+  const int64_t room = p.max_indices - before;
+  const int64_t written = min(room, static_cast<int64_t>(kept));
+  int32_t* out = p.kv_indices + before;
+  for (int64_t i = tid; i < written; i += 4 * kThreads) {
+    int32_t c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) c[u] = i + u * kThreads < written ? out[i + u * kThreads] : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) c[u] = table[c[u]];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u * kThreads < written) out[i + u * kThreads] = c[u];
   }
 }
 
 template <int kThreads, bool kCount>
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
-  const uint32_t between = p.columns;
-  const uint32_t bytes = 4 * (kCount ? kCountColumns : std::min(between, kKeysInShared));
+  const uint32_t columns = p.columns;
+  constexpr uint32_t kBinWords = kCount ? 0 : kBins;
+  const uint32_t bytes = 4 * (kCount ? kCountColumns : kBinWords + std::min(columns, kKeysInShared));
   if (bytes > 32768) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        page_select_kernel<kThreads, kCount>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kKeysInShared);
+    const cudaError_t e = cudaFuncSetAttribute(page_select_kernel<kThreads, kCount>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               4 * (kBinWords + kKeysInShared));
     if (e != cudaSuccess) return e;
   }
   page_select_kernel<kThreads, kCount><<<static_cast<unsigned>(p.rows), kThreads, bytes, stream>>>(p);
@@ -788,9 +884,13 @@ extern "C" mla_status mla_page_select(const float* scores, int64_t scores_stride
                       page_size, q_len, rows, top_pages, first_pages, last_pages, kv_indptr,
                       kv_last_page_len, kv_indices, max_indices, columns, err};
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  // Counting: 512 rows of 256 columns 9.6 us (by ranges 10.3), one row 4.2 (6.2); of 512
+  // columns 24.3 (10.3).  1,024 threads: a row of 16,384 columns 15.7 us (with 256
+  // threads 27.7), of 8,192 12.3 (14.4), but 512 rows of 8,192 41 us (25.7).
+  const int32_t few = rows > 152 ? 8192 : 4096;
   const cudaError_t e = table_pages <= static_cast<int32_t>(mla::kCountColumns)
                             ? mla::launch_select<256, true>(p, stream)
-                        : table_pages <= 4096 ? mla::launch_select<256, false>(p, stream)
-                                              : mla::launch_select<1024, false>(p, stream);
+                        : table_pages <= few ? mla::launch_select<256, false>(p, stream)
+                                             : mla::launch_select<1024, false>(p, stream);
   return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

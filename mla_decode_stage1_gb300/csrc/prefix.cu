@@ -527,20 +527,22 @@ __device__ __forceinline__ void load_queries(const void* q, int64_t row0, int li
                                                     (i < 4 ? 4 * h + i : 8) * kChunkBytes));
   }
   const uint8_t* src = rows + lane / kLanes * kRowBytes + lane % kLanes * 16 + 4 * h * kChunkBytes;
-  uint4 x[kLanes];
-#pragma unroll 1
+  // (a chunk ahead)
+  uint4 x[2][kLanes];
+  fetch_query<kFp8>(src, live, lane, x[0]);
+#pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t v[32];
-    fetch_query<kFp8>(src + c * kChunkBytes, live, lane, x);
-    stage_query<kFp8>(x, via, lane);
+    if (c < 3 || h == 0)
+      fetch_query<kFp8>(src + (c < 3 ? c + 1 : 8) * kChunkBytes, live, lane, x[(c + 1) & 1]);
+    stage_query<kFp8>(x[c & 1], via, lane);
     __syncwarp();
     own_query(via, lane, v);
     __syncwarp();
     tmem_st32(tmem + 32 * c, v);
   }
   if (h == 0) {
-    fetch_query<kFp8>(src + 8 * kChunkBytes, live, lane, x);
-    stage_query<kFp8>(x, rotated, lane);
+    stage_query<kFp8>(x[0], rotated, lane);
     fence_proxy_async_smem();
   }
   __syncwarp();

@@ -779,11 +779,19 @@ def run_select(mla, scores, table, lens, page, q_len, top, first, last, cap=None
     return ptr.tolist(), ll.tolist(), idx.tolist(), None if cols is None else cols.tolist(), need
 
 
-@pytest.mark.parametrize("lens,page,q_len,top,first,last", [
+SELECT_CASES = [
     ([0, 1, 64, 65, 1000], 8, 1, 8, 1, 1), ([5000] * 3, 8, 1, 100, 0, 1), ([5000], 8, 1, 100, 3, 7),
     ([4099], 1, 1, 4097, 1, 1), ([300_000], 16, 1, 2000, 1, 1), ([40_000, 7], 1, 1, 5, 4, 1),
     ([700, 3, 0, 64], 16, 4, 9, 2, 3), ([2048 + 13] * 70, 8, 1, 256, 1, 2),
-    ([16 * 8 + 1], 8, 1, 16, 1, 1), ([640], 64, 1, 1, 0, 1), ([9 * 64] * 5, 64, 64, 4, 1, 1)])
+    ([16 * 8 + 1], 8, 1, 16, 1, 1), ([640], 64, 1, 1, 0, 1), ([9 * 64] * 5, 64, 64, 4, 1, 1),
+    # around the sizes where another way of selecting begins
+    ([256, 255, 33, 32, 0], 1, 1, 31, 0, 1), ([257, 256, 40], 1, 1, 40, 1, 1),
+    ([4096, 5], 1, 1, 700, 2, 2), ([4097, 9], 1, 2, 700, 2, 2), ([4100 + i for i in range(160)], 1, 1, 33, 1, 1),
+    ([32768], 1, 1, 3000, 5, 5), ([32769, 100], 1, 1, 32768, 0, 1), ([70_001], 1, 1, 40_000, 1, 1),
+    ([70_000, 33_000], 1, 1, 300, 1, 1)]
+
+
+@pytest.mark.parametrize("lens,page,q_len,top,first,last", SELECT_CASES)
 @pytest.mark.parametrize("kind", ["random", "ties", "special"])
 def test_page_select(mla, lens, page, q_len, top, first, last, kind):
     g = gen(12)
