@@ -641,7 +641,8 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  * of group g's prefix (all of them full), then to pages of their own:
  *     out[b,t,h,:] = softmax over [prefix of b's group ; own tokens of b]
  * with the scores, values and lse of mla_decode_run.  The prefix's rows are read
- * and multiplied once for up to 256 query rows (16 query tokens of 16 heads).
+ * and multiplied once for up to 256 query rows (16 query tokens of 16 heads), unless
+ * that would take longer (`form`).
  *
  *   group_indptr_host   host int32 [num_groups+1], non-decreasing from 0; its
  *                       last entry is the batch size (at least 1).
@@ -658,6 +659,11 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  *                       A request of a group with a prefix has at least
  *                       q_len - 1 own tokens, so that each sees the whole prefix.
  *   num_sms             CTAs to plan for; 0 = the SM count of the device.
+ *   form                MLA_SHARED_ONCE: the prefix kernel.  MLA_SHARED_EACH: the
+ *                       decode kernel reads the prefix for every request, as
+ *                       mla_decode_run would on whole page tables, which is faster
+ *                       for few requests or short prefixes.  MLA_SHARED_AUTO: the
+ *                       one that is expected to be faster.
  * The plan follows mla_plan's rules: library-owned, one host thread at a time,
  * one workspace per plan.  The workspace holds the prefixes' rows in bf16 (1,152
  * bytes a token, the group's length rounded up to 128; not of a bf16 pool in pages
@@ -669,11 +675,17 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  */
 typedef struct mla_shared mla_shared;
 
+typedef enum {
+  MLA_SHARED_AUTO = 0,
+  MLA_SHARED_ONCE = 1,
+  MLA_SHARED_EACH = 2
+} mla_shared_form;
+
 typedef struct {
   int32_t batch_size;
   int32_t num_groups;
   int32_t q_len;
-  int32_t num_clusters;      /* clusters of CTAs that work on the prefixes */
+  int32_t num_clusters;      /* clusters of CTAs that work on the prefixes (0: MLA_SHARED_EACH) */
   int32_t block_rows;        /* query rows of such a cluster: 128 or 256 */
   int32_t num_items;         /* (up to block_rows query rows, range of their prefix) */
   int64_t prefix_tokens;     /* of groups with requests, once each */
@@ -685,7 +697,7 @@ mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* pref
                            int32_t num_groups, const int32_t* kv_indptr_host,
                            const int32_t* kv_last_page_len_host, int32_t q_len, int32_t page_size,
                            mla_dtype q_dtype, mla_dtype kv_dtype, int32_t num_sms,
-                           mla_shared** plan_out);
+                           mla_shared_form form, mla_shared** plan_out);
 mla_status mla_shared_get_info(const mla_shared* plan, mla_shared_info* info);
 void mla_shared_destroy(mla_shared* plan);
 
@@ -693,8 +705,8 @@ void mla_shared_destroy(mla_shared* plan);
  * mla_shared_run -- one decode call of that plan, enqueued on `stream`.
  *
  * Sums, maxima, the softmax's statistics and partial outputs are fp32.  Against
- * a prefix, probabilities are rounded to bf16 where they meet the values; the
- * stored values and the queries are exact there.
+ * a prefix (MLA_SHARED_ONCE), probabilities are rounded to bf16 where they meet the
+ * values; the stored values and the queries are exact there.
  *
  *   q, q_scale, kv .. kv_pool_rows, out, lse   as for mla_decode_run with a plan
  *                    of the same q_len.

@@ -284,8 +284,9 @@ namespace mla {
 mla_status decode_prepare(mla_plan* plan, const void* q, const float* q_scale, const void* kv,
                           const float* kv_scale, const uint8_t* kv_e8m0,
                           int64_t kv_e8m0_row_stride, int64_t kv_pool_rows,
-                          const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
-                          void* out, float* lse, cudaStream_t stream, DecodeLaunch* launch) {
+                          const int32_t* kv_indices, const int32_t* prefix_indices,
+                          void* workspace, size_t workspace_bytes, void* out, float* lse,
+                          cudaStream_t stream, DecodeLaunch* launch) {
   if (plan == nullptr || q == nullptr || kv == nullptr || out == nullptr || workspace == nullptr)
     return MLA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(workspace, 256))
@@ -311,7 +312,8 @@ mla_status decode_prepare(mla_plan* plan, const void* q, const float* q_scale, c
   const bool mx = plan->kv_dtype == MLA_DTYPE_MXFP4;
   int box_rows = mla::kTile;
   int gather = 0;
-  if (kv_indices != nullptr) {
+  const bool tables = kv_indices != nullptr || prefix_indices != nullptr;
+  if (tables) {
     if (kv_pool_rows % plan->page_size != 0) return MLA_ERR_INVALID_ARG;
     if (plan->page_size % 8 == 0 || mx)
       box_rows = 8;
@@ -359,6 +361,8 @@ mla_status decode_prepare(mla_plan* plan, const void* q, const float* q_scale, c
     p.q_scale = q_scale;
     p.kv_scale = kv_scale;
     p.kv_indices = kv_indices;
+    p.prefix_indices = prefix_indices;
+    p.identity = tables ? 0 : 1;
     p.items = reinterpret_cast<const WorkItem*>(ws + plan->off_items);
     p.heads = reinterpret_cast<const CtaHead*>(ws + plan->off_indptr);
     p.part_o = part_o;
@@ -444,6 +448,17 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
                               int32_t batch_size, int32_t q_len, int32_t page_size,
                               mla_dtype q_dtype, mla_dtype kv_dtype,
                               const mla_plan_options* options, mla_plan** plan_out) {
+  return mla::plan_with_prefixes(kv_indptr_host, kv_last_page_len_host, batch_size, q_len, page_size,
+                                 q_dtype, kv_dtype, options, nullptr, plan_out);
+}
+
+}  // extern "C"
+
+mla_status mla::plan_with_prefixes(const int32_t* kv_indptr_host,
+                                   const int32_t* kv_last_page_len_host, int32_t batch_size,
+                                   int32_t q_len, int32_t page_size, mla_dtype q_dtype,
+                                   mla_dtype kv_dtype, const mla_plan_options* options,
+                                   const PrefixPages* prefixes, mla_plan** plan_out) {
   if (plan_out == nullptr) return MLA_ERR_INVALID_ARG;
   *plan_out = nullptr;
   const mla_plan_options o = options != nullptr ? *options : mla_plan_options{0, 0, 0, 0, 0};
@@ -473,8 +488,10 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
   const bool pairs = q_len % 2 == 0 && (qmode == mla::kQFp8KvFp8 || qmode == mla::kQBf16KvFp8);
   const int32_t qv = pairs ? q_len / 2 : q_len;    // virtual requests per request
   const int32_t nv = batch_size * qv;
-  std::vector<int32_t> len(nv), page_base(nv), npages(nv), vis0(nv, 0);
-  std::vector<int64_t> tiles(nv);                  // cut units of each virtual request
+  // parts to be cut: the virtual requests' own pages, then (nv + r) their prefixes
+  const size_t parts = prefixes != nullptr ? 2 * static_cast<size_t>(nv) : nv;
+  std::vector<int32_t> len(parts), page_base(parts), npages(parts), vis0(parts, 0);
+  std::vector<int64_t> tiles(parts);               // cut units of each
   int64_t total_tok = 0, total_tiles = 0, total_units = 0;
   int64_t identity_rows = 0;      // pool rows the identity table reaches
   for (int32_t b = 0; b < batch_size; ++b) {
@@ -499,6 +516,18 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
       tiles[r] = (len[r] + unit - 1) / unit;
       total_tok += len[r];
       total_tiles += (len[r] + mla::kTile - 1) / mla::kTile;
+      total_units += tiles[r];
+    }
+    if (prefixes == nullptr) continue;
+    const int64_t keys = static_cast<int64_t>(prefixes->pages[b]) * page_size;
+    if (keys > INT32_MAX - mla::kTile) return MLA_ERR_INVALID_ARG;
+    for (int32_t t = 0; t < qv; ++t) {
+      const int32_t r = nv + b * qv + t;
+      len[r] = static_cast<int32_t>(keys);
+      vis0[r] = INT32_MAX - 1;
+      page_base[r] = ~prefixes->base[b];
+      npages[r] = prefixes->pages[b];
+      tiles[r] = (len[r] + unit - 1) / unit;
       total_units += tiles[r];
     }
   }
@@ -529,11 +558,15 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
   if (num_splits == 0) {
     const int32_t G = static_cast<int32_t>(std::min<int64_t>(num_sms, total_units));
     std::vector<int32_t> order;
+    auto add = [&](int32_t r) {
+      order.push_back(r);
+      if (prefixes != nullptr) order.push_back(nv + r);
+    };
     if (qv == 1 || G < qv) {
       // query-token-major order: the q_len passes over a request's KV stay
       // close in time when the CTAs are too few to group them
       for (int32_t t = 0; t < qv; ++t)
-        for (int32_t b = 0; b < batch_size; ++b) order.push_back(b * qv + t);
+        for (int32_t b = 0; b < batch_size; ++b) add(b * qv + t);
       plan_balanced(P, order, tiles, len, page_base, npages, G, item_cost, unit);
     } else {
       // one group of CTAs per query token (or pair), each balanced over
@@ -541,7 +574,7 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
       // same time, so the other passes are served from L2
       for (int32_t t = 0; t < qv; ++t) {
         order.clear();
-        for (int32_t b = 0; b < batch_size; ++b) order.push_back(b * qv + t);
+        for (int32_t b = 0; b < batch_size; ++b) add(b * qv + t);
         const int32_t Gt = static_cast<int32_t>((static_cast<int64_t>(G) * (t + 1)) / qv -
                                                 (static_cast<int64_t>(G) * t) / qv);
         plan_balanced(P, order, tiles, len, page_base, npages, Gt, item_cost, unit);
@@ -550,13 +583,19 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
   } else {
     plan_fixed(P, tiles, len, page_base, npages, num_splits, unit);
   }
-  for (WorkItem& w : P->items) w.vis0 = vis0[w.b];
+  for (WorkItem& w : P->items) {
+    w.vis0 = vis0[w.b];
+    if (w.b >= nv) w.b -= nv;
+  }
   assign_slots(P, len);
   layout_workspace(P);
   P->cluster = o.merge == 0 ? cluster_size_of(P) : 0;
   *plan_out = P;
   return MLA_OK;
 }
+
+extern "C" {
+
 
 mla_status mla_decode_plan_q(const int32_t* kv_indptr_host, const int32_t* kv_last_page_len_host,
                              int32_t batch_size, int32_t q_len, int32_t page_size,
@@ -623,7 +662,7 @@ mla_status mla_decode_run(mla_plan* plan, const void* q, const float* q_scale, c
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   mla::DecodeLaunch launch{};
   const mla_status st = mla::decode_prepare(plan, q, q_scale, kv, kv_scale, kv_e8m0,
-                                            kv_e8m0_row_stride, kv_pool_rows, kv_indices, workspace,
+                                            kv_e8m0_row_stride, kv_pool_rows, kv_indices, nullptr, workspace,
                                             workspace_bytes, out, lse, stream, &launch);
   return st != MLA_OK ? st : mla::decode_launch(plan, launch, stream);
 }

@@ -46,7 +46,8 @@ struct WorkItem {
   int32_t tok_begin;  // first token (multiple of kTile)
   int32_t tok_end;    // one past the last token
   int32_t slot;       // partial slot, or -1: write out/lse directly
-  int32_t page_base;  // kv_indptr[b]: first page-table entry of the request
+  int32_t page_base;  // kv_indptr[b]: first page-table entry of the request; ~entry: of a
+                      // prefix that it shares (prefix_indices)
   int32_t npages;     // page-table entries of the request
   int32_t vis0;       // two query tokens per request: tokens query token 0 sees
                       // (query token t sees vis0 + t); unused with one token
@@ -89,6 +90,7 @@ struct Stage1Params {
   const float* q_scale;         // device [1] (fp8 q) or null
   const float* kv_scale;        // device [1] (fp8 kv) or null
   const int32_t* kv_indices;    // page table or null (identity)
+  const int32_t* prefix_indices;  // that of shared prefixes, or null (identity)
   const WorkItem* items;
   const CtaHead* heads;         // [num_ctas]
   float* part_o;                // [num_partials,16,512] fp32, normalised
@@ -98,6 +100,7 @@ struct Stage1Params {
   int32_t* err;                 // device error word (the workspace header)
   uint64_t stamp;               // the plan's stamp; the workspace must carry the same
   int32_t page_size;
+  int32_t identity;             // 1: no page table
   int32_t box_rows;             // rows per TMA box: 128 (identity table) or 8 (page table)
   int32_t gather;               // 1: page size not a multiple of 8 (bf16 / fp8 KV); rows are
                                 // gathered one by one with cp.async instead of TMA boxes

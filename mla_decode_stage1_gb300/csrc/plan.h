@@ -61,8 +61,9 @@ struct DecodeLaunch {
 mla_status decode_prepare(mla_plan* plan, const void* q, const float* q_scale, const void* kv,
                           const float* kv_scale, const uint8_t* kv_e8m0,
                           int64_t kv_e8m0_row_stride, int64_t kv_pool_rows,
-                          const int32_t* kv_indices, void* workspace, size_t workspace_bytes,
-                          void* out, float* lse, cudaStream_t stream, DecodeLaunch* launch);
+                          const int32_t* kv_indices, const int32_t* prefix_indices,
+                          void* workspace, size_t workspace_bytes, void* out, float* lse,
+                          cudaStream_t stream, DecodeLaunch* launch);
 mla_status decode_launch(const mla_plan* plan, const DecodeLaunch& launch, cudaStream_t stream);
 
 // What the other host files take from api.cu: a process-wide unique stamp for
@@ -73,6 +74,18 @@ typedef CUresult (*TiledEncoder)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 TiledEncoder tiled_encoder();
+// mla_decode_plan_ex for requests that have pages in front of their own as well, which
+// all their query tokens see whole: prefix_pages[b] entries from prefix_base[b] on of
+// another page table (prefix_indices).  A part of either kind is an item of its own, so
+// every request's items write partial results: for plan_partials_only.
+struct PrefixPages {
+  const int32_t *base, *pages;
+};
+mla_status plan_with_prefixes(const int32_t* kv_indptr_host, const int32_t* kv_last_page_len_host,
+                              int32_t batch_size, int32_t q_len, int32_t page_size,
+                              mla_dtype q_dtype, mla_dtype kv_dtype,
+                              const mla_plan_options* options, const PrefixPages* prefixes,
+                              mla_plan** plan_out);
 // Turns a new plan into one whose every item writes a partial result and whose
 // run merges nothing: request b's are slots first[b] .. first[b] + count[b] - 1.
 // Its run splits a bf16 query without loss where the decode call rounds it a

@@ -22,11 +22,13 @@ struct mla_shared {
   bool paired = false;               // clusters of two score and two value CTAs, 256 rows
   bool direct = false;               // the prefix kernel reads the pool itself
   bool tall = false;                 // a tile's 128 keys stand together there
+  bool each = false;                 // the decode kernel reads the prefixes for every request
   int32_t most = 0;                  // partial results of a token, at most
   int32_t blocks = 1;                // of 128 rows in an item
   int32_t num_clusters = 0, num_slots = 0;
   int64_t prefix_tokens = 0, identity_rows = 0;
-  mla_plan* own = nullptr;           // over the requests' own ends, partial results only
+  mla_plan* own = nullptr;           // over the requests' own ends (and, `each`, their prefixes),
+                                     // partial results only
   std::vector<ExpandTile> tiles;
   std::vector<PrefixItem> items;
   std::vector<CtaItems> cluster_items;
@@ -113,24 +115,40 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t cluster
 // of 64 keys), but blocks of 256 rows may leave half of one empty, and 36 clusters of
 // four have a place where 76 of two have.  64 requests of a 32,768-token prefix: 73 us
 // paired, 87 not; 5 to 19 requests of three prefixes: 40 us paired, 39 not.
+// And whether the prefixes are to be read for every request instead, by the decode
+// kernel, which has no rows to gather and fewer kernels in a row.  The estimates are
+// linear fits to 128 calls of both forms (2 to 128 requests of 256 to 16,384 shared
+// tokens, all types, 1 to 4 query tokens): the form taken was slower than the other in
+// 4 of them, by 28% at most, and by 0.7% on average.  8 requests of 1,024 e4m3 tokens:
+// 14.5 us each on its own, 23.3 once for all; 32 of 16,384: 53 and 43; 128 of 16,384:
+// 181 and 74.
 void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
-                 bool whole_device) {
+                 bool whole_device, mla_shared_form form) {
   int32_t on_device[2] = {P->num_sms / 2, P->num_sms / 4};
   if (whole_device)
     for (int k = 0; k < 2; ++k) {
       const int32_t n = mla::prefix_clusters(k == 1);
       if (n > 0) on_device[k] = std::min(on_device[k], n);
     }
-  double time[2] = {0, 0};
+  const bool pairs = mla::kHeads != P->own->rows;        // two query tokens an item
+  const double tile_us = P->kv_dtype == MLA_DTYPE_BF16    ? 3.5
+                         : P->kv_dtype == MLA_DTYPE_MXFP4 ? 2.4
+                         : (P->q_dtype == MLA_DTYPE_BF16 ? 1.6 : 1.4) * (pairs ? 1.5 : 1.0);
+  double time[2] = {0, 0}, each = 0, tokens_us = 0;
   for (int32_t g = 0; g < P->groups; ++g) {
     const int64_t keys = (static_cast<int64_t>(prefix_indptr[g + 1]) - prefix_indptr[g]) * P->page_size;
     const int64_t tokens = static_cast<int64_t>(group_indptr[g + 1] - group_indptr[g]) * P->q_len;
     const double tiles = static_cast<double>((keys + mla::kSpTile - 1) / mla::kSpTile);
+    each += tiles * static_cast<double>(tokens) / (pairs ? 2 : 1) * tile_us / P->num_sms;
+    tokens_us += static_cast<double>(tokens) * 5.5 / P->num_sms;
     time[0] += tiles * static_cast<double>((tokens + kTokensPerBlock - 1) / kTokensPerBlock) *
                (P->direct && P->page_size % mla::kSpTile != 0 ? 3900 : 3300);
     time[1] += tiles * static_cast<double>((tokens + 2 * kTokensPerBlock - 1) / (2 * kTokensPerBlock)) * 2600;
   }
-  P->paired = on_device[1] > 0 && time[1] / std::max(1, on_device[1]) < time[0] / std::max(1, on_device[0]);
+  for (int k = 0; k < 2; ++k) time[k] /= std::max(1, on_device[k]);
+  P->paired = on_device[1] > 0 && time[1] < time[0];
+  const double once = 18 + (P->direct ? 0 : 1.6) + time[P->paired] / 1900 + tokens_us;
+  P->each = form == MLA_SHARED_EACH || (form == MLA_SHARED_AUTO && 12 + each < once);
   P->blocks = P->paired ? 2 : 1;
   P->tall = !P->paired && (!P->direct || P->page_size % mla::kSpTile == 0);
   P->num_clusters = std::max(1, on_device[P->paired]);
@@ -139,6 +157,7 @@ void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* pref
 mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
                      const int32_t* kv_indptr, const int32_t* last_len) {
   const int32_t t = P->q_len, per_block = P->blocks * kTokensPerBlock;
+  std::vector<int32_t> each_base(P->each ? P->bs : 0), each_pages(P->each ? P->bs : 0);
   std::vector<Block> blocks;
   std::vector<int32_t> block_of(P->bs, -1), first_of(P->bs, 0);   // first: the group's first token
   int64_t rows = 0;
@@ -158,9 +177,15 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
       int64_t n = (static_cast<int64_t>(kv_indptr[b + 1]) - kv_indptr[b]) * P->page_size;
       if (n > 0 && last_len != nullptr) n -= P->page_size - last_len[b];
       if (n < t - 1) return MLA_ERR_INVALID_ARG;
+      if (P->each) {
+        each_base[b] = prefix_indptr[g];
+        each_pages[b] = static_cast<int32_t>(np);
+        continue;
+      }
       block_of[b] = static_cast<int32_t>(blocks.size());
       first_of[b] = b0 * t;
     }
+    if (P->each) continue;
     const int64_t tokens = static_cast<int64_t>(b1 - b0) * t;
     for (int64_t a = 0; a < tokens; a += per_block) {
       Block b;
@@ -183,6 +208,17 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
     rows += (keys + mla::kSpTile - 1) / mla::kSpTile * mla::kSpTile;
   }
   cut_blocks(P, blocks, P->num_clusters);
+  if (P->each) {
+    mla_plan_destroy(P->own);
+    P->own = nullptr;
+    const mla_plan_options o{0, P->num_sms, 0, 0, 1};
+    const mla::PrefixPages prefixes{each_base.data(), each_pages.data()};
+    const mla_status st = mla::plan_with_prefixes(kv_indptr, last_len, P->bs, t, P->page_size,
+                                                  static_cast<mla_dtype>(P->q_dtype),
+                                                  static_cast<mla_dtype>(P->kv_dtype), &o,
+                                                  &prefixes, &P->own);
+    if (st != MLA_OK) return st;
+  }
   // partial results of every block, then of every query token
   std::vector<int32_t> first_slot(blocks.size(), 0), slots(blocks.size(), 0);
   {
@@ -267,9 +303,10 @@ mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* pref
                            int32_t num_groups, const int32_t* kv_indptr_host,
                            const int32_t* kv_last_page_len_host, int32_t q_len, int32_t page_size,
                            mla_dtype q_dtype, mla_dtype kv_dtype, int32_t num_sms,
-                           mla_shared** plan_out) {
+                           mla_shared_form form, mla_shared** plan_out) {
   if (plan_out == nullptr) return MLA_ERR_INVALID_ARG;
   *plan_out = nullptr;
+  if (form < MLA_SHARED_AUTO || form > MLA_SHARED_EACH) return MLA_ERR_INVALID_ARG;
   if (group_indptr_host == nullptr || prefix_indptr_host == nullptr || kv_indptr_host == nullptr ||
       num_groups < 1 || num_sms < 0)
     return MLA_ERR_INVALID_ARG;
@@ -301,7 +338,7 @@ mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* pref
     st = mla_decode_plan_ex(kv_indptr_host, kv_last_page_len_host, P->bs, q_len, page_size, q_dtype,
                             kv_dtype, &o, &P->own);
     if (st == MLA_OK) {
-      choose_form(P, group_indptr_host, prefix_indptr_host, whole_device);
+      choose_form(P, group_indptr_host, prefix_indptr_host, whole_device, form);
       st = make_plan(P, group_indptr_host, prefix_indptr_host, kv_indptr_host, kv_last_page_len_host);
     }
   } catch (...) {   // out of host memory
@@ -361,7 +398,7 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
   mla::DecodeLaunch own{};
   const mla_status st = mla::decode_prepare(
       plan->own, q, q_scale, kv, kv_scale, kv_e8m0, kv_e8m0_row_stride, kv_pool_rows, kv_indices,
-      ws + plan->off_own, plan->own->ws_bytes, out, nullptr, stream, &own);
+      plan->each ? prefix_indices : nullptr, ws + plan->off_own, plan->own->ws_bytes, out, nullptr, stream, &own);
   if (st != MLA_OK) return st;
   if (plan->uploaded_ws != workspace) {
     if (cudaMemcpyAsync(ws, plan->table.data(), plan->table.size(), cudaMemcpyHostToDevice,
@@ -417,7 +454,8 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     p.part_lse = part_lse;
     p.err = err;
     p.stamp = plan->stamp;
-    if (mla::launch_prefix(p, plan->paired, plan->num_clusters, stream) != cudaSuccess) return MLA_ERR_CUDA;
+    if (mla::launch_prefix(p, plan->paired, plan->num_clusters, stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
     own.stage1.beside = 1;
   }
   if (mla::decode_launch(plan->own, own, stream) != MLA_OK) return MLA_ERR_CUDA;

@@ -206,6 +206,16 @@ struct TileCursor {
   __device__ __forceinline__ int nvalid() const { return min(kTile, w.tok_end - t0()); }
 };
 
+// Page that holds a position `at` pages into an item: an entry of the request's page
+// table or, for a negative base, of that of the shared prefixes.
+__device__ __forceinline__ int page_at(const Stage1Params& p, int page_base, int at) {
+  const int32_t* table = page_base < 0 ? p.prefix_indices : p.kv_indices;
+  const int i = (page_base < 0 ? ~page_base : page_base) + at;
+  return table == nullptr ? i : ld_nc_early(table + i);
+}
+// The same without any page table.
+__device__ __forceinline__ int first_page(int page_base) { return page_base < 0 ? ~page_base : page_base; }
+
 // What lane `lane` needs to issue its TMA box of one tile.  The page-table
 // entry is loaded when the tile is looked ahead at and only checked (and
 // turned into a row) when the box is issued, so the load overlaps the wait.
@@ -222,10 +232,10 @@ __device__ __forceinline__ BoxFetch box_fetch(const Stage1Params& p, const TileC
   f.nbox = (c.nvalid() + p.box_rows - 1) / p.box_rows;
   if (lane >= f.nbox) return f;
   const int pos = c.t0() + lane * p.box_rows;
-  if (p.kv_indices == nullptr) {
-    f.raw = c.w.page_base * p.page_size + pos;
+  if (p.identity) {
+    f.raw = first_page(c.w.page_base) * p.page_size + pos;
   } else {
-    f.raw = ld_nc_early(p.kv_indices + c.w.page_base + pos / p.page_size);
+    f.raw = page_at(p, c.w.page_base, pos / p.page_size);
     f.off = pos % p.page_size;
   }
   return f;
@@ -233,7 +243,7 @@ __device__ __forceinline__ BoxFetch box_fetch(const Stage1Params& p, const TileC
 
 __device__ __forceinline__ int box_row(const Stage1Params& p, const BoxFetch& f, int lane) {
   if (lane >= f.nbox) return 0;
-  if (p.kv_indices == nullptr) return f.raw;
+  if (p.identity) return f.raw;
   int page = f.raw;
   if (page < 0 || static_cast<int64_t>(page + 1) * p.page_size > p.pool_rows) {
     atomicOr(p.err, kErrBadPage);
@@ -277,8 +287,7 @@ __device__ void run_producer(const Stage1Params& p, Misc* ms, uint32_t ring, int
 #pragma unroll
       for (int j = 0; j < 4; ++j) {       // loaded before the waits, used after
         const int r = lane + 32 * j;
-        page[j] = r < nvalid ? ld_nc_early(p.kv_indices + cur.w.page_base + (t0 + r) / p.page_size)
-                             : 0;
+        page[j] = r < nvalid ? page_at(p, cur.w.page_base, (t0 + r) / p.page_size) : 0;
       }
       // (the slot's previous tile must have landed before these arrivals)
       if (t >= static_cast<uint32_t>(L::kNumTiles)) {
@@ -623,8 +632,8 @@ struct TileAhead {
 // Raw page-table entry of token tq of a look-ahead tile (0 for the identity
 // table or a token past the tile's end).
 __device__ __forceinline__ int32_t scale_page(const Stage1Params& p, const TileAhead& c, int tq) {
-  if (c.ntile == 0 || tq >= c.nvalid() || p.kv_indices == nullptr) return 0;
-  return ld_nc_early(p.kv_indices + c.page_base + (c.t0() + tq) / p.page_size);
+  if (c.ntile == 0 || tq >= c.nvalid() || p.identity) return 0;
+  return page_at(p, c.page_base, (c.t0() + tq) / p.page_size);
 }
 
 // Pool row of token tq of a look-ahead tile, or -1 past the tile's end.
@@ -634,8 +643,8 @@ __device__ __forceinline__ int64_t pool_row(const Stage1Params& p, const TileAhe
                                             int32_t page) {
   if (c.ntile == 0 || tq >= c.nvalid()) return -1;
   const int pos = c.t0() + tq;
-  if (p.kv_indices == nullptr) {
-    const int64_t row = static_cast<int64_t>(c.page_base) * p.page_size + pos;
+  if (p.identity) {
+    const int64_t row = static_cast<int64_t>(first_page(c.page_base)) * p.page_size + pos;
     return row < p.pool_rows ? row : 0;   // (the host rejects such plans; never reached)
   }
   if (page < 0 || static_cast<int64_t>(page + 1) * p.page_size > p.pool_rows) {

@@ -28,7 +28,7 @@ def _declare(lib):
     P, i32, i64, sz, e = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                           ctypes.c_int)
     args = {
-        "mla_shared_plan": [P, P, i32, P, P, i32, i32, e, e, i32, ctypes.POINTER(P)],
+        "mla_shared_plan": [P, P, i32, P, P, i32, i32, e, e, i32, e, ctypes.POINTER(P)],
         "mla_shared_get_info": [P, ctypes.POINTER(SharedInfo)],
         "mla_shared_destroy": [P],
         "mla_shared_run": [P, P, P, P, P, P, i64, i64, P, P, P, sz, P, P, P],
@@ -47,6 +47,9 @@ def _declare(lib):
 _declare(_lib)
 _shared_run, _page_bounds, _page_scores, _page_select = (
     _lib.mla_shared_run, _lib.mla_page_bounds, _lib.mla_page_scores, _lib.mla_page_select)
+
+
+FORMS = {"auto": 0, "once": 1, "each": 2}
 
 
 class SharedPlan:
@@ -76,10 +79,14 @@ class SharedPlan:
 
 
 def mla_shared_plan(group_indptr, prefix_indptr, kv_indptr, kv_last_page_len=None, *, page_size: int,
-                    q_dtype: str, kv_dtype: str, q_len: int = 1, num_sms: int = 0) -> SharedPlan:
+                    q_dtype: str, kv_dtype: str, q_len: int = 1, num_sms: int = 0,
+                    form: str = "auto") -> SharedPlan:
     """Plan a decode call from HOST offsets: group_indptr (requests of each
     group), prefix_indptr (pages of each group's shared prefix, all full) and
-    kv_indptr (pages of each request's own) with optional last-page lengths."""
+    kv_indptr (pages of each request's own) with optional last-page lengths.
+    form: "once" (a prefix is read once for up to 16 query tokens), "each" (for
+    every request), or "auto" (what is expected to be faster)."""
+    _need(form in FORMS, f"form must be one of {tuple(FORMS)}")
     grp, grp_p = _i32_array(group_indptr)
     pre, pre_p = _i32_array(prefix_indptr)
     kvp, kvp_p = _i32_array(kv_indptr)
@@ -93,7 +100,7 @@ def mla_shared_plan(group_indptr, prefix_indptr, kv_indptr, kv_last_page_len=Non
     h = ctypes.c_void_p()
     _check("mla_shared_plan", _lib.mla_shared_plan(
         grp_p, pre_p, groups, kvp_p, last_p, int(q_len), int(page_size), DTYPES[q_dtype],
-        DTYPES[kv_dtype], int(num_sms), ctypes.byref(h)))
+        DTYPES[kv_dtype], int(num_sms), FORMS[form], ctypes.byref(h)))
     return SharedPlan(h, q_dtype, kv_dtype, int(pre[-1]), int(kvp[-1]))
 
 
@@ -166,10 +173,10 @@ class MlaShared:
     """Convenience owner of a shared plan and its workspace."""
 
     def __init__(self, group_indptr, prefix_indptr, kv_indptr, kv_last_page_len=None, *, page_size,
-                 q_dtype, kv_dtype, q_len=1, device="cuda"):
+                 q_dtype, kv_dtype, q_len=1, form="auto", device="cuda"):
         self.plan = mla_shared_plan(group_indptr, prefix_indptr, kv_indptr, kv_last_page_len,
                                     page_size=page_size, q_dtype=q_dtype, kv_dtype=kv_dtype,
-                                    q_len=q_len)
+                                    q_len=q_len, form=form)
         self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8, device=device)
 
     def __call__(self, q, kv, out, **kw):

@@ -22,10 +22,10 @@ def mem():
     return (ctypes.addressof(buf) + 255) & ~255
 
 
-def plan(mla, groups, prefix, kvp, last=None, ps=8, q_len=1, qd="bf16", kd="bf16", sms=152):
+def plan(mla, groups, prefix, kvp, last=None, ps=8, q_len=1, qd="bf16", kd="bf16", sms=152, form="once"):
     return mla.mla_shared_plan(np.asarray(groups, np.int32), np.asarray(prefix, np.int32),
                                np.asarray(kvp, np.int32), last, page_size=ps, q_len=q_len,
-                               q_dtype=qd, kv_dtype=kd, num_sms=sms)
+                               q_dtype=qd, kv_dtype=kd, num_sms=sms, form=form)
 
 
 @pytest.mark.parametrize("groups,prefix,kvp,last,kw,status", [
@@ -62,9 +62,15 @@ def test_shared_plan_refuses_mismatched_batches(mla):
     with pytest.raises(ValueError):
         plan(mla, [0], [0], [0])
     f = mla._lib.mla_shared_plan
-    assert f(None, None, 1, None, None, 1, 8, 0, 0, 8, None) == 1
+    assert f(None, None, 1, None, None, 1, 8, 0, 0, 8, 0, None) == 1
     h = ctypes.c_void_p()
-    assert f(None, None, 1, None, None, 1, 8, 0, 0, 8, ctypes.byref(h)) == 1 and not h
+    assert f(None, None, 1, None, None, 1, 8, 0, 0, 8, 0, ctypes.byref(h)) == 1 and not h
+    at = (ctypes.c_int32 * 2)(0, 1)
+    for form, status in ((-1, 1), (0, 0), (1, 0), (2, 0), (3, 1)):
+        assert f(at, at, 1, at, None, 1, 8, 0, 0, 8, form, ctypes.byref(h)) == status
+        mla._lib.mla_shared_destroy(h)
+    with pytest.raises(ValueError):
+        plan(mla, [0, 2], [0, 4], [0, 1, 2], form="never")
 
 
 def test_shared_plan_allows_short_ends(mla):
@@ -109,6 +115,16 @@ def test_shared_plan_takes_blocks_of_256_rows_where_they_fill(mla):
     assert plan(mla, [0, 256], [0, 1000], list(range(257))).info().block_rows == 256
     assert plan(mla, [0, 8], [0, 1000], list(range(9))).info().block_rows == 128
     assert plan(mla, [0, 256], [0, 1000], list(range(257)), sms=3).info().block_rows == 128
+
+
+def test_shared_plan_for_each_request(mla):
+    kw = dict(groups=[0, 9, 10, 30], prefix=[0, 50, 50, 113], kvp=list(range(31)))
+    p = plan(mla, form="each", **kw).info()
+    assert (p.num_items, p.num_clusters, p.prefix_tokens, p.own_tokens) == (0, 0, 113 * 8, 240)
+    assert plan(mla, form="auto", **kw).info().num_items == 0
+    assert plan(mla, [0, 64], [0, 4096], [0] * 65, form="auto").info().num_items > 0
+    # no rows are kept, whatever the pool
+    assert plan(mla, [0, 2], [0, 1000], [0, 1, 2], form="each").workspace_bytes < 152 * 2 * 33000 + 65536
 
 
 def run_args(p, a, **kw):

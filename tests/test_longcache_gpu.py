@@ -85,10 +85,10 @@ class Case:
     """Groups of requests: per (requests), prefix (pages), own (tokens)."""
 
     def __init__(self, per, prefix, own, page, q="bf16", kv="bf16", q_len=1, seed=1, table=True,
-                 rows=None, std=1.5, extra=2):
+                 rows=None, std=1.5, extra=2, form="once"):
         g = gen(seed)
         self.per, self.prefix, self.own, self.page, self.q_len = per, prefix, own, page, q_len
-        self.qd, self.kd, self.table = q, kv, table
+        self.qd, self.kd, self.table, self.form = q, kv, table, form
         self.bs = sum(per)
         own_pages = [-(-n // page) for n in own]
         total = sum(prefix) + sum(own_pages)
@@ -150,8 +150,9 @@ class Case:
                 n = len(k)
                 pv = p @ k[:, :512].abs()
                 inner = pv * (torch.expm1(2 * e)[:, None] + U + (3 * n + 64) * F)
-                if len(mine) and self.kd != "bf16":
-                    inner = inner + 2.0 ** -17 * (self.stored[mine][:, :512].abs() * self.scale).sum(0)
+                decoded = torch.cat([pre, mine]) if self.form == "each" else mine
+                if len(decoded) and self.kd != "bf16":
+                    inner = inner + 2.0 ** -17 * (self.stored[decoded][:, :512].abs() * self.scale).sum(0)
                 outs.append(o)
                 lses.append(lse)
                 var.append(p.square() @ k[:, :512].square() + o.square())
@@ -162,7 +163,7 @@ class Case:
     def plan(self, mla, num_sms=0):
         return mla.mla_shared_plan(indptr(self.per), self.prefix_at, self.own_at, self.last,
                                    page_size=self.page, q_dtype=self.qd, kv_dtype=self.kd,
-                                   q_len=self.q_len, num_sms=num_sms)
+                                   q_len=self.q_len, num_sms=num_sms, form=self.form)
 
     def run(self, mla, num_sms=0, check=True, plan=None, ws=None, want_lse=True):
         plan = self.plan(mla, num_sms) if plan is None else plan
@@ -213,13 +214,38 @@ def check_shared(mla, c, num_sms=0):
     ([5], [20], [4, 3, 64, 77, 5], 16, 4),
     ([3, 2], [9, 14], [2, 70, 33, 2, 2], 24, 3),
     ([4], [6], [1, 2, 130, 40], 32, 2)])
-def test_shared(mla, q, kv, per, prefix, own, page, q_len):
-    check_shared(mla, Case(per, prefix, own, page, q, kv, q_len))
+@pytest.mark.parametrize("form", ["once", "each"])
+def test_shared(mla, q, kv, per, prefix, own, page, q_len, form):
+    check_shared(mla, Case(per, prefix, own, page, q, kv, q_len, form=form))
 
 
 @pytest.mark.parametrize("q,kv", FORMATS)
-def test_shared_without_page_tables(mla, q, kv):
-    check_shared(mla, Case([2, 3], [13, 2], [40, 1, 0, 200, 9], 16, q, kv, table=False))
+@pytest.mark.parametrize("form,q_len", [("once", 1), ("each", 1), ("each", 2)])
+def test_shared_without_page_tables(mla, q, kv, form, q_len):
+    c = Case([2, 3], [13, 2], [40, 1, 1, 200, 9], 16, q, kv, q_len, table=False, form=form)
+    check_shared(mla, c)
+    # one of the two tables: the other's pages are still those of its offsets
+    o, lse = [x.clone() for x in c.run(mla)]
+    every = torch.arange(10000, dtype=torch.int32, device="cuda")
+    for pre, own in ((every, None), (None, every), (every, every)):
+        plan = c.plan(mla)
+        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+        mla.mla_shared_run(plan, c.query["q"], c.pool["kv"], o2, workspace=ws, lse=lse2,
+                           q_scale=c.query.get("q_scale"), kv_scale=c.pool.get("kv_scale"),
+                           kv_e8m0=c.pool.get("kv_e8m0"), prefix_indices=pre, kv_indices=own)
+        mla.mla_shared_check(plan, ws)
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("per,prefix,form", [([4], [64], "each"), ([40, 1], [700, 3], "once")])
+def test_shared_takes_the_faster_form(mla, per, prefix, form):
+    own = [5 * i for i in range(sum(per))]
+    auto = Case(per, prefix, own, 16, "fp8", "fp8", form="auto")
+    named = Case(per, prefix, own, 16, "fp8", "fp8", form=form)
+    assert (auto.plan(mla).info().num_items == 0) == (form == "each")
+    for x, y in zip(auto.run(mla), named.run(mla)):
+        assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("num_sms", [1, 2, 5, 8, 40, 152])
@@ -228,6 +254,7 @@ def test_shared_on_few_and_many_ctas(mla, num_sms):
     own = [(7 * i) % 50 for i in range(44)]
     check_shared(mla, Case([20, 8, 16], [100, 313, 4], own, 8, "fp8", "fp8"), num_sms)
     check_shared(mla, Case([20, 8, 16], [100, 313, 4], own, 8), num_sms)
+    check_shared(mla, Case([20, 8, 16], [100, 313, 4], own, 8, "bf16", "fp8", form="each"), num_sms)
 
 
 def test_shared_many_rows_and_long_prefixes(mla):
@@ -442,11 +469,12 @@ def test_shared_captured_and_on_another_stream(mla):
     mla.mla_shared_check(plan, ws)
 
 
-def test_shared_owner_and_optional_outputs(mla):
-    c = Case([4], [9], [3, 2, 0, 1], 8)
+@pytest.mark.parametrize("form", ["once", "each"])
+def test_shared_owner_and_optional_outputs(mla, form):
+    c = Case([4], [9], [3, 2, 0, 1], 8, form=form)
     o, _ = c.run(mla)
     owner = mla.MlaShared([0, 4], c.prefix_at, c.own_at, c.last, page_size=8, q_dtype="bf16",
-                          kv_dtype="bf16")
+                          kv_dtype="bf16", form=form)
     out = torch.empty(4, 16, 512, dtype=torch.bfloat16, device="cuda")
     assert owner(c.query["q"], c.pool["kv"], out, prefix_indices=c.prefix_ids,
                  kv_indices=c.own_ids) is out
