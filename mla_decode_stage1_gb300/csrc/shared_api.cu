@@ -116,12 +116,12 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t cluster
 // four have a place where 76 of two have.  64 requests of a 32,768-token prefix: 73 us
 // paired, 87 not; 5 to 19 requests of three prefixes: 40 us paired, 39 not.
 // And whether the prefixes are to be read for every request instead, by the decode
-// kernel, which has no rows to gather and fewer kernels in a row.  The estimates are
-// linear fits to 128 calls of both forms (2 to 128 requests of 256 to 16,384 shared
-// tokens, all types, 1 to 4 query tokens): the form taken was slower than the other in
-// 4 of them, by 28% at most, and by 0.7% on average.  8 requests of 1,024 e4m3 tokens:
-// 14.5 us each on its own, 23.3 once for all; 32 of 16,384: 53 and 43; 128 of 16,384:
-// 181 and 74.
+// kernel, which has no rows to gather and fewer kernels in a row.  The estimates (us)
+// are linear fits to 259 calls of both forms (1 to 5 groups, 2 to 128 requests, prefixes
+// of 64 to 32,768 tokens, all types, 1 to 4 query tokens), with which the form taken is
+// 0.9% slower than the better one on average, by more than a tenth in 10 of them.  8
+// requests of 1,024 e4m3 tokens: 14.5 us each on its own, 23.3 once for all; 32 of
+// 16,384: 53 and 43; 128 of 16,384: 181 and 74.
 void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
                  bool whole_device, mla_shared_form form) {
   int32_t on_device[2] = {P->num_sms / 2, P->num_sms / 4};
@@ -131,24 +131,30 @@ void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* pref
       if (n > 0) on_device[k] = std::min(on_device[k], n);
     }
   const bool pairs = mla::kHeads != P->own->rows;        // two query tokens an item
-  const double tile_us = P->kv_dtype == MLA_DTYPE_BF16    ? 3.5
-                         : P->kv_dtype == MLA_DTYPE_MXFP4 ? 2.4
-                         : (P->q_dtype == MLA_DTYPE_BF16 ? 1.6 : 1.4) * (pairs ? 1.5 : 1.0);
-  double time[2] = {0, 0}, each = 0, tokens_us = 0;
+  const double tile_us = P->kv_dtype == MLA_DTYPE_BF16    ? 4.2
+                         : P->kv_dtype == MLA_DTYPE_MXFP4 ? 2.9
+                         : (P->q_dtype == MLA_DTYPE_BF16 ? 1.9 : 1.8) * (pairs ? 1.4 : 1.0);
+  double time[2] = {0, 0}, each = 14.5, once = 18;
+  int64_t blocks[2] = {0, 0};
   for (int32_t g = 0; g < P->groups; ++g) {
     const int64_t keys = (static_cast<int64_t>(prefix_indptr[g + 1]) - prefix_indptr[g]) * P->page_size;
     const int64_t tokens = static_cast<int64_t>(group_indptr[g + 1] - group_indptr[g]) * P->q_len;
     const double tiles = static_cast<double>((keys + mla::kSpTile - 1) / mla::kSpTile);
-    each += tiles * static_cast<double>(tokens) / (pairs ? 2 : 1) * tile_us / P->num_sms;
-    tokens_us += static_cast<double>(tokens) * 5.5 / P->num_sms;
+    each += static_cast<double>(tokens) / (pairs ? 2 : 1) * (3 + tiles * tile_us) / P->num_sms;
+    once += static_cast<double>(tokens) * 15 / P->num_sms;
+    if (!P->direct) once += static_cast<double>(keys) * 0.33e-3;
+    if (keys > 0)
+      for (int k = 0; k < 2; ++k)
+        blocks[k] += (tokens + (k + 1) * kTokensPerBlock - 1) / ((k + 1) * kTokensPerBlock);
     time[0] += tiles * static_cast<double>((tokens + kTokensPerBlock - 1) / kTokensPerBlock) *
                (P->direct && P->page_size % mla::kSpTile != 0 ? 3900 : 3300);
     time[1] += tiles * static_cast<double>((tokens + 2 * kTokensPerBlock - 1) / (2 * kTokensPerBlock)) * 2600;
   }
   for (int k = 0; k < 2; ++k) time[k] /= std::max(1, on_device[k]);
   P->paired = on_device[1] > 0 && time[1] < time[0];
-  const double once = 18 + (P->direct ? 0 : 1.6) + time[P->paired] / 1900 + tokens_us;
-  P->each = form == MLA_SHARED_EACH || (form == MLA_SHARED_AUTO && 12 + each < once);
+  once += time[P->paired] / 1900 +
+          0.18 * on_device[P->paired] / static_cast<double>(std::max<int64_t>(1, blocks[P->paired]));
+  P->each = form == MLA_SHARED_EACH || (form == MLA_SHARED_AUTO && each < once);
   P->blocks = P->paired ? 2 : 1;
   P->tall = !P->paired && (!P->direct || P->page_size % mla::kSpTile == 0);
   P->num_clusters = std::max(1, on_device[P->paired]);
