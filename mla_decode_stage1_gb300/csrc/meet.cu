@@ -11,37 +11,45 @@
 // Bound: latency, and memory for many rows.  The prefix kernel's partials stand as
 // [dim / 8][row][dim % 8], so that both kernels move whole lines: a CTA takes a
 // token's 16 rows and 128 of the 512 dims, a thread 8 dims of a row (16 rows of 32
-// bytes stand together), with up to 8 partials in flight.
+// bytes stand together), with up to 8 partials in flight.  Of tokens with many
+// partials (kSlices 4) a CTA takes 32 dims, and a thread every fourth partial.
 
 #include "shared.h"
 
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256;                 // 16 rows x 16 groups of 8 dims
+constexpr int kThreads = 256;                 // 16 rows x 16 groups of 8 dims (or slices)
 
-template <int kAhead>
+// The larger of two maxima; NaN stays.
+__device__ __forceinline__ float top_of(float a, float b) {
+  return a != a ? a : b != b ? b : fmaxf(a, b);
+}
+
+template <int kAhead, int kSlices>
 __global__ void __launch_bounds__(kThreads) meet_kernel(const MeetParams p) {
-  const int64_t token = blockIdx.x / 4;
-  const int row = threadIdx.x & 15, group = blockIdx.x % 4 * 16 + (threadIdx.x >> 4);
+  constexpr int kGroups = 16 / kSlices;                  // of a CTA
+  const int64_t token = blockIdx.x / (4 * kSlices);
+  const int row = threadIdx.x & 15, slice = threadIdx.x / (16 * kGroups);
+  const int group = blockIdx.x % (4 * kSlices) * kGroups + (threadIdx.x >> 4) % kGroups;
   const MeetJob j = p.jobs[token];
   const bool sound = reinterpret_cast<const WsHeader*>(p.err)->stamp == p.stamp &&
                      check_of(j, p.stamp) == j.check;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are there
   if (!sound) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrStale);
     return;
   }
   const int n = j.own_count + j.prefix_count;
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // the partials are there
   float M = -INFINITY, wsum = 0.0f, acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-  for (int s0 = 0; s0 < n; s0 += kAhead) {
+  for (int s0 = slice; s0 < n; s0 += kAhead * kSlices) {
     float lse[kAhead];
     float4 v[kAhead][2];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int s = s0 + u;
+      const int s = s0 + u * kSlices;
       lse[u] = -INFINITY;
       v[u][0] = v[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (s >= n) continue;
@@ -61,9 +69,7 @@ __global__ void __launch_bounds__(kThreads) meet_kernel(const MeetParams p) {
     // the maximum so far (NaN stays: what it scales is NaN)
     float top = M;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) top = lse[u] != lse[u] ? lse[u] : fmaxf(top, lse[u]);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) top = lse[u] != lse[u] ? lse[u] : top;
+    for (int u = 0; u < kAhead; ++u) top = top_of(top, lse[u]);
     if (top == -INFINITY) continue;
     const float f = M == -INFINITY ? 0.0f : ex2(M - top);
     M = top;
@@ -80,6 +86,37 @@ __global__ void __launch_bounds__(kThreads) meet_kernel(const MeetParams p) {
       acc[4] += w * v[u][1].x; acc[5] += w * v[u][1].y;
       acc[6] += w * v[u][1].z; acc[7] += w * v[u][1].w;
     }
+  }
+  if constexpr (kSlices > 1) {
+    // the slices' sums, by the first one's threads
+    constexpr int kPer = 16 * kGroups;
+    __shared__ float parts[kSlices - 1][10][kPer];
+    const int at = threadIdx.x % kPer;
+    if (slice > 0) {
+      parts[slice - 1][0][at] = M;
+      parts[slice - 1][1][at] = wsum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) parts[slice - 1][2 + i][at] = acc[i];
+    }
+    __syncthreads();
+    if (slice > 0) return;
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < kSlices - 1; ++k) top = top_of(top, parts[k][0][at]);
+    if (top != -INFINITY) {
+      const float f = M == -INFINITY ? 0.0f : ex2(M - top);
+      wsum *= f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] *= f;
+#pragma unroll
+      for (int k = 0; k < kSlices - 1; ++k) {
+        const float w = parts[k][0][at] == -INFINITY ? 0.0f : ex2(parts[k][0][at] - top);
+        wsum += w * parts[k][1][at];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += w * parts[k][2 + i][at];
+      }
+    }
+    M = top;
   }
   const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
   uint32_t o[4];
@@ -98,7 +135,10 @@ __global__ void __launch_bounds__(kThreads) meet_kernel(const MeetParams p) {
 
 cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tokens * 4));
+  // In slices: 2 tokens of 65 partials 21 us a call, 28 not; 4 tokens of 9 12.5 and 14.5,
+  // but 32 tokens of 9 22.6 and 20.6.
+  const bool wide = p.most > 16 || (p.most > 6 && p.tokens * 4 < 152);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tokens * (wide ? 16 : 4)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -106,8 +146,9 @@ cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.most <= 4 ? cudaLaunchKernelEx(&cfg, meet_kernel<4>, p)
-                     : cudaLaunchKernelEx(&cfg, meet_kernel<8>, p);
+  return wide          ? cudaLaunchKernelEx(&cfg, meet_kernel<8, 4>, p)
+         : p.most <= 4 ? cudaLaunchKernelEx(&cfg, meet_kernel<4, 1>, p)
+                       : cudaLaunchKernelEx(&cfg, meet_kernel<8, 1>, p);
 }
 
 }  // namespace mla

@@ -119,8 +119,8 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t cluster
 // kernel, which has no rows to gather and fewer kernels in a row.  The estimates (us)
 // are linear fits to 259 calls of both forms (1 to 5 groups, 2 to 128 requests, prefixes
 // of 64 to 32,768 tokens, all types, 1 to 4 query tokens), with which the form taken is
-// 0.9% slower than the better one on average, by more than a tenth in 10 of them.  8
-// requests of 1,024 e4m3 tokens: 14.5 us each on its own, 23.3 once for all; 32 of
+// 0.4% slower than the better one on average, by more than a tenth in 3 of them.  8
+// requests of 1,024 e4m3 tokens: 12.5 us each on its own, 22.7 once for all; 32 of
 // 16,384: 53 and 43; 128 of 16,384: 181 and 74.
 void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
                  bool whole_device, mla_shared_form form) {
