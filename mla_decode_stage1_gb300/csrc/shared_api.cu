@@ -62,33 +62,37 @@ struct Block {
 // The blocks' key tiles, in order, cut into at most `clusters` ranges of nearly
 // equal cost (kItemCost for each item, 1 for each tile).  The smallest largest
 // cost that greedy ranges reach is found by bisection.
-void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t clusters) {
+template <class Emit>
+int64_t cut(const std::vector<Block>& blocks, int64_t cap, Emit&& emit) {
+  int64_t ranges = 0, left = 0;
+  for (size_t k = 0; k < blocks.size(); ++k) {
+    const int64_t tiles = (blocks[k].keys + mla::kSpTile - 1) / mla::kSpTile;
+    for (int64_t at = 0; at < tiles;) {
+      if (left <= kItemCost) {
+        left = cap;
+        ++ranges;
+      }
+      const int64_t take = std::min(left - kItemCost, tiles - at);
+      emit(k, at, take, ranges - 1);
+      left -= kItemCost + take;
+      at += take;
+    }
+  }
+  return ranges;
+}
+int64_t smallest_cost(const std::vector<Block>& blocks, int64_t clusters) {
   int64_t total = 0;
   for (const Block& b : blocks) total += (b.keys + mla::kSpTile - 1) / mla::kSpTile;
-  auto cut = [&](int64_t cap, auto&& emit) {
-    int64_t ranges = 0, left = 0;
-    for (size_t k = 0; k < blocks.size(); ++k) {
-      const int64_t tiles = (blocks[k].keys + mla::kSpTile - 1) / mla::kSpTile;
-      for (int64_t at = 0; at < tiles;) {
-        if (left <= kItemCost) {
-          left = cap;
-          ++ranges;
-        }
-        const int64_t take = std::min(left - kItemCost, tiles - at);
-        emit(k, at, take, ranges - 1);
-        left -= kItemCost + take;
-        at += take;
-      }
-    }
-    return ranges;
-  };
   int64_t lo = kItemCost + 1, hi = kItemCost * (1 + static_cast<int64_t>(blocks.size())) + total;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
-    if (cut(mid, [](size_t, int64_t, int64_t, int64_t) {}) <= clusters) hi = mid; else lo = mid + 1;
+    if (cut(blocks, mid, [](size_t, int64_t, int64_t, int64_t) {}) <= clusters) hi = mid; else lo = mid + 1;
   }
+  return lo;
+}
+void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t cost) {
   int64_t last = -1;
-  cut(lo, [&](size_t k, int64_t at, int64_t take, int64_t range) {
+  cut(blocks, cost, [&](size_t k, int64_t at, int64_t take, int64_t range) {
     const Block& b = blocks[k];
     if (range != last) {
       const int32_t n = static_cast<int32_t>(P->items.size());
@@ -110,60 +114,102 @@ void cut_blocks(mla_shared* P, const std::vector<Block>& blocks, int64_t cluster
   P->num_slots = static_cast<int32_t>(P->items.size());
 }
 
-// Whether to work in blocks of 256 rows, and on how many clusters.  A tile of 128
-// keys takes 2,600 cycles on a paired cluster and 3,300 on another (3,900 with boxes
+// Cycles of a tile in blocks of 128 and 256 rows.
+double tile_cycles(const mla_shared* P, bool paired) {
+  return paired ? 2600 : P->direct && P->page_size % mla::kSpTile != 0 ? 3900 : 3300;
+}
+
+// The decode kernel's time (us) on a number of CTAs: 9, and for each CTA its share of
+// the items' beginnings and ends and of their tiles.  Linear fits to 324 calls of 16 to
+// 512 items of up to 1,500 tokens on 8 to 64 CTAs (12% off, all in all).
+struct DecodeWork {
+  double item, tile, sum;
+  explicit DecodeWork(const mla_shared* P) : sum(0) {
+    const bool pairs = P->own->rows > mla::kHeads;       // two query tokens an item
+    switch (P->kv_dtype) {
+      case MLA_DTYPE_BF16: item = 0.8, tile = 4.1; break;
+      case MLA_DTYPE_MXFP4: item = 1.5, tile = 2.6; break;
+      default:
+        if (P->q_dtype == MLA_DTYPE_BF16)
+          item = pairs ? 5.0 : 3.5, tile = pairs ? 2.9 : 1.8;
+        else
+          item = pairs ? 2.7 : 1.2, tile = pairs ? 2.6 : 2.0;
+    }
+  }
+  void add(int64_t items, int64_t tiles) {
+    sum += item * static_cast<double>(items) + tile * static_cast<double>(tiles);
+  }
+  double on(int64_t ctas) const { return 9 + sum / static_cast<double>(ctas); }
+};
+
+// How the prefixes' tiles are cut (the largest cost of a cluster), and for how many CTAs
+// the requests' own ends.  Those run beside the prefix kernel on the SMs that it leaves
+// and are not to last longer than it does: with fewer clusters, where that takes less
+// time in all, or else (0) cut for all SMs, to come behind it.  `us`: until both are
+// through.  64 requests with 256 own tokens on average behind 32,768: 64 us on 32
+// clusters, 73 on 36; 128 behind 4,096: 39 on 24, 47 on 32.
+int64_t choose_cut(const mla_shared* P, const std::vector<Block>& blocks, const DecodeWork& own,
+                   int32_t* own_ctas, double* us) {
+  const double cost_us = tile_cycles(P, P->paired) / 1900;
+  const int64_t most = P->num_clusters;
+  int64_t best = smallest_cost(blocks, most);
+  *own_ctas = 0;
+  *us = static_cast<double>(best) * cost_us;
+  if (own.sum == 0) return best;
+  *us += own.on(P->num_sms);
+  for (int64_t n = most; n >= std::max<int64_t>(1, most / 2); --n) {
+    const int64_t idle = P->num_sms - n * (P->paired ? 4 : 2);
+    if (idle <= 0) continue;
+    const int64_t cost = smallest_cost(blocks, n);
+    const double t = std::max(static_cast<double>(cost) * cost_us, own.on(idle));
+    if (t >= *us) continue;
+    *us = t;
+    best = cost;
+    *own_ctas = static_cast<int32_t>(idle);
+  }
+  return best;
+}
+
+// Whether to work in blocks of 256 rows, and on how many clusters at most.  A tile of
+// 128 keys takes 2,600 cycles on a paired cluster and 3,300 on another (3,900 with boxes
 // of 64 keys), but blocks of 256 rows may leave half of one empty, and 36 clusters of
 // four have a place where 76 of two have.  64 requests of a 32,768-token prefix: 73 us
 // paired, 87 not; 5 to 19 requests of three prefixes: 40 us paired, 39 not.
-// And whether the prefixes are to be read for every request instead, by the decode
-// kernel, which has no rows to gather and fewer kernels in a row.  The estimates (us)
-// are linear fits to 259 calls of both forms (1 to 5 groups, 2 to 128 requests, prefixes
-// of 64 to 32,768 tokens, all types, 1 to 4 query tokens), with which the form taken is
-// 0.4% slower than the better one on average, by more than a tenth in 3 of them.  8
-// requests of 1,024 e4m3 tokens: 12.5 us each on its own, 22.7 once for all; 32 of
-// 16,384: 53 and 43; 128 of 16,384: 181 and 74.
-void choose_form(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
-                 bool whole_device, mla_shared_form form) {
+void choose_blocks(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
+                   bool whole_device) {
   int32_t on_device[2] = {P->num_sms / 2, P->num_sms / 4};
   if (whole_device)
     for (int k = 0; k < 2; ++k) {
       const int32_t n = mla::prefix_clusters(k == 1);
       if (n > 0) on_device[k] = std::min(on_device[k], n);
     }
-  const bool pairs = mla::kHeads != P->own->rows;        // two query tokens an item
-  const double tile_us = P->kv_dtype == MLA_DTYPE_BF16    ? 4.2
-                         : P->kv_dtype == MLA_DTYPE_MXFP4 ? 2.9
-                         : (P->q_dtype == MLA_DTYPE_BF16 ? 1.9 : 1.8) * (pairs ? 1.4 : 1.0);
-  double time[2] = {0, 0}, each = 14.5, once = 18;
-  int64_t blocks[2] = {0, 0};
+  double time[2] = {0, 0};
   for (int32_t g = 0; g < P->groups; ++g) {
     const int64_t keys = (static_cast<int64_t>(prefix_indptr[g + 1]) - prefix_indptr[g]) * P->page_size;
     const int64_t tokens = static_cast<int64_t>(group_indptr[g + 1] - group_indptr[g]) * P->q_len;
-    const double tiles = static_cast<double>((keys + mla::kSpTile - 1) / mla::kSpTile);
-    each += static_cast<double>(tokens) / (pairs ? 2 : 1) * (3 + tiles * tile_us) / P->num_sms;
-    once += static_cast<double>(tokens) * 15 / P->num_sms;
-    if (!P->direct) once += static_cast<double>(keys) * 0.33e-3;
-    if (keys > 0)
-      for (int k = 0; k < 2; ++k)
-        blocks[k] += (tokens + (k + 1) * kTokensPerBlock - 1) / ((k + 1) * kTokensPerBlock);
-    time[0] += tiles * static_cast<double>((tokens + kTokensPerBlock - 1) / kTokensPerBlock) *
-               (P->direct && P->page_size % mla::kSpTile != 0 ? 3900 : 3300);
-    time[1] += tiles * static_cast<double>((tokens + 2 * kTokensPerBlock - 1) / (2 * kTokensPerBlock)) * 2600;
+    const int64_t tiles = (keys + mla::kSpTile - 1) / mla::kSpTile;
+    for (int k = 0; k < 2; ++k) {
+      const int64_t per = (k + 1) * kTokensPerBlock;
+      time[k] += static_cast<double>(tiles * ((tokens + per - 1) / per)) * tile_cycles(P, k == 1) /
+                 std::max(1, on_device[k]);
+    }
   }
-  for (int k = 0; k < 2; ++k) time[k] /= std::max(1, on_device[k]);
   P->paired = on_device[1] > 0 && time[1] < time[0];
-  once += time[P->paired] / 1900 +
-          0.18 * on_device[P->paired] / static_cast<double>(std::max<int64_t>(1, blocks[P->paired]));
-  P->each = form == MLA_SHARED_EACH || (form == MLA_SHARED_AUTO && each < once);
   P->blocks = P->paired ? 2 : 1;
   P->tall = !P->paired && (!P->direct || P->page_size % mla::kSpTile == 0);
   P->num_clusters = std::max(1, on_device[P->paired]);
 }
 
 mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* prefix_indptr,
-                     const int32_t* kv_indptr, const int32_t* last_len) {
+                     const int32_t* kv_indptr, const int32_t* last_len, mla_shared_form form) {
   const int32_t t = P->q_len, per_block = P->blocks * kTokensPerBlock;
-  std::vector<int32_t> each_base(P->each ? P->bs : 0), each_pages(P->each ? P->bs : 0);
+  const int32_t per_request = P->own->bs / P->bs;        // items: query tokens, or pairs
+  std::vector<int32_t> each_base(P->bs, 0), each_pages(P->bs, 0);
+  DecodeWork own(P);
+  for (const mla::WorkItem& w : P->own->items) own.add(w.tok_begin == 0, 0);
+  own.add(0, P->own->total_tiles);
+  DecodeWork each = own;
+  int64_t gathered = 0;
   std::vector<Block> blocks;
   std::vector<int32_t> block_of(P->bs, -1), first_of(P->bs, 0);   // first: the group's first token
   int64_t rows = 0;
@@ -183,15 +229,12 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
       int64_t n = (static_cast<int64_t>(kv_indptr[b + 1]) - kv_indptr[b]) * P->page_size;
       if (n > 0 && last_len != nullptr) n -= P->page_size - last_len[b];
       if (n < t - 1) return MLA_ERR_INVALID_ARG;
-      if (P->each) {
-        each_base[b] = prefix_indptr[g];
-        each_pages[b] = static_cast<int32_t>(np);
-        continue;
-      }
+      each_base[b] = prefix_indptr[g];
+      each_pages[b] = static_cast<int32_t>(np);
+      each.add(per_request, per_request * ((keys + mla::kTile - 1) / mla::kTile));
       block_of[b] = static_cast<int32_t>(blocks.size());
       first_of[b] = b0 * t;
     }
-    if (P->each) continue;
     const int64_t tokens = static_cast<int64_t>(b1 - b0) * t;
     for (int64_t a = 0; a < tokens; a += per_block) {
       Block b;
@@ -203,6 +246,7 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
       blocks.push_back(b);
     }
     if (P->direct) continue;
+    gathered += keys;
     for (int64_t k = 0; k < keys; k += mla::kSpTile) {
       ExpandTile e{};
       e.page_base = prefix_indptr[g];
@@ -213,16 +257,30 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
     }
     rows += (keys + mla::kSpTile - 1) / mla::kSpTile * mla::kSpTile;
   }
-  cut_blocks(P, blocks, P->num_clusters);
+  // Whether the prefixes are to be read for every request instead, by the decode
+  // kernel, which has no rows to gather and fewer kernels in a row.
+  int32_t own_ctas = 0;
+  double once_us = 0;
+  const int64_t cost = choose_cut(P, blocks, own, &own_ctas, &once_us);
+  once_us += 8 + 0.33e-3 * static_cast<double>(gathered) + 6.0 * P->bs * t / P->num_sms;
+  P->each = form == MLA_SHARED_EACH || (form == MLA_SHARED_AUTO && each.on(P->num_sms) + 3 < once_us);
+  //DUMP
   if (P->each) {
+    own_ctas = 0;
+    blocks.clear();
+    P->tiles.clear();
+    block_of.assign(P->bs, -1);
+  }
+  cut_blocks(P, blocks, cost);
+  if (P->each || own_ctas > 0) {
     mla_plan_destroy(P->own);
     P->own = nullptr;
-    const mla_plan_options o{0, P->num_sms, 0, 0, 1};
+    const mla_plan_options o{0, own_ctas > 0 ? own_ctas : P->num_sms, 0, 0, 1};
     const mla::PrefixPages prefixes{each_base.data(), each_pages.data()};
     const mla_status st = mla::plan_with_prefixes(kv_indptr, last_len, P->bs, t, P->page_size,
                                                   static_cast<mla_dtype>(P->q_dtype),
                                                   static_cast<mla_dtype>(P->kv_dtype), &o,
-                                                  &prefixes, &P->own);
+                                                  P->each ? &prefixes : nullptr, &P->own);
     if (st != MLA_OK) return st;
   }
   // partial results of every block, then of every query token
@@ -344,8 +402,9 @@ mla_status mla_shared_plan(const int32_t* group_indptr_host, const int32_t* pref
     st = mla_decode_plan_ex(kv_indptr_host, kv_last_page_len_host, P->bs, q_len, page_size, q_dtype,
                             kv_dtype, &o, &P->own);
     if (st == MLA_OK) {
-      choose_form(P, group_indptr_host, prefix_indptr_host, whole_device, form);
-      st = make_plan(P, group_indptr_host, prefix_indptr_host, kv_indptr_host, kv_last_page_len_host);
+      choose_blocks(P, group_indptr_host, prefix_indptr_host, whole_device);
+      st = make_plan(P, group_indptr_host, prefix_indptr_host, kv_indptr_host, kv_last_page_len_host,
+                     form);
     }
   } catch (...) {   // out of host memory
     st = MLA_ERR_INVALID_ARG;

@@ -1655,8 +1655,9 @@ __global__ void __launch_bounds__(Layout<QM>::kThreads, 1) mla_stage1_kernel(con
     tmem_dealloc(tmem, L::kTmemCols);
   }
   // launched beside the kernel before it, on the SMs that one leaves: through
-  // only when that one is
-  if (p.beside && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // only when that one is (the last CTA, which takes no other's place, waits)
+  if (p.beside && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 int stage1_smem_bytes(int qmode) {
