@@ -12,7 +12,9 @@
 // [dim / 8][row][dim % 8], so that both kernels move whole lines: a CTA takes a
 // token's 16 rows and 128 of the 512 dims, a thread 8 dims of a row (16 rows of 32
 // bytes stand together), with up to 8 partials in flight.  Of tokens with many
-// partials (kSlices 4) a CTA takes 32 dims, and a thread every fourth partial.
+// partials (kSlices 4) a CTA takes 32 dims, and a thread every fourth partial.  64
+// tokens of 9 or 10 partials, 22 MB, take 9.4 us with all of it in DRAM; in a call it
+// comes from L2.
 
 #include "shared.h"
 
