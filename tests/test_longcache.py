@@ -127,6 +127,17 @@ def test_shared_plan_for_each_request(mla):
     assert plan(mla, [0, 2], [0, 1000], [0, 1, 2], form="each").workspace_bytes < 152 * 2 * 33000 + 65536
 
 
+def test_shared_plan_leaves_sms_for_the_own_ends(mla):
+    # 64 requests with 500 own tokens behind 16,384: the decode kernel's CTAs and the
+    # clusters' fit the SMs together; without own tokens the clusters have them all
+    p = plan(mla, [0, 64], [0, 2048], [63 * i for i in range(65)]).info()
+    alone = plan(mla, [0, 64], [0, 2048], [0] * 65).info()
+    assert p.num_clusters < alone.num_clusters == 38
+    assert plan(mla, [0, 64], [0, 2048], [63 * i for i in range(65)], sms=3).info().num_clusters == 1
+    # any number of CTAs is planned for in no time
+    assert plan(mla, [0, 64], [0, 2048], [63 * i for i in range(65)], sms=1 << 20).info().num_items > 0
+
+
 def run_args(p, a, **kw):
     d = dict(plan=p.handle, q=a, qs=None, kv=a, ks=None, e8=None, e8s=0, rows=1 << 20, pidx=a, idx=a,
              ws=a, wsb=p.workspace_bytes, out=a, lse=None)
@@ -183,12 +194,13 @@ def bounds_args(a, **kw):
 @pytest.mark.parametrize("kw", [
     dict(kv=None), dict(dtype=3), dict(dtype=-1), dict(dtype=2), dict(dtype=2, e8=1, e8s=17),
     dict(rows=0), dict(rows=1 << 31), dict(page=0), dict(old=None), dict(bs=0), dict(table=None),
-    dict(stride=3), dict(cols=-1), dict(bounds=None), dict(pages=0)])
+    dict(stride=3), dict(cols=-1), dict(bounds=None), dict(pages=0),
+    dict(bs=1 << 20, cols=2048, stride=2048)])
 def test_page_bounds_refuses(mla, mem, kw):
     assert mla._lib.mla_page_bounds(*bounds_args(mem, **kw)) == 1
 
 
-@pytest.mark.parametrize("name,by", [("kv", 8), ("old", 2), ("new", 1), ("table", 2), ("bounds", 8),
+@pytest.mark.parametrize("name,by", [("kv", 8), ("old", 2), ("new", 1), ("table", 2), ("bounds", 16),
                                      ("err", 2)])
 def test_page_bounds_refuses_misaligned(mla, mem, name, by):
     assert mla._lib.mla_page_bounds(*bounds_args(mem, **{name: mem + by})) == 1
@@ -212,7 +224,7 @@ def test_page_scores_refuses(mla, mem, kw, status):
     assert mla._lib.mla_page_scores(*scores_args(mem, **kw)) == status
 
 
-@pytest.mark.parametrize("name,by", [("q", 8), ("bounds", 8), ("lens", 2), ("table", 1), ("scores", 2),
+@pytest.mark.parametrize("name,by", [("q", 8), ("bounds", 16), ("lens", 2), ("table", 1), ("scores", 2),
                                      ("ks", 2), ("err", 1)])
 def test_page_scores_refuses_misaligned(mla, mem, name, by):
     assert mla._lib.mla_page_scores(*scores_args(mem, **{name: mem + by})) == 1
