@@ -34,6 +34,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
   constexpr int kPieces = KV == MLA_DTYPE_BF16 ? 72 : KV == MLA_DTYPE_FP8_E4M3 ? 36 : 18;
   constexpr int kStep = kThreads / kPieces, kSteps = kRowsPerCta / kStep;
   constexpr int kRowBytes = kPieces * 16;
+  // (launched while the kernel before it ends; what follows may count on that end too)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const ExpandTile t = p.tiles[blockIdx.x / kParts];
   if (reinterpret_cast<const WsHeader*>(p.err)->stamp != p.stamp || check_of(t, p.stamp) != t.check) {
@@ -94,13 +96,10 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
 
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.num_tiles) * kParts);
-  if (p.kv_dtype == MLA_DTYPE_BF16)
-    gather_kernel<MLA_DTYPE_BF16><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.kv_dtype == MLA_DTYPE_FP8_E4M3)
-    gather_kernel<MLA_DTYPE_FP8_E4M3><<<grid, kThreads, 0, stream>>>(p);
-  else
-    gather_kernel<MLA_DTYPE_MXFP4><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  auto* kernel = p.kv_dtype == MLA_DTYPE_BF16       ? gather_kernel<MLA_DTYPE_BF16>
+                 : p.kv_dtype == MLA_DTYPE_FP8_E4M3 ? gather_kernel<MLA_DTYPE_FP8_E4M3>
+                                                    : gather_kernel<MLA_DTYPE_MXFP4>;
+  return launch_dependent(kernel, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace mla

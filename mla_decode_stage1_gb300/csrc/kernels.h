@@ -114,7 +114,8 @@ struct Stage1Params {
   const uint8_t* kv_e8m0;       // MXFP4 only: e8m0 scale rows (18 bytes used per row)
   int64_t sc_stride;            // bytes between scale rows (even, >= 18)
   int32_t exact_q;              // 1: bf16 q is split into two e4m3 terms without loss
-  int32_t beside;               // 1: may run beside the kernel launched before it
+  int32_t beside;               // 1: runs beside the kernel launched before it and ends
+                                // after it; 2: is launched while that one ends
 };
 
 struct Stage2Params {

@@ -136,21 +136,12 @@ __global__ void __launch_bounds__(kThreads) meet_kernel(const MeetParams p) {
 }  // namespace
 
 cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
   // In slices: 2 tokens of 65 partials 21 us a call, 28 not; 4 tokens of 9 12.5 and 14.5,
   // but 32 tokens of 9 22.6 and 20.6.
   const bool wide = p.most > 16 || (p.most > 6 && p.tokens * 4 < 152);
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tokens * (wide ? 16 : 4)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return wide          ? cudaLaunchKernelEx(&cfg, meet_kernel<8, 4>, p)
-         : p.most <= 4 ? cudaLaunchKernelEx(&cfg, meet_kernel<4, 1>, p)
-                       : cudaLaunchKernelEx(&cfg, meet_kernel<8, 1>, p);
+  const dim3 grid(static_cast<unsigned>(p.tokens * (wide ? 16 : 4)));
+  auto* kernel = wide ? meet_kernel<8, 4> : p.most <= 4 ? meet_kernel<4, 1> : meet_kernel<8, 1>;
+  return launch_dependent(kernel, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace mla

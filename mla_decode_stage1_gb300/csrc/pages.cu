@@ -9,6 +9,7 @@
 
 #include "layer.h"
 #include "ptx.cuh"
+#include "shared.h"
 
 namespace mla {
 namespace {
@@ -27,6 +28,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+// These kernels are launched while the one before them in the stream ends: all that
+// they read and write is touched behind this wait for its end.
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 __device__ __forceinline__ void report(int32_t* err, int32_t bits) {
   if (err != nullptr) atomicOr(err, bits);
@@ -85,6 +91,7 @@ __global__ void __launch_bounds__(kBoundThreads, KV == MLA_DTYPE_BF16 ? 4 : 3)
     new_len = n < 0 ? 0 : n;
     return o < 0 || n < 0 ? kErrBadLength : 0;
   };
+  wait_for_stream();
   uint32_t mine = blockIdx.x;                            // the next page of the list to do
   uint32_t before = 0;                                   // pages of the chunks before
   for (int b0 = 0; b0 < p.bs; b0 += kBoundThreads) {
@@ -272,6 +279,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
   const int64_t cta0 = static_cast<int64_t>(chunk) * (kScoreWarps * 8 * kTiles);
   const int64_t page0 = cta0 + warp * (8 * kTiles);
   const int g = lane >> 2, c = lane & 3;
+  wait_for_stream();
   // (read beside the length; what is behind it is not looked at)
   int32_t entry[kTiles];
 #pragma unroll
@@ -520,6 +528,7 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(const SelectParam
   const float* scores = p.scores + r * p.scores_stride;
   const int32_t* table = p.table + r / p.q_len * p.table_stride;
   const uint32_t columns = p.columns;
+  wait_for_stream();
   // The first columns of a thread, read beside the length: what is behind it is not
   // looked at.
   float early[kEarly];
@@ -780,8 +789,8 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
                                                4 * (kBinWords + kKeysInShared));
     if (e != cudaSuccess) return e;
   }
-  page_select_kernel<kThreads, kCount><<<static_cast<unsigned>(p.rows), kThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(page_select_kernel<kThreads, kCount>, dim3(static_cast<unsigned>(p.rows)), kThreads,
+                bytes, stream, p);
 }
 
 }  // namespace
@@ -819,13 +828,11 @@ extern "C" mla_status mla_page_bounds(const void* kv, mla_dtype kv_dtype, const 
   const int64_t most = static_cast<int64_t>(batch_size) * std::max(table_pages, 1);
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, 1216)));
   const cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  if (kv_dtype == MLA_DTYPE_BF16)
-    mla::page_bounds_kernel<MLA_DTYPE_BF16><<<grid, mla::kBoundThreads, 0, stream>>>(p);
-  else if (kv_dtype == MLA_DTYPE_FP8_E4M3)
-    mla::page_bounds_kernel<MLA_DTYPE_FP8_E4M3><<<grid, mla::kBoundThreads, 0, stream>>>(p);
-  else
-    mla::page_bounds_kernel<MLA_DTYPE_MXFP4><<<grid, mla::kBoundThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  auto* kernel = kv_dtype == MLA_DTYPE_BF16       ? mla::page_bounds_kernel<MLA_DTYPE_BF16>
+                 : kv_dtype == MLA_DTYPE_FP8_E4M3 ? mla::page_bounds_kernel<MLA_DTYPE_FP8_E4M3>
+                                                  : mla::page_bounds_kernel<MLA_DTYPE_MXFP4>;
+  const cudaError_t e = mla::launch_dependent(kernel, grid, mla::kBoundThreads, 0, stream, p);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 extern "C" mla_status mla_page_scores(const void* q, mla_dtype q_dtype, const float* q_scale,
@@ -858,11 +865,9 @@ extern "C" mla_status mla_page_scores(const void* q, mla_dtype q_dtype, const fl
   p.chunks = (table_pages - 1) / (wide ? 4 * kPages : kPages) + 1;
   if (static_cast<int64_t>(p.chunks) * batch_size > INT32_MAX) return MLA_ERR_INVALID_ARG;
   const dim3 grid(p.chunks * batch_size, q_len);
-  if (wide)
-    mla::page_scores_kernel<4, 3><<<grid, 32 * mla::kScoreWarps, 0, stream>>>(p);
-  else
-    mla::page_scores_kernel<1, 4><<<grid, 32 * mla::kScoreWarps, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  auto* kernel = wide ? mla::page_scores_kernel<4, 3> : mla::page_scores_kernel<1, 4>;
+  const cudaError_t e = mla::launch_dependent(kernel, grid, 32 * mla::kScoreWarps, 0, stream, p);
+  return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 extern "C" mla_status mla_page_select(const float* scores, int64_t scores_stride,

@@ -851,6 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   at.half = static_cast<int>(rank) % R::kCtas;
   at.first = static_cast<uint32_t>(at.kind * R::kCtas);
   at.peer = rank ^ R::kCtas;
+  // (the first kernel of its call: behind what the caller has launched; else only the
+  // gathered rows are waited for, by the loads)
+  if (p.direct) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&ms->full[i]), 1);
     for (int i = 0; i < 22; ++i) mbar_init(smem_u32(&ms->empty[i]), 1);
@@ -971,8 +974,7 @@ template <bool kPaired>
 cudaError_t launch(const PrefixParams& p, int clusters, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  // (with nothing of the call before it, it follows what the caller has launched)
-  const cudaError_t e = configure<kPaired>(&cfg, attr, clusters, !p.direct, stream);
+  const cudaError_t e = configure<kPaired>(&cfg, attr, clusters, true, stream);
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, prefix_kernel<kPaired>, p);
 }
 template <bool kPaired>

@@ -6,6 +6,25 @@
 
 namespace mla {
 
+// A launch as a programmatic dependent of the kernel before it in the stream: the
+// kernel begins while that one ends, and waits for its end before it touches memory
+// (a trip less between the kernels of a step: 1 to 3 us a call).
+template <class Params>
+cudaError_t launch_dependent(void (*kernel)(const Params), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, const Params& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 constexpr int kSpRows = 128;     // query rows of a CTA: 8 tokens x 16 heads
 constexpr int kSpTile = 128;     // keys of a tile
 
@@ -90,10 +109,11 @@ struct MeetParams {
 };
 
 // The kernels of a call are chained as programmatic dependents, in the order
-// gather, prefix, the decode kernel over the own ends, meet.  The prefix kernel
-// waits for the gathered rows only before it loads them; the decode kernel reads
-// nothing of the others and runs on the SMs that they leave; each ends after the
-// one before it, so that the last one waits for all.
+// gather, prefix, the decode kernel over the own ends, meet.  The first one waits
+// for the end of what the caller has launched before it touches memory.  The prefix
+// kernel waits for the gathered rows only before it loads them; the decode kernel
+// reads nothing of the others and runs on the SMs that they leave; each ends after
+// the one before it, so that the last one waits for all.
 cudaError_t launch_gather(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_prefix(const PrefixParams& p, bool paired, int clusters, cudaStream_t stream);
 // Clusters of the prefix kernel that the current device holds at a time (0: unknown).

@@ -530,6 +530,8 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
     if (mla::launch_prefix(p, plan->paired, plan->num_clusters, stream) != cudaSuccess)
       return MLA_ERR_CUDA;
     own.stage1.beside = 1;
+  } else {
+    own.stage1.beside = 2;
   }
   if (mla::decode_launch(plan->own, own, stream) != MLA_OK) return MLA_ERR_CUDA;
   mla::MeetParams m{};

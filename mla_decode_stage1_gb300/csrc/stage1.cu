@@ -1526,6 +1526,7 @@ __global__ void __launch_bounds__(Layout<QM>::kThreads, 1) mla_stage1_kernel(con
   const uint32_t ring = smem_u32(smem);
   Misc* ms = reinterpret_cast<Misc*>(smem + L::kMiscOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.beside == 2) asm volatile("griddepcontrol.wait;" ::: "memory");
   const CtaHead& head = p.heads[blockIdx.x];
   // bf16 / fp8: the CTA's item range and first item are loaded at once, so
   // that the loads overlap the set-up below (MXFP4 reads them after its
@@ -1656,7 +1657,7 @@ __global__ void __launch_bounds__(Layout<QM>::kThreads, 1) mla_stage1_kernel(con
   }
   // launched beside the kernel before it, on the SMs that one leaves: through
   // only when that one is (the last CTA, which takes no other's place, waits)
-  if (p.beside && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
+  if (p.beside == 1 && blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
