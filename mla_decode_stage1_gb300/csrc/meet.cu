@@ -11,7 +11,7 @@
 // Bound: latency, and memory for many rows.  The prefix kernel's partials stand as
 // [dim / 8][row][dim % 8], so that both kernels move whole lines: a CTA takes a
 // token's 16 rows and 128 of the 512 dims, a thread 8 dims of a row (16 rows of 32
-// bytes stand together), with up to 8 partials in flight.  Of tokens with many
+// bytes stand together), with up to 4 partials in flight.  Of tokens with many
 // partials (kSlices 4) a CTA takes 32 dims, and a thread every fourth partial.  64
 // tokens of 9 or 10 partials, 22 MB, take 9.4 us with all of it in DRAM; in a call it
 // comes from L2.
@@ -137,10 +137,11 @@ __global__ void __launch_bounds__(kThreads) meet_kernel(const MeetParams p) {
 
 cudaError_t launch_meet(const MeetParams& p, cudaStream_t stream) {
   // In slices: 2 tokens of 65 partials 21 us a call, 28 not; 4 tokens of 9 12.5 and 14.5,
-  // but 32 tokens of 9 22.6 and 20.6.
+  // but 32 tokens of 9 22.6 and 20.6.  (4 in flight where 8 took 73.5 instead of 71.8:
+  // 256 tokens of 4 or 5.)
   const bool wide = p.most > 16 || (p.most > 6 && p.tokens * 4 < 152);
   const dim3 grid(static_cast<unsigned>(p.tokens * (wide ? 16 : 4)));
-  auto* kernel = wide ? meet_kernel<8, 4> : p.most <= 4 ? meet_kernel<4, 1> : meet_kernel<8, 1>;
+  auto* kernel = wide ? meet_kernel<8, 4> : meet_kernel<4, 1>;
   return launch_dependent(kernel, grid, kThreads, 0, stream, p);
 }
 
