@@ -443,6 +443,108 @@ def test_shared_first_calls_of_plans_on_cold_memory(mla, per, q):
         assert torch.equal(o, outs[0]) and torch.equal(lse, lses[0])
 
 
+def test_shared_plans_on_several_streams_at_once(mla):
+    cases = [Case([9, 3], [77, 12], [(5 * i) % 40 for i in range(12)], 16, "bf16", "fp8"),
+             Case([40], [700], [3 * i for i in range(40)], 16, "fp8", "fp8"),
+             Case([2, 30], [90, 64], [100] * 32, 64), Case([4], [31], [64, 3, 5, 9], 8, "bf16", "mxfp4", q_len=2),
+             Case([17], [300], [30] * 17, 8, "fp8", "fp8", form="each"), Case([1], [2000], [1], 8)]
+    plans = [c.plan(mla) for c in cases]
+    wss = [torch.full((p.workspace_bytes,), 0xFF, dtype=torch.uint8, device="cuda") for p in plans]
+    first = [[x.clone() for x in c.run(mla, plan=p, ws=w)] for c, p, w in zip(cases, plans, wss)]
+    outs = [torch.empty_like(o) for o, _ in first]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i in range(40):
+        for k, (c, p, w, o) in enumerate(zip(cases, plans, wss, outs)):
+            mla.mla_shared_run(p, c.query["q"], c.pool["kv"], o, workspace=w, stream=streams[k % 3],
+                               q_scale=c.query.get("q_scale"), kv_scale=c.pool.get("kv_scale"),
+                               kv_e8m0=c.pool.get("kv_e8m0"), prefix_indices=c.prefix_ids,
+                               kv_indices=c.own_ids)
+        if i % 8 == 7:
+            torch.cuda.synchronize()
+            for o, f in zip(outs, first):
+                assert torch.equal(o, f[0])
+                o.zero_()
+            torch.cuda.synchronize()
+    for p, w in zip(plans, wss):
+        mla.mla_shared_check(p, w)
+
+
+def test_calls_wait_for_what_is_in_the_stream(mla):
+    """Inputs that a kernel, a copy or another stream writes just before the call, eagerly
+    and in a graph."""
+    g = gen(21)
+    lens, pages, page = i32([900, 64, 3000]), 256, 16
+    table = torch.randperm(pages * 3, generator=g, device="cuda")[: 3 * 200].int().reshape(3, 200)
+    kv = torch.randn(pages * 3 * page, 576, generator=g, device="cuda").bfloat16()
+    bounds = torch.zeros(pages * 3, 2, 576, dtype=torch.bfloat16, device="cuda")
+    q = torch.randn(3, 16, 576, generator=g, device="cuda").bfloat16()
+    scores = torch.randn(3, 200, generator=g, device="cuda")
+    ptr, last, idx = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (4, 3, 90))
+
+    def bounds_call():
+        mla.mla_page_bounds(kv, bounds, table, torch.zeros_like(lens), lens, page_size=page, kv_dtype="bf16")
+        return [bounds]
+
+    def scores_call():
+        mla.mla_page_scores(q, bounds, table, lens, scores, page_size=page)
+        return [scores]
+
+    def select_call():
+        mla.mla_page_select(scores, table, lens, page_size=page, top_pages=30, kv_indptr=ptr,
+                            kv_last_page_len=last, kv_indices=idx)
+        return [ptr, last, idx]
+
+    shared = []
+    for kd, size, form in (("bf16", 64, "once"), ("fp8", 16, "once"), ("bf16", 16, "each")):
+        c = Case([9], [40], [5] * 9, size, kv=kd, form=form)
+        plan = c.plan(mla)
+        ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        out = torch.empty(9, 16, 512, dtype=torch.bfloat16, device="cuda")
+
+        def call(c=c, plan=plan, ws=ws, out=out):
+            mla.mla_shared_run(plan, c.query["q"], c.pool["kv"], out, workspace=ws,
+                               kv_scale=c.pool.get("kv_scale"), prefix_indices=c.prefix_ids,
+                               kv_indices=c.own_ids)
+            return [out]
+        shared.append((c.query["q"], call))
+    side = torch.cuda.Stream()
+    for x, call in [(kv, bounds_call), (q, scores_call), (scores, select_call)] + shared:
+        keep = x.clone()
+        ref = [o.clone() for o in call()]
+
+        def produce(how):
+            if how == "copy":
+                x.copy_(keep)
+            elif how == "kernel":
+                torch.add(keep, 0, out=x)
+            else:
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    torch.add(keep, 0, out=x)
+                torch.cuda.current_stream().wait_stream(side)
+
+        for how in ("copy", "kernel", "stream"):
+            for _ in range(4):
+                x.zero_()
+                torch.cuda._sleep(100000)
+                produce(how)
+                got = [o.clone() for o in call()]
+                assert all(torch.equal(a, b) for a, b in zip(got, ref))
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                produce(how)
+                outs = call()
+            for _ in range(4):
+                x.zero_()
+                for o in outs:
+                    if o is not x:
+                        o.zero_()
+                graph.replay()
+                assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+
+
 def test_shared_captured_and_on_another_stream(mla):
     c = Case([9, 3], [77, 12], [(5 * i) % 40 for i in range(12)], 16, "bf16", "fp8")
     plan = c.plan(mla)
