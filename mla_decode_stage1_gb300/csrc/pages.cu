@@ -49,9 +49,9 @@ __device__ __forceinline__ void report(int32_t* err, int32_t bits) {
 // Bound: memory, one pass over the new rows; latency for a step of one token.  The
 // pages of all requests are one list (every CTA adds up the requests' counts, from
 // L2), handed out to the CTAs in turn, so that requests of any lengths are even work.
-// bf16 rows in pages of 32, 34 MB, take 11.4 us (3.1 TB/s; 12.0 with 4 rows of a thread
-// ahead instead of 8); a row for each of 256 requests 6.7 (2 of it the launch; 8.2 with
-// 8 e4m3 rows ahead).
+// bf16 rows in pages of 32, 34 MB, take 8.9 us (3.8 TB/s; 0.8 more with 4 rows of a thread
+// ahead instead of 8); a row for each of 256 requests 4.8 (1.5 more with 8 e4m3 rows
+// ahead).
 
 constexpr uint32_t kPosInf2 = 0x7f807f80u, kNegInf2 = 0xff80ff80u, kNan2 = 0x7fff7fffu;
 constexpr int kBoundThreads = 288;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kBoundThreads, KV == MLA_DTYPE_BF16 ? 4 : 3)
 // bytes (16 dims) of a page's bounds, a quad whole lines, kAhead steps of 64 dims
 // ahead of their use.  They are its share of four instructions: the order of the sum over d is
 // free, so lane c of a quad takes dims 16 c .. 16 c + 15 of 64, for the queries as
-// well.  32,768 pages, 78 MB with all else, take 16.3 us (4.8 TB/s, of 6.8 that a copy
+// well.  32,768 pages, 78 MB with all else, take 13.4 us (5.8 TB/s, of 6.8 that a copy
 // reaches).
 
 constexpr int kScoreWarps = 4;
@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
 // loads of them under way at once.
 //
 // Bound: latency, of loads that wait for one another above all: the scores (and for
-// short rows the pages) are read beside the lengths.  256 rows of 128 columns 5.6 us,
-// one of 16,384 15 us (2 us of either is the launch).
+// short rows the pages) are read beside the lengths.  256 rows of 128 columns 4.1 us,
+// one of 16,384 13 us.
 
 struct SelectParams {
   const float* scores;
