@@ -919,17 +919,19 @@ SELECT_CASES = [
     ([256, 255, 33, 32, 0], 1, 1, 31, 0, 1), ([257, 256, 40], 1, 1, 40, 1, 1),
     ([4096, 5], 1, 1, 700, 2, 2), ([4097, 9], 1, 2, 700, 2, 2), ([4100 + i for i in range(160)], 1, 1, 33, 1, 1),
     ([32768], 1, 1, 3000, 5, 5), ([32769, 100], 1, 1, 32768, 0, 1), ([70_001], 1, 1, 40_000, 1, 1),
-    ([70_000, 33_000], 1, 1, 300, 1, 1)]
+    ([70_000, 33_000], 1, 1, 300, 1, 1), ([9000, 4, 4104], 1, 1, 4099, 1, 1), ([400_123, 50], 1, 1, 5000, 2, 1)]
 
 
 @pytest.mark.parametrize("lens,page,q_len,top,first,last", SELECT_CASES)
-@pytest.mark.parametrize("kind", ["random", "ties", "special"])
+@pytest.mark.parametrize("kind", ["random", "ties", "special", "equal"])
 def test_page_select(mla, lens, page, q_len, top, first, last, kind):
     g = gen(12)
     rows, width = len(lens) * q_len, max(1, max(-(-n // page) for n in lens))
     x = torch.randn(rows, width + 5, generator=g, device="cuda")
     if kind == "ties":
         x = x.round()
+    if kind == "equal":
+        x = torch.full_like(x, -3.5)
     if kind == "special":
         pick = torch.randint(0, 12, x.shape, generator=g, device="cuda")
         for i, v in enumerate((NAN, INF, -INF, 0.0, -0.0, 1e-42, -1e-42)):
