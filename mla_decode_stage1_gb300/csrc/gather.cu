@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
       atomicOr(p.err, kErrBadPage);
       row = in < p.pool_rows ? in : 0;
     }
-    v[i] = ld_nc_na_v4(p.kv + row * kRowBytes + piece * 16);
-    if constexpr (KV == MLA_DTYPE_MXFP4) e[i] = ld_nc_u8_early(p.e8m0 + row * p.e8m0_stride + piece);
+    v[i] = ld_na_v4(p.kv + row * kRowBytes + piece * 16);
+    if constexpr (KV == MLA_DTYPE_MXFP4) e[i] = ld_u8(p.e8m0 + row * p.e8m0_stride + piece);
   }
   uint16_t* dst = p.rows + (static_cast<int64_t>(t.out_row) + row0) * kQkDim;
 #pragma unroll

@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(kBoundThreads, KV == MLA_DTYPE_BF16 ? 4 : 3)
         for (int u = 0; u < kAhead; ++u) {
           // (past the end: this thread's first row again)
           const int64_t row = row0 + (r + u * kRows < r1 ? r + u * kRows : r);
-          v[u] = ld_nc_na_v4(p.kv + (row * kPieces + piece) * 16);
+          v[u] = ld_na_v4(p.kv + (row * kPieces + piece) * 16);
           if constexpr (KV == MLA_DTYPE_MXFP4)
-            e[u] = ld_nc_u8_early(p.e8m0 + row * p.e8m0_stride + piece);
+            e[u] = ld_u8(p.e8m0 + row * p.e8m0_stride + piece);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {

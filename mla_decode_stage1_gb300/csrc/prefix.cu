@@ -478,8 +478,7 @@ __device__ __forceinline__ void fetch_query(const uint8_t* src, int live, int la
 #pragma unroll
   for (int i = 0; i < kLanes; ++i) {
     const int r = 32 / kLanes * i + lane / kLanes;
-    x[i] = r < live ? __ldg(reinterpret_cast<const uint4*>(src + 32 / kLanes * i * kQkDim * (kFp8 ? 1 : 2)))
-                    : make_uint4(0, 0, 0, 0);
+    x[i] = r < live ? ld_na_v4(src + 32 / kLanes * i * kQkDim * (kFp8 ? 1 : 2)) : make_uint4(0, 0, 0, 0);
   }
 }
 // The same as bf16 rows of 128 bytes at `dst` (row 0 of the warp, a multiple of 8

@@ -8,7 +8,9 @@ namespace mla {
 
 // A launch as a programmatic dependent of the kernel before it in the stream: the
 // kernel begins while that one ends, and waits for its end before it touches memory
-// (a trip less between the kernels of a step: 1 to 3 us a call).
+// (a trip less between the kernels of a step: 1 to 3 us a call).  What the kernel before
+// may have written is read with plain loads, not with those for memory that stays the
+// same while a kernel runs.
 template <class Params>
 cudaError_t launch_dependent(void (*kernel)(const Params), dim3 grid, int threads, size_t smem,
                              cudaStream_t stream, const Params& p) {
@@ -23,6 +25,20 @@ cudaError_t launch_dependent(void (*kernel)(const Params), dim3 grid, int thread
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+__device__ __forceinline__ uint4 ld_na_v4(const void* ptr) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(ptr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u8(const uint8_t* ptr) {
+  uint16_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=h"(v) : "l"(ptr) : "memory");
+  return v;
 }
 
 constexpr int kSpRows = 128;     // query rows of a CTA: 8 tokens x 16 heads
