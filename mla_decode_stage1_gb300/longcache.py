@@ -48,6 +48,8 @@ _declare(_lib)
 _shared_run, _page_bounds, _page_scores, _page_select = (
     _lib.mla_shared_run, _lib.mla_page_bounds, _lib.mla_page_scores, _lib.mla_page_select)
 
+# (a look-up in torch costs 50 ns, a call makes up to ten)
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 
 FORMS = {"auto": 0, "once": 1, "each": 2}
 
@@ -104,16 +106,16 @@ def mla_shared_plan(group_indptr, prefix_indptr, kv_indptr, kv_last_page_len=Non
     return SharedPlan(h, q_dtype, kv_dtype, int(pre[-1]), int(kvp[-1]))
 
 
-_Q_DTYPES = {"bf16": torch.bfloat16, "fp8": torch.uint8}
+_Q_DTYPES = {"bf16": _BF16, "fp8": _U8}
 
 
 def _table(name, t, entries):
     """Pointer of a page table with room for the plan's entries, or None."""
     if t is None:
         return None
-    if not (t.is_cuda and t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous()
+    if not (t.is_cuda and t.dtype is _I32 and t.dim() == 1 and t.is_contiguous()
             and t.shape[0] >= entries):
-        _vec(name, t, torch.int32)
+        _vec(name, t, _I32)
         raise ValueError(f"{name} must hold the plan's {entries} pages")
     return t.data_ptr()
 
@@ -138,16 +140,16 @@ def mla_shared_run(plan: SharedPlan, q, kv, out, *, workspace, prefix_indices=No
     if not _query_ok(q, _Q_DTYPES[plan.q_dtype], T):
         raise ValueError(f"q must be a contiguous CUDA tensor [{T}, {HEADS}, {QK_DIM}] of "
                          f"{_Q_DTYPES[plan.q_dtype]}")
-    if not (out.is_cuda and out.dtype is torch.bfloat16 and out.is_contiguous()
+    if not (out.is_cuda and out.dtype is _BF16 and out.is_contiguous()
             and out.numel() == T * (HEADS * V_DIM)):
-        _dense("out", out, torch.bfloat16, (T, HEADS, V_DIM))
-    if lse is not None and not (lse.is_cuda and lse.dtype is torch.float32 and lse.is_contiguous()
+        _dense("out", out, _BF16, (T, HEADS, V_DIM))
+    if lse is not None and not (lse.is_cuda and lse.dtype is _F32 and lse.is_contiguous()
                                 and lse.numel() == T * HEADS):
-        _dense("lse", lse, torch.float32, (T, HEADS))
+        _dense("lse", lse, _F32, (T, HEADS))
     qs = None
     if plan.q_dtype == "fp8":
         _need(q_scale is not None, "fp8 q needs q_scale")
-        _word("q_scale", q_scale, torch.float32)
+        _word("q_scale", q_scale, _F32)
         qs = q_scale.data_ptr()
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
@@ -177,7 +179,7 @@ class MlaShared:
         self.plan = mla_shared_plan(group_indptr, prefix_indptr, kv_indptr, kv_last_page_len,
                                     page_size=page_size, q_dtype=q_dtype, kv_dtype=kv_dtype,
                                     q_len=q_len, form=form)
-        self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8, device=device)
+        self.workspace = torch.empty(self.plan.workspace_bytes, dtype=_U8, device=device)
 
     def __call__(self, q, kv, out, **kw):
         mla_shared_run(self.plan, q, kv, out, workspace=self.workspace, **kw)
@@ -187,7 +189,7 @@ class MlaShared:
 def _blocks(block_table, bs):
     """(pointer, row stride, columns) of a block table with dense rows."""
     size, strides = block_table.shape, block_table.stride()
-    if not (block_table.is_cuda and block_table.dtype is torch.int32 and len(size) == 2
+    if not (block_table.is_cuda and block_table.dtype is _I32 and len(size) == 2
             and size[0] == bs and (strides[1] == 1 or size[1] <= 1)):
         raise ValueError(f"block_table must be a CUDA tensor [{bs}, columns] of torch.int32 with "
                          "dense rows")
@@ -196,15 +198,15 @@ def _blocks(block_table, bs):
 
 def _bounds(bounds):
     size = bounds.shape
-    if not (bounds.is_cuda and bounds.dtype is torch.bfloat16 and len(size) == 3 and size[1] == 2
+    if not (bounds.is_cuda and bounds.dtype is _BF16 and len(size) == 3 and size[1] == 2
             and size[2] == QK_DIM and bounds.is_contiguous()):
         raise ValueError(f"bounds must be a contiguous CUDA tensor [pages, 2, {QK_DIM}] of bfloat16")
     return size[0]
 
 
 def _lengths(name, t):
-    if not (t.is_cuda and t.dtype is torch.int32 and t.dim() == 1 and t.is_contiguous()):
-        _vec(name, t, torch.int32)
+    if not (t.is_cuda and t.dtype is _I32 and t.dim() == 1 and t.is_contiguous()):
+        _vec(name, t, _I32)
     return t.shape[0]
 
 
@@ -223,7 +225,7 @@ def mla_page_bounds(kv, bounds, block_table, old_lens, new_lens=None, *, page_si
         raise ValueError(f"new_lens must have {bs} elements")
     table, stride, columns = _blocks(block_table, bs)
     pages = _bounds(bounds)
-    _word("err", err, torch.int32)
+    _word("err", err, _I32)
     width, dtype = _POOLS[kv_dtype]
     size = kv.shape
     if not (kv.is_cuda and kv.dtype is dtype and len(size) == 2 and size[1] == width
@@ -242,7 +244,7 @@ def mla_page_bounds(kv, bounds, block_table, old_lens, new_lens=None, *, page_si
 def _scores(scores, rows, columns):
     """Row stride of scores [rows, at least columns] with dense rows."""
     size, strides = scores.shape, scores.stride()
-    if not (scores.is_cuda and scores.dtype is torch.float32 and len(size) == 2 and size[0] == rows
+    if not (scores.is_cuda and scores.dtype is _F32 and len(size) == 2 and size[0] == rows
             and size[1] >= columns and (strides[1] == 1 or size[1] <= 1)):
         raise ValueError(f"scores must be a CUDA tensor [{rows}, >= {columns}] of float32 with dense "
                          "rows")
@@ -261,12 +263,12 @@ def mla_page_scores(q, bounds, block_table, lens, scores, *, page_size: int, q_l
     table, stride, columns = _blocks(block_table, bs)
     pages = _bounds(bounds)
     fp8 = q_scale is not None
-    if not _query_ok(q, torch.uint8 if fp8 else torch.bfloat16, bs * q_len):
+    if not _query_ok(q, _U8 if fp8 else _BF16, bs * q_len):
         raise ValueError(f"q must be a contiguous CUDA tensor [{bs * q_len}, {HEADS}, {QK_DIM}] of "
                          f"{'uint8' if fp8 else 'bfloat16'}")
-    _word("q_scale", q_scale, torch.float32)
-    _word("kv_scale", kv_scale, torch.float32)
-    _word("err", err, torch.int32)
+    _word("q_scale", q_scale, _F32)
+    _word("kv_scale", kv_scale, _F32)
+    _word("err", err, _I32)
     status = _page_scores(q.data_ptr(), 1 if fp8 else 0, _ptr(q_scale), _ptr(kv_scale),
                           bounds.data_ptr(), pages, lens.data_ptr(), bs, q_len, page_size, table,
                           stride, columns, scores.data_ptr(), _scores(scores, bs * q_len, columns),
@@ -286,21 +288,20 @@ def mla_page_select(scores, block_table, lens, *, page_size: int, top_pages: int
     if _several_devices:
         _on_current_device(stream, scores, block_table, lens, kv_indptr, kv_last_page_len, kv_indices,
                            columns, err)
-    i32 = torch.int32
     bs = _lengths("lens", lens)
     rows = bs * q_len
     table, stride, cols = _blocks(block_table, bs)
-    if not (kv_indptr.is_cuda and kv_indptr.dtype is i32 and kv_indptr.is_contiguous()
+    if not (kv_indptr.is_cuda and kv_indptr.dtype is _I32 and kv_indptr.is_contiguous()
             and kv_indptr.shape == (rows + 1,) and kv_last_page_len.is_cuda
-            and kv_last_page_len.dtype is i32 and kv_last_page_len.is_contiguous()
-            and kv_last_page_len.shape == (rows,) and kv_indices.is_cuda and kv_indices.dtype is i32
+            and kv_last_page_len.dtype is _I32 and kv_last_page_len.is_contiguous()
+            and kv_last_page_len.shape == (rows,) and kv_indices.is_cuda and kv_indices.dtype is _I32
             and kv_indices.is_contiguous() and kv_indices.dim() == 1):
-        _vec("kv_indptr", kv_indptr, i32, rows + 1)
-        _vec("kv_last_page_len", kv_last_page_len, i32, rows)
-        _vec("kv_indices", kv_indices, i32)
+        _vec("kv_indptr", kv_indptr, _I32, rows + 1)
+        _vec("kv_last_page_len", kv_last_page_len, _I32, rows)
+        _vec("kv_indices", kv_indices, _I32)
     if columns is not None:
-        _dense("columns", columns, i32, (rows, top_pages))
-    _word("err", err, i32)
+        _dense("columns", columns, _I32, (rows, top_pages))
+    _word("err", err, _I32)
     status = _page_select(scores.data_ptr(), _scores(scores, rows, cols), lens.data_ptr(), bs, q_len,
                           page_size, table, stride, cols, top_pages, first_pages, last_pages,
                           kv_indptr.data_ptr(), kv_last_page_len.data_ptr(), kv_indices.data_ptr(),
