@@ -29,7 +29,8 @@
 // the queries on their way (as fast as keys and queries together come in), 2 with the
 // first scores, 34 with the other tiles, 3.5 with the last products and 4 with the
 // output, 256 KB a CTA at 32 bytes a cycle.  Copies of keys to both CTAs at once
-// (multicast) changed nothing, nor did queries that were asked for earlier.
+// (multicast) changed nothing, nor did queries that were asked for earlier or taken up
+// in thirds.
 //
 // Probabilities are rounded to bf16, the type of the values that they meet; the
 // sums that divide the output are of the unrounded ones.  Scores, sums, maxima
