@@ -685,7 +685,7 @@ typedef struct {
   int32_t batch_size;
   int32_t num_groups;
   int32_t q_len;
-  int32_t num_clusters;      /* clusters of CTAs that work on the prefixes (0: MLA_SHARED_EACH) */
+  int32_t num_clusters;      /* clusters of CTAs that work on the prefixes (0: none, MLA_SHARED_EACH) */
   int32_t block_rows;        /* query rows of such a cluster: 128 or 256 */
   int32_t num_items;         /* (up to block_rows query rows, range of their prefix) */
   int64_t prefix_tokens;     /* of groups with requests, once each */
