@@ -93,22 +93,23 @@ __device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, in
 
 // Global load issued exactly where it is written (an asm volatile cannot be
 // re-materialised at its use, which would put the full memory latency back
-// on the consumer's path).
-__device__ __forceinline__ int32_t ld_nc_early(const int32_t* ptr) {
+// on the consumer's path).  Coherent, as the other loads here: a kernel that is
+// launched while the one before it ends may read what that one writes.
+__device__ __forceinline__ int32_t ld_early(const int32_t* ptr) {
   int32_t v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(ptr));
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(ptr));
   return v;
 }
 
-__device__ __forceinline__ uint64_t ld_nc_early_u64(const uint64_t* ptr) {
+__device__ __forceinline__ uint64_t ld_early_u64(const uint64_t* ptr) {
   uint64_t v;
-  asm volatile("ld.global.nc.b64 %0, [%1];" : "=l"(v) : "l"(ptr));
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(ptr));
   return v;
 }
 // 16 bytes, issued where it is written, not kept in L1 (read once).
-__device__ __forceinline__ uint4 ld_nc_na_v4(const void* ptr) {
+__device__ __forceinline__ uint4 ld_early_na_v4(const void* ptr) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(ptr));
   return v;
@@ -118,9 +119,9 @@ __device__ __forceinline__ uint4 ld_nc_na_v4(const void* ptr) {
 __device__ __forceinline__ void prefetch_l2_last(const void* ptr) {
   asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(ptr));
 }
-__device__ __forceinline__ uint32_t ld_nc_u8_early(const uint8_t* ptr) {
+__device__ __forceinline__ uint32_t ld_early_u8(const uint8_t* ptr) {
   uint16_t v;
-  asm volatile("ld.global.nc.u8 %0, [%1];" : "=h"(v) : "l"(ptr));
+  asm volatile("ld.global.u8 %0, [%1];" : "=h"(v) : "l"(ptr));
   return v;
 }
 

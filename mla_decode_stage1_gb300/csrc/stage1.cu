@@ -211,7 +211,7 @@ struct TileCursor {
 __device__ __forceinline__ int page_at(const Stage1Params& p, int page_base, int at) {
   const int32_t* table = page_base < 0 ? p.prefix_indices : p.kv_indices;
   const int i = (page_base < 0 ? ~page_base : page_base) + at;
-  return table == nullptr ? i : ld_nc_early(table + i);
+  return table == nullptr ? i : ld_early(table + i);
 }
 // The same without any page table.
 __device__ __forceinline__ int first_page(int page_base) { return page_base < 0 ? ~page_base : page_base; }
@@ -665,7 +665,7 @@ __device__ __forceinline__ void scale_load(const Stage1Params& p, int64_t row, i
   }
   const uint8_t* src = p.kv_e8m0 + row * p.sc_stride + hb;
 #pragma unroll
-  for (int i = 0; i < 9; ++i) e[i] = ld_nc_u8_early(src + 2 * i);
+  for (int i = 0; i < 9; ++i) e[i] = ld_early_u8(src + 2 * i);
 }
 
 // ----------------------------------------------------- q staging helpers
@@ -762,7 +762,7 @@ __device__ __forceinline__ void q_convert(const Stage1Params& p, Misc* ms, const
     q_term_scale(p, amax, s_hi, inv_hi);
     for (int v = i; v < kV; v += n)
       q_split_store(src[v], v, s_hi, inv_hi, dst, L::kQAtomBytes, L::kRows);
-    const float kvs = (QM == kQBf16KvMx) ? 1.0f : __ldg(p.kv_scale);
+    const float kvs = (QM == kQBf16KvMx) ? 1.0f : *p.kv_scale;
     c_hi = s_hi * kvs * kSmScale * kLog2e;
     c_lo = c_hi * (1.0f / 16.0f);
   } else if constexpr (QM == kQFp8KvFp8 || QM == kQFp8KvFp8x2) {
@@ -771,7 +771,7 @@ __device__ __forceinline__ void q_convert(const Stage1Params& p, Misc* ms, const
       const int h = v / 36, d0 = (v % 36) * 16;
       *reinterpret_cast<uint4*>(dst + (d0 >> 7) * L::kQAtomBytes + sw128(h, d0 & 127)) = src[v];
     }
-    c_hi = __ldg(p.q_scale) * __ldg(p.kv_scale) * kSmScale * kLog2e;
+    c_hi = *p.q_scale * *p.kv_scale * kSmScale * kLog2e;
   } else {
     // bf16 operand for kind::f16; fp8 q is decoded exactly to bf16 first.
     for (int v = i; v < kHeads * 72; v += n) {       // 72 vectors of 8 values per head
@@ -796,7 +796,7 @@ __device__ __forceinline__ void q_convert(const Stage1Params& p, Misc* ms, const
       const int atom = d0 >> 6, xb = (d0 & 63) * 2;
       *reinterpret_cast<uint4*>(dst + atom * L::kQAtomBytes + sw128(h, xb)) = x;
     }
-    c_hi = (QM == kQFp8KvBf16 ? __ldg(p.q_scale) : 1.0f) * kSmScale * kLog2e;
+    c_hi = (QM == kQFp8KvBf16 ? *p.q_scale : 1.0f) * kSmScale * kLog2e;
   }
 }
 
@@ -820,7 +820,7 @@ __device__ __forceinline__ void q_convert_mx(const Stage1Params& p, Misc* ms, in
   for (int u = 0; u < kPer; ++u) {
     const int v = i + kN * u;
     if (v >= kV) break;
-    const uint4 x = __ldg(src + v);
+    const uint4 x = src[v];
     const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -841,7 +841,7 @@ __device__ __forceinline__ void q_convert_mx(const Stage1Params& p, Misc* ms, in
 #pragma unroll 1
   for (int u = 0; u < kPer; ++u) {
     const int v = i + kN * u;
-    if (v < kV) q_split_store(__ldg(src + v), v, s_hi, inv_hi, dst, L::kQAtomBytes, L::kRows);
+    if (v < kV) q_split_store(src[v], v, s_hi, inv_hi, dst, L::kQAtomBytes, L::kRows);
   }
   c_hi = s_hi * kSmScale * kLog2e;
   c_lo = c_hi * (1.0f / 16.0f);
@@ -901,7 +901,7 @@ __device__ __forceinline__ bool half_of_tile(bool ok, bool live, bool fast, uint
       o0 = make_uint4(e0.x, e0.y, e1.x, e1.y);
       o1 = make_uint4(e2.x, e2.y, e3.x, e3.y);
     }
-    if (next != nullptr) x[j] = ld_nc_na_v4(next + 32 * j);
+    if (next != nullptr) x[j] = ld_early_na_v4(next + 32 * j);
     *reinterpret_cast<uint4*>(dst + j * 512 + pc0) = o0;
     *reinterpret_cast<uint4*>(dst + j * 512 + pc1) = o1;
   }
@@ -960,7 +960,7 @@ __device__ void run_dequant_mx(const Stage1Params& p, Misc* ms, uint8_t* ring_ge
     if (r0 >= 0) {
       const uint8_t* src = p.kv + r0 * L::kRawRowBytes + 16 * h;
 #pragma unroll
-      for (int j = 0; j < 9; ++j) x[j] = ld_nc_na_v4(src + 32 * j);
+      for (int j = 0; j < 9; ++j) x[j] = ld_early_na_v4(src + 32 * j);
     }
     scale_load(p, r0, h, ec);
   }
@@ -1370,7 +1370,7 @@ __device__ void run_softmax(const Stage1Params& p, Misc* ms, uint8_t* ring_gen, 
     reduce_heads<false, kH>(l, lt, ms->red[g & 1u], h0, qw, lane, bar);
     if (*abort) return;
     // fp8 V entered the UMMAs as raw e4m3: its per-tensor scale is applied here.
-    const float vscale = (L::kKv8 && !L::kMx) ? __ldg(p.kv_scale) : 1.0f;
+    const float vscale = (L::kKv8 && !L::kMx) ? *p.kv_scale : 1.0f;
     float inv[kH];
 #pragma unroll
     for (int h = 0; h < kH; ++h) inv[h] = vscale / lt[h];
@@ -1545,8 +1545,8 @@ __global__ void __launch_bounds__(Layout<QM>::kThreads, 1) mla_stage1_kernel(con
     // this address since) nothing is read from the table and nothing is
     // written; mla_decode_check reports it.  The two stamps are loaded first
     // and compared after the barrier set-up, which hides their latency.
-    const uint64_t hs = ld_nc_early_u64(&reinterpret_cast<const WsHeader*>(p.err)->stamp);
-    const uint64_t cs = ld_nc_early_u64(&head.stamp);
+    const uint64_t hs = ld_early_u64(&reinterpret_cast<const WsHeader*>(p.err)->stamp);
+    const uint64_t cs = ld_early_u64(&head.stamp);
     for (int i = 0; i < L::kNumTiles; ++i) {
       mbar_init(smem_u32(&ms->full[i]), p.gather ? 32 : 1);   // gather: one per producer lane
       mbar_init(smem_u32(&ms->empty[i]), L::kPvIssuers);

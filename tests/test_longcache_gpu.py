@@ -545,6 +545,54 @@ def test_calls_wait_for_what_is_in_the_stream(mla):
                 assert all(torch.equal(a, b) for a, b in zip(outs, ref))
 
 
+@pytest.mark.parametrize("q,kv,page,q_len,form", [
+    ("bf16", "bf16", 16, 1, "each"), ("fp8", "fp8", 8, 1, "each"), ("bf16", "fp8", 12, 1, "each"),
+    ("bf16", "fp8", 16, 2, "each"), ("fp8", "fp8", 5, 2, "each"), ("fp8", "bf16", 8, 1, "each"),
+    ("bf16", "mxfp4", 16, 1, "each"), ("bf16", "mxfp4", 7, 2, "each"),
+    ("bf16", "bf16", 64, 1, "once"), ("fp8", "fp8", 12, 1, "once"), ("bf16", "mxfp4", 16, 1, "once")])
+def test_shared_reads_what_was_written_just_before(mla, q, kv, page, q_len, form):
+    """Every input in turn, pages and scales among them, is produced by the kernel that the
+    call follows, eagerly and in a graph."""
+    c = Case([5, 2], [33, 40], [5, 30, 2, 9, 70, 3, 1], page, q, kv, q_len=q_len, form=form, seed=31)
+    plan = c.plan(mla)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    inputs = dict(c.query, **c.pool, prefix=c.prefix_ids, own=c.own_ids)
+    out = torch.empty(c.bs * q_len, 16, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(c.bs * q_len, 16, device="cuda")
+
+    def call():
+        mla.mla_shared_run(plan, inputs["q"], inputs["kv"], out, workspace=ws, lse=lse,
+                           q_scale=inputs.get("q_scale"), kv_scale=inputs.get("kv_scale"),
+                           kv_e8m0=inputs.get("kv_e8m0"), prefix_indices=inputs["prefix"],
+                           kv_indices=inputs["own"])
+    call()
+    mla.mla_shared_check(plan, ws)
+    ref, ref_lse = out.clone(), lse.clone()
+    for name, x in inputs.items():
+        keep = x.clone()
+        # (other pages of the pool, another scale, zeros)
+        other = x.flip(0) if name in ("prefix", "own") else 3 * x if name.endswith("_scale") else 0 * x
+        x.copy_(other)
+        call()
+        assert not torch.equal(lse, ref_lse) or not torch.equal(out, ref)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            torch.mul(keep, 1, out=x)
+            call()
+        for step in range(4):
+            x.copy_(other)
+            out.zero_()
+            if step % 2:
+                graph.replay()
+            else:
+                torch.cuda._sleep(100000)
+                torch.mul(keep, 1, out=x)
+                call()
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    mla.mla_shared_check(plan, ws)
+
+
 def test_shared_captured_and_on_another_stream(mla):
     c = Case([9, 3], [77, 12], [(5 * i) % 40 for i in range(12)], 16, "bf16", "fp8")
     plan = c.plan(mla)
