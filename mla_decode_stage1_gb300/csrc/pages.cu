@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
   for (int i = 0; i < kTiles; ++i)
     entry[i] = p.table[b * p.table_stride + min(page0 + 8 * i + g, static_cast<int64_t>(p.columns - 1))];
   int64_t n = p.lens[b];
-  const bool first_cta = chunk == 0 && t == 0 && threadIdx.x == 0;
+  // (later query tokens see more)
+  const bool first_cta = chunk == 0 && threadIdx.x == 0;
   if (n < 0) {
     if (first_cta) report(p.err, kErrBadLength);
     n = 0;

@@ -923,6 +923,28 @@ def test_page_scores_report(mla):
     mla.mla_error_check(err)
 
 
+@pytest.mark.parametrize("lens,q_len,page,columns", [
+    # the first query token's pages fit, the last one's do not
+    ([6401], 4, 64, 100), ([16, 17, 3], 2, 8, 2), ([8 * 64 + 3], 64, 8, 64), ([9, 0], 2, 1, 8)])
+def test_page_scores_report_pages_that_only_later_query_tokens_lack(mla, lens, q_len, page, columns):
+    g = gen(32)
+    b = torch.randn(4, 2, 576, generator=g, device="cuda").sort(1)[0].bfloat16()
+    q = torch.randn(len(lens) * q_len, 16, 576, generator=g, device="cuda").bfloat16()
+    table = torch.randint(0, 4, (len(lens), columns), generator=g, device="cuda").int()
+    s, err = torch.empty(len(lens) * q_len, columns, device="cuda"), word()
+    mla.mla_page_scores(q, b, table, i32(lens), s, page_size=page, q_len=q_len, err=err)
+    with pytest.raises(mla.MlaError) as e:
+        mla.mla_error_check(err)
+    assert e.value.status == 6
+    for r, x in enumerate(s):
+        n = min(columns, -(-max(0, lens[r // q_len] - q_len + 1 + r % q_len) // page))
+        assert torch.isfinite(x[:n]).all() and torch.isneginf(x[n:]).all()
+    # one token less, and everything fits
+    mla.mla_page_scores(q, b, table, i32([min(n, page * columns) for n in lens]), s, page_size=page,
+                        q_len=q_len, err=err)
+    mla.mla_error_check(err)
+
+
 # --------------------------------------------------------------------- select
 def plain_select(scores, table, lens, page, q_len, top, first, last):
     ptr, last_len, idx, cols = [0], [], [], []
