@@ -483,9 +483,11 @@ __device__ __forceinline__ void fetch_query(const uint8_t* src, int live, int la
   }
 }
 // The same as bf16 rows of 128 bytes at `dst` (row 0 of the warp, a multiple of 8
-// rows behind a 1,024-byte boundary), in the 128-byte swizzle.
+// rows behind a 1,024-byte boundary), in the 128-byte swizzle; with `sign` 0x80008000
+// all of it negated.
 template <bool kFp8>
-__device__ __forceinline__ void stage_query(const uint4 (&x)[kFp8 ? 4 : 8], uint32_t dst, int lane) {
+__device__ __forceinline__ void stage_query(const uint4 (&x)[kFp8 ? 4 : 8], uint32_t dst, uint32_t sign,
+                                            int lane) {
   constexpr int kLanes = kFp8 ? 4 : 8;
 #pragma unroll
   for (int i = 0; i < kLanes; ++i) {
@@ -499,12 +501,13 @@ __device__ __forceinline__ void stage_query(const uint4 (&x)[kFp8 ? 4 : 8], uint
       for (int k = 0; k < 8; ++k) {
         const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1))));
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        v[k] = bf16x2_of(f.x, f.y);
+        v[k] = bf16x2_of(f.x, f.y) ^ sign;
       }
       st_shared_16(at + ((piece ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
       st_shared_16(at + (((piece + 1) ^ (r & 7)) << 4), v[4], v[5], v[6], v[7]);
     } else {
-      st_shared_16(at + (((lane & 7) ^ (r & 7)) << 4), x[i].x, x[i].y, x[i].z, x[i].w);
+      st_shared_16(at + (((lane & 7) ^ (r & 7)) << 4), x[i].x ^ sign, x[i].y ^ sign, x[i].z ^ sign,
+                   x[i].w ^ sign);
     }
   }
 }
@@ -522,7 +525,8 @@ __device__ __forceinline__ void own_query(uint32_t src, int lane, uint32_t* v) {
 // by way of 4 KB of shared memory; with h = 0 the rotated ones to shared memory.
 template <bool kFp8>
 __device__ __forceinline__ void load_queries(const void* q, int64_t row0, int live, int h,
-                                             uint32_t via, uint32_t tmem, uint32_t rotated, int lane) {
+                                             uint32_t sign, uint32_t via, uint32_t tmem,
+                                             uint32_t rotated, int lane) {
   constexpr int kRowBytes = kQkDim * (kFp8 ? 1 : 2), kChunkBytes = kRowBytes / kChunks;
   constexpr int kLanes = kFp8 ? 4 : 8;
   const uint8_t* rows = static_cast<const uint8_t*>(q) + row0 * kRowBytes;
@@ -542,14 +546,14 @@ __device__ __forceinline__ void load_queries(const void* q, int64_t row0, int li
     uint32_t v[32];
     if (c < 3 || h == 0)
       fetch_query<kFp8>(src + (c < 3 ? c + 1 : 8) * kChunkBytes, live, lane, x[(c + 1) & 1]);
-    stage_query<kFp8>(x[c & 1], via, lane);
+    stage_query<kFp8>(x[c & 1], via, sign, lane);
     __syncwarp();
     own_query(via, lane, v);
     __syncwarp();
     tmem_st32(tmem + 32 * c, v);
   }
   if (h == 0) {
-    stage_query<kFp8>(x[0], rotated, lane);
+    stage_query<kFp8>(x[0], rotated, sign, lane);
     fence_proxy_async_smem();
   }
   __syncwarp();
@@ -565,7 +569,13 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
   const uint32_t stage0 = smem + kStageAt + h * kHalfBytes + row * 128, swizzle = row & 7;
   const float qs = p.q_scale != nullptr ? *p.q_scale : 1.0f;
   const float ks = p.kv_scale != nullptr ? *p.kv_scale : 1.0f;
-  const float scale = qs * ks * (kLog2e / 24.0f);
+  // A row's maximum is that of its products, so their factor has to be positive: a
+  // negative one turns the queries around, and instead of 0 it is the smallest number,
+  // with which finite products still come to 0 (2^-21 at most) but -inf, where there is
+  // no key, does not become NaN.
+  const float factor = qs * ks * (kLog2e / 24.0f);
+  const uint32_t sign = factor < 0.0f ? 0x80008000u : 0u;
+  const float scale = factor == 0.0f ? __uint_as_float(1u) : fabsf(factor);
   const uint64_t scale2 = pack_f32x2(scale, scale);
   uint32_t tile = 0;
   Turn<Ring<kPaired>::kPTiles> turn;
@@ -590,9 +600,9 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
         return;
       const uint32_t rotated = smem + Ring<kPaired>::kQrAt + warp * 4096;
       if (p.q_fp8)
-        load_queries<true>(p.q, q_row0, live, h, via, tq + 128 * h, rotated, lane);
+        load_queries<true>(p.q, q_row0, live, h, sign, via, tq + 128 * h, rotated, lane);
       else
-        load_queries<false>(p.q, q_row0, live, h, via, tq + 128 * h, rotated, lane);
+        load_queries<false>(p.q, q_row0, live, h, sign, via, tq + 128 * h, rotated, lane);
       tc_fence_before();
       arrive_at_first<kPaired, true>(at, &ms->q_ready, lane);
     }

@@ -308,6 +308,27 @@ def test_shared_equal_and_extreme_scores(mla):
     check_shared(mla, c)
 
 
+@pytest.mark.parametrize("form", ["once", "each"])
+@pytest.mark.parametrize("q,kv,q_scale,kv_scale,std", [
+    ("bf16", "fp8", 1.0, 0.0, 1.5), ("fp8", "fp8", 0.0, 0.0131, 1.5), ("fp8", "bf16", 0.0, 1.0, 1.5),
+    ("bf16", "fp8", 1.0, -0.0131, 1.5), ("bf16", "fp8", 1.0, -0.0131, 60.0),
+    ("fp8", "fp8", -0.8, 0.0131, 1.5), ("fp8", "fp8", -0.8, -0.0131, 1.5), ("fp8", "bf16", -0.8, 1.0, 1.5)])
+def test_shared_scales_of_zero_and_below(mla, q, kv, q_scale, kv_scale, std, form):
+    """Scales are factors like any other: 0 (that of a pool of zeros) makes all scores
+    equal, a negative one turns their order around."""
+    for per, prefix, page in (([3], [31], 8), ([20], [64], 16), ([2, 9], [0, 3], 64)):
+        c = Case(per, prefix, [(7 * i) % 40 for i in range(sum(per))], page, q, kv, std=std, form=form)
+        if q == "fp8":
+            c.query["q_scale"].fill_(q_scale)
+            c.qv = c.query["q"].view(torch.float8_e4m3fn).double() * c.query["q_scale"].double()
+        if kv == "fp8":
+            # (the reference's bounds take a positive scale: its sign with the values)
+            c.pool["kv_scale"].fill_(kv_scale)
+            c.scale = abs(float(c.pool["kv_scale"].double()))
+            c.stored = c.stored * math.copysign(1.0, kv_scale)
+        check_shared(mla, c)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8", "mxfp4"])
 def test_shared_values_that_are_not_finite(mla, kv):
     """A bad row reaches exactly the requests that attend to it."""
