@@ -255,17 +255,18 @@ def mla_page_scores(q, bounds, block_table, lens, scores, *, page_size: int, q_l
                     q_scale=None, kv_scale=None, err=None, stream=None) -> None:
     """Upper bounds of the decode call's scores, page by page: scores fp32
     [requests * q_len, columns], -inf where a query token sees no token of a
-    page.  q as mla_decode_run takes it (uint8: e4m3 bytes, with q_scale), lens
-    int32 [requests] with the new tokens."""
+    page.  q as mla_decode_run takes it (uint8: e4m3 bytes, with q_scale, which a
+    bf16 q ignores), lens int32 [requests] with the new tokens."""
     if _several_devices:
         _on_current_device(stream, q, bounds, block_table, lens, scores, q_scale, kv_scale, err)
     bs = _lengths("lens", lens)
     table, stride, columns = _blocks(block_table, bs)
     pages = _bounds(bounds)
-    fp8 = q_scale is not None
+    fp8 = q.dtype is _U8
     if not _query_ok(q, _U8 if fp8 else _BF16, bs * q_len):
         raise ValueError(f"q must be a contiguous CUDA tensor [{bs * q_len}, {HEADS}, {QK_DIM}] of "
-                         f"{'uint8' if fp8 else 'bfloat16'}")
+                         "bfloat16 or uint8")
+    _need(q_scale is not None or not fp8, "fp8 q needs q_scale")
     _word("q_scale", q_scale, _F32)
     _word("kv_scale", kv_scale, _F32)
     _word("err", err, _I32)

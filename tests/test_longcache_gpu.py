@@ -966,6 +966,25 @@ def test_page_scores_report_pages_that_only_later_query_tokens_lack(mla, lens, q
     mla.mla_error_check(err)
 
 
+def test_page_scores_take_the_type_of_the_query(mla):
+    """A bf16 query's scale is ignored, as by the decode call; e4m3 bytes need one."""
+    g = gen(33)
+    b = torch.randn(4, 2, 576, generator=g, device="cuda").sort(1)[0].bfloat16()
+    q = torch.randn(1, 16, 576, generator=g, device="cuda").bfloat16()
+    table, n = i32([[2, 1, 3]]), i32([20])
+    s, t, scale = (torch.empty(1, 3, device="cuda"), torch.empty(1, 3, device="cuda"),
+                   torch.full((1,), 0.25, device="cuda"))
+    mla.mla_page_scores(q, b, table, n, s, page_size=8)
+    mla.mla_page_scores(q, b, table, n, t, page_size=8, q_scale=scale)
+    assert torch.equal(s, t)
+    e = q.to(torch.float8_e4m3fn)
+    mla.mla_page_scores(e.bfloat16(), b, table, n, s, page_size=8)
+    mla.mla_page_scores(e.view(torch.uint8), b, table, n, t, page_size=8, q_scale=scale)
+    assert torch.equal(0.25 * s, t)
+    with pytest.raises(ValueError):
+        mla.mla_page_scores(e.view(torch.uint8), b, table, n, t, page_size=8)
+
+
 # --------------------------------------------------------------------- select
 def plain_select(scores, table, lens, page, q_len, top, first, last):
     ptr, last_len, idx, cols = [0], [], [], []
