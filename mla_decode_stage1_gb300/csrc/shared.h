@@ -116,6 +116,7 @@ struct MeetParams {
   int32_t own_rows;
   int32_t blocks;              // of 128 rows in a slot of the prefix kernel
   int32_t most;                // partial results of a token, at most
+  int32_t alone;               // 1: the only kernel of its call (nothing is cached)
   const float* prefix_o;       // [slots][blocks][64][128][8]
   const float* prefix_lse;
   uint16_t* out;

@@ -542,6 +542,7 @@ mla_status mla_shared_run(mla_shared* plan, const void* q, const float* q_scale,
   m.own_rows = plan->own->rows;
   m.blocks = plan->blocks;
   m.most = plan->most;
+  m.alone = plan->num_clusters == 0 && plan->own->num_ctas == 0 ? 1 : 0;
   m.prefix_o = part_o;
   m.prefix_lse = part_lse;
   m.out = static_cast<uint16_t*>(out);

@@ -614,6 +614,43 @@ def test_shared_reads_what_was_written_just_before(mla, q, kv, page, q_len, form
     mla.mla_shared_check(plan, ws)
 
 
+@pytest.mark.parametrize("form", ["once", "each"])
+def test_shared_call_with_nothing_cached(mla, form):
+    """The join is then the call's only kernel: it too comes behind what the stream holds,
+    which here writes the outputs, and the work table."""
+    c = Case([3, 2], [0, 0], [0] * 5, 16, form=form)
+    plan = c.plan(mla)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = torch.empty(5, 16, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(5, 16, device="cuda")
+
+    def call():
+        mla.mla_shared_run(plan, c.query["q"], c.pool["kv"], out, workspace=ws, lse=lse,
+                           prefix_indices=c.prefix_ids, kv_indices=c.own_ids)
+    call()
+    mla.mla_shared_check(plan, ws)
+    for _ in range(5):
+        torch.cuda._sleep(100000)
+        out.fill_(7)
+        lse.fill_(7)
+        call()
+        assert (out == 0).all() and torch.isneginf(lse).all()
+    mla.mla_shared_check(plan, ws)
+    table = ws.clone()
+    zeros = torch.zeros_like(ws)
+    for _ in range(3):
+        torch.cuda._sleep(100000)
+        torch.mul(zeros, 1, out=ws)
+        call()
+        with pytest.raises(mla.MlaError) as e:
+            mla.mla_shared_check(plan, ws)
+        assert e.value.status == 3
+        torch.cuda._sleep(100000)
+        torch.mul(table, 1, out=ws)
+        call()
+        mla.mla_shared_check(plan, ws)
+
+
 def test_shared_captured_and_on_another_stream(mla):
     c = Case([9, 3], [77, 12], [(5 * i) % 40 for i in range(12)], 16, "bf16", "fp8")
     plan = c.plan(mla)
