@@ -245,7 +245,7 @@ __device__ __forceinline__ int box_row(const Stage1Params& p, const BoxFetch& f,
   if (lane >= f.nbox) return 0;
   if (p.identity) return f.raw;
   int page = f.raw;
-  if (page < 0 || static_cast<int64_t>(page + 1) * p.page_size > p.pool_rows) {
+  if (page < 0 || (static_cast<int64_t>(page) + 1) * p.page_size > p.pool_rows) {
     atomicOr(p.err, kErrBadPage);
     page = 0;
   }
@@ -303,7 +303,7 @@ __device__ void run_producer(const Stage1Params& p, Misc* ms, uint32_t ring, int
         const int r = lane + 32 * j;
         if (r >= nvalid) continue;
         int pg = page[j];
-        if (pg < 0 || static_cast<int64_t>(pg + 1) * p.page_size > p.pool_rows) {
+        if (pg < 0 || (static_cast<int64_t>(pg) + 1) * p.page_size > p.pool_rows) {
           atomicOr(p.err, kErrBadPage);
           pg = 0;
         }
@@ -647,7 +647,7 @@ __device__ __forceinline__ int64_t pool_row(const Stage1Params& p, const TileAhe
     const int64_t row = static_cast<int64_t>(first_page(c.page_base)) * p.page_size + pos;
     return row < p.pool_rows ? row : 0;   // (the host rejects such plans; never reached)
   }
-  if (page < 0 || static_cast<int64_t>(page + 1) * p.page_size > p.pool_rows) {
+  if (page < 0 || (static_cast<int64_t>(page) + 1) * p.page_size > p.pool_rows) {
     atomicOr(p.err, kErrBadPage);
     page = 0;
   }

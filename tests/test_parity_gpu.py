@@ -702,6 +702,40 @@ def test_page_outside_the_pool_is_reported(kv_dtype, page_size):
     compare(o[good], l[good], o_ref, l_ref, kv_dtype, [lengths[b] for b in good])
 
 
+@pytest.mark.parametrize("kv_dtype,page_size", [("fp8", 8), ("bf16", 4), ("bf16", 16), ("mxfp4", 8),
+                                                ("fp8", 1), ("mxfp4", 5)])
+def test_largest_page_numbers_are_outside_the_pool(kv_dtype, page_size):
+    # entries whose successor, or whose first row, passes 32 bits
+    mla = _mla()
+    import workloads as synth
+    lengths = [300, 200, 129, 77]
+    w = synth.make_workload(bs=4, lengths=lengths, page_size=page_size, q_dtype="bf16",
+                            kv_dtype=kv_dtype, permute_pages=True, seed=59)
+    keep = w.kv_indices.clone()
+    good = [0, 2]
+    o_ref, l_ref = oracle.mla_decode(**synth.oracle_args(w, select=good))
+    plan = mla.mla_decode_plan(w.kv_indptr, w.kv_last_page_len, page_size=page_size,
+                               q_dtype="bf16", kv_dtype=kv_dtype)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    for bad in (2**31 - 1, 2**31 - 2, 2**31 // page_size - 1, -2**31):
+        ind = keep.clone()
+        ind[int(w.kv_indptr[1]) + 1] = bad
+        ind[int(w.kv_indptr[3])] = bad
+        w.kv_indices = ind
+        d = w.to("cuda")
+        out = torch.full((w.bs, 16, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((w.bs, 16), float("nan"), dtype=torch.float32, device="cuda")
+        mla.mla_decode_run(plan, d.q, d.kv, out, workspace=ws, kv_scale=d.kv_scale,
+                           kv_e8m0=d.kv_e8m0, kv_indices=d.kv_indices, lse=lse)
+        with pytest.raises(mla.MlaError) as e:
+            mla.mla_decode_check(plan, ws)
+        assert e.value.status == 1                    # MLA_ERR_INVALID_ARG
+        o = out.float().cpu().numpy().astype(np.float64)
+        l = lse.cpu().numpy().astype(np.float64)
+        assert np.isfinite(o).all()
+        compare(o[good], l[good], o_ref, l_ref, kv_dtype, [lengths[b] for b in good])
+
+
 def test_decode_call_captures_in_a_cuda_graph():
     # after one run has uploaded the plan's table into the workspace, a call
     # only launches kernels on the stream: it can be captured in a CUDA graph
