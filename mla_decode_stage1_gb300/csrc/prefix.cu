@@ -97,6 +97,10 @@ constexpr uint32_t kColQ = 0, kColS = 256, kColO = 0;
 // A row's maximum is kept until a score exceeds it by a factor of 2^8, and then
 // moves by a power of two, so that a byte tells the factor.
 constexpr float kLag = 8.0f;
+// From here on a maximum, which is rounded, may be far from the product that it was
+// rounded from (half a step): scores are then rounded in the same way before it is
+// taken off.
+constexpr float kFar = 16777216.0f;
 constexpr uint32_t kPHalfBytes = kHalfBytes;
 constexpr uint32_t kFactorBytes = kSpRows, kFinBytes = kSpRows * 4;
 
@@ -572,8 +576,9 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
   // A row's maximum is that of its products, so their factor has to be positive: a
   // negative one turns the queries around, and instead of 0 it is the smallest number,
   // with which finite products still come to 0 (2^-21 at most) but -inf, where there is
-  // no key, does not become NaN.
-  const float factor = qs * ks * (kLog2e / 24.0f);
+  // no key, does not become NaN.  (Multiplied as by the decode kernel, whose equal
+  // scores are to stay equal.)
+  const float factor = qs * ks * (1.0f / 24.0f) * kLog2e;
   const uint32_t sign = factor < 0.0f ? 0x80008000u : 0u;
   const float scale = factor == 0.0f ? __uint_as_float(1u) : fabsf(factor);
   const uint64_t scale2 = pack_f32x2(scale, scale);
@@ -644,21 +649,27 @@ __device__ void run_softmax(const PrefixParams& p, Misc* ms, const Place& at, ui
       if (top > m + kLag) {
         const float d = ceilf(top - m);                  // (the first tile: infinite)
         drop = d < 200.0f ? static_cast<uint32_t>(d) : 200u;
-        m = m == -INFINITY ? top : m + d;
+        m = d < 200.0f ? m + d : top;
         l *= factor_of(drop);
       }
       // a row that has seen no score above -inf keeps p = 2^(-inf) = 0
       const float off = m == -INFINITY ? 0.0f : -m;
       const uint64_t off2 = pack_f32x2(off, off);
+      uint64_t by2 = scale2;
+      if (fabsf(m) >= kFar) {
+        by2 = pack_f32x2(1.0f, 1.0f);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * scale);
+      }
       uint64_t sum0 = 0, sum1 = 0;
       uint32_t pk[32];
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
         float x0, x1, x2, x3;
-        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale2,
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), by2,
                                off2), x0, x1);
         unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])),
-                               scale2, off2), x2, x3);
+                               by2, off2), x2, x3);
         x0 = ex2(x0); x1 = ex2(x1); x2 = ex2(x2); x3 = ex2(x3);
         sum0 = add_f32x2(sum0, pack_f32x2(x0, x1));
         sum1 = add_f32x2(sum1, pack_f32x2(x2, x3));

@@ -309,6 +309,38 @@ def test_shared_equal_and_extreme_scores(mla):
 
 
 @pytest.mark.parametrize("form", ["once", "each"])
+@pytest.mark.parametrize("power", [10, 22, 28, 29, 36, 70])
+@pytest.mark.parametrize("q,kv", FORMATS)
+def test_shared_scores_of_any_size(mla, q, kv, power, form):
+    """Values -2 .. 2 times a power of two: products and their sums are exact, and scores
+    so far apart that the largest ones of a row have all the weight."""
+    g = gen(34)
+    for per, prefix, own, page in (([3], [170], [30, 0, 9], 8), ([20], [40], [11] * 20, 64)):
+        total = sum(prefix) + sum(-(-n // page) for n in own) + 2
+        k = torch.randint(-2, 3, (total * page, 576), generator=g, device="cuda").float()
+        c = Case(per, prefix, own, page, q, kv, rows=k * 2.0 ** power if kv != "fp8" else k, form=form)
+        x = torch.randint(-2, 3, c.query["q"].shape, generator=g, device="cuda").float()
+        if q == "fp8":
+            c.query["q"].copy_(x.to(torch.float8_e4m3fn).view(torch.uint8))
+            c.query["q_scale"].fill_(1.0)
+        else:
+            c.query["q"].copy_(x.bfloat16())
+        if kv == "fp8":
+            c.pool["kv"].copy_(k.to(torch.float8_e4m3fn).view(torch.uint8))
+            c.pool["kv_scale"].fill_(2.0 ** power)
+        o, lse = c.run(mla)
+        for b in range(c.bs):
+            keys = k[torch.cat(c.keys_of(b))].double()
+            s = x[b].double() @ keys.T
+            w = (s == s.amax(1, keepdim=True)).double()
+            ref = w @ keys[:, :512] / w.sum(1, keepdim=True)
+            # probabilities and output to bf16; the products of scale and score, the sums
+            assert ((o[b].double() / 2.0 ** power - ref).abs() <= 2 * (2 * U + 64 * F)).all()
+            top = s.amax(1) * 2.0 ** power / 24
+            assert ((lse[b].double() - top - w.sum(1).log()).abs() <= 16 * F * (top.abs() + 8)).all()
+
+
+@pytest.mark.parametrize("form", ["once", "each"])
 @pytest.mark.parametrize("q,kv,q_scale,kv_scale,std", [
     ("bf16", "fp8", 1.0, 0.0, 1.5), ("fp8", "fp8", 0.0, 0.0131, 1.5), ("fp8", "bf16", 0.0, 1.0, 1.5),
     ("bf16", "fp8", 1.0, -0.0131, 1.5), ("bf16", "fp8", 1.0, -0.0131, 60.0),
