@@ -665,11 +665,12 @@ mla_status mla_prefill_check(const mla_prefill* plan, void* workspace, mla_strea
  *                       for few requests or short prefixes.  MLA_SHARED_AUTO: the
  *                       one that is expected to be faster.
  * The plan follows mla_plan's rules: library-owned, one host thread at a time,
- * one workspace per plan.  The workspace holds the prefixes' rows in bf16 (1,152
- * bytes a token, the group's length rounded up to 128; not of a bf16 pool in pages
- * of a multiple of 64, which is read where it stands), the partial results (2 KB a
- * row of each of num_items, 32 KB and more for each range of own tokens) and the
- * work tables.
+ * one workspace per plan.  It is for these lengths: a step that adds tokens makes
+ * its own, which all layers of the step can use.  The workspace holds the
+ * prefixes' rows in bf16 (1,152 bytes a token, the group's length rounded up to
+ * 128; not of a bf16 pool in pages of a multiple of 64, which is read where it
+ * stands), the partial results (2 KB a row of each of num_items, 32 KB and more for
+ * each range of own tokens) and the work tables.
  * Errors: MLA_ERR_INVALID_ARG (also out of host memory), MLA_ERR_UNSUPPORTED (a
  * pair of types), MLA_ERR_CUDA.
  */
@@ -747,7 +748,7 @@ mla_status mla_shared_check(const mla_shared* plan, void* workspace, mla_stream_
  *   bounds          bf16 [num_pages][2][576], 32-byte aligned: the smallest
  *                   values, then the largest, exactly as stored (an e4m3 pool's
  *                   values without kv_scale).  Both are NaN for a dim with a value
- *                   that is not finite.
+ *                   that is not finite (as an MXFP4 value of 2^128 and more).
  * A page must not get new tokens from two places of a call (two requests, or two
  * columns of one).  batch_size x table_pages is below 2^31.
  * On the device: a negative length counts as 0, a page outside the pool or the
@@ -780,7 +781,7 @@ mla_status mla_page_bounds(const void* kv, mla_dtype kv_dtype, const uint8_t* kv
  * A page with NaN bounds scores NaN.  Sums are fp32.  On the device: a negative
  * length counts as 0, a page outside the bounds is read as page 0 (both
  * MLA_ERR_INVALID_ARG); tokens beyond the table's columns do not count
- * (MLA_ERR_CAPACITY).
+ * (MLA_ERR_CAPACITY).  With table_pages 0 nothing is read, written or reported.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (q_dtype), MLA_ERR_CUDA.
  */
 mla_status mla_page_scores(const void* q, mla_dtype q_dtype, const float* q_scale,

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
   }
   __syncthreads();
   // The instruction's own sums round towards zero: 8 in a row, then one rounded
-  // addition (72 in a row were 1.2e-6 off, against 2e-7).
+  // addition (72 in a row were 1.2e-6 off, against 1e-7).
   float sum[kTiles][4];
 #pragma unroll
   for (int i = 0; i < kTiles; ++i)
@@ -432,7 +432,9 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
 //
 // Bound: latency, of loads that wait for one another above all: the scores (and for
 // short rows the pages) are read beside the lengths.  256 rows of 128 columns 4.1 us,
-// one of 16,384 13 us.
+// one of 16,384 13 us, of 32,768 20.  The keys of longer rows do not fit in shared
+// memory, and every round reads the scores again: one of 32,769 35 us, of 65,536 64, of
+// 131,072 150.
 
 struct SelectParams {
   const float* scores;
@@ -861,7 +863,8 @@ extern "C" mla_status mla_page_scores(const void* q, mla_dtype q_dtype, const fl
   constexpr int32_t kPages = mla::kScoreWarps * 8;
   const int64_t rows = static_cast<int64_t>(batch_size) * q_len;
   // A tile a warp while all CTAs are on the machine at once (4 an SM): 32,768 pages
-  // take 18.7 us in 1,024 such CTAs, 16.4 in 256 of four tiles a warp (two an SM).
+  // take 18.7 us in 1,024 such CTAs, 16.4 in 256 of four tiles a warp (two an SM; all 255
+  // registers, and 24 bytes a thread spilled).
   const bool wide = rows * ((table_pages - 1) / kPages + 1) > 4 * 152;
   p.chunks = (table_pages - 1) / (wide ? 4 * kPages : kPages) + 1;
   if (static_cast<int64_t>(p.chunks) * batch_size > INT32_MAX) return MLA_ERR_INVALID_ARG;

@@ -26,9 +26,10 @@
 //
 // Measured: 1,024 rows (64 requests) against 32,768 keys, 73 GFLOP, 50 us on 36
 // clusters, 1.46 PFLOP/s.  Of these 1.5 us pass until a cluster's CTAs have met, 4 with
-// the queries on their way (as fast as keys and queries together come in), 2 with the
-// first scores, 34 with the other tiles, 3.5 with the last products and 4 with the
-// output, 256 KB a CTA at 32 bytes a cycle.  Copies of keys to both CTAs at once
+// the queries on their way (147 KB, and as many of keys, come to a score CTA in that
+// time, at 37 bytes a cycle; an SM takes up to 69, so what holds them up is not known),
+// 2 with the first scores, 34 with the other tiles, 3.5 with the last products and 4 with
+// the output, 256 KB a CTA at 32 bytes a cycle.  Copies of keys to both CTAs at once
 // (multicast) changed nothing, nor did queries that were asked for earlier or taken up
 // in thirds.
 //

@@ -271,7 +271,6 @@ mla_status make_plan(mla_shared* P, const int32_t* group_indptr, const int32_t* 
   const int64_t cost = choose_cut(P, blocks, own, &own_ctas, &once_us);
   once_us += 8 + 0.33e-3 * static_cast<double>(gathered) + 6.0 * P->bs * t / P->num_sms;
   P->each = form == MLA_SHARED_EACH || (form == MLA_SHARED_AUTO && each.on(P->num_sms) + 3 < once_us);
-  //DUMP
   if (P->each) {
     own_ctas = 0;
     blocks.clear();
