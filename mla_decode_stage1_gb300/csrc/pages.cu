@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_scores_kernel(const Sco
 // loads of them under way at once.
 //
 // Bound: latency, of loads that wait for one another above all: the scores (and for
-// short rows the pages) are read beside the lengths.  256 rows of 128 columns 4.1 us,
+// short rows the pages) are read beside the lengths.  256 rows of 128 columns 2.7 us,
 // one of 16,384 13 us, of 32,768 20.  The keys of longer rows do not fit in shared
 // memory, and every round reads the scores again: one of 32,769 35 us, of 65,536 64, of
 // 131,072 150.
