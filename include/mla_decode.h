@@ -287,6 +287,7 @@ void mla_plan_destroy(mla_plan* plan);
  *              pages' [total_kv, 18] layout), row stride in bytes: even and
  *              >= 18, base 2-byte aligned (MLA_ERR_INVALID_ARG below 18,
  *              MLA_ERR_UNSUPPORTED if odd).  NULL / ignored for other KV types.
+ *              Values below 2^-98 may be up to 2^-100 off.
  *   kv_pool_rows  number of rows in the KV pool (bounds every access).
  *   kv_indices device int32 page table, indexed from kv_indptr; NULL = the
  *              identity table (request b's pages are kv_indptr[b]..; they

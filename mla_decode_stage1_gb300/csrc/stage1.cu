@@ -601,6 +601,11 @@ __device__ __forceinline__ uint2 e2m1x8_to_e4m3(uint32_t w, uint32_t lo, uint32_
 // 0.  The loads of a tile are issued one tile ahead and its page-table entry
 // two tiles ahead, so neither waits on the path.
 
+// Smallest exponent of a token: P' is at least 2^(kMxLeast - 123) times 2^-m for a
+// score of 0, a normal number up to m = 40, and 2^24 times 2^(127 - kMxLeast + 8) of
+// a sum is one too.
+constexpr int kMxLeast = 37;
+
 // A light cursor over the same tiles as TileCursor, for looking ahead: only
 // what locating a token's pool row needs (ntile == 0 once past the end).
 struct TileAhead {
@@ -928,7 +933,10 @@ __device__ __forceinline__ bool half_of_tile(bool ok, bool live, bool fast, uint
 // With r_t the token's largest e8m0 exponent, block b becomes
 // e2m1 * 2^(E_b - r_t): exact in e4m3 while E_b - r_t >= -8.  The remaining
 // factor 2^(r_t - 127) of the token is left to the softmax (u_t in shared
-// memory).  The e4m3 magnitudes of a block are computed for
+// memory).  r_t is at least kMxLeast: a token of zeros, whose scale bytes are
+// the smallest there are, has all its weight in the sum, and P' = p 2^u has to
+// stay a number from which 2^-u makes p again (values below 2^-98, which are
+// no longer exact with that, are 0 beside any score).  The e4m3 magnitudes of a block are computed for
 // E_b - r_t >= -5 (every block of the token within five binades of its
 // largest, the common case) and looked up otherwise.  Rows past the tile's
 // end are written as zeros, so that 0 * V stays 0 in PV.
@@ -989,7 +997,7 @@ __device__ void run_dequant_mx(const Stage1Params& p, Misc* ms, uint8_t* ring_ge
     // this tile's scale bytes: r = max over all 18 (this thread's nine and
     // those of lane ^ 4, the other half of the token), and the smallest of
     // this thread's nine
-    int r = 0, emin = 255;
+    int r = kMxLeast, emin = 255;
 #pragma unroll
     for (int j = 0; j < 9; ++j) {
       r = max(r, static_cast<int>(ec[j]));

@@ -361,6 +361,26 @@ def test_shared_scales_of_zero_and_below(mla, q, kv, q_scale, kv_scale, std, for
         check_shared(mla, c)
 
 
+@pytest.mark.parametrize("form", ["once", "each"])
+@pytest.mark.parametrize("scale", [0, 2, 8, 27, 87, 127])
+def test_shared_mxfp4_tokens_of_zeros(mla, scale, form):
+    """Blocks of zeros have the smallest scale byte: such tokens have scores of 0 and
+    their full weight."""
+    for std in (0.3, 1.5):
+        c = Case([3, 17], [33, 9], [20, 3, 1] + [5] * 17, 8, "bf16", "mxfp4", std=std, form=form)
+        zero = torch.rand(len(c.stored), generator=gen(35), device="cuda") < 0.6
+        c.pool["kv"][zero] = 0
+        c.pool["kv_e8m0"][zero] = scale
+        c.stored[zero] = 0
+        check_shared(mla, c)
+    # nothing but zeros
+    c.pool["kv"].zero_()
+    c.pool["kv_e8m0"].fill_(scale)
+    o, lse = c.run(mla)
+    n = torch.tensor([len(torch.cat(c.keys_of(b))) for b in range(c.bs)], device="cuda").double()
+    assert (o == 0).all() and ((lse.double() - n.log()[:, None]).abs() <= 64 * F * (1 + n.log()[:, None])).all()
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8", "mxfp4"])
 def test_shared_values_that_are_not_finite(mla, kv):
     """A bad row reaches exactly the requests that attend to it."""

@@ -702,6 +702,52 @@ def test_page_outside_the_pool_is_reported(kv_dtype, page_size):
     compare(o[good], l[good], o_ref, l_ref, kv_dtype, [lengths[b] for b in good])
 
 
+@pytest.mark.parametrize("scale", [0, 1, 5, 26, 27, 28, 60, 86, 87, 88, 127])
+@pytest.mark.parametrize("page_size", [8, 5])
+def test_mxfp4_tokens_of_zeros(scale, page_size):
+    # a block of zeros is stored with the smallest scale byte (0): tokens of
+    # nothing else have a score of 0 and their full weight in the softmax,
+    # beside others and on their own
+    mla = _mla()
+    import workloads as synth
+    lengths = [300, 40, 129, 77, 1]
+    w = synth.make_workload(bs=5, lengths=lengths, page_size=page_size, q_dtype="bf16",
+                            kv_dtype="mxfp4", permute_pages=True, seed=60)
+    rng = np.random.default_rng(61)
+    zero = rng.random(w.pool_rows) < 0.6
+    ids = w.kv_indices.numpy() if torch.is_tensor(w.kv_indices) else np.asarray(w.kv_indices)
+    for b in (1, 4):                                  # requests of zeros only
+        for p in ids[int(w.kv_indptr[b]): int(w.kv_indptr[b + 1])]:
+            zero[p * page_size: (p + 1) * page_size] = True
+    zero = torch.from_numpy(zero)
+    w.kv[zero] = 0
+    w.kv_e8m0[zero] = scale
+    for num_sms in (0, 3):
+        o, lse, _ = run_gpu(w, num_sms=num_sms)
+        o_ref, l_ref = oracle.mla_decode(**synth.oracle_args(w))
+        mixed = [0, 2, 3]
+        compare(o[mixed], lse[mixed], o_ref[mixed], l_ref[mixed], "mxfp4", [lengths[b] for b in mixed])
+        for b in (1, 4):
+            assert (o[b] == 0).all()
+            # sums of ones, with factors of powers of two; log2 and its product
+            assert np.abs(lse[b] - np.log(lengths[b])).max() <= 2e-6 * (1 + np.log(lengths[b]))
+
+
+@pytest.mark.parametrize("scale", [0, 3, 20, 27, 40, 86, 87, 100])
+def test_mxfp4_tokens_of_tiny_values(scale):
+    # values of 2^(scale - 127), beside tokens of ordinary ones
+    mla = _mla()
+    import workloads as synth
+    lengths = [700, 260, 33]
+    w = synth.make_workload(bs=3, lengths=lengths, page_size=8, q_dtype="bf16", kv_dtype="mxfp4",
+                            permute_pages=True, seed=62)
+    tiny = torch.from_numpy(np.random.default_rng(63).random(w.pool_rows) < 0.7)
+    w.kv_e8m0[tiny] = scale
+    o, lse, _ = run_gpu(w)
+    o_ref, l_ref = oracle.mla_decode(**synth.oracle_args(w))
+    compare(o, lse, o_ref, l_ref, "mxfp4", lengths)
+
+
 @pytest.mark.parametrize("kv_dtype,page_size", [("fp8", 8), ("bf16", 4), ("bf16", 16), ("mxfp4", 8),
                                                 ("fp8", 1), ("mxfp4", 5)])
 def test_largest_page_numbers_are_outside_the_pool(kv_dtype, page_size):
