@@ -112,8 +112,9 @@ typedef struct {
  *                         current CUDA device.
  *   plan_out              receives the new plan (library-owned).
  * Errors: MLA_ERR_INVALID_ARG (null/negative/non-monotone input, bad
- * last-page length), MLA_ERR_UNSUPPORTED (dtype or page size combination not
- * implemented), MLA_ERR_CUDA (device query failed when num_sms == 0).
+ * last-page length; also out of host memory), MLA_ERR_UNSUPPORTED (dtype or page
+ * size combination not implemented), MLA_ERR_CUDA (device query failed when
+ * num_sms == 0).
  */
 mla_status mla_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_last_page_len_host,
                            int32_t batch_size, int32_t page_size, mla_dtype q_dtype,

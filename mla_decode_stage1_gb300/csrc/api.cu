@@ -10,6 +10,7 @@
 #include <chrono>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -448,8 +449,12 @@ mla_status mla_decode_plan_ex(const int32_t* kv_indptr_host, const int32_t* kv_l
                               int32_t batch_size, int32_t q_len, int32_t page_size,
                               mla_dtype q_dtype, mla_dtype kv_dtype,
                               const mla_plan_options* options, mla_plan** plan_out) {
-  return mla::plan_with_prefixes(kv_indptr_host, kv_last_page_len_host, batch_size, q_len, page_size,
-                                 q_dtype, kv_dtype, options, nullptr, plan_out);
+  try {
+    return mla::plan_with_prefixes(kv_indptr_host, kv_last_page_len_host, batch_size, q_len, page_size,
+                                   q_dtype, kv_dtype, options, nullptr, plan_out);
+  } catch (...) {   // out of host memory
+    return MLA_ERR_INVALID_ARG;
+  }
 }
 
 }  // extern "C"
@@ -537,8 +542,8 @@ mla_status mla::plan_with_prefixes(const int32_t* kv_indptr_host,
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return MLA_ERR_CUDA;
   }
-  mla_plan* P = new (std::nothrow) mla_plan();
-  if (P == nullptr) return MLA_ERR_INVALID_ARG;
+  std::unique_ptr<mla_plan> owner(new mla_plan());   // (until the plan is whole)
+  mla_plan* P = owner.get();
   P->bs = nv;
   P->nreq = batch_size;
   P->rows = pairs ? 2 * mla::kHeads : mla::kHeads;
@@ -590,7 +595,7 @@ mla_status mla::plan_with_prefixes(const int32_t* kv_indptr_host,
   assign_slots(P, len);
   layout_workspace(P);
   P->cluster = o.merge == 0 ? cluster_size_of(P) : 0;
-  *plan_out = P;
+  *plan_out = owner.release();
   return MLA_OK;
 }
 

@@ -431,6 +431,39 @@ def test_plan_item_cost_bounds(mla):
         assert worst <= equal
 
 
+def test_plans_that_do_not_fit_host_memory_are_refused():
+    # (a process of its own, whose address space may grow by 40 MB: a plan of 2 million
+    # requests takes some hundred)
+    import subprocess
+    import sys
+    code = """
+import resource
+import numpy as np
+import mla_decode_stage1_gb300 as mla
+mla.mla_shared_plan
+n = 2_000_000
+indptr = np.arange(n + 1, dtype=np.int32)
+calls = [lambda: mla.mla_decode_plan(indptr, page_size=8, q_dtype="fp8", kv_dtype="fp8", num_sms=152),
+         lambda: mla.mla_shared_plan([0, n], [0, 1], indptr, page_size=8, q_dtype="fp8",
+                                     kv_dtype="fp8", num_sms=152)]
+size = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+old = resource.getrlimit(resource.RLIMIT_AS)
+for call in calls:
+    resource.setrlimit(resource.RLIMIT_AS, (size + (40 << 20), old[1]))
+    try:
+        call()
+        status = 0
+    except mla.MlaError as e:
+        status = e.status
+    resource.setrlimit(resource.RLIMIT_AS, old)
+    assert status == 1, status
+    assert mla.mla_decode_plan([0, 3], page_size=8, q_dtype="fp8", kv_dtype="fp8", num_sms=152)
+print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "refused" in r.stdout, r.stderr[-2000:]
+
+
 def test_plan_options_validated(mla):
     indptr = np.array([0, 100], np.int32)
     for kw in (dict(unit=48), dict(unit=256), dict(item_cost=-1), dict(item_cost=65)):
